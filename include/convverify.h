@@ -51,7 +51,7 @@ extern "C" {
 #define CV_API
 #endif
 
-#define CV_ABI_VERSION 8
+#define CV_ABI_VERSION 9
 #define CV_MAX_T 128 /* draft tokens per verify call */
 
 typedef enum cv_dtype {
@@ -104,7 +104,9 @@ enum {
     CV_ERR_WIDTH = -5,        /* conv width outside 2..4 */
     CV_ERR_DTYPE = -6,        /* dtype not a cv_dtype */
     CV_ERR_HEAD_DIM = -7,     /* qk_channels > 0 and head_dim not a power of two in 8..256, or
-                                 qk_channels not a multiple of head_dim, or qk_channels > dim */
+                                 qk_channels not a multiple of head_dim, or qk_channels > dim;
+                                 linear attention: dk or dv outside 1..256, or n_heads not a
+                                 multiple of n_qk_heads; block norm: group not a divisor of dim */
     CV_ERR_LAYOUT = -8,       /* unknown layout, DEDUP with win_step_stride != win_col_stride,
                                  HISTORY passed to cv_conv_commit, or column-major state rows
                                  outside HISTORY */
@@ -114,7 +116,8 @@ enum {
     CV_ERR_ALIAS = -10,       /* out or window has the same base address as x, conv_state or weight,
                                  or out and window share a base address */
     CV_ERR_LAUNCH = -11,      /* the CUDA launch failed (cudaGetLastError after the launch) */
-    CV_ERR_SMEM = -12         /* the tile does not fit in shared memory for any block size */
+    CV_ERR_SMEM = -12,        /* the tile does not fit in shared memory for any block size */
+    CV_ERR_WORKSPACE = -13    /* the workspace is NULL, misaligned or smaller than the call needs */
 };
 
 /* Per-sequence bits written to err[s] (0 = fine or padded). */
@@ -376,6 +379,146 @@ typedef struct cv_launch_plan {
 } cv_launch_plan;
 
 CV_API int cv_verify_plan(const cv_verify_args *args, cv_launch_plan *plan);
+
+/*
+ * Linear attention with a decay for each head, the recurrence that follows the conv in a hybrid
+ * layer.  Every value head h keeps a state S [dk][dv] in fp32 and reads the q|k head
+ * h * n_qk_heads / n_heads (integer division).  One token does
+ *     S   <- exp(g) S + b k v^T         g = log_decay[h], b = gain[h] (1 without gain)
+ *     out  = scale * S^T q + skip[h] v  (no last term without skip)
+ * with the updated state, everything in fp32; out is rounded once to dtype.  g may be -infinity (the
+ * state is dropped: exp(g) = 0), it is meant to be <= 0.
+ *
+ * cv_linattn_tokens holds one run of tokens per sequence: T tokens for each of the n_seq sequences
+ * (cu NULL; token t of sequence s at s*seq_stride + t*tok_stride) or, with cu (int32 [n_seq + 1]
+ * device array), rows [cu[s], cu[s+1]) packed back to back (the seq strides are ignored), at most T
+ * of them and all within [0, total_tokens).  Strides are in elements; the innermost stride of q, k
+ * and v is 1, and that of log_decay and gain (fp32, [.., n_heads]) is 1 too.  q, k and v may be
+ * slices of one conv output row.
+ */
+typedef struct cv_linattn_tokens {
+    int32_t T;            /* tokens per sequence (cu NULL), or the largest count (cu) */
+    int32_t total_tokens; /* rows with cu */
+    const int32_t *cu;
+    const void *q, *k, *v;
+    int64_t q_seq_stride, q_tok_stride, q_head_stride;
+    int64_t k_seq_stride, k_tok_stride, k_head_stride;
+    int64_t v_seq_stride, v_tok_stride, v_head_stride;
+    const float *log_decay;
+    int64_t decay_seq_stride, decay_tok_stride;
+    const float *gain; /* or NULL (1) */
+    int64_t gain_seq_stride, gain_tok_stride;
+} cv_linattn_tokens;
+
+/*
+ * Arguments of cv_linattn_prefill and cv_linattn_step.
+ *   n_seq, n_heads, n_qk_heads   sequences 0..65535; value heads 1..4096, a multiple of the q|k heads
+ *   dk, dv             1..256: channels of q and k, and of v and out, per head
+ *   dtype              cv_dtype of q, k, v and out
+ *   tok                the tokens.  prefill: cu is required (prompts packed back to back, any length
+ *                      up to T).  step: T is 0..CV_MAX_T; 0 = no tokens (only the commit of prev)
+ *   skip               fp32 [n_heads] or NULL
+ *   out                write-only, rows as tok's: (s, t, h, c) at s*out_seq_stride (cu: no such term)
+ *                      + t*out_tok_stride + h*out_head_stride + c
+ *   state              fp32 [n_slots][n_heads][dk][dv], read-modify-write: element (slot, h, i, j) at
+ *                      slot*state_slot_stride + h*state_head_stride + i*dv + j
+ *   cache_idx          int32 [n_seq] or NULL (slot = s); negative = padded sequence: nothing of it is
+ *                      read or written
+ *   has_initial_state  int32 [n_seq] or NULL (all have one): 0 starts from a zero state, the slot's
+ *                      old content is not read
+ *   err                int32 [n_seq] or NULL: CV_SEQ_* bits (0 for fine and padded sequences).  A
+ *                      flagged sequence is left untouched
+ * step only:
+ *   prev               the previous step's drafts (q is not read; T = 0: none) and accept_len, int32
+ *                      [n_seq], how many of them were accepted, 0..T_s (else CV_SEQ_BAD_ACCEPT): the
+ *                      state is first advanced over those tokens and written, then the outputs of tok
+ *                      are computed from it
+ *   update_state       nonzero: the state is left after all of tok's tokens (decoding).  Zero: the
+ *                      outputs only (a verify, committed as prev of the next call)
+ * prefill only:
+ *   workspace          device buffer of at least the bytes cv_linattn_workspace reports, 256-byte
+ *                      aligned; its content means nothing before and after the call.  NULL when 0
+ * Preconditions the library cannot check: distinct sequences use distinct slots; out and state do not
+ * overlap an input, each other, or the workspace.
+ */
+typedef struct cv_linattn_args {
+    int32_t n_seq, n_heads, n_qk_heads, dk, dv;
+    int32_t dtype; /* cv_dtype */
+    float scale;
+    int32_t n_slots;
+    cv_linattn_tokens tok;
+    const float *skip;
+    void *out;
+    int64_t out_seq_stride, out_tok_stride, out_head_stride;
+    float *state;
+    int64_t state_slot_stride, state_head_stride;
+    const int32_t *cache_idx;
+    const int32_t *has_initial_state;
+    int32_t *err;
+    cv_linattn_tokens prev;
+    const int32_t *accept_len;
+    int32_t update_state;
+    void *workspace;
+    int64_t workspace_bytes;
+} cv_linattn_args;
+
+/* cv_linattn_prefill -- outputs of whole prompts and their final states (update_state and prev are
+ * ignored; the state is always left after the last token; an empty prompt leaves it, or writes zeros
+ * without an initial state). */
+CV_API int cv_linattn_prefill(const cv_linattn_args *args, void *stream);
+
+/* cv_linattn_workspace -- validates args as cv_linattn_prefill does (pointers apart) and sets *bytes
+ * to the workspace that call needs on the current device (0 = none). */
+CV_API int cv_linattn_workspace(const cv_linattn_args *args, int64_t *bytes);
+
+/* cv_linattn_step -- one new token or a run of draft tokens per sequence, after the commit of the
+ * previous step's accepted drafts (see prev and update_state).  With T = 0 only the commit runs. */
+CV_API int cv_linattn_step(const cv_linattn_args *args, void *stream);
+
+/*
+ * cv_block_norm -- the RMS norms around a block, fused with its gate and its scaled residual.  For
+ * every row of dim channels, all in fp32 with one rounding per output:
+ *     a = y                                      gate act(z) = z*sigmoid(z) or sigmoid(z)
+ *     a = a * act(z)                             with a gate and gate_first
+ *     a = a / sqrt(mean over its group of a^2 + eps) * post_weight    with group > 0
+ *     a = a * act(z)                             with a gate otherwise
+ *     without residual:  out = a
+ *     with residual:     r = residual + scale * channel_scale * a
+ *                        residual_out = r        and, unless out is NULL,
+ *                        out = r / sqrt(mean over the row of r^2 + eps) * pre_weight
+ *   rows, dim          rows >= 0 (0 = nothing to do), dim 1..65536
+ *   group              0 = no first norm, else a divisor of dim (group = dim: one norm over the row);
+ *                      a row of more than about 58,000 groups is CV_ERR_SMEM
+ *   post_weight        [group] (shared by the groups, needs group > 0) or NULL; pre_weight, channel_scale [dim] or NULL
+ *   dtype              cv_dtype of y, gate, out and the weights; residual_dtype that of residual and
+ *                      residual_out (dtype, or CV_F32 beside bf16)
+ *   *_stride           row strides in elements; channels are contiguous
+ * out may be y or gate, and residual_out may be residual, each with equal base and stride (every
+ * row is read before it is written); any other overlap is undefined.
+ */
+enum { CV_GATE_SILU = 0, CV_GATE_SIGMOID = 1 };
+typedef struct cv_norm_args {
+    int64_t rows;
+    int32_t dim, group;
+    int32_t dtype, residual_dtype; /* cv_dtype */
+    int32_t gate_act, gate_first;  /* CV_GATE_* */
+    float eps, scale;
+    const void *y;
+    int64_t y_stride;
+    const void *gate; /* or NULL */
+    int64_t gate_stride;
+    const void *post_weight;
+    const void *residual; /* or NULL */
+    int64_t residual_stride;
+    void *residual_out;
+    int64_t residual_out_stride;
+    const void *channel_scale;
+    const void *pre_weight;
+    void *out;
+    int64_t out_stride;
+} cv_norm_args;
+
+CV_API int cv_block_norm(const cv_norm_args *args, void *stream);
 
 /* cv_status_string -- a static, NUL-terminated description of a status code (never NULL). */
 CV_API const char *cv_status_string(int status);

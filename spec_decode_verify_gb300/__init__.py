@@ -8,6 +8,13 @@ CPU path: CPU tensors are rejected and a missing library raises.
     conv_verify(x, conv_state, weight, bias, out, window, layout=..., qk_channels=..., head_dim=...)
     conv_commit(conv_state, window, accept_len, layout=..., T=..., width=..., x=...)
     conv_prefill(x, conv_state, weight, bias, out, cu_seqlens, max_seqlen=..., qk_channels=..., head_dim=...)
+
+and the operators that follow the conv in a hybrid layer:
+
+    linattn_prefill(q, k, v, log_decay, state, out, cu_seqlens, max_seqlen=...)
+    linattn_step(q, k, v, log_decay, state, out, prev=LinattnDrafts(...), update_state=...)
+    linattn_commit(LinattnDrafts(...), state)
+    block_norm(y, out, gate=..., group=..., post_weight=..., residual=..., residual_out=..., pre_weight=...)
 """
 from __future__ import annotations
 
@@ -17,7 +24,8 @@ from typing import Optional
 
 __all__ = ["conv_verify", "conv_commit", "conv_prefill", "verify_plan", "status_string", "load_library", "library_path",
            "CvError", "DENSE", "DEDUP", "HISTORY", "RECOMPUTE", "SEQ_BAD_SLOT", "SEQ_BAD_OFFSET", "SEQ_BAD_ACCEPT",
-           "SEQ_TIMEOUT", "SEQ_BAD_SPAN", "SEQ_BAD_TREE"]
+           "SEQ_TIMEOUT", "SEQ_BAD_SPAN", "SEQ_BAD_TREE", "linattn_prefill", "linattn_step", "linattn_commit",
+           "linattn_workspace", "LinattnDrafts", "block_norm"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 library_path = os.path.join(_PKG, "_build", "libconvverify.so")
@@ -77,6 +85,41 @@ class LaunchPlan(ctypes.Structure):
                 ("channels_per_block", c_i32), ("path", c_i32), ("stages", c_i32), ("token_groups", c_i32)]
 
 
+class LinattnTokens(ctypes.Structure):
+    """Mirror of cv_linattn_tokens."""
+    _fields_ = [
+        ("T", c_i32), ("total_tokens", c_i32), ("cu", c_vp), ("q", c_vp), ("k", c_vp), ("v", c_vp),
+        ("q_seq_stride", c_i64), ("q_tok_stride", c_i64), ("q_head_stride", c_i64),
+        ("k_seq_stride", c_i64), ("k_tok_stride", c_i64), ("k_head_stride", c_i64),
+        ("v_seq_stride", c_i64), ("v_tok_stride", c_i64), ("v_head_stride", c_i64),
+        ("log_decay", c_vp), ("decay_seq_stride", c_i64), ("decay_tok_stride", c_i64),
+        ("gain", c_vp), ("gain_seq_stride", c_i64), ("gain_tok_stride", c_i64),
+    ]
+
+
+class LinattnArgs(ctypes.Structure):
+    """Mirror of cv_linattn_args."""
+    _fields_ = [
+        ("n_seq", c_i32), ("n_heads", c_i32), ("n_qk_heads", c_i32), ("dk", c_i32), ("dv", c_i32), ("dtype", c_i32),
+        ("scale", ctypes.c_float), ("n_slots", c_i32), ("tok", LinattnTokens), ("skip", c_vp), ("out", c_vp),
+        ("out_seq_stride", c_i64), ("out_tok_stride", c_i64), ("out_head_stride", c_i64), ("state", c_vp),
+        ("state_slot_stride", c_i64), ("state_head_stride", c_i64), ("cache_idx", c_vp), ("has_initial_state", c_vp),
+        ("err", c_vp), ("prev", LinattnTokens), ("accept_len", c_vp), ("update_state", c_i32), ("workspace", c_vp),
+        ("workspace_bytes", c_i64),
+    ]
+
+
+class NormArgs(ctypes.Structure):
+    """Mirror of cv_norm_args."""
+    _fields_ = [
+        ("rows", c_i64), ("dim", c_i32), ("group", c_i32), ("dtype", c_i32), ("residual_dtype", c_i32),
+        ("gate_act", c_i32), ("gate_first", c_i32), ("eps", ctypes.c_float), ("scale", ctypes.c_float),
+        ("y", c_vp), ("y_stride", c_i64), ("gate", c_vp), ("gate_stride", c_i64), ("post_weight", c_vp),
+        ("residual", c_vp), ("residual_stride", c_i64), ("residual_out", c_vp), ("residual_out_stride", c_i64),
+        ("channel_scale", c_vp), ("pre_weight", c_vp), ("out", c_vp), ("out_stride", c_i64),
+    ]
+
+
 class CvError(RuntimeError):
     def __init__(self, status: int, what: str):
         super().__init__(f"{what}: {status_string(status)} (status {status})")
@@ -103,6 +146,14 @@ def load_library(path: Optional[str] = None):
     lib.cv_conv_prefill.restype = c_i32
     lib.cv_verify_plan.argtypes = [ctypes.POINTER(VerifyArgs), ctypes.POINTER(LaunchPlan)]
     lib.cv_verify_plan.restype = c_i32
+    lib.cv_linattn_prefill.argtypes = [ctypes.POINTER(LinattnArgs), c_vp]
+    lib.cv_linattn_prefill.restype = c_i32
+    lib.cv_linattn_workspace.argtypes = [ctypes.POINTER(LinattnArgs), ctypes.POINTER(c_i64)]
+    lib.cv_linattn_workspace.restype = c_i32
+    lib.cv_linattn_step.argtypes = [ctypes.POINTER(LinattnArgs), c_vp]
+    lib.cv_linattn_step.restype = c_i32
+    lib.cv_block_norm.argtypes = [ctypes.POINTER(NormArgs), c_vp]
+    lib.cv_block_norm.restype = c_i32
     lib.cv_status_string.argtypes = [c_i32]
     lib.cv_status_string.restype = ctypes.c_char_p
     lib.cv_abi_version.argtypes = []
@@ -404,3 +455,246 @@ def conv_prefill(x, conv_state, weight, bias, out, cu_seqlens, *, max_seqlen, qk
     rc = load_library().cv_conv_prefill(ctypes.byref(a), _stream_ptr(stream))
     if rc != 0:
         raise CvError(rc, "cv_conv_prefill")
+
+
+class LinattnDrafts:
+    """Drafts of an earlier linattn_step and how many of each sequence's were accepted.
+
+    k [n_seq, T, n_qk_heads, dk], v [n_seq, T, n_heads, dv], log_decay fp32 [n_seq, T, n_heads], gain
+    like log_decay or None; with cu_draft (int32 [n_seq + 1]) packed rows [total, ...] instead, T then
+    being the largest count (required).  accept_len int32 [n_seq]: 0 .. the sequence's draft count."""
+    __slots__ = ("k", "v", "log_decay", "gain", "accept_len", "cu_draft", "T")
+
+    def __init__(self, k, v, log_decay, accept_len, *, gain=None, cu_draft=None, T=None):
+        self.k, self.v, self.log_decay, self.gain, self.accept_len = k, v, log_decay, gain, accept_len
+        self.cu_draft, self.T = cu_draft, T
+
+
+def _linattn_tokens(q, k, v, log_decay, gain, cu, T, n_seq, ptr, what) -> LinattnTokens:
+    """cv_linattn_tokens of [n_seq, T, heads, d] rows, or of packed [total, heads, d] rows with cu."""
+    import torch
+    nd = 3 if cu is not None else 4
+    if k.dim() != nd or v.dim() != nd or log_decay.dim() != nd - 1 or (q is not None and q.dim() != nd):
+        raise ValueError(f"{what}: q, k and v must be [n_seq, T, heads, d] and log_decay [n_seq, T, heads], "
+                         "or [total, ...] with packed rows")
+    lead, H = tuple(v.shape[:-2]), v.shape[-2]
+    if tuple(k.shape[:-2]) != lead or (q is not None and q.shape != k.shape):
+        raise ValueError(f"{what}: q and k must agree, and have the rows of v")
+    _need_shape(log_decay, "log_decay", lead + (H,))
+    if v.dtype != k.dtype or (q is not None and q.dtype != k.dtype):
+        raise TypeError("q, k and v must share one dtype")
+    for t in (log_decay, gain):
+        if t is not None and t.dtype != torch.float32:
+            raise TypeError("log_decay and gain must be float32")
+    if k.stride(-1) != 1 or v.stride(-1) != 1 or (q is not None and q.stride(-1) != 1):
+        raise ValueError("q, k and v need a unit innermost stride")
+    if H > 1 and (log_decay.stride(-1) != 1 or (gain is not None and gain.stride(-1) != 1)):
+        raise ValueError("log_decay and gain need a unit innermost stride")
+    if gain is not None:
+        _need_shape(gain, "gain", lead + (H,))
+    if cu is None:
+        if lead[0] != n_seq:
+            raise ValueError(f"{what}: {n_seq} sequences expected, got {lead[0]}")
+        if T is not None and T != lead[1]:
+            raise ValueError(f"{what}: T = {T} but the rows hold {lead[1]} tokens")
+        T, total = lead[1], 0
+    else:
+        _need_int32(cu, "cu", shape=(n_seq + 1,))
+        if T is None:
+            raise ValueError(f"{what}: packed rows need T, the largest count")
+        total = lead[0]
+    some = (total if cu is not None else n_seq * T) > 0
+
+    def st(t):
+        s = t.stride()
+        return (0, s[0], s[1]) if nd == 3 else (s[0], s[1], s[2])
+
+    gs, bs = log_decay.stride(), gain.stride() if gain is not None else (0, 0)
+    return LinattnTokens(
+        int(T), total, ptr(cu, "cu", False), ptr(q, "q", some) if q is not None else None, ptr(k, "k", some),
+        ptr(v, "v", some), *(st(q) if q is not None else (0, 0, 0)), *st(k), *st(v),
+        ptr(log_decay, "log_decay", some), 0 if nd == 3 else gs[0], gs[nd - 3], ptr(gain, "gain", False),
+        0 if nd == 3 or gain is None else bs[0], bs[nd - 3])
+
+
+def make_linattn_args(q, k, v, log_decay, state, out, *, n_seq, gain=None, skip=None, scale=None, cu=None, T=None,
+                      prev=None, update_state=False, cache_idx=None, has_initial_state=None, err=None,
+                      workspace=None, check_device=True) -> LinattnArgs:
+    """Build cv_linattn_args (see linattn_prefill and linattn_step; q None: no tokens, prev alone)."""
+    import torch
+    ptr = _dev_ptr if check_device else (lambda t, n, required=True: None if t is None else t.data_ptr())
+    if state.dim() != 4 or state.dtype != torch.float32:
+        raise ValueError("state must be float32 [n_slots, n_heads, dk, dv]")
+    n_slots, H, dk, dv = state.shape
+    if (dv > 1 and state.stride(3) != 1) or (dk > 1 and state.stride(2) != dv):
+        raise ValueError("the [dk, dv] state of a head must be contiguous")
+    for t, name in ((cache_idx, "cache_idx"), (has_initial_state, "has_initial_state"), (err, "err")):
+        _need_int32(t, name, n=n_seq)
+    a = LinattnArgs(n_seq=n_seq, n_heads=H, dk=dk, dv=dv, n_slots=n_slots, state=ptr(state, "state"),
+                    state_slot_stride=state.stride(0), state_head_stride=state.stride(1),
+                    cache_idx=ptr(cache_idx, "cache_idx", False),
+                    has_initial_state=ptr(has_initial_state, "has_initial_state", False), err=ptr(err, "err", False),
+                    update_state=int(update_state), scale=float(dk ** -0.5 if scale is None else scale))
+    some = q if q is not None else prev.k
+    a.dtype = _dtype_code(some)
+    a.n_qk_heads = some.shape[-2]
+    if q is not None:
+        a.tok = _linattn_tokens(q, k, v, log_decay, gain, cu, T, n_seq, ptr, "tokens")
+        if k.shape[-1] != dk or tuple(v.shape[-2:]) != (H, dv):
+            raise ValueError(f"heads of q|k [.., {k.shape[-1]}] and v {tuple(v.shape[-2:])} do not fit the state "
+                             f"{tuple(state.shape)}")
+        _need_shape(out, "out", v.shape)
+        if out.dtype != v.dtype or out.stride(-1) != 1:
+            raise ValueError("out needs the dtype of v and a unit innermost stride")
+        os = out.stride()
+        a.out = ptr(out, "out", out.numel() > 0)
+        a.out_seq_stride, a.out_tok_stride, a.out_head_stride = (0, os[0], os[1]) if cu is not None else os[:3]
+    if skip is not None:
+        _need_shape(skip, "skip", (H,))
+        if skip.dtype != torch.float32 or not skip.is_contiguous():
+            raise ValueError("skip must be contiguous float32")
+        a.skip = ptr(skip, "skip")
+    if prev is not None:
+        a.prev = _linattn_tokens(None, prev.k, prev.v, prev.log_decay, prev.gain, prev.cu_draft, prev.T, n_seq, ptr,
+                                 "previous drafts")
+        if prev.k.dtype != some.dtype or prev.k.shape[-2:] != (a.n_qk_heads, dk) or prev.v.shape[-2:] != (H, dv):
+            raise ValueError("the previous drafts must have the dtype, heads and head sizes of the tokens")
+        _need_int32(prev.accept_len, "accept_len", n=n_seq)
+        a.accept_len = ptr(prev.accept_len, "accept_len")
+    if workspace is not None:
+        a.workspace, a.workspace_bytes = ptr(workspace, "workspace"), workspace.numel() * workspace.element_size()
+    return a
+
+
+def linattn_workspace(q, k, v, log_decay, state, out, cu_seqlens, *, max_seqlen, **kw) -> int:
+    """Bytes of workspace linattn_prefill needs for these arguments on the current device (0 = none)."""
+    a = make_linattn_args(q, k, v, log_decay, state, out, n_seq=cu_seqlens.shape[0] - 1, cu=cu_seqlens, T=max_seqlen,
+                          check_device=False, **kw)
+    return _linattn_workspace(a)
+
+
+def _linattn_workspace(a: LinattnArgs) -> int:
+    n = c_i64(0)
+    rc = load_library().cv_linattn_workspace(ctypes.byref(a), ctypes.byref(n))
+    if rc != 0:
+        raise CvError(rc, "cv_linattn_workspace")
+    return n.value
+
+
+def linattn_prefill(q, k, v, log_decay, state, out, cu_seqlens, *, max_seqlen, gain=None, skip=None, scale=None,
+                    cache_idx=None, has_initial_state=None, err=None, workspace=None, stream=None) -> None:
+    """Queue linear attention with a decay for each head over packed prompts (cv_linattn_prefill).
+
+    q, k [total, n_qk_heads, dk], v and out [total, n_heads, dv] (innermost stride 1, the others free:
+    slices of one conv output will do), log_decay and gain fp32 [total, n_heads], skip fp32 [n_heads],
+    state fp32 [n_slots, n_heads, dk, dv], cu_seqlens int32 [n_seq + 1], max_seqlen a host bound on the
+    lengths; scale defaults to dk**-0.5.  Writes out, state (and err).  workspace: a uint8 buffer of
+    linattn_workspace bytes; by default torch's allocator gives one for the call."""
+    if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
+        raise ValueError("cu_seqlens must be [n_seq + 1]")
+    a = make_linattn_args(q, k, v, log_decay, state, out, n_seq=cu_seqlens.shape[0] - 1, gain=gain, skip=skip,
+                          scale=scale, cu=cu_seqlens, T=max_seqlen, cache_idx=cache_idx,
+                          has_initial_state=has_initial_state, err=err, workspace=workspace)
+    if workspace is None:
+        need = _linattn_workspace(a)
+        if need > 0:
+            import torch
+            if stream is not None and not isinstance(stream, torch.cuda.Stream):
+                raise ValueError("pass workspace with a raw stream handle")
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+            if stream is not None:
+                workspace.record_stream(stream)
+            a.workspace, a.workspace_bytes = workspace.data_ptr(), need
+    rc = load_library().cv_linattn_prefill(ctypes.byref(a), _stream_ptr(stream))
+    if rc != 0:
+        raise CvError(rc, "cv_linattn_prefill")
+
+
+def linattn_step(q, k, v, log_decay, state, out, *, gain=None, skip=None, scale=None, update_state=True, prev=None,
+                 cache_idx=None, has_initial_state=None, cu_draft=None, T=None, err=None, stream=None) -> None:
+    """Queue one step of the same recurrence (cv_linattn_step): T new tokens for each sequence.
+
+    q, k [n_seq, T, n_qk_heads, dk], v and out [n_seq, T, n_heads, dv], log_decay and gain fp32
+    [n_seq, T, n_heads]; with cu_draft packed rows [total, ...], T then being the largest count.
+    prev (LinattnDrafts): the state is first advanced over the accepted drafts of the previous step.
+    update_state False leaves the state there (a verify: pass these tokens as prev next time, or to
+    linattn_commit); True leaves it after the new tokens (decoding)."""
+    n_seq = cu_draft.shape[0] - 1 if cu_draft is not None else q.shape[0]
+    a = make_linattn_args(q, k, v, log_decay, state, out, n_seq=n_seq, gain=gain, skip=skip, scale=scale, cu=cu_draft,
+                          T=T, prev=prev, update_state=update_state, cache_idx=cache_idx,
+                          has_initial_state=has_initial_state, err=err)
+    rc = load_library().cv_linattn_step(ctypes.byref(a), _stream_ptr(stream))
+    if rc != 0:
+        raise CvError(rc, "cv_linattn_step")
+
+
+def linattn_commit(drafts: LinattnDrafts, state, *, cache_idx=None, has_initial_state=None, err=None,
+                   stream=None) -> None:
+    """Queue the commit alone: the state advanced over each sequence's accepted drafts."""
+    n_seq = drafts.accept_len.shape[0]
+    a = make_linattn_args(None, None, None, None, state, None, n_seq=n_seq, prev=drafts, cache_idx=cache_idx,
+                          has_initial_state=has_initial_state, err=err)
+    rc = load_library().cv_linattn_step(ctypes.byref(a), _stream_ptr(stream))
+    if rc != 0:
+        raise CvError(rc, "cv_linattn_step")
+
+
+def make_norm_args(y, out, *, gate=None, gate_act=None, gate_first=False, group=0, post_weight=None, residual=None,
+                   residual_out=None, scale=1.0, channel_scale=None, pre_weight=None, eps=1e-6,
+                   check_device=True) -> NormArgs:
+    """Build cv_norm_args (see block_norm)."""
+    ptr = _dev_ptr if check_device else (lambda t, n, required=True: None if t is None else t.data_ptr())
+    if y.dim() != 2:
+        raise ValueError("y must be [rows, dim]")
+    rows, dim = y.shape
+    act = {"silu": 0, "sigmoid": 1}.get(gate_act or "silu")
+    if act is None:
+        raise ValueError(f"unknown gate activation {gate_act!r}")
+    for t, name in ((gate, "gate"), (out, "out"), (residual, "residual"), (residual_out, "residual_out")):
+        if t is not None:
+            _need_shape(t, name, (rows, dim))
+            if t.stride(1) != 1 and dim > 1:
+                raise ValueError(f"{name} needs a unit channel stride")
+    if y.stride(1) != 1 and dim > 1:
+        raise ValueError("y needs a unit channel stride")
+    for t, name, n in ((post_weight, "post_weight", group), (channel_scale, "channel_scale", dim),
+                       (pre_weight, "pre_weight", dim)):
+        if t is not None:
+            _need_shape(t, name, (n,))
+            if t.dtype != y.dtype or not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous and have the dtype of y")
+    for t in (gate, out):
+        if t is not None and t.dtype != y.dtype:
+            raise TypeError("y, gate and out must share one dtype")
+    if residual is None:
+        if out is None or residual_out is not None or channel_scale is not None or pre_weight is not None:
+            raise ValueError("without a residual, out is required and residual_out, channel_scale and pre_weight "
+                             "have no meaning")
+    elif residual_out is None or residual_out.dtype != residual.dtype:
+        raise ValueError("residual needs residual_out of its dtype")
+    dt = _dtype_code(y)
+    return NormArgs(
+        rows, dim, group, dt, dt if residual is None else _dtype_code(residual), act, int(gate_first), eps, scale,
+        ptr(y, "y"), y.stride(0), ptr(gate, "gate", False), gate.stride(0) if gate is not None else 0,
+        ptr(post_weight, "post_weight", False), ptr(residual, "residual", False),
+        residual.stride(0) if residual is not None else 0, ptr(residual_out, "residual_out", False),
+        residual_out.stride(0) if residual_out is not None else 0, ptr(channel_scale, "channel_scale", False),
+        ptr(pre_weight, "pre_weight", False), ptr(out, "out", False), out.stride(0) if out is not None else 0)
+
+
+def block_norm(y, out, *, gate=None, gate_act=None, gate_first=False, group=0, post_weight=None, residual=None,
+               residual_out=None, scale=1.0, channel_scale=None, pre_weight=None, eps=1e-6, stream=None) -> None:
+    """Queue the norms around a block with its gate and scaled residual (cv_block_norm).
+
+    y [rows, dim] is gated by gate (gate_act "silu" or "sigmoid"; before the norm with gate_first, else
+    after) and RMS-normed over groups of ``group`` channels (0: not at all) with post_weight [group].
+    Without residual, out receives that.  With residual (fp32 or the dtype of y), residual_out receives
+    residual + scale * channel_scale * that, and out (may be None) its RMS norm over the row with
+    pre_weight [dim].  Row strides are free, channels contiguous; out may be y or gate, and residual_out
+    may be residual."""
+    a = make_norm_args(y, out, gate=gate, gate_act=gate_act, gate_first=gate_first, group=group,
+                       post_weight=post_weight, residual=residual, residual_out=residual_out, scale=scale,
+                       channel_scale=channel_scale, pre_weight=pre_weight, eps=eps)
+    rc = load_library().cv_block_norm(ctypes.byref(a), _stream_ptr(stream))
+    if rc != 0:
+        raise CvError(rc, "cv_block_norm")

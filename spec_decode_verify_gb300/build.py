@@ -17,9 +17,10 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libconvverify.so")
 INCLUDE = os.path.join(ROOT, "include")
-# the verify library, then (last) the bandwidth probe of bench.py --probe-mix, linked on its own
+# the library (conv, linear attention, block norms), then (last) the bandwidth probe of bench.py --probe-mix, linked on its own
 SOURCES = (["cv_abi.cu"] + [f"cv_inst_{d}_w{w}.cu" for d in ("bf16", "f32") for w in (2, 3, 4)] +
-           [f"cv_inst_varlen_{d}_w{w}.cu" for d in ("bf16", "f32") for w in (2, 3, 4)] + ["cv_probe.cu"])
+           [f"cv_inst_varlen_{d}_w{w}.cu" for d in ("bf16", "f32") for w in (2, 3, 4)] +
+           ["cv_abi_layer.cu", "cv_linattn_step.cu", "cv_norm.cu", "cv_probe.cu"])
 PROBE_LIB = os.path.join(BUILD, "libcvprobe.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",

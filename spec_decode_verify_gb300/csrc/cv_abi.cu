@@ -13,15 +13,23 @@
 //                             takes it when its state rows are the packed [dim][T+W-2] rows, and
 //                             the general kernel otherwise.  Mixed dtypes (state and snapshots in
 //                             the other dtype) take it for T <= 8, the general kernel otherwise.
-#include <atomic>
 #include <cstdint>
 #include <cstring>
 
 #include "convverify.h"
+#include "cv_host.h"
 #include "cv_launch.h"
 #include "cv_verify_tree.cuh"  // tree_buffer_bytes
 
 namespace {
+
+using cvk::aligned16;
+using cvk::DeviceLimits;
+using cvk::device_limits;
+using cvk::ensure_smem;
+using cvk::launch_pdl;
+using cvk::pow2;
+using cvk::stride16;
 
 constexpr int kFastThreads = 128;
 constexpr int kFastThreadsMax = 256;   // the one-pass kernel's launch bound (threads x token groups)
@@ -56,41 +64,6 @@ constexpr int kPrefillMaxChunk = 128;  // tokens per prefill block, at most / at
 constexpr int kPrefillMinChunk = 32;   // the kernel's 8-token batch, and >= W-1)
 constexpr int kPrefillRing = 4;        // batches of staged x rows per prefill thread (as the kernel's)
 
-// The device the launch plans size for: SM count (the persistent grids), shared memory per SM
-// (residency) and per block (opt-in maximum), queried once per device and cached.  Without a
-// usable device (cv_verify_plan on a host without a GPU) the plans are made for a GB300: 152 SMs,
-// 228 KB per SM, 227 KB per block.
-struct DeviceLimits {
-    int sms, smem_per_sm, smem_per_block;
-};
-DeviceLimits device_limits() {
-    constexpr DeviceLimits kGB300{152, 232448, 227 * 1024};
-    constexpr int kMaxDevices = 64;
-    static std::atomic<int> cached[kMaxDevices][3];  // zero until queried
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) {
-        cudaGetLastError();  // clear the error the failed query recorded
-        return kGB300;
-    }
-    if (dev < kMaxDevices && cached[dev][0].load(std::memory_order_acquire) > 0)
-        return {cached[dev][0].load(std::memory_order_relaxed), cached[dev][1].load(std::memory_order_relaxed),
-                cached[dev][2].load(std::memory_order_relaxed)};
-    DeviceLimits d{0, 0, 0};
-    if (cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&d.smem_per_sm, cudaDevAttrMaxSharedMemoryPerMultiprocessor, dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&d.smem_per_block, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) != cudaSuccess ||
-        d.sms < 1) {
-        cudaGetLastError();
-        return kGB300;
-    }
-    if (dev < kMaxDevices) {
-        cached[dev][1].store(d.smem_per_sm, std::memory_order_relaxed);
-        cached[dev][2].store(d.smem_per_block, std::memory_order_relaxed);
-        cached[dev][0].store(d.sms, std::memory_order_release);
-    }
-    return d;
-}
-
 // Tokens per unit of the pipelined kernel for packed drafts: the whole draft when T <= 8, else
 // chunks of 8 (so any T runs with the registers of an 8-token unit); T otherwise.
 constexpr int kVarlenChunk = 8;
@@ -106,10 +79,6 @@ long long pipe_list_len(const cv_verify_args *a) {
 bool pipe_compacts(const cv_verify_args *a) {
     return (a->cache_idx != nullptr || a->cu_draft != nullptr) && pipe_list_len(a) <= kCompactMaxEntries;
 }
-
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-bool stride16(long long stride_elems, int esize) { return ((stride_elems * esize) & 15) == 0; }
-bool pow2(int v) { return v > 0 && (v & (v - 1)) == 0; }
 
 const cvk::KernelSet &kernel_set(int dtype, int width) {
     if (dtype == CV_BF16) {
@@ -420,46 +389,6 @@ int plan_verify(const cv_verify_args *a, cv_launch_plan *pl) {
     pl->grid_x = (a->dim + pl->channels_per_block - 1) / pl->channels_per_block;
     pl->grid_y = a->n_seq;
     return CV_OK;
-}
-
-// Launch with programmatic stream serialization: the kernel may be scheduled while the previous
-// grid in the stream finishes; every kernel waits (griddepcontrol.wait) for that grid's completion
-// before its first global-memory access, so the order of the stream's work is kept.
-template <typename P>
-cudaError_t launch_pdl(void (*kernel)(P), dim3 grid, dim3 block, int smem, cudaStream_t stream, const P &p) {
-    cudaLaunchConfig_t cfg;
-    std::memset(&cfg, 0, sizeof cfg);
-    cfg.gridDim = grid;
-    cfg.blockDim = block;
-    cfg.dynamicSmemBytes = (size_t)smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    std::memset(attr, 0, sizeof attr);
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, p);
-}
-
-// Opt a kernel into more than 48 KB of dynamic shared memory (once per kernel and device).
-cudaError_t ensure_smem(const void *kernel, int bytes) {
-    if (bytes <= 48 * 1024) return cudaSuccess;
-    static std::atomic<unsigned long long> done_cache[64][4];  // tiny open-addressing cache
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    const unsigned long long key = reinterpret_cast<uintptr_t>(kernel) ^ ((unsigned long long)dev << 56);
-    const unsigned h = (unsigned)((key >> 4) * 0x9E3779B1u) & 63u;
-    for (auto &slot : done_cache[h])
-        if (slot.load(std::memory_order_relaxed) == key) return cudaSuccess;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, device_limits().smem_per_block);
-    if (e != cudaSuccess) return e;
-    for (auto &slot : done_cache[h]) {
-        unsigned long long z = 0;
-        if (slot.compare_exchange_strong(z, key)) break;
-    }
-    return cudaSuccess;
 }
 
 int launch_verify(const cv_verify_args *a, const cv_launch_plan &pl, cudaStream_t stream) {
@@ -788,13 +717,14 @@ const char *cv_status_string(int status) {
         case CV_ERR_TOKENS: return "T outside 1..CV_MAX_T";
         case CV_ERR_WIDTH: return "conv width outside 2..4";
         case CV_ERR_DTYPE: return "unknown dtype";
-        case CV_ERR_HEAD_DIM: return "invalid head_dim / qk_channels";
+        case CV_ERR_HEAD_DIM: return "invalid head_dim / qk_channels, head counts or norm group";
         case CV_ERR_LAYOUT:
             return "unknown window layout, dedup step stride != column stride, or history layout passed to commit";
         case CV_ERR_STRIDE: return "negative stride or overlapping state rows";
         case CV_ERR_ALIAS: return "an output buffer has the base address of an input or of the other output";
         case CV_ERR_LAUNCH: return "CUDA launch failed";
         case CV_ERR_SMEM: return "tile does not fit in shared memory";
+        case CV_ERR_WORKSPACE: return "workspace missing, misaligned or too small";
         default: return "unknown status";
     }
 }

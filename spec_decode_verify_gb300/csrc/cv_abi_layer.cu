@@ -1,0 +1,252 @@
+// C ABI of the operators beside the conv: linear attention (prompts, single tokens and drafts) and the
+// block norms.  As for the conv, every check runs on the host before anything is launched.
+#include <cstdint>
+#include <cstring>
+
+#include "convverify.h"
+#include "cv_host.h"
+#include "cv_linattn.h"
+#include "cv_norm.h"
+
+namespace {
+
+using cvk::device_limits;
+using cvk::launch_pdl;
+
+constexpr int kMaxHeads = 4096;
+constexpr int kMaxHeadDim = 256;
+constexpr int kMaxNormDim = 65536;
+
+bool aligned(const void *p, int bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
+int esize_of(int dtype) { return dtype == CV_BF16 ? 2 : 4; }
+
+// ---- linear attention
+
+int check_run(const cv_linattn_tokens &r) {
+    const int64_t strides[] = {r.q_seq_stride, r.q_tok_stride, r.q_head_stride, r.k_seq_stride, r.k_tok_stride,
+                               r.k_head_stride, r.v_seq_stride, r.v_tok_stride, r.v_head_stride, r.decay_seq_stride,
+                               r.decay_tok_stride, r.gain_seq_stride, r.gain_tok_stride};
+    for (int64_t s : strides)
+        if (s < 0) return CV_ERR_STRIDE;
+    if (r.cu && r.total_tokens < 0) return CV_ERR_SHAPE;
+    return CV_OK;
+}
+
+// Whether a run holds any token at all (buffers may be NULL otherwise).
+bool run_empty(const cv_linattn_tokens &r) { return r.T == 0 || (r.cu && r.total_tokens == 0); }
+
+int check_linattn(const cv_linattn_args *a, bool step, bool pointers) {
+    if (!a) return CV_ERR_NULL_ARGS;
+    if (a->dtype != CV_F32 && a->dtype != CV_BF16) return CV_ERR_DTYPE;
+    if (a->n_seq < 0 || a->n_seq > 65535 || a->n_slots < 1 || a->n_heads < 1 || a->n_heads > kMaxHeads)
+        return CV_ERR_SHAPE;
+    if (a->dk < 1 || a->dk > kMaxHeadDim || a->dv < 1 || a->dv > kMaxHeadDim || a->n_qk_heads < 1 ||
+        a->n_heads % a->n_qk_heads != 0)
+        return CV_ERR_HEAD_DIM;
+    if (a->tok.T < 0 || (step && (a->tok.T > CV_MAX_T || a->prev.T < 0 || a->prev.T > CV_MAX_T))) return CV_ERR_TOKENS;
+    int rc = check_run(a->tok);
+    if (rc == CV_OK && step) rc = check_run(a->prev);
+    if (rc != CV_OK) return rc;
+    if (a->out_seq_stride < 0 || a->out_tok_stride < 0 || a->out_head_stride < 0 || a->state_slot_stride < 0 ||
+        a->state_head_stride < 0)
+        return CV_ERR_STRIDE;
+    // heads and slots of the state must not overlap
+    if (a->n_heads > 1 && a->state_head_stride < (int64_t)a->dk * a->dv) return CV_ERR_STRIDE;
+    if (a->n_slots > 1 && a->state_slot_stride < (int64_t)a->dk * a->dv) return CV_ERR_STRIDE;
+    if (!pointers || a->n_seq == 0) return CV_OK;
+    if (!a->state || !aligned(a->state, 4)) return CV_ERR_NULL_POINTER;
+    if (!step && !a->tok.cu) return CV_ERR_NULL_POINTER;
+    if (!run_empty(a->tok)) {
+        if (!a->tok.q || !a->tok.k || !a->tok.v || !a->tok.log_decay || !a->out) return CV_ERR_NULL_POINTER;
+        const void *in[] = {a->tok.q, a->tok.k, a->tok.v, a->tok.log_decay, a->tok.gain, a->state};
+        for (const void *p : in)
+            if (a->out == p) return CV_ERR_ALIAS;
+    }
+    if (step && a->prev.T > 0) {
+        if (!a->accept_len) return CV_ERR_NULL_POINTER;
+        if (!run_empty(a->prev) && (!a->prev.k || !a->prev.v || !a->prev.log_decay)) return CV_ERR_NULL_POINTER;
+    }
+    return CV_OK;
+}
+
+// Four elements at every multiple of 4 channels may be loaded at once.
+bool rows4(const void *p, int64_t seq, int64_t tok, int64_t head, bool packed, int d, int es) {
+    return d % 4 == 0 && aligned(p, 4 * es) && (packed || seq % 4 == 0) && tok % 4 == 0 && head % 4 == 0;
+}
+
+cvk::LinattnRun make_run(const cv_linattn_tokens &t, const cv_linattn_args *a, bool with_q) {
+    const int es = esize_of(a->dtype);
+    cvk::LinattnRun r;
+    std::memset(&r, 0, sizeof r);
+    r.q = t.q, r.q_seq = t.q_seq_stride, r.q_tok = t.q_tok_stride, r.q_head = t.q_head_stride;
+    r.k = t.k, r.k_seq = t.k_seq_stride, r.k_tok = t.k_tok_stride, r.k_head = t.k_head_stride;
+    r.v = t.v, r.v_seq = t.v_seq_stride, r.v_tok = t.v_tok_stride, r.v_head = t.v_head_stride;
+    r.g = t.log_decay, r.g_seq = t.decay_seq_stride, r.g_tok = t.decay_tok_stride;
+    r.b = t.gain, r.b_seq = t.gain_seq_stride, r.b_tok = t.gain_tok_stride;
+    r.cu = t.cu, r.T = t.T, r.total = t.total_tokens;
+    r.vec = rows4(t.k, r.k_seq, r.k_tok, r.k_head, t.cu, a->dk, es) &&
+            rows4(t.v, r.v_seq, r.v_tok, r.v_head, t.cu, a->dv, es) &&
+            (!with_q || rows4(t.q, r.q_seq, r.q_tok, r.q_head, t.cu, a->dk, es));
+    return r;
+}
+
+cvk::LinattnParams make_linattn(const cv_linattn_args *a, bool step) {
+    cvk::LinattnParams p;
+    std::memset(&p, 0, sizeof p);
+    p.tok = make_run(a->tok, a, true);
+    if (step) p.prev = make_run(a->prev, a, false);
+    p.skip = a->skip;
+    p.out = a->out, p.o_seq = a->out_seq_stride, p.o_tok = a->out_tok_stride, p.o_head = a->out_head_stride;
+    p.state = a->state, p.st_slot = a->state_slot_stride, p.st_head = a->state_head_stride;
+    p.cache_idx = a->cache_idx, p.has_init = a->has_initial_state, p.err = a->err;
+    p.accept = step ? a->accept_len : nullptr;
+    p.n_seq = a->n_seq, p.n_heads = a->n_heads, p.n_qk = a->n_qk_heads, p.dk = a->dk, p.dv = a->dv;
+    p.n_slots = a->n_slots;
+    p.bf16 = a->dtype == CV_BF16;
+    p.update = step ? a->update_state != 0 : 1;
+    p.st_vec = a->dv % 4 == 0 && aligned(a->state, 16) && a->state_slot_stride % 4 == 0 && a->state_head_stride % 4 == 0;
+    p.scale = a->scale;
+    return p;
+}
+
+int launch_recurrent(const cv_linattn_args *a, bool step, cudaStream_t stream) {
+    cvk::LinattnParams p = make_linattn(a, step);
+    // the widest slice of a head whose grid still gives every SM two blocks
+    int vs = a->dk <= 128 && a->dv > 64 ? 128 : a->dv > 32 ? 64 : 32;
+    const long long heads = (long long)a->n_seq * a->n_heads;
+    while (vs > 32 && heads * ((a->dv + vs - 1) / vs) < 2LL * device_limits().sms) vs /= 2;
+    p.slices = (a->dv + vs - 1) / vs;
+    const int most = step && a->prev.T > a->tok.T ? a->prev.T : a->tok.T;
+    const cvk::StepKernel k = cvk::step_kernel(vs, a->dk, most <= 1 ? 1 : most <= 4 ? 4 : cvk::kStepMaxGroup);
+    if (cvk::ensure_smem(reinterpret_cast<const void *>(k.fn), k.smem_bytes) != cudaSuccess) return CV_ERR_LAUNCH;
+    if (launch_pdl(k.fn, dim3((unsigned)(heads * p.slices)), dim3(cvk::kStepThreads), k.smem_bytes, stream, p) !=
+        cudaSuccess)
+        return CV_ERR_LAUNCH;
+    return cudaGetLastError() == cudaSuccess ? CV_OK : CV_ERR_LAUNCH;
+}
+
+// ---- block norm
+
+int check_norm(const cv_norm_args *a) {
+    if (!a) return CV_ERR_NULL_ARGS;
+    if (a->dtype != CV_F32 && a->dtype != CV_BF16) return CV_ERR_DTYPE;
+    if (a->residual && a->residual_dtype != a->dtype && a->residual_dtype != CV_F32) return CV_ERR_DTYPE;
+    if (a->rows < 0 || a->dim < 1 || a->dim > kMaxNormDim) return CV_ERR_SHAPE;
+    if (a->group < 0 || (a->group > 0 && a->dim % a->group != 0) || (a->group == 0 && a->post_weight))
+        return CV_ERR_HEAD_DIM;
+    if (a->gate && a->gate_act != CV_GATE_SILU && a->gate_act != CV_GATE_SIGMOID) return CV_ERR_LAYOUT;
+    if (a->y_stride < 0 || a->gate_stride < 0 || a->residual_stride < 0) return CV_ERR_STRIDE;
+    if ((a->out && a->rows > 1 && a->out_stride < a->dim) ||
+        (a->residual && a->rows > 1 && a->residual_out_stride < a->dim))
+        return CV_ERR_STRIDE;
+    if (a->rows == 0) return CV_OK;
+    if (!a->y || (a->residual ? !a->residual_out : !a->out)) return CV_ERR_NULL_POINTER;
+    if (a->out) {
+        if (a->out == a->residual || a->out == a->residual_out || a->out == a->post_weight || a->out == a->pre_weight ||
+            a->out == a->channel_scale || (a->out == a->y && a->out_stride != a->y_stride) ||
+            (a->out == a->gate && a->out_stride != a->gate_stride))
+            return CV_ERR_ALIAS;
+    }
+    if (a->residual &&
+        (a->residual_out == a->y || a->residual_out == a->gate || a->residual_out == a->post_weight ||
+         a->residual_out == a->pre_weight || a->residual_out == a->channel_scale ||
+         (a->residual_out == a->residual && a->residual_out_stride != a->residual_stride)))
+        return CV_ERR_ALIAS;
+    return CV_OK;
+}
+
+// A row buffer that may be absent: V elements of es bytes per 16-byte access at every multiple of V.
+bool vec_row(const void *p, int64_t stride, int64_t rows, int es) {
+    return !p || (aligned(p, 16) && (rows <= 1 || (stride * es) % 16 == 0));
+}
+
+int launch_norm(const cv_norm_args *a, cudaStream_t stream) {
+    const int es = esize_of(a->dtype), V = 16 / es;
+    const bool res = a->residual != nullptr, res32 = res && a->residual_dtype == CV_F32;
+    cvk::NormParams p;
+    std::memset(&p, 0, sizeof p);
+    p.rows = a->rows, p.dim = a->dim, p.group = a->group;
+    p.gate_act = a->gate_act, p.gate_first = a->gate_first != 0;
+    p.eps = a->eps, p.scale = a->scale;
+    p.y = a->y, p.gate = a->gate, p.post = a->post_weight;
+    p.res = a->residual, p.cs = res ? a->channel_scale : nullptr, p.pre = res ? a->pre_weight : nullptr;
+    p.out = a->out, p.res_out = res ? a->residual_out : nullptr;
+    p.y_row = a->y_stride, p.gate_row = a->gate_stride, p.res_row = a->residual_stride;
+    p.res_out_row = a->residual_out_stride, p.out_row = a->out_stride;
+    const bool vec = vec_row(p.y, p.y_row, a->rows, es) && vec_row(p.gate, p.gate_row, a->rows, es) &&
+                     vec_row(p.out, p.out_row, a->rows, es) && vec_row(p.res, p.res_row, a->rows, res32 ? 4 : es) &&
+                     vec_row(p.res_out, p.res_out_row, a->rows, res32 ? 4 : es) && vec_row(p.post, 0, 1, es) &&
+                     vec_row(p.cs, 0, 1, es) && vec_row(p.pre, 0, 1, es);
+    const bool bf16 = a->dtype == CV_BF16;
+
+    // narrow groups without a residual: up to 32 lanes a group
+    if (!res && a->group > 0) {
+        const bool v = vec && a->group % V == 0;
+        const int per = v ? V : 1, most = v ? 2 : 16;
+        if (a->group <= 32 * per * most) {
+            const int need = (a->group + per - 1) / per;  // accesses a group
+            p.lanes = 1;
+            while (p.lanes < 32 && p.lanes < need) p.lanes *= 2;
+            const long long groups = a->rows * (a->dim / a->group);
+            const int per_block = cvk::kNormGroupThreads / p.lanes;
+            const long long blocks = (groups + per_block - 1) / per_block, cap = 16LL * device_limits().sms;
+            const auto k = cvk::norm_groups_kernel(bf16, v, (need + p.lanes - 1) / p.lanes);
+            if (launch_pdl(k, dim3((unsigned)(blocks < cap ? blocks : cap)), dim3(cvk::kNormGroupThreads), 0, stream,
+                           p) != cudaSuccess)
+                return CV_ERR_LAUNCH;
+            return cudaGetLastError() == cudaSuccess ? CV_OK : CV_ERR_LAUNCH;
+        }
+    }
+    const unsigned grid = (unsigned)(a->rows < 0x7fffffff ? a->rows : 0x7fffffff);
+    if ((a->group == 0 || a->group == a->dim) && a->dim <= cvk::kNormRowThreads * cvk::kNormRowElems) {
+        const bool v = vec && a->dim % V == 0;
+        int elems = 8;
+        while (elems < cvk::kNormRowElems && elems * cvk::kNormRowThreads < a->dim) elems *= 2;
+        const int threads = (a->dim + elems - 1) / elems;
+        if (launch_pdl(cvk::norm_row_kernel(bf16, res32, v, elems), dim3(grid), dim3((threads + 31) / 32 * 32), 0,
+                       stream, p) != cudaSuccess)
+            return CV_ERR_LAUNCH;
+        return cudaGetLastError() == cudaSuccess ? CV_OK : CV_ERR_LAUNCH;
+    }
+    const int groups = a->group > 0 ? a->dim / a->group : 0, smem = (cvk::kNormAnyThreads / 32 + groups) * 4;
+    const auto k = cvk::norm_any_kernel(bf16, res32);
+    if (smem > device_limits().smem_per_block) return CV_ERR_SMEM;
+    if (cvk::ensure_smem(reinterpret_cast<const void *>(k), smem) != cudaSuccess) return CV_ERR_LAUNCH;
+    if (launch_pdl(k, dim3(grid), dim3(cvk::kNormAnyThreads), smem, stream, p) != cudaSuccess) return CV_ERR_LAUNCH;
+    return cudaGetLastError() == cudaSuccess ? CV_OK : CV_ERR_LAUNCH;
+}
+
+}  // namespace
+
+extern "C" {
+
+int cv_linattn_workspace(const cv_linattn_args *args, int64_t *bytes) {
+    if (!bytes) return CV_ERR_NULL_POINTER;
+    const int rc = check_linattn(args, false, false);
+    if (rc != CV_OK) return rc;
+    *bytes = 0;
+    return CV_OK;
+}
+
+int cv_linattn_prefill(const cv_linattn_args *args, void *stream) {
+    const int rc = check_linattn(args, false, true);
+    if (rc != CV_OK) return rc;
+    if (args->n_seq == 0) return CV_OK;
+    return launch_recurrent(args, false, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int cv_linattn_step(const cv_linattn_args *args, void *stream) {
+    const int rc = check_linattn(args, true, true);
+    if (rc != CV_OK) return rc;
+    if (args->n_seq == 0) return CV_OK;
+    return launch_recurrent(args, true, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int cv_block_norm(const cv_norm_args *args, void *stream) {
+    const int rc = check_norm(args);
+    if (rc != CV_OK) return rc;
+    if (args->rows == 0) return CV_OK;
+    return launch_norm(args, reinterpret_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

@@ -1,0 +1,61 @@
+// Internal: parameters and kernel tables of the linear-attention kernels.
+#pragma once
+
+#include <cuda_runtime.h>
+
+namespace cvk {
+
+// One run of tokens per sequence (cv_linattn_tokens).
+struct LinattnRun {
+    const void *q, *k, *v;
+    long long q_seq, q_tok, q_head;
+    long long k_seq, k_tok, k_head;
+    long long v_seq, v_tok, v_head;
+    const float *g;
+    long long g_seq, g_tok;
+    const float *b;
+    long long b_seq, b_tok;
+    const int *cu;
+    int T, total;
+    int vec;  // rows of q, k and v allow loads of 4 elements at multiples of 4 (checked on the host)
+};
+
+struct LinattnParams {
+    LinattnRun tok, prev;
+    const float *skip;
+    void *out;
+    long long o_seq, o_tok, o_head;
+    float *state;
+    long long st_slot, st_head;
+    const int *cache_idx;
+    const int *has_init;
+    const int *accept;
+    int *err;
+    int n_seq, n_heads, n_qk, dk, dv, n_slots;
+    int bf16;    // dtype of q, k, v and out: bf16, else fp32
+    int update;  // leave the state after the tokens
+    int st_vec;  // state rows allow 16-byte accesses (checked on the host)
+    int slices;  // column slices of a head's state, one block each
+    float scale;
+};
+
+constexpr int kStepThreads = 256;
+constexpr int kStepMaxGroup = 8;  // tokens per pass over the state tile, at most
+
+// Shared memory of linattn_step<VS, R, TG>, in floats: q, k [rows][TG], v [TG][VS], the warps' partial
+// outputs [row groups][TG][VS], the token products [TG][TG], the decays and gains [TG] each.
+__host__ __device__ constexpr int step_smem_floats(int VS, int R, int TG) {
+    return 2 * (R * (kStepThreads / (VS / 4))) * TG + TG * VS + 4 * kStepThreads * TG + TG * TG + 2 * TG;
+}
+
+using LinattnKernel = void (*)(LinattnParams);
+
+// The recurrent kernel for slices of VS columns and at most rows_max state rows, TG tokens a pass.
+struct StepKernel {
+    LinattnKernel fn;
+    int rows_max, smem_bytes;
+};
+// vs: 128, 64 or 32; tg: 1, 4 or 8; dk <= 256 (128 with vs 128).
+StepKernel step_kernel(int vs, int dk, int tg);
+
+}  // namespace cvk

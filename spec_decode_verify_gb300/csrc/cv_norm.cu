@@ -1,0 +1,314 @@
+// The RMS norms around a block, fused with its gate and its scaled residual.
+//
+// Per row:  a = y [* act(z)];  a *= rsqrt(mean_group a^2 + eps) * w_post;  a [*= act(z)];
+//           r = res + scale * cs * a;  out = r * rsqrt(mean_row r^2 + eps) * w_pre.
+// Sums are fp32 in a fixed order (per thread, a shuffle tree, then the warps in order), so a row's
+// bits do not depend on the other rows.  r enters the second norm unrounded.  Every tensor is read
+// and written once: the kernels are bound by HBM (large calls) or by latency (a few rows).
+//   norm_groups  no residual, narrow groups (a norm for each head): a group's elements sit in up to
+//                32 lanes of one warp, 16 bytes a lane, so no shared memory and no barrier
+//   norm_row     a block a row, the row's values in registers between the two norms
+//   norm_any     a block a row, values read again (from L1/L2) for each pass: rows too wide for
+//                registers and residual rows with several groups
+#include "cv_device.cuh"
+#include "cv_norm.h"
+
+namespace cvk {
+namespace {
+
+// V consecutive elements as fp32 (V * sizeof(B) is 16 or 32 bytes in 16-byte accesses, or V = 1).
+template <typename B, int V>
+__device__ __forceinline__ void load_run(float *r, const void *base, long long i) {
+    const B *p = reinterpret_cast<const B *>(base) + i;
+    if constexpr (V == 1) {
+        r[0] = widen<B>(*p);
+    } else {
+        constexpr int W = V * (int)sizeof(B) / 4;
+        uint32_t w[W];
+        ldv<16, W>(w, p);
+#pragma unroll
+        for (int j = 0; j < V; ++j) r[j] = elem_f<B>(w, j);
+    }
+}
+template <typename B, int V>
+__device__ __forceinline__ void store_run(void *base, long long i, const float *r) {
+    B *p = reinterpret_cast<B *>(base) + i;
+    if constexpr (V == 1) {
+        *p = narrow<B>(r[0]);
+    } else {
+        constexpr int W = V * (int)sizeof(B) / 4;
+        uint32_t w[W];
+#pragma unroll
+        for (int j = 0; j < W; ++j) {
+            if constexpr (sizeof(B) == 2)
+                w[j] = pack_halves(narrow<uint16_t>(r[2 * j]), narrow<uint16_t>(r[2 * j + 1]));
+            else
+                w[j] = __float_as_uint(r[j]);
+        }
+        stv<16, W>(p, w);
+    }
+}
+
+__device__ __forceinline__ float gate_of(float z, int act) {
+    const float s = 1.0f / (1.0f + expf(-z));
+    return act == 0 ? z * s : s;
+}
+
+template <typename B, int V, int NV>
+__global__ void __launch_bounds__(kNormGroupThreads) norm_groups(const __grid_constant__ NormParams p) {
+    grid_dep_wait();
+    grid_dep_launch();
+    const int lane = threadIdx.x % p.lanes;  // within the group
+    const int per_row = p.dim / p.group;
+    const long long total = p.rows * per_row;
+    const long long step = (long long)gridDim.x * (kNormGroupThreads / p.lanes);
+    // whole warps walk the groups together, so the shuffles below always have all lanes
+    long long gi = (long long)blockIdx.x * (kNormGroupThreads / p.lanes) + threadIdx.x / p.lanes;
+    const long long rounds = (total + step - 1) / step;
+    for (long long it = 0; it < rounds; ++it, gi += step) {
+        const bool on = gi < total;
+        const long long row = on ? gi / per_row : 0;
+        const int c0 = on ? (int)(gi % per_row) * p.group : 0;
+        float a[NV][V], g[NV][V], sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * p.lanes + lane) * V;
+            const bool in = on && c < p.group;
+#pragma unroll
+            for (int j = 0; j < V; ++j) a[i][j] = 0.0f, g[i][j] = 1.0f;
+            if (in) {
+                load_run<B, V>(a[i], p.y, row * p.y_row + c0 + c);
+                if (p.gate) load_run<B, V>(g[i], p.gate, row * p.gate_row + c0 + c);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                if (p.gate) g[i][j] = gate_of(g[i][j], p.gate_act);
+                if (p.gate_first) a[i][j] *= g[i][j];
+                sum = fmaf(a[i][j], a[i][j], sum);
+            }
+        for (int o = p.lanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        const float inv = rsqrtf(sum / (float)p.group + p.eps);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * p.lanes + lane) * V;
+            if (!on || c >= p.group) continue;
+            float w[V];
+            if (p.post) load_run<B, V>(w, p.post, c);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                float u = a[i][j] * inv;
+                if (p.post) u *= w[j];
+                if (!p.gate_first) u *= g[i][j];
+                a[i][j] = u;
+            }
+            store_run<B, V>(p.out, row * p.out_row + c0 + c, a[i]);
+        }
+    }
+}
+
+// Sum over the block, the same for every thread (warps added in order).
+__device__ __forceinline__ float block_sum(float v, float *sh) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    const int nw = (blockDim.x + 31) / 32;
+    if (nw == 1) return v;
+    __syncthreads();  // the last use of sh is over
+    if (threadIdx.x % 32 == 0) sh[threadIdx.x / 32] = v;
+    __syncthreads();
+    v = 0.0f;
+    for (int i = 0; i < nw; ++i) v += sh[i];
+    return v;
+}
+
+template <typename B, typename RB, int V, int NV>
+__global__ void __launch_bounds__(kNormRowThreads) norm_row(const __grid_constant__ NormParams p) {
+    __shared__ float sh[kNormRowThreads / 32];
+    grid_dep_wait();
+    grid_dep_launch();
+    const int nt = blockDim.x;
+    for (long long row = blockIdx.x; row < p.rows; row += gridDim.x) {
+        float a[NV][V], g[NV][V], r[NV][V];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * nt + threadIdx.x) * V;
+#pragma unroll
+            for (int j = 0; j < V; ++j) a[i][j] = 0.0f, g[i][j] = 1.0f, r[i][j] = 0.0f;
+            if (c < p.dim) {
+                load_run<B, V>(a[i], p.y, row * p.y_row + c);
+                if (p.gate) load_run<B, V>(g[i], p.gate, row * p.gate_row + c);
+                if (p.res) load_run<RB, V>(r[i], p.res, row * p.res_row + c);
+            }
+        }
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                if (p.gate) g[i][j] = gate_of(g[i][j], p.gate_act);
+                if (p.gate_first) a[i][j] *= g[i][j];
+                sum = fmaf(a[i][j], a[i][j], sum);
+            }
+        const float inv = p.group > 0 ? rsqrtf(block_sum(sum, sh) / (float)p.dim + p.eps) : 1.0f;
+        sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * nt + threadIdx.x) * V;
+            if (c >= p.dim) continue;
+            float w[V], cs[V];
+            if (p.post) load_run<B, V>(w, p.post, c);
+            if (p.cs) load_run<B, V>(cs, p.cs, c);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                float u = a[i][j] * inv;
+                if (p.post) u *= w[j];
+                if (!p.gate_first) u *= g[i][j];
+                if (p.res) {
+                    const float f = p.cs ? p.scale * cs[j] : p.scale;
+                    u = fmaf(f, u, r[i][j]);
+                    sum = fmaf(u, u, sum);
+                }
+                a[i][j] = u;
+            }
+            store_run<RB, V>(p.res ? p.res_out : p.out, row * (p.res ? p.res_out_row : p.out_row) + c, a[i]);
+        }
+        if (p.res && p.out) {
+            const float inv2 = rsqrtf(block_sum(sum, sh) / (float)p.dim + p.eps);
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int c = (i * nt + threadIdx.x) * V;
+                if (c >= p.dim) continue;
+                float w[V];
+                if (p.pre) load_run<B, V>(w, p.pre, c);
+#pragma unroll
+                for (int j = 0; j < V; ++j) a[i][j] = a[i][j] * inv2 * (p.pre ? w[j] : 1.0f);
+                store_run<B, V>(p.out, row * p.out_row + c, a[i]);
+            }
+        }
+    }
+}
+
+template <typename B, typename RB>
+__global__ void __launch_bounds__(kNormAnyThreads) norm_any(const __grid_constant__ NormParams p) {
+    extern __shared__ float sh[];  // the warps' sums, then one factor per group
+    float *const inv = sh + kNormAnyThreads / 32;
+    grid_dep_wait();
+    grid_dep_launch();
+    const int tid = threadIdx.x, lane = tid % 32;
+    const int n_groups = p.group > 0 ? p.dim / p.group : 0;
+    for (long long row = blockIdx.x; row < p.rows; row += gridDim.x) {
+        auto gate = [&](int c) {
+            float z;
+            load_run<B, 1>(&z, p.gate, row * p.gate_row + c);
+            return gate_of(z, p.gate_act);
+        };
+        auto value = [&](int c) {  // the first norm's input
+            float v;
+            load_run<B, 1>(&v, p.y, row * p.y_row + c);
+            return p.gate && p.gate_first ? v * gate(c) : v;
+        };
+        // narrow groups: a warp each; a few wide ones: the whole block on each
+        if (n_groups >= kNormAnyThreads / 32) {
+            for (int g = tid / 32; g < n_groups; g += kNormAnyThreads / 32) {
+                float sum = 0.0f;
+                for (int c = lane; c < p.group; c += 32) {
+                    const float v = value(g * p.group + c);
+                    sum = fmaf(v, v, sum);
+                }
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                if (lane == 0) inv[g] = rsqrtf(sum / (float)p.group + p.eps);
+            }
+        } else {
+            for (int g = 0; g < n_groups; ++g) {
+                float sum = 0.0f;
+                for (int c = tid; c < p.group; c += kNormAnyThreads) {
+                    const float v = value(g * p.group + c);
+                    sum = fmaf(v, v, sum);
+                }
+                sum = block_sum(sum, sh);
+                if (tid == 0) inv[g] = rsqrtf(sum / (float)p.group + p.eps);
+            }
+        }
+        __syncthreads();
+        auto first = [&](int c) {  // after the first norm and the gate
+            float u = value(c), w;
+            if (p.group > 0) u *= inv[c / p.group];
+            if (p.post) {
+                load_run<B, 1>(&w, p.post, c % p.group);
+                u *= w;
+            }
+            return p.gate && !p.gate_first ? u * gate(c) : u;
+        };
+        auto resid = [&](int c) {
+            float r, f;
+            load_run<RB, 1>(&r, p.res, row * p.res_row + c);
+            if (p.cs) load_run<B, 1>(&f, p.cs, c);
+            return fmaf(p.cs ? p.scale * f : p.scale, first(c), r);
+        };
+        if (!p.res) {
+            for (int c = tid; c < p.dim; c += kNormAnyThreads) {
+                const float u = first(c);
+                store_run<B, 1>(p.out, row * p.out_row + c, &u);
+            }
+        } else {
+            float sum = 0.0f, inv2 = 1.0f;
+            if (p.out) {
+                for (int c = tid; c < p.dim; c += kNormAnyThreads) {
+                    const float r = resid(c);
+                    sum = fmaf(r, r, sum);
+                }
+                inv2 = rsqrtf(block_sum(sum, sh) / (float)p.dim + p.eps);
+            }
+            // each thread reads its channel once more before it writes it: in-place calls are safe
+            for (int c = tid; c < p.dim; c += kNormAnyThreads) {
+                const float r = resid(c);
+                store_run<RB, 1>(p.res_out, row * p.res_out_row + c, &r);
+                if (p.out) {
+                    float x = r * inv2, w;
+                    if (p.pre) {
+                        load_run<B, 1>(&w, p.pre, c);
+                        x *= w;
+                    }
+                    store_run<B, 1>(p.out, row * p.out_row + c, &x);
+                }
+            }
+        }
+        __syncthreads();  // inv and sh are free for the next row
+    }
+}
+
+template <typename B, typename RB, int V>
+NormKernel pick_row(int elems) {
+    if (elems == 8) return norm_row<B, RB, V, 8 / V>;
+    if (elems == 16) return norm_row<B, RB, V, 16 / V>;
+    return norm_row<B, RB, V, 32 / V>;
+}
+
+}  // namespace
+
+NormKernel norm_groups_kernel(bool bf16, bool vec, int nv) {
+    if (bf16) {
+        if (vec) return nv == 1 ? norm_groups<uint16_t, 8, 1> : norm_groups<uint16_t, 8, 2>;
+        return nv <= 4 ? norm_groups<uint16_t, 1, 4> : norm_groups<uint16_t, 1, 16>;
+    }
+    if (vec) return nv == 1 ? norm_groups<uint32_t, 4, 1> : norm_groups<uint32_t, 4, 2>;
+    return nv <= 4 ? norm_groups<uint32_t, 1, 4> : norm_groups<uint32_t, 1, 16>;
+}
+
+NormKernel norm_row_kernel(bool bf16, bool res_f32, bool vec, int elems) {
+    if (bf16) {
+        if (res_f32) return vec ? pick_row<uint16_t, uint32_t, 8>(elems) : pick_row<uint16_t, uint32_t, 1>(elems);
+        return vec ? pick_row<uint16_t, uint16_t, 8>(elems) : pick_row<uint16_t, uint16_t, 1>(elems);
+    }
+    return vec ? pick_row<uint32_t, uint32_t, 4>(elems) : pick_row<uint32_t, uint32_t, 1>(elems);
+}
+
+NormKernel norm_any_kernel(bool bf16, bool res_f32) {
+    if (!bf16) return norm_any<uint32_t, uint32_t>;
+    return res_f32 ? norm_any<uint16_t, uint32_t> : norm_any<uint16_t, uint16_t>;
+}
+
+}  // namespace cvk

@@ -1,0 +1,33 @@
+// Internal: parameters and kernel tables of the block norms.
+#pragma once
+
+#include <cuda_runtime.h>
+
+namespace cvk {
+
+struct NormParams {
+    long long rows;
+    int dim, group;
+    int gate_act, gate_first;
+    float eps, scale;
+    const void *y, *gate, *post, *res, *cs, *pre;
+    void *out, *res_out;
+    long long y_row, gate_row, res_row, res_out_row, out_row;
+    int lanes;  // norm_groups: lanes per group (a power of two, at most 32)
+};
+
+using NormKernel = void (*)(NormParams);
+
+constexpr int kNormGroupThreads = 256;
+constexpr int kNormRowThreads = 512;  // norm_row: threads a row, at most
+constexpr int kNormRowElems = 32;     // norm_row: elements a thread, at most
+constexpr int kNormAnyThreads = 256;
+
+// Groups of at most 32 lanes * nv vectors (nv 1 or 2), no residual.
+NormKernel norm_groups_kernel(bool bf16, bool vec, int nv);
+// One block a row, the row in registers (elems = 8, 16 or 32 elements a thread).
+NormKernel norm_row_kernel(bool bf16, bool res_f32, bool vec, int elems);
+// One block a row, the row read again for each pass: any dim and any group.
+NormKernel norm_any_kernel(bool bf16, bool res_f32);
+
+}  // namespace cvk
