@@ -125,6 +125,84 @@ int launch_recurrent(const cv_linattn_args *a, bool step, cudaStream_t stream) {
     return cudaGetLastError() == cudaSuccess ? CV_OK : CV_ERR_LAUNCH;
 }
 
+// The chunked kernel's launch for these arguments; pieces 0: the recurrent kernel takes them.
+struct ChunkPlan {
+    int pieces, seg_len;
+    long long ws_states;  // pieces whose own states go through the workspace
+    int dv_pad;
+};
+constexpr int kMinPieceChunks = 4;
+
+ChunkPlan plan_chunks(const cv_linattn_args *a) {
+    ChunkPlan pl{0, 0, 0, a->dv <= 64 ? 64 : 128};
+    const cv_linattn_tokens &t = a->tok;
+    auto rows8 = [](const void *p, int64_t tok, int64_t head) {
+        return aligned(p, 16) && tok % 8 == 0 && head % 8 == 0;
+    };
+    if (a->dtype != CV_BF16 || a->dk % 8 != 0 || a->dv % 8 != 0 || a->dk > 128 || a->dv > 128 ||
+        !rows8(t.q, t.q_tok_stride, t.q_head_stride) || !rows8(t.k, t.k_tok_stride, t.k_head_stride) ||
+        !rows8(t.v, t.v_tok_stride, t.v_head_stride) || !rows8(a->out, a->out_tok_stride, a->out_head_stride) ||
+        !aligned(a->state, 16) || a->state_slot_stride % 4 != 0 || a->state_head_stride % 4 != 0)
+        return pl;
+    const int64_t longest = t.T < t.total_tokens ? t.T : t.total_tokens;
+    const int64_t whole = (longest + cvk::kChunk - 1) / cvk::kChunk * cvk::kChunk;
+    const int64_t heads = (int64_t)a->n_seq * a->n_heads, sms = device_limits().sms;
+    pl.pieces = 1;
+    pl.seg_len = (int)(whole > 0 ? whole : cvk::kChunk);
+    // Few heads: cut the length into pieces until every SM has one.  A cut costs a pass over k and v for
+    // the pieces' own states, so pieces are not short, and a grid that is mostly full stays uncut.
+    for (int64_t len = (int64_t)kMinPieceChunks * cvk::kChunk; len < whole; len += cvk::kChunk) {
+        const int64_t n = (whole + len - 1) / len;
+        int64_t most = a->n_seq * n;
+        if (t.total_tokens / len + a->n_seq < most) most = t.total_tokens / len + a->n_seq;
+        if (a->n_heads * most > sms || heads * n > 4 * sms) continue;
+        pl.pieces = (int)n;
+        pl.seg_len = (int)len;
+        pl.ws_states = heads * (n - 1);
+        break;
+    }
+    return pl;
+}
+
+int64_t chunk_workspace(const ChunkPlan &pl) {
+    return pl.ws_states * (cvk::kChunk * pl.dv_pad * 4) + (pl.ws_states * 4 + 255) / 256 * 256;
+}
+
+int launch_chunks(const cv_linattn_args *a, const ChunkPlan &pl, cudaStream_t stream) {
+    cvk::LinattnChunkParams p;
+    std::memset(&p, 0, sizeof p);
+    p.a = make_linattn(a, false);
+    p.n_segs = pl.pieces;
+    p.seg_len = pl.seg_len;
+    const int64_t units = (int64_t)a->n_seq * a->n_heads * pl.pieces, sms = device_limits().sms;
+    if (units > 0x7fffffff) return CV_ERR_SHAPE;
+    p.units = (int)units;
+    p.sort = units > sms && a->n_seq <= cvk::kChunkMaxSorted;
+    p.dv_pad = pl.dv_pad;
+    if (pl.ws_states > 0) {
+        if (!a->workspace || !aligned(a->workspace, 256) || a->workspace_bytes < chunk_workspace(pl))
+            return CV_ERR_WORKSPACE;
+        p.ws_state = reinterpret_cast<float *>(a->workspace);
+        p.ws_decay = p.ws_state + pl.ws_states * cvk::kChunk * pl.dv_pad;
+    }
+    const cvk::ChunkKernel k = cvk::chunk_kernel(a->dv);
+    if (cvk::ensure_smem(reinterpret_cast<const void *>(k.fn), k.smem_bytes) != cudaSuccess) return CV_ERR_LAUNCH;
+    // the kernel ORs its bits into err
+    if (a->err && cudaMemsetAsync(a->err, 0, sizeof(int32_t) * (size_t)a->n_seq, stream) != cudaSuccess)
+        return CV_ERR_LAUNCH;
+    const dim3 grid((unsigned)(units < sms ? units : sms)), block(cvk::kChunkThreads);
+    if (pl.ws_states > 0) {
+        p.state_only = 1;
+        if (launch_pdl(k.fn, grid, block, k.smem_bytes, stream, p) != cudaSuccess) return CV_ERR_LAUNCH;
+        p.state_only = 0;
+        const unsigned parts = (unsigned)(a->n_seq * (int64_t)a->n_heads * (pl.dv_pad / 4));
+        if (launch_pdl(cvk::chunk_join_kernel(), dim3(parts), dim3(cvk::kJoinThreads), 0, stream, p) != cudaSuccess)
+            return CV_ERR_LAUNCH;
+    }
+    if (launch_pdl(k.fn, grid, block, k.smem_bytes, stream, p) != cudaSuccess) return CV_ERR_LAUNCH;
+    return cudaGetLastError() == cudaSuccess ? CV_OK : CV_ERR_LAUNCH;
+}
+
 // ---- block norm
 
 int check_norm(const cv_norm_args *a) {
@@ -224,7 +302,7 @@ int cv_linattn_workspace(const cv_linattn_args *args, int64_t *bytes) {
     if (!bytes) return CV_ERR_NULL_POINTER;
     const int rc = check_linattn(args, false, false);
     if (rc != CV_OK) return rc;
-    *bytes = 0;
+    *bytes = args->n_seq > 0 ? chunk_workspace(plan_chunks(args)) : 0;
     return CV_OK;
 }
 
@@ -232,6 +310,8 @@ int cv_linattn_prefill(const cv_linattn_args *args, void *stream) {
     const int rc = check_linattn(args, false, true);
     if (rc != CV_OK) return rc;
     if (args->n_seq == 0) return CV_OK;
+    const ChunkPlan pl = plan_chunks(args);
+    if (pl.pieces > 0) return launch_chunks(args, pl, reinterpret_cast<cudaStream_t>(stream));
     return launch_recurrent(args, false, reinterpret_cast<cudaStream_t>(stream));
 }
 

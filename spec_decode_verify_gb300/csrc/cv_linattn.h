@@ -58,4 +58,29 @@ struct StepKernel {
 // vs: 128, 64 or 32; tg: 1, 4 or 8; dk <= 256 (128 with vs 128).
 StepKernel step_kernel(int vs, int dk, int tg);
 
+// The chunked kernel for prompts (bf16, dk and dv multiples of 8 up to 128).
+constexpr int kChunk = 128;            // tokens a chunk
+constexpr int kChunkThreads = 672;     // 20 warps of roles and the one that issues the products
+constexpr int kChunkMaxSorted = 64;    // sequences that are taken longest first
+struct LinattnChunkParams {
+    LinattnParams a;
+    int n_segs;      // pieces a sequence is cut into, at most
+    int seg_len;     // tokens a piece, a multiple of kChunk
+    int units;       // sequences * pieces * heads
+    int sort;        // take the longest sequences first
+    int dv_pad;      // columns of a state in the workspace (64 or 128)
+    int state_only;  // the pieces' own states into the workspace, instead of outputs
+    float *ws_state;  // [sequence][head][n_segs - 1][dv / 4][128] groups of 4 columns of a state row
+    float *ws_decay;  // [sequence][head][n_segs - 1]
+};
+using LinattnChunkKernel = void (*)(LinattnChunkParams);
+struct ChunkKernel {
+    LinattnChunkKernel fn;
+    int dv_pad, smem_bytes;
+};
+ChunkKernel chunk_kernel(int dv);
+// Turns the pieces' own states in the workspace into the states the next pieces start from.
+LinattnChunkKernel chunk_join_kernel();
+constexpr int kJoinThreads = 128;
+
 }  // namespace cvk

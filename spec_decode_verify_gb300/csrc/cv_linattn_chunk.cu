@@ -1,0 +1,760 @@
+// Linear attention with a decay for each head over prompts: chunked form on the tensor cores.
+//
+// Mathematics.  For a chunk of C = 128 tokens with G_i = sum_{u<=i} g_u and the state S before it,
+//   out_i = scale * exp(G_i) S^T q_i  +  sum_{j<=i} A_ij v_j,
+//   A_ij  = scale * exp(G_i - G_j) b_j (q_i . k_j)   (+ skip on the diagonal)
+//   S'    = exp(G_C) S + K'^T V,      K'_j = exp(G_C - G_j) b_j k_j
+// so a chunk is five products of 128 x 128 x 128: Q K^T, Q S, A V, and K'^T V twice, because K' is
+// written as a high and a low bf16 part (together 16 significant bits): the state stays fp32 through
+// any number of chunks.  A and the copy of S that Q S reads are rounded to bf16, as the outputs are.
+// The exponents are sums over the tokens between i and j, never differences of long sums, so a large
+// decay early in a chunk costs later tokens no precision; log decays below -200 count as -200
+// (exp(-200) is 0 in fp32).
+//
+// Layout.  A block (one per SM) takes units (sequence, head, piece of its length) and walks each unit's
+// chunks; every role below runs the same stream of chunks, so the next unit's loads and products
+// start while the last one's outputs are still being written.
+//   load    4 warps, two for each of two stages: q, k, v tiles by cp.async, swizzled, rows past the end
+//           and padded channels zero
+//   scores  4 warps, a row a thread: Q K^T from tensor memory, times the decays, back to it as A
+//   keys    4 warps, a token a thread: K' in place of K, its low part in place of Q once Q is used up
+//   state   4 warps, a row of S a thread: S from tensor memory, bf16 copy to shared memory, S times the
+//           chunk's decay back
+//   output  4 warps, a row a thread: out = scale exp(G) (Q S) + A V, rounded and stored
+//   issue   1 thread: all products
+// Shared memory: 2 stages of (q 32 KB, k 32 KB, v 32 or 16 KB), the copy of S; tensor memory: Q K^T
+// (then A) 128 columns, Q S, A V and S dv columns each.
+//
+// Every wait is bounded; one that gives up ends the block's work, flags the sequences it had left and
+// returns.
+#include "cv_linattn.h"
+#include "cv_tcgen05.cuh"
+
+namespace cvk {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kMinLog2 = -200.0f * kLog2e;
+constexpr unsigned kPolls = 1u << 20;
+constexpr int kTileQK = kChunk * 256;  // bytes of a q or k tile: two blocks of 64 channels
+
+// Barriers, in order (8 bytes each), then the small arrays.
+struct ChunkShared {
+    uint64_t full[2], empty[2];
+    uint64_t scores, weights, a_ready, keys, q_used, s_init, s_ready, s_done, out, out_free, last;
+    uint32_t tmem;
+    int dead;
+    uint8_t order[kChunkMaxSorted];
+    alignas(16) float g[2][kChunk];
+    alignas(16) float b[2][kChunk];  // log2 decays (0 past the end) and gains (0 past the end)
+    alignas(16) float cw[kChunk];                  // weights of a column relative to the end of its 32 tokens
+};
+
+template <int DV>
+__host__ __device__ constexpr int chunk_smem_bytes() {
+    return 2 * (2 * kTileQK + kChunk * DV * 2) + kChunk * DV * 2 + (int)sizeof(ChunkShared);
+}
+
+struct Unit {
+    int s, h, hq, seg, slot, row0, n, chunks;
+    bool on, init, last;
+};
+
+__device__ __forceinline__ Unit unit_of(const LinattnChunkParams &p, const ChunkShared *sh, int idx) {
+    Unit u;
+    const LinattnParams &a = p.a;
+    u.h = idx % a.n_heads;
+    const int r = idx / a.n_heads;
+    u.seg = r % p.n_segs;
+    const int rank = r / p.n_segs;
+    u.s = p.sort ? sh->order[rank] : rank;
+    u.hq = (int)((long long)u.h * a.n_qk / a.n_heads);
+    u.slot = a.cache_idx ? __ldg(a.cache_idx + u.s) : u.s;
+    int L, row0;
+    const int st = draft_span(a.tok.cu, u.s, a.tok.T, a.tok.total, L, row0);
+    u.on = u.slot >= 0 && u.slot < a.n_slots && st == 0;
+    const long long start = (long long)u.seg * p.seg_len;
+    if (u.on && start >= L && u.seg > 0) u.on = false;
+    if (u.on && p.state_only && start + p.seg_len >= L) u.on = false;
+    u.row0 = row0 + (int)(u.on ? start : 0);
+    u.n = u.on ? min(p.seg_len, L - (int)start) : 0;
+    u.chunks = (u.n + kChunk - 1) / kChunk;
+    u.last = u.on && start + u.n >= L;
+    u.init = a.has_init ? __ldg(a.has_init + u.s) != 0 : true;
+    return u;
+}
+
+// The block's n-th unit (-1: none).  Sorted units go out forwards and backwards in turn, so a block that
+// got a long one first gets a short one next.
+__device__ __forceinline__ int unit_index(const LinattnChunkParams &p, int n) {
+    const int G = gridDim.x, b = blockIdx.x;
+    const long long idx = (long long)n * G + (p.sort && (n & 1) ? G - 1 - b : b);
+    return idx < p.units ? (int)idx : (long long)n * G < p.units ? -2 : -1;
+}
+
+// Bounded wait of a whole warp; false once the block has given up.
+__device__ __forceinline__ bool wait_warp(uint64_t *bar, unsigned parity, volatile int *dead) {
+    for (unsigned i = 0; i < kPolls; ++i) {
+        if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+        if (__any_sync(0xffffffffu, *dead)) return false;
+    }
+    *dead = 1;
+    return false;
+}
+__device__ __forceinline__ bool wait_one(uint64_t *bar, unsigned parity, volatile int *dead) {
+    for (unsigned i = 0; i < kPolls; ++i) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if (*dead) return false;
+    }
+    *dead = 1;
+    return false;
+}
+// One arrival for the warp, after all its lanes' earlier work.
+__device__ __forceinline__ void arrive_warp(uint64_t *bar) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+// Inclusive sum over the lanes up to this one.
+__device__ __forceinline__ float prefix_sum(float v, int lane) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const float x = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += x;
+    }
+    return v;
+}
+// Sum over the lanes after this one.
+__device__ __forceinline__ float suffix_after(float v, int lane) {
+    float t = __shfl_down_sync(0xffffffffu, v, 1);
+    if (lane == 31) t = 0.0f;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const float x = __shfl_down_sync(0xffffffffu, t, o);
+        if (lane + o < 32) t += x;
+    }
+    return t;
+}
+__device__ __forceinline__ float clamp_log2(float g) {
+    g *= kLog2e;
+    return g < kMinLog2 ? kMinLog2 : g;  // a NaN stays
+}
+
+__device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void *src, bool on) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(on ? 16u : 0u) : "memory");
+}
+
+// A NaN or an infinity in v spoils the rows above it in A V (0 * NaN).  This computes one row of the
+// outputs' part inside the chunk the long way, over the tokens up to the row itself only.
+__device__ __noinline__ void row_long_way(const LinattnParams &a, const Unit &u, int t0, int i, int c0, float *o) {
+    const uint16_t *q = reinterpret_cast<const uint16_t *>(a.tok.q) + (u.row0 + t0 + i) * a.tok.q_tok + u.hq * a.tok.q_head;
+    float dec = 1.0f;
+    for (int x = 0; x < 16; ++x) o[x] = 0.0f;
+    for (int j = i; j >= 0; --j) {
+        const long long row = u.row0 + t0 + j;
+        const uint16_t *k = reinterpret_cast<const uint16_t *>(a.tok.k) + row * a.tok.k_tok + u.hq * a.tok.k_head;
+        const uint16_t *v = reinterpret_cast<const uint16_t *>(a.tok.v) + row * a.tok.v_tok + (long long)u.h * a.tok.v_head;
+        float dot = 0.0f;
+        for (int x = 0; x < a.dk; ++x) dot = fmaf(widen<uint16_t>(q[x]), widen<uint16_t>(k[x]), dot);
+        float w = a.scale * dec * dot * (a.tok.b ? a.tok.b[row * a.tok.b_tok + u.h] : 1.0f);
+        if (j == i && a.skip) w += a.skip[u.h];
+        for (int x = 0; x < 16; ++x)
+            if (c0 + x < a.dv) o[x] = fmaf(w, widen<uint16_t>(v[c0 + x]), o[x]);
+        dec *= exp2_fast(clamp_log2(a.tok.g[row * a.tok.g_tok + u.h]));
+    }
+}
+
+template <int DV>
+__global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_constant__ LinattnChunkParams p) {
+    constexpr int kTileV = kChunk * DV * 2;
+    constexpr int kStage = 2 * kTileQK + kTileV;
+    constexpr uint32_t kColP = 0, kColQS = 128, kColAV = 128 + DV, kColS = 128 + 2 * DV, kCols = 512;
+    extern __shared__ __align__(1024) unsigned char smem[];
+    unsigned char *const s_copy = smem + 2 * kStage;
+    ChunkShared *const sh = reinterpret_cast<ChunkShared *>(s_copy + kTileV);
+    const LinattnParams &a = p.a;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const bool so = p.state_only;
+
+    // the layout below needs its bytes and the swizzle's alignment
+    if (dynamic_smem_bytes() < chunk_smem_bytes<DV>() || (smem_u32(smem) & 1023u) != 0) return;
+    if (warp == 20) tmem_alloc(&sh->tmem, kCols);
+    if (tid == 0) {
+        sh->dead = 0;
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sh->full[i], 2);
+            mbar_init(&sh->empty[i], so ? 1 : 5);
+        }
+        mbar_init(&sh->scores, 1);
+        mbar_init(&sh->weights, 4);
+        mbar_init(&sh->a_ready, 4);
+        mbar_init(&sh->keys, 4);
+        mbar_init(&sh->q_used, 1);
+        mbar_init(&sh->s_init, 4);
+        mbar_init(&sh->s_ready, 4);
+        mbar_init(&sh->s_done, 1);
+        mbar_init(&sh->out, 1);
+        mbar_init(&sh->out_free, 4);
+        mbar_init(&sh->last, 1);
+        mbar_init_fence();
+    }
+    grid_dep_wait();
+    grid_dep_launch();
+    if (p.sort && tid < a.n_seq) {
+        const int len = __ldg(a.tok.cu + tid + 1) - __ldg(a.tok.cu + tid);
+        int rank = 0;
+        for (int i = 0; i < a.n_seq; ++i) {
+            const int other = __ldg(a.tok.cu + i + 1) - __ldg(a.tok.cu + i);
+            rank += other > len || (other == len && i < tid);
+        }
+        sh->order[rank] = (uint8_t)tid;
+    }
+    tmem_fence_before();
+    __syncthreads();
+    tmem_fence_after();
+    const uint32_t tm = sh->tmem;
+    volatile int *const dead = &sh->dead;
+    const int role = warp >> 2;
+    const int w4 = warp & 3;  // the quarter of tensor memory this warp reaches
+    const uint32_t tl = tm + ((uint32_t)(32 * w4) << 16);
+
+    int it = 0;  // chunks of the stream so far
+    if (role == 4 && warp < 20) {
+        // ------------------------------------------------------------------------------ load
+        const int stage = w4 >> 1, t64 = tid & 63;
+        unsigned char *const base = smem + stage * kStage;
+        const int piece = t64 & 15, r0 = t64 >> 4;  // rows r0, r0 + 4, ..: one 16-byte piece each
+        bool ok = true;
+        for (int n = 0, idx; ok && (idx = unit_index(p, n)) != -1; ++n) {
+            if (idx < 0) continue;
+            const Unit u = unit_of(p, sh, idx);
+            if (a.err && u.h == 0 && u.seg == 0 && warp == 16 && lane == 0 && u.slot >= 0) {
+                int L, row0;
+                const int st = (u.slot >= a.n_slots ? 1 : 0) | draft_span(a.tok.cu, u.s, a.tok.T, a.tok.total, L, row0);
+                if (st) atomicOr(a.err + u.s, st);
+            }
+            for (int c = 0; c < u.chunks; ++c, ++it) {
+                if ((it & 1) != stage) continue;
+                if (it >= 2 && !wait_warp(&sh->empty[stage], ((it >> 1) & 1) ^ 1, dead)) {
+                    ok = false;
+                    break;
+                }
+                const int t0 = c * kChunk, rows = min(kChunk, u.n - t0);
+                const long long row = u.row0 + t0;
+                // decays and gains of tokens t64 and t64 + 64
+                float g[2], b[2];
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const int t = t64 + 64 * x;
+                    g[x] = t < rows ? __ldg(a.tok.g + (row + t) * a.tok.g_tok + u.h) : 0.0f;
+                    b[x] = t < rows ? (a.tok.b ? __ldg(a.tok.b + (row + t) * a.tok.b_tok + u.h) : 1.0f) : 0.0f;
+                }
+                auto tile = [&](uint32_t dst, const void *src, long long tok, long long head, int d, int halves) {
+                    const uint16_t *s0 = reinterpret_cast<const uint16_t *>(src) + row * tok + head;
+                    const int col = piece * 8;
+                    if (col >= halves * 64) return;
+                    const uint32_t d0 = dst + (piece >> 3) * (kChunk * 128);
+#pragma unroll 8
+                    for (int r = r0; r < kChunk; r += 4) {
+                        const bool in = r < rows && col < d;
+                        cp_async16_zfill(d0 + swizzled(r, piece & 7), in ? s0 + r * tok + col : s0, in);
+                    }
+                };
+                const uint32_t d = smem_u32(base);
+                tile(d + kTileQK, a.tok.k, a.tok.k_tok, u.hq * a.tok.k_head, a.dk, 2);
+                if (!so) tile(d, a.tok.q, a.tok.q_tok, u.hq * a.tok.q_head, a.dk, 2);
+                if (DV == 128) {
+                    tile(d + 2 * kTileQK, a.tok.v, a.tok.v_tok, u.h * a.tok.v_head, a.dv, 2);
+                } else {  // 8 pieces a row: every thread a piece of every other row of its set
+                    const uint16_t *s0 = reinterpret_cast<const uint16_t *>(a.tok.v) + row * a.tok.v_tok + u.h * a.tok.v_head;
+                    const int pc = t64 & 7;
+#pragma unroll 8
+                    for (int r = t64 >> 3; r < kChunk; r += 8) {
+                        const bool in = r < rows && pc * 8 < a.dv;
+                        cp_async16_zfill(d + 2 * kTileQK + swizzled(r, pc), in ? s0 + r * a.tok.v_tok + pc * 8 : s0, in);
+                    }
+                }
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    sh->g[stage][t64 + 64 * x] = clamp_log2(g[x]);
+                    sh->b[stage][t64 + 64 * x] = b[x];
+                }
+                cp_async_wait_all();
+                fence_smem_to_async();
+                arrive_warp(&sh->full[stage]);
+            }
+        }
+        cp_async_wait_all();
+    } else if (role == 0 && !so) {
+        // ---------------------------------------------------------------------------- scores
+        const float scale = a.scale;
+        bool ok = true;
+        for (int n = 0, idx; ok && (idx = unit_index(p, n)) != -1; ++n) {
+            if (idx < 0) continue;
+            const Unit u = unit_of(p, sh, idx);
+            const float skip = a.skip ? __ldg(a.skip + u.h) : 0.0f;
+            for (int c = 0; c < u.chunks; ++c, ++it) {
+                const int stage = it & 1;
+                if (!wait_warp(&sh->full[stage], (it >> 1) & 1, dead) || !wait_warp(&sh->scores, it & 1, dead)) {
+                    ok = false;
+                    break;
+                }
+                tmem_fence_after();
+                const float gi = sh->g[stage][32 * w4 + lane], bi = sh->b[stage][32 * w4 + lane];
+                const float G = prefix_sum(gi, lane);
+                sh->cw[32 * w4 + lane] = exp2_fast(suffix_after(gi, lane)) * bi;
+                arrive_warp(&sh->weights);
+                uint32_t r[32], o[16];
+                // the 32 x 32 block on the diagonal: exponents from the sums within it
+                tmem_ld32(r, tl + kColP + 32 * w4);
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {
+                    const float Gj = __shfl_sync(0xffffffffu, G, j), bj = __shfl_sync(0xffffffffu, bi, j);
+                    float v = __uint_as_float(r[j]) * scale * (exp2_fast(G - Gj) * bj);
+                    if (j == lane) v += skip;
+                    r[j] = __float_as_uint(j <= lane ? v : 0.0f);
+                }
+                uint32_t diag[16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j) diag[j] = pack_bf16(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
+                if (!wait_warp(&sh->weights, it & 1, dead)) {
+                    ok = false;
+                    break;
+                }
+                // blocks left of it, nearest first while the exponent grows; A overlays the scores' columns:
+                // block J is written to columns 16 J .., which only blocks up to J / 2 had occupied, so it
+                // goes in ascending order
+                float between[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int J = 3; J > 0; --J) {
+                    const float tot = warp_sum(sh->g[stage][32 * J + lane]);
+                    if (J < w4) between[J] = (J < 3 ? between[J + 1] : 0.0f) + tot;
+                }
+#pragma unroll
+                for (int J = 0; J < 4; ++J) {
+                    if (J < w4) {
+                        tmem_ld32(r, tl + kColP + 32 * J);
+                        const float rf = exp2_fast(G + (J < 3 ? between[J + 1] : 0.0f)) * scale;
+#pragma unroll
+                        for (int j = 0; j < 32; j += 4) {
+                            const float4 cw = *reinterpret_cast<const float4 *>(sh->cw + 32 * J + j);
+                            o[j / 2] = pack_bf16(__uint_as_float(r[j]) * (rf * cw.x), __uint_as_float(r[j + 1]) * (rf * cw.y));
+                            o[j / 2 + 1] =
+                                pack_bf16(__uint_as_float(r[j + 2]) * (rf * cw.z), __uint_as_float(r[j + 3]) * (rf * cw.w));
+                        }
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) o[j] = J == w4 ? diag[j] : 0u;
+                    }
+                    tmem_st16(tl + kColP + 16 * J, o);
+                }
+                tmem_wait_st();
+                tmem_fence_before();
+                arrive_warp(&sh->a_ready);
+            }
+        }
+    } else if (role == 1) {
+        // ------------------------------------------------------------------------------ keys
+        const int t = 32 * w4 + lane;
+        bool ok = true;
+        for (int n = 0, idx; ok && (idx = unit_index(p, n)) != -1; ++n) {
+            if (idx < 0) continue;
+            const Unit u = unit_of(p, sh, idx);
+            for (int c = 0; c < u.chunks; ++c, ++it) {
+                const int stage = it & 1;
+                if (!wait_warp(&sh->full[stage], (it >> 1) & 1, dead)) {
+                    ok = false;
+                    break;
+                }
+                float after = suffix_after(sh->g[stage][t], lane);
+#pragma unroll
+                for (int J = 1; J < 4; ++J) {
+                    const float tot = warp_sum(sh->g[stage][32 * J + lane]);
+                    if (J > w4) after += tot;
+                }
+                const float w = exp2_fast(after) * sh->b[stage][t];
+                if (!so && !wait_warp(&sh->scores, it & 1, dead)) {  // K is used up
+                    ok = false;
+                    break;
+                }
+                unsigned char *const kt = smem + stage * kStage + kTileQK;
+                unsigned char *const qt = smem + stage * kStage;
+                uint32_t lo[64];
+#pragma unroll
+                for (int x = 0; x < 16; ++x) {
+                    uint4 *at = reinterpret_cast<uint4 *>(kt + (x >> 3) * (kChunk * 128) + swizzled(t, x & 7));
+                    const uint4 v = *at;
+                    const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+                    uint32_t hi[4];
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        const float f0 = __uint_as_float(in[y] << 16) * w, f1 = __uint_as_float(in[y] & 0xffff0000u) * w;
+                        hi[y] = pack_bf16(f0, f1);
+                        lo[4 * x + y] = pack_bf16(f0 - __uint_as_float(hi[y] << 16), f1 - __uint_as_float(hi[y] & 0xffff0000u));
+                    }
+                    *at = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                }
+                if (!so && !wait_warp(&sh->q_used, it & 1, dead)) {
+                    ok = false;
+                    break;
+                }
+#pragma unroll
+                for (int x = 0; x < 16; ++x)
+                    *reinterpret_cast<uint4 *>(qt + (x >> 3) * (kChunk * 128) + swizzled(t, x & 7)) =
+                        make_uint4(lo[4 * x], lo[4 * x + 1], lo[4 * x + 2], lo[4 * x + 3]);
+                fence_smem_to_async();
+                arrive_warp(&sh->keys);
+            }
+        }
+    } else if (role == 2) {
+        // ----------------------------------------------------------------------------- state
+        const int r = 32 * w4 + lane;  // the row of S
+        const uint32_t ts = tl + kColS;
+        // rows of this warp through its quarter of the copy's shared memory, 64 columns at a time
+        float4 *const mine = reinterpret_cast<float4 *>(s_copy + w4 * (kTileV / 4));
+        constexpr int PW = DV / 8;           // float4 pieces of a row per pass: the quarter holds 32 rows of them
+        constexpr int PASSES = DV / 4 / PW;  // 2
+        bool ok = true;
+        int units = 0;
+        for (int n = 0, idx; ok && (idx = unit_index(p, n)) != -1; ++n) {
+            if (idx < 0) continue;
+            const Unit u = unit_of(p, sh, idx);
+            if (!u.on) continue;
+            float *const st = a.state + (long long)u.slot * a.st_slot + (long long)u.h * a.st_head;
+            const long long wsi = ((long long)u.s * a.n_heads + u.h) * (p.n_segs - 1);
+            if (u.chunks == 0) {  // an empty prompt: zeros without an initial state
+                if (!u.init && r < a.dk)
+                    for (int j = 0; j < a.dv; j += 4)
+                        *reinterpret_cast<float4 *>(st + (long long)r * a.dv + j) = make_float4(0.f, 0.f, 0.f, 0.f);
+                continue;
+            }
+            // the state before the unit
+            const bool zero = so ? true : u.seg == 0 && !u.init;
+            if (zero || u.seg > 0) {
+                const float4 *src = reinterpret_cast<const float4 *>(p.ws_state) + (wsi + u.seg - 1) * (32 * DV);
+#pragma unroll
+                for (int j = 0; j < DV; j += 32) {
+                    uint32_t v[32];
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) {
+                        const float4 f = zero ? make_float4(0.f, 0.f, 0.f, 0.f) : src[(j / 4 + x) * 128 + r];
+                        v[4 * x] = __float_as_uint(f.x), v[4 * x + 1] = __float_as_uint(f.y);
+                        v[4 * x + 2] = __float_as_uint(f.z), v[4 * x + 3] = __float_as_uint(f.w);
+                    }
+                    tmem_st32(ts + j, v);
+                }
+            } else {
+                for (int h = 0; h < PASSES; ++h) {
+                    __syncwarp();
+                    for (int e = lane; e < 32 * PW; e += 32) {
+                        const int row = e / PW, q = e % PW, col = (h * PW + q) * 4;
+                        float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+                        if (32 * w4 + row < a.dk && col < a.dv)
+                            f = *reinterpret_cast<const float4 *>(st + (long long)(32 * w4 + row) * a.dv + col);
+                        mine[row * PW + (q ^ (row & 7))] = f;
+                    }
+                    __syncwarp();
+#pragma unroll
+                    for (int j = 0; j < PW; j += 8) {
+                        uint32_t v[32];
+#pragma unroll
+                        for (int x = 0; x < 8; ++x) {
+                            const float4 f = mine[lane * PW + ((j + x) ^ (lane & 7))];
+                            v[4 * x] = __float_as_uint(f.x), v[4 * x + 1] = __float_as_uint(f.y);
+                            v[4 * x + 2] = __float_as_uint(f.z), v[4 * x + 3] = __float_as_uint(f.w);
+                        }
+                        tmem_st32(ts + (h * PW + j) * 4, v);
+                    }
+                }
+                __syncwarp();
+            }
+            tmem_wait_st();
+            // the copy's rows go over every warp's quarter: all are through with theirs first
+            arrive_warp(&sh->s_init);
+            if (!wait_warp(&sh->s_init, units++ & 1, dead)) break;
+            float total = 1.0f;
+            for (int c = 0; c < u.chunks; ++c, ++it) {
+                const int stage = it & 1;
+                if (!wait_warp(&sh->full[stage], (it >> 1) & 1, dead) ||
+                    (c > 0 && !wait_warp(&sh->s_done, (it - 1) & 1, dead))) {
+                    ok = false;
+                    break;
+                }
+                tmem_fence_after();
+                const float *gs = sh->g[stage];
+                const float tot = exp2_fast(warp_sum((gs[lane] + gs[lane + 32]) + (gs[lane + 64] + gs[lane + 96])));
+                total *= tot;
+#pragma unroll
+                for (int j = 0; j < DV; j += 32) {
+                    uint32_t v[32];
+                    tmem_ld32(v, ts + j);
+                    if (!so) {
+#pragma unroll
+                        for (int x = 0; x < 32; x += 8) {
+                            uint4 o;
+                            o.x = pack_bf16(__uint_as_float(v[x]), __uint_as_float(v[x + 1]));
+                            o.y = pack_bf16(__uint_as_float(v[x + 2]), __uint_as_float(v[x + 3]));
+                            o.z = pack_bf16(__uint_as_float(v[x + 4]), __uint_as_float(v[x + 5]));
+                            o.w = pack_bf16(__uint_as_float(v[x + 6]), __uint_as_float(v[x + 7]));
+                            const int pc = (j + x) / 8;
+                            *reinterpret_cast<uint4 *>(s_copy + (pc >> 3) * (kChunk * 128) + swizzled(r, pc & 7)) = o;
+                        }
+                    }
+#pragma unroll
+                    for (int x = 0; x < 32; ++x) v[x] = __float_as_uint(__uint_as_float(v[x]) * tot);
+                    tmem_st32(ts + j, v);
+                }
+                tmem_wait_st();
+                tmem_fence_before();
+                fence_smem_to_async();
+                arrive_warp(&sh->s_ready);
+            }
+            if (!ok || !wait_warp(&sh->s_done, (it - 1) & 1, dead)) {
+                ok = false;
+                break;
+            }
+            tmem_fence_after();
+            // the state after it
+            if (so) {
+                float4 *dst = reinterpret_cast<float4 *>(p.ws_state) + (wsi + u.seg) * (32 * DV);
+#pragma unroll
+                for (int j = 0; j < DV; j += 32) {
+                    uint32_t v[32];
+                    tmem_ld32(v, ts + j);
+#pragma unroll
+                    for (int x = 0; x < 8; ++x)
+                        dst[(j / 4 + x) * 128 + r] = make_float4(__uint_as_float(v[4 * x]), __uint_as_float(v[4 * x + 1]),
+                                                                 __uint_as_float(v[4 * x + 2]), __uint_as_float(v[4 * x + 3]));
+                }
+                if (tid == 2 * 128) p.ws_decay[wsi + u.seg] = total;
+            } else if (u.last) {
+                for (int h = 0; h < PASSES; ++h) {
+                    __syncwarp();
+#pragma unroll
+                    for (int j = 0; j < PW; j += 8) {
+                        uint32_t v[32];
+                        tmem_ld32(v, ts + (h * PW + j) * 4);
+#pragma unroll
+                        for (int x = 0; x < 8; ++x)
+                            mine[lane * PW + ((j + x) ^ (lane & 7))] =
+                                make_float4(__uint_as_float(v[4 * x]), __uint_as_float(v[4 * x + 1]),
+                                            __uint_as_float(v[4 * x + 2]), __uint_as_float(v[4 * x + 3]));
+                    }
+                    __syncwarp();
+                    for (int e = lane; e < 32 * PW; e += 32) {
+                        const int row = e / PW, q = e % PW, col = (h * PW + q) * 4;
+                        if (32 * w4 + row < a.dk && col < a.dv)
+                            *reinterpret_cast<float4 *>(st + (long long)(32 * w4 + row) * a.dv + col) =
+                                mine[row * PW + (q ^ (row & 7))];
+                    }
+                }
+                __syncwarp();
+            }
+        }
+    } else if (role == 3 && !so) {
+        // ---------------------------------------------------------------------------- output
+        const int i = 32 * w4 + lane;  // the row of the chunk
+        bool ok = true;
+        for (int n = 0, idx; ok && (idx = unit_index(p, n)) != -1; ++n) {
+            if (idx < 0) continue;
+            const Unit u = unit_of(p, sh, idx);
+            for (int c = 0; c < u.chunks; ++c, ++it) {
+                const int stage = it & 1;
+                if (!wait_warp(&sh->full[stage], (it >> 1) & 1, dead)) {
+                    ok = false;
+                    break;
+                }
+                float G = prefix_sum(sh->g[stage][i], lane);
+#pragma unroll
+                for (int J = 0; J < 3; ++J) {
+                    const float tot = warp_sum(sh->g[stage][32 * J + lane]);
+                    if (J < w4) G += tot;
+                }
+                const float pre = exp2_fast(G) * a.scale;
+                arrive_warp(&sh->empty[stage]);
+                if (!wait_warp(&sh->out, it & 1, dead)) {
+                    ok = false;
+                    break;
+                }
+                tmem_fence_after();
+                const int t0 = c * kChunk;
+                const bool mine = t0 + i < u.n;
+                uint16_t *const dst = reinterpret_cast<uint16_t *>(a.out) + (long long)(u.row0 + t0 + i) * a.o_tok +
+                                      (long long)u.h * a.o_head;
+                bool bad = false;
+                auto store = [&](int j, const uint32_t *o) {
+                    if (!mine) return;
+                    if (j < a.dv) *reinterpret_cast<uint4 *>(dst + j) = make_uint4(o[0], o[1], o[2], o[3]);
+                    if (j + 8 < a.dv) *reinterpret_cast<uint4 *>(dst + j + 8) = make_uint4(o[4], o[5], o[6], o[7]);
+                };
+#pragma unroll
+                for (int j = 0; j < DV; j += 16) {
+                    uint32_t x[16], y[16], o[8];
+                    tmem_ld16x2(x, y, tl + kColQS + j, tl + kColAV + j);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float f0 = fmaf(pre, __uint_as_float(x[2 * e]), __uint_as_float(y[2 * e]));
+                        const float f1 = fmaf(pre, __uint_as_float(x[2 * e + 1]), __uint_as_float(y[2 * e + 1]));
+                        bad |= !(fabsf(f0) <= 3.4e38f) || !(fabsf(f1) <= 3.4e38f);
+                        o[e] = pack_bf16(f0, f1);
+                    }
+                    store(j, o);
+                }
+                if (__any_sync(0xffffffffu, bad && mine)) {
+                    // is it a value of this chunk?
+                    bool found = false;
+                    for (int t = lane; t < min(kChunk, u.n - t0); t += 32) {
+                        const uint16_t *v = reinterpret_cast<const uint16_t *>(a.tok.v) +
+                                            (u.row0 + t0 + t) * a.tok.v_tok + (long long)u.h * a.tok.v_head;
+                        for (int e = 0; e < a.dv; ++e) found |= (v[e] & 0x7f80) == 0x7f80;
+                    }
+                    if (__any_sync(0xffffffffu, found))
+                        for (int j = 0; j < DV; j += 16) {
+                            uint32_t x[16], y[16], o[8];
+                            float part[16];
+                            tmem_ld16x2(x, y, tl + kColQS + j, tl + kColAV + j);
+                            if (mine) row_long_way(a, u, t0, i, j, part);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                o[e] = pack_bf16(fmaf(pre, __uint_as_float(x[2 * e]), part[2 * e]),
+                                                 fmaf(pre, __uint_as_float(x[2 * e + 1]), part[2 * e + 1]));
+                            store(j, o);
+                            __syncwarp();
+                        }
+                }
+                tmem_fence_before();
+                arrive_warp(&sh->out_free);
+            }
+        }
+    } else if (warp == 20 && lane == 0) {
+        // ----------------------------------------------------------------------------- issue
+        const uint32_t sb = smem_u32(smem), sc = smem_u32(s_copy);
+        constexpr uint32_t kBlock = kChunk * 128;
+        constexpr uint32_t id_qk = mma_desc(128, false, false), id_qs = mma_desc(DV, false, true),
+                           id_kv = mma_desc(DV, true, true);
+        int left = 0, n = 0;  // chunks left of the current unit, the next unit
+        auto more = [&]() {
+            for (int idx; left == 0 && (idx = unit_index(p, n)) != -1; ++n)
+                if (idx >= 0) left = unit_of(p, sh, idx).chunks;
+            if (left == 0) return false;
+            --left;
+            return true;
+        };
+        auto scores = [&](int i) {
+            if (!wait_one(&sh->full[i & 1], (i >> 1) & 1, dead)) return false;
+            tmem_fence_after();
+            const uint32_t q = sb + (i & 1) * kStage, k = q + kTileQK;
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+                const uint32_t off = (x >> 2) * kBlock + (x & 3) * 32;
+                mma_ss(tm + kColP, desc_k(q + off), desc_k(k + off), id_qk, x > 0);
+            }
+            mma_commit(&sh->scores);
+            return true;
+        };
+        bool have = more();
+        bool ok = !have || so || scores(0);
+        while (ok && have) {
+            const uint32_t q = sb + (it & 1) * kStage, k = q + kTileQK, v = k + kTileQK;
+            if (!wait_one(&sh->s_ready, it & 1, dead)) break;
+            if (!so) {
+                if (it > 0 && !wait_one(&sh->out_free, (it - 1) & 1, dead)) break;
+                tmem_fence_after();
+#pragma unroll
+                for (int x = 0; x < 8; ++x)
+                    mma_ss(tm + kColQS, desc_k(q + (x >> 2) * kBlock + (x & 3) * 32), desc_mn(sc + x * 2048, kBlock),
+                           id_qs, x > 0);
+                mma_commit(&sh->q_used);
+            }
+            if (!wait_one(&sh->keys, it & 1, dead)) break;
+            tmem_fence_after();
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+                mma_ss(tm + kColS, desc_mn(k + x * 2048, kBlock), desc_mn(v + x * 2048, kBlock), id_kv, true);
+                mma_ss(tm + kColS, desc_mn(q + x * 2048, kBlock), desc_mn(v + x * 2048, kBlock), id_kv, true);
+            }
+            mma_commit(&sh->s_done);
+            if (!so) {
+                if (!wait_one(&sh->a_ready, it & 1, dead)) break;
+                tmem_fence_after();
+#pragma unroll
+                for (int x = 0; x < 8; ++x)
+                    mma_ts(tm + kColAV, tm + kColP + x * 8, desc_mn(v + x * 2048, kBlock), id_qs, x > 0);
+                mma_commit(&sh->out);
+            }
+            mma_commit(&sh->empty[it & 1]);
+            ++it;
+            have = more();
+            if (have && !so && !scores(it)) break;
+        }
+        // nothing of the block's is in flight when it gives tensor memory back
+        mma_commit(&sh->last);
+        mbar_wait_bounded(&sh->last, 0, kPolls);
+    }
+    __syncwarp();
+    tmem_fence_before();
+    __syncthreads();
+    if (*dead && tid == 0 && a.err)
+        for (int n = 0, idx; (idx = unit_index(p, n)) != -1; ++n)
+            if (idx >= 0) {
+                const Unit u = unit_of(p, sh, idx);
+                if (u.on) atomicOr(a.err + u.s, kSeqTimeout);
+            }
+    if (warp == 20) {
+        tmem_fence_after();
+        tmem_free(tm, kCols);
+    }
+}
+
+// S_0 = the initial state; S_{i+1} = decay_i S_i + own_i, written over own_i.  A thread takes 4 columns
+// of a row; the pieces are read ahead 8 at a time, since only the sums depend on one another.
+__global__ void __launch_bounds__(kJoinThreads) chunk_join(const __grid_constant__ LinattnChunkParams p) {
+    grid_dep_wait();
+    grid_dep_launch();
+    const LinattnParams &a = p.a;
+    const int dv_pad = p.dv_pad, parts = dv_pad / 4;  // blocks a head: 128 rows by 4 columns each
+    const int part = blockIdx.x % parts, sh = blockIdx.x / parts;
+    const int h = sh % a.n_heads, s = sh / a.n_heads, row = threadIdx.x, col = part * 4;
+    const int slot = a.cache_idx ? __ldg(a.cache_idx + s) : s;
+    int L, row0;
+    if (slot < 0 || slot >= a.n_slots || draft_span(a.tok.cu, s, a.tok.T, a.tok.total, L, row0)) return;
+    const int n = (L + p.seg_len - 1) / p.seg_len - 1;  // pieces with a next one
+    const bool init = a.has_init ? __ldg(a.has_init + s) != 0 : true;
+    float4 S = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (init && row < a.dk && col < a.dv)
+        S = *reinterpret_cast<const float4 *>(a.state + (long long)slot * a.st_slot + (long long)h * a.st_head +
+                                              (long long)row * a.dv + col);
+    const long long base = ((long long)s * a.n_heads + h) * (p.n_segs - 1);
+    float4 *const own = reinterpret_cast<float4 *>(p.ws_state) + base * (32 * dv_pad) + part * 128 + row;
+    const float *const dec = p.ws_decay + base;
+    const long long step = 32LL * dv_pad;
+    for (int i0 = 0; i0 < n; i0 += 8) {
+        float4 f[8];
+        float d[8];
+#pragma unroll
+        for (int x = 0; x < 8; ++x)
+            if (i0 + x < n) f[x] = own[(i0 + x) * step], d[x] = dec[i0 + x];
+#pragma unroll
+        for (int x = 0; x < 8; ++x)
+            if (i0 + x < n) {
+                S.x = fmaf(d[x], S.x, f[x].x), S.y = fmaf(d[x], S.y, f[x].y);
+                S.z = fmaf(d[x], S.z, f[x].z), S.w = fmaf(d[x], S.w, f[x].w);
+                own[(i0 + x) * step] = S;
+            }
+    }
+}
+
+}  // namespace
+
+ChunkKernel chunk_kernel(int dv) {
+    if (dv <= 64) return {linattn_chunk<64>, 64, chunk_smem_bytes<64>()};
+    return {linattn_chunk<128>, 128, chunk_smem_bytes<128>()};
+}
+LinattnChunkKernel chunk_join_kernel() { return chunk_join; }
+
+}  // namespace cvk

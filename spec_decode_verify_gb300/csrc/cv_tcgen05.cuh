@@ -1,0 +1,126 @@
+// Device wrappers of the tcgen05 instructions (sm_103a): tensor memory, matrix products, and the
+// descriptors of operands in shared memory.  Every operand tile here is stored as rows of 64 bf16
+// (128 bytes) in the 128-byte swizzle: the 16-byte piece c of row r sits at piece c ^ (r % 8).  A tile
+// of more than 64 columns is several such blocks one after the other.  The same bytes serve both
+// ways: with the row index as the operand's M or N (K contiguous: "K-major") or as its K (M or N
+// contiguous: "MN-major").
+#pragma once
+
+#include "cv_device.cuh"
+
+namespace cvk {
+
+__device__ __forceinline__ int swizzled(int row, int piece) { return row * 128 + ((piece ^ (row & 7)) << 4); }
+
+// Shared-memory operand descriptor: start address (bits 0-13), leading byte offset (16-29) and stride
+// byte offset (32-45) in units of 16 bytes, version 1 (46), 128-byte swizzle (61-63: 2).
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
+    return (uint64_t)((addr >> 4) & 0x3fff) | ((uint64_t)((lbo >> 4) & 0x3fff) << 16) |
+           ((uint64_t)((sbo >> 4) & 0x3fff) << 32) | (1ull << 46) | (2ull << 61);
+}
+// K-major: 8-row groups 1024 bytes apart (the leading offset is not used with a swizzle).
+__device__ __forceinline__ uint64_t desc_k(uint32_t addr) { return smem_desc(addr, 16, 1024); }
+// MN-major: blocks of 64 M or N elements `block` bytes apart, groups of 8 K rows 1024 bytes apart.
+__device__ __forceinline__ uint64_t desc_mn(uint32_t addr, uint32_t block) { return smem_desc(addr, block, 1024); }
+
+// Instruction descriptor: bf16 operands, fp32 accumulator, M = 128.
+__device__ __forceinline__ constexpr uint32_t mma_desc(int n, bool a_mn, bool b_mn) {
+    return (1u << 4) | (1u << 7) | (1u << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
+           ((uint32_t)(n >> 3) << 17) | (8u << 24);
+}
+
+// D (tensor memory) = A B (+ D when acc), K = 16 per instruction; issued by one thread.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+        : "memory");
+}
+// The same with A in tensor memory (two bf16 of a row per 32-bit column).
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+        : "memory");
+}
+// Arrive on `bar` once every tcgen05 operation this thread has issued is complete.
+__device__ __forceinline__ void mma_commit(uint64_t *bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(smem_u32(bar))
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory"); }
+__device__ __forceinline__ void tmem_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory"); }
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
+
+// Tensor memory allocation by one warp; the address lands in shared memory.
+__device__ __forceinline__ void tmem_alloc(uint32_t *dst, uint32_t cols) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(smem_u32(dst)), "r"(cols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::: "memory");
+}
+__device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols) {
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(addr), "r"(cols) : "memory");
+}
+
+#define CV_R4(r, i) "=r"((r)[i]), "=r"((r)[i + 1]), "=r"((r)[i + 2]), "=r"((r)[i + 3])
+#define CV_R16(r, i) CV_R4(r, i), CV_R4(r, i + 4), CV_R4(r, i + 8), CV_R4(r, i + 12)
+#define CV_I4(r, i) "r"((r)[i]), "r"((r)[i + 1]), "r"((r)[i + 2]), "r"((r)[i + 3])
+#define CV_I16(r, i) CV_I4(r, i), CV_I4(r, i + 4), CV_I4(r, i + 8), CV_I4(r, i + 12)
+
+// 32 columns of the calling warp's 32 lanes, complete on return.
+__device__ __forceinline__ void tmem_ld32(uint32_t *r, uint32_t addr) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n"
+        "tcgen05.wait::ld.sync.aligned;\n"
+        : CV_R16(r, 0), CV_R16(r, 16)
+        : "r"(addr)
+        : "memory");
+}
+// 16 columns at each of two addresses.
+__device__ __forceinline__ void tmem_ld16x2(uint32_t *a, uint32_t *b, uint32_t addr_a, uint32_t addr_b) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15}, [%32];\n"
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, "
+        "%29, %30, %31}, [%33];\n"
+        "tcgen05.wait::ld.sync.aligned;\n"
+        : CV_R16(a, 0), CV_R16(b, 0)
+        : "r"(addr_a), "r"(addr_b)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t *r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16};\n" ::"r"(addr),
+        CV_I16(r, 0)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t *r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};\n" ::"r"(addr),
+        CV_I16(r, 0), CV_I16(r, 16)
+        : "memory");
+}
+
+#undef CV_R4
+#undef CV_R16
+#undef CV_I4
+#undef CV_I16
+
+// Two fp32 values rounded to bf16 in one word, the first in the low half.
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+}  // namespace cvk
