@@ -40,14 +40,17 @@ constexpr int kTileQK = kChunk * 256;  // bytes of a q or k tile: two blocks of 
 
 // Barriers, in order (8 bytes each), then the small arrays.
 struct ChunkShared {
-    uint64_t full[2], empty[2];
-    uint64_t scores, weights, a_ready, keys, q_used, s_init, s_ready, s_done, out, out_free, last;
+    uint64_t full[2], empty[2], q_empty[2];
+    uint64_t scores, a_ready, keys, q_used, s_init, s_ready, s_done, out, out_free, last;
     uint32_t tmem;
     int dead;
     uint8_t order[kChunkMaxSorted];
-    alignas(16) float g[2][kChunk];
-    alignas(16) float b[2][kChunk];  // log2 decays (0 past the end) and gains (0 past the end)
-    alignas(16) float cw[kChunk];                  // weights of a column relative to the end of its 32 tokens
+    // Of each stage, with the chunk as four blocks of 32 tokens: the sum of log2 decays in the token's
+    // block up to it, the token's weight at the end of its block (gain * 2^(sum after it)), and the
+    // blocks' sums.  Tokens past the end: no decay, no weight.
+    alignas(16) float G[2][kChunk];
+    alignas(16) float cw[2][kChunk];
+    alignas(16) float tot[2][4];
 };
 
 template <int DV>
@@ -60,7 +63,7 @@ struct Unit {
     bool on, init, last;
 };
 
-__device__ __forceinline__ Unit unit_of(const LinattnChunkParams &p, const ChunkShared *sh, int idx) {
+__device__ __noinline__ Unit unit_of(const LinattnChunkParams &p, const ChunkShared *sh, int idx) {
     Unit u;
     const LinattnParams &a = p.a;
     u.h = idx % a.n_heads;
@@ -115,11 +118,6 @@ __device__ __forceinline__ void arrive_warp(uint64_t *bar) {
     if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
 
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
-}
 // Inclusive sum over the lanes up to this one.
 __device__ __forceinline__ float prefix_sum(float v, int lane) {
 #pragma unroll
@@ -169,6 +167,20 @@ __device__ __noinline__ void row_long_way(const LinattnParams &a, const Unit &u,
     }
 }
 
+// 32 scores of a row times rf * cw_j, rounded to bf16 pairs.
+__device__ __forceinline__ void weigh(const uint32_t *r, float rf, const float *cw, uint32_t *o) {
+    const f2 rf2 = f2_pack(rf, rf);
+#pragma unroll
+    for (int j = 0; j < 32; j += 4) {
+        const float4 c = *reinterpret_cast<const float4 *>(cw + j);
+        float f0, f1;
+        f2_unpack(f2_mul(f2_pack(__uint_as_float(r[j]), __uint_as_float(r[j + 1])), f2_mul(rf2, f2_pack(c.x, c.y))), f0, f1);
+        o[j / 2] = pack_bf16(f0, f1);
+        f2_unpack(f2_mul(f2_pack(__uint_as_float(r[j + 2]), __uint_as_float(r[j + 3])), f2_mul(rf2, f2_pack(c.z, c.w))), f0, f1);
+        o[j / 2 + 1] = pack_bf16(f0, f1);
+    }
+}
+
 template <int DV>
 __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_constant__ LinattnChunkParams p) {
     constexpr int kTileV = kChunk * DV * 2;
@@ -188,10 +200,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
         sh->dead = 0;
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh->full[i], 2);
-            mbar_init(&sh->empty[i], so ? 1 : 5);
+            mbar_init(&sh->empty[i], 1);
+            mbar_init(&sh->q_empty[i], 4);
         }
         mbar_init(&sh->scores, 1);
-        mbar_init(&sh->weights, 4);
         mbar_init(&sh->a_ready, 4);
         mbar_init(&sh->keys, 4);
         mbar_init(&sh->q_used, 1);
@@ -228,7 +240,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
         // ------------------------------------------------------------------------------ load
         const int stage = w4 >> 1, t64 = tid & 63;
         unsigned char *const base = smem + stage * kStage;
-        const int piece = t64 & 15, r0 = t64 >> 4;  // rows r0, r0 + 4, ..: one 16-byte piece each
         bool ok = true;
         for (int n = 0, idx; ok && (idx = unit_index(p, n)) != -1; ++n) {
             if (idx < 0) continue;
@@ -254,35 +265,34 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
                     g[x] = t < rows ? __ldg(a.tok.g + (row + t) * a.tok.g_tok + u.h) : 0.0f;
                     b[x] = t < rows ? (a.tok.b ? __ldg(a.tok.b + (row + t) * a.tok.b_tok + u.h) : 1.0f) : 0.0f;
                 }
-                auto tile = [&](uint32_t dst, const void *src, long long tok, long long head, int d, int halves) {
-                    const uint16_t *s0 = reinterpret_cast<const uint16_t *>(src) + row * tok + head;
-                    const int col = piece * 8;
-                    if (col >= halves * 64) return;
-                    const uint32_t d0 = dst + (piece >> 3) * (kChunk * 128);
-#pragma unroll 8
-                    for (int r = r0; r < kChunk; r += 4) {
-                        const bool in = r < rows && col < d;
-                        cp_async16_zfill(d0 + swizzled(r, piece & 7), in ? s0 + r * tok + col : s0, in);
-                    }
-                };
                 const uint32_t d = smem_u32(base);
-                tile(d + kTileQK, a.tok.k, a.tok.k_tok, u.hq * a.tok.k_head, a.dk, 2);
-                if (!so) tile(d, a.tok.q, a.tok.q_tok, u.hq * a.tok.q_head, a.dk, 2);
-                if (DV == 128) {
-                    tile(d + 2 * kTileQK, a.tok.v, a.tok.v_tok, u.h * a.tok.v_head, a.dv, 2);
-                } else {  // 8 pieces a row: every thread a piece of every other row of its set
-                    const uint16_t *s0 = reinterpret_cast<const uint16_t *>(a.tok.v) + row * a.tok.v_tok + u.h * a.tok.v_head;
-                    const int pc = t64 & 7;
-#pragma unroll 8
-                    for (int r = t64 >> 3; r < kChunk; r += 8) {
-                        const bool in = r < rows && pc * 8 < a.dv;
-                        cp_async16_zfill(d + 2 * kTileQK + swizzled(r, pc), in ? s0 + r * a.tok.v_tok + pc * 8 : s0, in);
+                // rows of 16 pieces (two blocks of 64 channels) or of 8
+                auto tile = [&](uint32_t dst, const void *src, long long at, long long tok, int width, bool wide) {
+                    const int pc = wide ? t64 & 15 : t64 & 7, r0 = wide ? t64 >> 4 : t64 >> 3, by = wide ? 4 : 8;
+                    const uint16_t *s0 = reinterpret_cast<const uint16_t *>(src) + at;
+                    const uint16_t *ptr = s0 + r0 * tok + pc * 8;
+                    const int end = pc * 8 < width ? rows : 0;
+                    const uint32_t d0 = dst + (pc >> 3) * (kChunk * 128);
+#pragma unroll 4
+                    for (int r = r0; r < kChunk; r += by, ptr += by * tok)
+                        cp_async16_zfill(d0 + swizzled(r, pc & 7), r < end ? ptr : s0, r < end);
+                };
+                tile(d + kTileQK, a.tok.k, row * a.tok.k_tok + u.hq * a.tok.k_head, a.tok.k_tok, a.dk, true);
+                tile(d + 2 * kTileQK, a.tok.v, row * a.tok.v_tok + u.h * a.tok.v_head, a.tok.v_tok, a.dv, DV == 128);
+                if (!so) {
+                    // the q tile carries the outputs out
+                    if (it >= 2 && !wait_warp(&sh->q_empty[stage], ((it >> 1) & 1) ^ 1, dead)) {
+                        ok = false;
+                        break;
                     }
+                    tile(d, a.tok.q, row * a.tok.q_tok + u.hq * a.tok.q_head, a.tok.q_tok, a.dk, true);
                 }
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    sh->g[stage][t64 + 64 * x] = clamp_log2(g[x]);
-                    sh->b[stage][t64 + 64 * x] = b[x];
+                for (int x = 0; x < 2; ++x) {  // a warp's 32 tokens are a block
+                    const float l2 = clamp_log2(g[x]), G = prefix_sum(l2, lane);
+                    sh->G[stage][t64 + 64 * x] = G;
+                    sh->cw[stage][t64 + 64 * x] = exp2_fast(suffix_after(l2, lane)) * b[x];
+                    if (lane == 31) sh->tot[stage][2 * x + (w4 & 1)] = G;
                 }
                 cp_async_wait_all();
                 fence_smem_to_async();
@@ -305,54 +315,57 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
                     break;
                 }
                 tmem_fence_after();
-                const float gi = sh->g[stage][32 * w4 + lane], bi = sh->b[stage][32 * w4 + lane];
-                const float G = prefix_sum(gi, lane);
-                sh->cw[32 * w4 + lane] = exp2_fast(suffix_after(gi, lane)) * bi;
-                arrive_warp(&sh->weights);
+                const float G = sh->G[stage][32 * w4 + lane];
+                const float *const cw = sh->cw[stage];
+                const float t1 = sh->tot[stage][1], t2 = sh->tot[stage][2];
                 uint32_t r[32], o[16];
-                // the 32 x 32 block on the diagonal: exponents from the sums within it
-                tmem_ld32(r, tl + kColP + 32 * w4);
-#pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                    const float Gj = __shfl_sync(0xffffffffu, G, j), bj = __shfl_sync(0xffffffffu, bi, j);
-                    float v = __uint_as_float(r[j]) * scale * (exp2_fast(G - Gj) * bj);
-                    if (j == lane) v += skip;
-                    r[j] = __float_as_uint(j <= lane ? v : 0.0f);
-                }
-                uint32_t diag[16];
-#pragma unroll
-                for (int j = 0; j < 16; ++j) diag[j] = pack_bf16(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
-                if (!wait_warp(&sh->weights, it & 1, dead)) {
-                    ok = false;
-                    break;
-                }
-                // blocks left of it, nearest first while the exponent grows; A overlays the scores' columns:
-                // block J is written to columns 16 J .., which only blocks up to J / 2 had occupied, so it
-                // goes in ascending order
-                float between[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                for (int J = 3; J > 0; --J) {
-                    const float tot = warp_sum(sh->g[stage][32 * J + lane]);
-                    if (J < w4) between[J] = (J < 3 ? between[J + 1] : 0.0f) + tot;
-                }
-#pragma unroll
-                for (int J = 0; J < 4; ++J) {
-                    if (J < w4) {
-                        tmem_ld32(r, tl + kColP + 32 * J);
-                        const float rf = exp2_fast(G + (J < 3 ? between[J + 1] : 0.0f)) * scale;
-#pragma unroll
-                        for (int j = 0; j < 32; j += 4) {
-                            const float4 cw = *reinterpret_cast<const float4 *>(sh->cw + 32 * J + j);
-                            o[j / 2] = pack_bf16(__uint_as_float(r[j]) * (rf * cw.x), __uint_as_float(r[j + 1]) * (rf * cw.y));
-                            o[j / 2 + 1] =
-                                pack_bf16(__uint_as_float(r[j + 2]) * (rf * cw.z), __uint_as_float(r[j + 3]) * (rf * cw.w));
-                        }
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) o[j] = J == w4 ? diag[j] : 0u;
-                    }
+                // Row i against block J left of its own: 2^(G_i + blocks between) * cw_j.  A overlays the
+                // scores: block J goes to columns 16 J .., whose scores were read in an earlier round.
+#pragma unroll 1
+                for (int J = 0; J < w4; ++J) {
+                    const float between = (J < 1 && w4 > 1 ? t1 : 0.0f) + (J < 2 && w4 > 2 ? t2 : 0.0f);
+                    const float rf = exp2_fast(G + between) * scale;
+                    tmem_ld32(r, tl + kColP + 32 * J);
+                    weigh(r, rf, cw + 32 * J, o);
                     tmem_st16(tl + kColP + 16 * J, o);
                 }
+                // The block on the diagonal: 2^(G_i - G_j) b_j = 2^(G_i - G_end) cw_j while the block's whole
+                // decay is far from fp32's range, else one exponential per pair.
+                tmem_ld32(r, tl + kColP + 32 * w4);
+                const float end = sh->tot[stage][w4];
+                if (end > -100.0f) {
+                    const float rf = exp2_fast(G - end) * scale;
+                    if (a.skip) {  // rf * cw_i = scale * b_i at j = i
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) {
+                            const float v = __uint_as_float(r[j]) * (rf * cw[32 * w4 + j]);
+                            r[j] = __float_as_uint(j == lane ? v + skip : v);
+                        }
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) o[j] = pack_bf16(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
+                    } else {
+                        weigh(r, rf, cw + 32 * w4, o);
+                    }
+                } else {
+                    const long long row = u.row0 + c * kChunk + 32 * w4 + lane;
+                    const bool in = c * kChunk + 32 * w4 + lane < u.n;
+                    const float bi = in ? (a.tok.b ? __ldg(a.tok.b + row * a.tok.b_tok + u.h) : 1.0f) : 0.0f;
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        const float Gj = __shfl_sync(0xffffffffu, G, j), bj = __shfl_sync(0xffffffffu, bi, j);
+                        const float v = __uint_as_float(r[j]) * scale * (exp2_fast(G - Gj) * bj);
+                        r[j] = __float_as_uint(j == lane ? v + skip : v);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) o[j] = pack_bf16(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
+                }
+#pragma unroll
+                for (int j = 0; j < 16; ++j) o[j] &= lane > 2 * j ? 0xffffffffu : lane == 2 * j ? 0xffffu : 0u;
+                tmem_st16(tl + kColP + 16 * w4, o);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) o[j] = 0u;
+#pragma unroll 1
+                for (int J = w4 + 1; J < 4; ++J) tmem_st16(tl + kColP + 16 * J, o);
                 tmem_wait_st();
                 tmem_fence_before();
                 arrive_warp(&sh->a_ready);
@@ -371,13 +384,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
                     ok = false;
                     break;
                 }
-                float after = suffix_after(sh->g[stage][t], lane);
-#pragma unroll
-                for (int J = 1; J < 4; ++J) {
-                    const float tot = warp_sum(sh->g[stage][32 * J + lane]);
-                    if (J > w4) after += tot;
-                }
-                const float w = exp2_fast(after) * sh->b[stage][t];
+                const float *const bt = sh->tot[stage];
+                const float later = (w4 < 1 ? bt[1] : 0.0f) + (w4 < 2 ? bt[2] : 0.0f) + (w4 < 3 ? bt[3] : 0.0f);
+                const float w = exp2_fast(later) * sh->cw[stage][t];
+                const f2 w2 = f2_pack(w, w), neg = f2_pack(-1.0f, -1.0f);
                 if (!so && !wait_warp(&sh->scores, it & 1, dead)) {  // K is used up
                     ok = false;
                     break;
@@ -393,9 +403,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
                     uint32_t hi[4];
 #pragma unroll
                     for (int y = 0; y < 4; ++y) {
-                        const float f0 = __uint_as_float(in[y] << 16) * w, f1 = __uint_as_float(in[y] & 0xffff0000u) * w;
+                        const f2 f = f2_mul(f2_pack(__uint_as_float(in[y] << 16), __uint_as_float(in[y] & 0xffff0000u)), w2);
+                        float f0, f1;
+                        f2_unpack(f, f0, f1);
                         hi[y] = pack_bf16(f0, f1);
-                        lo[4 * x + y] = pack_bf16(f0 - __uint_as_float(hi[y] << 16), f1 - __uint_as_float(hi[y] & 0xffff0000u));
+                        f2_unpack(f2_fma(f2_pack(__uint_as_float(hi[y] << 16), __uint_as_float(hi[y] & 0xffff0000u)), neg, f),
+                                  f0, f1);
+                        lo[4 * x + y] = pack_bf16(f0, f1);
                     }
                     *at = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                 }
@@ -408,6 +422,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
                     *reinterpret_cast<uint4 *>(qt + (x >> 3) * (kChunk * 128) + swizzled(t, x & 7)) =
                         make_uint4(lo[4 * x], lo[4 * x + 1], lo[4 * x + 2], lo[4 * x + 3]);
                 fence_smem_to_async();
+                // without outputs nothing else keeps this role from running a chunk ahead of the issue thread,
+                // which would then miss a phase
+                if (so && it > 0 && !wait_warp(&sh->s_done, (it - 1) & 1, dead)) {
+                    ok = false;
+                    break;
+                }
                 arrive_warp(&sh->keys);
             }
         }
@@ -486,10 +506,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
                     break;
                 }
                 tmem_fence_after();
-                const float *gs = sh->g[stage];
-                const float tot = exp2_fast(warp_sum((gs[lane] + gs[lane + 32]) + (gs[lane + 64] + gs[lane + 96])));
+                const float4 bt = *reinterpret_cast<const float4 *>(sh->tot[stage]);
+                const float tot = exp2_fast((bt.x + bt.y) + (bt.z + bt.w));
+                const f2 tot2 = f2_pack(tot, tot);
                 total *= tot;
-#pragma unroll
+#pragma unroll 1
                 for (int j = 0; j < DV; j += 32) {
                     uint32_t v[32];
                     tmem_ld32(v, ts + j);
@@ -506,7 +527,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
                         }
                     }
 #pragma unroll
-                    for (int x = 0; x < 32; ++x) v[x] = __float_as_uint(__uint_as_float(v[x]) * tot);
+                    for (int x = 0; x < 32; x += 2) {
+                        float f0, f1;
+                        f2_unpack(f2_mul(f2_pack(__uint_as_float(v[x]), __uint_as_float(v[x + 1])), tot2), f0, f1);
+                        v[x] = __float_as_uint(f0), v[x + 1] = __float_as_uint(f1);
+                    }
                     tmem_st32(ts + j, v);
                 }
                 tmem_wait_st();
@@ -569,14 +594,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
                     ok = false;
                     break;
                 }
-                float G = prefix_sum(sh->g[stage][i], lane);
-#pragma unroll
-                for (int J = 0; J < 3; ++J) {
-                    const float tot = warp_sum(sh->g[stage][32 * J + lane]);
-                    if (J < w4) G += tot;
-                }
+                const float *const bt = sh->tot[stage];
+                const float G = sh->G[stage][i] + ((w4 > 0 ? bt[0] : 0.0f) + (w4 > 1 ? bt[1] : 0.0f) + (w4 > 2 ? bt[2] : 0.0f));
                 const float pre = exp2_fast(G) * a.scale;
-                arrive_warp(&sh->empty[stage]);
+                const f2 pre2 = f2_pack(pre, pre);
                 if (!wait_warp(&sh->out, it & 1, dead)) {
                     ok = false;
                     break;
@@ -584,27 +605,31 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
                 tmem_fence_after();
                 const int t0 = c * kChunk;
                 const bool mine = t0 + i < u.n;
-                uint16_t *const dst = reinterpret_cast<uint16_t *>(a.out) + (long long)(u.row0 + t0 + i) * a.o_tok +
-                                      (long long)u.h * a.o_head;
-                bool bad = false;
+                unsigned char *const qt = smem + stage * kStage;  // q is used up: the rows go through its tile
+                f2 bad2 = f2_pack(0.0f, 0.0f);  // stays 0 while every output is finite
                 auto store = [&](int j, const uint32_t *o) {
-                    if (!mine) return;
-                    if (j < a.dv) *reinterpret_cast<uint4 *>(dst + j) = make_uint4(o[0], o[1], o[2], o[3]);
-                    if (j + 8 < a.dv) *reinterpret_cast<uint4 *>(dst + j + 8) = make_uint4(o[4], o[5], o[6], o[7]);
+                    unsigned char *const at = qt + (j >> 6) * (kChunk * 128);
+                    *reinterpret_cast<uint4 *>(at + swizzled(i, (j >> 3) & 7)) = make_uint4(o[0], o[1], o[2], o[3]);
+                    *reinterpret_cast<uint4 *>(at + swizzled(i, ((j >> 3) & 7) + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
                 };
-#pragma unroll
+#pragma unroll 1
                 for (int j = 0; j < DV; j += 16) {
                     uint32_t x[16], y[16], o[8];
                     tmem_ld16x2(x, y, tl + kColQS + j, tl + kColAV + j);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        const float f0 = fmaf(pre, __uint_as_float(x[2 * e]), __uint_as_float(y[2 * e]));
-                        const float f1 = fmaf(pre, __uint_as_float(x[2 * e + 1]), __uint_as_float(y[2 * e + 1]));
-                        bad |= !(fabsf(f0) <= 3.4e38f) || !(fabsf(f1) <= 3.4e38f);
+                        const f2 f = f2_fma(pre2, f2_pack(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])),
+                                            f2_pack(__uint_as_float(y[2 * e]), __uint_as_float(y[2 * e + 1])));
+                        float f0, f1;
+                        f2_unpack(f, f0, f1);
+                        bad2 = f2_fma(f, f2_pack(0.0f, 0.0f), bad2);
                         o[e] = pack_bf16(f0, f1);
                     }
                     store(j, o);
                 }
+                float bad0, bad1;
+                f2_unpack(bad2, bad0, bad1);
+                const bool bad = !(bad0 + bad1 == 0.0f);
                 if (__any_sync(0xffffffffu, bad && mine)) {
                     // is it a value of this chunk?
                     bool found = false;
@@ -614,6 +639,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
                         for (int e = 0; e < a.dv; ++e) found |= (v[e] & 0x7f80) == 0x7f80;
                     }
                     if (__any_sync(0xffffffffu, found))
+#pragma unroll 1
                         for (int j = 0; j < DV; j += 16) {
                             uint32_t x[16], y[16], o[8];
                             float part[16];
@@ -629,6 +655,18 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
                 }
                 tmem_fence_before();
                 arrive_warp(&sh->out_free);
+                // whole rows from there to memory, DV * 2 contiguous bytes each
+                constexpr int PC = DV / 8, RP = 32 / PC;
+                const int pc = lane % PC, r0 = 32 * w4 + lane / PC;
+                uint16_t *dst = reinterpret_cast<uint16_t *>(a.out) + (long long)(u.row0 + t0 + r0) * a.o_tok +
+                                (long long)u.h * a.o_head + pc * 8;
+                const int end = pc * 8 < a.dv ? u.n - t0 : 0;
+#pragma unroll 4
+                for (int r = r0; r < 32 * w4 + 32; r += RP, dst += RP * a.o_tok) {
+                    const uint4 v = *reinterpret_cast<const uint4 *>(qt + (pc >> 3) * (kChunk * 128) + swizzled(r, pc & 7));
+                    if (r < end) *reinterpret_cast<uint4 *>(dst) = v;
+                }
+                arrive_warp(&sh->q_empty[stage]);
             }
         }
     } else if (warp == 20 && lane == 0) {
