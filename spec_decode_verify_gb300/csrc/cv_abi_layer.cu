@@ -16,6 +16,9 @@ using cvk::launch_pdl;
 constexpr int kMaxHeads = 4096;
 constexpr int kMaxHeadDim = 256;
 constexpr int kMaxNormDim = 65536;
+constexpr int kNormRowWide = 256;    // norm_row: threads a row while elements a thread allow it (many rows)
+constexpr int kNormGroupBlocks = 8;  // resident blocks of norm_groups per SM
+constexpr int kNormGroupGrid = 16;   // its blocks per SM, at most
 
 bool aligned(const void *p, int bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
 int esize_of(int dtype) { return dtype == CV_BF16 ? 2 : 4; }
@@ -233,9 +236,9 @@ int check_norm(const cv_norm_args *a) {
     return CV_OK;
 }
 
-// A row buffer that may be absent: V elements of es bytes per 16-byte access at every multiple of V.
-bool vec_row(const void *p, int64_t stride, int64_t rows, int es) {
-    return !p || (aligned(p, 16) && (rows <= 1 || (stride * es) % 16 == 0));
+// A row buffer that may be absent: accesses of `bytes` at every multiple of them.
+bool vec_row(const void *p, int64_t stride, int64_t rows, int es, int bytes) {
+    return !p || (aligned(p, bytes) && (rows <= 1 || (stride * es) % bytes == 0));
 }
 
 int launch_norm(const cv_norm_args *a, cudaStream_t stream) {
@@ -251,24 +254,34 @@ int launch_norm(const cv_norm_args *a, cudaStream_t stream) {
     p.out = a->out, p.res_out = res ? a->residual_out : nullptr;
     p.y_row = a->y_stride, p.gate_row = a->gate_stride, p.res_row = a->residual_stride;
     p.res_out_row = a->residual_out_stride, p.out_row = a->out_stride;
-    const bool vec = vec_row(p.y, p.y_row, a->rows, es) && vec_row(p.gate, p.gate_row, a->rows, es) &&
-                     vec_row(p.out, p.out_row, a->rows, es) && vec_row(p.res, p.res_row, a->rows, res32 ? 4 : es) &&
-                     vec_row(p.res_out, p.res_out_row, a->rows, res32 ? 4 : es) && vec_row(p.post, 0, 1, es) &&
-                     vec_row(p.cs, 0, 1, es) && vec_row(p.pre, 0, 1, es);
+    // whether every tensor allows accesses of n elements
+    auto runs = [&](int n) {
+        const int rs = res32 ? 4 : es, b = n * es, rb = n * rs < 16 ? n * rs : 16;
+        return vec_row(p.y, p.y_row, a->rows, es, b) && vec_row(p.gate, p.gate_row, a->rows, es, b) &&
+               vec_row(p.out, p.out_row, a->rows, es, b) && vec_row(p.res, p.res_row, a->rows, rs, rb) &&
+               vec_row(p.res_out, p.res_out_row, a->rows, rs, rb) && vec_row(p.post, 0, 1, es, b) &&
+               vec_row(p.cs, 0, 1, es, b) && vec_row(p.pre, 0, 1, es, b);
+    };
+    const bool vec = runs(V);
     const bool bf16 = a->dtype == CV_BF16;
 
     // narrow groups without a residual: up to 32 lanes a group
     if (!res && a->group > 0) {
         const bool v = vec && a->group % V == 0;
-        const int per = v ? V : 1, most = v ? 2 : 16;
+        const int per = v ? V : 1, most = v ? 2 : 4;
         if (a->group <= 32 * per * most) {
             const int need = (a->group + per - 1) / per;  // accesses a group
             p.lanes = 1;
             while (p.lanes < 32 && p.lanes < need) p.lanes *= 2;
             const long long groups = a->rows * (a->dim / a->group);
-            const int per_block = cvk::kNormGroupThreads / p.lanes;
-            const long long blocks = (groups + per_block - 1) / per_block, cap = 16LL * device_limits().sms;
-            const auto k = cvk::norm_groups_kernel(bf16, v, (need + p.lanes - 1) / p.lanes);
+            const int nv = (need + p.lanes - 1) / p.lanes, per_block = cvk::kNormGroupThreads / p.lanes;
+            p.flat = a->rows == 1 || (a->y_stride == a->dim && a->out_stride == a->dim && (!a->gate || a->gate_stride == a->dim));
+            if (p.flat) p.y_row = p.gate_row = p.out_row = a->group;
+            const long long sms = device_limits().sms;
+            // several groups a thread once that leaves every SM a full set of blocks
+            const int unroll = v && nv == 1 && groups >= sms * kNormGroupBlocks * per_block * cvk::kNormUnroll ? cvk::kNormUnroll : 1;
+            const long long blocks = (groups + per_block * unroll - 1) / (per_block * unroll), cap = sms * kNormGroupGrid;
+            const auto k = cvk::norm_groups_kernel(bf16, v, nv, unroll);
             if (launch_pdl(k, dim3((unsigned)(blocks < cap ? blocks : cap)), dim3(cvk::kNormGroupThreads), 0, stream,
                            p) != cudaSuccess)
                 return CV_ERR_LAUNCH;
@@ -277,9 +290,10 @@ int launch_norm(const cv_norm_args *a, cudaStream_t stream) {
     }
     const unsigned grid = (unsigned)(a->rows < 0x7fffffff ? a->rows : 0x7fffffff);
     if ((a->group == 0 || a->group == a->dim) && a->dim <= cvk::kNormRowThreads * cvk::kNormRowElems) {
-        const bool v = vec && a->dim % V == 0;
+        const int v = vec && a->dim % V == 0 ? V : bf16 && a->dim % 2 == 0 && runs(2) ? 2 : 1;
         int elems = 8;
-        while (elems < cvk::kNormRowElems && elems * cvk::kNormRowThreads < a->dim) elems *= 2;
+        while (elems < cvk::kNormRowElems && elems * (a->rows > device_limits().sms ? kNormRowWide : cvk::kNormRowThreads) < a->dim)
+            elems *= 2;
         const int threads = (a->dim + elems - 1) / elems;
         if (launch_pdl(cvk::norm_row_kernel(bf16, res32, v, elems), dim3(grid), dim3((threads + 31) / 32 * 32), 0,
                        stream, p) != cudaSuccess)

@@ -16,19 +16,34 @@
 namespace cvk {
 namespace {
 
-// V consecutive elements as fp32 (V * sizeof(B) is 16 or 32 bytes in 16-byte accesses, or V = 1).
+// V consecutive elements as raw words: 16 or 32 bytes in 16-byte accesses, or V = 2 in one access of 4 or
+// 8 bytes, or V = 1.
+template <typename B, int V>
+struct Run {
+    static constexpr int W = V == 1 ? 1 : V * (int)sizeof(B) / 4;
+    uint32_t w[W];
+    __device__ __forceinline__ void load(const void *base, long long i) {
+        const B *p = reinterpret_cast<const B *>(base) + i;
+        if constexpr (V == 1)
+            w[0] = *p;
+        else if constexpr (W == 1)
+            w[0] = *reinterpret_cast<const uint32_t *>(p);
+        else
+            ldv<W == 2 ? 8 : 16, W>(w, p);
+    }
+    __device__ __forceinline__ float operator[](int j) const {
+        if constexpr (V == 1)
+            return widen<B>((B)w[0]);
+        else
+            return elem_f<B>(w, j);
+    }
+};
 template <typename B, int V>
 __device__ __forceinline__ void load_run(float *r, const void *base, long long i) {
-    const B *p = reinterpret_cast<const B *>(base) + i;
-    if constexpr (V == 1) {
-        r[0] = widen<B>(*p);
-    } else {
-        constexpr int W = V * (int)sizeof(B) / 4;
-        uint32_t w[W];
-        ldv<16, W>(w, p);
+    Run<B, V> t;
+    t.load(base, i);
 #pragma unroll
-        for (int j = 0; j < V; ++j) r[j] = elem_f<B>(w, j);
-    }
+    for (int j = 0; j < V; ++j) r[j] = t[j];
 }
 template <typename B, int V>
 __device__ __forceinline__ void store_run(void *base, long long i, const float *r) {
@@ -45,66 +60,119 @@ __device__ __forceinline__ void store_run(void *base, long long i, const float *
             else
                 w[j] = __float_as_uint(r[j]);
         }
-        stv<16, W>(p, w);
+        if constexpr (W == 1)
+            *reinterpret_cast<uint32_t *>(p) = w[0];
+        else
+            stv<W == 2 ? 8 : 16, W>(p, w);
     }
 }
 
+// act(z) for n values: silu as the conv computes it, or the sigmoid by the same fast instructions, with
+// the exact forms below -80, where those flush.
+__device__ __forceinline__ float sigmoid_fast(float z) {
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z * -1.4426950408889634f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+    return r;
+}
+template <int N>
+__device__ __forceinline__ void gate_run(const float *z, float *g, int act) {
+    if (act == 0) {
+        silu_run<N>(z, g);
+    } else {
+        float lo = z[0];
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            g[i] = sigmoid_fast(z[i]);
+            lo = fminf(lo, z[i]);
+        }
+        if (lo < -80.0f) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) g[i] = z[i] < -80.0f ? 1.0f / (1.0f + expf(-z[i])) : g[i];
+        }
+    }
+}
 __device__ __forceinline__ float gate_of(float z, int act) {
-    const float s = 1.0f / (1.0f + expf(-z));
-    return act == 0 ? z * s : s;
+    float g;
+    gate_run<1>(&z, &g, act);
+    return g;
 }
 
-template <typename B, int V, int NV>
+// U groups a thread at once, so that U loads of each tensor are in flight.
+template <typename B, int V, int NV, int U>
 __global__ void __launch_bounds__(kNormGroupThreads) norm_groups(const __grid_constant__ NormParams p) {
     grid_dep_wait();
     grid_dep_launch();
     const int lane = threadIdx.x % p.lanes;  // within the group
-    const int per_row = p.dim / p.group;
-    const long long total = p.rows * per_row;
-    const long long step = (long long)gridDim.x * (kNormGroupThreads / p.lanes);
+    const int per_block = kNormGroupThreads / p.lanes;
+    const int per_row = p.flat ? 1 : p.dim / p.group;
+    const long long total = p.rows * (p.dim / p.group);
+    const long long step = (long long)gridDim.x * per_block * U;
+    const long long first = (long long)blockIdx.x * per_block * U;
     // whole warps walk the groups together, so the shuffles below always have all lanes
-    long long gi = (long long)blockIdx.x * (kNormGroupThreads / p.lanes) + threadIdx.x / p.lanes;
-    const long long rounds = (total + step - 1) / step;
-    for (long long it = 0; it < rounds; ++it, gi += step) {
-        const bool on = gi < total;
-        const long long row = on ? gi / per_row : 0;
-        const int c0 = on ? (int)(gi % per_row) * p.group : 0;
-        float a[NV][V], g[NV][V], sum = 0.0f;
+    for (long long base = first; base < total; base += step) {
+        Run<B, V> y[U][NV], z[U][NV];
+        long long row[U];
+        int c0[U];
+        bool on[U];
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = (i * p.lanes + lane) * V;
-            const bool in = on && c < p.group;
+        for (int x = 0; x < U; ++x) {
+            const long long gi = base + x * per_block + threadIdx.x / p.lanes;
+            on[x] = gi < total;
+            // rows one after the other (flat): a group is a row of its own
+            if (p.flat)
+                row[x] = gi, c0[x] = 0;
+            else if (total <= 0x7fffffff)
+                row[x] = (unsigned)gi / (unsigned)per_row, c0[x] = (int)((unsigned)gi % (unsigned)per_row) * p.group;
+            else
+                row[x] = gi / per_row, c0[x] = (int)(gi % per_row) * p.group;
 #pragma unroll
-            for (int j = 0; j < V; ++j) a[i][j] = 0.0f, g[i][j] = 1.0f;
-            if (in) {
-                load_run<B, V>(a[i], p.y, row * p.y_row + c0 + c);
-                if (p.gate) load_run<B, V>(g[i], p.gate, row * p.gate_row + c0 + c);
+            for (int i = 0; i < NV; ++i) {
+                const int c = (i * p.lanes + lane) * V;
+#pragma unroll
+                for (int j = 0; j < Run<B, V>::W; ++j) y[x][i].w[j] = z[x][i].w[j] = 0u;
+                if (on[x] && c < p.group) {
+                    y[x][i].load(p.y, row[x] * p.y_row + c0[x] + c);
+                    if (p.gate) z[x][i].load(p.gate, row[x] * p.gate_row + c0[x] + c);
+                }
             }
         }
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
+        for (int x = 0; x < U; ++x) {
+            float a[NV][V], g[NV][V], sum = 0.0f;
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                if (p.gate) g[i][j] = gate_of(g[i][j], p.gate_act);
-                if (p.gate_first) a[i][j] *= g[i][j];
-                sum = fmaf(a[i][j], a[i][j], sum);
+            for (int i = 0; i < NV; ++i) {
+#pragma unroll
+                for (int j = 0; j < V; ++j) a[i][j] = y[x][i][j];
+                if (p.gate) {
+                    float t[V];
+#pragma unroll
+                    for (int j = 0; j < V; ++j) t[j] = z[x][i][j];
+                    gate_run<V>(t, g[i], p.gate_act);
+                    if (p.gate_first)
+#pragma unroll
+                        for (int j = 0; j < V; ++j) a[i][j] *= g[i][j];
+                }
+#pragma unroll
+                for (int j = 0; j < V; ++j) sum = fmaf(a[i][j], a[i][j], sum);
             }
-        for (int o = p.lanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        const float inv = rsqrtf(sum / (float)p.group + p.eps);
+            for (int o = p.lanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            const float inv = rsqrtf(sum / (float)p.group + p.eps);
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = (i * p.lanes + lane) * V;
-            if (!on || c >= p.group) continue;
-            float w[V];
-            if (p.post) load_run<B, V>(w, p.post, c);
+            for (int i = 0; i < NV; ++i) {
+                const int c = (i * p.lanes + lane) * V;
+                if (!on[x] || c >= p.group) continue;
+                Run<B, V> w;
+                if (p.post) w.load(p.post, c);
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                float u = a[i][j] * inv;
-                if (p.post) u *= w[j];
-                if (!p.gate_first) u *= g[i][j];
-                a[i][j] = u;
+                for (int j = 0; j < V; ++j) {
+                    float u = a[i][j] * inv;
+                    if (p.post) u *= w[j];
+                    if (p.gate && !p.gate_first) u *= g[i][j];
+                    a[i][j] = u;
+                }
+                store_run<B, V>(p.out, row[x] * p.out_row + c0[x] + c, a[i]);
             }
-            store_run<B, V>(p.out, row * p.out_row + c0 + c, a[i]);
         }
     }
 }
@@ -126,47 +194,73 @@ __device__ __forceinline__ float block_sum(float v, float *sh) {
 template <typename B, typename RB, int V, int NV>
 __global__ void __launch_bounds__(kNormRowThreads) norm_row(const __grid_constant__ NormParams p) {
     __shared__ float sh[kNormRowThreads / 32];
+    // the weights too are loaded before the first sum while registers allow it
+    constexpr bool kEarly = NV * Run<B, V>::W <= 8;
+    const int nt = blockDim.x;
     grid_dep_wait();
     grid_dep_launch();
-    const int nt = blockDim.x;
     for (long long row = blockIdx.x; row < p.rows; row += gridDim.x) {
-        float a[NV][V], g[NV][V], r[NV][V];
+        Run<B, V> y[NV], z[NV], w[kEarly ? NV : 1], cs[kEarly ? NV : 1], w2[kEarly ? NV : 1];
+        Run<RB, V> r[NV];
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (i * nt + threadIdx.x) * V;
+            const bool in = c < p.dim;
 #pragma unroll
-            for (int j = 0; j < V; ++j) a[i][j] = 0.0f, g[i][j] = 1.0f, r[i][j] = 0.0f;
-            if (c < p.dim) {
-                load_run<B, V>(a[i], p.y, row * p.y_row + c);
-                if (p.gate) load_run<B, V>(g[i], p.gate, row * p.gate_row + c);
-                if (p.res) load_run<RB, V>(r[i], p.res, row * p.res_row + c);
+            for (int j = 0; j < Run<B, V>::W; ++j) y[i].w[j] = z[i].w[j] = 0u;
+#pragma unroll
+            for (int j = 0; j < Run<RB, V>::W; ++j) r[i].w[j] = 0u;
+            if (in) {
+                y[i].load(p.y, row * p.y_row + c);
+                if (p.gate) z[i].load(p.gate, row * p.gate_row + c);
+                if (p.res) r[i].load(p.res, row * p.res_row + c);
+                if constexpr (kEarly) {
+                    if (p.post) w[i].load(p.post, c);
+                    if (p.cs) cs[i].load(p.cs, c);
+                    if (p.pre) w2[i].load(p.pre, c);
+                }
             }
         }
-        float sum = 0.0f;
+        float a[NV][V], sum = 0.0f;
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
+        for (int i = 0; i < NV; ++i) {
+            float t[V], g[V];
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                if (p.gate) g[i][j] = gate_of(g[i][j], p.gate_act);
-                if (p.gate_first) a[i][j] *= g[i][j];
-                sum = fmaf(a[i][j], a[i][j], sum);
+            for (int j = 0; j < V; ++j) a[i][j] = y[i][j];
+            if (p.gate && p.gate_first) {
+#pragma unroll
+                for (int j = 0; j < V; ++j) t[j] = z[i][j];
+                gate_run<V>(t, g, p.gate_act);
+#pragma unroll
+                for (int j = 0; j < V; ++j) a[i][j] *= g[j];
             }
+#pragma unroll
+            for (int j = 0; j < V; ++j) sum = fmaf(a[i][j], a[i][j], sum);
+        }
         const float inv = p.group > 0 ? rsqrtf(block_sum(sum, sh) / (float)p.dim + p.eps) : 1.0f;
         sum = 0.0f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (i * nt + threadIdx.x) * V;
             if (c >= p.dim) continue;
-            float w[V], cs[V];
-            if (p.post) load_run<B, V>(w, p.post, c);
-            if (p.cs) load_run<B, V>(cs, p.cs, c);
+            const int e = kEarly ? i : 0;
+            if constexpr (!kEarly) {
+                if (p.post) w[0].load(p.post, c);
+                if (p.cs) cs[0].load(p.cs, c);
+            }
+            float t[V], g[V];
+            if (p.gate && !p.gate_first) {
+#pragma unroll
+                for (int j = 0; j < V; ++j) t[j] = z[i][j];
+                gate_run<V>(t, g, p.gate_act);
+            }
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 float u = a[i][j] * inv;
-                if (p.post) u *= w[j];
-                if (!p.gate_first) u *= g[i][j];
+                if (p.post) u *= w[e][j];
+                if (p.gate && !p.gate_first) u *= g[j];
                 if (p.res) {
-                    const float f = p.cs ? p.scale * cs[j] : p.scale;
+                    const float f = p.cs ? p.scale * cs[e][j] : p.scale;
                     u = fmaf(f, u, r[i][j]);
                     sum = fmaf(u, u, sum);
                 }
@@ -180,10 +274,12 @@ __global__ void __launch_bounds__(kNormRowThreads) norm_row(const __grid_constan
             for (int i = 0; i < NV; ++i) {
                 const int c = (i * nt + threadIdx.x) * V;
                 if (c >= p.dim) continue;
-                float w[V];
-                if (p.pre) load_run<B, V>(w, p.pre, c);
+                const int e = kEarly ? i : 0;
+                if constexpr (!kEarly) {
+                    if (p.pre) w2[0].load(p.pre, c);
+                }
 #pragma unroll
-                for (int j = 0; j < V; ++j) a[i][j] = a[i][j] * inv2 * (p.pre ? w[j] : 1.0f);
+                for (int j = 0; j < V; ++j) a[i][j] = a[i][j] * inv2 * (p.pre ? w2[e][j] : 1.0f);
                 store_run<B, V>(p.out, row * p.out_row + c, a[i]);
             }
         }
@@ -289,21 +385,28 @@ NormKernel pick_row(int elems) {
 
 }  // namespace
 
-NormKernel norm_groups_kernel(bool bf16, bool vec, int nv) {
+NormKernel norm_groups_kernel(bool bf16, bool vec, int nv, int unroll) {
     if (bf16) {
-        if (vec) return nv == 1 ? norm_groups<uint16_t, 8, 1> : norm_groups<uint16_t, 8, 2>;
-        return nv <= 4 ? norm_groups<uint16_t, 1, 4> : norm_groups<uint16_t, 1, 16>;
+        if (vec && nv == 1) return unroll > 1 ? norm_groups<uint16_t, 8, 1, kNormUnroll> : norm_groups<uint16_t, 8, 1, 1>;
+        if (vec) return norm_groups<uint16_t, 8, 2, 1>;
+        return norm_groups<uint16_t, 1, 4, 1>;
     }
-    if (vec) return nv == 1 ? norm_groups<uint32_t, 4, 1> : norm_groups<uint32_t, 4, 2>;
-    return nv <= 4 ? norm_groups<uint32_t, 1, 4> : norm_groups<uint32_t, 1, 16>;
+    if (vec && nv == 1) return unroll > 1 ? norm_groups<uint32_t, 4, 1, kNormUnroll> : norm_groups<uint32_t, 4, 1, 1>;
+    if (vec) return norm_groups<uint32_t, 4, 2, 1>;
+    return norm_groups<uint32_t, 1, 4, 1>;
 }
 
-NormKernel norm_row_kernel(bool bf16, bool res_f32, bool vec, int elems) {
+NormKernel norm_row_kernel(bool bf16, bool res_f32, int v, int elems) {
     if (bf16) {
-        if (res_f32) return vec ? pick_row<uint16_t, uint32_t, 8>(elems) : pick_row<uint16_t, uint32_t, 1>(elems);
-        return vec ? pick_row<uint16_t, uint16_t, 8>(elems) : pick_row<uint16_t, uint16_t, 1>(elems);
+        if (res_f32)
+            return v == 8   ? pick_row<uint16_t, uint32_t, 8>(elems)
+                   : v == 2 ? pick_row<uint16_t, uint32_t, 2>(elems)
+                            : pick_row<uint16_t, uint32_t, 1>(elems);
+        return v == 8   ? pick_row<uint16_t, uint16_t, 8>(elems)
+               : v == 2 ? pick_row<uint16_t, uint16_t, 2>(elems)
+                        : pick_row<uint16_t, uint16_t, 1>(elems);
     }
-    return vec ? pick_row<uint32_t, uint32_t, 4>(elems) : pick_row<uint32_t, uint32_t, 1>(elems);
+    return v == 4 ? pick_row<uint32_t, uint32_t, 4>(elems) : pick_row<uint32_t, uint32_t, 1>(elems);
 }
 
 NormKernel norm_any_kernel(bool bf16, bool res_f32) {

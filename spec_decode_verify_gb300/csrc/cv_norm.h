@@ -14,6 +14,7 @@ struct NormParams {
     void *out, *res_out;
     long long y_row, gate_row, res_row, res_out_row, out_row;
     int lanes;  // norm_groups: lanes per group (a power of two, at most 32)
+    int flat;   // norm_groups: rows and groups lie one after the other in every tensor: each group is a row
 };
 
 using NormKernel = void (*)(NormParams);
@@ -23,10 +24,13 @@ constexpr int kNormRowThreads = 512;  // norm_row: threads a row, at most
 constexpr int kNormRowElems = 32;     // norm_row: elements a thread, at most
 constexpr int kNormAnyThreads = 256;
 
-// Groups of at most 32 lanes * nv vectors (nv 1 or 2), no residual.
-NormKernel norm_groups_kernel(bool bf16, bool vec, int nv);
+constexpr int kNormUnroll = 2;        // norm_groups: groups a thread loads at once
+
+// Groups of at most 32 lanes * nv accesses (vec: 16 bytes, nv 1 or 2; else one element, nv up to 4), no residual; unroll 1 or kNormUnroll.
+NormKernel norm_groups_kernel(bool bf16, bool vec, int nv, int unroll);
 // One block a row, the row in registers (elems = 8, 16 or 32 elements a thread).
-NormKernel norm_row_kernel(bool bf16, bool res_f32, bool vec, int elems);
+// v: elements an access (16 bytes of dtype, 2 of bf16, or 1).
+NormKernel norm_row_kernel(bool bf16, bool res_f32, int v, int elems);
 // One block a row, the row read again for each pass: any dim and any group.
 NormKernel norm_any_kernel(bool bf16, bool res_f32);
 
