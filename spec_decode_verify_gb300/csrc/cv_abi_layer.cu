@@ -72,9 +72,9 @@ int check_linattn(const cv_linattn_args *a, bool step, bool pointers) {
     return CV_OK;
 }
 
-// Four elements at every multiple of 4 channels may be loaded at once.
-bool rows4(const void *p, int64_t seq, int64_t tok, int64_t head, bool packed, int d, int es) {
-    return d % 4 == 0 && aligned(p, 4 * es) && (packed || seq % 4 == 0) && tok % 4 == 0 && head % 4 == 0;
+// n elements at every multiple of n channels may be loaded at once.
+bool rows_of(int n, const void *p, int64_t seq, int64_t tok, int64_t head, bool packed, int d, int es) {
+    return d % n == 0 && aligned(p, n * es) && (packed || seq % n == 0) && tok % n == 0 && head % n == 0;
 }
 
 cvk::LinattnRun make_run(const cv_linattn_tokens &t, const cv_linattn_args *a, bool with_q) {
@@ -87,9 +87,13 @@ cvk::LinattnRun make_run(const cv_linattn_tokens &t, const cv_linattn_args *a, b
     r.g = t.log_decay, r.g_seq = t.decay_seq_stride, r.g_tok = t.decay_tok_stride;
     r.b = t.gain, r.b_seq = t.gain_seq_stride, r.b_tok = t.gain_tok_stride;
     r.cu = t.cu, r.T = t.T, r.total = t.total_tokens;
-    r.vec = rows4(t.k, r.k_seq, r.k_tok, r.k_head, t.cu, a->dk, es) &&
-            rows4(t.v, r.v_seq, r.v_tok, r.v_head, t.cu, a->dv, es) &&
-            (!with_q || rows4(t.q, r.q_seq, r.q_tok, r.q_head, t.cu, a->dk, es));
+    auto all = [&](int n) {
+        return rows_of(n, t.k, r.k_seq, r.k_tok, r.k_head, t.cu, a->dk, es) &&
+               rows_of(n, t.v, r.v_seq, r.v_tok, r.v_head, t.cu, a->dv, es) &&
+               (!with_q || rows_of(n, t.q, r.q_seq, r.q_tok, r.q_head, t.cu, a->dk, es));
+    };
+    r.vec = all(4);
+    r.vec16 = all(16 / es);
     return r;
 }
 
@@ -114,16 +118,21 @@ cvk::LinattnParams make_linattn(const cv_linattn_args *a, bool step) {
 
 int launch_recurrent(const cv_linattn_args *a, bool step, cudaStream_t stream) {
     cvk::LinattnParams p = make_linattn(a, step);
-    // the widest slice of a head whose grid still gives every SM two blocks
-    int vs = a->dk <= 128 && a->dv > 64 ? 128 : a->dv > 32 ? 64 : 32;
-    const long long heads = (long long)a->n_seq * a->n_heads;
-    while (vs > 32 && heads * ((a->dv + vs - 1) / vs) < 2LL * device_limits().sms) vs /= 2;
-    p.slices = (a->dv + vs - 1) / vs;
+    const long long heads = (long long)a->n_seq * a->n_heads, sms = device_limits().sms;
     const int most = step && a->prev.T > a->tok.T ? a->prev.T : a->tok.T;
-    const cvk::StepKernel k = cvk::step_kernel(vs, a->dk, most <= 1 ? 1 : most <= 4 ? 4 : cvk::kStepMaxGroup);
+    const bool stream_ok = p.st_vec && (run_empty(a->tok) || p.tok.vec16) && (!step || run_empty(a->prev) || p.prev.vec16);
+    // the widest slice of a head whose grid still gives every SM two blocks
+    int vs = stream_ok && a->dk <= 128 && a->dv > 64 ? 128 : a->dv > 32 ? 64 : 32;
+    while (vs > 32 && heads * ((a->dv + vs - 1) / vs) < 2 * sms) vs /= 2;
+    p.slices = (a->dv + vs - 1) / vs;
+    const long long units = heads * p.slices;
+    // tokens a pass; fp32 rows are twice as long: 4 of them leave room for two blocks per SM
+    int tg = most <= 1 ? 1 : most <= 4 && stream_ok ? 4 : cvk::kStepMaxGroup;
+    if (stream_ok && tg > 4 && !p.bf16 && vs == 128) tg = 4;
+    const cvk::StepKernel k = stream_ok ? cvk::stream_kernel(vs, a->dk, tg, p.bf16) : cvk::step_kernel(vs, a->dk, tg);
     if (cvk::ensure_smem(reinterpret_cast<const void *>(k.fn), k.smem_bytes) != cudaSuccess) return CV_ERR_LAUNCH;
-    if (launch_pdl(k.fn, dim3((unsigned)(heads * p.slices)), dim3(cvk::kStepThreads), k.smem_bytes, stream, p) !=
-        cudaSuccess)
+    const long long grid = stream_ok && units > 2 * sms ? 2 * sms : units;
+    if (launch_pdl(k.fn, dim3((unsigned)grid), dim3(cvk::kStepThreads), k.smem_bytes, stream, p) != cudaSuccess)
         return CV_ERR_LAUNCH;
     return cudaGetLastError() == cudaSuccess ? CV_OK : CV_ERR_LAUNCH;
 }

@@ -18,6 +18,7 @@ struct LinattnRun {
     const int *cu;
     int T, total;
     int vec;  // rows of q, k and v allow loads of 4 elements at multiples of 4 (checked on the host)
+    int vec16;  // and of 16 bytes at every multiple of 16 bytes
 };
 
 struct LinattnParams {
@@ -55,8 +56,31 @@ struct StepKernel {
     LinattnKernel fn;
     int rows_max, smem_bytes;
 };
-// vs: 128, 64 or 32; tg: 1, 4 or 8; dk <= 256 (128 with vs 128).
+// Any alignment; vs: 64 or 32; tg: 1 or kStepMaxGroup; dk <= 256.
 StepKernel step_kernel(int vs, int dk, int tg);
+// Rows aligned to 16 bytes; vs: 128 (dk <= 128), 64 or 32; tg: 1, 4 or 8.
+StepKernel stream_kernel(int vs, int dk, int tg, bool bf16);
+
+// Shared memory of linattn_stream, in bytes from its start: the state tile, two buffers of raw rows (k, q
+// and v of TG tokens, each row 16 bytes longer than it is to spread the banks, decays, gains), then
+// q and k [rows][TG], v [TG][VS], partial outputs [row groups][min(TG, 4)][VS], token products, decays, gains,
+// and the units at hand.
+struct StepUnit {
+    int s, h, slice;
+    int slot, n_tok, row0, n_prev, prow0, status;
+    bool on, init;
+};
+struct StreamLayout {
+    int raw, raw_bytes, q, ring, bytes;
+    __host__ __device__ constexpr StreamLayout(int VS, int R, int TG, bool bf16)
+        : raw(R * kStepThreads * 16),
+          raw_bytes(TG * (2 * (R * (kStepThreads / (VS / 4)) * (bf16 ? 2 : 4) + 16) + VS * (bf16 ? 2 : 4) + 16) +
+                    (TG * 8 + 15) / 16 * 16),
+          q(raw + 2 * raw_bytes),
+          ring(q + 4 * (2 * R * (kStepThreads / (VS / 4)) * TG + TG * VS + 4 * kStepThreads * (TG < 4 ? TG : 4) + TG * TG +
+                        2 * TG)),
+          bytes(ring + 4 * (int)sizeof(StepUnit)) {}
+};
 
 // The chunked kernel for prompts (bf16, dk and dv multiples of 8 up to 128).
 constexpr int kChunk = 128;            // tokens a chunk

@@ -274,20 +274,347 @@ __global__ void __launch_bounds__(kStepThreads, 2) linattn_step(const __grid_con
     if (p.update && (n_tok > 0 || !init)) store_state();
 }
 
+// The same with everything loaded ahead: blocks stay (a multiple of the SM count) and walk the units
+// (sequence, head, column slice); while one unit is computed from registers, the next one's state tile
+// and the next group's tokens are on their way into shared memory by cp.async.  A thread copies the
+// state words it will own itself, so the tile needs no barrier.  Needs 16-byte-aligned rows.
+template <int BYTES>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void *src, bool on) {
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(on ? 16u : 0u) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;\n" ::"r"(dst), "l"(src), "n"(BYTES), "r"(on ? BYTES : 0)
+                     : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
+}
+
+template <int VS, int R, int TG>
+__global__ void __launch_bounds__(kStepThreads, 2) linattn_stream(const __grid_constant__ LinattnParams p) {
+    constexpr int LANES = VS / 4;
+    constexpr int RG = kStepThreads / LANES;
+    constexpr int DKP = R * RG;
+    constexpr int TR = TG < 4 ? TG : 4;  // tokens whose partial outputs are summed at once
+    extern __shared__ __align__(16) unsigned char smem[];
+    const StreamLayout lay(VS, R, TG, p.bf16);
+    float4 *const tile = reinterpret_cast<float4 *>(smem);  // [R][threads]
+    float *const qs = reinterpret_cast<float *>(smem + lay.q);  // [DKP][TG]
+    float *const ks = qs + DKP * TG;                            // [DKP][TG]
+    float *const vs = ks + DKP * TG;                            // [TG][VS]
+    float *const red = vs + TG * VS;                            // [RG][TR][VS]
+    float *const pt = red + RG * TR * VS;                       // [TG][TG]
+    float *const as = pt + TG * TG, *const bs = as + TG;        // [TG] decays, gains
+    StepUnit *const ring = reinterpret_cast<StepUnit *>(smem + lay.ring);  // unit n at n % 4
+    if (dynamic_smem_bytes() < (unsigned)lay.bytes) return;
+
+    const int tid = threadIdx.x, lane_c = (tid % LANES) * 4, rg = tid / LANES;
+    const int es = p.bf16 ? 2 : 4, pitch_k = DKP * es + 16, pitch_v = VS * es + 16;
+    const long long total = (long long)p.n_seq * p.n_heads * p.slices;
+    grid_dep_wait();
+    grid_dep_launch();
+
+    auto unit_of = [&](long long idx) {
+        StepUnit u;
+        u.on = idx < total;
+        u.slot = -1, u.n_tok = u.n_prev = u.row0 = u.prow0 = u.status = u.s = u.h = u.slice = 0;
+        u.init = true;
+        if (!u.on) return u;
+        u.slice = (int)(idx % p.slices);
+        const int unit = (int)(idx / p.slices);
+        u.h = unit % p.n_heads, u.s = unit / p.n_heads;
+        u.slot = p.cache_idx ? __ldg(p.cache_idx + u.s) : u.s;
+        u.n_tok = p.tok.T, u.n_prev = p.prev.T;
+        if (u.slot >= p.n_slots) u.status |= 1;
+        if (p.tok.cu) u.status |= draft_span(p.tok.cu, u.s, p.tok.T, p.tok.total, u.n_tok, u.row0);
+        if (p.prev.T > 0) {
+            if (p.prev.cu) u.status |= draft_span(p.prev.cu, u.s, p.prev.T, p.prev.total, u.n_prev, u.prow0);
+            const int a = __ldg(p.accept + u.s);
+            if (a < 0 || a > u.n_prev) u.status |= 4;
+            u.n_prev = a;
+        }
+        if (p.has_init) u.init = __ldg(p.has_init + u.s) != 0;
+        if (u.slot < 0) u.status = 0;
+        u.on = u.slot >= 0 && u.status == 0;
+        return u;
+    };
+    auto groups_of = [](const StepUnit &u) {
+        return u.on ? (u.n_prev + TG - 1) / TG + (u.n_tok + TG - 1) / TG : 0;
+    };
+    auto state_at = [&](const StepUnit &u) {
+        return p.state + (long long)u.slot * p.st_slot + (long long)u.h * p.st_head + u.slice * VS + lane_c;
+    };
+    // the unit's state words of this thread -> shared memory
+    auto fetch_state = [&](const StepUnit &u) {
+        const float *const st = state_at(u);
+        const bool col = u.init && u.slice * VS + lane_c < p.dv;
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const int row = i * RG + rg;
+            const bool in = col && row < p.dk;
+            copy_async<16>(smem_u32(tile + i * kStepThreads + tid), in ? st + (long long)row * p.dv : p.state, in);
+        }
+    };
+    // group g of the unit -> raw rows in buffer b (previous drafts first), zeros past the tokens
+    auto fetch_group = [&](const StepUnit &u, int g, int b) {
+        const int gp = (u.n_prev + TG - 1) / TG;
+        const bool old = g < gp;
+        const LinattnRun &run = old ? p.prev : p.tok;
+        const int t0 = (old ? g : g - gp) * TG, n = min(TG, (old ? u.n_prev : u.n_tok) - t0);
+        const long long sq = run.cu ? 0 : u.s, first = (long long)(old ? u.prow0 : u.row0) + t0;
+        const int hq = (int)((long long)u.h * p.n_qk / p.n_heads);
+        const uint32_t base = smem_u32(smem + lay.raw + b * lay.raw_bytes);
+        const int per = 16 / es;  // elements a copy
+        auto rows = [&](uint32_t dst, int pitch, const void *src, long long seq, long long tok, long long off, int width,
+                        int padded) {
+            const unsigned char *s0 = reinterpret_cast<const unsigned char *>(src);
+            for (int e = tid; e < TG * (padded / per); e += kStepThreads) {
+                const int t = e / (padded / per), c = (e % (padded / per)) * per;
+                const bool in = t < n && c < width;
+                copy_async<16>(dst + t * pitch + c * es, in ? s0 + (sq * seq + (first + t) * tok + off + c) * es : s0, in);
+            }
+        };
+        rows(base, pitch_k, run.k, run.k_seq, run.k_tok, hq * run.k_head, p.dk, DKP);
+        if (!old) rows(base + TG * pitch_k, pitch_k, run.q, run.q_seq, run.q_tok, hq * run.q_head, p.dk, DKP);
+        const int vw = min(VS, p.dv - u.slice * VS);
+        rows(base + 2 * TG * pitch_k, pitch_v, run.v, run.v_seq, run.v_tok, (long long)u.h * run.v_head + u.slice * VS, vw, VS);
+        if (tid < TG) {
+            const bool in = tid < n;
+            const uint32_t at = base + 2 * TG * pitch_k + TG * pitch_v + tid * 4;
+            copy_async<4>(at, in ? run.g + sq * run.g_seq + (first + tid) * run.g_tok + u.h : run.g, in);
+            if (run.b) copy_async<4>(at + TG * 4, in ? run.b + sq * run.b_seq + (first + tid) * run.b_tok + u.h : run.b, in);
+        }
+    };
+
+    if (tid < 2) ring[tid] = unit_of(blockIdx.x + (long long)tid * gridDim.x);
+    __syncthreads();
+    if (ring[0].on) fetch_state(ring[0]);
+    if (groups_of(ring[0]) > 0) fetch_group(ring[0], 0, 0);
+    copies_commit();
+    int buf = 0;  // buffer of the group to compute next
+
+    int turn = 0;
+    for (long long idx = blockIdx.x; idx < total; idx += gridDim.x, ++turn) {
+        copies_wait<0>();  // the tile and the first group
+        __syncthreads();
+        const StepUnit &cur = ring[turn & 3], &nxt = ring[(turn + 1) & 3];
+        if (tid == kStepThreads - 1) ring[(turn + 2) & 3] = unit_of(idx + 2LL * gridDim.x);
+        if (p.err && cur.h == 0 && cur.slice == 0 && tid == 0) p.err[cur.s] = cur.status;
+        float S[R][4];
+        const int gp = (cur.n_prev + TG - 1) / TG, ng = groups_of(cur);
+        const int c = cur.slice * VS + lane_c;
+        float *const st = state_at(cur);
+        auto store_state = [&]() {
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                const int row = i * RG + rg;
+                if (row < p.dk && c < p.dv)
+                    *reinterpret_cast<float4 *>(st + (long long)row * p.dv) = make_float4(S[i][0], S[i][1], S[i][2], S[i][3]);
+            }
+        };
+        if (cur.on) {
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                const float4 w = tile[i * kStepThreads + tid];
+                S[i][0] = w.x, S[i][1] = w.y, S[i][2] = w.z, S[i][3] = w.w;
+            }
+            // a new sequence without accepted drafts: its zeros, unless its tokens' state is written below
+            if (gp == 0 && !cur.init && (p.update ? cur.n_tok == 0 : p.prev.T > 0)) store_state();
+        }
+        bool state_pending = false;  // the next unit's tile was committed after the next group's rows
+        const float sk = p.skip ? __ldg(p.skip + cur.h) : 0.0f;
+        for (int g = 0; g < ng; ++g) {
+            if (g > 0) {
+                if (state_pending)
+                    copies_wait<1>();
+                else
+                    copies_wait<0>();
+                __syncthreads();  // the rows are there, the last group's shared values are used up
+            }
+            state_pending = false;
+            const bool old = g < gp;
+            const int t0 = (old ? g : g - gp) * TG, n = min(TG, (old ? cur.n_prev : cur.n_tok) - t0);
+            {
+                const unsigned char *const raw = smem + lay.raw + buf * lay.raw_bytes;
+                auto four = [&](const unsigned char *at) {
+                    if (!p.bf16) return *reinterpret_cast<const float4 *>(at);
+                    const uint2 w = *reinterpret_cast<const uint2 *>(at);
+                    return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u),
+                                       __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u));
+                };
+#pragma unroll
+                for (int e = tid; e < TG * (DKP / 4); e += kStepThreads) {
+                    const int t = e % TG, i = (e / TG) * 4;
+                    const float4 kv = four(raw + t * pitch_k + i * es);
+                    ks[i * TG + t] = kv.x, ks[(i + 1) * TG + t] = kv.y, ks[(i + 2) * TG + t] = kv.z, ks[(i + 3) * TG + t] = kv.w;
+                    if (!old) {
+                        const float4 qv = four(raw + (TG + t) * pitch_k + i * es);
+                        qs[i * TG + t] = qv.x, qs[(i + 1) * TG + t] = qv.y, qs[(i + 2) * TG + t] = qv.z,
+                        qs[(i + 3) * TG + t] = qv.w;
+                    }
+                }
+#pragma unroll
+                for (int e = tid; e < TG * LANES; e += kStepThreads) {
+                    const int t = e / LANES, i = (e % LANES) * 4;
+                    *reinterpret_cast<float4 *>(vs + t * VS + i) = four(raw + 2 * TG * pitch_k + t * pitch_v + i * es);
+                }
+                if (tid < TG) {
+                    const float *const gb = reinterpret_cast<const float *>(raw + 2 * TG * pitch_k + TG * pitch_v);
+                    as[tid] = tid < n ? expf(gb[tid]) : 1.0f;
+                    bs[tid] = tid < n ? ((old ? p.prev.b : p.tok.b) ? gb[TG + tid] : 1.0f) : 0.0f;
+                }
+            }
+            // what comes next sets out now
+            buf ^= 1;
+            if (g + 1 < ng)
+                fetch_group(cur, g + 1, buf);
+            else if (groups_of(nxt) > 0)
+                fetch_group(nxt, 0, buf);
+            copies_commit();
+            if (g == 0 && nxt.on) {
+                fetch_state(nxt);
+                copies_commit();
+                state_pending = true;
+            }
+            __syncthreads();
+
+            auto advance = [&]() {
+                float vw[TG][4], tail = 1.0f;
+#pragma unroll
+                for (int t = TG - 1; t >= 0; --t) {
+                    const float4 v = *reinterpret_cast<const float4 *>(vs + t * VS + lane_c);
+                    const float w = tail * bs[t];
+                    vw[t][0] = w * v.x, vw[t][1] = w * v.y, vw[t][2] = w * v.z, vw[t][3] = w * v.w;
+                    if (t < n) tail *= as[t];
+                }
+#pragma unroll
+                for (int i = 0; i < R; ++i) {
+                    float kr[TG];
+                    load_group<TG>(kr, ks + (i * RG + rg) * TG);
+                    const f2 tail2 = f2_pack(tail, tail);
+                    f2 s01 = f2_mul(f2_pack(S[i][0], S[i][1]), tail2), s23 = f2_mul(f2_pack(S[i][2], S[i][3]), tail2);
+#pragma unroll
+                    for (int t = 0; t < TG; ++t) {
+                        const f2 k2 = f2_pack(kr[t], kr[t]);
+                        s01 = f2_fma(k2, f2_pack(vw[t][0], vw[t][1]), s01);
+                        s23 = f2_fma(k2, f2_pack(vw[t][2], vw[t][3]), s23);
+                    }
+                    f2_unpack(s01, S[i][0], S[i][1]);
+                    f2_unpack(s23, S[i][2], S[i][3]);
+                }
+            };
+            if (old) {
+                advance();
+                if (g + 1 == gp && !(p.update && cur.n_tok > 0)) store_state();
+                continue;
+            }
+            // (q_t . k_u) for u <= t < n: LP lanes per pair
+            constexpr int PPW = TG * TG / 8 > 0 ? TG * TG / 8 : 1;
+            constexpr int LP = 32 / PPW;
+            const int pair = (tid / 32) * PPW + (tid % 32) / LP;
+            if (tid / 32 < (TG * TG + PPW - 1) / PPW) {
+                const int t = pair / TG, u = pair % TG;
+                float acc = 0.0f;
+#pragma unroll 8
+                for (int r = tid % LP; r < DKP; r += LP) acc = fmaf(qs[r * TG + t], ks[r * TG + u], acc);
+#pragma unroll
+                for (int o = LP / 2; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
+                if (u <= t && t < n) {
+                    float w = bs[u];
+                    for (int x = u + 1; x <= t; ++x) w *= as[x];
+                    if (tid % LP == 0) pt[t * TG + u] = acc * w;
+                }
+            }
+            // the row groups' parts of S^T q, all tokens of the group
+            f2 acc[TG][2];
+#pragma unroll
+            for (int t = 0; t < TG; ++t) acc[t][0] = acc[t][1] = f2_pack(0.0f, 0.0f);
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                float qr[TG];
+                load_group<TG>(qr, qs + (i * RG + rg) * TG);
+                const f2 s01 = f2_pack(S[i][0], S[i][1]), s23 = f2_pack(S[i][2], S[i][3]);
+#pragma unroll
+                for (int t = 0; t < TG; ++t) {
+                    const f2 q2 = f2_pack(qr[t], qr[t]);
+                    acc[t][0] = f2_fma(q2, s01, acc[t][0]);
+                    acc[t][1] = f2_fma(q2, s23, acc[t][1]);
+                }
+            }
+            const long long out0 = (p.tok.cu ? 0 : cur.s * p.o_seq) + ((long long)cur.row0 + t0) * p.o_tok +
+                                   (long long)cur.h * p.o_head + cur.slice * VS;
+#pragma unroll
+            for (int tr = 0; tr < TG; tr += TR) {
+                if (tr > 0) __syncthreads();
+#pragma unroll
+                for (int t = 0; t < TR; ++t) {
+                    float4 a;
+                    f2_unpack(acc[tr + t][0], a.x, a.y);
+                    f2_unpack(acc[tr + t][1], a.z, a.w);
+                    *reinterpret_cast<float4 *>(red + (rg * TR + t) * VS + lane_c) = a;
+                }
+                __syncthreads();
+                for (int e = tid; e < TR * VS && tr + e / VS < n; e += kStepThreads) {
+                    const int t = tr + e / VS, j = e % VS;
+                    if (cur.slice * VS + j >= p.dv) continue;
+                    float o = 0.0f, a = 1.0f;
+#pragma unroll
+                    for (int w = 0; w < RG; ++w) o += red[(w * TR + e / VS) * VS + j];
+                    for (int u = 0; u <= t; ++u) a *= as[u];
+                    o *= a;
+                    for (int u = 0; u <= t; ++u) o = fmaf(pt[t * TG + u], vs[u * VS + j], o);
+                    o *= p.scale;
+                    if (p.skip) o = fmaf(sk, vs[t * VS + j], o);
+                    const long long at = out0 + t * p.o_tok + j;
+                    if (p.bf16)
+                        reinterpret_cast<uint16_t *>(p.out)[at] = narrow<uint16_t>(o);
+                    else
+                        reinterpret_cast<float *>(p.out)[at] = o;
+                }
+            }
+            if (g + 1 < ng || p.update) advance();
+            if (g + 1 == ng && p.update) store_state();
+        }
+        if (ng == 0) {  // no group: the next unit's loads set out here
+            if (nxt.on) fetch_state(nxt);
+            if (groups_of(nxt) > 0) fetch_group(nxt, 0, buf);
+            copies_commit();
+        }
+    }
+    copies_wait<0>();
+}
+
 template <int VS, int R>
 StepKernel pick(int tg) {
     constexpr int rows = R * (kStepThreads / (VS / 4));
     if (tg == 1) return {linattn_step<VS, R, 1>, rows, step_smem_floats(VS, R, 1) * 4};
-    if (tg == 4) return {linattn_step<VS, R, 4>, rows, step_smem_floats(VS, R, 4) * 4};
-    return {linattn_step<VS, R, 8>, rows, step_smem_floats(VS, R, 8) * 4};
+    return {linattn_step<VS, R, kStepMaxGroup>, rows, step_smem_floats(VS, R, kStepMaxGroup) * 4};
+}
+template <int VS, int R>
+StepKernel pick_stream(int tg, bool bf16) {
+    constexpr int rows = R * (kStepThreads / (VS / 4));
+    if (tg == 1) return {linattn_stream<VS, R, 1>, rows, StreamLayout(VS, R, 1, bf16).bytes};
+    if (tg == 4) return {linattn_stream<VS, R, 4>, rows, StreamLayout(VS, R, 4, bf16).bytes};
+    return {linattn_stream<VS, R, 8>, rows, StreamLayout(VS, R, 8, bf16).bytes};
 }
 
 }  // namespace
 
 StepKernel step_kernel(int vs, int dk, int tg) {
-    if (vs == 128) return dk <= 64 ? pick<128, 8>(tg) : pick<128, 16>(tg);
     if (vs == 64) return dk <= 64 ? pick<64, 4>(tg) : dk <= 128 ? pick<64, 8>(tg) : pick<64, 16>(tg);
     return dk <= 64 ? pick<32, 2>(tg) : dk <= 128 ? pick<32, 4>(tg) : pick<32, 8>(tg);
+}
+StepKernel stream_kernel(int vs, int dk, int tg, bool bf16) {
+    if (vs == 128) return dk <= 64 ? pick_stream<128, 8>(tg, bf16) : pick_stream<128, 16>(tg, bf16);
+    if (vs == 64)
+        return dk <= 64    ? pick_stream<64, 4>(tg, bf16)
+               : dk <= 128 ? pick_stream<64, 8>(tg, bf16)
+                           : pick_stream<64, 16>(tg, bf16);
+    return dk <= 64    ? pick_stream<32, 2>(tg, bf16)
+           : dk <= 128 ? pick_stream<32, 4>(tg, bf16)
+                       : pick_stream<32, 8>(tg, bf16);
 }
 
 }  // namespace cvk
