@@ -112,6 +112,8 @@ cvk::LinattnParams make_linattn(const cv_linattn_args *a, bool step) {
     p.bf16 = a->dtype == CV_BF16;
     p.update = step ? a->update_state != 0 : 1;
     p.st_vec = a->dv % 4 == 0 && aligned(a->state, 16) && a->state_slot_stride % 4 == 0 && a->state_head_stride % 4 == 0;
+    p.o_vec = rows_of(4, a->out, a->out_seq_stride, a->out_tok_stride, a->out_head_stride, a->tok.cu, a->dv,
+                      esize_of(a->dtype));
     p.scale = a->scale;
     return p;
 }
@@ -120,19 +122,20 @@ int launch_recurrent(const cv_linattn_args *a, bool step, cudaStream_t stream) {
     cvk::LinattnParams p = make_linattn(a, step);
     const long long heads = (long long)a->n_seq * a->n_heads, sms = device_limits().sms;
     const int most = step && a->prev.T > a->tok.T ? a->prev.T : a->tok.T;
-    const bool stream_ok = p.st_vec && (run_empty(a->tok) || p.tok.vec16) && (!step || run_empty(a->prev) || p.prev.vec16);
+    const bool stream_ok = p.st_vec && a->dk <= 128 && (run_empty(a->tok) || p.tok.vec16) && (!step || run_empty(a->prev) || p.prev.vec16);
     // the widest slice of a head whose grid still gives every SM two blocks
-    int vs = stream_ok && a->dk <= 128 && a->dv > 64 ? 128 : a->dv > 32 ? 64 : 32;
-    while (vs > 32 && heads * ((a->dv + vs - 1) / vs) < 2 * sms) vs /= 2;
+    int vs = stream_ok ? 128 : 64;
+    while (vs > 32 && (vs / 2 >= a->dv || heads * ((a->dv + vs - 1) / vs) < 2 * sms)) vs /= 2;
     p.slices = (a->dv + vs - 1) / vs;
     const long long units = heads * p.slices;
-    // tokens a pass; fp32 rows are twice as long: 4 of them leave room for two blocks per SM
-    int tg = most <= 1 ? 1 : most <= 4 && stream_ok ? 4 : cvk::kStepMaxGroup;
-    if (stream_ok && tg > 4 && !p.bf16 && vs == 128) tg = 4;
-    const cvk::StepKernel k = stream_ok ? cvk::stream_kernel(vs, a->dk, tg, p.bf16) : cvk::step_kernel(vs, a->dk, tg);
+    const int tg = most <= 1 ? 1 : cvk::kStepMaxGroup;
+    const cvk::StepKernel k = stream_ok ? cvk::stream_kernel(vs / 16, a->dk, tg, p.bf16) : cvk::step_kernel(vs, a->dk, tg);
     if (cvk::ensure_smem(reinterpret_cast<const void *>(k.fn), k.smem_bytes) != cudaSuccess) return CV_ERR_LAUNCH;
-    const long long grid = stream_ok && units > 2 * sms ? 2 * sms : units;
-    if (launch_pdl(k.fn, dim3((unsigned)grid), dim3(cvk::kStepThreads), k.smem_bytes, stream, p) != cudaSuccess)
+    // resident blocks of the streaming kernel: its registers allow 16 warps per SM
+    const long long resident = sms * (256 / vs);
+    const int threads = stream_ok ? 2 * vs : cvk::kStepThreads;
+    if (launch_pdl(k.fn, dim3((unsigned)(stream_ok && units > resident ? resident : units)), dim3(threads), k.smem_bytes,
+                   stream, p) != cudaSuccess)
         return CV_ERR_LAUNCH;
     return cudaGetLastError() == cudaSuccess ? CV_OK : CV_ERR_LAUNCH;
 }

@@ -35,6 +35,7 @@ struct LinattnParams {
     int n_seq, n_heads, n_qk, dk, dv, n_slots;
     int bf16;    // dtype of q, k, v and out: bf16, else fp32
     int update;  // leave the state after the tokens
+    int o_vec;   // out allows 4 elements at once at multiples of 4 (checked on the host)
     int st_vec;  // state rows allow 16-byte accesses (checked on the host)
     int slices;  // column slices of a head's state, one block each
     float scale;
@@ -58,27 +59,25 @@ struct StepKernel {
 };
 // Any alignment; vs: 64 or 32; tg: 1 or kStepMaxGroup; dk <= 256.
 StepKernel step_kernel(int vs, int dk, int tg);
-// Rows aligned to 16 bytes; vs: 128 (dk <= 128), 64 or 32; tg: 1, 4 or 8.
-StepKernel stream_kernel(int vs, int dk, int tg, bool bf16);
+// Rows aligned to 16 bytes; blocks of 2, 4 or 8 warps of 16 columns each; dk <= 128; tg: 1 or kStepMaxGroup.
+StepKernel stream_kernel(int warps, int dk, int tg, bool bf16);
 
 // Shared memory of linattn_stream, in bytes from its start: the state tile, two buffers of raw rows (k, q
-// and v of TG tokens, each row 16 bytes longer than it is to spread the banks, decays, gains), then
-// q and k [rows][TG], v [TG][VS], partial outputs [row groups][min(TG, 4)][VS], token products, decays, gains,
-// and the units at hand.
+// and v of TG tokens, each row 16 bytes longer than it is to spread the banks; decays, gains), the products
+// of the group's tokens, and the units at hand.
 struct StepUnit {
     int s, h, slice;
     int slot, n_tok, row0, n_prev, prow0, status;
     bool on, init;
 };
 struct StreamLayout {
-    int raw, raw_bytes, q, ring, bytes;
-    __host__ __device__ constexpr StreamLayout(int VS, int R, int TG, bool bf16)
-        : raw(R * kStepThreads * 16),
-          raw_bytes(TG * (2 * (R * (kStepThreads / (VS / 4)) * (bf16 ? 2 : 4) + 16) + VS * (bf16 ? 2 : 4) + 16) +
-                    (TG * 8 + 15) / 16 * 16),
-          q(raw + 2 * raw_bytes),
-          ring(q + 4 * (2 * R * (kStepThreads / (VS / 4)) * TG + TG * VS + 4 * kStepThreads * (TG < 4 ? TG : 4) + TG * TG +
-                        2 * TG)),
+    int raw, raw_bytes, products, ring, bytes;
+    __host__ __device__ static constexpr int row_bytes(int d, bool bf16) { return d * (bf16 ? 2 : 4) + 16; }
+    __host__ __device__ constexpr StreamLayout(int warps, int R, int TG, bool bf16)
+        : raw(R * warps * 32 * 16),
+          raw_bytes(TG * (2 * row_bytes(8 * R, bf16) + row_bytes(16 * warps, bf16)) + (TG * 8 + 15) / 16 * 16),
+          products(raw + 2 * raw_bytes),
+          ring(products + TG * TG * 4),
           bytes(ring + 4 * (int)sizeof(StepUnit)) {}
 };
 
