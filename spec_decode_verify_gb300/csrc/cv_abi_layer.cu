@@ -1,5 +1,8 @@
 // C ABI of the operators beside the conv: linear attention (prompts, single tokens and drafts) and the
 // block norms.  As for the conv, every check runs on the host before anything is launched.
+#include <cuda.h>
+
+#include <atomic>
 #include <cstdint>
 #include <cstring>
 
@@ -147,14 +150,48 @@ struct ChunkPlan {
     int dv_pad;
 };
 constexpr int kMinPieceChunks = 4;
+constexpr int64_t kMaxStride = 1LL << 38;  // elements: a tensor map's strides are below 2^40 bytes
+
+// The driver's encoder of tensor maps, looked up once.
+using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
+                                 const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiled encode_tiled() {
+    static std::atomic<EncodeTiled> found{nullptr};
+    EncodeTiled f = found.load(std::memory_order_relaxed);
+    if (f) return f;
+    void *fn = nullptr;
+    cudaDriverEntryPointQueryResult st;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &st) != cudaSuccess ||
+        st != cudaDriverEntryPointSuccess) {
+        cudaGetLastError();
+        return nullptr;
+    }
+    f = reinterpret_cast<EncodeTiled>(fn);
+    found.store(f, std::memory_order_relaxed);
+    return f;
+}
+// A map of [tokens][heads][d] bf16 rows read in boxes of 128 tokens of one head's 64 channels.
+bool encode_rows(CUtensorMap *map, const void *p, int d, int heads, int64_t tokens, int64_t head, int64_t tok) {
+    const EncodeTiled encode = encode_tiled();
+    if (!encode) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)tokens};
+    const cuuint64_t strides[2] = {(cuuint64_t)(heads > 1 ? head : d) * 2, (cuuint64_t)tok * 2};
+    const cuuint32_t box[3] = {64, 1, cvk::kChunk}, step[3] = {1, 1, 1};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(p), dims, strides, box, step,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 ChunkPlan plan_chunks(const cv_linattn_args *a) {
     ChunkPlan pl{0, 0, 0, a->dv <= 64 ? 64 : 128};
     const cv_linattn_tokens &t = a->tok;
+    // what the copies by TMA (q, k, v) and of 16 bytes (out, state) need
     auto rows8 = [](const void *p, int64_t tok, int64_t head) {
-        return aligned(p, 16) && tok % 8 == 0 && head % 8 == 0;
+        return aligned(p, 16) && tok % 8 == 0 && head % 8 == 0 && tok > 0 && tok < kMaxStride && head < kMaxStride;
     };
     if (a->dtype != CV_BF16 || a->dk % 8 != 0 || a->dv % 8 != 0 || a->dk > 128 || a->dv > 128 ||
+        (a->n_qk_heads > 1 && (t.q_head_stride == 0 || t.k_head_stride == 0)) || (a->n_heads > 1 && t.v_head_stride == 0) ||
         !rows8(t.q, t.q_tok_stride, t.q_head_stride) || !rows8(t.k, t.k_tok_stride, t.k_head_stride) ||
         !rows8(t.v, t.v_tok_stride, t.v_head_stride) || !rows8(a->out, a->out_tok_stride, a->out_head_stride) ||
         !aligned(a->state, 16) || a->state_slot_stride % 4 != 0 || a->state_head_stride % 4 != 0)
@@ -200,6 +237,12 @@ int launch_chunks(const cv_linattn_args *a, const ChunkPlan &pl, cudaStream_t st
         p.ws_state = reinterpret_cast<float *>(a->workspace);
         p.ws_decay = p.ws_state + pl.ws_states * cvk::kChunk * pl.dv_pad;
     }
+    const cv_linattn_tokens &t = a->tok;
+    if (t.total_tokens > 0 &&
+        (!encode_rows(&p.q_map, t.q, a->dk, a->n_qk_heads, t.total_tokens, t.q_head_stride, t.q_tok_stride) ||
+         !encode_rows(&p.k_map, t.k, a->dk, a->n_qk_heads, t.total_tokens, t.k_head_stride, t.k_tok_stride) ||
+         !encode_rows(&p.v_map, t.v, a->dv, a->n_heads, t.total_tokens, t.v_head_stride, t.v_tok_stride)))
+        return CV_ERR_LAUNCH;
     const cvk::ChunkKernel k = cvk::chunk_kernel(a->dv);
     if (cvk::ensure_smem(reinterpret_cast<const void *>(k.fn), k.smem_bytes) != cudaSuccess) return CV_ERR_LAUNCH;
     // the kernel ORs its bits into err

@@ -1,6 +1,7 @@
 // Internal: parameters and kernel tables of the linear-attention kernels.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 namespace cvk {
@@ -83,9 +84,10 @@ struct StreamLayout {
 
 // The chunked kernel for prompts (bf16, dk and dv multiples of 8 up to 128).
 constexpr int kChunk = 128;            // tokens a chunk
-constexpr int kChunkThreads = 672;     // 20 warps of roles and the one that issues the products
+constexpr int kChunkThreads = 640;     // 16 warps of the four large roles, 4 of one each
 constexpr int kChunkMaxSorted = 64;    // sequences that are taken longest first
 struct LinattnChunkParams {
+    CUtensorMap q_map, k_map, v_map;  // [token][head][channel], boxes of 128 x 1 x 64, 128-byte swizzle
     LinattnParams a;
     int n_segs;      // pieces a sequence is cut into, at most
     int seg_len;     // tokens a piece, a multiple of kChunk

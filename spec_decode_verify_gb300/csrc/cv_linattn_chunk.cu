@@ -14,16 +14,17 @@
 // Layout.  A block (one per SM) takes units (sequence, head, piece of its length) and walks each unit's
 // chunks; every role below runs the same stream of chunks, so the next unit's loads and products
 // start while the last one's outputs are still being written.
-//   load    4 warps, two for each of two stages: q, k, v tiles by cp.async, swizzled, rows past the end
-//           and padded channels zero
 //   scores  4 warps, a row a thread: Q K^T from tensor memory, times the decays, back to it as A
-//   keys    4 warps, a token a thread: K' in place of K, its low part in place of Q once Q is used up
+//   keys    4 warps, a token a thread: K' in place of K (once Q K^T is done) and its low part
 //   state   4 warps, a row of S a thread: S from tensor memory, bf16 copy to shared memory, S times the
 //           chunk's decay back
-//   output  4 warps, a row a thread: out = scale exp(G) (Q S) + A V, rounded and stored
-//   issue   1 thread: all products
-// Shared memory: 2 stages of (q 32 KB, k 32 KB, v 32 or 16 KB), the copy of S; tensor memory: Q K^T
-// (then A) 128 columns, Q S, A V and S dv columns each.
+//   output  4 warps, a row a thread: out = scale exp(G) (Q S) + A V, rounded, through the dead v tile out
+//   decays  1 warp: sums of the log decays, ahead of the others
+//   load    1 thread: q, k, v tiles by TMA in the 128-byte swizzle, channels past the end zero
+//   issue   1 thread: all products, in the order Q K^T, Q S, K'^T V, A V
+// Shared memory: k and v in two stages, q, the low part of K' and the copy of S once (32 KB each at 128
+// channels); tensor memory: Q K^T (then A) 128 columns, Q S, A V and S dv columns each.  A chunk's products
+// take 2560 cycles of the tensor pipe; the longest cycle through the roles is K'^T V -> S -> Q S.
 //
 // Every wait is bounded; one that gives up ends the block's work, flags the sequences it had left and
 // returns.
@@ -35,13 +36,13 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kMinLog2 = -200.0f * kLog2e;
-constexpr unsigned kPolls = 1u << 20;
+constexpr unsigned kPolls = 1u << 16;
 constexpr int kTileQK = kChunk * 256;  // bytes of a q or k tile: two blocks of 64 channels
 
 // Barriers, in order (8 bytes each), then the small arrays.
 struct ChunkShared {
-    uint64_t full[2], empty[2], q_empty[2];
-    uint64_t scores, a_ready, keys, q_used, s_init, s_ready, s_done, out, out_free, last;
+    uint64_t kv_full[2], g_full[2], k_empty[2], v_empty[2];
+    uint64_t q_full, scores, a_ready, keys, q_used, s_init, s_ready, s_done, out, out_free, last;
     uint32_t tmem;
     int dead;
     uint8_t order[kChunkMaxSorted];
@@ -55,7 +56,7 @@ struct ChunkShared {
 
 template <int DV>
 __host__ __device__ constexpr int chunk_smem_bytes() {
-    return 2 * (2 * kTileQK + kChunk * DV * 2) + kChunk * DV * 2 + (int)sizeof(ChunkShared);
+    return 2 * (kTileQK + kChunk * DV * 2) + 2 * kTileQK + kChunk * DV * 2 + (int)sizeof(ChunkShared);
 }
 
 struct Unit {
@@ -95,10 +96,20 @@ __device__ __forceinline__ int unit_index(const LinattnChunkParams &p, int n) {
     return idx < p.units ? (int)idx : (long long)n * G < p.units ? -2 : -1;
 }
 
+// One poll of a barrier's phase, which may suspend the thread for up to 20 us.
+__device__ __forceinline__ bool poll(uint64_t *bar, unsigned parity) {
+    unsigned done;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 20000;\n selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(done)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return done != 0;
+}
 // Bounded wait of a whole warp; false once the block has given up.
 __device__ __forceinline__ bool wait_warp(uint64_t *bar, unsigned parity, volatile int *dead) {
     for (unsigned i = 0; i < kPolls; ++i) {
-        if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+        if (__all_sync(0xffffffffu, poll(bar, parity))) return true;
         if (__any_sync(0xffffffffu, *dead)) return false;
     }
     *dead = 1;
@@ -106,7 +117,7 @@ __device__ __forceinline__ bool wait_warp(uint64_t *bar, unsigned parity, volati
 }
 __device__ __forceinline__ bool wait_one(uint64_t *bar, unsigned parity, volatile int *dead) {
     for (unsigned i = 0; i < kPolls; ++i) {
-        if (mbar_try_wait(bar, parity)) return true;
+        if (poll(bar, parity)) return true;
         if (*dead) return false;
     }
     *dead = 1;
@@ -143,8 +154,13 @@ __device__ __forceinline__ float clamp_log2(float g) {
     return g < kMinLog2 ? kMinLog2 : g;  // a NaN stays
 }
 
-__device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void *src, bool on) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(on ? 16u : 0u) : "memory");
+// A box of 64 channels of 128 tokens of one head into shared memory.
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap *map, int c, int h, int t, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];\n" ::"r"(
+            dst),
+        "l"(map), "r"(c), "r"(h), "r"(t), "r"(smem_u32(bar))
+        : "memory");
 }
 
 // A NaN or an infinity in v spoils the rows above it in A V (0 * NaN).  This computes one row of the
@@ -183,11 +199,11 @@ __device__ __forceinline__ void weigh(const uint32_t *r, float rf, const float *
 
 template <int DV>
 __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_constant__ LinattnChunkParams p) {
-    constexpr int kTileV = kChunk * DV * 2;
-    constexpr int kStage = 2 * kTileQK + kTileV;
+    constexpr int kTileV = kChunk * DV * 2, kBlock = kChunk * 128;  // a tile's blocks of 64 channels
     constexpr uint32_t kColP = 0, kColQS = 128, kColAV = 128 + DV, kColS = 128 + 2 * DV, kCols = 512;
     extern __shared__ __align__(1024) unsigned char smem[];
-    unsigned char *const s_copy = smem + 2 * kStage;
+    unsigned char *const k_tile = smem, *const v_tile = smem + 2 * kTileQK;  // stage s at + s * its size
+    unsigned char *const q_tile = v_tile + 2 * kTileV, *const lo_tile = q_tile + kTileQK, *const s_copy = lo_tile + kTileQK;
     ChunkShared *const sh = reinterpret_cast<ChunkShared *>(s_copy + kTileV);
     const LinattnParams &a = p.a;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -195,14 +211,16 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
 
     // the layout below needs its bytes and the swizzle's alignment
     if (dynamic_smem_bytes() < chunk_smem_bytes<DV>() || (smem_u32(smem) & 1023u) != 0) return;
-    if (warp == 20) tmem_alloc(&sh->tmem, kCols);
+    if (warp == 19) tmem_alloc(&sh->tmem, kCols);
     if (tid == 0) {
         sh->dead = 0;
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&sh->full[i], 2);
-            mbar_init(&sh->empty[i], 1);
-            mbar_init(&sh->q_empty[i], 4);
+            mbar_init(&sh->kv_full[i], 1);
+            mbar_init(&sh->g_full[i], 1);
+            mbar_init(&sh->k_empty[i], 1);
+            mbar_init(&sh->v_empty[i], 4);
         }
+        mbar_init(&sh->q_full, 1);
         mbar_init(&sh->scores, 1);
         mbar_init(&sh->a_ready, 4);
         mbar_init(&sh->keys, 4);
@@ -236,70 +254,82 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
     const uint32_t tl = tm + ((uint32_t)(32 * w4) << 16);
 
     int it = 0;  // chunks of the stream so far
-    if (role == 4 && warp < 20) {
-        // ------------------------------------------------------------------------------ load
-        const int stage = w4 >> 1, t64 = tid & 63;
-        unsigned char *const base = smem + stage * kStage;
+    if (warp == 16) {
+        // ---------------------------------------------------------------------------- decays
         bool ok = true;
         for (int n = 0, idx; ok && (idx = unit_index(p, n)) != -1; ++n) {
             if (idx < 0) continue;
             const Unit u = unit_of(p, sh, idx);
-            if (a.err && u.h == 0 && u.seg == 0 && warp == 16 && lane == 0 && u.slot >= 0) {
+            if (a.err && u.h == 0 && u.seg == 0 && lane == 0 && u.slot >= 0) {
                 int L, row0;
                 const int st = (u.slot >= a.n_slots ? 1 : 0) | draft_span(a.tok.cu, u.s, a.tok.T, a.tok.total, L, row0);
                 if (st) atomicOr(a.err + u.s, st);
             }
             for (int c = 0; c < u.chunks; ++c, ++it) {
-                if ((it & 1) != stage) continue;
-                if (it >= 2 && !wait_warp(&sh->empty[stage], ((it >> 1) & 1) ^ 1, dead)) {
-                    ok = false;
-                    break;
-                }
-                const int t0 = c * kChunk, rows = min(kChunk, u.n - t0);
-                const long long row = u.row0 + t0;
-                // decays and gains of tokens t64 and t64 + 64
-                float g[2], b[2];
+                const int stage = it & 1, rows = u.n - c * kChunk;
+                const long long row = u.row0 + c * kChunk;
+                float g[4], b[4];
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const int t = t64 + 64 * x;
+                for (int x = 0; x < 4; ++x) {
+                    const int t = 32 * x + lane;
                     g[x] = t < rows ? __ldg(a.tok.g + (row + t) * a.tok.g_tok + u.h) : 0.0f;
                     b[x] = t < rows ? (a.tok.b ? __ldg(a.tok.b + (row + t) * a.tok.b_tok + u.h) : 1.0f) : 0.0f;
                 }
-                const uint32_t d = smem_u32(base);
-                // rows of 16 pieces (two blocks of 64 channels) or of 8
-                auto tile = [&](uint32_t dst, const void *src, long long at, long long tok, int width, bool wide) {
-                    const int pc = wide ? t64 & 15 : t64 & 7, r0 = wide ? t64 >> 4 : t64 >> 3, by = wide ? 4 : 8;
-                    const uint16_t *s0 = reinterpret_cast<const uint16_t *>(src) + at;
-                    const uint16_t *ptr = s0 + r0 * tok + pc * 8;
-                    const int end = pc * 8 < width ? rows : 0;
-                    const uint32_t d0 = dst + (pc >> 3) * (kChunk * 128);
-#pragma unroll 4
-                    for (int r = r0; r < kChunk; r += by, ptr += by * tok)
-                        cp_async16_zfill(d0 + swizzled(r, pc & 7), r < end ? ptr : s0, r < end);
-                };
-                tile(d + kTileQK, a.tok.k, row * a.tok.k_tok + u.hq * a.tok.k_head, a.tok.k_tok, a.dk, true);
-                tile(d + 2 * kTileQK, a.tok.v, row * a.tok.v_tok + u.h * a.tok.v_head, a.tok.v_tok, a.dv, DV == 128);
+                // the last chunk in this place is through with them once its outputs are out
+                if (it >= 2 && !wait_warp(so ? &sh->k_empty[stage] : &sh->v_empty[stage], ((it >> 1) & 1) ^ 1, dead)) {
+                    ok = false;
+                    break;
+                }
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {  // a block of 32 tokens each
+                    const float l2 = clamp_log2(g[x]), G = prefix_sum(l2, lane);
+                    sh->G[stage][32 * x + lane] = G;
+                    sh->cw[stage][32 * x + lane] = exp2_fast(suffix_after(l2, lane)) * b[x];
+                    if (lane == 31) sh->tot[stage][x] = G;
+                }
+                arrive_warp(&sh->g_full[stage]);
+            }
+        }
+    } else if (warp == 17 && lane == 0) {
+        // ------------------------------------------------------------------------------ load
+        bool ok = true;
+        for (int n = 0, idx; ok && (idx = unit_index(p, n)) != -1; ++n) {
+            if (idx < 0) continue;
+            const Unit u = unit_of(p, sh, idx);
+            for (int c = 0; c < u.chunks; ++c, ++it) {
+                const int stage = it & 1, row = u.row0 + c * kChunk;
+                const unsigned ph = ((it >> 1) & 1) ^ 1;
+                if (it >= 2 && (!wait_one(&sh->k_empty[stage], ph, dead) || (!so && !wait_one(&sh->v_empty[stage], ph, dead)))) {
+                    ok = false;
+                    break;
+                }
+                uint64_t *const bar = &sh->kv_full[stage];
+                const uint32_t k = smem_u32(k_tile + stage * kTileQK), v = smem_u32(v_tile + stage * kTileV);
+                mbar_arrive_expect_tx(bar, kTileQK + kTileV);
+                tma_load(k, &p.k_map, 0, u.hq, row, bar);
+                tma_load(k + kBlock, &p.k_map, 64, u.hq, row, bar);
+                tma_load(v, &p.v_map, 0, u.h, row, bar);
+                if (DV == 128) tma_load(v + kBlock, &p.v_map, 64, u.h, row, bar);
                 if (!so) {
-                    // the q tile carries the outputs out
-                    if (it >= 2 && !wait_warp(&sh->q_empty[stage], ((it >> 1) & 1) ^ 1, dead)) {
+                    if (it >= 1 && !wait_one(&sh->q_used, (it - 1) & 1, dead)) {
+                        ++it;  // this chunk's k and v are in flight
                         ok = false;
                         break;
                     }
-                    tile(d, a.tok.q, row * a.tok.q_tok + u.hq * a.tok.q_head, a.tok.q_tok, a.dk, true);
+                    const uint32_t q = smem_u32(q_tile);
+                    mbar_arrive_expect_tx(&sh->q_full, kTileQK);
+                    tma_load(q, &p.q_map, 0, u.hq, row, &sh->q_full);
+                    tma_load(q + kBlock, &p.q_map, 64, u.hq, row, &sh->q_full);
                 }
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {  // a warp's 32 tokens are a block
-                    const float l2 = clamp_log2(g[x]), G = prefix_sum(l2, lane);
-                    sh->G[stage][t64 + 64 * x] = G;
-                    sh->cw[stage][t64 + 64 * x] = exp2_fast(suffix_after(l2, lane)) * b[x];
-                    if (lane == 31) sh->tot[stage][2 * x + (w4 & 1)] = G;
-                }
-                cp_async_wait_all();
-                fence_smem_to_async();
-                arrive_warp(&sh->full[stage]);
             }
         }
-        cp_async_wait_all();
+        // nothing of the block's is in flight when it returns
+        if (!ok) {
+            if (it >= 1) mbar_wait_bounded(&sh->kv_full[(it - 1) & 1], ((it - 1) >> 1) & 1, kPolls);
+            if (it >= 2) mbar_wait_bounded(&sh->kv_full[it & 1], ((it - 2) >> 1) & 1, kPolls);
+            for (unsigned i = 0; !so && i < 2; ++i)  // whichever phase q's last copy completes
+                if (mbar_wait_bounded(&sh->q_full, i, kPolls / 64)) break;
+        }
     } else if (role == 0 && !so) {
         // ---------------------------------------------------------------------------- scores
         const float scale = a.scale;
@@ -310,7 +340,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
             const float skip = a.skip ? __ldg(a.skip + u.h) : 0.0f;
             for (int c = 0; c < u.chunks; ++c, ++it) {
                 const int stage = it & 1;
-                if (!wait_warp(&sh->full[stage], (it >> 1) & 1, dead) || !wait_warp(&sh->scores, it & 1, dead)) {
+                if (!wait_warp(&sh->g_full[stage], (it >> 1) & 1, dead) || !wait_warp(&sh->scores, it & 1, dead)) {
                     ok = false;
                     break;
                 }
@@ -318,20 +348,25 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
                 const float G = sh->G[stage][32 * w4 + lane];
                 const float *const cw = sh->cw[stage];
                 const float t1 = sh->tot[stage][1], t2 = sh->tot[stage][2];
-                uint32_t r[32], o[16];
+                uint32_t r[32], o[16], next[32];
+                tmem_ld32(r, tl + kColP);
                 // Row i against block J left of its own: 2^(G_i + blocks between) * cw_j.  A overlays the
                 // scores: block J goes to columns 16 J .., whose scores were read in an earlier round.
 #pragma unroll 1
                 for (int J = 0; J < w4; ++J) {
                     const float between = (J < 1 && w4 > 1 ? t1 : 0.0f) + (J < 2 && w4 > 2 ? t2 : 0.0f);
                     const float rf = exp2_fast(G + between) * scale;
-                    tmem_ld32(r, tl + kColP + 32 * J);
+                    tmem_wait_ld(r);
+                    tmem_ld32(next, tl + kColP + 32 * J + 32);
                     weigh(r, rf, cw + 32 * J, o);
                     tmem_st16(tl + kColP + 16 * J, o);
+                    tmem_wait_ld(next);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) r[j] = next[j];
                 }
                 // The block on the diagonal: 2^(G_i - G_j) b_j = 2^(G_i - G_end) cw_j while the block's whole
                 // decay is far from fp32's range, else one exponential per pair.
-                tmem_ld32(r, tl + kColP + 32 * w4);
+                tmem_wait_ld(r);
                 const float end = sh->tot[stage][w4];
                 if (end > -100.0f) {
                     const float rf = exp2_fast(G - end) * scale;
@@ -380,7 +415,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
             const Unit u = unit_of(p, sh, idx);
             for (int c = 0; c < u.chunks; ++c, ++it) {
                 const int stage = it & 1;
-                if (!wait_warp(&sh->full[stage], (it >> 1) & 1, dead)) {
+                if (!wait_warp(&sh->g_full[stage], (it >> 1) & 1, dead) || !wait_warp(&sh->kv_full[stage], (it >> 1) & 1, dead)) {
                     ok = false;
                     break;
                 }
@@ -388,46 +423,57 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
                 const float later = (w4 < 1 ? bt[1] : 0.0f) + (w4 < 2 ? bt[2] : 0.0f) + (w4 < 3 ? bt[3] : 0.0f);
                 const float w = exp2_fast(later) * sh->cw[stage][t];
                 const f2 w2 = f2_pack(w, w), neg = f2_pack(-1.0f, -1.0f);
-                if (!so && !wait_warp(&sh->scores, it & 1, dead)) {  // K is used up
+                // the tile holds whatever follows the sequence there
+                const uint32_t keep = t < u.n - c * kChunk ? 0xffffffffu : 0u;
+                // the low part's place is free once the last chunk's products are done (and this role never runs
+                // two phases ahead of the issue thread)
+                if (it > 0 && !wait_warp(&sh->s_done, (it - 1) & 1, dead)) {
                     ok = false;
                     break;
                 }
-                unsigned char *const kt = smem + stage * kStage + kTileQK;
-                unsigned char *const qt = smem + stage * kStage;
-                uint32_t lo[64];
+                unsigned char *const kt = k_tile + stage * kTileQK;
+                uint32_t hi[64];
 #pragma unroll
-                for (int x = 0; x < 16; ++x) {
-                    uint4 *at = reinterpret_cast<uint4 *>(kt + (x >> 3) * (kChunk * 128) + swizzled(t, x & 7));
-                    const uint4 v = *at;
-                    const uint32_t in[4] = {v.x, v.y, v.z, v.w};
-                    uint32_t hi[4];
+                for (int x0 = 0; x0 < 16; x0 += 4) {  // four pieces at a time: their latencies overlap
+                    uint4 in[4], lo[4];
 #pragma unroll
-                    for (int y = 0; y < 4; ++y) {
-                        const f2 f = f2_mul(f2_pack(__uint_as_float(in[y] << 16), __uint_as_float(in[y] & 0xffff0000u)), w2);
-                        float f0, f1;
-                        f2_unpack(f, f0, f1);
-                        hi[y] = pack_bf16(f0, f1);
-                        f2_unpack(f2_fma(f2_pack(__uint_as_float(hi[y] << 16), __uint_as_float(hi[y] & 0xffff0000u)), neg, f),
-                                  f0, f1);
-                        lo[4 * x + y] = pack_bf16(f0, f1);
+                    for (int x = 0; x < 4; ++x)
+                        in[x] = *reinterpret_cast<const uint4 *>(kt + (x0 >> 3) * kBlock + swizzled(t, (x0 + x) & 7));
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const uint32_t w[4] = {in[x].x & keep, in[x].y & keep, in[x].z & keep, in[x].w & keep};
+                        uint32_t l[4];
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) {
+                            const f2 f = f2_mul(f2_pack(__uint_as_float(w[y] << 16), __uint_as_float(w[y] & 0xffff0000u)), w2);
+                            float f0, f1;
+                            f2_unpack(f, f0, f1);
+                            const uint32_t h = pack_bf16(f0, f1);
+                            hi[4 * (x0 + x) + y] = h;
+                            f2_unpack(f2_fma(f2_pack(__uint_as_float(h << 16), __uint_as_float(h & 0xffff0000u)), neg, f), f0, f1);
+                            l[y] = pack_bf16(f0, f1);
+                        }
+                        lo[x] = make_uint4(l[0], l[1], l[2], l[3]);
                     }
-                    *at = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+                        *reinterpret_cast<uint4 *>(lo_tile + (x0 >> 3) * kBlock + swizzled(t, (x0 + x) & 7)) = lo[x];
                 }
-                if (!so && !wait_warp(&sh->q_used, it & 1, dead)) {
+                if (!keep) {  // v past the end: zeros too
+#pragma unroll 1
+                    for (int x = 0; x < DV / 8; ++x)
+                        *reinterpret_cast<uint4 *>(v_tile + stage * kTileV + (x >> 3) * kBlock + swizzled(t, x & 7)) =
+                            make_uint4(0u, 0u, 0u, 0u);
+                }
+                if (!so && !wait_warp(&sh->scores, it & 1, dead)) {  // k is used up
                     ok = false;
                     break;
                 }
 #pragma unroll
                 for (int x = 0; x < 16; ++x)
-                    *reinterpret_cast<uint4 *>(qt + (x >> 3) * (kChunk * 128) + swizzled(t, x & 7)) =
-                        make_uint4(lo[4 * x], lo[4 * x + 1], lo[4 * x + 2], lo[4 * x + 3]);
+                    *reinterpret_cast<uint4 *>(kt + (x >> 3) * kBlock + swizzled(t, x & 7)) =
+                        make_uint4(hi[4 * x], hi[4 * x + 1], hi[4 * x + 2], hi[4 * x + 3]);
                 fence_smem_to_async();
-                // without outputs nothing else keeps this role from running a chunk ahead of the issue thread,
-                // which would then miss a phase
-                if (so && it > 0 && !wait_warp(&sh->s_done, (it - 1) & 1, dead)) {
-                    ok = false;
-                    break;
-                }
                 arrive_warp(&sh->keys);
             }
         }
@@ -500,7 +546,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
             float total = 1.0f;
             for (int c = 0; c < u.chunks; ++c, ++it) {
                 const int stage = it & 1;
-                if (!wait_warp(&sh->full[stage], (it >> 1) & 1, dead) ||
+                // the last chunk's products into S are done, and those that read the copy
+                if (!wait_warp(&sh->g_full[stage], (it >> 1) & 1, dead) ||
                     (c > 0 && !wait_warp(&sh->s_done, (it - 1) & 1, dead))) {
                     ok = false;
                     break;
@@ -510,10 +557,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
                 const float tot = exp2_fast((bt.x + bt.y) + (bt.z + bt.w));
                 const f2 tot2 = f2_pack(tot, tot);
                 total *= tot;
+                uint32_t v[32], next[32];
+                tmem_ld32(v, ts);
 #pragma unroll 1
                 for (int j = 0; j < DV; j += 32) {
-                    uint32_t v[32];
-                    tmem_ld32(v, ts + j);
+                    tmem_wait_ld(v);
+                    if (j + 32 < DV) tmem_ld32(next, ts + j + 32);
                     if (!so) {
 #pragma unroll
                         for (int x = 0; x < 32; x += 8) {
@@ -523,7 +572,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
                             o.z = pack_bf16(__uint_as_float(v[x + 4]), __uint_as_float(v[x + 5]));
                             o.w = pack_bf16(__uint_as_float(v[x + 6]), __uint_as_float(v[x + 7]));
                             const int pc = (j + x) / 8;
-                            *reinterpret_cast<uint4 *>(s_copy + (pc >> 3) * (kChunk * 128) + swizzled(r, pc & 7)) = o;
+                            *reinterpret_cast<uint4 *>(s_copy + (pc >> 3) * kBlock + swizzled(r, pc & 7)) = o;
                         }
                     }
 #pragma unroll
@@ -533,6 +582,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
                         v[x] = __float_as_uint(f0), v[x + 1] = __float_as_uint(f1);
                     }
                     tmem_st32(ts + j, v);
+                    if (j + 32 < DV) {
+                        tmem_wait_ld(next);
+#pragma unroll
+                        for (int x = 0; x < 32; ++x) v[x] = next[x];
+                    }
                 }
                 tmem_wait_st();
                 tmem_fence_before();
@@ -551,6 +605,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
                 for (int j = 0; j < DV; j += 32) {
                     uint32_t v[32];
                     tmem_ld32(v, ts + j);
+                    tmem_wait_ld(v);
 #pragma unroll
                     for (int x = 0; x < 8; ++x)
                         dst[(j / 4 + x) * 128 + r] = make_float4(__uint_as_float(v[4 * x]), __uint_as_float(v[4 * x + 1]),
@@ -564,6 +619,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
                     for (int j = 0; j < PW; j += 8) {
                         uint32_t v[32];
                         tmem_ld32(v, ts + (h * PW + j) * 4);
+                        tmem_wait_ld(v);
 #pragma unroll
                         for (int x = 0; x < 8; ++x)
                             mine[lane * PW + ((j + x) ^ (lane & 7))] =
@@ -590,7 +646,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
             const Unit u = unit_of(p, sh, idx);
             for (int c = 0; c < u.chunks; ++c, ++it) {
                 const int stage = it & 1;
-                if (!wait_warp(&sh->full[stage], (it >> 1) & 1, dead)) {
+                if (!wait_warp(&sh->g_full[stage], (it >> 1) & 1, dead)) {
                     ok = false;
                     break;
                 }
@@ -605,27 +661,35 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
                 tmem_fence_after();
                 const int t0 = c * kChunk;
                 const bool mine = t0 + i < u.n;
-                unsigned char *const qt = smem + stage * kStage;  // q is used up: the rows go through its tile
+                unsigned char *const vt = v_tile + stage * kTileV;  // v is used up: the rows go through its tile
                 f2 bad2 = f2_pack(0.0f, 0.0f);  // stays 0 while every output is finite
                 auto store = [&](int j, const uint32_t *o) {
-                    unsigned char *const at = qt + (j >> 6) * (kChunk * 128);
+                    unsigned char *const at = vt + (j >> 6) * kBlock;
                     *reinterpret_cast<uint4 *>(at + swizzled(i, (j >> 3) & 7)) = make_uint4(o[0], o[1], o[2], o[3]);
                     *reinterpret_cast<uint4 *>(at + swizzled(i, ((j >> 3) & 7) + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
                 };
+                uint32_t xy[32], next[32];  // 16 columns of Q S, then of A V
+                tmem_ld16x2(xy, tl + kColQS, tl + kColAV);
 #pragma unroll 1
                 for (int j = 0; j < DV; j += 16) {
-                    uint32_t x[16], y[16], o[8];
-                    tmem_ld16x2(x, y, tl + kColQS + j, tl + kColAV + j);
+                    uint32_t o[8];
+                    tmem_wait_ld(xy);
+                    if (j + 16 < DV) tmem_ld16x2(next, tl + kColQS + j + 16, tl + kColAV + j + 16);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        const f2 f = f2_fma(pre2, f2_pack(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])),
-                                            f2_pack(__uint_as_float(y[2 * e]), __uint_as_float(y[2 * e + 1])));
+                        const f2 f = f2_fma(pre2, f2_pack(__uint_as_float(xy[2 * e]), __uint_as_float(xy[2 * e + 1])),
+                                            f2_pack(__uint_as_float(xy[16 + 2 * e]), __uint_as_float(xy[17 + 2 * e])));
                         float f0, f1;
                         f2_unpack(f, f0, f1);
                         bad2 = f2_fma(f, f2_pack(0.0f, 0.0f), bad2);
                         o[e] = pack_bf16(f0, f1);
                     }
                     store(j, o);
+                    if (j + 16 < DV) {
+                        tmem_wait_ld(next);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) xy[e] = next[e];
+                    }
                 }
                 float bad0, bad1;
                 f2_unpack(bad2, bad0, bad1);
@@ -641,14 +705,15 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
                     if (__any_sync(0xffffffffu, found))
 #pragma unroll 1
                         for (int j = 0; j < DV; j += 16) {
-                            uint32_t x[16], y[16], o[8];
+                            uint32_t o[8];
                             float part[16];
-                            tmem_ld16x2(x, y, tl + kColQS + j, tl + kColAV + j);
+                            tmem_ld16x2(xy, tl + kColQS + j, tl + kColAV + j);
+                            tmem_wait_ld(xy);
                             if (mine) row_long_way(a, u, t0, i, j, part);
 #pragma unroll
                             for (int e = 0; e < 8; ++e)
-                                o[e] = pack_bf16(fmaf(pre, __uint_as_float(x[2 * e]), part[2 * e]),
-                                                 fmaf(pre, __uint_as_float(x[2 * e + 1]), part[2 * e + 1]));
+                                o[e] = pack_bf16(fmaf(pre, __uint_as_float(xy[2 * e]), part[2 * e]),
+                                                 fmaf(pre, __uint_as_float(xy[2 * e + 1]), part[2 * e + 1]));
                             store(j, o);
                             __syncwarp();
                         }
@@ -663,72 +728,67 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
                 const int end = pc * 8 < a.dv ? u.n - t0 : 0;
 #pragma unroll 4
                 for (int r = r0; r < 32 * w4 + 32; r += RP, dst += RP * a.o_tok) {
-                    const uint4 v = *reinterpret_cast<const uint4 *>(qt + (pc >> 3) * (kChunk * 128) + swizzled(r, pc & 7));
+                    const uint4 v = *reinterpret_cast<const uint4 *>(vt + (pc >> 3) * kBlock + swizzled(r, pc & 7));
                     if (r < end) *reinterpret_cast<uint4 *>(dst) = v;
                 }
-                arrive_warp(&sh->q_empty[stage]);
+                fence_smem_to_async();
+                arrive_warp(&sh->v_empty[stage]);
             }
         }
-    } else if (warp == 20 && lane == 0) {
+    } else if (warp == 18 && lane == 0) {
         // ----------------------------------------------------------------------------- issue
-        const uint32_t sb = smem_u32(smem), sc = smem_u32(s_copy);
-        constexpr uint32_t kBlock = kChunk * 128;
+        const uint32_t q = desc_k(smem_u32(q_tile)), sc = desc_mn(smem_u32(s_copy), kBlock),
+                       lo = desc_mn(smem_u32(lo_tile), kBlock);
         constexpr uint32_t id_qk = mma_desc(128, false, false), id_qs = mma_desc(DV, false, true),
                            id_kv = mma_desc(DV, true, true);
-        int left = 0, n = 0;  // chunks left of the current unit, the next unit
-        auto more = [&]() {
-            for (int idx; left == 0 && (idx = unit_index(p, n)) != -1; ++n)
-                if (idx >= 0) left = unit_of(p, sh, idx).chunks;
-            if (left == 0) return false;
-            --left;
-            return true;
-        };
-        auto scores = [&](int i) {
-            if (!wait_one(&sh->full[i & 1], (i >> 1) & 1, dead)) return false;
-            tmem_fence_after();
-            const uint32_t q = sb + (i & 1) * kStage, k = q + kTileQK;
+        bool ok = true;
+        for (int n = 0, idx; ok && (idx = unit_index(p, n)) != -1; ++n) {
+            if (idx < 0) continue;
+            const int chunks = unit_of(p, sh, idx).chunks;
+            for (int c = 0; c < chunks; ++c, ++it) {
+                const int stage = it & 1;
+                const uint32_t kt = smem_u32(k_tile + stage * kTileQK), k = desc_mn(kt, kBlock),
+                               v = desc_mn(smem_u32(v_tile + stage * kTileV), kBlock);
+                ok = false;
+                if (!so) {
+                    // the last chunk's A, under the scores, is used up by the products before these
+                    if (!wait_one(&sh->kv_full[stage], (it >> 1) & 1, dead) || !wait_one(&sh->q_full, it & 1, dead)) break;
+                    tmem_fence_after();
 #pragma unroll
-            for (int x = 0; x < 8; ++x) {
-                const uint32_t off = (x >> 2) * kBlock + (x & 3) * 32;
-                mma_ss(tm + kColP, desc_k(q + off), desc_k(k + off), id_qk, x > 0);
-            }
-            mma_commit(&sh->scores);
-            return true;
-        };
-        bool have = more();
-        bool ok = !have || so || scores(0);
-        while (ok && have) {
-            const uint32_t q = sb + (it & 1) * kStage, k = q + kTileQK, v = k + kTileQK;
-            if (!wait_one(&sh->s_ready, it & 1, dead)) break;
-            if (!so) {
-                if (it > 0 && !wait_one(&sh->out_free, (it - 1) & 1, dead)) break;
+                    for (int x = 0; x < 8; ++x) {
+                        const uint32_t off = ((x >> 2) * kBlock + (x & 3) * 32) >> 4;
+                        mma_ss(tm + kColP, q + off, desc_k(kt) + off, id_qk, x > 0);
+                    }
+                    mma_commit(&sh->scores);
+                }
+                if (!wait_one(&sh->s_ready, it & 1, dead)) break;
+                if (!so) {
+                    if (it > 0 && !wait_one(&sh->out_free, (it - 1) & 1, dead)) break;
+                    tmem_fence_after();
+#pragma unroll
+                    for (int x = 0; x < 8; ++x)
+                        mma_ss(tm + kColQS, q + (((x >> 2) * kBlock + (x & 3) * 32) >> 4), sc + x * 128, id_qs, x > 0);
+                    mma_commit(&sh->q_used);
+                }
+                if (!wait_one(&sh->keys, it & 1, dead)) break;
                 tmem_fence_after();
 #pragma unroll
-                for (int x = 0; x < 8; ++x)
-                    mma_ss(tm + kColQS, desc_k(q + (x >> 2) * kBlock + (x & 3) * 32), desc_mn(sc + x * 2048, kBlock),
-                           id_qs, x > 0);
-                mma_commit(&sh->q_used);
-            }
-            if (!wait_one(&sh->keys, it & 1, dead)) break;
-            tmem_fence_after();
+                for (int x = 0; x < 8; ++x) {
+                    mma_ss(tm + kColS, k + x * 128, v + x * 128, id_kv, true);
+                    mma_ss(tm + kColS, lo + x * 128, v + x * 128, id_kv, true);
+                }
+                mma_commit(&sh->s_done);
+                mma_commit(&sh->k_empty[stage]);
+                if (!so) {
+                    if (!wait_one(&sh->a_ready, it & 1, dead)) break;
+                    tmem_fence_after();
 #pragma unroll
-            for (int x = 0; x < 8; ++x) {
-                mma_ss(tm + kColS, desc_mn(k + x * 2048, kBlock), desc_mn(v + x * 2048, kBlock), id_kv, true);
-                mma_ss(tm + kColS, desc_mn(q + x * 2048, kBlock), desc_mn(v + x * 2048, kBlock), id_kv, true);
+                    for (int x = 0; x < 8; ++x)
+                        mma_ts(tm + kColAV, tm + kColP + x * 8, v + x * 128, id_qs, x > 0);
+                    mma_commit(&sh->out);
+                }
+                ok = true;
             }
-            mma_commit(&sh->s_done);
-            if (!so) {
-                if (!wait_one(&sh->a_ready, it & 1, dead)) break;
-                tmem_fence_after();
-#pragma unroll
-                for (int x = 0; x < 8; ++x)
-                    mma_ts(tm + kColAV, tm + kColP + x * 8, desc_mn(v + x * 2048, kBlock), id_qs, x > 0);
-                mma_commit(&sh->out);
-            }
-            mma_commit(&sh->empty[it & 1]);
-            ++it;
-            have = more();
-            if (have && !so && !scores(it)) break;
         }
         // nothing of the block's is in flight when it gives tensor memory back
         mma_commit(&sh->last);
@@ -743,7 +803,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
                 const Unit u = unit_of(p, sh, idx);
                 if (u.on) atomicOr(a.err + u.s, kSeqTimeout);
             }
-    if (warp == 20) {
+    if (warp == 19) {
         tmem_fence_after();
         tmem_free(tm, kCols);
     }

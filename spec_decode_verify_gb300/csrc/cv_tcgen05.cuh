@@ -13,15 +13,15 @@ namespace cvk {
 __device__ __forceinline__ int swizzled(int row, int piece) { return row * 128 + ((piece ^ (row & 7)) << 4); }
 
 // Shared-memory operand descriptor: start address (bits 0-13), leading byte offset (16-29) and stride
-// byte offset (32-45) in units of 16 bytes, version 1 (46), 128-byte swizzle (61-63: 2).
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
-    return (uint64_t)((addr >> 4) & 0x3fff) | ((uint64_t)((lbo >> 4) & 0x3fff) << 16) |
-           ((uint64_t)((sbo >> 4) & 0x3fff) << 32) | (1ull << 46) | (2ull << 61);
+// byte offset (32-45) in units of 16 bytes, version 1 (46), 128-byte swizzle (61-63: 2).  Only the low word
+// depends on the address; a step inside a tile is an addition to it.
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);  // groups of 8 rows 1024 bytes apart
+// K-major (the leading offset is not used with a swizzle).
+__device__ __forceinline__ uint32_t desc_k(uint32_t addr) { return ((addr >> 4) & 0x3fff) | (1u << 16); }
+// MN-major: blocks of 64 M or N elements `block` bytes apart; the 8-row groups run along K.
+__device__ __forceinline__ uint32_t desc_mn(uint32_t addr, uint32_t block) {
+    return ((addr >> 4) & 0x3fff) | ((block >> 4) << 16);
 }
-// K-major: 8-row groups 1024 bytes apart (the leading offset is not used with a swizzle).
-__device__ __forceinline__ uint64_t desc_k(uint32_t addr) { return smem_desc(addr, 16, 1024); }
-// MN-major: blocks of 64 M or N elements `block` bytes apart, groups of 8 K rows 1024 bytes apart.
-__device__ __forceinline__ uint64_t desc_mn(uint32_t addr, uint32_t block) { return smem_desc(addr, block, 1024); }
 
 // Instruction descriptor: bf16 operands, fp32 accumulator, M = 128.
 __device__ __forceinline__ constexpr uint32_t mma_desc(int n, bool a_mn, bool b_mn) {
@@ -30,19 +30,19 @@ __device__ __forceinline__ constexpr uint32_t mma_desc(int n, bool a_mn, bool b_
 }
 
 // D (tensor memory) = A B (+ D when acc), K = 16 per instruction; issued by one thread.
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool acc) {
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+        "{\n .reg .pred p;\n .reg .b64 da, db;\n setp.ne.u32 p, %4, 0;\n mov.b64 da, {%1, %5};\n mov.b64 db, {%2, %5};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n}\n" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)acc), "r"(kDescHigh)
         : "memory");
 }
 // The same with A in tensor memory (two bf16 of a row per 32-bit column).
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool acc) {
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+        "{\n .reg .pred p;\n .reg .b64 db;\n setp.ne.u32 p, %4, 0;\n mov.b64 db, {%2, %5};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n}\n" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)acc), "r"(kDescHigh)
         : "memory");
 }
 // Arrive on `bar` once every tcgen05 operation this thread has issued is complete.
@@ -65,31 +65,35 @@ __device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols) {
 }
 
 #define CV_R4(r, i) "=r"((r)[i]), "=r"((r)[i + 1]), "=r"((r)[i + 2]), "=r"((r)[i + 3])
+#define CV_P4(r, i) "+r"((r)[i]), "+r"((r)[i + 1]), "+r"((r)[i + 2]), "+r"((r)[i + 3])
+#define CV_P16(r, i) CV_P4(r, i), CV_P4(r, i + 4), CV_P4(r, i + 8), CV_P4(r, i + 12)
 #define CV_R16(r, i) CV_R4(r, i), CV_R4(r, i + 4), CV_R4(r, i + 8), CV_R4(r, i + 12)
 #define CV_I4(r, i) "r"((r)[i]), "r"((r)[i + 1]), "r"((r)[i + 2]), "r"((r)[i + 3])
 #define CV_I16(r, i) CV_I4(r, i), CV_I4(r, i + 4), CV_I4(r, i + 8), CV_I4(r, i + 12)
 
-// 32 columns of the calling warp's 32 lanes, complete on return.
+// 32 columns of the calling warp's 32 lanes; the values are there after tmem_wait_ld on the same array.
 __device__ __forceinline__ void tmem_ld32(uint32_t *r, uint32_t addr) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
         "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n"
-        "tcgen05.wait::ld.sync.aligned;\n"
         : CV_R16(r, 0), CV_R16(r, 16)
         : "r"(addr)
         : "memory");
 }
-// 16 columns at each of two addresses.
-__device__ __forceinline__ void tmem_ld16x2(uint32_t *a, uint32_t *b, uint32_t addr_a, uint32_t addr_b) {
+// 16 columns at each of two addresses, the second's values from r[16] on.
+__device__ __forceinline__ void tmem_ld16x2(uint32_t *r, uint32_t addr_a, uint32_t addr_b) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
         "%15}, [%32];\n"
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, "
         "%29, %30, %31}, [%33];\n"
-        "tcgen05.wait::ld.sync.aligned;\n"
-        : CV_R16(a, 0), CV_R16(b, 0)
+        : CV_R16(r, 0), CV_R16(r, 16)
         : "r"(addr_a), "r"(addr_b)
         : "memory");
+}
+// All this thread's loads from tensor memory are complete; the array ties later uses of its values to it.
+__device__ __forceinline__ void tmem_wait_ld(uint32_t *r) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;\n" : CV_P16(r, 0), CV_P16(r, 16)::"memory");
 }
 __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t *r) {
     asm volatile(
@@ -106,6 +110,8 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t *r) {
         : "memory");
 }
 
+#undef CV_P4
+#undef CV_P16
 #undef CV_R4
 #undef CV_R16
 #undef CV_I4
