@@ -84,7 +84,7 @@ struct StreamLayout {
 
 // The chunked kernel for prompts (bf16, dk and dv multiples of 8 up to 128).
 constexpr int kChunk = 128;            // tokens a chunk
-constexpr int kChunkThreads = 640;     // 16 warps of the four large roles, 4 of one each
+constexpr int kChunkThreads = 768;     // 20 warps of the four large roles, 4 more
 constexpr int kChunkMaxSorted = 64;    // sequences that are taken longest first
 struct LinattnChunkParams {
     CUtensorMap q_map, k_map, v_map;  // [token][head][channel], boxes of 128 x 1 x 64, 128-byte swizzle

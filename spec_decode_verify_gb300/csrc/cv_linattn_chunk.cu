@@ -1,25 +1,25 @@
 // Linear attention with a decay for each head over prompts: chunked form on the tensor cores.
 //
 // Mathematics.  For a chunk of C = 128 tokens with G_i = sum_{u<=i} g_u and the state S before it,
-//   out_i = scale * exp(G_i) S^T q_i  +  sum_{j<=i} A_ij v_j,
-//   A_ij  = scale * exp(G_i - G_j) b_j (q_i . k_j)   (+ skip on the diagonal)
-//   S'    = exp(G_C) S + K'^T V,      K'_j = exp(G_C - G_j) b_j k_j
+//   out_i = scale * exp(G_i) ( S^T q_i + sum_{j<=i} A_ij v_j ),      A_ij = exp(-G_j) b_j (q_i . k_j)
+//   S'    = exp(G_C) S + K'^T V,                                     K'_j = exp(G_C - G_j) b_j k_j
 // so a chunk is five products of 128 x 128 x 128: Q K^T, Q S, A V, and K'^T V twice, because K' is
 // written as a high and a low bf16 part (together 16 significant bits): the state stays fp32 through
 // any number of chunks.  A and the copy of S that Q S reads are rounded to bf16, as the outputs are.
-// The exponents are sums over the tokens between i and j, never differences of long sums, so a large
-// decay early in a chunk costs later tokens no precision; log decays below -200 count as -200
-// (exp(-200) is 0 in fp32).
+// exp(-G_j) grows with the decay: a chunk that decays by more than 2^80 takes, block of 32 tokens by
+// block, A_ij = scale exp(G_i - G_j) b_j (q_i . k_j) instead, from sums over the tokens between i and j alone.
+// The exponents of K' are sums over the tokens after j, so a large decay early in a chunk costs later tokens
+// no precision; log decays below -200 count as -200 (exp(-200) is 0 in fp32).
 //
 // Layout.  A block (one per SM) takes units (sequence, head, piece of its length) and walks each unit's
 // chunks; every role below runs the same stream of chunks, so the next unit's loads and products
 // start while the last one's outputs are still being written.
 //   scores  4 warps, a row a thread: Q K^T from tensor memory, times the decays, back to it as A
-//   keys    4 warps, a token a thread: K' in place of K (once Q K^T is done) and its low part
 //   state   4 warps, a row of S a thread: S from tensor memory, bf16 copy to shared memory, S times the
 //           chunk's decay back
-//   output  4 warps, a row a thread: out = scale exp(G) (Q S) + A V, rounded, through the dead v tile out
-//   decays  1 warp: sums of the log decays, ahead of the others
+//   output  4 warps, a row a thread: out from Q S and A V, rounded, through the dead v tile to memory
+//   keys    8 warps, half a token a thread: K' in place of K (once Q K^T is done) and its low part
+//   decays  1 warp: sums of the log decays and the weights made of them, ahead of the others
 //   load    1 thread: q, k, v tiles by TMA in the 128-byte swizzle, channels past the end zero
 //   issue   1 thread: all products, in the order Q K^T, Q S, K'^T V, A V
 // Shared memory: k and v in two stages, q, the low part of K' and the copy of S once (32 KB each at 128
@@ -36,22 +36,24 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kMinLog2 = -200.0f * kLog2e;
+constexpr float kStrong = -80.0f;  // log2 of a chunk's decay from which on A is made block by block
 constexpr unsigned kPolls = 1u << 16;
 constexpr int kTileQK = kChunk * 256;  // bytes of a q or k tile: two blocks of 64 channels
 
 // Barriers, in order (8 bytes each), then the small arrays.
 struct ChunkShared {
-    uint64_t kv_full[2], g_full[2], k_empty[2], v_empty[2];
-    uint64_t q_full, scores, a_ready, keys, q_used, s_init, s_ready, s_done, out, out_free, last;
+    uint64_t kv_full[2], k_empty[2], v_empty[2];
+    uint64_t g_full, g_empty, q_full, scores, a_ready, keys, q_used, s_init, s_ready, s_done, out, out_free, last;
     uint32_t tmem;
     int dead;
     uint8_t order[kChunkMaxSorted];
-    // Of each stage, with the chunk as four blocks of 32 tokens: the sum of log2 decays in the token's
-    // block up to it, the token's weight at the end of its block (gain * 2^(sum after it)), and the
+    // Of the chunk at hand: each token's sum of log2 decays up to it (over the chunk, or over its block of 32
+    // where the chunk decays by more than 2^80), its weight as a column of A, its weight in K', and the
     // blocks' sums.  Tokens past the end: no decay, no weight.
-    alignas(16) float G[2][kChunk];
-    alignas(16) float cw[2][kChunk];
-    alignas(16) float tot[2][4];
+    alignas(16) float G[kChunk];
+    alignas(16) float col[kChunk];
+    alignas(16) float key[kChunk];
+    alignas(16) float tot[4];
 };
 
 template <int DV>
@@ -168,7 +170,7 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap *map, i
 __device__ __noinline__ void row_long_way(const LinattnParams &a, const Unit &u, int t0, int i, int c0, float *o) {
     const uint16_t *q = reinterpret_cast<const uint16_t *>(a.tok.q) + (u.row0 + t0 + i) * a.tok.q_tok + u.hq * a.tok.q_head;
     float dec = 1.0f;
-    for (int x = 0; x < 16; ++x) o[x] = 0.0f;
+    for (int x = 0; x < 8; ++x) o[x] = 0.0f;
     for (int j = i; j >= 0; --j) {
         const long long row = u.row0 + t0 + j;
         const uint16_t *k = reinterpret_cast<const uint16_t *>(a.tok.k) + row * a.tok.k_tok + u.hq * a.tok.k_head;
@@ -177,23 +179,76 @@ __device__ __noinline__ void row_long_way(const LinattnParams &a, const Unit &u,
         for (int x = 0; x < a.dk; ++x) dot = fmaf(widen<uint16_t>(q[x]), widen<uint16_t>(k[x]), dot);
         float w = a.scale * dec * dot * (a.tok.b ? a.tok.b[row * a.tok.b_tok + u.h] : 1.0f);
         if (j == i && a.skip) w += a.skip[u.h];
-        for (int x = 0; x < 16; ++x)
+        for (int x = 0; x < 8; ++x)
             if (c0 + x < a.dv) o[x] = fmaf(w, widen<uint16_t>(v[c0 + x]), o[x]);
         dec *= exp2_fast(clamp_log2(a.tok.g[row * a.tok.g_tok + u.h]));
     }
 }
 
-// 32 scores of a row times rf * cw_j, rounded to bf16 pairs.
-__device__ __forceinline__ void weigh(const uint32_t *r, float rf, const float *cw, uint32_t *o) {
+// Either bf16 half is a NaN or an infinity.
+__device__ __forceinline__ bool not_finite(uint32_t w) {
+    return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
+}
+// 16 scores of a row times rf * col_j, rounded to bf16 pairs.
+template <bool ROW>
+__device__ __forceinline__ void weigh(const uint32_t *r, float rf, const float *col, uint32_t *o) {
     const f2 rf2 = f2_pack(rf, rf);
 #pragma unroll
-    for (int j = 0; j < 32; j += 4) {
-        const float4 c = *reinterpret_cast<const float4 *>(cw + j);
+    for (int j = 0; j < 16; j += 4) {
+        const ulonglong2 c = *reinterpret_cast<const ulonglong2 *>(col + j);
         float f0, f1;
-        f2_unpack(f2_mul(f2_pack(__uint_as_float(r[j]), __uint_as_float(r[j + 1])), f2_mul(rf2, f2_pack(c.x, c.y))), f0, f1);
+        f2_unpack(f2_mul(f2_pack(__uint_as_float(r[j]), __uint_as_float(r[j + 1])), ROW ? f2_mul(rf2, c.x) : c.x), f0, f1);
         o[j / 2] = pack_bf16(f0, f1);
-        f2_unpack(f2_mul(f2_pack(__uint_as_float(r[j + 2]), __uint_as_float(r[j + 3])), f2_mul(rf2, f2_pack(c.z, c.w))), f0, f1);
+        f2_unpack(f2_mul(f2_pack(__uint_as_float(r[j + 2]), __uint_as_float(r[j + 3])), ROW ? f2_mul(rf2, c.y) : c.y), f0, f1);
         o[j / 2 + 1] = pack_bf16(f0, f1);
+    }
+}
+// The same without a row factor, plus `own` in column `at` (none when it is outside).
+__device__ __forceinline__ void weigh_own(const uint32_t *r, const float *col, float own, int at, uint32_t *o) {
+    float v[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) v[j] = fmaf(__uint_as_float(r[j]), col[j], j == at ? own : 0.0f);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) o[j] = pack_bf16(v[2 * j], v[2 * j + 1]);
+}
+// Lane i keeps columns up to i - j0 of 16 packed ones (a diagonal block's part right of the diagonal goes).
+__device__ __forceinline__ void keep_lower(uint32_t *o, int left) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) o[j] &= left > 2 * j ? 0xffffffffu : left == 2 * j ? 0xffffu : 0u;
+}
+// Row i of A for a chunk that decays by more than 2^80: exponents from the sums between i and j.
+template <int DV>
+__device__ __noinline__ void scores_strong(const LinattnParams &a, const Unit &u, const ChunkShared *sh, int c, uint32_t tp,
+                                           int w4, int lane, float skip) {
+    const float G = sh->G[32 * w4 + lane], t1 = sh->tot[1], t2 = sh->tot[2], scale = a.scale;
+    const bool in = c * kChunk + 32 * w4 + lane < u.n;
+    const long long row = u.row0 + c * kChunk + 32 * w4 + lane;
+    const float bi = in ? (a.tok.b ? __ldg(a.tok.b + row * a.tok.b_tok + u.h) : 1.0f) : 0.0f;
+    for (int x = 0; x < 8; ++x) {  // 16 columns at a time, ascending: A goes where earlier scores were
+        const int J = x >> 1, j0 = 16 * (x & 1);
+        uint32_t r[16], o[8];
+        if (J > w4) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) o[j] = 0u;
+        } else {
+            tmem_ld16(r, tp + 16 * x);
+            tmem_wait_ld(r);
+            if (J < w4) {
+                const float between = (J < 1 && w4 > 1 ? t1 : 0.0f) + (J < 2 && w4 > 2 ? t2 : 0.0f);
+                weigh<true>(r, exp2_fast(G + between) * scale, sh->col + 16 * x, o);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    const float Gj = __shfl_sync(0xffffffffu, G, j0 + j), bj = __shfl_sync(0xffffffffu, bi, j0 + j);
+                    const float v = __uint_as_float(r[j]) * scale * (exp2_fast(G - Gj) * bj);
+                    r[j] = __float_as_uint(j0 + j == lane ? v + skip : v);
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) o[j] = pack_bf16(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
+                keep_lower(o, lane - j0);
+            }
+        }
+        tmem_st8(tp + 8 * x, o);
     }
 }
 
@@ -208,22 +263,25 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
     const LinattnParams &a = p.a;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const bool so = p.state_only;
+    // (the skip weight enters A divided by scale, which therefore has to be a number of ordinary size)
+    const float strong_at = a.skip && !(fabsf(a.scale) > 1e-4f) ? INFINITY : kStrong;
 
     // the layout below needs its bytes and the swizzle's alignment
     if (dynamic_smem_bytes() < chunk_smem_bytes<DV>() || (smem_u32(smem) & 1023u) != 0) return;
-    if (warp == 19) tmem_alloc(&sh->tmem, kCols);
+    if (warp == 23) tmem_alloc(&sh->tmem, kCols);
     if (tid == 0) {
         sh->dead = 0;
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh->kv_full[i], 1);
-            mbar_init(&sh->g_full[i], 1);
             mbar_init(&sh->k_empty[i], 1);
             mbar_init(&sh->v_empty[i], 4);
         }
+        mbar_init(&sh->g_full, 1);
+        mbar_init(&sh->g_empty, so ? 12 : 20);
         mbar_init(&sh->q_full, 1);
         mbar_init(&sh->scores, 1);
         mbar_init(&sh->a_ready, 4);
-        mbar_init(&sh->keys, 4);
+        mbar_init(&sh->keys, 8);
         mbar_init(&sh->q_used, 1);
         mbar_init(&sh->s_init, 4);
         mbar_init(&sh->s_ready, 4);
@@ -254,7 +312,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
     const uint32_t tl = tm + ((uint32_t)(32 * w4) << 16);
 
     int it = 0;  // chunks of the stream so far
-    if (warp == 16) {
+    if (warp == 20) {
         // ---------------------------------------------------------------------------- decays
         bool ok = true;
         for (int n = 0, idx; ok && (idx = unit_index(p, n)) != -1; ++n) {
@@ -266,31 +324,42 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
                 if (st) atomicOr(a.err + u.s, st);
             }
             for (int c = 0; c < u.chunks; ++c, ++it) {
-                const int stage = it & 1, rows = u.n - c * kChunk;
+                const int rows = u.n - c * kChunk;
                 const long long row = u.row0 + c * kChunk;
-                float g[4], b[4];
+                float g[4], b[4], G[4], after[4], tot[4];
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
+                for (int x = 0; x < 4; ++x) {  // a block of 32 tokens each
                     const int t = 32 * x + lane;
                     g[x] = t < rows ? __ldg(a.tok.g + (row + t) * a.tok.g_tok + u.h) : 0.0f;
                     b[x] = t < rows ? (a.tok.b ? __ldg(a.tok.b + (row + t) * a.tok.b_tok + u.h) : 1.0f) : 0.0f;
                 }
-                // the last chunk in this place is through with them once its outputs are out
-                if (it >= 2 && !wait_warp(so ? &sh->k_empty[stage] : &sh->v_empty[stage], ((it >> 1) & 1) ^ 1, dead)) {
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const float l2 = clamp_log2(g[x]);
+                    G[x] = prefix_sum(l2, lane);
+                    after[x] = suffix_after(l2, lane);
+                    tot[x] = __shfl_sync(0xffffffffu, G[x], 31);
+                }
+                const bool strong = !((tot[0] + tot[1]) + (tot[2] + tot[3]) > strong_at);
+                if (it > 0 && !wait_warp(&sh->g_empty, (it - 1) & 1, dead)) {
                     ok = false;
                     break;
                 }
+                float before = 0.0f, later = tot[1] + tot[2] + tot[3];
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {  // a block of 32 tokens each
-                    const float l2 = clamp_log2(g[x]), G = prefix_sum(l2, lane);
-                    sh->G[stage][32 * x + lane] = G;
-                    sh->cw[stage][32 * x + lane] = exp2_fast(suffix_after(l2, lane)) * b[x];
-                    if (lane == 31) sh->tot[stage][x] = G;
+                for (int x = 0; x < 4; ++x) {
+                    const float all = before + G[x];
+                    sh->G[32 * x + lane] = strong ? G[x] : all;
+                    sh->col[32 * x + lane] = exp2_fast(strong ? after[x] : -all) * b[x];
+                    sh->key[32 * x + lane] = exp2_fast(after[x] + later) * b[x];
+                    if (lane == 0) sh->tot[x] = tot[x];
+                    before += tot[x];
+                    later = x < 2 ? (x < 1 ? tot[2] + tot[3] : tot[3]) : 0.0f;
                 }
-                arrive_warp(&sh->g_full[stage]);
+                arrive_warp(&sh->g_full);
             }
         }
-    } else if (warp == 17 && lane == 0) {
+    } else if (warp == 21 && lane == 0) {
         // ------------------------------------------------------------------------------ load
         bool ok = true;
         for (int n = 0, idx; ok && (idx = unit_index(p, n)) != -1; ++n) {
@@ -332,152 +401,65 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
         }
     } else if (role == 0 && !so) {
         // ---------------------------------------------------------------------------- scores
-        const float scale = a.scale;
         bool ok = true;
+        const uint32_t tp = tl + kColP;
         for (int n = 0, idx; ok && (idx = unit_index(p, n)) != -1; ++n) {
             if (idx < 0) continue;
             const Unit u = unit_of(p, sh, idx);
             const float skip = a.skip ? __ldg(a.skip + u.h) : 0.0f;
             for (int c = 0; c < u.chunks; ++c, ++it) {
-                const int stage = it & 1;
-                if (!wait_warp(&sh->g_full[stage], (it >> 1) & 1, dead) || !wait_warp(&sh->scores, it & 1, dead)) {
+                if (!wait_warp(&sh->g_full, it & 1, dead) || !wait_warp(&sh->scores, it & 1, dead)) {
                     ok = false;
                     break;
                 }
                 tmem_fence_after();
-                const float G = sh->G[stage][32 * w4 + lane];
-                const float *const cw = sh->cw[stage];
-                const float t1 = sh->tot[stage][1], t2 = sh->tot[stage][2];
-                uint32_t r[32], o[16], next[32];
-                tmem_ld32(r, tl + kColP);
-                // Row i against block J left of its own: 2^(G_i + blocks between) * cw_j.  A overlays the
-                // scores: block J goes to columns 16 J .., whose scores were read in an earlier round.
+                const float4 bt = *reinterpret_cast<const float4 *>(sh->tot);
+                if ((bt.x + bt.y) + (bt.z + bt.w) > strong_at) {
+                    // A overlays the scores: 16 columns go where earlier ones were read
+                    uint32_t r[16], s2[16], o[8];
+                    tmem_ld16(r, tp);
 #pragma unroll 1
-                for (int J = 0; J < w4; ++J) {
-                    const float between = (J < 1 && w4 > 1 ? t1 : 0.0f) + (J < 2 && w4 > 2 ? t2 : 0.0f);
-                    const float rf = exp2_fast(G + between) * scale;
+                    for (int x = 0; x < 2 * w4; x += 2) {
+                        tmem_wait_ld(r);
+                        tmem_ld16(s2, tp + 16 * x + 16);
+                        weigh<false>(r, 1.0f, sh->col + 16 * x, o);
+                        tmem_st8(tp + 8 * x, o);
+                        tmem_wait_ld(s2);
+                        tmem_ld16(r, tp + 16 * x + 32);
+                        weigh<false>(s2, 1.0f, sh->col + 16 * x + 16, o);
+                        tmem_st8(tp + 8 * x + 8, o);
+                    }
+                    // the block on the diagonal; with skip, A_ii holds skip / (scale exp(G_i)) too
+                    const float own = a.skip ? skip / a.scale * exp2_fast(-sh->G[32 * w4 + lane]) : 0.0f;
                     tmem_wait_ld(r);
-                    tmem_ld32(next, tl + kColP + 32 * J + 32);
-                    weigh(r, rf, cw + 32 * J, o);
-                    tmem_st16(tl + kColP + 16 * J, o);
-                    tmem_wait_ld(next);
+                    tmem_ld16(s2, tp + 32 * w4 + 16);
+                    if (a.skip)
+                        weigh_own(r, sh->col + 32 * w4, own, lane, o);
+                    else
+                        weigh<false>(r, 1.0f, sh->col + 32 * w4, o);
+                    keep_lower(o, lane);
+                    tmem_st8(tp + 16 * w4, o);
+                    tmem_wait_ld(s2);
+                    if (a.skip)
+                        weigh_own(s2, sh->col + 32 * w4 + 16, own, lane - 16, o);
+                    else
+                        weigh<false>(s2, 1.0f, sh->col + 32 * w4 + 16, o);
+                    keep_lower(o, lane - 16);
+                    tmem_st8(tp + 16 * w4 + 8, o);
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) r[j] = next[j];
-                }
-                // The block on the diagonal: 2^(G_i - G_j) b_j = 2^(G_i - G_end) cw_j while the block's whole
-                // decay is far from fp32's range, else one exponential per pair.
-                tmem_wait_ld(r);
-                const float end = sh->tot[stage][w4];
-                if (end > -100.0f) {
-                    const float rf = exp2_fast(G - end) * scale;
-                    if (a.skip) {  // rf * cw_i = scale * b_i at j = i
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) {
-                            const float v = __uint_as_float(r[j]) * (rf * cw[32 * w4 + j]);
-                            r[j] = __float_as_uint(j == lane ? v + skip : v);
-                        }
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) o[j] = pack_bf16(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
-                    } else {
-                        weigh(r, rf, cw + 32 * w4, o);
-                    }
-                } else {
-                    const long long row = u.row0 + c * kChunk + 32 * w4 + lane;
-                    const bool in = c * kChunk + 32 * w4 + lane < u.n;
-                    const float bi = in ? (a.tok.b ? __ldg(a.tok.b + row * a.tok.b_tok + u.h) : 1.0f) : 0.0f;
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        const float Gj = __shfl_sync(0xffffffffu, G, j), bj = __shfl_sync(0xffffffffu, bi, j);
-                        const float v = __uint_as_float(r[j]) * scale * (exp2_fast(G - Gj) * bj);
-                        r[j] = __float_as_uint(j == lane ? v + skip : v);
-                    }
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) o[j] = pack_bf16(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
-                }
-#pragma unroll
-                for (int j = 0; j < 16; ++j) o[j] &= lane > 2 * j ? 0xffffffffu : lane == 2 * j ? 0xffffu : 0u;
-                tmem_st16(tl + kColP + 16 * w4, o);
-#pragma unroll
-                for (int j = 0; j < 16; ++j) o[j] = 0u;
+                    for (int j = 0; j < 8; ++j) o[j] = 0u;
 #pragma unroll 1
-                for (int J = w4 + 1; J < 4; ++J) tmem_st16(tl + kColP + 16 * J, o);
+                    for (int x = 2 * w4 + 2; x < 8; ++x) tmem_st8(tp + 8 * x, o);
+                } else {
+                    scores_strong<DV>(a, u, sh, c, tp, w4, lane, skip);
+                }
                 tmem_wait_st();
                 tmem_fence_before();
                 arrive_warp(&sh->a_ready);
+                arrive_warp(&sh->g_empty);
             }
         }
     } else if (role == 1) {
-        // ------------------------------------------------------------------------------ keys
-        const int t = 32 * w4 + lane;
-        bool ok = true;
-        for (int n = 0, idx; ok && (idx = unit_index(p, n)) != -1; ++n) {
-            if (idx < 0) continue;
-            const Unit u = unit_of(p, sh, idx);
-            for (int c = 0; c < u.chunks; ++c, ++it) {
-                const int stage = it & 1;
-                if (!wait_warp(&sh->g_full[stage], (it >> 1) & 1, dead) || !wait_warp(&sh->kv_full[stage], (it >> 1) & 1, dead)) {
-                    ok = false;
-                    break;
-                }
-                const float *const bt = sh->tot[stage];
-                const float later = (w4 < 1 ? bt[1] : 0.0f) + (w4 < 2 ? bt[2] : 0.0f) + (w4 < 3 ? bt[3] : 0.0f);
-                const float w = exp2_fast(later) * sh->cw[stage][t];
-                const f2 w2 = f2_pack(w, w), neg = f2_pack(-1.0f, -1.0f);
-                // the tile holds whatever follows the sequence there
-                const uint32_t keep = t < u.n - c * kChunk ? 0xffffffffu : 0u;
-                // the low part's place is free once the last chunk's products are done (and this role never runs
-                // two phases ahead of the issue thread)
-                if (it > 0 && !wait_warp(&sh->s_done, (it - 1) & 1, dead)) {
-                    ok = false;
-                    break;
-                }
-                unsigned char *const kt = k_tile + stage * kTileQK;
-                uint32_t hi[64];
-#pragma unroll
-                for (int x0 = 0; x0 < 16; x0 += 4) {  // four pieces at a time: their latencies overlap
-                    uint4 in[4], lo[4];
-#pragma unroll
-                    for (int x = 0; x < 4; ++x)
-                        in[x] = *reinterpret_cast<const uint4 *>(kt + (x0 >> 3) * kBlock + swizzled(t, (x0 + x) & 7));
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        const uint32_t w[4] = {in[x].x & keep, in[x].y & keep, in[x].z & keep, in[x].w & keep};
-                        uint32_t l[4];
-#pragma unroll
-                        for (int y = 0; y < 4; ++y) {
-                            const f2 f = f2_mul(f2_pack(__uint_as_float(w[y] << 16), __uint_as_float(w[y] & 0xffff0000u)), w2);
-                            float f0, f1;
-                            f2_unpack(f, f0, f1);
-                            const uint32_t h = pack_bf16(f0, f1);
-                            hi[4 * (x0 + x) + y] = h;
-                            f2_unpack(f2_fma(f2_pack(__uint_as_float(h << 16), __uint_as_float(h & 0xffff0000u)), neg, f), f0, f1);
-                            l[y] = pack_bf16(f0, f1);
-                        }
-                        lo[x] = make_uint4(l[0], l[1], l[2], l[3]);
-                    }
-#pragma unroll
-                    for (int x = 0; x < 4; ++x)
-                        *reinterpret_cast<uint4 *>(lo_tile + (x0 >> 3) * kBlock + swizzled(t, (x0 + x) & 7)) = lo[x];
-                }
-                if (!keep) {  // v past the end: zeros too
-#pragma unroll 1
-                    for (int x = 0; x < DV / 8; ++x)
-                        *reinterpret_cast<uint4 *>(v_tile + stage * kTileV + (x >> 3) * kBlock + swizzled(t, x & 7)) =
-                            make_uint4(0u, 0u, 0u, 0u);
-                }
-                if (!so && !wait_warp(&sh->scores, it & 1, dead)) {  // k is used up
-                    ok = false;
-                    break;
-                }
-#pragma unroll
-                for (int x = 0; x < 16; ++x)
-                    *reinterpret_cast<uint4 *>(kt + (x >> 3) * kBlock + swizzled(t, x & 7)) =
-                        make_uint4(hi[4 * x], hi[4 * x + 1], hi[4 * x + 2], hi[4 * x + 3]);
-                fence_smem_to_async();
-                arrive_warp(&sh->keys);
-            }
-        }
-    } else if (role == 2) {
         // ----------------------------------------------------------------------------- state
         const int r = 32 * w4 + lane;  // the row of S
         const uint32_t ts = tl + kColS;
@@ -503,20 +485,22 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
             const bool zero = so ? true : u.seg == 0 && !u.init;
             if (zero || u.seg > 0) {
                 const float4 *src = reinterpret_cast<const float4 *>(p.ws_state) + (wsi + u.seg - 1) * (32 * DV);
+#pragma unroll 1
+                for (int j = 0; j < DV; j += 16) {
+                    uint32_t v[16];
 #pragma unroll
-                for (int j = 0; j < DV; j += 32) {
-                    uint32_t v[32];
-#pragma unroll
-                    for (int x = 0; x < 8; ++x) {
+                    for (int x = 0; x < 4; ++x) {
                         const float4 f = zero ? make_float4(0.f, 0.f, 0.f, 0.f) : src[(j / 4 + x) * 128 + r];
                         v[4 * x] = __float_as_uint(f.x), v[4 * x + 1] = __float_as_uint(f.y);
                         v[4 * x + 2] = __float_as_uint(f.z), v[4 * x + 3] = __float_as_uint(f.w);
                     }
-                    tmem_st32(ts + j, v);
+                    tmem_st16(ts + j, v);
                 }
             } else {
+#pragma unroll 1
                 for (int h = 0; h < PASSES; ++h) {
                     __syncwarp();
+#pragma unroll 4
                     for (int e = lane; e < 32 * PW; e += 32) {
                         const int row = e / PW, q = e % PW, col = (h * PW + q) * 4;
                         float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -525,16 +509,16 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
                         mine[row * PW + (q ^ (row & 7))] = f;
                     }
                     __syncwarp();
+#pragma unroll 1
+                    for (int j = 0; j < PW; j += 4) {
+                        uint32_t v[16];
 #pragma unroll
-                    for (int j = 0; j < PW; j += 8) {
-                        uint32_t v[32];
-#pragma unroll
-                        for (int x = 0; x < 8; ++x) {
+                        for (int x = 0; x < 4; ++x) {
                             const float4 f = mine[lane * PW + ((j + x) ^ (lane & 7))];
                             v[4 * x] = __float_as_uint(f.x), v[4 * x + 1] = __float_as_uint(f.y);
                             v[4 * x + 2] = __float_as_uint(f.z), v[4 * x + 3] = __float_as_uint(f.w);
                         }
-                        tmem_st32(ts + (h * PW + j) * 4, v);
+                        tmem_st16(ts + (h * PW + j) * 4, v);
                     }
                 }
                 __syncwarp();
@@ -545,48 +529,49 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
             if (!wait_warp(&sh->s_init, units++ & 1, dead)) break;
             float total = 1.0f;
             for (int c = 0; c < u.chunks; ++c, ++it) {
-                const int stage = it & 1;
                 // the last chunk's products into S are done, and those that read the copy
-                if (!wait_warp(&sh->g_full[stage], (it >> 1) & 1, dead) ||
-                    (c > 0 && !wait_warp(&sh->s_done, (it - 1) & 1, dead))) {
+                if (!wait_warp(&sh->g_full, it & 1, dead) || (c > 0 && !wait_warp(&sh->s_done, (it - 1) & 1, dead))) {
                     ok = false;
                     break;
                 }
                 tmem_fence_after();
-                const float4 bt = *reinterpret_cast<const float4 *>(sh->tot[stage]);
+                uint32_t v[16], v2[16];
+                tmem_ld16(v, ts);
+                const float4 bt = *reinterpret_cast<const float4 *>(sh->tot);
+                arrive_warp(&sh->g_empty);
                 const float tot = exp2_fast((bt.x + bt.y) + (bt.z + bt.w));
                 const f2 tot2 = f2_pack(tot, tot);
                 total *= tot;
-                uint32_t v[32], next[32];
-                tmem_ld32(v, ts);
+                auto piece = [&](uint32_t *x, int j) {  // 16 columns: the copy, and times the decay back
+                    if (!so) {
+                        unsigned char *const at = s_copy + (j >> 6) * kBlock;
+                        *reinterpret_cast<uint4 *>(at + swizzled(r, (j >> 3) & 7)) =
+                            make_uint4(pack_bf16(__uint_as_float(x[0]), __uint_as_float(x[1])),
+                                       pack_bf16(__uint_as_float(x[2]), __uint_as_float(x[3])),
+                                       pack_bf16(__uint_as_float(x[4]), __uint_as_float(x[5])),
+                                       pack_bf16(__uint_as_float(x[6]), __uint_as_float(x[7])));
+                        *reinterpret_cast<uint4 *>(at + swizzled(r, ((j >> 3) & 7) + 1)) =
+                            make_uint4(pack_bf16(__uint_as_float(x[8]), __uint_as_float(x[9])),
+                                       pack_bf16(__uint_as_float(x[10]), __uint_as_float(x[11])),
+                                       pack_bf16(__uint_as_float(x[12]), __uint_as_float(x[13])),
+                                       pack_bf16(__uint_as_float(x[14]), __uint_as_float(x[15])));
+                    }
+#pragma unroll
+                    for (int e = 0; e < 16; e += 2) {
+                        float f0, f1;
+                        f2_unpack(f2_mul(f2_pack(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), tot2), f0, f1);
+                        x[e] = __float_as_uint(f0), x[e + 1] = __float_as_uint(f1);
+                    }
+                    tmem_st16(ts + j, x);
+                };
 #pragma unroll 1
                 for (int j = 0; j < DV; j += 32) {
                     tmem_wait_ld(v);
-                    if (j + 32 < DV) tmem_ld32(next, ts + j + 32);
-                    if (!so) {
-#pragma unroll
-                        for (int x = 0; x < 32; x += 8) {
-                            uint4 o;
-                            o.x = pack_bf16(__uint_as_float(v[x]), __uint_as_float(v[x + 1]));
-                            o.y = pack_bf16(__uint_as_float(v[x + 2]), __uint_as_float(v[x + 3]));
-                            o.z = pack_bf16(__uint_as_float(v[x + 4]), __uint_as_float(v[x + 5]));
-                            o.w = pack_bf16(__uint_as_float(v[x + 6]), __uint_as_float(v[x + 7]));
-                            const int pc = (j + x) / 8;
-                            *reinterpret_cast<uint4 *>(s_copy + (pc >> 3) * kBlock + swizzled(r, pc & 7)) = o;
-                        }
-                    }
-#pragma unroll
-                    for (int x = 0; x < 32; x += 2) {
-                        float f0, f1;
-                        f2_unpack(f2_mul(f2_pack(__uint_as_float(v[x]), __uint_as_float(v[x + 1])), tot2), f0, f1);
-                        v[x] = __float_as_uint(f0), v[x + 1] = __float_as_uint(f1);
-                    }
-                    tmem_st32(ts + j, v);
-                    if (j + 32 < DV) {
-                        tmem_wait_ld(next);
-#pragma unroll
-                        for (int x = 0; x < 32; ++x) v[x] = next[x];
-                    }
+                    tmem_ld16(v2, ts + j + 16);
+                    piece(v, j);
+                    tmem_wait_ld(v2);
+                    if (j + 32 < DV) tmem_ld16(v, ts + j + 32);
+                    piece(v2, j + 16);
                 }
                 tmem_wait_st();
                 tmem_fence_before();
@@ -601,32 +586,34 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
             // the state after it
             if (so) {
                 float4 *dst = reinterpret_cast<float4 *>(p.ws_state) + (wsi + u.seg) * (32 * DV);
-#pragma unroll
-                for (int j = 0; j < DV; j += 32) {
-                    uint32_t v[32];
-                    tmem_ld32(v, ts + j);
+#pragma unroll 1
+                for (int j = 0; j < DV; j += 16) {
+                    uint32_t v[16];
+                    tmem_ld16(v, ts + j);
                     tmem_wait_ld(v);
 #pragma unroll
-                    for (int x = 0; x < 8; ++x)
+                    for (int x = 0; x < 4; ++x)
                         dst[(j / 4 + x) * 128 + r] = make_float4(__uint_as_float(v[4 * x]), __uint_as_float(v[4 * x + 1]),
                                                                  __uint_as_float(v[4 * x + 2]), __uint_as_float(v[4 * x + 3]));
                 }
-                if (tid == 2 * 128) p.ws_decay[wsi + u.seg] = total;
+                if (r == 0) p.ws_decay[wsi + u.seg] = total;
             } else if (u.last) {
+#pragma unroll 1
                 for (int h = 0; h < PASSES; ++h) {
                     __syncwarp();
-#pragma unroll
-                    for (int j = 0; j < PW; j += 8) {
-                        uint32_t v[32];
-                        tmem_ld32(v, ts + (h * PW + j) * 4);
+#pragma unroll 1
+                    for (int j = 0; j < PW; j += 4) {
+                        uint32_t v[16];
+                        tmem_ld16(v, ts + (h * PW + j) * 4);
                         tmem_wait_ld(v);
 #pragma unroll
-                        for (int x = 0; x < 8; ++x)
+                        for (int x = 0; x < 4; ++x)
                             mine[lane * PW + ((j + x) ^ (lane & 7))] =
                                 make_float4(__uint_as_float(v[4 * x]), __uint_as_float(v[4 * x + 1]),
                                             __uint_as_float(v[4 * x + 2]), __uint_as_float(v[4 * x + 3]));
                     }
                     __syncwarp();
+#pragma unroll 4
                     for (int e = lane; e < 32 * PW; e += 32) {
                         const int row = e / PW, q = e % PW, col = (h * PW + q) * 4;
                         if (32 * w4 + row < a.dk && col < a.dv)
@@ -637,7 +624,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
                 __syncwarp();
             }
         }
-    } else if (role == 3 && !so) {
+    } else if (role == 2 && !so) {
         // ---------------------------------------------------------------------------- output
         const int i = 32 * w4 + lane;  // the row of the chunk
         bool ok = true;
@@ -646,77 +633,80 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
             const Unit u = unit_of(p, sh, idx);
             for (int c = 0; c < u.chunks; ++c, ++it) {
                 const int stage = it & 1;
-                if (!wait_warp(&sh->g_full[stage], (it >> 1) & 1, dead)) {
+                if (!wait_warp(&sh->g_full, it & 1, dead)) {
                     ok = false;
                     break;
                 }
-                const float *const bt = sh->tot[stage];
-                const float G = sh->G[stage][i] + ((w4 > 0 ? bt[0] : 0.0f) + (w4 > 1 ? bt[1] : 0.0f) + (w4 > 2 ? bt[2] : 0.0f));
+                // out = pre * (Q S) + post * (A V)
+                const float4 bt = *reinterpret_cast<const float4 *>(sh->tot);
+                float G = sh->G[i], post = 1.0f;
+                const bool strong = !((bt.x + bt.y) + (bt.z + bt.w) > strong_at);
+                if (strong) G += (w4 > 0 ? bt.x : 0.0f) + (w4 > 1 ? bt.y : 0.0f) + (w4 > 2 ? bt.z : 0.0f);
+                arrive_warp(&sh->g_empty);
                 const float pre = exp2_fast(G) * a.scale;
-                const f2 pre2 = f2_pack(pre, pre);
+                if (!strong) post = pre;
+                const f2 pre2 = f2_pack(pre, pre), post2 = f2_pack(post, post);
                 if (!wait_warp(&sh->out, it & 1, dead)) {
                     ok = false;
                     break;
                 }
                 tmem_fence_after();
                 const int t0 = c * kChunk;
-                const bool mine = t0 + i < u.n;
                 unsigned char *const vt = v_tile + stage * kTileV;  // v is used up: the rows go through its tile
-                f2 bad2 = f2_pack(0.0f, 0.0f);  // stays 0 while every output is finite
-                auto store = [&](int j, const uint32_t *o) {
-                    unsigned char *const at = vt + (j >> 6) * kBlock;
-                    *reinterpret_cast<uint4 *>(at + swizzled(i, (j >> 3) & 7)) = make_uint4(o[0], o[1], o[2], o[3]);
-                    *reinterpret_cast<uint4 *>(at + swizzled(i, ((j >> 3) & 7) + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
-                };
-                uint32_t xy[32], next[32];  // 16 columns of Q S, then of A V
-                tmem_ld16x2(xy, tl + kColQS, tl + kColAV);
-#pragma unroll 1
-                for (int j = 0; j < DV; j += 16) {
-                    uint32_t o[8];
-                    tmem_wait_ld(xy);
-                    if (j + 16 < DV) tmem_ld16x2(next, tl + kColQS + j + 16, tl + kColAV + j + 16);
+                uint32_t x1[8], y1[8], x2[8], y2[8];
+                auto piece = [&](const uint32_t *x, const uint32_t *y, int j) {  // 8 columns
+                    uint32_t o[4];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const f2 f = f2_fma(pre2, f2_pack(__uint_as_float(xy[2 * e]), __uint_as_float(xy[2 * e + 1])),
-                                            f2_pack(__uint_as_float(xy[16 + 2 * e]), __uint_as_float(xy[17 + 2 * e])));
+                    for (int e = 0; e < 4; ++e) {
                         float f0, f1;
-                        f2_unpack(f, f0, f1);
-                        bad2 = f2_fma(f, f2_pack(0.0f, 0.0f), bad2);
+                        f2_unpack(f2_fma(pre2, f2_pack(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])),
+                                         f2_mul(post2, f2_pack(__uint_as_float(y[2 * e]), __uint_as_float(y[2 * e + 1])))),
+                                  f0, f1);
                         o[e] = pack_bf16(f0, f1);
                     }
-                    store(j, o);
-                    if (j + 16 < DV) {
-                        tmem_wait_ld(next);
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) xy[e] = next[e];
-                    }
-                }
-                float bad0, bad1;
-                f2_unpack(bad2, bad0, bad1);
-                const bool bad = !(bad0 + bad1 == 0.0f);
-                if (__any_sync(0xffffffffu, bad && mine)) {
-                    // is it a value of this chunk?
-                    bool found = false;
-                    for (int t = lane; t < min(kChunk, u.n - t0); t += 32) {
-                        const uint16_t *v = reinterpret_cast<const uint16_t *>(a.tok.v) +
-                                            (u.row0 + t0 + t) * a.tok.v_tok + (long long)u.h * a.tok.v_head;
-                        for (int e = 0; e < a.dv; ++e) found |= (v[e] & 0x7f80) == 0x7f80;
-                    }
-                    if (__any_sync(0xffffffffu, found))
+                    *reinterpret_cast<uint4 *>(vt + (j >> 6) * kBlock + swizzled(i, (j >> 3) & 7)) = make_uint4(o[0], o[1], o[2], o[3]);
+                };
+                tmem_ld8x2(x1, y1, tl + kColQS, tl + kColAV);
 #pragma unroll 1
-                        for (int j = 0; j < DV; j += 16) {
-                            uint32_t o[8];
-                            float part[16];
-                            tmem_ld16x2(xy, tl + kColQS + j, tl + kColAV + j);
-                            tmem_wait_ld(xy);
-                            if (mine) row_long_way(a, u, t0, i, j, part);
-#pragma unroll
-                            for (int e = 0; e < 8; ++e)
-                                o[e] = pack_bf16(fmaf(pre, __uint_as_float(xy[2 * e]), part[2 * e]),
-                                                 fmaf(pre, __uint_as_float(xy[2 * e + 1]), part[2 * e + 1]));
-                            store(j, o);
-                            __syncwarp();
+                for (int j = 0; j < DV; j += 16) {
+                    tmem_wait_ld8x2(x1, y1);
+                    tmem_ld8x2(x2, y2, tl + kColQS + j + 8, tl + kColAV + j + 8);
+                    piece(x1, y1, j);
+                    tmem_wait_ld8x2(x2, y2);
+                    if (j + 16 < DV) tmem_ld8x2(x1, y1, tl + kColQS + j + 16, tl + kColAV + j + 16);
+                    piece(x2, y2, j + 8);
+                }
+                __syncwarp();
+                // A NaN or an infinity in v spoils its column in every row of the chunk, so the warp's first row
+                // shows it.
+                {
+                    const uint4 f = *reinterpret_cast<const uint4 *>(vt + ((lane * 8 >> 6) & (DV / 64 - 1)) * kBlock +
+                                                                     swizzled(32 * w4, lane & 7));
+                    const bool bad = lane < DV / 8 && (not_finite(f.x) || not_finite(f.y) || not_finite(f.z) || not_finite(f.w));
+                    if (__any_sync(0xffffffffu, bad) && t0 + 32 * w4 < u.n) {
+                        bool found = false;
+                        for (int t = lane; t < min(kChunk, u.n - t0); t += 32) {
+                            const uint16_t *v = reinterpret_cast<const uint16_t *>(a.tok.v) +
+                                                (u.row0 + t0 + t) * a.tok.v_tok + (long long)u.h * a.tok.v_head;
+                            for (int e = 0; e < a.dv; ++e) found |= (v[e] & 0x7f80) == 0x7f80;
                         }
+                        if (__any_sync(0xffffffffu, found))
+#pragma unroll 1
+                            for (int j = 0; j < DV; j += 8) {
+                                float part[8] = {};
+                                tmem_ld8x2(x1, y1, tl + kColQS + j, tl + kColAV + j);
+                                tmem_wait_ld8x2(x1, y1);
+                                if (t0 + i < u.n) row_long_way(a, u, t0, i, j, part);
+                                uint32_t o[4];
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    o[e] = pack_bf16(fmaf(pre, __uint_as_float(x1[2 * e]), part[2 * e]),
+                                                     fmaf(pre, __uint_as_float(x1[2 * e + 1]), part[2 * e + 1]));
+                                *reinterpret_cast<uint4 *>(vt + (j >> 6) * kBlock + swizzled(i, (j >> 3) & 7)) =
+                                    make_uint4(o[0], o[1], o[2], o[3]);
+                                __syncwarp();
+                            }
+                    }
                 }
                 tmem_fence_before();
                 arrive_warp(&sh->out_free);
@@ -735,7 +725,80 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
                 arrive_warp(&sh->v_empty[stage]);
             }
         }
-    } else if (warp == 18 && lane == 0) {
+    } else if (role == 3 || role == 4) {
+        // ------------------------------------------------------------------------------ keys
+        const int t = 32 * w4 + lane, half = role - 3;  // the token, and which 64 of its channels
+        bool ok = true;
+        for (int n = 0, idx; ok && (idx = unit_index(p, n)) != -1; ++n) {
+            if (idx < 0) continue;
+            const Unit u = unit_of(p, sh, idx);
+            for (int c = 0; c < u.chunks; ++c, ++it) {
+                const int stage = it & 1;
+                if (!wait_warp(&sh->g_full, it & 1, dead)) {
+                    ok = false;
+                    break;
+                }
+                const float w = sh->key[t];
+                arrive_warp(&sh->g_empty);
+                // the low part's place is free once the last chunk's products are done (and this role never runs
+                // two phases ahead of the issue thread)
+                if (!wait_warp(&sh->kv_full[stage], (it >> 1) & 1, dead) ||
+                    (it > 0 && !wait_warp(&sh->s_done, (it - 1) & 1, dead))) {
+                    ok = false;
+                    break;
+                }
+                const f2 w2 = f2_pack(w, w), neg = f2_pack(-1.0f, -1.0f);
+                unsigned char *const kt = k_tile + stage * kTileQK + half * kBlock, *const lt = lo_tile + half * kBlock;
+                uint32_t hi[32];
+                if (t < u.n - c * kChunk) {
+#pragma unroll
+                    for (int x0 = 0; x0 < 8; x0 += 4) {  // four pieces at a time: their latencies overlap
+                        uint4 in[4];
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) in[x] = *reinterpret_cast<const uint4 *>(kt + swizzled(t, x0 + x));
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            const uint32_t k[4] = {in[x].x, in[x].y, in[x].z, in[x].w};
+                            uint32_t l[4];
+#pragma unroll
+                            for (int y = 0; y < 4; ++y) {
+                                const f2 f = f2_mul(f2_pack(__uint_as_float(k[y] << 16), __uint_as_float(k[y] & 0xffff0000u)), w2);
+                                float f0, f1;
+                                f2_unpack(f, f0, f1);
+                                const uint32_t h = pack_bf16(f0, f1);
+                                hi[4 * (x0 + x) + y] = h;
+                                f2_unpack(f2_fma(f2_pack(__uint_as_float(h << 16), __uint_as_float(h & 0xffff0000u)), neg, f),
+                                          f0, f1);
+                                l[y] = pack_bf16(f0, f1);
+                            }
+                            *reinterpret_cast<uint4 *>(lt + swizzled(t, x0 + x)) = make_uint4(l[0], l[1], l[2], l[3]);
+                        }
+                    }
+                } else {  // the tiles hold whatever follows the sequence there: zeros instead, in v too
+#pragma unroll
+                    for (int x = 0; x < 32; ++x) hi[x] = 0u;
+#pragma unroll 1
+                    for (int x = 0; x < 8; ++x) {
+                        *reinterpret_cast<uint4 *>(lt + swizzled(t, x)) = make_uint4(0u, 0u, 0u, 0u);
+                        if (half * 64 < DV)
+                            *reinterpret_cast<uint4 *>(v_tile + stage * kTileV + half * kBlock + swizzled(t, x)) =
+                                make_uint4(0u, 0u, 0u, 0u);
+                    }
+                }
+                __syncwarp();
+                if (!so && !wait_warp(&sh->scores, it & 1, dead)) {  // k is used up
+                    ok = false;
+                    break;
+                }
+#pragma unroll
+                for (int x = 0; x < 8; ++x)
+                    *reinterpret_cast<uint4 *>(kt + swizzled(t, x)) =
+                        make_uint4(hi[4 * x], hi[4 * x + 1], hi[4 * x + 2], hi[4 * x + 3]);
+                fence_smem_to_async();
+                arrive_warp(&sh->keys);
+            }
+        }
+    } else if (warp == 22 && lane == 0) {
         // ----------------------------------------------------------------------------- issue
         const uint32_t q = desc_k(smem_u32(q_tile)), sc = desc_mn(smem_u32(s_copy), kBlock),
                        lo = desc_mn(smem_u32(lo_tile), kBlock);
@@ -803,7 +866,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
                 const Unit u = unit_of(p, sh, idx);
                 if (u.on) atomicOr(a.err + u.s, kSeqTimeout);
             }
-    if (warp == 19) {
+    if (warp == 23) {
         tmem_fence_after();
         tmem_free(tm, kCols);
     }

@@ -71,29 +71,35 @@ __device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols) {
 #define CV_I4(r, i) "r"((r)[i]), "r"((r)[i + 1]), "r"((r)[i + 2]), "r"((r)[i + 3])
 #define CV_I16(r, i) CV_I4(r, i), CV_I4(r, i + 4), CV_I4(r, i + 8), CV_I4(r, i + 12)
 
-// 32 columns of the calling warp's 32 lanes; the values are there after tmem_wait_ld on the same array.
-__device__ __forceinline__ void tmem_ld32(uint32_t *r, uint32_t addr) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n"
-        : CV_R16(r, 0), CV_R16(r, 16)
-        : "r"(addr)
-        : "memory");
-}
-// 16 columns at each of two addresses, the second's values from r[16] on.
-__device__ __forceinline__ void tmem_ld16x2(uint32_t *r, uint32_t addr_a, uint32_t addr_b) {
+// 16 columns of the calling warp's 32 lanes; the values are there after tmem_wait_ld on the same array.
+__device__ __forceinline__ void tmem_ld16(uint32_t *r, uint32_t addr) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-        "%15}, [%32];\n"
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, "
-        "%29, %30, %31}, [%33];\n"
-        : CV_R16(r, 0), CV_R16(r, 16)
-        : "r"(addr_a), "r"(addr_b)
+        "%15}, [%16];\n"
+        : CV_R16(r, 0)
+        : "r"(addr)
         : "memory");
 }
 // All this thread's loads from tensor memory are complete; the array ties later uses of its values to it.
 __device__ __forceinline__ void tmem_wait_ld(uint32_t *r) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;\n" : CV_P16(r, 0), CV_P16(r, 16)::"memory");
+    asm volatile("tcgen05.wait::ld.sync.aligned;\n" : CV_P16(r, 0)::"memory");
+}
+// 8 columns at each of two addresses, and their wait.
+__device__ __forceinline__ void tmem_ld8x2(uint32_t *a, uint32_t *b, uint32_t addr_a, uint32_t addr_b) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%16];\n"
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%8, %9, %10, %11, %12, %13, %14, %15}, [%17];\n"
+        : CV_R4(a, 0), CV_R4(a, 4), CV_R4(b, 0), CV_R4(b, 4)
+        : "r"(addr_a), "r"(addr_b)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld8x2(uint32_t *a, uint32_t *b) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;\n" : CV_P4(a, 0), CV_P4(a, 4), CV_P4(b, 0), CV_P4(b, 4)::"memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t addr, const uint32_t *r) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"r"(addr), CV_I4(r, 0),
+                 CV_I4(r, 4)
+                 : "memory");
 }
 __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t *r) {
     asm volatile(
@@ -102,14 +108,6 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t *r) {
         CV_I16(r, 0)
         : "memory");
 }
-__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t *r) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};\n" ::"r"(addr),
-        CV_I16(r, 0), CV_I16(r, 16)
-        : "memory");
-}
-
 #undef CV_P4
 #undef CV_P16
 #undef CV_R4
