@@ -20,7 +20,7 @@
 //   output  4 warps, a row a thread: out from Q S and A V, rounded, through the dead v tile to memory
 //   keys    8 warps, half a token a thread: K' in place of K (once Q K^T is done) and its low part
 //   decays  1 warp: sums of the log decays and the weights made of them, ahead of the others
-//   load    1 thread: q, k, v tiles by TMA in the 128-byte swizzle, channels past the end zero
+//   load    2 threads: q, k, v tiles by TMA in the 128-byte swizzle, channels past the end zero
 //   issue   1 thread: all products, in the order Q K^T, Q S, K'^T V, A V
 // Shared memory: k and v in two stages, q, the low part of K' and the copy of S once (32 KB each at 128
 // channels); tensor memory: Q K^T (then A) 128 columns, Q S, A V and S dv columns each.  A chunk's products
@@ -42,7 +42,7 @@ constexpr int kTileQK = kChunk * 256;  // bytes of a q or k tile: two blocks of 
 
 // Barriers, in order (8 bytes each), then the small arrays.
 struct ChunkShared {
-    uint64_t kv_full[2], k_empty[2], v_empty[2];
+    uint64_t k_full[2], v_full[2], k_empty[2], v_empty[2];
     uint64_t g_full, g_empty, q_full, scores, a_ready, keys, q_used, s_init, s_ready, s_done, out, out_free, last;
     uint32_t tmem;
     int dead;
@@ -110,6 +110,7 @@ __device__ __forceinline__ bool poll(uint64_t *bar, unsigned parity) {
 }
 // Bounded wait of a whole warp; false once the block has given up.
 __device__ __forceinline__ bool wait_warp(uint64_t *bar, unsigned parity, volatile int *dead) {
+#pragma unroll 1
     for (unsigned i = 0; i < kPolls; ++i) {
         if (__all_sync(0xffffffffu, poll(bar, parity))) return true;
         if (__any_sync(0xffffffffu, *dead)) return false;
@@ -118,6 +119,7 @@ __device__ __forceinline__ bool wait_warp(uint64_t *bar, unsigned parity, volati
     return false;
 }
 __device__ __forceinline__ bool wait_one(uint64_t *bar, unsigned parity, volatile int *dead) {
+#pragma unroll 1
     for (unsigned i = 0; i < kPolls; ++i) {
         if (poll(bar, parity)) return true;
         if (*dead) return false;
@@ -272,7 +274,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
     if (tid == 0) {
         sh->dead = 0;
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&sh->kv_full[i], 1);
+            mbar_init(&sh->k_full[i], 1);
+            mbar_init(&sh->v_full[i], 1);
             mbar_init(&sh->k_empty[i], 1);
             mbar_init(&sh->v_empty[i], 4);
         }
@@ -360,28 +363,25 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
             }
         }
     } else if (warp == 21 && lane == 0) {
-        // ------------------------------------------------------------------------------ load
+        // ---------------------------------------------------------------------- load: k and q
         bool ok = true;
+        int k_sent = 0, q_sent = 0;
         for (int n = 0, idx; ok && (idx = unit_index(p, n)) != -1; ++n) {
             if (idx < 0) continue;
             const Unit u = unit_of(p, sh, idx);
             for (int c = 0; c < u.chunks; ++c, ++it) {
                 const int stage = it & 1, row = u.row0 + c * kChunk;
-                const unsigned ph = ((it >> 1) & 1) ^ 1;
-                if (it >= 2 && (!wait_one(&sh->k_empty[stage], ph, dead) || (!so && !wait_one(&sh->v_empty[stage], ph, dead)))) {
+                if (it >= 2 && !wait_one(&sh->k_empty[stage], ((it >> 1) & 1) ^ 1, dead)) {
                     ok = false;
                     break;
                 }
-                uint64_t *const bar = &sh->kv_full[stage];
-                const uint32_t k = smem_u32(k_tile + stage * kTileQK), v = smem_u32(v_tile + stage * kTileV);
-                mbar_arrive_expect_tx(bar, kTileQK + kTileV);
-                tma_load(k, &p.k_map, 0, u.hq, row, bar);
-                tma_load(k + kBlock, &p.k_map, 64, u.hq, row, bar);
-                tma_load(v, &p.v_map, 0, u.h, row, bar);
-                if (DV == 128) tma_load(v + kBlock, &p.v_map, 64, u.h, row, bar);
+                const uint32_t k = smem_u32(k_tile + stage * kTileQK);
+                mbar_arrive_expect_tx(&sh->k_full[stage], kTileQK);
+                tma_load(k, &p.k_map, 0, u.hq, row, &sh->k_full[stage]);
+                tma_load(k + kBlock, &p.k_map, 64, u.hq, row, &sh->k_full[stage]);
+                ++k_sent;
                 if (!so) {
                     if (it >= 1 && !wait_one(&sh->q_used, (it - 1) & 1, dead)) {
-                        ++it;  // this chunk's k and v are in flight
                         ok = false;
                         break;
                     }
@@ -389,16 +389,34 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
                     mbar_arrive_expect_tx(&sh->q_full, kTileQK);
                     tma_load(q, &p.q_map, 0, u.hq, row, &sh->q_full);
                     tma_load(q + kBlock, &p.q_map, 64, u.hq, row, &sh->q_full);
+                    ++q_sent;
                 }
             }
         }
         // nothing of the block's is in flight when it returns
-        if (!ok) {
-            if (it >= 1) mbar_wait_bounded(&sh->kv_full[(it - 1) & 1], ((it - 1) >> 1) & 1, kPolls);
-            if (it >= 2) mbar_wait_bounded(&sh->kv_full[it & 1], ((it - 2) >> 1) & 1, kPolls);
-            for (unsigned i = 0; !so && i < 2; ++i)  // whichever phase q's last copy completes
-                if (mbar_wait_bounded(&sh->q_full, i, kPolls / 64)) break;
+        for (int x = max(0, k_sent - 2); x < k_sent; ++x) mbar_wait_bounded(&sh->k_full[x & 1], (x >> 1) & 1, kPolls);
+        if (q_sent > 0) mbar_wait_bounded(&sh->q_full, (q_sent - 1) & 1, kPolls);
+    } else if (warp == 23 && lane == 0) {
+        // --------------------------------------------------------------------------- load: v
+        bool ok = true;
+        int sent = 0;
+        for (int n = 0, idx; ok && (idx = unit_index(p, n)) != -1; ++n) {
+            if (idx < 0) continue;
+            const Unit u = unit_of(p, sh, idx);
+            for (int c = 0; c < u.chunks; ++c, ++it) {
+                const int stage = it & 1, row = u.row0 + c * kChunk;
+                if (it >= 2 && !wait_one(so ? &sh->k_empty[stage] : &sh->v_empty[stage], ((it >> 1) & 1) ^ 1, dead)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t v = smem_u32(v_tile + stage * kTileV);
+                mbar_arrive_expect_tx(&sh->v_full[stage], kTileV);
+                tma_load(v, &p.v_map, 0, u.h, row, &sh->v_full[stage]);
+                if (DV == 128) tma_load(v + kBlock, &p.v_map, 64, u.h, row, &sh->v_full[stage]);
+                ++sent;
+            }
         }
+        for (int x = max(0, sent - 2); x < sent; ++x) mbar_wait_bounded(&sh->v_full[x & 1], (x >> 1) & 1, kPolls);
     } else if (role == 0 && !so) {
         // ---------------------------------------------------------------------------- scores
         bool ok = true;
@@ -742,7 +760,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
                 arrive_warp(&sh->g_empty);
                 // the low part's place is free once the last chunk's products are done (and this role never runs
                 // two phases ahead of the issue thread)
-                if (!wait_warp(&sh->kv_full[stage], (it >> 1) & 1, dead) ||
+                if (!wait_warp(&sh->k_full[stage], (it >> 1) & 1, dead) ||
                     (it > 0 && !wait_warp(&sh->s_done, (it - 1) & 1, dead))) {
                     ok = false;
                     break;
@@ -774,16 +792,22 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
                             *reinterpret_cast<uint4 *>(lt + swizzled(t, x0 + x)) = make_uint4(l[0], l[1], l[2], l[3]);
                         }
                     }
-                } else {  // the tiles hold whatever follows the sequence there: zeros instead, in v too
+                } else {  // the tiles hold whatever follows the sequence there: zeros instead
 #pragma unroll
                     for (int x = 0; x < 32; ++x) hi[x] = 0u;
 #pragma unroll 1
-                    for (int x = 0; x < 8; ++x) {
-                        *reinterpret_cast<uint4 *>(lt + swizzled(t, x)) = make_uint4(0u, 0u, 0u, 0u);
-                        if (half * 64 < DV)
+                    for (int x = 0; x < 8; ++x) *reinterpret_cast<uint4 *>(lt + swizzled(t, x)) = make_uint4(0u, 0u, 0u, 0u);
+                }
+                if (u.n - c * kChunk < kChunk && half * 64 < DV) {  // in v too
+                    if (!wait_warp(&sh->v_full[stage], (it >> 1) & 1, dead)) {
+                        ok = false;
+                        break;
+                    }
+                    if (t >= u.n - c * kChunk)
+#pragma unroll 1
+                        for (int x = 0; x < 8; ++x)
                             *reinterpret_cast<uint4 *>(v_tile + stage * kTileV + half * kBlock + swizzled(t, x)) =
                                 make_uint4(0u, 0u, 0u, 0u);
-                    }
                 }
                 __syncwarp();
                 if (!so && !wait_warp(&sh->scores, it & 1, dead)) {  // k is used up
@@ -815,7 +839,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
                 ok = false;
                 if (!so) {
                     // the last chunk's A, under the scores, is used up by the products before these
-                    if (!wait_one(&sh->kv_full[stage], (it >> 1) & 1, dead) || !wait_one(&sh->q_full, it & 1, dead)) break;
+                    if (!wait_one(&sh->k_full[stage], (it >> 1) & 1, dead) || !wait_one(&sh->q_full, it & 1, dead)) break;
                     tmem_fence_after();
 #pragma unroll
                     for (int x = 0; x < 8; ++x) {
@@ -833,7 +857,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
                         mma_ss(tm + kColQS, q + (((x >> 2) * kBlock + (x & 3) * 32) >> 4), sc + x * 128, id_qs, x > 0);
                     mma_commit(&sh->q_used);
                 }
-                if (!wait_one(&sh->keys, it & 1, dead)) break;
+                if (!wait_one(&sh->v_full[stage], (it >> 1) & 1, dead) || !wait_one(&sh->keys, it & 1, dead)) break;
                 tmem_fence_after();
 #pragma unroll
                 for (int x = 0; x < 8; ++x) {
