@@ -66,7 +66,7 @@ struct Unit {
     bool on, init, last;
 };
 
-__device__ __noinline__ Unit unit_of(const LinattnChunkParams &p, const ChunkShared *sh, int idx) {
+__device__ __forceinline__ Unit unit_of(const LinattnChunkParams &p, const ChunkShared *sh, int idx) {
     Unit u;
     const LinattnParams &a = p.a;
     u.h = idx % a.n_heads;
@@ -74,7 +74,7 @@ __device__ __noinline__ Unit unit_of(const LinattnChunkParams &p, const ChunkSha
     u.seg = r % p.n_segs;
     const int rank = r / p.n_segs;
     u.s = p.sort ? sh->order[rank] : rank;
-    u.hq = (int)((long long)u.h * a.n_qk / a.n_heads);
+    u.hq = (int)((unsigned)u.h * (unsigned)a.n_qk / (unsigned)a.n_heads);
     u.slot = a.cache_idx ? __ldg(a.cache_idx + u.s) : u.s;
     int L, row0;
     const int st = draft_span(a.tok.cu, u.s, a.tok.T, a.tok.total, L, row0);
@@ -133,26 +133,6 @@ __device__ __forceinline__ void arrive_warp(uint64_t *bar) {
     if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
 
-// Inclusive sum over the lanes up to this one.
-__device__ __forceinline__ float prefix_sum(float v, int lane) {
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const float x = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o) v += x;
-    }
-    return v;
-}
-// Sum over the lanes after this one.
-__device__ __forceinline__ float suffix_after(float v, int lane) {
-    float t = __shfl_down_sync(0xffffffffu, v, 1);
-    if (lane == 31) t = 0.0f;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const float x = __shfl_down_sync(0xffffffffu, t, o);
-        if (lane + o < 32) t += x;
-    }
-    return t;
-}
 __device__ __forceinline__ float clamp_log2(float g) {
     g *= kLog2e;
     return g < kMinLog2 ? kMinLog2 : g;  // a NaN stays
@@ -169,27 +149,36 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap *map, i
 
 // A NaN or an infinity in v spoils the rows above it in A V (0 * NaN).  This computes one row of the
 // outputs' part inside the chunk the long way, over the tokens up to the row itself only.
-__device__ __noinline__ void row_long_way(const LinattnParams &a, const Unit &u, int t0, int i, int c0, float *o) {
-    const uint16_t *q = reinterpret_cast<const uint16_t *>(a.tok.q) + (u.row0 + t0 + i) * a.tok.q_tok + u.hq * a.tok.q_head;
+__device__ __noinline__ void row_long_way(const LinattnParams &a, int row0, int h, int hq, int i, int c0, float *o) {
+    const uint16_t *q = reinterpret_cast<const uint16_t *>(a.tok.q) + (row0 + i) * a.tok.q_tok + hq * a.tok.q_head;
     float dec = 1.0f;
     for (int x = 0; x < 8; ++x) o[x] = 0.0f;
     for (int j = i; j >= 0; --j) {
-        const long long row = u.row0 + t0 + j;
-        const uint16_t *k = reinterpret_cast<const uint16_t *>(a.tok.k) + row * a.tok.k_tok + u.hq * a.tok.k_head;
-        const uint16_t *v = reinterpret_cast<const uint16_t *>(a.tok.v) + row * a.tok.v_tok + (long long)u.h * a.tok.v_head;
+        const long long row = row0 + j;
+        const uint16_t *k = reinterpret_cast<const uint16_t *>(a.tok.k) + row * a.tok.k_tok + hq * a.tok.k_head;
+        const uint16_t *v = reinterpret_cast<const uint16_t *>(a.tok.v) + row * a.tok.v_tok + (long long)h * a.tok.v_head;
         float dot = 0.0f;
         for (int x = 0; x < a.dk; ++x) dot = fmaf(widen<uint16_t>(q[x]), widen<uint16_t>(k[x]), dot);
-        float w = a.scale * dec * dot * (a.tok.b ? a.tok.b[row * a.tok.b_tok + u.h] : 1.0f);
-        if (j == i && a.skip) w += a.skip[u.h];
+        float w = a.scale * dec * dot * (a.tok.b ? a.tok.b[row * a.tok.b_tok + h] : 1.0f);
+        if (j == i && a.skip) w += a.skip[h];
         for (int x = 0; x < 8; ++x)
             if (c0 + x < a.dv) o[x] = fmaf(w, widen<uint16_t>(v[c0 + x]), o[x]);
-        dec *= exp2_fast(clamp_log2(a.tok.g[row * a.tok.g_tok + u.h]));
+        dec *= exp2_fast(clamp_log2(a.tok.g[row * a.tok.g_tok + h]));
     }
 }
 
 // Either bf16 half is a NaN or an infinity.
 __device__ __forceinline__ bool not_finite(uint32_t w) {
     return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
+}
+// Two elements of k times the weight, as a high and a low bf16 part.
+__device__ __forceinline__ void split(uint32_t k, f2 w2, f2 neg, uint32_t &hi, uint32_t &lo) {
+    const f2 f = f2_mul(f2_pack(__uint_as_float(k << 16), __uint_as_float(k & 0xffff0000u)), w2);
+    float f0, f1;
+    f2_unpack(f, f0, f1);
+    hi = pack_bf16(f0, f1);
+    f2_unpack(f2_fma(f2_pack(__uint_as_float(hi << 16), __uint_as_float(hi & 0xffff0000u)), neg, f), f0, f1);
+    lo = pack_bf16(f0, f1);
 }
 // 16 scores of a row times rf * col_j, rounded to bf16 pairs.
 template <bool ROW>
@@ -220,12 +209,12 @@ __device__ __forceinline__ void keep_lower(uint32_t *o, int left) {
 }
 // Row i of A for a chunk that decays by more than 2^80: exponents from the sums between i and j.
 template <int DV>
-__device__ __noinline__ void scores_strong(const LinattnParams &a, const Unit &u, const ChunkShared *sh, int c, uint32_t tp,
-                                           int w4, int lane, float skip) {
+__device__ __noinline__ void scores_strong(const LinattnParams &a, int row0, int rows, int h, const ChunkShared *sh,
+                                           uint32_t tp, int w4, int lane, float skip) {
     const float G = sh->G[32 * w4 + lane], t1 = sh->tot[1], t2 = sh->tot[2], scale = a.scale;
-    const bool in = c * kChunk + 32 * w4 + lane < u.n;
-    const long long row = u.row0 + c * kChunk + 32 * w4 + lane;
-    const float bi = in ? (a.tok.b ? __ldg(a.tok.b + row * a.tok.b_tok + u.h) : 1.0f) : 0.0f;
+    const bool in = 32 * w4 + lane < rows;
+    const long long row = row0 + 32 * w4 + lane;
+    const float bi = in ? (a.tok.b ? __ldg(a.tok.b + row * a.tok.b_tok + h) : 1.0f) : 0.0f;
     for (int x = 0; x < 8; ++x) {  // 16 columns at a time, ascending: A goes where earlier scores were
         const int J = x >> 1, j0 = 16 * (x & 1);
         uint32_t r[16], o[8];
@@ -329,36 +318,49 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
             for (int c = 0; c < u.chunks; ++c, ++it) {
                 const int rows = u.n - c * kChunk;
                 const long long row = u.row0 + c * kChunk;
-                float g[4], b[4], G[4], after[4], tot[4];
+                // four tokens a lane, a block of 32 in 8 lanes
+                float g[4], b[4], G[4], after[4];
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {  // a block of 32 tokens each
-                    const int t = 32 * x + lane;
+                for (int x = 0; x < 4; ++x) {
+                    const int t = 4 * lane + x;
                     g[x] = t < rows ? __ldg(a.tok.g + (row + t) * a.tok.g_tok + u.h) : 0.0f;
                     b[x] = t < rows ? (a.tok.b ? __ldg(a.tok.b + (row + t) * a.tok.b_tok + u.h) : 1.0f) : 0.0f;
                 }
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    const float l2 = clamp_log2(g[x]);
-                    G[x] = prefix_sum(l2, lane);
-                    after[x] = suffix_after(l2, lane);
-                    tot[x] = __shfl_sync(0xffffffffu, G[x], 31);
+                for (int x = 0; x < 4; ++x) g[x] = clamp_log2(g[x]);
+                G[0] = g[0], G[1] = G[0] + g[1], G[2] = G[1] + g[2], G[3] = G[2] + g[3];
+                after[3] = 0.0f, after[2] = g[3], after[1] = g[3] + g[2], after[0] = after[1] + g[1];
+                float up = G[3], down = G[3];  // of this lane and those before (after) it in the block
+#pragma unroll
+                for (int o = 1; o < 8; o <<= 1) {
+                    const float x = __shfl_up_sync(0xffffffffu, up, o, 8), y = __shfl_down_sync(0xffffffffu, down, o, 8);
+                    if ((lane & 7) >= o) up += x;
+                    if ((lane & 7) + o < 8) down += y;
                 }
-                const bool strong = !((tot[0] + tot[1]) + (tot[2] + tot[3]) > strong_at);
+                float before = __shfl_up_sync(0xffffffffu, up, 1, 8), later = __shfl_down_sync(0xffffffffu, down, 1, 8);
+                if ((lane & 7) == 0) before = 0.0f;
+                if ((lane & 7) == 7) later = 0.0f;
+                const float t0 = __shfl_sync(0xffffffffu, up, 7), t1 = __shfl_sync(0xffffffffu, up, 15),
+                            t2 = __shfl_sync(0xffffffffu, up, 23), t3 = __shfl_sync(0xffffffffu, up, 31);
+                const int block = lane >> 3;
+                const bool strong = !((t0 + t1) + (t2 + t3) > strong_at);
+                if (!strong) before += (block > 0 ? t0 : 0.0f) + (block > 1 ? t1 : 0.0f) + (block > 2 ? t2 : 0.0f);
+                const float ahead = (block < 1 ? t1 : 0.0f) + (block < 2 ? t2 : 0.0f) + (block < 3 ? t3 : 0.0f);
                 if (it > 0 && !wait_warp(&sh->g_empty, (it - 1) & 1, dead)) {
                     ok = false;
                     break;
                 }
-                float before = 0.0f, later = tot[1] + tot[2] + tot[3];
+                float col[4], key[4];
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
-                    const float all = before + G[x];
-                    sh->G[32 * x + lane] = strong ? G[x] : all;
-                    sh->col[32 * x + lane] = exp2_fast(strong ? after[x] : -all) * b[x];
-                    sh->key[32 * x + lane] = exp2_fast(after[x] + later) * b[x];
-                    if (lane == 0) sh->tot[x] = tot[x];
-                    before += tot[x];
-                    later = x < 2 ? (x < 1 ? tot[2] + tot[3] : tot[3]) : 0.0f;
+                    G[x] += before;
+                    col[x] = exp2_fast(strong ? after[x] + later : -G[x]) * b[x];
+                    key[x] = exp2_fast(after[x] + later + ahead) * b[x];
                 }
+                *reinterpret_cast<float4 *>(sh->G + 4 * lane) = make_float4(G[0], G[1], G[2], G[3]);
+                *reinterpret_cast<float4 *>(sh->col + 4 * lane) = make_float4(col[0], col[1], col[2], col[3]);
+                *reinterpret_cast<float4 *>(sh->key + 4 * lane) = make_float4(key[0], key[1], key[2], key[3]);
+                if (lane == 0) *reinterpret_cast<float4 *>(sh->tot) = make_float4(t0, t1, t2, t3);
                 arrive_warp(&sh->g_full);
             }
         }
@@ -433,43 +435,29 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
                 tmem_fence_after();
                 const float4 bt = *reinterpret_cast<const float4 *>(sh->tot);
                 if ((bt.x + bt.y) + (bt.z + bt.w) > strong_at) {
-                    // A overlays the scores: 16 columns go where earlier ones were read
-                    uint32_t r[16], s2[16], o[8];
-                    tmem_ld16(r, tp);
-#pragma unroll 1
-                    for (int x = 0; x < 2 * w4; x += 2) {
-                        tmem_wait_ld(r);
-                        tmem_ld16(s2, tp + 16 * x + 16);
-                        weigh<false>(r, 1.0f, sh->col + 16 * x, o);
-                        tmem_st8(tp + 8 * x, o);
-                        tmem_wait_ld(s2);
-                        tmem_ld16(r, tp + 16 * x + 32);
-                        weigh<false>(s2, 1.0f, sh->col + 16 * x + 16, o);
-                        tmem_st8(tp + 8 * x + 8, o);
-                    }
-                    // the block on the diagonal; with skip, A_ii holds skip / (scale exp(G_i)) too
+                    // A overlays the scores: 16 columns go where earlier ones were read.  With skip, A_ii holds
+                    // skip / (scale exp(G_i)) too.
                     const float own = a.skip ? skip / a.scale * exp2_fast(-sh->G[32 * w4 + lane]) : 0.0f;
-                    tmem_wait_ld(r);
-                    tmem_ld16(s2, tp + 32 * w4 + 16);
-                    if (a.skip)
-                        weigh_own(r, sh->col + 32 * w4, own, lane, o);
-                    else
-                        weigh<false>(r, 1.0f, sh->col + 32 * w4, o);
-                    keep_lower(o, lane);
-                    tmem_st8(tp + 16 * w4, o);
-                    tmem_wait_ld(s2);
-                    if (a.skip)
-                        weigh_own(s2, sh->col + 32 * w4 + 16, own, lane - 16, o);
-                    else
-                        weigh<false>(s2, 1.0f, sh->col + 32 * w4 + 16, o);
-                    keep_lower(o, lane - 16);
-                    tmem_st8(tp + 16 * w4 + 8, o);
+                    uint32_t r[16], o[8];
+                    int x = 0;
+#pragma unroll 1
+                    for (; x < 2 * w4 + 2; ++x) {
+                        tmem_ld16(r, tp + 16 * x);
+                        const int left = 32 * w4 + lane - 16 * x;  // the row's own column among these
+                        tmem_wait_ld(r);
+                        if (a.skip)
+                            weigh_own(r, sh->col + 16 * x, own, left, o);
+                        else
+                            weigh<false>(r, 1.0f, sh->col + 16 * x, o);
+                        if (x >= 2 * w4) keep_lower(o, left);
+                        tmem_st8(tp + 8 * x, o);
+                    }
 #pragma unroll
                     for (int j = 0; j < 8; ++j) o[j] = 0u;
 #pragma unroll 1
-                    for (int x = 2 * w4 + 2; x < 8; ++x) tmem_st8(tp + 8 * x, o);
+                    for (; x < 8; ++x) tmem_st8(tp + 8 * x, o);
                 } else {
-                    scores_strong<DV>(a, u, sh, c, tp, w4, lane, skip);
+                    scores_strong<DV>(a, u.row0 + c * kChunk, u.n - c * kChunk, u.h, sh, tp, w4, lane, skip);
                 }
                 tmem_wait_st();
                 tmem_fence_before();
@@ -547,14 +535,15 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
             if (!wait_warp(&sh->s_init, units++ & 1, dead)) break;
             float total = 1.0f;
             for (int c = 0; c < u.chunks; ++c, ++it) {
-                // the last chunk's products into S are done, and those that read the copy
-                if (!wait_warp(&sh->g_full, it & 1, dead) || (c > 0 && !wait_warp(&sh->s_done, (it - 1) & 1, dead))) {
+                // the last chunk's products into S are done, and those that read the copy (at a unit's start they were
+                // waited for at the end of the one before)
+                if (!wait_warp(&sh->g_full, it & 1, dead) || (c > 0 && (!wait_warp(&sh->s_done, (it - 1) & 1, dead) ||
+                              (!so && !wait_warp(&sh->q_used, (it - 1) & 1, dead))))) {
                     ok = false;
                     break;
                 }
                 tmem_fence_after();
-                uint32_t v[16], v2[16];
-                tmem_ld16(v, ts);
+                uint32_t v[16];
                 const float4 bt = *reinterpret_cast<const float4 *>(sh->tot);
                 arrive_warp(&sh->g_empty);
                 const float tot = exp2_fast((bt.x + bt.y) + (bt.z + bt.w));
@@ -583,20 +572,17 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
                     tmem_st16(ts + j, x);
                 };
 #pragma unroll 1
-                for (int j = 0; j < DV; j += 32) {
+                for (int j = 0; j < DV; j += 16) {
+                    tmem_ld16(v, ts + j);
                     tmem_wait_ld(v);
-                    tmem_ld16(v2, ts + j + 16);
                     piece(v, j);
-                    tmem_wait_ld(v2);
-                    if (j + 32 < DV) tmem_ld16(v, ts + j + 32);
-                    piece(v2, j + 16);
                 }
                 tmem_wait_st();
                 tmem_fence_before();
                 fence_smem_to_async();
                 arrive_warp(&sh->s_ready);
             }
-            if (!ok || !wait_warp(&sh->s_done, (it - 1) & 1, dead)) {
+            if (!ok || !wait_warp(&sh->s_done, (it - 1) & 1, dead) || (!so && !wait_warp(&sh->q_used, (it - 1) & 1, dead))) {
                 ok = false;
                 break;
             }
@@ -671,28 +657,25 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
                 tmem_fence_after();
                 const int t0 = c * kChunk;
                 unsigned char *const vt = v_tile + stage * kTileV;  // v is used up: the rows go through its tile
-                uint32_t x1[8], y1[8], x2[8], y2[8];
-                auto piece = [&](const uint32_t *x, const uint32_t *y, int j) {  // 8 columns
-                    uint32_t o[4];
+                uint32_t x1[8], y1[8];
+#pragma unroll 1
+                for (int j = 0; j < DV; j += 16) {
+                    uint32_t x[16], y[16], o[8];
+                    tmem_ld16(x, tl + kColQS + j);
+                    tmem_ld16(y, tl + kColAV + j);
+                    tmem_wait_ld(x);
+                    tmem_wait_ld(y);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
+                    for (int e = 0; e < 8; ++e) {
                         float f0, f1;
                         f2_unpack(f2_fma(pre2, f2_pack(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])),
                                          f2_mul(post2, f2_pack(__uint_as_float(y[2 * e]), __uint_as_float(y[2 * e + 1])))),
                                   f0, f1);
                         o[e] = pack_bf16(f0, f1);
                     }
-                    *reinterpret_cast<uint4 *>(vt + (j >> 6) * kBlock + swizzled(i, (j >> 3) & 7)) = make_uint4(o[0], o[1], o[2], o[3]);
-                };
-                tmem_ld8x2(x1, y1, tl + kColQS, tl + kColAV);
-#pragma unroll 1
-                for (int j = 0; j < DV; j += 16) {
-                    tmem_wait_ld8x2(x1, y1);
-                    tmem_ld8x2(x2, y2, tl + kColQS + j + 8, tl + kColAV + j + 8);
-                    piece(x1, y1, j);
-                    tmem_wait_ld8x2(x2, y2);
-                    if (j + 16 < DV) tmem_ld8x2(x1, y1, tl + kColQS + j + 16, tl + kColAV + j + 16);
-                    piece(x2, y2, j + 8);
+                    unsigned char *const at = vt + (j >> 6) * kBlock;
+                    *reinterpret_cast<uint4 *>(at + swizzled(i, (j >> 3) & 7)) = make_uint4(o[0], o[1], o[2], o[3]);
+                    *reinterpret_cast<uint4 *>(at + swizzled(i, ((j >> 3) & 7) + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
                 }
                 __syncwarp();
                 // A NaN or an infinity in v spoils its column in every row of the chunk, so the warp's first row
@@ -714,7 +697,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
                                 float part[8] = {};
                                 tmem_ld8x2(x1, y1, tl + kColQS + j, tl + kColAV + j);
                                 tmem_wait_ld8x2(x1, y1);
-                                if (t0 + i < u.n) row_long_way(a, u, t0, i, j, part);
+                                if (t0 + i < u.n) row_long_way(a, u.row0 + t0, u.h, u.hq, i, j, part);
                                 uint32_t o[4];
 #pragma unroll
                                 for (int e = 0; e < 4; ++e)
@@ -765,65 +748,48 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
                     ok = false;
                     break;
                 }
+                if (!so && !wait_warp(&sh->scores, it & 1, dead)) {  // k is used up
+                    ok = false;
+                    break;
+                }
                 const f2 w2 = f2_pack(w, w), neg = f2_pack(-1.0f, -1.0f);
                 unsigned char *const kt = k_tile + stage * kTileQK + half * kBlock, *const lt = lo_tile + half * kBlock;
-                uint32_t hi[32];
-                if (t < u.n - c * kChunk) {
-#pragma unroll
-                    for (int x0 = 0; x0 < 8; x0 += 4) {  // four pieces at a time: their latencies overlap
-                        uint4 in[4];
-#pragma unroll
-                        for (int x = 0; x < 4; ++x) in[x] = *reinterpret_cast<const uint4 *>(kt + swizzled(t, x0 + x));
-#pragma unroll
-                        for (int x = 0; x < 4; ++x) {
-                            const uint32_t k[4] = {in[x].x, in[x].y, in[x].z, in[x].w};
-                            uint32_t l[4];
-#pragma unroll
-                            for (int y = 0; y < 4; ++y) {
-                                const f2 f = f2_mul(f2_pack(__uint_as_float(k[y] << 16), __uint_as_float(k[y] & 0xffff0000u)), w2);
-                                float f0, f1;
-                                f2_unpack(f, f0, f1);
-                                const uint32_t h = pack_bf16(f0, f1);
-                                hi[4 * (x0 + x) + y] = h;
-                                f2_unpack(f2_fma(f2_pack(__uint_as_float(h << 16), __uint_as_float(h & 0xffff0000u)), neg, f),
-                                          f0, f1);
-                                l[y] = pack_bf16(f0, f1);
-                            }
-                            *reinterpret_cast<uint4 *>(lt + swizzled(t, x0 + x)) = make_uint4(l[0], l[1], l[2], l[3]);
-                        }
-                    }
-                } else {  // the tiles hold whatever follows the sequence there: zeros instead
-#pragma unroll
-                    for (int x = 0; x < 32; ++x) hi[x] = 0u;
+                const bool in = t < u.n - c * kChunk;
 #pragma unroll 1
-                    for (int x = 0; x < 8; ++x) *reinterpret_cast<uint4 *>(lt + swizzled(t, x)) = make_uint4(0u, 0u, 0u, 0u);
+                for (int x0 = 0; x0 < 8; x0 += 2) {
+                    uint4 k[2], hi[2], lo[2];
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) k[x] = *reinterpret_cast<const uint4 *>(kt + swizzled(t, x0 + x));
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        split(k[x].x, w2, neg, hi[x].x, lo[x].x);
+                        split(k[x].y, w2, neg, hi[x].y, lo[x].y);
+                        split(k[x].z, w2, neg, hi[x].z, lo[x].z);
+                        split(k[x].w, w2, neg, hi[x].w, lo[x].w);
+                        // past the end the tile holds whatever follows the sequence there: zeros instead
+                        if (!in) hi[x] = lo[x] = make_uint4(0u, 0u, 0u, 0u);
+                        *reinterpret_cast<uint4 *>(kt + swizzled(t, x0 + x)) = hi[x];
+                        *reinterpret_cast<uint4 *>(lt + swizzled(t, x0 + x)) = lo[x];
+                    }
                 }
                 if (u.n - c * kChunk < kChunk && half * 64 < DV) {  // in v too
                     if (!wait_warp(&sh->v_full[stage], (it >> 1) & 1, dead)) {
                         ok = false;
                         break;
                     }
-                    if (t >= u.n - c * kChunk)
+                    if (!in)
 #pragma unroll 1
                         for (int x = 0; x < 8; ++x)
                             *reinterpret_cast<uint4 *>(v_tile + stage * kTileV + half * kBlock + swizzled(t, x)) =
                                 make_uint4(0u, 0u, 0u, 0u);
                 }
-                __syncwarp();
-                if (!so && !wait_warp(&sh->scores, it & 1, dead)) {  // k is used up
-                    ok = false;
-                    break;
-                }
-#pragma unroll
-                for (int x = 0; x < 8; ++x)
-                    *reinterpret_cast<uint4 *>(kt + swizzled(t, x)) =
-                        make_uint4(hi[4 * x], hi[4 * x + 1], hi[4 * x + 2], hi[4 * x + 3]);
                 fence_smem_to_async();
                 arrive_warp(&sh->keys);
             }
         }
-    } else if (warp == 22 && lane == 0) {
+    } else if (warp == 22) {
         // ----------------------------------------------------------------------------- issue
+        const uint32_t lead = elect_lane();
         const uint32_t q = desc_k(smem_u32(q_tile)), sc = desc_mn(smem_u32(s_copy), kBlock),
                        lo = desc_mn(smem_u32(lo_tile), kBlock);
         constexpr uint32_t id_qk = mma_desc(128, false, false), id_qs = mma_desc(DV, false, true),
@@ -839,46 +805,46 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
                 ok = false;
                 if (!so) {
                     // the last chunk's A, under the scores, is used up by the products before these
-                    if (!wait_one(&sh->k_full[stage], (it >> 1) & 1, dead) || !wait_one(&sh->q_full, it & 1, dead)) break;
+                    if (!wait_warp(&sh->k_full[stage], (it >> 1) & 1, dead) || !wait_warp(&sh->q_full, it & 1, dead)) break;
                     tmem_fence_after();
-#pragma unroll
+#pragma unroll 1
                     for (int x = 0; x < 8; ++x) {
                         const uint32_t off = ((x >> 2) * kBlock + (x & 3) * 32) >> 4;
-                        mma_ss(tm + kColP, q + off, desc_k(kt) + off, id_qk, x > 0);
+                        mma_ss(lead, tm + kColP, q + off, desc_k(kt) + off, id_qk, x > 0);
                     }
-                    mma_commit(&sh->scores);
+                    mma_commit(lead, &sh->scores);
                 }
-                if (!wait_one(&sh->s_ready, it & 1, dead)) break;
+                if (!wait_warp(&sh->s_ready, it & 1, dead)) break;
                 if (!so) {
-                    if (it > 0 && !wait_one(&sh->out_free, (it - 1) & 1, dead)) break;
+                    if (it > 0 && !wait_warp(&sh->out_free, (it - 1) & 1, dead)) break;
                     tmem_fence_after();
-#pragma unroll
+#pragma unroll 1
                     for (int x = 0; x < 8; ++x)
-                        mma_ss(tm + kColQS, q + (((x >> 2) * kBlock + (x & 3) * 32) >> 4), sc + x * 128, id_qs, x > 0);
-                    mma_commit(&sh->q_used);
+                        mma_ss(lead, tm + kColQS, q + (((x >> 2) * kBlock + (x & 3) * 32) >> 4), sc + x * 128, id_qs, x > 0);
+                    mma_commit(lead, &sh->q_used);
                 }
-                if (!wait_one(&sh->v_full[stage], (it >> 1) & 1, dead) || !wait_one(&sh->keys, it & 1, dead)) break;
+                if (!wait_warp(&sh->v_full[stage], (it >> 1) & 1, dead) || !wait_warp(&sh->keys, it & 1, dead)) break;
                 tmem_fence_after();
-#pragma unroll
+#pragma unroll 1
                 for (int x = 0; x < 8; ++x) {
-                    mma_ss(tm + kColS, k + x * 128, v + x * 128, id_kv, true);
-                    mma_ss(tm + kColS, lo + x * 128, v + x * 128, id_kv, true);
+                    mma_ss(lead, tm + kColS, k + x * 128, v + x * 128, id_kv, true);
+                    mma_ss(lead, tm + kColS, lo + x * 128, v + x * 128, id_kv, true);
                 }
-                mma_commit(&sh->s_done);
-                mma_commit(&sh->k_empty[stage]);
+                mma_commit(lead, &sh->s_done);
+                mma_commit(lead, &sh->k_empty[stage]);
                 if (!so) {
-                    if (!wait_one(&sh->a_ready, it & 1, dead)) break;
+                    if (!wait_warp(&sh->a_ready, it & 1, dead)) break;
                     tmem_fence_after();
-#pragma unroll
+#pragma unroll 1
                     for (int x = 0; x < 8; ++x)
-                        mma_ts(tm + kColAV, tm + kColP + x * 8, v + x * 128, id_qs, x > 0);
-                    mma_commit(&sh->out);
+                        mma_ts(lead, tm + kColAV, tm + kColP + x * 8, v + x * 128, id_qs, x > 0);
+                    mma_commit(lead, &sh->out);
                 }
                 ok = true;
             }
         }
         // nothing of the block's is in flight when it gives tensor memory back
-        mma_commit(&sh->last);
+        mma_commit(lead, &sh->last);
         mbar_wait_bounded(&sh->last, 0, kPolls);
     }
     __syncwarp();

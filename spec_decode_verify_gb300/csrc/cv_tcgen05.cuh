@@ -29,26 +29,37 @@ __device__ __forceinline__ constexpr uint32_t mma_desc(int n, bool a_mn, bool b_
            ((uint32_t)(n >> 3) << 17) | (8u << 24);
 }
 
-// D (tensor memory) = A B (+ D when acc), K = 16 per instruction; issued by one thread.
-__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool acc) {
+// One lane of the calling warp, the same every time.  The warp runs the issuing code as a whole, so that its
+// addresses and descriptors are uniform; only the instructions below are this lane's alone.
+__device__ __forceinline__ uint32_t elect_lane() {
+    uint32_t r;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+    return r;
+}
+// D (tensor memory) = A B (+ D when acc), K = 16 per instruction.
+__device__ __forceinline__ void mma_ss(uint32_t lead, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool acc) {
     asm volatile(
-        "{\n .reg .pred p;\n .reg .b64 da, db;\n setp.ne.u32 p, %4, 0;\n mov.b64 da, {%1, %5};\n mov.b64 db, {%2, %5};\n"
-        " tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n}\n" ::"r"(d),
-        "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)acc), "r"(kDescHigh)
+        "{\n .reg .pred p, q;\n .reg .b64 da, db;\n setp.ne.u32 p, %4, 0;\n setp.ne.u32 q, %6, 0;\n"
+        " mov.b64 da, {%1, %5};\n mov.b64 db, {%2, %5};\n"
+        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n}\n" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)acc), "r"(kDescHigh), "r"(lead)
         : "memory");
 }
 // The same with A in tensor memory (two bf16 of a row per 32-bit column).
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool acc) {
+__device__ __forceinline__ void mma_ts(uint32_t lead, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool acc) {
     asm volatile(
-        "{\n .reg .pred p;\n .reg .b64 db;\n setp.ne.u32 p, %4, 0;\n mov.b64 db, {%2, %5};\n"
-        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n}\n" ::"r"(d),
-        "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)acc), "r"(kDescHigh)
+        "{\n .reg .pred p, q;\n .reg .b64 db;\n setp.ne.u32 p, %4, 0;\n setp.ne.u32 q, %6, 0;\n mov.b64 db, {%2, %5};\n"
+        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n}\n" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)acc), "r"(kDescHigh), "r"(lead)
         : "memory");
 }
-// Arrive on `bar` once every tcgen05 operation this thread has issued is complete.
-__device__ __forceinline__ void mma_commit(uint64_t *bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(smem_u32(bar))
-                 : "memory");
+// Arrive on `bar` once every tcgen05 operation the lane has issued is complete.
+__device__ __forceinline__ void mma_commit(uint32_t lead, uint64_t *bar) {
+    asm volatile(
+        "{\n .reg .pred q;\n setp.ne.u32 q, %1, 0;\n"
+        " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(smem_u32(bar)),
+        "r"(lead)
+        : "memory");
 }
 __device__ __forceinline__ void tmem_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory"); }
 __device__ __forceinline__ void tmem_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory"); }
