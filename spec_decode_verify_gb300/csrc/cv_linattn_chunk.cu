@@ -43,17 +43,17 @@ constexpr int kTileQK = kChunk * 256;  // bytes of a q or k tile: two blocks of 
 // Barriers, in order (8 bytes each), then the small arrays.
 struct ChunkShared {
     uint64_t k_full[2], v_full[2], k_empty[2], v_empty[2];
-    uint64_t g_full, g_empty, q_full, scores, a_ready, keys, q_used, s_init, s_ready, s_done, out, out_free, last;
+    uint64_t g_full[2], g_empty[2], key_empty, q_full, scores, a_ready, keys, q_used, s_init, s_ready, s_done, out, out_free, last;
     uint32_t tmem;
     int dead;
     uint8_t order[kChunkMaxSorted];
-    // Of the chunk at hand: each token's sum of log2 decays up to it (over the chunk, or over its block of 32
-    // where the chunk decays by more than 2^80), its weight as a column of A, its weight in K', and the
-    // blocks' sums.  Tokens past the end: no decay, no weight.
-    alignas(16) float G[kChunk];
-    alignas(16) float col[kChunk];
+    // Of a chunk: each token's sum of log2 decays up to it (over the chunk, or over its block of 32 where the
+    // chunk decays by more than 2^80), its weight as a column of A, the blocks' sums, and its weight in K'.
+    // Tokens past the end: no decay, no weight.
+    alignas(16) float G[2][kChunk];
+    alignas(16) float col[2][kChunk];
+    alignas(16) float tot[2][4];
     alignas(16) float key[kChunk];
-    alignas(16) float tot[4];
 };
 
 template <int DV>
@@ -209,9 +209,9 @@ __device__ __forceinline__ void keep_lower(uint32_t *o, int left) {
 }
 // Row i of A for a chunk that decays by more than 2^80: exponents from the sums between i and j.
 template <int DV>
-__device__ __noinline__ void scores_strong(const LinattnParams &a, int row0, int rows, int h, const ChunkShared *sh,
-                                           uint32_t tp, int w4, int lane, float skip) {
-    const float G = sh->G[32 * w4 + lane], t1 = sh->tot[1], t2 = sh->tot[2], scale = a.scale;
+__device__ __noinline__ void scores_strong(const LinattnParams &a, int row0, int rows, int h, const float *Gs, const float *col,
+                                           const float *tot, uint32_t tp, int w4, int lane, float skip) {
+    const float G = Gs[32 * w4 + lane], t1 = tot[1], t2 = tot[2], scale = a.scale;
     const bool in = 32 * w4 + lane < rows;
     const long long row = row0 + 32 * w4 + lane;
     const float bi = in ? (a.tok.b ? __ldg(a.tok.b + row * a.tok.b_tok + h) : 1.0f) : 0.0f;
@@ -226,7 +226,7 @@ __device__ __noinline__ void scores_strong(const LinattnParams &a, int row0, int
             tmem_wait_ld(r);
             if (J < w4) {
                 const float between = (J < 1 && w4 > 1 ? t1 : 0.0f) + (J < 2 && w4 > 2 ? t2 : 0.0f);
-                weigh<true>(r, exp2_fast(G + between) * scale, sh->col + 16 * x, o);
+                weigh<true>(r, exp2_fast(G + between) * scale, col + 16 * x, o);
             } else {
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {
@@ -267,9 +267,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
             mbar_init(&sh->v_full[i], 1);
             mbar_init(&sh->k_empty[i], 1);
             mbar_init(&sh->v_empty[i], 4);
+            mbar_init(&sh->g_full[i], 1);
+            mbar_init(&sh->g_empty[i], so ? 4 : 12);
         }
-        mbar_init(&sh->g_full, 1);
-        mbar_init(&sh->g_empty, so ? 12 : 20);
+        mbar_init(&sh->key_empty, 8);
         mbar_init(&sh->q_full, 1);
         mbar_init(&sh->scores, 1);
         mbar_init(&sh->a_ready, 4);
@@ -346,7 +347,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
                 const bool strong = !((t0 + t1) + (t2 + t3) > strong_at);
                 if (!strong) before += (block > 0 ? t0 : 0.0f) + (block > 1 ? t1 : 0.0f) + (block > 2 ? t2 : 0.0f);
                 const float ahead = (block < 1 ? t1 : 0.0f) + (block < 2 ? t2 : 0.0f) + (block < 3 ? t3 : 0.0f);
-                if (it > 0 && !wait_warp(&sh->g_empty, (it - 1) & 1, dead)) {
+                const int stage = it & 1;
+                if ((it > 1 && !wait_warp(&sh->g_empty[stage], ((it >> 1) & 1) ^ 1, dead)) ||
+                    (it > 0 && !wait_warp(&sh->key_empty, (it - 1) & 1, dead))) {
                     ok = false;
                     break;
                 }
@@ -357,11 +360,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
                     col[x] = exp2_fast(strong ? after[x] + later : -G[x]) * b[x];
                     key[x] = exp2_fast(after[x] + later + ahead) * b[x];
                 }
-                *reinterpret_cast<float4 *>(sh->G + 4 * lane) = make_float4(G[0], G[1], G[2], G[3]);
-                *reinterpret_cast<float4 *>(sh->col + 4 * lane) = make_float4(col[0], col[1], col[2], col[3]);
+                *reinterpret_cast<float4 *>(sh->G[stage] + 4 * lane) = make_float4(G[0], G[1], G[2], G[3]);
+                *reinterpret_cast<float4 *>(sh->col[stage] + 4 * lane) = make_float4(col[0], col[1], col[2], col[3]);
                 *reinterpret_cast<float4 *>(sh->key + 4 * lane) = make_float4(key[0], key[1], key[2], key[3]);
-                if (lane == 0) *reinterpret_cast<float4 *>(sh->tot) = make_float4(t0, t1, t2, t3);
-                arrive_warp(&sh->g_full);
+                if (lane == 0) *reinterpret_cast<float4 *>(sh->tot[stage]) = make_float4(t0, t1, t2, t3);
+                arrive_warp(&sh->g_full[stage]);
             }
         }
     } else if (warp == 21 && lane == 0) {
@@ -428,16 +431,17 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
             const Unit u = unit_of(p, sh, idx);
             const float skip = a.skip ? __ldg(a.skip + u.h) : 0.0f;
             for (int c = 0; c < u.chunks; ++c, ++it) {
-                if (!wait_warp(&sh->g_full, it & 1, dead) || !wait_warp(&sh->scores, it & 1, dead)) {
+                const int stage = it & 1;
+                if (!wait_warp(&sh->g_full[stage], (it >> 1) & 1, dead) || !wait_warp(&sh->scores, it & 1, dead)) {
                     ok = false;
                     break;
                 }
                 tmem_fence_after();
-                const float4 bt = *reinterpret_cast<const float4 *>(sh->tot);
+                const float4 bt = *reinterpret_cast<const float4 *>(sh->tot[stage]);
                 if ((bt.x + bt.y) + (bt.z + bt.w) > strong_at) {
                     // A overlays the scores: 16 columns go where earlier ones were read.  With skip, A_ii holds
                     // skip / (scale exp(G_i)) too.
-                    const float own = a.skip ? skip / a.scale * exp2_fast(-sh->G[32 * w4 + lane]) : 0.0f;
+                    const float own = a.skip ? skip / a.scale * exp2_fast(-sh->G[stage][32 * w4 + lane]) : 0.0f;
                     uint32_t r[16], o[8];
                     int x = 0;
 #pragma unroll 1
@@ -446,9 +450,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
                         const int left = 32 * w4 + lane - 16 * x;  // the row's own column among these
                         tmem_wait_ld(r);
                         if (a.skip)
-                            weigh_own(r, sh->col + 16 * x, own, left, o);
+                            weigh_own(r, sh->col[stage] + 16 * x, own, left, o);
                         else
-                            weigh<false>(r, 1.0f, sh->col + 16 * x, o);
+                            weigh<false>(r, 1.0f, sh->col[stage] + 16 * x, o);
                         if (x >= 2 * w4) keep_lower(o, left);
                         tmem_st8(tp + 8 * x, o);
                     }
@@ -457,12 +461,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
 #pragma unroll 1
                     for (; x < 8; ++x) tmem_st8(tp + 8 * x, o);
                 } else {
-                    scores_strong<DV>(a, u.row0 + c * kChunk, u.n - c * kChunk, u.h, sh, tp, w4, lane, skip);
+                    scores_strong<DV>(a, u.row0 + c * kChunk, u.n - c * kChunk, u.h, sh->G[stage], sh->col[stage], sh->tot[stage], tp, w4, lane, skip);
                 }
                 tmem_wait_st();
                 tmem_fence_before();
                 arrive_warp(&sh->a_ready);
-                arrive_warp(&sh->g_empty);
+                arrive_warp(&sh->g_empty[stage]);
             }
         }
     } else if (role == 1) {
@@ -535,17 +539,18 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
             if (!wait_warp(&sh->s_init, units++ & 1, dead)) break;
             float total = 1.0f;
             for (int c = 0; c < u.chunks; ++c, ++it) {
+                const int stage = it & 1;
                 // the last chunk's products into S are done, and those that read the copy (at a unit's start they were
                 // waited for at the end of the one before)
-                if (!wait_warp(&sh->g_full, it & 1, dead) || (c > 0 && (!wait_warp(&sh->s_done, (it - 1) & 1, dead) ||
+                if (!wait_warp(&sh->g_full[stage], (it >> 1) & 1, dead) || (c > 0 && (!wait_warp(&sh->s_done, (it - 1) & 1, dead) ||
                               (!so && !wait_warp(&sh->q_used, (it - 1) & 1, dead))))) {
                     ok = false;
                     break;
                 }
                 tmem_fence_after();
                 uint32_t v[16];
-                const float4 bt = *reinterpret_cast<const float4 *>(sh->tot);
-                arrive_warp(&sh->g_empty);
+                const float4 bt = *reinterpret_cast<const float4 *>(sh->tot[stage]);
+                arrive_warp(&sh->g_empty[stage]);
                 const float tot = exp2_fast((bt.x + bt.y) + (bt.z + bt.w));
                 const f2 tot2 = f2_pack(tot, tot);
                 total *= tot;
@@ -637,16 +642,16 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
             const Unit u = unit_of(p, sh, idx);
             for (int c = 0; c < u.chunks; ++c, ++it) {
                 const int stage = it & 1;
-                if (!wait_warp(&sh->g_full, it & 1, dead)) {
+                if (!wait_warp(&sh->g_full[stage], (it >> 1) & 1, dead)) {
                     ok = false;
                     break;
                 }
                 // out = pre * (Q S) + post * (A V)
-                const float4 bt = *reinterpret_cast<const float4 *>(sh->tot);
-                float G = sh->G[i], post = 1.0f;
+                const float4 bt = *reinterpret_cast<const float4 *>(sh->tot[stage]);
+                float G = sh->G[stage][i], post = 1.0f;
                 const bool strong = !((bt.x + bt.y) + (bt.z + bt.w) > strong_at);
                 if (strong) G += (w4 > 0 ? bt.x : 0.0f) + (w4 > 1 ? bt.y : 0.0f) + (w4 > 2 ? bt.z : 0.0f);
-                arrive_warp(&sh->g_empty);
+                arrive_warp(&sh->g_empty[stage]);
                 const float pre = exp2_fast(G) * a.scale;
                 if (!strong) post = pre;
                 const f2 pre2 = f2_pack(pre, pre), post2 = f2_pack(post, post);
@@ -658,7 +663,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
                 const int t0 = c * kChunk;
                 unsigned char *const vt = v_tile + stage * kTileV;  // v is used up: the rows go through its tile
                 uint32_t x1[8], y1[8];
-#pragma unroll 1
+#pragma unroll 2
                 for (int j = 0; j < DV; j += 16) {
                     uint32_t x[16], y[16], o[8];
                     tmem_ld16(x, tl + kColQS + j);
@@ -735,12 +740,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
             const Unit u = unit_of(p, sh, idx);
             for (int c = 0; c < u.chunks; ++c, ++it) {
                 const int stage = it & 1;
-                if (!wait_warp(&sh->g_full, it & 1, dead)) {
+                if (!wait_warp(&sh->g_full[stage], (it >> 1) & 1, dead)) {
                     ok = false;
                     break;
                 }
                 const float w = sh->key[t];
-                arrive_warp(&sh->g_empty);
+                arrive_warp(&sh->key_empty);
                 // the low part's place is free once the last chunk's products are done (and this role never runs
                 // two phases ahead of the issue thread)
                 if (!wait_warp(&sh->k_full[stage], (it >> 1) & 1, dead) ||
