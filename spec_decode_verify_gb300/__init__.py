@@ -20,6 +20,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional
 
 __all__ = ["conv_verify", "conv_commit", "conv_prefill", "verify_plan", "status_string", "load_library", "library_path",
@@ -34,6 +35,7 @@ DENSE, DEDUP, HISTORY, RECOMPUTE = 1, 2, 3, 4
 F32, BF16 = 0, 1
 SEQ_BAD_SLOT, SEQ_BAD_OFFSET, SEQ_BAD_ACCEPT, SEQ_TIMEOUT, SEQ_BAD_SPAN, SEQ_BAD_TREE = 1, 2, 4, 8, 16, 32
 MAX_T = 128
+ERR_WORKSPACE = -13
 
 c_i32, c_i64, c_vp = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p
 
@@ -231,6 +233,20 @@ def _stream_ptr(stream) -> Optional[int]:
     import torch
     if stream is None:
         stream = torch.cuda.current_stream()
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+_current_stream = None
+
+
+def _stream_of(stream, t) -> int:
+    """The handle of ``stream``, by default torch's current stream on the device of ``t``."""
+    if stream is None:
+        global _current_stream
+        if _current_stream is None:
+            import torch
+            _current_stream = torch._C._cuda_getCurrentRawStream
+        return _current_stream(t.get_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -470,100 +486,135 @@ class LinattnDrafts:
         self.cu_draft, self.T = cu_draft, T
 
 
-def _linattn_tokens(q, k, v, log_decay, gain, cu, T, n_seq, ptr, what) -> LinattnTokens:
-    """cv_linattn_tokens of [n_seq, T, heads, d] rows, or of packed [total, heads, d] rows with cu."""
+# cv_linattn_tokens and cv_linattn_args as the struct module writes them: one call fills all fields
+_TOKENS = "iiQQQQ9qQ2qQ2q"
+_LINATTN = struct.Struct("<6ifi" + _TOKENS + "QQ3qQ2qQQQ" + _TOKENS + "QiiQq")
+_NO_TOKENS = (0,) * 21
+_NORM = struct.Struct("<q6i2fQqQqQQqQqQQQq")
+
+
+def _pointer(t, name, check_device, required=True) -> int:
+    if t is None:
+        if required:
+            raise ValueError(f"{name} is required")
+        return 0
+    if check_device and not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (there is no CPU path)")
+    return t.data_ptr()
+
+
+def _index_array(t, name, n, check_device) -> int:
+    """Pointer of an int32 array of at least n elements, or 0."""
+    if t is None:
+        return 0
+    if t.dtype is not _i32 or t.numel() < n or not t.is_contiguous():
+        _need_int32(t, name, n=n)
+    return _pointer(t, name, check_device)
+
+
+# torch's types, looked up once (the package does not import torch by itself)
+_f32 = _bf16 = _i32 = None
+
+
+def _load_types():
+    global _f32, _bf16, _i32
     import torch
-    nd = 3 if cu is not None else 4
-    if k.dim() != nd or v.dim() != nd or log_decay.dim() != nd - 1 or (q is not None and q.dim() != nd):
-        raise ValueError(f"{what}: q, k and v must be [n_seq, T, heads, d] and log_decay [n_seq, T, heads], "
-                         "or [total, ...] with packed rows")
-    lead, H = tuple(v.shape[:-2]), v.shape[-2]
-    if tuple(k.shape[:-2]) != lead or (q is not None and q.shape != k.shape):
-        raise ValueError(f"{what}: q and k must agree, and have the rows of v")
-    _need_shape(log_decay, "log_decay", lead + (H,))
-    if v.dtype != k.dtype or (q is not None and q.dtype != k.dtype):
+    _bf16, _i32, _f32 = torch.bfloat16, torch.int32, torch.float32
+    return _f32
+
+
+def _linattn_tokens(q, k, v, log_decay, gain, cu, T, n_seq, check_device, what) -> tuple:
+    """The fields of cv_linattn_tokens for [n_seq, T, heads, d] rows, or packed [total, heads, d] rows with
+    cu."""
+    f32 = _f32 or _load_types()
+    packed = cu is not None
+    nd = 3 if packed else 4
+    ks, vs, gs = k.shape, v.shape, log_decay.shape
+    if len(ks) != nd or len(vs) != nd or len(gs) != nd - 1 or (q is not None and q.shape != ks):
+        raise ValueError(f"{what}: q and k must agree, and q, k and v be [n_seq, T, heads, d] and log_decay "
+                         "[n_seq, T, heads], or [total, ...] with packed rows")
+    if ks[:-2] != vs[:-2] or gs != vs[:-1] or (gain is not None and gain.shape != gs):
+        raise ValueError(f"{what}: q, k, v, log_decay and gain must have the same rows, and log_decay and gain the heads "
+                         f"of v: {tuple(ks)}, {tuple(vs)}, {tuple(gs)}")
+    dt = k.dtype
+    if v.dtype is not dt or (q is not None and q.dtype is not dt):
         raise TypeError("q, k and v must share one dtype")
-    for t in (log_decay, gain):
-        if t is not None and t.dtype != torch.float32:
-            raise TypeError("log_decay and gain must be float32")
-    if k.stride(-1) != 1 or v.stride(-1) != 1 or (q is not None and q.stride(-1) != 1):
+    if log_decay.dtype is not f32 or (gain is not None and gain.dtype is not f32):
+        raise TypeError("log_decay and gain must be float32")
+    kt, vt, gt = k.stride(), v.stride(), log_decay.stride()
+    qt = q.stride() if q is not None else kt
+    bt = gain.stride() if gain is not None else gt
+    if kt[-1] != 1 or vt[-1] != 1 or qt[-1] != 1:
         raise ValueError("q, k and v need a unit innermost stride")
-    if H > 1 and (log_decay.stride(-1) != 1 or (gain is not None and gain.stride(-1) != 1)):
+    if gs[-1] > 1 and (gt[-1] != 1 or bt[-1] != 1):
         raise ValueError("log_decay and gain need a unit innermost stride")
-    if gain is not None:
-        _need_shape(gain, "gain", lead + (H,))
-    if cu is None:
-        if lead[0] != n_seq:
-            raise ValueError(f"{what}: {n_seq} sequences expected, got {lead[0]}")
-        if T is not None and T != lead[1]:
-            raise ValueError(f"{what}: T = {T} but the rows hold {lead[1]} tokens")
-        T, total = lead[1], 0
-    else:
-        _need_int32(cu, "cu", shape=(n_seq + 1,))
+    if packed:
+        if cu.dtype is not _i32 or cu.shape != (n_seq + 1,) or not cu.is_contiguous():
+            _need_int32(cu, "cu", shape=(n_seq + 1,))
         if T is None:
             raise ValueError(f"{what}: packed rows need T, the largest count")
-        total = lead[0]
-    some = (total if cu is not None else n_seq * T) > 0
-
-    def st(t):
-        s = t.stride()
-        return (0, s[0], s[1]) if nd == 3 else (s[0], s[1], s[2])
-
-    gs, bs = log_decay.stride(), gain.stride() if gain is not None else (0, 0)
-    return LinattnTokens(
-        int(T), total, ptr(cu, "cu", False), ptr(q, "q", some) if q is not None else None, ptr(k, "k", some),
-        ptr(v, "v", some), *(st(q) if q is not None else (0, 0, 0)), *st(k), *st(v),
-        ptr(log_decay, "log_decay", some), 0 if nd == 3 else gs[0], gs[nd - 3], ptr(gain, "gain", False),
-        0 if nd == 3 or gain is None else bs[0], bs[nd - 3])
+        total = vs[0]
+        qt, kt, vt, gt, bt = (0, qt[0], qt[1]), (0, kt[0], kt[1]), (0, vt[0], vt[1]), (0, gt[0]), (0, bt[0])
+    else:
+        if vs[0] != n_seq:
+            raise ValueError(f"{what}: {n_seq} sequences expected, got {vs[0]}")
+        if T is not None and T != vs[1]:
+            raise ValueError(f"{what}: T = {T} but the rows hold {vs[1]} tokens")
+        T, total = vs[1], 0
+    if check_device and not (k.is_cuda and v.is_cuda and log_decay.is_cuda and (q is None or q.is_cuda) and
+                             (gain is None or gain.is_cuda) and (cu is None or cu.is_cuda)):
+        raise ValueError(f"{what}: expected a CUDA tensor (there is no CPU path)")
+    return (int(T), total, cu.data_ptr() if packed else 0, q.data_ptr() if q is not None else 0, k.data_ptr(), v.data_ptr(),
+            qt[0], qt[1], qt[2], kt[0], kt[1], kt[2], vt[0], vt[1], vt[2], log_decay.data_ptr(), gt[0], gt[1],
+            gain.data_ptr() if gain is not None else 0, bt[0], bt[1])
 
 
 def make_linattn_args(q, k, v, log_decay, state, out, *, n_seq, gain=None, skip=None, scale=None, cu=None, T=None,
                       prev=None, update_state=False, cache_idx=None, has_initial_state=None, err=None,
                       workspace=None, check_device=True) -> LinattnArgs:
     """Build cv_linattn_args (see linattn_prefill and linattn_step; q None: no tokens, prev alone)."""
-    import torch
-    ptr = _dev_ptr if check_device else (lambda t, n, required=True: None if t is None else t.data_ptr())
-    if state.dim() != 4 or state.dtype != torch.float32:
+    f32 = _f32 or _load_types()
+    ss, st = state.shape, state.stride()
+    if len(ss) != 4 or state.dtype is not f32:
         raise ValueError("state must be float32 [n_slots, n_heads, dk, dv]")
-    n_slots, H, dk, dv = state.shape
-    if (dv > 1 and state.stride(3) != 1) or (dk > 1 and state.stride(2) != dv):
+    n_slots, H, dk, dv = ss
+    if (dv > 1 and st[3] != 1) or (dk > 1 and st[2] != dv):
         raise ValueError("the [dk, dv] state of a head must be contiguous")
-    for t, name in ((cache_idx, "cache_idx"), (has_initial_state, "has_initial_state"), (err, "err")):
-        _need_int32(t, name, n=n_seq)
-    a = LinattnArgs(n_seq=n_seq, n_heads=H, dk=dk, dv=dv, n_slots=n_slots, state=ptr(state, "state"),
-                    state_slot_stride=state.stride(0), state_head_stride=state.stride(1),
-                    cache_idx=ptr(cache_idx, "cache_idx", False),
-                    has_initial_state=ptr(has_initial_state, "has_initial_state", False), err=ptr(err, "err", False),
-                    update_state=int(update_state), scale=float(dk ** -0.5 if scale is None else scale))
-    some = q if q is not None else prev.k
-    a.dtype = _dtype_code(some)
-    a.n_qk_heads = some.shape[-2]
+    first = q if q is not None else prev.k
+    nq = first.shape[-2]
+    tok, o, os = _NO_TOKENS, 0, (0, 0, 0)
     if q is not None:
-        a.tok = _linattn_tokens(q, k, v, log_decay, gain, cu, T, n_seq, ptr, "tokens")
-        if k.shape[-1] != dk or tuple(v.shape[-2:]) != (H, dv):
-            raise ValueError(f"heads of q|k [.., {k.shape[-1]}] and v {tuple(v.shape[-2:])} do not fit the state "
-                             f"{tuple(state.shape)}")
-        _need_shape(out, "out", v.shape)
-        if out.dtype != v.dtype or out.stride(-1) != 1:
-            raise ValueError("out needs the dtype of v and a unit innermost stride")
-        os = out.stride()
-        a.out = ptr(out, "out", out.numel() > 0)
-        a.out_seq_stride, a.out_tok_stride, a.out_head_stride = (0, os[0], os[1]) if cu is not None else os[:3]
+        tok = _linattn_tokens(q, k, v, log_decay, gain, cu, T, n_seq, check_device, "tokens")
+        if q.shape[-1] != dk or v.shape[-2] != H or v.shape[-1] != dv:
+            raise ValueError(f"heads of q|k [.., {q.shape[-1]}] and v {tuple(v.shape[-2:])} do not fit the state {tuple(ss)}")
+        if out.shape != v.shape or out.dtype is not v.dtype or out.stride(-1) != 1:
+            raise ValueError("out needs the shape and dtype of v and a unit innermost stride")
+        o, os = _pointer(out, "out", check_device), out.stride()
+        os = (0, os[0], os[1]) if cu is not None else os
+    sk = 0
     if skip is not None:
         _need_shape(skip, "skip", (H,))
-        if skip.dtype != torch.float32 or not skip.is_contiguous():
+        if skip.dtype is not f32 or not skip.is_contiguous():
             raise ValueError("skip must be contiguous float32")
-        a.skip = ptr(skip, "skip")
+        sk = _pointer(skip, "skip", check_device)
+    old, accept = _NO_TOKENS, 0
     if prev is not None:
-        a.prev = _linattn_tokens(None, prev.k, prev.v, prev.log_decay, prev.gain, prev.cu_draft, prev.T, n_seq, ptr,
-                                 "previous drafts")
-        if prev.k.dtype != some.dtype or prev.k.shape[-2:] != (a.n_qk_heads, dk) or prev.v.shape[-2:] != (H, dv):
+        pk, pv = prev.k, prev.v
+        old = _linattn_tokens(None, pk, pv, prev.log_decay, prev.gain, prev.cu_draft, prev.T, n_seq, check_device,
+                              "previous drafts")
+        if pk.dtype is not first.dtype or pk.shape[-2] != nq or pk.shape[-1] != dk or pv.shape[-2] != H or pv.shape[-1] != dv:
             raise ValueError("the previous drafts must have the dtype, heads and head sizes of the tokens")
-        _need_int32(prev.accept_len, "accept_len", n=n_seq)
-        a.accept_len = ptr(prev.accept_len, "accept_len")
+        if prev.accept_len is None:
+            raise ValueError("accept_len is required")
+        accept = _index_array(prev.accept_len, "accept_len", n_seq, check_device)
+    ws, ws_bytes = 0, 0
     if workspace is not None:
-        a.workspace, a.workspace_bytes = ptr(workspace, "workspace"), workspace.numel() * workspace.element_size()
-    return a
+        ws, ws_bytes = _pointer(workspace, "workspace", check_device), workspace.numel() * workspace.element_size()
+    return LinattnArgs.from_buffer_copy(_LINATTN.pack(
+        n_seq, H, nq, dk, dv, BF16 if first.dtype is _bf16 else _dtype_code(first), dk ** -0.5 if scale is None else scale, n_slots, *tok, sk, o, os[0], os[1],
+        os[2], _pointer(state, "state", check_device), st[0], st[1], _index_array(cache_idx, "cache_idx", n_seq, check_device),
+        _index_array(has_initial_state, "has_initial_state", n_seq, check_device),
+        _index_array(err, "err", n_seq, check_device), *old, accept, 1 if update_state else 0, 0, ws, ws_bytes))
 
 
 def linattn_workspace(q, k, v, log_decay, state, out, cu_seqlens, *, max_seqlen, **kw) -> int:
@@ -595,17 +646,18 @@ def linattn_prefill(q, k, v, log_decay, state, out, cu_seqlens, *, max_seqlen, g
     a = make_linattn_args(q, k, v, log_decay, state, out, n_seq=cu_seqlens.shape[0] - 1, gain=gain, skip=skip,
                           scale=scale, cu=cu_seqlens, T=max_seqlen, cache_idx=cache_idx,
                           has_initial_state=has_initial_state, err=err, workspace=workspace)
-    if workspace is None:
+    lib, on = load_library(), _stream_of(stream, q)
+    rc = lib.cv_linattn_prefill(ctypes.byref(a), on)
+    if rc == ERR_WORKSPACE and workspace is None:  # nothing was launched: this call needs one
+        import torch
+        if stream is not None and not isinstance(stream, torch.cuda.Stream):
+            raise ValueError("pass workspace with a raw stream handle")
         need = _linattn_workspace(a)
-        if need > 0:
-            import torch
-            if stream is not None and not isinstance(stream, torch.cuda.Stream):
-                raise ValueError("pass workspace with a raw stream handle")
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-            if stream is not None:
-                workspace.record_stream(stream)
-            a.workspace, a.workspace_bytes = workspace.data_ptr(), need
-    rc = load_library().cv_linattn_prefill(ctypes.byref(a), _stream_ptr(stream))
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        if stream is not None:
+            workspace.record_stream(stream)
+        a.workspace, a.workspace_bytes = workspace.data_ptr(), need
+        rc = lib.cv_linattn_prefill(ctypes.byref(a), on)
     if rc != 0:
         raise CvError(rc, "cv_linattn_prefill")
 
@@ -623,7 +675,7 @@ def linattn_step(q, k, v, log_decay, state, out, *, gain=None, skip=None, scale=
     a = make_linattn_args(q, k, v, log_decay, state, out, n_seq=n_seq, gain=gain, skip=skip, scale=scale, cu=cu_draft,
                           T=T, prev=prev, update_state=update_state, cache_idx=cache_idx,
                           has_initial_state=has_initial_state, err=err)
-    rc = load_library().cv_linattn_step(ctypes.byref(a), _stream_ptr(stream))
+    rc = load_library().cv_linattn_step(ctypes.byref(a), _stream_of(stream, q))
     if rc != 0:
         raise CvError(rc, "cv_linattn_step")
 
@@ -634,7 +686,7 @@ def linattn_commit(drafts: LinattnDrafts, state, *, cache_idx=None, has_initial_
     n_seq = drafts.accept_len.shape[0]
     a = make_linattn_args(None, None, None, None, state, None, n_seq=n_seq, prev=drafts, cache_idx=cache_idx,
                           has_initial_state=has_initial_state, err=err)
-    rc = load_library().cv_linattn_step(ctypes.byref(a), _stream_ptr(stream))
+    rc = load_library().cv_linattn_step(ctypes.byref(a), _stream_of(stream, state))
     if rc != 0:
         raise CvError(rc, "cv_linattn_step")
 
@@ -643,43 +695,47 @@ def make_norm_args(y, out, *, gate=None, gate_act=None, gate_first=False, group=
                    residual_out=None, scale=1.0, channel_scale=None, pre_weight=None, eps=1e-6,
                    check_device=True) -> NormArgs:
     """Build cv_norm_args (see block_norm)."""
-    ptr = _dev_ptr if check_device else (lambda t, n, required=True: None if t is None else t.data_ptr())
-    if y.dim() != 2:
+    shape = y.shape
+    if len(shape) != 2:
         raise ValueError("y must be [rows, dim]")
-    rows, dim = y.shape
-    act = {"silu": 0, "sigmoid": 1}.get(gate_act or "silu")
+    rows, dim = shape
+    dt = y.dtype
+    f32 = _f32 or _load_types()
+    act = 0 if gate_act in (None, "silu") else 1 if gate_act == "sigmoid" else None
     if act is None:
         raise ValueError(f"unknown gate activation {gate_act!r}")
-    for t, name in ((gate, "gate"), (out, "out"), (residual, "residual"), (residual_out, "residual_out")):
-        if t is not None:
-            _need_shape(t, name, (rows, dim))
-            if t.stride(1) != 1 and dim > 1:
-                raise ValueError(f"{name} needs a unit channel stride")
-    if y.stride(1) != 1 and dim > 1:
-        raise ValueError("y needs a unit channel stride")
-    for t, name, n in ((post_weight, "post_weight", group), (channel_scale, "channel_scale", dim),
-                       (pre_weight, "pre_weight", dim)):
-        if t is not None:
-            _need_shape(t, name, (n,))
-            if t.dtype != y.dtype or not t.is_contiguous():
-                raise ValueError(f"{name} must be contiguous and have the dtype of y")
-    for t in (gate, out):
-        if t is not None and t.dtype != y.dtype:
+
+    def row(t, name, like):  # pointer and row stride
+        if t is None:
+            return 0, 0
+        if t.shape != shape:
+            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+        st = t.stride()
+        if st[1] != 1 and dim > 1:
+            raise ValueError(f"{name} needs a unit channel stride")
+        if like and t.dtype is not dt:
             raise TypeError("y, gate and out must share one dtype")
+        return _pointer(t, name, check_device), st[0]
+
+    def vec(t, name, n):
+        if t is None:
+            return 0
+        if t.dim() != 1 or t.shape[0] != n or t.dtype is not dt or not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous [{n}] and have the dtype of y")
+        return _pointer(t, name, check_device)
+
     if residual is None:
         if out is None or residual_out is not None or channel_scale is not None or pre_weight is not None:
             raise ValueError("without a residual, out is required and residual_out, channel_scale and pre_weight "
                              "have no meaning")
-    elif residual_out is None or residual_out.dtype != residual.dtype:
+    elif residual_out is None or residual_out.dtype is not residual.dtype:
         raise ValueError("residual needs residual_out of its dtype")
-    dt = _dtype_code(y)
-    return NormArgs(
-        rows, dim, group, dt, dt if residual is None else _dtype_code(residual), act, int(gate_first), eps, scale,
-        ptr(y, "y"), y.stride(0), ptr(gate, "gate", False), gate.stride(0) if gate is not None else 0,
-        ptr(post_weight, "post_weight", False), ptr(residual, "residual", False),
-        residual.stride(0) if residual is not None else 0, ptr(residual_out, "residual_out", False),
-        residual_out.stride(0) if residual_out is not None else 0, ptr(channel_scale, "channel_scale", False),
-        ptr(pre_weight, "pre_weight", False), ptr(out, "out", False), out.stride(0) if out is not None else 0)
+    code = BF16 if dt is _bf16 else _dtype_code(y)
+    return NormArgs.from_buffer_copy(_NORM.pack(
+        rows, dim, group, code, code if residual is None else F32 if residual.dtype is f32 else _dtype_code(residual), act, 1 if gate_first else 0, eps, scale,
+        *row(y, "y", True), *row(gate, "gate", True), vec(post_weight, "post_weight", group),
+        *row(residual, "residual", False), *row(residual_out, "residual_out", False),
+        vec(channel_scale, "channel_scale", dim), vec(pre_weight, "pre_weight", dim), *row(out, "out", True)))
 
 
 def block_norm(y, out, *, gate=None, gate_act=None, gate_first=False, group=0, post_weight=None, residual=None,
@@ -695,6 +751,6 @@ def block_norm(y, out, *, gate=None, gate_act=None, gate_first=False, group=0, p
     a = make_norm_args(y, out, gate=gate, gate_act=gate_act, gate_first=gate_first, group=group,
                        post_weight=post_weight, residual=residual, residual_out=residual_out, scale=scale,
                        channel_scale=channel_scale, pre_weight=pre_weight, eps=eps)
-    rc = load_library().cv_block_norm(ctypes.byref(a), _stream_ptr(stream))
+    rc = load_library().cv_block_norm(ctypes.byref(a), _stream_of(stream, y))
     if rc != 0:
         raise CvError(rc, "cv_block_norm")
