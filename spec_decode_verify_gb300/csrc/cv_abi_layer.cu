@@ -121,25 +121,76 @@ cvk::LinattnParams make_linattn(const cv_linattn_args *a, bool step) {
     return p;
 }
 
-int launch_recurrent(const cv_linattn_args *a, bool step, cudaStream_t stream) {
-    cvk::LinattnParams p = make_linattn(a, step);
+constexpr int kMinPieceTokens = 32;  // of a prompt cut for the recurrent kernel
+constexpr int kMaxPieces = 64;
+
+// The recurrent kernel's launch.
+struct StepPlan {
+    bool stream;  // the streaming kernel
+    int vs, slices, tg, pieces, piece_len;
+    long long units, resident;
+};
+int64_t step_workspace(const cv_linattn_args *a, const StepPlan &pl) {
+    const int64_t states = (int64_t)a->n_seq * a->n_heads * (pl.pieces - 1);
+    return states * a->dk * a->dv * 4 + (states * 4 + 255) / 256 * 256;
+}
+
+StepPlan plan_step(const cv_linattn_args *a, const cvk::LinattnParams &p, bool step) {
+    StepPlan pl;
     const long long heads = (long long)a->n_seq * a->n_heads, sms = device_limits().sms;
     const int most = step && a->prev.T > a->tok.T ? a->prev.T : a->tok.T;
-    const bool stream_ok = p.st_vec && a->dk <= 128 && (run_empty(a->tok) || p.tok.vec16) && (!step || run_empty(a->prev) || p.prev.vec16);
+    pl.stream = p.st_vec && a->dk <= 128 && (run_empty(a->tok) || p.tok.vec16) &&
+                (!step || run_empty(a->prev) || p.prev.vec16);
+    pl.tg = most <= 1 ? 1 : cvk::kStepMaxGroup;
+    pl.pieces = 1, pl.piece_len = 0;
+    pl.vs = pl.stream ? 128 : 64;
+    while (pl.vs > 32 && pl.vs / 2 >= a->dv) pl.vs /= 2;
+    // Few heads and long prompts: the length is cut into pieces that fill the resident blocks.  A cut costs a
+    // pass for the pieces' own states and their join, so two pieces are not worth it.
+    const int64_t longest = a->tok.T < a->tok.total_tokens ? a->tok.T : a->tok.total_tokens;
+    if (!step && pl.stream) {
+        const int64_t slots = sms * (256 / pl.vs) / (heads * ((a->dv + pl.vs - 1) / pl.vs));
+        int64_t len = slots > 0 ? (longest + slots - 1) / slots : longest;
+        if (len < kMinPieceTokens) len = kMinPieceTokens;
+        if (len < (longest + kMaxPieces - 1) / kMaxPieces) len = (longest + kMaxPieces - 1) / kMaxPieces;
+        len = (len + cvk::kStepMaxGroup - 1) / cvk::kStepMaxGroup * cvk::kStepMaxGroup;
+        const int64_t n = (longest + len - 1) / len;
+        if (n > 2) pl.pieces = (int)n, pl.piece_len = (int)len;
+    }
     // the widest slice of a head whose grid still gives every SM two blocks
-    int vs = stream_ok ? 128 : 64;
-    while (vs > 32 && (vs / 2 >= a->dv || heads * ((a->dv + vs - 1) / vs) < 2 * sms)) vs /= 2;
-    p.slices = (a->dv + vs - 1) / vs;
-    const long long units = heads * p.slices;
-    const int tg = most <= 1 ? 1 : cvk::kStepMaxGroup;
-    const cvk::StepKernel k = stream_ok ? cvk::stream_kernel(vs / 16, a->dk, tg, p.bf16) : cvk::step_kernel(vs, a->dk, tg);
+    while (pl.vs > 32 && heads * pl.pieces * ((a->dv + pl.vs - 1) / pl.vs) < 2 * sms) pl.vs /= 2;
+    pl.slices = (a->dv + pl.vs - 1) / pl.vs;
+    pl.units = heads * pl.pieces * pl.slices;
+    pl.resident = sms * (256 / pl.vs);  // the streaming kernel's registers allow 16 warps per SM
+    return pl;
+}
+
+int launch_recurrent(const cv_linattn_args *a, bool step, cudaStream_t stream) {
+    cvk::LinattnParams p = make_linattn(a, step);
+    const StepPlan pl = plan_step(a, p, step);
+    if (pl.units > 0x7fffffff) return CV_ERR_SHAPE;
+    p.slices = pl.slices, p.pieces = pl.pieces, p.piece_len = pl.piece_len;
+    const cvk::StepKernel k = pl.stream ? cvk::stream_kernel(pl.vs / 16, a->dk, pl.tg, p.bf16)
+                                        : cvk::step_kernel(pl.vs, a->dk, pl.tg);
     if (cvk::ensure_smem(reinterpret_cast<const void *>(k.fn), k.smem_bytes) != cudaSuccess) return CV_ERR_LAUNCH;
-    // resident blocks of the streaming kernel: its registers allow 16 warps per SM
-    const long long resident = sms * (256 / vs);
-    const int threads = stream_ok ? 2 * vs : cvk::kStepThreads;
-    if (launch_pdl(k.fn, dim3((unsigned)(stream_ok && units > resident ? resident : units)), dim3(threads), k.smem_bytes,
-                   stream, p) != cudaSuccess)
-        return CV_ERR_LAUNCH;
+    const dim3 grid((unsigned)(pl.stream && pl.units > pl.resident ? pl.resident : pl.units));
+    const dim3 block(pl.stream ? 2 * pl.vs : cvk::kStepThreads);
+    if (pl.pieces > 1) {
+        if (!a->workspace || !aligned(a->workspace, 256) || a->workspace_bytes < step_workspace(a, pl))
+            return CV_ERR_WORKSPACE;
+        const int64_t states = (int64_t)a->n_seq * a->n_heads;
+        p.ws_state = reinterpret_cast<float *>(a->workspace);
+        p.ws_decay = p.ws_state + states * (pl.pieces - 1) * a->dk * a->dv;
+        cvk::LinattnParams own = p;  // the tokens as a run to advance over, from zero
+        own.prev = p.tok, own.tok.T = 0, own.tok.cu = nullptr, own.accept = nullptr;
+        own.own_states = 1, own.update = 0;
+        if (launch_pdl(k.fn, grid, block, k.smem_bytes, stream, own) != cudaSuccess) return CV_ERR_LAUNCH;
+        const int64_t parts = ((int64_t)a->dk * a->dv + cvk::kStateJoinThreads - 1) / cvk::kStateJoinThreads;
+        if (launch_pdl(cvk::state_join_kernel(), dim3((unsigned)(states * parts)), dim3(cvk::kStateJoinThreads), 0, stream,
+                       p) != cudaSuccess)
+            return CV_ERR_LAUNCH;
+    }
+    if (launch_pdl(k.fn, grid, block, k.smem_bytes, stream, p) != cudaSuccess) return CV_ERR_LAUNCH;
     return cudaGetLastError() == cudaSuccess ? CV_OK : CV_ERR_LAUNCH;
 }
 
@@ -371,7 +422,10 @@ int cv_linattn_workspace(const cv_linattn_args *args, int64_t *bytes) {
     if (!bytes) return CV_ERR_NULL_POINTER;
     const int rc = check_linattn(args, false, false);
     if (rc != CV_OK) return rc;
-    *bytes = args->n_seq > 0 ? chunk_workspace(plan_chunks(args)) : 0;
+    *bytes = 0;
+    if (args->n_seq == 0) return CV_OK;
+    const ChunkPlan pl = plan_chunks(args);
+    *bytes = pl.pieces > 0 ? chunk_workspace(pl) : step_workspace(args, plan_step(args, make_linattn(args, false), false));
     return CV_OK;
 }
 

@@ -39,6 +39,11 @@ struct LinattnParams {
     int o_vec;   // out allows 4 elements at once at multiples of 4 (checked on the host)
     int st_vec;  // state rows allow 16-byte accesses (checked on the host)
     int slices;  // column slices of a head's state, one block each
+    // long prompts of few heads: pieces a sequence is cut into (1: whole), their length in tokens, and whether
+    // this launch makes the pieces' own states (and decays) instead of outputs
+    int pieces, piece_len, own_states;
+    float *ws_state;  // [sequence][head][pieces - 1][dk][dv]
+    float *ws_decay;  // [sequence][head][pieces - 1]
     float scale;
 };
 
@@ -63,13 +68,19 @@ StepKernel step_kernel(int vs, int dk, int tg);
 // Rows aligned to 16 bytes; blocks of 2, 4 or 8 warps of 16 columns each; dk <= 128; tg: 1 or kStepMaxGroup.
 StepKernel stream_kernel(int warps, int dk, int tg, bool bf16);
 
+// Turns the pieces' own states into the states the next pieces start from.
+LinattnKernel state_join_kernel();
+constexpr int kStateJoinThreads = 128;
+
 // Shared memory of linattn_stream, in bytes from its start: the state tile, two buffers of raw rows (k, q
 // and v of TG tokens, each row 16 bytes longer than it is to spread the banks; decays, gains), the products
 // of the group's tokens, and the units at hand.
 struct StepUnit {
-    int s, h, slice;
-    int slot, n_tok, row0, n_prev, prow0, status;
-    bool on, init;
+    int s, h, slice, piece;
+    int n_tok, row0, n_prev, prow0, status;
+    bool on, init, update;
+    const float *from;  // the head's state before the unit (init), and after it
+    float *to;
 };
 struct StreamLayout {
     int raw, raw_bytes, products, ring, bytes;
@@ -78,7 +89,7 @@ struct StreamLayout {
         : raw(R * warps * 32 * 16),
           raw_bytes(TG * (2 * row_bytes(8 * R, bf16) + row_bytes(16 * warps, bf16)) + (TG * 8 + 15) / 16 * 16),
           products(raw + 2 * raw_bytes),
-          ring(products + TG * TG * 4),
+          ring((products + TG * TG * 4 + 7) / 8 * 8),
           bytes(ring + 4 * (int)sizeof(StepUnit)) {}
 };
 

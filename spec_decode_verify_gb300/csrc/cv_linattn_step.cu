@@ -346,43 +346,62 @@ __global__ void __launch_bounds__(kStepThreads, 2) linattn_stream(const __grid_c
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rg = lane >> 2, quad = lane & 3, vc = warp * 16 + quad * 4;  // vc: column within the unit
-    const unsigned total = (unsigned)p.n_seq * (unsigned)(p.n_heads * p.slices);
+    const unsigned total = (unsigned)p.n_seq * (unsigned)(p.pieces * p.n_heads * p.slices);
     grid_dep_wait();
     grid_dep_launch();
 
     auto unit_of = [&](unsigned idx) {
         StepUnit u;
         u.on = idx < total;
-        u.slot = -1, u.n_tok = u.n_prev = u.row0 = u.prow0 = u.status = u.s = u.h = u.slice = 0;
-        u.init = true;
+        u.n_tok = u.n_prev = u.row0 = u.prow0 = u.status = u.s = u.h = u.slice = u.piece = 0;
+        u.init = true, u.update = p.update;
+        u.from = u.to = p.state;
         if (!u.on) return u;
         u.slice = (int)(idx % (unsigned)p.slices);
-        const unsigned unit = idx / (unsigned)p.slices;
-        u.h = (int)(unit % (unsigned)p.n_heads), u.s = (int)(unit / (unsigned)p.n_heads);
-        u.slot = p.cache_idx ? __ldg(p.cache_idx + u.s) : u.s;
+        unsigned unit = idx / (unsigned)p.slices;
+        u.h = (int)(unit % (unsigned)p.n_heads);
+        unit /= (unsigned)p.n_heads;
+        u.piece = (int)(unit % (unsigned)p.pieces), u.s = (int)(unit / (unsigned)p.pieces);
+        const int slot = p.cache_idx ? __ldg(p.cache_idx + u.s) : u.s;
         u.n_tok = p.tok.T, u.n_prev = p.prev.T;
-        if (u.slot >= p.n_slots) u.status |= 1;
+        if (slot >= p.n_slots) u.status |= 1;
         if (p.tok.cu) u.status |= draft_span(p.tok.cu, u.s, p.tok.T, p.tok.total, u.n_tok, u.row0);
         if (p.prev.T > 0) {
             if (p.prev.cu) u.status |= draft_span(p.prev.cu, u.s, p.prev.T, p.prev.total, u.n_prev, u.prow0);
-            const int a = __ldg(p.accept + u.s);
-            if (a < 0 || a > u.n_prev) u.status |= 4;
-            u.n_prev = a;
+            if (p.accept) {
+                const int a = __ldg(p.accept + u.s);
+                if (a < 0 || a > u.n_prev) u.status |= 4;
+                u.n_prev = a;
+            }
         }
         if (p.has_init) u.init = __ldg(p.has_init + u.s) != 0;
-        if (u.slot < 0) u.status = 0;
-        u.on = u.slot >= 0 && u.status == 0;
+        if (slot < 0) u.status = 0;
+        u.on = slot >= 0 && u.status == 0;
+        if (!u.on) return u;
+        u.from = u.to = p.state + (long long)slot * p.st_slot + (long long)u.h * p.st_head;
+        if (p.pieces > 1) {
+            // in a launch for the pieces' own states the tokens are the run `prev`, from zero
+            int &n = p.own_states ? u.n_prev : u.n_tok, &row = p.own_states ? u.prow0 : u.row0;
+            const long long start = (long long)u.piece * p.piece_len;
+            const bool last = start + p.piece_len >= n;
+            u.on = u.piece == 0 || start < n;
+            if (p.own_states && last) u.on = false;
+            float *const ws = p.ws_state + (((long long)u.s * p.n_heads + u.h) * (p.pieces - 1) + u.piece) * p.dk * p.dv;
+            n = u.on ? min(p.piece_len, n - (int)start) : 0;
+            row += u.on ? (int)start : 0;
+            if (p.own_states) u.init = false, u.to = ws;
+            else if (u.piece > 0) u.init = true, u.from = ws - (long long)p.dk * p.dv;
+            if (!last) u.update = p.own_states;
+        }
         return u;
     };
     auto groups_of = [](const StepUnit &u) {
         return u.on ? (u.n_prev + TG - 1) / TG + (u.n_tok + TG - 1) / TG : 0;
     };
-    // this lane's first state word of the unit (row rg * R)
-    auto state_at = [&](const StepUnit &u) {
-        return p.state + (long long)u.slot * p.st_slot + (long long)u.h * p.st_head + u.slice * VS + vc + rg * R * p.dv;
-    };
+    // from a head's state to this lane's first word of it (row rg * R)
+    auto lane_of = [&](const StepUnit &u) { return u.slice * VS + vc + rg * R * p.dv; };
     auto fetch_state = [&](const StepUnit &u) {
-        const float *st = state_at(u);
+        const float *st = u.from + lane_of(u);
         const bool col = u.init && u.slice * VS + vc < p.dv;
         const uint32_t dst = smem_u32(tile + tid);
 #pragma unroll
@@ -435,12 +454,12 @@ __global__ void __launch_bounds__(kStepThreads, 2) linattn_stream(const __grid_c
         __syncthreads();
         const StepUnit &cur = ring[turn & 3], &nxt = ring[(turn + 1) & 3];
         if (tid == nt - 1) ring[(turn + 2) & 3] = unit_of(idx + 2 * gridDim.x);
-        if (p.err && cur.h == 0 && cur.slice == 0 && tid == 0) p.err[cur.s] = cur.status;
+        if (p.err && cur.h == 0 && cur.slice == 0 && cur.piece == 0 && !p.own_states && tid == 0) p.err[cur.s] = cur.status;
         f2 S[RP][kTileWords];
         const int gp = (cur.n_prev + TG - 1) / TG, ng = groups_of(cur);
         const bool col = cur.slice * VS + vc < p.dv;
         auto store_state = [&]() {
-            float *st = state_at(cur);
+            float *st = cur.to + lane_of(cur);
 #pragma unroll
             for (int m = 0; m < RP; ++m) {
                 float4 w[2];
@@ -461,9 +480,10 @@ __global__ void __launch_bounds__(kStepThreads, 2) linattn_stream(const __grid_c
                 S[m][2] = f2_pack(w.z, x.z), S[m][3] = f2_pack(w.w, x.w);
             }
             // a new sequence without accepted drafts: its zeros, unless its tokens' state is written below
-            if (gp == 0 && !cur.init && (p.update ? cur.n_tok == 0 : p.prev.T > 0)) store_state();
+            if (gp == 0 && !cur.init && (cur.update ? cur.n_tok == 0 : p.prev.T > 0)) store_state();
         }
         bool state_pending = false;  // the next unit's tile was committed after the next group's rows
+        float decay = 1.0f;          // of the previous drafts
         for (int g = 0; g < ng; ++g) {
             if (g > 0) {
                 if (state_pending)
@@ -532,7 +552,8 @@ __global__ void __launch_bounds__(kStepThreads, 2) linattn_stream(const __grid_c
             };
             if (old) {
                 advance();
-                if (g + 1 == gp && !(p.update && cur.n_tok > 0)) store_state();
+                decay *= __shfl_sync(0xffffffffu, upto, TG - 1, TG);
+                if (g + 1 == gp && !(cur.update && cur.n_tok > 0)) store_state();
                 continue;
             }
             const unsigned char *const raw_q = raw + TG * PITCH;
@@ -638,9 +659,11 @@ __global__ void __launch_bounds__(kStepThreads, 2) linattn_stream(const __grid_c
                     *reinterpret_cast<float4 *>(reinterpret_cast<float *>(p.out) + at) = x;
                 }
             }
-            if (g + 1 < ng || p.update) advance();
-            if (g + 1 == ng && p.update) store_state();
+            if (g + 1 < ng || cur.update) advance();
+            if (g + 1 == ng && cur.update) store_state();
         }
+        if (p.own_states && cur.on && cur.slice == 0 && tid == 0)
+            p.ws_decay[((long long)cur.s * p.n_heads + cur.h) * (p.pieces - 1) + cur.piece] = decay;
         if (ng == 0) {  // no group: the next unit's loads set out here
             if (groups_of(nxt) > 0) fetch_group(nxt, 0, buf);
             if (nxt.on) fetch_state(nxt);
@@ -648,6 +671,34 @@ __global__ void __launch_bounds__(kStepThreads, 2) linattn_stream(const __grid_c
         }
     }
     copies_wait<0>();
+}
+
+// S_0 = the initial state; S_{i+1} = decay_i S_i + own_i, written over own_i.  One word a thread; the pieces
+// are read ahead 8 at a time, since only the sums depend on one another.
+__global__ void __launch_bounds__(kStateJoinThreads) state_join(const __grid_constant__ LinattnParams p) {
+    grid_dep_wait();
+    grid_dep_launch();
+    const int words = p.dk * p.dv, parts = (words + kStateJoinThreads - 1) / kStateJoinThreads;
+    const int e = (int)(blockIdx.x % (unsigned)parts) * kStateJoinThreads + threadIdx.x;
+    const int sh = (int)(blockIdx.x / (unsigned)parts), h = sh % p.n_heads, s = sh / p.n_heads;
+    const int slot = p.cache_idx ? __ldg(p.cache_idx + s) : s;
+    int L, row0;
+    if (slot < 0 || slot >= p.n_slots || draft_span(p.tok.cu, s, p.tok.T, p.tok.total, L, row0) || e >= words) return;
+    const int n = (L + p.piece_len - 1) / p.piece_len - 1;  // pieces with a next one
+    const bool init = p.has_init ? __ldg(p.has_init + s) != 0 : true;
+    float S = init && n > 0 ? p.state[(long long)slot * p.st_slot + (long long)h * p.st_head + e] : 0.0f;
+    const long long base = (long long)sh * (p.pieces - 1);
+    float *const own = p.ws_state + base * words + e;
+    const float *const dec = p.ws_decay + base;
+    for (int i0 = 0; i0 < n; i0 += 8) {
+        float f[8], d[8];
+#pragma unroll
+        for (int x = 0; x < 8; ++x)
+            if (i0 + x < n) f[x] = own[(long long)(i0 + x) * words], d[x] = dec[i0 + x];
+#pragma unroll
+        for (int x = 0; x < 8; ++x)
+            if (i0 + x < n) own[(long long)(i0 + x) * words] = S = fmaf(d[x], S, f[x]);
+    }
 }
 
 template <int VS, int R>
@@ -667,6 +718,7 @@ StepKernel step_kernel(int vs, int dk, int tg) {
     if (vs == 64) return dk <= 64 ? pick<64, 4>(tg) : dk <= 128 ? pick<64, 8>(tg) : pick<64, 16>(tg);
     return dk <= 64 ? pick<32, 2>(tg) : dk <= 128 ? pick<32, 4>(tg) : pick<32, 8>(tg);
 }
+LinattnKernel state_join_kernel() { return state_join; }
 StepKernel stream_kernel(int warps, int dk, int tg, bool bf16) {
     if (dk <= 64) return tg == 1 ? pick_stream<8, 1>(warps, bf16) : pick_stream<8, kStepMaxGroup>(warps, bf16);
     return tg == 1 ? pick_stream<16, 1>(warps, bf16) : pick_stream<16, kStepMaxGroup>(warps, bf16);

@@ -347,6 +347,27 @@ def test_prefill_long_prompts_split_over_their_length(cuda_lib, counts, nq, nh):
     c.check(c.prefill(cuda_lib), True, chunked=True)
 
 
+@pytest.mark.parametrize("dtype,counts,nq,nh,dk,dv", [
+    ("f32", [900], 1, 1, 64, 64), ("f32", [1, 333, 600, 0], 1, 2, 128, 32), ("f32", [97, 98], 2, 2, 20, 128),
+    ("f32", [2000], 1, 3, 128, 128), ("bf16", [500, 77], 1, 1, 128, 136)])
+def test_prefill_recurrent_prompts_split_over_their_length(cuda_lib, dtype, counts, nq, nh, dk, dv):
+    """Prompts the chunked kernel does not take, cut into pieces; slow decays make every piece matter."""
+    c = Case(len(counts), nq, nh, dk, dv, dtype, counts=counts, gain=True, seed=17, decay=0.003, no_init=(len(counts) - 1,))
+    c.check(c.prefill(cuda_lib), True)
+
+
+def test_prefill_own_workspace(cuda_lib):
+    """A caller's workspace of the reported size will do, a smaller one is refused before anything is launched."""
+    c = Case(1, 1, 2, 64, 64, "f32", counts=[700], seed=18)
+    d = c.device()
+    need = cuda_lib.linattn_workspace(d["q"], d["k"], d["v"], d["g"], d["state"], d["out"], d["cu"], max_seqlen=700)
+    assert need > 0
+    with pytest.raises(cuda_lib.CvError) as e:
+        c.prefill(cuda_lib, d, workspace=torch.empty(need - 256, dtype=torch.uint8, device="cuda"))
+    assert e.value.status == -13 and bool((d["out"] == SENT).all())
+    c.check(c.prefill(cuda_lib, d, workspace=torch.empty(need, dtype=torch.uint8, device="cuda")), True)
+
+
 def test_prefill_padded_and_bad_spans(cuda_lib):
     c = Case(5, 1, 2, 64, 64, "bf16", counts=[40, 150, 30, 200, 10], seed=3, pad_seqs=(1,))
     d = c.device()
