@@ -18,12 +18,12 @@
 //   state   4 warps, a row of S a thread: S from tensor memory, bf16 copy to shared memory, S times the
 //           chunk's decay back
 //   output  4 warps, a row a thread: out from Q S and A V, rounded, through the dead v tile to memory
-//   keys    8 warps, half a token a thread: K' in place of K (once Q K^T is done) and its low part
+//   keys    8 warps, half a token a thread: K' as a high and a low part from the k tile
 //   decays  1 warp: sums of the log decays and the weights made of them, ahead of the others
 //   load    2 threads: q, k, v tiles by TMA in the 128-byte swizzle, channels past the end zero
 //   issue   1 thread: all products, in the order Q K^T, Q S, K'^T V, A V
-// Shared memory: k and v in two stages, q, the low part of K' and the copy of S once (32 KB each at 128
-// channels); tensor memory: Q K^T (then A) 128 columns, Q S, A V and S dv columns each.  A chunk's products
+// Shared memory: v in two stages, k, q, both parts of K' and the copy of S once (32 KB each at 128 channels); tensor memory: Q K^T (then A) 128 columns, S and
+// two buffers of Q S + A V dv columns each.  A chunk's products
 // take 2560 cycles of the tensor pipe; the longest cycle through the roles is K'^T V -> S -> Q S.
 //
 // Every wait is bounded; one that gives up ends the block's work, flags the sequences it had left and
@@ -42,10 +42,12 @@ constexpr int kTileQK = kChunk * 256;  // bytes of a q or k tile: two blocks of 
 
 // Barriers, in order (8 bytes each), then the small arrays.
 struct ChunkShared {
-    uint64_t k_full[2], v_full[2], k_empty[2], v_empty[2];
-    uint64_t g_full[2], g_empty[2], key_empty, q_full, scores, a_ready, keys, q_used, s_init, s_ready, s_done, out, out_free, last;
+    uint64_t v_full[2], v_empty[2];
+    uint64_t g_full[2], g_empty[2], out[2], out_free[2];
+    uint64_t key_empty, k_full, k_empty, q_full, scores, a_ready, keys, q_used, s_init, s_ready, s_done, last;
     uint32_t tmem;
     int dead;
+    int apart[2];  // why the chunk's Q S and A V are kept apart: 1 it decays by more than 2^80, 2 its v holds a NaN or inf
     uint8_t order[kChunkMaxSorted];
     // Of a chunk: each token's sum of log2 decays up to it (over the chunk, or over its block of 32 where the
     // chunk decays by more than 2^80), its weight as a column of A, the blocks' sums, and its weight in K'.
@@ -56,9 +58,11 @@ struct ChunkShared {
     alignas(16) float key[kChunk];
 };
 
+static_assert(sizeof(ChunkShared) <= 3072, "what 227 KB leave beside the tiles");
+
 template <int DV>
 __host__ __device__ constexpr int chunk_smem_bytes() {
-    return 2 * (kTileQK + kChunk * DV * 2) + 2 * kTileQK + kChunk * DV * 2 + (int)sizeof(ChunkShared);
+    return 4 * kTileQK + 3 * kChunk * DV * 2 + (int)sizeof(ChunkShared);
 }
 
 struct Unit {
@@ -90,8 +94,10 @@ __device__ __forceinline__ Unit unit_of(const LinattnChunkParams &p, const Chunk
     return u;
 }
 
-// The block's n-th unit (-1: none).  Sorted units go out forwards and backwards in turn, so a block that
-// got a long one first gets a short one next.
+// The block's n-th unit: -1 none any more, -2 none this time.  Sorted units go out forwards and backwards in
+// turn, so a block that got a long one first gets a short one next.  (Packing them into the blocks by their
+// lengths, which leaves 4 % between the fullest block and the mean where this leaves 19 %, measured no faster:
+// 8 prompts of 1.5k-5.8k tokens, 48 heads, 333 us against 320.)
 __device__ __forceinline__ int unit_index(const LinattnChunkParams &p, int n) {
     const int G = gridDim.x, b = blockIdx.x;
     const long long idx = (long long)n * G + (p.sort && (n & 1) ? G - 1 - b : b);
@@ -108,8 +114,17 @@ __device__ __forceinline__ bool poll(uint64_t *bar, unsigned parity) {
         : "memory");
     return done != 0;
 }
-// Bounded wait of a whole warp; false once the block has given up.
-__device__ __forceinline__ bool wait_warp(uint64_t *bar, unsigned parity, volatile int *dead) {
+// Whether the phase is over, for the whole warp.
+__device__ __forceinline__ bool over(uint64_t *bar, unsigned parity) {
+    unsigned done;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(done)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return __all_sync(0xffffffffu, done != 0);
+}
+__device__ __noinline__ bool wait_long(uint64_t *bar, unsigned parity, volatile int *dead) {
 #pragma unroll 1
     for (unsigned i = 0; i < kPolls; ++i) {
         if (__all_sync(0xffffffffu, poll(bar, parity))) return true;
@@ -117,6 +132,10 @@ __device__ __forceinline__ bool wait_warp(uint64_t *bar, unsigned parity, volati
     }
     *dead = 1;
     return false;
+}
+// Bounded wait of a whole warp; false once the block has given up.
+__device__ __forceinline__ bool wait_warp(uint64_t *bar, unsigned parity, volatile int *dead) {
+    return over(bar, parity) || wait_long(bar, parity, dead);
 }
 __device__ __forceinline__ bool wait_one(uint64_t *bar, unsigned parity, volatile int *dead) {
 #pragma unroll 1
@@ -167,10 +186,6 @@ __device__ __noinline__ void row_long_way(const LinattnParams &a, int row0, int 
     }
 }
 
-// Either bf16 half is a NaN or an infinity.
-__device__ __forceinline__ bool not_finite(uint32_t w) {
-    return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
-}
 // Two elements of k times the weight, as a high and a low bf16 part.
 __device__ __forceinline__ void split(uint32_t k, f2 w2, f2 neg, uint32_t &hi, uint32_t &lo) {
     const f2 f = f2_mul(f2_pack(__uint_as_float(k << 16), __uint_as_float(k & 0xffff0000u)), w2);
@@ -246,10 +261,11 @@ __device__ __noinline__ void scores_strong(const LinattnParams &a, int row0, int
 template <int DV>
 __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_constant__ LinattnChunkParams p) {
     constexpr int kTileV = kChunk * DV * 2, kBlock = kChunk * 128;  // a tile's blocks of 64 channels
-    constexpr uint32_t kColP = 0, kColQS = 128, kColAV = 128 + DV, kColS = 128 + 2 * DV, kCols = 512;
+    constexpr uint32_t kColP = 0, kColO = 128, kColS = 128 + 2 * DV, kCols = 512;  // (two buffers of outputs)
     extern __shared__ __align__(1024) unsigned char smem[];
-    unsigned char *const k_tile = smem, *const v_tile = smem + 2 * kTileQK;  // stage s at + s * its size
-    unsigned char *const q_tile = v_tile + 2 * kTileV, *const lo_tile = q_tile + kTileQK, *const s_copy = lo_tile + kTileQK;
+    unsigned char *const k_tile = smem, *const hi_tile = k_tile + kTileQK, *const lo_tile = hi_tile + kTileQK;
+    unsigned char *const q_tile = lo_tile + kTileQK, *const v_tile = q_tile + kTileQK;  // v: stage s at + s * its size
+    unsigned char *const s_copy = v_tile + 2 * kTileV;
     ChunkShared *const sh = reinterpret_cast<ChunkShared *>(s_copy + kTileV);
     const LinattnParams &a = p.a;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -263,24 +279,24 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
     if (tid == 0) {
         sh->dead = 0;
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&sh->k_full[i], 1);
             mbar_init(&sh->v_full[i], 1);
-            mbar_init(&sh->k_empty[i], 1);
-            mbar_init(&sh->v_empty[i], 4);
+            mbar_init(&sh->v_empty[i], so ? 1 : 4);
+            mbar_init(&sh->out[i], 1);
+            mbar_init(&sh->out_free[i], 4);
             mbar_init(&sh->g_full[i], 1);
             mbar_init(&sh->g_empty[i], so ? 4 : 12);
         }
         mbar_init(&sh->key_empty, 8);
+        mbar_init(&sh->k_full, 1);
+        mbar_init(&sh->k_empty, so ? 8 : 9);
         mbar_init(&sh->q_full, 1);
         mbar_init(&sh->scores, 1);
-        mbar_init(&sh->a_ready, 4);
+        mbar_init(&sh->a_ready, 12);
         mbar_init(&sh->keys, 8);
         mbar_init(&sh->q_used, 1);
         mbar_init(&sh->s_init, 4);
         mbar_init(&sh->s_ready, 4);
         mbar_init(&sh->s_done, 1);
-        mbar_init(&sh->out, 1);
-        mbar_init(&sh->out_free, 4);
         mbar_init(&sh->last, 1);
         mbar_init_fence();
     }
@@ -363,7 +379,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
                 *reinterpret_cast<float4 *>(sh->G[stage] + 4 * lane) = make_float4(G[0], G[1], G[2], G[3]);
                 *reinterpret_cast<float4 *>(sh->col[stage] + 4 * lane) = make_float4(col[0], col[1], col[2], col[3]);
                 *reinterpret_cast<float4 *>(sh->key + 4 * lane) = make_float4(key[0], key[1], key[2], key[3]);
-                if (lane == 0) *reinterpret_cast<float4 *>(sh->tot[stage]) = make_float4(t0, t1, t2, t3);
+                if (lane == 0) {
+                    *reinterpret_cast<float4 *>(sh->tot[stage]) = make_float4(t0, t1, t2, t3);
+                    sh->apart[stage] = strong;
+                }
                 arrive_warp(&sh->g_full[stage]);
             }
         }
@@ -375,15 +394,15 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
             if (idx < 0) continue;
             const Unit u = unit_of(p, sh, idx);
             for (int c = 0; c < u.chunks; ++c, ++it) {
-                const int stage = it & 1, row = u.row0 + c * kChunk;
-                if (it >= 2 && !wait_one(&sh->k_empty[stage], ((it >> 1) & 1) ^ 1, dead)) {
+                const int row = u.row0 + c * kChunk;
+                if (it >= 1 && !wait_one(&sh->k_empty, (it - 1) & 1, dead)) {
                     ok = false;
                     break;
                 }
-                const uint32_t k = smem_u32(k_tile + stage * kTileQK);
-                mbar_arrive_expect_tx(&sh->k_full[stage], kTileQK);
-                tma_load(k, &p.k_map, 0, u.hq, row, &sh->k_full[stage]);
-                tma_load(k + kBlock, &p.k_map, 64, u.hq, row, &sh->k_full[stage]);
+                const uint32_t k = smem_u32(k_tile);
+                mbar_arrive_expect_tx(&sh->k_full, kTileQK);
+                tma_load(k, &p.k_map, 0, u.hq, row, &sh->k_full);
+                tma_load(k + kBlock, &p.k_map, 64, u.hq, row, &sh->k_full);
                 ++k_sent;
                 if (!so) {
                     if (it >= 1 && !wait_one(&sh->q_used, (it - 1) & 1, dead)) {
@@ -399,7 +418,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
             }
         }
         // nothing of the block's is in flight when it returns
-        for (int x = max(0, k_sent - 2); x < k_sent; ++x) mbar_wait_bounded(&sh->k_full[x & 1], (x >> 1) & 1, kPolls);
+        if (k_sent > 0) mbar_wait_bounded(&sh->k_full, (k_sent - 1) & 1, kPolls);
         if (q_sent > 0) mbar_wait_bounded(&sh->q_full, (q_sent - 1) & 1, kPolls);
     } else if (warp == 23 && lane == 0) {
         // --------------------------------------------------------------------------- load: v
@@ -410,7 +429,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
             const Unit u = unit_of(p, sh, idx);
             for (int c = 0; c < u.chunks; ++c, ++it) {
                 const int stage = it & 1, row = u.row0 + c * kChunk;
-                if (it >= 2 && !wait_one(so ? &sh->k_empty[stage] : &sh->v_empty[stage], ((it >> 1) & 1) ^ 1, dead)) {
+                if (it >= 2 && !wait_one(&sh->v_empty[stage], ((it >> 1) & 1) ^ 1, dead)) {
                     ok = false;
                     break;
                 }
@@ -646,76 +665,63 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
                     ok = false;
                     break;
                 }
-                // out = pre * (Q S) + post * (A V)
+                // out = pre * (Q S + A V), or pre * (Q S) + post * (A V) where they are kept apart
                 const float4 bt = *reinterpret_cast<const float4 *>(sh->tot[stage]);
-                float G = sh->G[stage][i], post = 1.0f;
+                float G = sh->G[stage][i];
                 const bool strong = !((bt.x + bt.y) + (bt.z + bt.w) > strong_at);
                 if (strong) G += (w4 > 0 ? bt.x : 0.0f) + (w4 > 1 ? bt.y : 0.0f) + (w4 > 2 ? bt.z : 0.0f);
-                arrive_warp(&sh->g_empty[stage]);
                 const float pre = exp2_fast(G) * a.scale;
-                if (!strong) post = pre;
-                const f2 pre2 = f2_pack(pre, pre), post2 = f2_pack(post, post);
-                if (!wait_warp(&sh->out, it & 1, dead)) {
+                if (!wait_warp(&sh->out[it & 1], (it >> 1) & 1, dead)) {
                     ok = false;
                     break;
                 }
                 tmem_fence_after();
+                const bool v_bad = *(volatile int *)&sh->apart[stage] & 2;
+                arrive_warp(&sh->g_empty[stage]);
                 const int t0 = c * kChunk;
                 unsigned char *const vt = v_tile + stage * kTileV;  // v is used up: the rows go through its tile
-                uint32_t x1[8], y1[8];
+                const uint32_t to = tl + kColO + (it & 1) * DV, ta = tl + kColO + (~it & 1) * DV;
+                if (!strong && !v_bad) {
+                    const f2 pre2 = f2_pack(pre, pre);
 #pragma unroll 2
-                for (int j = 0; j < DV; j += 16) {
-                    uint32_t x[16], y[16], o[8];
-                    tmem_ld16(x, tl + kColQS + j);
-                    tmem_ld16(y, tl + kColAV + j);
-                    tmem_wait_ld(x);
-                    tmem_wait_ld(y);
+                    for (int j = 0; j < DV; j += 16) {
+                        uint32_t x[16], o[8];
+                        tmem_ld16(x, to + j);
+                        tmem_wait_ld(x);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        float f0, f1;
-                        f2_unpack(f2_fma(pre2, f2_pack(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])),
-                                         f2_mul(post2, f2_pack(__uint_as_float(y[2 * e]), __uint_as_float(y[2 * e + 1])))),
-                                  f0, f1);
-                        o[e] = pack_bf16(f0, f1);
+                        for (int e = 0; e < 8; ++e) {
+                            float f0, f1;
+                            f2_unpack(f2_mul(pre2, f2_pack(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]))), f0, f1);
+                            o[e] = pack_bf16(f0, f1);
+                        }
+                        unsigned char *const at = vt + (j >> 6) * kBlock;
+                        *reinterpret_cast<uint4 *>(at + swizzled(i, (j >> 3) & 7)) = make_uint4(o[0], o[1], o[2], o[3]);
+                        *reinterpret_cast<uint4 *>(at + swizzled(i, ((j >> 3) & 7) + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
                     }
-                    unsigned char *const at = vt + (j >> 6) * kBlock;
-                    *reinterpret_cast<uint4 *>(at + swizzled(i, (j >> 3) & 7)) = make_uint4(o[0], o[1], o[2], o[3]);
-                    *reinterpret_cast<uint4 *>(at + swizzled(i, ((j >> 3) & 7) + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
+                } else {
+                    // a NaN or an infinity in v has spoiled its column in all rows of A V: the long way then
+                    const float post = strong ? 1.0f : pre;
+#pragma unroll 1
+                    for (int j = 0; j < DV; j += 8) {
+                        uint32_t x[8], y[8], o[4];
+                        float part[8];
+                        tmem_ld8x2(x, y, to + j, ta + j);
+                        tmem_wait_ld8x2(x, y);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) part[e] = post * __uint_as_float(y[e]);
+                        if (v_bad && t0 + i < u.n) row_long_way(a, u.row0 + t0, u.h, u.hq, i, j, part);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            o[e] = pack_bf16(fmaf(pre, __uint_as_float(x[2 * e]), part[2 * e]),
+                                             fmaf(pre, __uint_as_float(x[2 * e + 1]), part[2 * e + 1]));
+                        *reinterpret_cast<uint4 *>(vt + (j >> 6) * kBlock + swizzled(i, (j >> 3) & 7)) =
+                            make_uint4(o[0], o[1], o[2], o[3]);
+                        __syncwarp();
+                    }
                 }
                 __syncwarp();
-                // A NaN or an infinity in v spoils its column in every row of the chunk, so the warp's first row
-                // shows it.
-                {
-                    const uint4 f = *reinterpret_cast<const uint4 *>(vt + ((lane * 8 >> 6) & (DV / 64 - 1)) * kBlock +
-                                                                     swizzled(32 * w4, lane & 7));
-                    const bool bad = lane < DV / 8 && (not_finite(f.x) || not_finite(f.y) || not_finite(f.z) || not_finite(f.w));
-                    if (__any_sync(0xffffffffu, bad) && t0 + 32 * w4 < u.n) {
-                        bool found = false;
-                        for (int t = lane; t < min(kChunk, u.n - t0); t += 32) {
-                            const uint16_t *v = reinterpret_cast<const uint16_t *>(a.tok.v) +
-                                                (u.row0 + t0 + t) * a.tok.v_tok + (long long)u.h * a.tok.v_head;
-                            for (int e = 0; e < a.dv; ++e) found |= (v[e] & 0x7f80) == 0x7f80;
-                        }
-                        if (__any_sync(0xffffffffu, found))
-#pragma unroll 1
-                            for (int j = 0; j < DV; j += 8) {
-                                float part[8] = {};
-                                tmem_ld8x2(x1, y1, tl + kColQS + j, tl + kColAV + j);
-                                tmem_wait_ld8x2(x1, y1);
-                                if (t0 + i < u.n) row_long_way(a, u.row0 + t0, u.h, u.hq, i, j, part);
-                                uint32_t o[4];
-#pragma unroll
-                                for (int e = 0; e < 4; ++e)
-                                    o[e] = pack_bf16(fmaf(pre, __uint_as_float(x1[2 * e]), part[2 * e]),
-                                                     fmaf(pre, __uint_as_float(x1[2 * e + 1]), part[2 * e + 1]));
-                                *reinterpret_cast<uint4 *>(vt + (j >> 6) * kBlock + swizzled(i, (j >> 3) & 7)) =
-                                    make_uint4(o[0], o[1], o[2], o[3]);
-                                __syncwarp();
-                            }
-                    }
-                }
                 tmem_fence_before();
-                arrive_warp(&sh->out_free);
+                arrive_warp(&sh->out_free[it & 1]);
                 // whole rows from there to memory, DV * 2 contiguous bytes each
                 constexpr int PC = DV / 8, RP = 32 / PC;
                 const int pc = lane % PC, r0 = 32 * w4 + lane / PC;
@@ -746,25 +752,20 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
                 }
                 const float w = sh->key[t];
                 arrive_warp(&sh->key_empty);
-                // the low part's place is free once the last chunk's products are done (and this role never runs
-                // two phases ahead of the issue thread)
-                if (!wait_warp(&sh->k_full[stage], (it >> 1) & 1, dead) ||
-                    (it > 0 && !wait_warp(&sh->s_done, (it - 1) & 1, dead))) {
-                    ok = false;
-                    break;
-                }
-                if (!so && !wait_warp(&sh->scores, it & 1, dead)) {  // k is used up
+                // K' has its place once the last chunk's products are done (and this role never runs two phases
+                // ahead of the issuing warp)
+                if (!wait_warp(&sh->k_full, it & 1, dead) || (it > 0 && !wait_warp(&sh->s_done, (it - 1) & 1, dead))) {
                     ok = false;
                     break;
                 }
                 const f2 w2 = f2_pack(w, w), neg = f2_pack(-1.0f, -1.0f);
-                unsigned char *const kt = k_tile + stage * kTileQK + half * kBlock, *const lt = lo_tile + half * kBlock;
+                const int at = half * kBlock;
                 const bool in = t < u.n - c * kChunk;
 #pragma unroll 1
                 for (int x0 = 0; x0 < 8; x0 += 2) {
                     uint4 k[2], hi[2], lo[2];
 #pragma unroll
-                    for (int x = 0; x < 2; ++x) k[x] = *reinterpret_cast<const uint4 *>(kt + swizzled(t, x0 + x));
+                    for (int x = 0; x < 2; ++x) k[x] = *reinterpret_cast<const uint4 *>(k_tile + at + swizzled(t, x0 + x));
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
                         split(k[x].x, w2, neg, hi[x].x, lo[x].x);
@@ -773,77 +774,102 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
                         split(k[x].w, w2, neg, hi[x].w, lo[x].w);
                         // past the end the tile holds whatever follows the sequence there: zeros instead
                         if (!in) hi[x] = lo[x] = make_uint4(0u, 0u, 0u, 0u);
-                        *reinterpret_cast<uint4 *>(kt + swizzled(t, x0 + x)) = hi[x];
-                        *reinterpret_cast<uint4 *>(lt + swizzled(t, x0 + x)) = lo[x];
+                        *reinterpret_cast<uint4 *>(hi_tile + at + swizzled(t, x0 + x)) = hi[x];
+                        *reinterpret_cast<uint4 *>(lo_tile + at + swizzled(t, x0 + x)) = lo[x];
                     }
                 }
-                if (u.n - c * kChunk < kChunk && half * 64 < DV) {  // in v too
+                arrive_warp(&sh->k_empty);
+                unsigned char *const vt = v_tile + stage * kTileV + half * kBlock;
+                if (half * 64 < DV) {
                     if (!wait_warp(&sh->v_full[stage], (it >> 1) & 1, dead)) {
                         ok = false;
                         break;
                     }
-                    if (!in)
+                    if (!in)  // in v too
 #pragma unroll 1
-                        for (int x = 0; x < 8; ++x)
-                            *reinterpret_cast<uint4 *>(v_tile + stage * kTileV + half * kBlock + swizzled(t, x)) =
-                                make_uint4(0u, 0u, 0u, 0u);
+                        for (int x = 0; x < 8; ++x) *reinterpret_cast<uint4 *>(vt + swizzled(t, x)) = make_uint4(0u, 0u, 0u, 0u);
                 }
                 fence_smem_to_async();
                 arrive_warp(&sh->keys);
+                if (so) continue;
+                if (half * 64 < DV) {  // while the state's products run: is there a NaN or an infinity in v?
+                    uint32_t high = 0u;  // of exponents plus one: set where it is all ones
+#pragma unroll 2
+                    for (int x = 0; x < 8; ++x) {
+                        const uint4 w = *reinterpret_cast<const uint4 *>(vt + swizzled(t, x));
+                        high |= ((w.x & 0x7f807f80u) + 0x00800080u) | ((w.y & 0x7f807f80u) + 0x00800080u) |
+                                ((w.z & 0x7f807f80u) + 0x00800080u) | ((w.w & 0x7f807f80u) + 0x00800080u);
+                    }
+                    if (__any_sync(0xffffffffu, high & 0x80008000u) && lane == 0) atomicOr(&sh->apart[stage], 2);
+                }
+                // (an arrival before the last chunk's phase is over would count there)
+                if (it > 0 && !wait_warp(&sh->a_ready, (it - 1) & 1, dead)) {
+                    ok = false;
+                    break;
+                }
+                arrive_warp(&sh->a_ready);
             }
         }
     } else if (warp == 22) {
         // ----------------------------------------------------------------------------- issue
         const uint32_t lead = elect_lane();
-        const uint32_t q = desc_k(smem_u32(q_tile)), sc = desc_mn(smem_u32(s_copy), kBlock),
-                       lo = desc_mn(smem_u32(lo_tile), kBlock);
+        const uint32_t q = desc_k(smem_u32(q_tile)), kt = desc_k(smem_u32(k_tile)), sc = desc_mn(smem_u32(s_copy), kBlock),
+                       hi = desc_mn(smem_u32(hi_tile), kBlock), lo = desc_mn(smem_u32(lo_tile), kBlock);
         constexpr uint32_t id_qk = mma_desc(128, false, false), id_qs = mma_desc(DV, false, true),
                            id_kv = mma_desc(DV, true, true);
+        bool apart_before = false;
         bool ok = true;
         for (int n = 0, idx; ok && (idx = unit_index(p, n)) != -1; ++n) {
             if (idx < 0) continue;
             const int chunks = unit_of(p, sh, idx).chunks;
             for (int c = 0; c < chunks; ++c, ++it) {
                 const int stage = it & 1;
-                const uint32_t kt = smem_u32(k_tile + stage * kTileQK), k = desc_mn(kt, kBlock),
-                               v = desc_mn(smem_u32(v_tile + stage * kTileV), kBlock);
+                const uint32_t v = desc_mn(smem_u32(v_tile + stage * kTileV), kBlock);
                 ok = false;
                 if (!so) {
                     // the last chunk's A, under the scores, is used up by the products before these
-                    if (!wait_warp(&sh->k_full[stage], (it >> 1) & 1, dead) || !wait_warp(&sh->q_full, it & 1, dead)) break;
+                    if (!wait_warp(&sh->k_full, it & 1, dead) || !wait_warp(&sh->q_full, it & 1, dead)) break;
                     tmem_fence_after();
 #pragma unroll 1
                     for (int x = 0; x < 8; ++x) {
                         const uint32_t off = ((x >> 2) * kBlock + (x & 3) * 32) >> 4;
-                        mma_ss(lead, tm + kColP, q + off, desc_k(kt) + off, id_qk, x > 0);
+                        mma_ss(lead, tm + kColP, q + off, kt + off, id_qk, x > 0);
                     }
                     mma_commit(lead, &sh->scores);
+                    mma_commit(lead, &sh->k_empty);
                 }
                 if (!wait_warp(&sh->s_ready, it & 1, dead)) break;
+                // Q S and A V add up in one buffer, of two in turn; a chunk that keeps them apart takes both
+                const uint32_t mine = tm + kColO + (it & 1) * DV, other = tm + kColO + (~it & 1) * DV;
                 if (!so) {
-                    if (it > 0 && !wait_warp(&sh->out_free, (it - 1) & 1, dead)) break;
+                    if ((it > 1 && !wait_warp(&sh->out_free[it & 1], ((it >> 1) & 1) ^ 1, dead)) ||
+                        (apart_before && !wait_warp(&sh->out_free[~it & 1], ((it - 1) >> 1) & 1, dead)))
+                        break;
                     tmem_fence_after();
 #pragma unroll 1
                     for (int x = 0; x < 8; ++x)
-                        mma_ss(lead, tm + kColQS, q + (((x >> 2) * kBlock + (x & 3) * 32) >> 4), sc + x * 128, id_qs, x > 0);
+                        mma_ss(lead, mine, q + (((x >> 2) * kBlock + (x & 3) * 32) >> 4), sc + x * 128, id_qs, x > 0);
                     mma_commit(lead, &sh->q_used);
                 }
-                if (!wait_warp(&sh->v_full[stage], (it >> 1) & 1, dead) || !wait_warp(&sh->keys, it & 1, dead)) break;
+                if (!wait_warp(&sh->keys, it & 1, dead)) break;  // (these waited for v)
                 tmem_fence_after();
 #pragma unroll 1
                 for (int x = 0; x < 8; ++x) {
-                    mma_ss(lead, tm + kColS, k + x * 128, v + x * 128, id_kv, true);
+                    mma_ss(lead, tm + kColS, hi + x * 128, v + x * 128, id_kv, true);
                     mma_ss(lead, tm + kColS, lo + x * 128, v + x * 128, id_kv, true);
                 }
                 mma_commit(lead, &sh->s_done);
-                mma_commit(lead, &sh->k_empty[stage]);
+                if (so) mma_commit(lead, &sh->v_empty[stage]);
                 if (!so) {
                     if (!wait_warp(&sh->a_ready, it & 1, dead)) break;
+                    const bool apart = *(volatile int *)&sh->apart[stage] != 0;
+                    if (apart && it > 0 && !apart_before && !wait_warp(&sh->out_free[~it & 1], ((it - 1) >> 1) & 1, dead)) break;
                     tmem_fence_after();
 #pragma unroll 1
                     for (int x = 0; x < 8; ++x)
-                        mma_ts(lead, tm + kColAV, tm + kColP + x * 8, v + x * 128, id_qs, x > 0);
-                    mma_commit(lead, &sh->out);
+                        mma_ts(lead, apart ? other : mine, tm + kColP + x * 8, v + x * 128, id_qs, !apart || x > 0);
+                    mma_commit(lead, &sh->out[it & 1]);
+                    apart_before = apart;
                 }
                 ok = true;
             }

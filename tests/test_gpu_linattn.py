@@ -390,10 +390,18 @@ def test_prefill_equals_its_parts(cuda_lib):
     c.check(d, True, chunked=True)
 
 
-def test_prefill_repeats_bit_for_bit(cuda_lib):
-    c = Case(3, 1, 4, 128, 128, "bf16", counts=[700, 129, 1500], seed=21)
-    a, b = c.prefill(cuda_lib), c.prefill(cuda_lib)
-    assert torch.equal(a["out"], b["out"]) and torch.equal(a["state"], b["state"])
+@pytest.mark.parametrize("counts,nq,nh,dk,dv", [
+    ([700, 129, 1500], 1, 4, 128, 128),
+    ([(37 * i * i) % 2900 + 1 for i in range(30)], 2, 6, 64, 128),  # several units a block, of very different lengths
+    ([(53 * i * i) % 1700 for i in range(12)], 4, 24, 128, 64)])
+def test_prefill_repeats_bit_for_bit(cuda_lib, counts, nq, nh, dk, dv):
+    """The roles of the chunked kernel hand work on through barriers alone: a missed one shows as a difference."""
+    c = Case(len(counts), nq, nh, dk, dv, "bf16", counts=counts, seed=21, gain=True)
+    first = c.prefill(cuda_lib)
+    assert first["err"].tolist() == [0] * len(counts)
+    for _ in range(6):
+        d = c.prefill(cuda_lib)
+        assert torch.equal(d["out"], first["out"]) and torch.equal(d["state"], first["state"])
 
 
 def test_prefill_on_another_stream(cuda_lib):
