@@ -200,7 +200,10 @@ struct ChunkPlan {
     long long ws_states;  // pieces whose own states go through the workspace
     int dv_pad;
 };
-constexpr int kMinPieceChunks = 4;
+// Prompts of at most so many tokens go to the recurrent kernel, more where there are heads for every SM
+// (measured, 32 heads of 128, recurrent / chunked: 1 prompt of 8 tokens 7.6 / 9.1 us, of 16 11.3 / 9.2; 64 prompts
+// of 16 tokens 104 / 132 us, of 24 144 / 134).
+constexpr int kShortFew = 8, kShortMany = 16;
 constexpr int64_t kMaxStride = 1LL << 38;  // elements: a tensor map's strides are below 2^40 bytes
 
 // The driver's encoder of tensor maps, looked up once.
@@ -250,11 +253,13 @@ ChunkPlan plan_chunks(const cv_linattn_args *a) {
     const int64_t longest = t.T < t.total_tokens ? t.T : t.total_tokens;
     const int64_t whole = (longest + cvk::kChunk - 1) / cvk::kChunk * cvk::kChunk;
     const int64_t heads = (int64_t)a->n_seq * a->n_heads, sms = device_limits().sms;
+    if (longest <= (heads > sms ? kShortMany : kShortFew)) return pl;
     pl.pieces = 1;
     pl.seg_len = (int)(whole > 0 ? whole : cvk::kChunk);
     // Few heads: cut the length into pieces until every SM has one.  A cut costs a pass over k and v for
-    // the pieces' own states, so pieces are not short, and a grid that is mostly full stays uncut.
-    for (int64_t len = (int64_t)kMinPieceChunks * cvk::kChunk; len < whole; len += cvk::kChunk) {
+    // the pieces' own states and their join, and a grid that is mostly full stays uncut (measured, 4 heads of 2,000
+    // tokens: pieces of at least 4 / 2 / 1 chunks 32 / 24 / 21 us).
+    for (int64_t len = cvk::kChunk; len < whole; len += cvk::kChunk) {
         const int64_t n = (whole + len - 1) / len;
         int64_t most = a->n_seq * n;
         if (t.total_tokens / len + a->n_seq < most) most = t.total_tokens / len + a->n_seq;

@@ -427,6 +427,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
         for (int n = 0, idx; ok && (idx = unit_index(p, n)) != -1; ++n) {
             if (idx < 0) continue;
             const Unit u = unit_of(p, sh, idx);
+            // the unit's first state, into L2 before the state warps come to it
+            if (u.on && !so && (u.seg > 0 || u.init)) {
+                const float *const st =
+                    u.seg > 0 ? p.ws_state + (((long long)u.s * a.n_heads + u.h) * (p.n_segs - 1) + u.seg - 1) * (kChunk * DV)
+                              : a.state + (long long)u.slot * a.st_slot + (long long)u.h * a.st_head;
+                bulk_prefetch_l2(st, (unsigned)(u.seg > 0 ? kChunk * DV : a.dk * a.dv) * 4);
+            }
             for (int c = 0; c < u.chunks; ++c, ++it) {
                 const int stage = it & 1, row = u.row0 + c * kChunk;
                 if (it >= 2 && !wait_one(&sh->v_empty[stage], ((it >> 1) & 1) ^ 1, dead)) {
