@@ -19,7 +19,6 @@ using cvk::launch_pdl;
 constexpr int kMaxHeads = 4096;
 constexpr int kMaxHeadDim = 256;
 constexpr int kMaxNormDim = 65536;
-constexpr int kNormRowWide = 256;    // norm_row: threads a row while elements a thread allow it (many rows)
 constexpr int kNormGroupBlocks = 8;  // resident blocks of norm_groups per SM
 constexpr int kNormGroupGrid = 16;   // its blocks per SM, at most
 
@@ -352,6 +351,11 @@ bool vec_row(const void *p, int64_t stride, int64_t rows, int es, int bytes) {
     return !p || (aligned(p, bytes) && (rows <= 1 || (stride * es) % bytes == 0));
 }
 
+// norm_row, more than kNormRowMany rows an SM: threads a row while elements a thread allow it, so that several rows
+// share an SM (7324 rows of 8192, bf16: 99 us with 256 threads, 152 with 512; 300 rows of 4096: 4.9 against 3.8).
+constexpr int kNormRowWide = 256, kNormRowMany = 4;
+constexpr int kNormRowAhead = 16;  // rows an SM from which the next rows are prefetched
+
 int launch_norm(const cv_norm_args *a, cudaStream_t stream) {
     const int es = esize_of(a->dtype), V = 16 / es;
     const bool res = a->residual != nullptr, res32 = res && a->residual_dtype == CV_F32;
@@ -400,13 +404,22 @@ int launch_norm(const cv_norm_args *a, cudaStream_t stream) {
         }
     }
     const unsigned grid = (unsigned)(a->rows < 0x7fffffff ? a->rows : 0x7fffffff);
-    if ((a->group == 0 || a->group == a->dim) && a->dim <= cvk::kNormRowThreads * cvk::kNormRowElems) {
-        const int v = vec && a->dim % V == 0 ? V : bf16 && a->dim % 2 == 0 && runs(2) ? 2 : 1;
-        int elems = 8;
-        while (elems < cvk::kNormRowElems && elems * (a->rows > device_limits().sms ? kNormRowWide : cvk::kNormRowThreads) < a->dim)
-            elems *= 2;
+    const int v = vec && a->dim % V == 0 ? V : a->dim % 2 == 0 && runs(2) ? 2 : 1;
+    if ((a->group == 0 || a->group == a->dim) && a->dim <= cvk::kNormRowThreads * cvk::norm_row_elems(v)) {
+        const int64_t sms = device_limits().sms;
+        const bool many = a->rows > kNormRowMany * sms;
+        p.ahead = a->rows > kNormRowAhead * sms ? sms : a->rows;
+        int elems = 8, rows = 1;
+        while (elems < cvk::norm_row_elems(v) && elems * (many && v > 2 ? kNormRowWide : cvk::kNormRowThreads) < a->dim)
+            elems *= many && v == 8 ? 4 : 2;  // 16 of bf16 keep too few loads in flight (rows of 4096: 133 us, 32: 93)
+        // A warp a row, several rows a block (30000 residual rows of 64, bf16: 15.5 us; a block of one warp for each:
+        // 31).  16-byte accesses stop at 8 elements a thread: above, a block a row with the next rows prefetched is
+        // faster (rows of 512: 39 us against 45).
+        if (many && a->dim <= (v > 2 ? 8 : 16) * 32) elems = a->dim <= 8 * 32 ? 8 : 16, rows = kNormRowWide / 32;
         const int threads = (a->dim + elems - 1) / elems;
-        if (launch_pdl(cvk::norm_row_kernel(bf16, res32, v, elems), dim3(grid), dim3((threads + 31) / 32 * 32), 0,
+        const int64_t blocks = (a->rows + rows - 1) / rows;
+        if (launch_pdl(cvk::norm_row_kernel(bf16, res32, v, elems), dim3((unsigned)(blocks < 0x7fffffff ? blocks : 0x7fffffff)),
+                       dim3((threads + 31) / 32 * 32, rows), 0,
                        stream, p) != cudaSuccess)
             return CV_ERR_LAUNCH;
         return cudaGetLastError() == cudaSuccess ? CV_OK : CV_ERR_LAUNCH;
