@@ -130,7 +130,7 @@ struct StepPlan {
     long long units, resident;
 };
 int64_t step_workspace(const cv_linattn_args *a, const StepPlan &pl) {
-    const int64_t states = (int64_t)a->n_seq * a->n_heads * (pl.pieces - 1);
+    const int64_t states = pl.pieces > 1 ? (int64_t)a->n_seq * a->n_heads * pl.pieces : 0;
     return states * a->dk * a->dv * 4 + (states * 4 + 255) / 256 * 256;
 }
 
@@ -148,8 +148,12 @@ StepPlan plan_step(const cv_linattn_args *a, const cvk::LinattnParams &p, bool s
     // pass for the pieces' own states and their join, so two pieces are not worth it.
     const int64_t longest = a->tok.T < a->tok.total_tokens ? a->tok.T : a->tok.total_tokens;
     if (!step && pl.stream) {
-        const int64_t slots = sms * (256 / pl.vs) / (heads * ((a->dv + pl.vs - 1) / pl.vs));
-        int64_t len = slots > 0 ? (longest + slots - 1) / slots : longest;
+        // pieces that are resident at once; each sequence's last is half a piece on average
+        const int64_t slots = sms * (256 / pl.vs) / ((int64_t)a->n_heads * ((a->dv + pl.vs - 1) / pl.vs));
+        const int64_t halves = 2 * slots - a->n_seq, per = slots / a->n_seq;
+        int64_t len = longest;
+        if (a->n_seq > cvk::kStepMaxCounted) len = per > 0 ? (longest + per - 1) / per : longest;
+        else if (halves > 0) len = (2 * a->tok.total_tokens + halves - 1) / halves;
         if (len < kMinPieceTokens) len = kMinPieceTokens;
         if (len < (longest + kMaxPieces - 1) / kMaxPieces) len = (longest + kMaxPieces - 1) / kMaxPieces;
         len = (len + cvk::kStepMaxGroup - 1) / cvk::kStepMaxGroup * cvk::kStepMaxGroup;
@@ -179,7 +183,7 @@ int launch_recurrent(const cv_linattn_args *a, bool step, cudaStream_t stream) {
             return CV_ERR_WORKSPACE;
         const int64_t states = (int64_t)a->n_seq * a->n_heads;
         p.ws_state = reinterpret_cast<float *>(a->workspace);
-        p.ws_decay = p.ws_state + states * (pl.pieces - 1) * a->dk * a->dv;
+        p.ws_decay = p.ws_state + states * pl.pieces * a->dk * a->dv;
         cvk::LinattnParams own = p;  // the tokens as a run to advance over, from zero
         own.prev = p.tok, own.tok.T = 0, own.tok.cu = nullptr, own.accept = nullptr;
         own.own_states = 1, own.update = 0;
@@ -196,7 +200,7 @@ int launch_recurrent(const cv_linattn_args *a, bool step, cudaStream_t stream) {
 // The chunked kernel's launch for these arguments; pieces 0: the recurrent kernel takes them.
 struct ChunkPlan {
     int pieces, seg_len;
-    long long ws_states;  // pieces whose own states go through the workspace
+    long long ws_states;  // states of pieces that go through the workspace
     int dv_pad;
 };
 // Prompts of at most so many tokens go to the recurrent kernel, more where there are heads for every SM
@@ -255,18 +259,34 @@ ChunkPlan plan_chunks(const cv_linattn_args *a) {
     if (longest <= (heads > sms ? kShortMany : kShortFew)) return pl;
     pl.pieces = 1;
     pl.seg_len = (int)(whole > 0 ? whole : cvk::kChunk);
-    // Few heads: cut the length into pieces until every SM has one.  A cut costs a pass over k and v for
-    // the pieces' own states and their join, and a grid that is mostly full stays uncut (measured, 4 heads of 2,000
-    // tokens: pieces of at least 4 / 2 / 1 chunks 32 / 24 / 21 us).
-    for (int64_t len = cvk::kChunk; len < whole; len += cvk::kChunk) {
-        const int64_t n = (whole + len - 1) / len;
-        int64_t most = a->n_seq * n;
-        if (t.total_tokens / len + a->n_seq < most) most = t.total_tokens / len + a->n_seq;
-        if (a->n_heads * most > sms || heads * n > 4 * sms) continue;
-        pl.pieces = (int)n;
-        pl.seg_len = (int)len;
-        pl.ws_states = heads * (n - 1);
-        break;
+    // Few heads: cut the length into pieces.  A cut costs a pass over k and v for the pieces' own states and their
+    // join.  The estimate is in tenths of a us, from measured launches (128 columns): 5.7 us and 3.6 us a chunk of the
+    // fullest SM uncut; cut 13.5 us, 5.2 us a chunk and 0.35 us a piece of the join (1 prompt of 32k tokens, 6 heads:
+    // 83 us in 24 pieces; 4.1k, 4 heads: 32 us in 33), and 4.5 us for each further piece that an SM takes.  Lengths are on the device, so the fullest SM is estimated
+    // from their sum.
+    const int64_t chunks = whole / cvk::kChunk, mean = (a->n_heads * t.total_tokens / cvk::kChunk + sms - 1) / sms;
+    int64_t best = 57 + 36 * (chunks > mean ? chunks : mean);
+    for (int64_t n = 2; n <= chunks && n <= sms && heads * n <= 8 * sms;) {
+        const int64_t len = (chunks + n - 1) / n;
+        n = (chunks + len - 1) / len;
+        int64_t full = a->n_seq * n, units = full;
+        if (a->n_seq <= cvk::kChunkMaxSorted) {  // (otherwise pieces past a sequence's end take their turns too)
+            const int64_t of = t.total_tokens / (len * cvk::kChunk);
+            full = of < full ? of : full;
+            units = of + a->n_seq < units ? of + a->n_seq : units;
+        }
+        int64_t fullest = len;
+        if (a->n_heads * units > sms) {
+            const int64_t rounds = (a->n_heads * full + sms - 1) / sms * len, spread = mean + (len + 1) / 2;
+            fullest = rounds > spread ? rounds : spread;
+        }
+        const int64_t cost = 135 + 52 * fullest + 45 * ((a->n_heads * units - 1) / sms) + 7 * n / 2;
+        if (cost < best) {
+            best = cost;
+            pl.pieces = (int)n, pl.seg_len = (int)(len * cvk::kChunk), pl.ws_states = heads * n;
+        }
+        if (len == 1) break;
+        n = (chunks + len - 2) / (len - 1);
     }
     return pl;
 }
@@ -284,7 +304,7 @@ int launch_chunks(const cv_linattn_args *a, const ChunkPlan &pl, cudaStream_t st
     const int64_t units = (int64_t)a->n_seq * a->n_heads * pl.pieces, sms = device_limits().sms;
     if (units > 0x7fffffff) return CV_ERR_SHAPE;
     p.units = (int)units;
-    p.sort = units > sms && a->n_seq <= cvk::kChunkMaxSorted;
+    p.sort = (units > sms || pl.pieces > 1) && a->n_seq <= cvk::kChunkMaxSorted;
     p.dv_pad = pl.dv_pad;
     if (pl.ws_states > 0) {
         if (!a->workspace || !aligned(a->workspace, 256) || a->workspace_bytes < chunk_workspace(pl))

@@ -42,8 +42,8 @@ struct LinattnParams {
     // long prompts of few heads: pieces a sequence is cut into (1: whole), their length in tokens, and whether
     // this launch makes the pieces' own states (and decays) instead of outputs
     int pieces, piece_len, own_states;
-    float *ws_state;  // [sequence][head][pieces - 1][dk][dv]
-    float *ws_decay;  // [sequence][head][pieces - 1]
+    float *ws_state;  // [sequence][head][pieces][dk][dv]: the state before each piece of a cut sequence
+    float *ws_decay;  // [sequence][head][pieces]: over a piece
     float scale;
 };
 
@@ -96,18 +96,19 @@ struct StreamLayout {
 // The chunked kernel for prompts (bf16, dk and dv multiples of 8 up to 128).
 constexpr int kChunk = 128;            // tokens a chunk
 constexpr int kChunkThreads = 768;     // 20 warps of the four large roles, 4 more
-constexpr int kChunkMaxSorted = 64;    // sequences that are taken longest first
+constexpr int kChunkMaxSorted = 64;    // sequences whose pieces are counted and taken longest first
+constexpr int kStepMaxCounted = 32;    // the same of the recurrent kernel
 struct LinattnChunkParams {
     CUtensorMap q_map, k_map, v_map;  // [token][head][channel], boxes of 128 x 1 x 64, 128-byte swizzle
     LinattnParams a;
     int n_segs;      // pieces a sequence is cut into, at most
     int seg_len;     // tokens a piece, a multiple of kChunk
     int units;       // sequences * pieces * heads
-    int sort;        // take the longest sequences first
+    int sort;        // count only the pieces that there are, and take long ones first
     int dv_pad;      // columns of a state in the workspace (64 or 128)
     int state_only;  // the pieces' own states into the workspace, instead of outputs
-    float *ws_state;  // [sequence][head][n_segs - 1][dv / 4][128] groups of 4 columns of a state row
-    float *ws_decay;  // [sequence][head][n_segs - 1]
+    float *ws_state;  // [sequence][head][n_segs][dv / 4][128] groups of 4 columns of a state row, before each piece
+    float *ws_decay;  // [sequence][head][n_segs]: over a piece
 };
 using LinattnChunkKernel = void (*)(LinattnChunkParams);
 struct ChunkKernel {

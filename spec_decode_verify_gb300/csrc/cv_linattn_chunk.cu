@@ -48,7 +48,11 @@ struct ChunkShared {
     uint32_t tmem;
     int dead;
     int apart[2];  // why the chunk's Q S and A V are kept apart: 1 it decays by more than 2^80, 2 its v holds a NaN or inf
+    // The work of sorted launches: first the full pieces, sequence by sequence (first: the number before a
+    // sequence's own), then the shorter rests, longest first (order: their sequences).  Uncut, all are rests.
     uint8_t order[kChunkMaxSorted];
+    uint16_t first[kChunkMaxSorted + 1];
+    int full, units;
     // Of a chunk: each token's sum of log2 decays up to it (over the chunk, or over its block of 32 where the
     // chunk decays by more than 2^80), its weight as a column of A, the blocks' sums, and its weight in K'.
     // Tokens past the end: no decay, no weight.
@@ -68,6 +72,7 @@ __host__ __device__ constexpr int chunk_smem_bytes() {
 struct Unit {
     int s, h, hq, seg, slot, row0, n, chunks;
     bool on, init, last;
+    bool cut;  // one of several pieces: its state before it is in the workspace
 };
 
 __device__ __forceinline__ Unit unit_of(const LinattnChunkParams &p, const ChunkShared *sh, int idx) {
@@ -75,9 +80,22 @@ __device__ __forceinline__ Unit unit_of(const LinattnChunkParams &p, const Chunk
     const LinattnParams &a = p.a;
     u.h = idx % a.n_heads;
     const int r = idx / a.n_heads;
-    u.seg = r % p.n_segs;
-    const int rank = r / p.n_segs;
-    u.s = p.sort ? sh->order[rank] : rank;
+    if (p.n_segs == 1) {
+        u.seg = 0, u.s = p.sort ? sh->order[r] : r;
+    } else if (!p.sort) {
+        u.seg = r % p.n_segs, u.s = r / p.n_segs;
+    } else if (r >= sh->full) {
+        u.s = sh->order[r - sh->full];
+        u.seg = sh->first[u.s + 1] - sh->first[u.s];
+    } else {
+        int lo = 0, hi = a.n_seq - 1;  // the last sequence whose first piece is at most r
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (sh->first[mid] <= r) lo = mid;
+            else hi = mid - 1;
+        }
+        u.s = lo, u.seg = r - sh->first[lo];
+    }
     u.hq = (int)((unsigned)u.h * (unsigned)a.n_qk / (unsigned)a.n_heads);
     u.slot = a.cache_idx ? __ldg(a.cache_idx + u.s) : u.s;
     int L, row0;
@@ -90,6 +108,7 @@ __device__ __forceinline__ Unit unit_of(const LinattnChunkParams &p, const Chunk
     u.n = u.on ? min(p.seg_len, L - (int)start) : 0;
     u.chunks = (u.n + kChunk - 1) / kChunk;
     u.last = u.on && start + u.n >= L;
+    u.cut = u.on && L > p.seg_len;
     u.init = a.has_init ? __ldg(a.has_init + u.s) != 0 : true;
     return u;
 }
@@ -98,10 +117,11 @@ __device__ __forceinline__ Unit unit_of(const LinattnChunkParams &p, const Chunk
 // turn, so a block that got a long one first gets a short one next.  (Packing them into the blocks by their
 // lengths, which leaves 4 % between the fullest block and the mean where this leaves 19 %, measured no faster:
 // 8 prompts of 1.5k-5.8k tokens, 48 heads, 333 us against 320.)
-__device__ __forceinline__ int unit_index(const LinattnChunkParams &p, int n) {
+__device__ __forceinline__ int unit_index(const LinattnChunkParams &p, const ChunkShared *sh, int n) {
     const int G = gridDim.x, b = blockIdx.x;
     const long long idx = (long long)n * G + (p.sort && (n & 1) ? G - 1 - b : b);
-    return idx < p.units ? (int)idx : (long long)n * G < p.units ? -2 : -1;
+    const int units = p.sort ? sh->units : p.units;
+    return idx < units ? (int)idx : (long long)n * G < units ? -2 : -1;
 }
 
 // One poll of a barrier's phase, which may suspend the thread for up to 20 us.
@@ -302,14 +322,33 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
     }
     grid_dep_wait();
     grid_dep_launch();
-    if (p.sort && tid < a.n_seq) {
-        const int len = __ldg(a.tok.cu + tid + 1) - __ldg(a.tok.cu + tid);
-        int rank = 0;
-        for (int i = 0; i < a.n_seq; ++i) {
-            const int other = __ldg(a.tok.cu + i + 1) - __ldg(a.tok.cu + i);
-            rank += other > len || (other == len && i < tid);
+    if (p.sort) {
+        // each sequence's full pieces and the length of its rest (-1 none; a sequence without tokens has one of
+        // length zero; only pieces with a next one have states of their own)
+        int *const fulls = reinterpret_cast<int *>(sh->G), *const rests = reinterpret_cast<int *>(sh->col);
+        static_assert(kChunkMaxSorted <= kChunk, "a sequence's counts");
+        if (tid < a.n_seq) {
+            int L, row0;
+            if (draft_span(a.tok.cu, tid, a.tok.T, a.tok.total, L, row0)) L = 0;
+            const int f = p.n_segs > 1 ? L / p.seg_len : 0, rest = L - f * p.seg_len;
+            fulls[tid] = so && rest == 0 && f > 0 ? f - 1 : f;
+            rests[tid] = so || (rest == 0 && L > 0) ? -1 : rest;
         }
-        sh->order[rank] = (uint8_t)tid;
+        __syncthreads();
+        if (tid < a.n_seq) {
+            const int rest = rests[tid];
+            int before = 0, full = 0, parts = 0, rank = 0;
+            for (int i = 0; i < a.n_seq; ++i) {
+                const int other = rests[i];
+                before += i < tid ? fulls[i] : 0;
+                full += fulls[i];
+                parts += other >= 0;
+                rank += other > rest || (other == rest && i < tid);
+            }
+            sh->first[tid] = (uint16_t)before;
+            if (rest >= 0) sh->order[rank] = (uint8_t)tid;
+            if (tid == 0) sh->first[a.n_seq] = (uint16_t)full, sh->full = full, sh->units = (full + parts) * a.n_heads;
+        }
     }
     tmem_fence_before();
     __syncthreads();
@@ -324,7 +363,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
     if (warp == 20) {
         // ---------------------------------------------------------------------------- decays
         bool ok = true;
-        for (int n = 0, idx; ok && (idx = unit_index(p, n)) != -1; ++n) {
+        for (int n = 0, idx; ok && (idx = unit_index(p, sh, n)) != -1; ++n) {
             if (idx < 0) continue;
             const Unit u = unit_of(p, sh, idx);
             if (a.err && u.h == 0 && u.seg == 0 && lane == 0 && u.slot >= 0) {
@@ -390,7 +429,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
         // ---------------------------------------------------------------------- load: k and q
         bool ok = true;
         int k_sent = 0, q_sent = 0;
-        for (int n = 0, idx; ok && (idx = unit_index(p, n)) != -1; ++n) {
+        for (int n = 0, idx; ok && (idx = unit_index(p, sh, n)) != -1; ++n) {
             if (idx < 0) continue;
             const Unit u = unit_of(p, sh, idx);
             for (int c = 0; c < u.chunks; ++c, ++it) {
@@ -424,15 +463,15 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
         // --------------------------------------------------------------------------- load: v
         bool ok = true;
         int sent = 0;
-        for (int n = 0, idx; ok && (idx = unit_index(p, n)) != -1; ++n) {
+        for (int n = 0, idx; ok && (idx = unit_index(p, sh, n)) != -1; ++n) {
             if (idx < 0) continue;
             const Unit u = unit_of(p, sh, idx);
             // the unit's first state, into L2 before the state warps come to it
             if (u.on && !so && (u.seg > 0 || u.init)) {
                 const float *const st =
-                    u.seg > 0 ? p.ws_state + (((long long)u.s * a.n_heads + u.h) * (p.n_segs - 1) + u.seg - 1) * (kChunk * DV)
-                              : a.state + (long long)u.slot * a.st_slot + (long long)u.h * a.st_head;
-                bulk_prefetch_l2(st, (unsigned)(u.seg > 0 ? kChunk * DV : a.dk * a.dv) * 4);
+                    u.cut ? p.ws_state + (((long long)u.s * a.n_heads + u.h) * p.n_segs + u.seg) * (kChunk * DV)
+                          : a.state + (long long)u.slot * a.st_slot + (long long)u.h * a.st_head;
+                bulk_prefetch_l2(st, (unsigned)(u.cut ? kChunk * DV : a.dk * a.dv) * 4);
             }
             for (int c = 0; c < u.chunks; ++c, ++it) {
                 const int stage = it & 1, row = u.row0 + c * kChunk;
@@ -452,7 +491,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
         // ---------------------------------------------------------------------------- scores
         bool ok = true;
         const uint32_t tp = tl + kColP;
-        for (int n = 0, idx; ok && (idx = unit_index(p, n)) != -1; ++n) {
+        for (int n = 0, idx; ok && (idx = unit_index(p, sh, n)) != -1; ++n) {
             if (idx < 0) continue;
             const Unit u = unit_of(p, sh, idx);
             const float skip = a.skip ? __ldg(a.skip + u.h) : 0.0f;
@@ -505,12 +544,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
         constexpr int PASSES = DV / 4 / PW;  // 2
         bool ok = true;
         int units = 0;
-        for (int n = 0, idx; ok && (idx = unit_index(p, n)) != -1; ++n) {
+        for (int n = 0, idx; ok && (idx = unit_index(p, sh, n)) != -1; ++n) {
             if (idx < 0) continue;
             const Unit u = unit_of(p, sh, idx);
             if (!u.on) continue;
             float *const st = a.state + (long long)u.slot * a.st_slot + (long long)u.h * a.st_head;
-            const long long wsi = ((long long)u.s * a.n_heads + u.h) * (p.n_segs - 1);
+            const long long wsi = ((long long)u.s * a.n_heads + u.h) * p.n_segs;
             if (u.chunks == 0) {  // an empty prompt: zeros without an initial state
                 if (!u.init && r < a.dk)
                     for (int j = 0; j < a.dv; j += 4)
@@ -519,8 +558,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
             }
             // the state before the unit
             const bool zero = so ? true : u.seg == 0 && !u.init;
-            if (zero || u.seg > 0) {
-                const float4 *src = reinterpret_cast<const float4 *>(p.ws_state) + (wsi + u.seg - 1) * (32 * DV);
+            if (zero || u.cut) {
+                const float4 *src = reinterpret_cast<const float4 *>(p.ws_state) + (wsi + u.seg) * (32 * DV);
 #pragma unroll 1
                 for (int j = 0; j < DV; j += 16) {
                     uint32_t v[16];
@@ -620,7 +659,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
             tmem_fence_after();
             // the state after it
             if (so) {
-                float4 *dst = reinterpret_cast<float4 *>(p.ws_state) + (wsi + u.seg) * (32 * DV);
+                float4 *dst = reinterpret_cast<float4 *>(p.ws_state) + (wsi + u.seg + 1) * (32 * DV);
 #pragma unroll 1
                 for (int j = 0; j < DV; j += 16) {
                     uint32_t v[16];
@@ -663,7 +702,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
         // ---------------------------------------------------------------------------- output
         const int i = 32 * w4 + lane;  // the row of the chunk
         bool ok = true;
-        for (int n = 0, idx; ok && (idx = unit_index(p, n)) != -1; ++n) {
+        for (int n = 0, idx; ok && (idx = unit_index(p, sh, n)) != -1; ++n) {
             if (idx < 0) continue;
             const Unit u = unit_of(p, sh, idx);
             for (int c = 0; c < u.chunks; ++c, ++it) {
@@ -748,7 +787,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
         // ------------------------------------------------------------------------------ keys
         const int t = 32 * w4 + lane, half = role - 3;  // the token, and which 64 of its channels
         bool ok = true;
-        for (int n = 0, idx; ok && (idx = unit_index(p, n)) != -1; ++n) {
+        for (int n = 0, idx; ok && (idx = unit_index(p, sh, n)) != -1; ++n) {
             if (idx < 0) continue;
             const Unit u = unit_of(p, sh, idx);
             for (int c = 0; c < u.chunks; ++c, ++it) {
@@ -826,7 +865,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
                            id_kv = mma_desc(DV, true, true);
         bool apart_before = false;
         bool ok = true;
-        for (int n = 0, idx; ok && (idx = unit_index(p, n)) != -1; ++n) {
+        for (int n = 0, idx; ok && (idx = unit_index(p, sh, n)) != -1; ++n) {
             if (idx < 0) continue;
             const int chunks = unit_of(p, sh, idx).chunks;
             for (int c = 0; c < chunks; ++c, ++it) {
@@ -889,7 +928,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
     tmem_fence_before();
     __syncthreads();
     if (*dead && tid == 0 && a.err)
-        for (int n = 0, idx; (idx = unit_index(p, n)) != -1; ++n)
+        for (int n = 0, idx; (idx = unit_index(p, sh, n)) != -1; ++n)
             if (idx >= 0) {
                 const Unit u = unit_of(p, sh, idx);
                 if (u.on) atomicOr(a.err + u.s, kSeqTimeout);
@@ -918,22 +957,24 @@ __global__ void __launch_bounds__(kJoinThreads) chunk_join(const __grid_constant
     if (init && row < a.dk && col < a.dv)
         S = *reinterpret_cast<const float4 *>(a.state + (long long)slot * a.st_slot + (long long)h * a.st_head +
                                               (long long)row * a.dv + col);
-    const long long base = ((long long)s * a.n_heads + h) * (p.n_segs - 1);
+    const long long base = ((long long)s * a.n_heads + h) * p.n_segs;
     float4 *const own = reinterpret_cast<float4 *>(p.ws_state) + base * (32 * dv_pad) + part * 128 + row;
     const float *const dec = p.ws_decay + base;
     const long long step = 32LL * dv_pad;
+    // The first piece's state too: the last piece writes the sequence's while the first may not have begun.
+    if (n > 0) *own = S;
     for (int i0 = 0; i0 < n; i0 += 8) {
         float4 f[8];
         float d[8];
 #pragma unroll
         for (int x = 0; x < 8; ++x)
-            if (i0 + x < n) f[x] = own[(i0 + x) * step], d[x] = dec[i0 + x];
+            if (i0 + x < n) f[x] = own[(i0 + x + 1) * step], d[x] = dec[i0 + x];
 #pragma unroll
         for (int x = 0; x < 8; ++x)
             if (i0 + x < n) {
                 S.x = fmaf(d[x], S.x, f[x].x), S.y = fmaf(d[x], S.y, f[x].y);
                 S.z = fmaf(d[x], S.z, f[x].z), S.w = fmaf(d[x], S.w, f[x].w);
-                own[(i0 + x) * step] = S;
+                own[(i0 + x + 1) * step] = S;
             }
     }
 }

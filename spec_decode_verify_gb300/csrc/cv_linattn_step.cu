@@ -362,6 +362,26 @@ __global__ void __launch_bounds__(kStepThreads, 2) linattn_stream(const __grid_c
         u.h = (int)(unit % (unsigned)p.n_heads);
         unit /= (unsigned)p.n_heads;
         u.piece = (int)(unit % (unsigned)p.pieces), u.s = (int)(unit / (unsigned)p.pieces);
+        if (p.pieces > 1 && p.n_seq <= kStepMaxCounted) {
+            // only the pieces that there are (of a sequence's own states: those with a next one)
+            const LinattnRun &run = p.own_states ? p.prev : p.tok;
+            u.on = false;
+            for (int s = 0; s < p.n_seq; ++s) {
+                int L, row0;
+                if (draft_span(run.cu, s, run.T, run.total, L, row0)) L = 0;
+                const int some = (L + p.piece_len - 1) / p.piece_len;
+                const unsigned n = (unsigned)(p.own_states ? max(some - 1, 0) : max(some, 1));
+                if (unit < n) {
+                    u.s = s, u.piece = (int)unit, u.on = true;
+                    break;
+                }
+                unit -= n;
+            }
+            if (!u.on) {
+                u.s = 0, u.piece = 1;  // (a first piece would report the sequence's status)
+                return u;
+            }
+        }
         const int slot = p.cache_idx ? __ldg(p.cache_idx + u.s) : u.s;
         u.n_tok = p.tok.T, u.n_prev = p.prev.T;
         if (slot >= p.n_slots) u.status |= 1;
@@ -386,11 +406,12 @@ __global__ void __launch_bounds__(kStepThreads, 2) linattn_stream(const __grid_c
             const bool last = start + p.piece_len >= n;
             u.on = u.piece == 0 || start < n;
             if (p.own_states && last) u.on = false;
-            float *const ws = p.ws_state + (((long long)u.s * p.n_heads + u.h) * (p.pieces - 1) + u.piece) * p.dk * p.dv;
+            const bool cut = n > p.piece_len;
+            float *const ws = p.ws_state + (((long long)u.s * p.n_heads + u.h) * p.pieces + u.piece) * p.dk * p.dv;
             n = u.on ? min(p.piece_len, n - (int)start) : 0;
             row += u.on ? (int)start : 0;
-            if (p.own_states) u.init = false, u.to = ws;
-            else if (u.piece > 0) u.init = true, u.from = ws - (long long)p.dk * p.dv;
+            if (p.own_states) u.init = false, u.to = ws + (long long)p.dk * p.dv;
+            else if (cut) u.init = u.init || u.piece > 0, u.from = ws;
             if (!last) u.update = p.own_states;
         }
         return u;
@@ -663,7 +684,7 @@ __global__ void __launch_bounds__(kStepThreads, 2) linattn_stream(const __grid_c
             if (g + 1 == ng && cur.update) store_state();
         }
         if (p.own_states && cur.on && cur.slice == 0 && tid == 0)
-            p.ws_decay[((long long)cur.s * p.n_heads + cur.h) * (p.pieces - 1) + cur.piece] = decay;
+            p.ws_decay[((long long)cur.s * p.n_heads + cur.h) * p.pieces + cur.piece] = decay;
         if (ng == 0) {  // no group: the next unit's loads set out here
             if (groups_of(nxt) > 0) fetch_group(nxt, 0, buf);
             if (nxt.on) fetch_state(nxt);
@@ -687,17 +708,19 @@ __global__ void __launch_bounds__(kStateJoinThreads) state_join(const __grid_con
     const int n = (L + p.piece_len - 1) / p.piece_len - 1;  // pieces with a next one
     const bool init = p.has_init ? __ldg(p.has_init + s) != 0 : true;
     float S = init && n > 0 ? p.state[(long long)slot * p.st_slot + (long long)h * p.st_head + e] : 0.0f;
-    const long long base = (long long)sh * (p.pieces - 1);
+    const long long base = (long long)sh * p.pieces;
     float *const own = p.ws_state + base * words + e;
     const float *const dec = p.ws_decay + base;
+    // The first piece's state too: the last piece writes the sequence's while the first may not have begun.
+    if (n > 0) *own = S;
     for (int i0 = 0; i0 < n; i0 += 8) {
         float f[8], d[8];
 #pragma unroll
         for (int x = 0; x < 8; ++x)
-            if (i0 + x < n) f[x] = own[(long long)(i0 + x) * words], d[x] = dec[i0 + x];
+            if (i0 + x < n) f[x] = own[(long long)(i0 + x + 1) * words], d[x] = dec[i0 + x];
 #pragma unroll
         for (int x = 0; x < 8; ++x)
-            if (i0 + x < n) own[(long long)(i0 + x) * words] = S = fmaf(d[x], S, f[x]);
+            if (i0 + x < n) own[(long long)(i0 + x + 1) * words] = S = fmaf(d[x], S, f[x]);
     }
 }
 

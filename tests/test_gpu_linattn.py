@@ -404,6 +404,22 @@ def test_prefill_repeats_bit_for_bit(cuda_lib, counts, nq, nh, dk, dv):
         assert torch.equal(d["out"], first["out"]) and torch.equal(d["state"], first["state"])
 
 
+@pytest.mark.parametrize("dtype,counts,nq,nh,dk,dv", [
+    ("bf16", [3000, 2670, 2171, 118, 1907, 1020, 2658, 212], 4, 8, 64, 64),  # more pieces than SMs
+    ("bf16", [0, 2300, 130, 0, 700], 1, 3, 128, 128),
+    ("f32", [428, 1257, 0, 115], 8, 24, 128, 128),
+    ("f32", [91, 148, 18, 284, 226, 93, 63, 49, 0, 252, 158, 126], 1, 4, 128, 88)])
+def test_prefill_cut_ragged_prompts(cuda_lib, dtype, counts, nq, nh, dk, dv):
+    """Pieces of one prompt run in any order: the first reads the state that the last one writes."""
+    c = Case(len(counts), nq, nh, dk, dv, dtype, counts=counts, seed=23, gain=True)
+    first = c.prefill(cuda_lib)
+    assert first["err"].tolist() == [0] * len(counts)
+    c.check(first, True, chunked=dtype == "bf16")
+    for _ in range(8):
+        d = c.prefill(cuda_lib)
+        assert torch.equal(d["out"], first["out"]) and torch.equal(d["state"], first["state"])
+
+
 def test_prefill_on_another_stream(cuda_lib):
     c = Case(2, 1, 2, 128, 128, "bf16", counts=[900, 333], seed=22)
     d = c.device()
