@@ -142,7 +142,10 @@ StepPlan plan_step(const cv_linattn_args *a, const cvk::LinattnParams &p, bool s
                 (!step || run_empty(a->prev) || p.prev.vec16);
     pl.tg = most <= 1 ? 1 : cvk::kStepMaxGroup;
     pl.pieces = 1, pl.piece_len = 0;
-    pl.vs = pl.stream ? 128 : 64;
+    // Blocks share the products of their tokens' q and k, so runs of tokens take 128 columns (128 x 8 drafts of 48
+    // heads: 172 us, 201 with 64); single tokens have one product, and smaller blocks overlap better (64 tokens of
+    // 32 heads: 22.4 us, 24.2 with 128).
+    pl.vs = pl.stream && pl.tg > 1 ? 128 : 64;
     while (pl.vs > 32 && pl.vs / 2 >= a->dv) pl.vs /= 2;
     // Few heads and long prompts: the length is cut into pieces that fill the resident blocks.  A cut costs a
     // pass for the pieces' own states and their join, so two pieces are not worth it.
@@ -261,9 +264,9 @@ ChunkPlan plan_chunks(const cv_linattn_args *a) {
     pl.seg_len = (int)(whole > 0 ? whole : cvk::kChunk);
     // Few heads: cut the length into pieces.  A cut costs a pass over k and v for the pieces' own states and their
     // join.  The estimate is in tenths of a us, from measured launches (128 columns): 5.7 us and 3.6 us a chunk of the
-    // fullest SM uncut; cut 13.5 us, 5.2 us a chunk and 0.35 us a piece of the join (1 prompt of 32k tokens, 6 heads:
-    // 83 us in 24 pieces; 4.1k, 4 heads: 32 us in 33), and 4.5 us for each further piece that an SM takes.  Lengths are on the device, so the fullest SM is estimated
-    // from their sum.
+    // fullest SM uncut; cut 13.5 us, 5.2 us a chunk, 0.35 us a piece of the join and 4.5 us for each further piece
+    // that an SM takes (1 prompt of 32k tokens, 6 heads: 83 us in 24 pieces; 4.1k tokens, 4 heads: 28 us in 33).
+    // Lengths are on the device, so the fullest SM is estimated from their sum.
     const int64_t chunks = whole / cvk::kChunk, mean = (a->n_heads * t.total_tokens / cvk::kChunk + sms - 1) / sms;
     int64_t best = 57 + 36 * (chunks > mean ? chunks : mean);
     for (int64_t n = 2; n <= chunks && n <= sms && heads * n <= 8 * sms;) {

@@ -58,10 +58,10 @@ __host__ __device__ constexpr int step_smem_floats(int VS, int R, int TG) {
 
 using LinattnKernel = void (*)(LinattnParams);
 
-// The recurrent kernel for slices of VS columns and at most rows_max state rows, TG tokens a pass.
+// The recurrent kernel for slices of VS columns, TG tokens a pass.
 struct StepKernel {
     LinattnKernel fn;
-    int rows_max, smem_bytes;
+    int smem_bytes;
 };
 // Any alignment; vs: 64 or 32; tg: 1 or kStepMaxGroup; dk <= 256.
 StepKernel step_kernel(int vs, int dk, int tg);

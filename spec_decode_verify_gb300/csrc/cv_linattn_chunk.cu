@@ -22,9 +22,13 @@
 //   decays  1 warp: sums of the log decays and the weights made of them, ahead of the others
 //   load    2 threads: q, k, v tiles by TMA in the 128-byte swizzle, channels past the end zero
 //   issue   1 thread: all products, in the order Q K^T, Q S, K'^T V, A V
-// Shared memory: v in two stages, k, q, both parts of K' and the copy of S once (32 KB each at 128 channels); tensor memory: Q K^T (then A) 128 columns, S and
-// two buffers of Q S + A V dv columns each.  A chunk's products
-// take 2560 cycles of the tensor pipe; the longest cycle through the roles is K'^T V -> S -> Q S.
+// Shared memory: v in two stages, k, q, both parts of K' and the copy of S once (32 KB each at 128 channels).
+// Tensor memory: Q K^T (then A) 128 columns, S and two buffers of Q S + A V dv columns each.
+//
+// Measured: 8 prompts of 1.5k-5.8k tokens, 48 heads of 128 x 128: 320 us, 3.3 TB/s (HBM's floor is 156 us), tensor
+// pipe 30 % and issue slots 35-40 % busy.  A chunk takes 3.6 us of an SM; its products need 1.7 us of the tensor
+// pipe, and what bounds it is the longest cycle through the roles, K'^T V -> S -> Q S, and the shared memory that
+// all of them read and write.
 //
 // Every wait is bounded; one that gives up ends the block's work, flags the sequences it had left and
 // returns.

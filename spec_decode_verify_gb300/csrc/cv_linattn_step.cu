@@ -274,7 +274,7 @@ __global__ void __launch_bounds__(kStepThreads, 2) linattn_step(const __grid_con
     if (p.update && (n_tok > 0 || !init)) store_state();
 }
 
-// The same for aligned rows, with everything loaded ahead.  Blocks stay (two per SM) and walk the units
+// The same for aligned rows, with everything loaded ahead.  Blocks stay (16 warps per SM) and walk the units
 // (sequence, head, 16 columns a warp); while one unit is computed from registers, the next one's state tile
 // and the next group's rows are on their way into shared memory by cp.async.
 //
@@ -282,8 +282,13 @@ __global__ void __launch_bounds__(kStepThreads, 2) linattn_step(const __grid_con
 // consecutive rows, held in registers as pairs of rows (S[m][j] = rows 2m, 2m + 1 of column j).  A token's
 // q or k, as it lies in memory, is then read as R * 2 (bf16) consecutive bytes per lane and multiplies
 // pairs of rows by paired fp32 instructions; the sum over the row groups stays inside the warp.  Only the
-// products q_t . k_u are shared by the block's warps.  Measured on 128 x 8 drafts with the commit (48 heads
-// of 128, 13 padded): 239 us with rows spread over the warps and fp32 copies of q and k, see below for this.
+// products q_t . k_u are shared by the block's warps.
+//
+// Measured: 128 x 8 drafts with the commit of the previous ones (48 heads of 128 x 128, 13 padded) 172 us,
+// 4.4 TB/s, half the issue slots busy: the paired multiply-adds, the reads of q and k and a group's two barriers
+// share the time with HBM (rows spread over the warps and fp32 copies of q and k took 239 us).  64 single fp32
+// tokens of 32 heads of 64 x 128: 22 us, 6.0 TB/s, bound by HBM; 1 token of 48 heads of 128 x 128: 5 us, bound
+// by latency.
 constexpr int kTileWords = 4;  // columns a lane
 
 // N consecutive pairs of rows of a token's q or k.
@@ -726,13 +731,12 @@ __global__ void __launch_bounds__(kStateJoinThreads) state_join(const __grid_con
 
 template <int VS, int R>
 StepKernel pick(int tg) {
-    constexpr int rows = R * (kStepThreads / (VS / 4));
-    if (tg == 1) return {linattn_step<VS, R, 1>, rows, step_smem_floats(VS, R, 1) * 4};
-    return {linattn_step<VS, R, kStepMaxGroup>, rows, step_smem_floats(VS, R, kStepMaxGroup) * 4};
+    if (tg == 1) return {linattn_step<VS, R, 1>, step_smem_floats(VS, R, 1) * 4};
+    return {linattn_step<VS, R, kStepMaxGroup>, step_smem_floats(VS, R, kStepMaxGroup) * 4};
 }
 template <int R, int TG>
 StepKernel pick_stream(int warps, bool bf16) {
-    return {bf16 ? linattn_stream<R, TG, true> : linattn_stream<R, TG, false>, 8 * R, StreamLayout(warps, R, TG, bf16).bytes};
+    return {bf16 ? linattn_stream<R, TG, true> : linattn_stream<R, TG, false>, StreamLayout(warps, R, TG, bf16).bytes};
 }
 
 }  // namespace
