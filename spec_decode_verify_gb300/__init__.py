@@ -653,9 +653,9 @@ def linattn_prefill(q, k, v, log_decay, state, out, cu_seqlens, *, max_seqlen, g
         if stream is not None and not isinstance(stream, torch.cuda.Stream):
             raise ValueError("pass workspace with a raw stream handle")
         need = _linattn_workspace(a)
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-        if stream is not None:
-            workspace.record_stream(stream)
+        # from the stream's own pool: a block freed on another stream may still be in use there
+        with torch.cuda.stream(stream):
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
         a.workspace, a.workspace_bytes = workspace.data_ptr(), need
         rc = lib.cv_linattn_prefill(ctypes.byref(a), on)
     if rc != 0:

@@ -26,7 +26,7 @@
 // Tensor memory: Q K^T (then A) 128 columns, S and two buffers of Q S + A V dv columns each.
 //
 // Measured: 8 prompts of 1.5k-5.8k tokens, 48 heads of 128 x 128: 320 us, 3.3 TB/s (HBM's floor is 156 us), tensor
-// pipe 30 % and issue slots 35-40 % busy.  A chunk takes 3.6 us of an SM; its products need 1.7 us of the tensor
+// pipe 30 % and issue slots 44 % busy.  A chunk takes 3.6 us of an SM; its products need 1.7 us of the tensor
 // pipe, and what bounds it is the longest cycle through the roles, K'^T V -> S -> Q S, and the shared memory that
 // all of them read and write.
 //
