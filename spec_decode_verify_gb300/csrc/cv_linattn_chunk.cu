@@ -21,14 +21,16 @@
 //   keys    8 warps, half a token a thread: K' as a high and a low part from the k tile
 //   decays  1 warp: sums of the log decays and the weights made of them, ahead of the others
 //   load    2 threads: q, k, v tiles by TMA in the 128-byte swizzle, channels past the end zero
-//   issue   1 thread: all products, in the order Q K^T, Q S, K'^T V, A V
+//   issue   1 thread: all products, in the order Q K^T, Q S, K'^T V (64 columns after the others, so that the
+//           state warps begin the next chunk meanwhile: 311 us, 320 in one), A V
 // Shared memory: v in two stages, k, q, both parts of K' and the copy of S once (32 KB each at 128 channels).
 // Tensor memory: Q K^T (then A) 128 columns, S and two buffers of Q S + A V dv columns each.
 //
-// Measured: 8 prompts of 1.5k-5.8k tokens, 48 heads of 128 x 128: 320 us, 3.3 TB/s (HBM's floor is 156 us), tensor
-// pipe 30 % and issue slots 44 % busy.  A chunk takes 3.6 us of an SM; its products need 1.7 us of the tensor
-// pipe, and what bounds it is the longest cycle through the roles, K'^T V -> S -> Q S, and the shared memory that
-// all of them read and write.
+// Measured: 8 prompts of 1.5k-5.8k tokens, 48 heads of 128 x 128: 311 us, 3.4 TB/s (HBM's floor is 156 us), tensor
+// pipe 30 % and issue slots 44 % busy.  A chunk takes 3.5 us of an SM; its products need 1.7 us of the tensor
+// pipe.  What bounds it is the longest cycle through the roles, K'^T V -> S -> Q S, and the shared memory that all
+// of them read and write: about 600 KB a chunk (the operands of the products 288, tiles in and out 160, K' made of
+// k 96, the copy of S 32, the look for NaN in v 32), 2.4 us at 128 bytes a cycle.
 //
 // Every wait is bounded; one that gives up ends the block's work, flags the sequences it had left and
 // returns.
@@ -48,7 +50,7 @@ constexpr int kTileQK = kChunk * 256;  // bytes of a q or k tile: two blocks of 
 struct ChunkShared {
     uint64_t v_full[2], v_empty[2];
     uint64_t g_full[2], g_empty[2], out[2], out_free[2];
-    uint64_t key_empty, k_full, k_empty, q_full, scores, a_ready, keys, q_used, s_init, s_ready, s_done, last;
+    uint64_t key_empty, k_full, k_empty, q_full, scores, a_ready, keys, q_used, s_init, s_ready, s_done[2], last;
     uint32_t tmem;
     int dead;
     int apart[2];  // why the chunk's Q S and A V are kept apart: 1 it decays by more than 2^80, 2 its v holds a NaN or inf
@@ -285,6 +287,7 @@ __device__ __noinline__ void scores_strong(const LinattnParams &a, int row0, int
 template <int DV>
 __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_constant__ LinattnChunkParams p) {
     constexpr int kTileV = kChunk * DV * 2, kBlock = kChunk * 128;  // a tile's blocks of 64 channels
+    constexpr int HALVES = DV / 64;  // of S, by columns
     constexpr uint32_t kColP = 0, kColO = 128, kColS = 128 + 2 * DV, kCols = 512;  // (two buffers of outputs)
     extern __shared__ __align__(1024) unsigned char smem[];
     unsigned char *const k_tile = smem, *const hi_tile = k_tile + kTileQK, *const lo_tile = hi_tile + kTileQK;
@@ -307,6 +310,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
             mbar_init(&sh->v_empty[i], so ? 1 : 4);
             mbar_init(&sh->out[i], 1);
             mbar_init(&sh->out_free[i], 4);
+            mbar_init(&sh->s_done[i], 1);
             mbar_init(&sh->g_full[i], 1);
             mbar_init(&sh->g_empty[i], so ? 4 : 12);
         }
@@ -320,7 +324,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
         mbar_init(&sh->q_used, 1);
         mbar_init(&sh->s_init, 4);
         mbar_init(&sh->s_ready, 4);
-        mbar_init(&sh->s_done, 1);
         mbar_init(&sh->last, 1);
         mbar_init_fence();
     }
@@ -609,14 +612,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
             float total = 1.0f;
             for (int c = 0; c < u.chunks; ++c, ++it) {
                 const int stage = it & 1;
-                // the last chunk's products into S are done, and those that read the copy (at a unit's start they were
-                // waited for at the end of the one before)
-                if (!wait_warp(&sh->g_full[stage], (it >> 1) & 1, dead) || (c > 0 && (!wait_warp(&sh->s_done, (it - 1) & 1, dead) ||
-                              (!so && !wait_warp(&sh->q_used, (it - 1) & 1, dead))))) {
+                if (!wait_warp(&sh->g_full[stage], (it >> 1) & 1, dead)) {
                     ok = false;
                     break;
                 }
-                tmem_fence_after();
                 uint32_t v[16];
                 const float4 bt = *reinterpret_cast<const float4 *>(sh->tot[stage]);
                 arrive_warp(&sh->g_empty[stage]);
@@ -646,17 +645,28 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
                     tmem_st16(ts + j, x);
                 };
 #pragma unroll 1
-                for (int j = 0; j < DV; j += 16) {
-                    tmem_ld16(v, ts + j);
-                    tmem_wait_ld(v);
-                    piece(v, j);
+                for (int h = 0; h < HALVES; ++h) {
+                    // the last chunk's products into this half of S are done, and the one that read its copy (at a
+                    // unit's start they were waited for at the end of the one before)
+                    if (c > 0 && !wait_warp(&sh->s_done[h], (it - 1) & 1, dead)) {
+                        ok = false;
+                        break;
+                    }
+                    tmem_fence_after();
+#pragma unroll 1
+                    for (int j = h * 64; j < h * 64 + 64; j += 16) {
+                        tmem_ld16(v, ts + j);
+                        tmem_wait_ld(v);
+                        piece(v, j);
+                    }
                 }
+                if (!ok) break;
                 tmem_wait_st();
                 tmem_fence_before();
                 fence_smem_to_async();
                 arrive_warp(&sh->s_ready);
             }
-            if (!ok || !wait_warp(&sh->s_done, (it - 1) & 1, dead) || (!so && !wait_warp(&sh->q_used, (it - 1) & 1, dead))) {
+            if (!ok || !wait_warp(&sh->s_done[HALVES - 1], (it - 1) & 1, dead)) {
                 ok = false;
                 break;
             }
@@ -804,7 +814,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
                 arrive_warp(&sh->key_empty);
                 // K' has its place once the last chunk's products are done (and this role never runs two phases
                 // ahead of the issuing warp)
-                if (!wait_warp(&sh->k_full, it & 1, dead) || (it > 0 && !wait_warp(&sh->s_done, (it - 1) & 1, dead))) {
+                if (!wait_warp(&sh->k_full, it & 1, dead) || (it > 0 && !wait_warp(&sh->s_done[HALVES - 1], (it - 1) & 1, dead))) {
                     ok = false;
                     break;
                 }
@@ -865,8 +875,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
         const uint32_t lead = elect_lane();
         const uint32_t q = desc_k(smem_u32(q_tile)), kt = desc_k(smem_u32(k_tile)), sc = desc_mn(smem_u32(s_copy), kBlock),
                        hi = desc_mn(smem_u32(hi_tile), kBlock), lo = desc_mn(smem_u32(lo_tile), kBlock);
-        constexpr uint32_t id_qk = mma_desc(128, false, false), id_qs = mma_desc(DV, false, true),
-                           id_kv = mma_desc(DV, true, true);
+        constexpr uint32_t id_qk = mma_desc(128, false, false),
+                           id_kv = mma_desc(64, true, true), id_av = mma_desc(DV, false, true);
         bool apart_before = false;
         bool ok = true;
         for (int n = 0, idx; ok && (idx = unit_index(p, sh, n)) != -1; ++n) {
@@ -888,9 +898,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
                     mma_commit(lead, &sh->scores);
                     mma_commit(lead, &sh->k_empty);
                 }
-                if (!wait_warp(&sh->s_ready, it & 1, dead)) break;
                 // Q S and A V add up in one buffer, of two in turn; a chunk that keeps them apart takes both
                 const uint32_t mine = tm + kColO + (it & 1) * DV, other = tm + kColO + (~it & 1) * DV;
+                if (!wait_warp(&sh->s_ready, it & 1, dead)) break;
                 if (!so) {
                     if ((it > 1 && !wait_warp(&sh->out_free[it & 1], ((it >> 1) & 1) ^ 1, dead)) ||
                         (apart_before && !wait_warp(&sh->out_free[~it & 1], ((it - 1) >> 1) & 1, dead)))
@@ -898,17 +908,20 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
                     tmem_fence_after();
 #pragma unroll 1
                     for (int x = 0; x < 8; ++x)
-                        mma_ss(lead, mine, q + (((x >> 2) * kBlock + (x & 3) * 32) >> 4), sc + x * 128, id_qs, x > 0);
+                        mma_ss(lead, mine, q + (((x >> 2) * kBlock + (x & 3) * 32) >> 4), sc + x * 128, id_av, x > 0);
                     mma_commit(lead, &sh->q_used);
                 }
                 if (!wait_warp(&sh->keys, it & 1, dead)) break;  // (these waited for v)
                 tmem_fence_after();
 #pragma unroll 1
-                for (int x = 0; x < 8; ++x) {
-                    mma_ss(lead, tm + kColS, hi + x * 128, v + x * 128, id_kv, true);
-                    mma_ss(lead, tm + kColS, lo + x * 128, v + x * 128, id_kv, true);
+                for (int h = 0; h < HALVES; ++h) {
+#pragma unroll 1
+                    for (int x = 0; x < 8; ++x) {
+                        mma_ss(lead, tm + kColS + h * 64, hi + x * 128, v + h * (kBlock >> 4) + x * 128, id_kv, true);
+                        mma_ss(lead, tm + kColS + h * 64, lo + x * 128, v + h * (kBlock >> 4) + x * 128, id_kv, true);
+                    }
+                    mma_commit(lead, &sh->s_done[h]);
                 }
-                mma_commit(lead, &sh->s_done);
                 if (so) mma_commit(lead, &sh->v_empty[stage]);
                 if (!so) {
                     if (!wait_warp(&sh->a_ready, it & 1, dead)) break;
@@ -917,7 +930,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
                     tmem_fence_after();
 #pragma unroll 1
                     for (int x = 0; x < 8; ++x)
-                        mma_ts(lead, apart ? other : mine, tm + kColP + x * 8, v + x * 128, id_qs, !apart || x > 0);
+                        mma_ts(lead, apart ? other : mine, tm + kColP + x * 8, v + x * 128, id_av, !apart || x > 0);
                     mma_commit(lead, &sh->out[it & 1]);
                     apart_before = apart;
                 }
