@@ -2,12 +2,15 @@
 //
 // Per row:  a = y [* act(z)];  a *= rsqrt(mean_group a^2 + eps) * w_post;  a [*= act(z)];
 //           r = res + scale * cs * a;  out = r * rsqrt(mean_row r^2 + eps) * w_pre.
-// Sums are fp32 in a fixed order (per thread, a shuffle tree, then the warps in order), so a row's
-// bits do not depend on the other rows.  r enters the second norm unrounded.  Every tensor is read
-// and written once: the kernels are bound by HBM (large calls) or by latency (a few rows).
+// Sums are fp32 in a fixed order (per thread, a shuffle tree, then the warps in order): a row's bits do
+// not depend on the other rows' values (their number may choose another split of the row).  r enters the second
+// norm unrounded.  Every tensor is read and written once: the kernels are bound by HBM (large calls) or by
+// latency (a few rows).
 //   norm_groups  no residual, narrow groups (a norm for each head): a group's elements sit in up to
-//                32 lanes of one warp, 16 bytes a lane, so no shared memory and no barrier
-//   norm_row     a block a row, the row's values in registers between the two norms
+//                32 lanes of one warp, 16 bytes a lane, so no shared memory and no barrier (30822 x 6144
+//                gated, groups of 128, bf16: 202 us, 5.6 TB/s)
+//   norm_row     a block a row, the row's values in registers between the two norms (1023 x 4096, fp32
+//                residual: 12.9 us, one wave of rows; 14648 x 4096: 125 us, 6.7 TB/s)
 //   norm_any     a block a row, values read again (from L1/L2) for each pass: rows too wide for
 //                registers and residual rows with several groups
 #include "cv_device.cuh"

@@ -91,6 +91,15 @@ def test_residual_norm(cuda_lib, rows, dim, group, gate, dtype, res):
     check(cuda_lib, t, dim, dtype, scale=0.3, group=group)
 
 
+@pytest.mark.parametrize("dtype,res", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "f32")])
+@pytest.mark.parametrize("rows,dim", [(2501, 520), (2500, 1024), (643, 64), (650, 63), (701, 200), (611, 300), (645, 517),
+                                      (620, 1030), (610, 2047), (615, 4096), (3, 8199), (611, 8190)])
+def test_many_rows(cuda_lib, rows, dim, dtype, res):
+    """Enough rows that several share a block, or that later ones are prefetched."""
+    t = make(rows, dim, dtype, seed=dim, group=dim, gate=True, res=res, cs=dim % 2 == 0, pre=True)
+    check(cuda_lib, t, dim, dtype, scale=0.5, group=dim)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_residual_without_second_norm(cuda_lib, dtype):
     t = make(6, 512, dtype, seed=1, group=512, gate=True, res=dtype)
