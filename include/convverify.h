@@ -386,8 +386,16 @@ CV_API int cv_verify_plan(const cv_verify_args *args, cv_launch_plan *plan);
  * h * n_qk_heads / n_heads (integer division).  One token does
  *     S   <- exp(g) S + b k v^T         g = log_decay[h], b = gain[h] (1 without gain)
  *     out  = scale * S^T q + skip[h] v  (no last term without skip)
- * with the updated state, everything in fp32; out is rounded once to dtype.  g may be -infinity (the
- * state is dropped: exp(g) = 0), it is meant to be <= 0.
+ * with the updated state.  Sums, decays, gains and the state are fp32, and out is rounded once to dtype.
+ * g may be -infinity (the state is dropped: exp(g) = 0), it is meant to be <= 0.
+ * Precision: cv_linattn_step, and cv_linattn_prefill of fp32 tokens, do every product in fp32.
+ * cv_linattn_prefill of bf16 tokens (prompts of more than 8 to 16 tokens, dk and dv multiples of 8 up
+ * to 128, 16-byte aligned rows) multiplies on tensor cores, whose operands are bf16: the products q.k with their
+ * decays, and the copy of the state that q reads, are rounded to bf16 too (2^-8 of a term; together
+ * with the rounding of out 2.3e-3 of the outputs' norm, where that rounding alone leaves 1.7e-3), and the
+ * keys that enter the state hold 16 bits (2^-17 of a term, 3e-6 of the state's norm at any
+ * length).  On the way its sums are up to 2^80 times what they add to an output, so finite terms
+ * |b (q.k) v| above 2^47 may give infinities.  fp32 tokens avoid all of this.
  *
  * cv_linattn_tokens holds one run of tokens per sequence: T tokens for each of the n_seq sequences
  * (cu NULL; token t of sequence s at s*seq_stride + t*tok_stride) or, with cu (int32 [n_seq + 1]
