@@ -4,8 +4,10 @@
 //   out_i = scale * exp(G_i) ( S^T q_i + sum_{j<=i} A_ij v_j ),      A_ij = exp(-G_j) b_j (q_i . k_j)
 //   S'    = exp(G_C) S + K'^T V,                                     K'_j = exp(G_C - G_j) b_j k_j
 // so a chunk is five products of 128 x 128 x 128: Q K^T, Q S, A V, and K'^T V twice, because K' is
-// written as a high and a low bf16 part (together 16 significant bits): the state stays fp32 through
-// any number of chunks.  A and the copy of S that Q S reads are rounded to bf16, as the outputs are.
+// written as a high and a low bf16 part (together 16 significant bits).  K'^T V is summed from zero and added
+// to S in fp32: the tensor cores cut their sums off towards zero, so products onto S itself lost 5e-7 of
+// it a chunk (64 chunks of slow decays: off by 3.1e-5; now 9e-7 to 3e-6 at any length).  A and the copy of S
+// that Q S reads are rounded to bf16, as the outputs are.
 // exp(-G_j) grows with the decay: a chunk that decays by more than 2^80 takes, block of 32 tokens by
 // block, A_ij = scale exp(G_i - G_j) b_j (q_i . k_j) instead, from sums over the tokens between i and j alone.
 // The exponents of K' are sums over the tokens after j, so a large decay early in a chunk costs later tokens
@@ -15,8 +17,8 @@
 // chunks; every role below runs the same stream of chunks, so the next unit's loads and products
 // start while the last one's outputs are still being written.
 //   scores  4 warps, a row a thread: Q K^T from tensor memory, times the decays, back to it as A
-//   state   4 warps, a row of S a thread: S from tensor memory, bf16 copy to shared memory, S times the
-//           chunk's decay back
+//   state   4 warps, a row of S a thread: S times the last chunk's decay plus its K'^T V, both in tensor memory,
+//           back there in fp32 and as a bf16 copy to shared memory
 //   output  4 warps, a row a thread: out from Q S and A V, rounded, through the dead v tile to memory
 //   keys    8 warps, half a token a thread: K' as a high and a low part from the k tile
 //   decays  1 warp: sums of the log decays and the weights made of them, ahead of the others
@@ -24,9 +26,10 @@
 //   issue   1 thread: all products, in the order Q K^T, Q S, K'^T V (64 columns after the others, so that the
 //           state warps begin the next chunk meanwhile: 311 us, 320 in one), A V
 // Shared memory: v in two stages, k, q, both parts of K' and the copy of S once (32 KB each at 128 channels).
-// Tensor memory: Q K^T (then A) 128 columns, S and two buffers of Q S + A V dv columns each.
+// Tensor memory: Q K^T (then A) 128 columns, S and two buffers of dv columns each, which take turns as Q S + A V
+// and, between two chunks' outputs, as K'^T V.
 //
-// Measured: 8 prompts of 1.5k-5.8k tokens, 48 heads of 128 x 128: 311 us, 3.4 TB/s (HBM's floor is 156 us), tensor
+// Measured: 8 prompts of 1.5k-5.8k tokens, 48 heads of 128 x 128: 315 us, 3.3 TB/s (HBM's floor is 156 us), tensor
 // pipe 30 % and issue slots 44 % busy.  A chunk takes 3.5 us of an SM; its products need 1.7 us of the tensor
 // pipe.  What bounds it is the longest cycle through the roles, K'^T V -> S -> Q S, and the shared memory that all
 // of them read and write: about 600 KB a chunk (the operands of the products 288, tiles in and out 160, K' made of
@@ -50,7 +53,7 @@ constexpr int kTileQK = kChunk * 256;  // bytes of a q or k tile: two blocks of 
 struct ChunkShared {
     uint64_t v_full[2], v_empty[2];
     uint64_t g_full[2], g_empty[2], out[2], out_free[2];
-    uint64_t key_empty, k_full, k_empty, q_full, scores, a_ready, keys, q_used, s_init, s_ready, s_done[2], last;
+    uint64_t key_empty, k_full, k_empty, q_full, scores, a_ready, keys, q_used, s_init, s_ready, s_done[2], s_used, last;
     uint32_t tmem;
     int dead;
     int apart[2];  // why the chunk's Q S and A V are kept apart: 1 it decays by more than 2^80, 2 its v holds a NaN or inf
@@ -326,6 +329,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
         mbar_init(&sh->q_used, 1);
         mbar_init(&sh->s_init, 4);
         mbar_init(&sh->s_ready, 4);
+        mbar_init(&sh->s_used, 4);
         mbar_init(&sh->last, 1);
         mbar_init_fence();
     }
@@ -611,21 +615,52 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
             // the copy's rows go over every warp's quarter: all are through with theirs first
             arrive_warp(&sh->s_init);
             if (!wait_warp(&sh->s_init, units++ & 1, dead)) break;
-            float total = 1.0f;
+            float total = 1.0f, tot = 1.0f;  // decays of the unit so far, and of the last chunk
+            // 16 columns of S, and of the last chunk's products where there are any
+            auto current = [&](uint32_t *x, int j, bool products) {
+                tmem_ld16(x, ts + j);
+                if (!products) {
+                    tmem_wait_ld(x);
+                    return;
+                }
+                uint32_t y[16];
+                tmem_ld16(y, tl + kColO + (it & 1) * DV + j);
+                tmem_wait_ld(x);
+                tmem_tie(y);
+                const f2 tot2 = f2_pack(tot, tot);
+#pragma unroll
+                for (int e = 0; e < 16; e += 2) {
+                    float f0, f1;
+                    f2_unpack(f2_fma(f2_pack(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), tot2,
+                                     f2_pack(__uint_as_float(y[e]), __uint_as_float(y[e + 1]))),
+                              f0, f1);
+                    x[e] = __float_as_uint(f0), x[e + 1] = __float_as_uint(f1);
+                }
+            };
             for (int c = 0; c < u.chunks; ++c, ++it) {
                 const int stage = it & 1;
                 if (!wait_warp(&sh->g_full[stage], (it >> 1) & 1, dead)) {
                     ok = false;
                     break;
                 }
-                uint32_t v[16];
                 const float4 bt = *reinterpret_cast<const float4 *>(sh->tot[stage]);
                 arrive_warp(&sh->g_empty[stage]);
-                const float tot = exp2_fast((bt.x + bt.y) + (bt.z + bt.w));
-                const f2 tot2 = f2_pack(tot, tot);
-                total *= tot;
-                auto piece = [&](uint32_t *x, int j) {  // 16 columns: the copy, and times the decay back
-                    if (!so) {
+#pragma unroll 1
+                for (int h = 0; h < HALVES; ++h) {
+                    // the last chunk's products for this half are done, and the one that read its copy (at a
+                    // unit's start they were waited for at the end of the one before)
+                    if (c > 0 && !wait_warp(&sh->s_done[h], (it - 1) & 1, dead)) {
+                        ok = false;
+                        break;
+                    }
+                    tmem_fence_after();
+                    if (so && c == 0) continue;  // (from zero, and nothing reads a copy)
+#pragma unroll 1
+                    for (int j = h * 64; j < h * 64 + 64; j += 16) {
+                        uint32_t x[16];
+                        current(x, j, c > 0);
+                        if (c > 0) tmem_st16(ts + j, x);
+                        if (so) continue;
                         unsigned char *const at = s_copy + (j >> 6) * kBlock;
                         *reinterpret_cast<uint4 *>(at + swizzled(r, (j >> 3) & 7)) =
                             make_uint4(pack_bf16(__uint_as_float(x[0]), __uint_as_float(x[1])),
@@ -638,34 +673,14 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
                                        pack_bf16(__uint_as_float(x[12]), __uint_as_float(x[13])),
                                        pack_bf16(__uint_as_float(x[14]), __uint_as_float(x[15])));
                     }
-#pragma unroll
-                    for (int e = 0; e < 16; e += 2) {
-                        float f0, f1;
-                        f2_unpack(f2_mul(f2_pack(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), tot2), f0, f1);
-                        x[e] = __float_as_uint(f0), x[e + 1] = __float_as_uint(f1);
-                    }
-                    tmem_st16(ts + j, x);
-                };
-#pragma unroll 1
-                for (int h = 0; h < HALVES; ++h) {
-                    // the last chunk's products into this half of S are done, and the one that read its copy (at a
-                    // unit's start they were waited for at the end of the one before)
-                    if (c > 0 && !wait_warp(&sh->s_done[h], (it - 1) & 1, dead)) {
-                        ok = false;
-                        break;
-                    }
-                    tmem_fence_after();
-#pragma unroll 1
-                    for (int j = h * 64; j < h * 64 + 64; j += 16) {
-                        tmem_ld16(v, ts + j);
-                        tmem_wait_ld(v);
-                        piece(v, j);
-                    }
                 }
                 if (!ok) break;
+                tot = exp2_fast((bt.x + bt.y) + (bt.z + bt.w));
+                total *= tot;
                 tmem_wait_st();
                 tmem_fence_before();
                 fence_smem_to_async();
+                if (c > 0) arrive_warp(&sh->s_used);
                 arrive_warp(&sh->s_ready);
             }
             if (!ok || !wait_warp(&sh->s_done[HALVES - 1], (it - 1) & 1, dead)) {
@@ -679,8 +694,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
 #pragma unroll 1
                 for (int j = 0; j < DV; j += 16) {
                     uint32_t v[16];
-                    tmem_ld16(v, ts + j);
-                    tmem_wait_ld(v);
+                    current(v, j, true);
 #pragma unroll
                     for (int x = 0; x < 4; ++x)
                         dst[(j / 4 + x) * 128 + r] = make_float4(__uint_as_float(v[4 * x]), __uint_as_float(v[4 * x + 1]),
@@ -694,8 +708,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
 #pragma unroll 1
                     for (int j = 0; j < PW; j += 4) {
                         uint32_t v[16];
-                        tmem_ld16(v, ts + (h * PW + j) * 4);
-                        tmem_wait_ld(v);
+                        current(v, (h * PW + j) * 4, true);
 #pragma unroll
                         for (int x = 0; x < 4; ++x)
                             mine[lane * PW + ((j + x) ^ (lane & 7))] =
@@ -713,6 +726,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
                 }
                 __syncwarp();
             }
+            tmem_fence_before();
+            arrive_warp(&sh->s_used);
         }
     } else if (role == 2 && !so) {
         // ---------------------------------------------------------------------------- output
@@ -900,27 +915,29 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
                     mma_commit(lead, &sh->scores);
                     mma_commit(lead, &sh->k_empty);
                 }
-                // Q S and A V add up in one buffer, of two in turn; a chunk that keeps them apart takes both
+                // Q S and A V add up in one buffer, of two in turn.  K'^T V goes to the other, between the last
+                // chunk's outputs there and the next one's.  A chunk that keeps Q S and A V apart has A V there, once
+                // K'^T V has been read.
                 const uint32_t mine = tm + kColO + (it & 1) * DV, other = tm + kColO + (~it & 1) * DV;
-                if (!wait_warp(&sh->s_ready, it & 1, dead)) break;
+                if (!wait_warp(&sh->s_ready, it & 1, dead)) break;  // (the last K'^T V has been read from `mine`)
                 if (!so) {
-                    if ((it > 1 && !wait_warp(&sh->out_free[it & 1], ((it >> 1) & 1) ^ 1, dead)) ||
-                        (apart_before && !wait_warp(&sh->out_free[~it & 1], ((it - 1) >> 1) & 1, dead)))
-                        break;
+                    if (apart_before && !wait_warp(&sh->out_free[~it & 1], ((it - 1) >> 1) & 1, dead)) break;
                     tmem_fence_after();
 #pragma unroll 1
                     for (int x = 0; x < 8; ++x)
                         mma_ss(lead, mine, q + (((x >> 2) * kBlock + (x & 3) * 32) >> 4), sc + x * 128, id_av, x > 0);
                     mma_commit(lead, &sh->q_used);
                 }
-                if (!wait_warp(&sh->keys, it & 1, dead)) break;  // (these waited for v)
+                if (!wait_warp(&sh->keys, it & 1, dead) ||  // (these waited for v)
+                    (!so && it > 0 && !wait_warp(&sh->out_free[~it & 1], ((it - 1) >> 1) & 1, dead)))
+                    break;
                 tmem_fence_after();
 #pragma unroll 1
                 for (int h = 0; h < HALVES; ++h) {
 #pragma unroll 1
                     for (int x = 0; x < 8; ++x) {
-                        mma_ss(lead, tm + kColS + h * 64, hi + x * 128, v + h * (kBlock >> 4) + x * 128, id_kv, true);
-                        mma_ss(lead, tm + kColS + h * 64, lo + x * 128, v + h * (kBlock >> 4) + x * 128, id_kv, true);
+                        mma_ss(lead, other + h * 64, hi + x * 128, v + h * (kBlock >> 4) + x * 128, id_kv, x > 0);
+                        mma_ss(lead, other + h * 64, lo + x * 128, v + h * (kBlock >> 4) + x * 128, id_kv, true);
                     }
                     mma_commit(lead, &sh->s_done[h]);
                 }
@@ -928,7 +945,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
                 if (!so) {
                     if (!wait_warp(&sh->a_ready, it & 1, dead)) break;
                     const bool apart = *(volatile int *)&sh->apart[stage] != 0;
-                    if (apart && it > 0 && !apart_before && !wait_warp(&sh->out_free[~it & 1], ((it - 1) >> 1) & 1, dead)) break;
+                    if (apart && !wait_warp(&sh->s_used, it & 1, dead)) break;
                     tmem_fence_after();
 #pragma unroll 1
                     for (int x = 0; x < 8; ++x)

@@ -95,6 +95,8 @@ __device__ __forceinline__ void tmem_ld16(uint32_t *r, uint32_t addr) {
 __device__ __forceinline__ void tmem_wait_ld(uint32_t *r) {
     asm volatile("tcgen05.wait::ld.sync.aligned;\n" : CV_P16(r, 0)::"memory");
 }
+// The same for an array whose loads an earlier tmem_wait_ld has already waited for.
+__device__ __forceinline__ void tmem_tie(uint32_t *r) { asm volatile("" : CV_P16(r, 0)::"memory"); }
 // 8 columns at each of two addresses, and their wait.
 __device__ __forceinline__ void tmem_ld8x2(uint32_t *a, uint32_t *b, uint32_t addr_a, uint32_t addr_b) {
     asm volatile(

@@ -1,9 +1,10 @@
-"""GPU tests of bf16 prompts of linear attention: the precision that the header states."""
+"""GPU tests of bf16 prompts of linear attention: the precision that the header states, also along long prompts."""
 from __future__ import annotations
 
 import pytest
 import torch
 
+from layer_reference import linattn
 from test_gpu_linattn import Case
 
 pytestmark = pytest.mark.gpu
@@ -11,6 +12,21 @@ pytestmark = pytest.mark.gpu
 
 def relative(got, want):
     return float((got.detach().cpu().double() - want).norm() / want.norm())
+
+
+def copies(c, n):
+    """The one prompt of `c` n times over, in as many sequences of one call (each from its own copy of the state)."""
+    big = Case(n, c.nq, c.nh, c.dk, c.dv, "bf16" if c.dtype == torch.bfloat16 else "f32", counts=c.counts * n, seed=1)
+    x = c.tok["x"].repeat(n, 1)
+    for t in "qkv":
+        big.tok[t] = x.as_strided((x.shape[0], *c.tok[t].shape[1:]), c.tok[t].stride(), c.tok[t].storage_offset())
+    big.tok.update(x=x, g=c.tok["g"].repeat(n, 1), b=c.tok["b"].repeat(n, 1) if c.tok["b"] is not None else None)
+    big.state_wide[big.slot.long()] = c.state_wide[int(c.slot[0])].clone()
+    return big
+
+
+def workspace(cv, c, d):
+    return cv.linattn_workspace(d["q"], d["k"], d["v"], d["g"], d["state"], d["out"], d["cu"], max_seqlen=c.T)
 
 
 @pytest.mark.parametrize("dk,dv", [(64, 64), (128, 128)])
@@ -24,3 +40,24 @@ def test_bf16_prompt_precision_is_the_stated_one(cuda_lib, dk, dv):
     assert relative(d["out"], out) < 2 ** 0.5 * 2.0 ** -8
     slots = c.slot.long()
     assert relative(d["state"].cpu()[slots], state[slots]) < 2.0 ** -15
+
+
+@pytest.mark.parametrize("positive", [False, True])
+@pytest.mark.parametrize("length,n,cut", [(2048, 1, True), (2048, 160, False), (8192, 1, True), (8192, 160, False),
+                                          (32768, 1, True)])
+def test_state_keeps_its_bits_along_a_prompt(cuda_lib, length, n, cut, positive):
+    """The error of the state that a long prompt leaves, with decays near one, so that every chunk's roundings stay in
+    it.  Its terms carry 17 bits (2^-17 each); the sums are fp32.  Losing the keys' low part would
+    leave 1.7e-3, a state rounded to bf16 between chunks 4e-3."""
+    c = Case(1, 1, 1, 64, 64, "bf16", counts=[length], seed=length, decay=0.0005)
+    if positive:
+        c.tok["x"].abs_()
+    _, want, _, _ = linattn(c.state[int(c.slot[0])], None, c.tok["k"], c.tok["v"], c.tok["g"])
+    big = copies(c, n) if n > 1 else c
+    d = big.device()
+    assert (workspace(cuda_lib, big, d) > 0) == cut
+    big.prefill(cuda_lib, d)
+    got = d["state"].cpu()[big.slot.long()]
+    err = [relative(x, want) for x in got]
+    print(f"length {length} n {n} positive {positive}: {max(err):.2e}")
+    assert max(err) < 2.0 ** -15
