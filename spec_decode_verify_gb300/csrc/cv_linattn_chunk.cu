@@ -56,7 +56,9 @@ struct ChunkShared {
     uint64_t key_empty, k_full, k_empty, q_full, scores, a_ready, keys, q_used, s_init, s_ready, s_done[2], s_used, last;
     uint32_t tmem;
     int dead;
-    int apart[2];  // why the chunk's Q S and A V are kept apart: 1 it decays by more than 2^80, 2 its v holds a NaN or inf
+    // why the chunk's Q S and A V are kept apart: 1 it decays by more than 2^80, 2 its v holds a NaN or inf; and from
+    // bit 8 on, in which groups of 8 columns v does
+    int apart[2];
     // The work of sorted launches: first the full pieces, sequence by sequence (first: the number before a
     // sequence's own), then the shorter rests, longest first (order: their sequences).  Uncut, all are rests.
     uint8_t order[kChunkMaxSorted];
@@ -195,24 +197,54 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap *map, i
         : "memory");
 }
 
-// A NaN or an infinity in v spoils the rows above it in A V (0 * NaN).  This computes one row of the
-// outputs' part inside the chunk the long way, over the tokens up to the row itself only.
-__device__ __noinline__ void row_long_way(const LinattnParams &a, int row0, int h, int hq, int i, int c0, float *o) {
-    const uint16_t *q = reinterpret_cast<const uint16_t *>(a.tok.q) + (row0 + i) * a.tok.q_tok + hq * a.tok.q_head;
-    float dec = 1.0f;
-    for (int x = 0; x < 8; ++x) o[x] = 0.0f;
-    for (int j = i; j >= 0; --j) {
-        const long long row = row0 + j;
-        const uint16_t *k = reinterpret_cast<const uint16_t *>(a.tok.k) + row * a.tok.k_tok + hq * a.tok.k_head;
-        const uint16_t *v = reinterpret_cast<const uint16_t *>(a.tok.v) + row * a.tok.v_tok + (long long)h * a.tok.v_head;
-        float dot = 0.0f;
-        for (int x = 0; x < a.dk; ++x) dot = fmaf(widen<uint16_t>(q[x]), widen<uint16_t>(k[x]), dot);
-        float w = a.scale * dec * dot * (a.tok.b ? a.tok.b[row * a.tok.b_tok + h] : 1.0f);
-        if (j == i && a.skip) w += a.skip[h];
-        for (int x = 0; x < 8; ++x)
-            if (c0 + x < a.dv) o[x] = fmaf(w, widen<uint16_t>(v[c0 + x]), o[x]);
-        dec *= exp2_fast(clamp_log2(a.tok.g[row * a.tok.g_tok + h]));
+// A NaN or an infinity in v spoils its column for the rows above it in A V (0 * NaN).  This computes 8 columns of
+// row i of A V again, over the tokens up to the row itself only, from A in tensor memory: a warp's lanes hold 32 rows of
+// v and pass them around (a prompt of 2048 tokens, one head: 52 us, with an infinity in every chunk 60, in every
+// column of every chunk 135).
+__device__ __noinline__ void row_long_way(const LinattnParams &a, long long row0, int rows, int h, uint32_t tp, int i, int c0,
+                                          float *o) {
+    const uint16_t *const v =
+        reinterpret_cast<const uint16_t *>(a.tok.v) + row0 * a.tok.v_tok + (long long)h * a.tok.v_head + c0;
+    const int lane = i & 31;
+    float sum[8];
+#pragma unroll
+    for (int x = 0; x < 8; ++x) sum[x] = 0.0f;
+#pragma unroll 1
+    for (int b = 0; b <= i >> 5; ++b) {
+        uint4 mine = make_uint4(0u, 0u, 0u, 0u);
+        if (32 * b + lane < rows) mine = __ldg(reinterpret_cast<const uint4 *>(v + (long long)(32 * b + lane) * a.tok.v_tok));
+        uint32_t w[16];
+        tmem_ld16(w, tp + 16 * b);
+        tmem_wait_ld(w);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+            const uint32_t r[4] = {__shfl_sync(0xffffffffu, mine.x, j), __shfl_sync(0xffffffffu, mine.y, j),
+                                   __shfl_sync(0xffffffffu, mine.z, j), __shfl_sync(0xffffffffu, mine.w, j)};
+            const float f = __uint_as_float(j & 1 ? w[j / 2] & 0xffff0000u : w[j / 2] << 16);
+            if (32 * b + j <= i) {
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    sum[2 * x] = fmaf(f, __uint_as_float(r[x] << 16), sum[2 * x]);
+                    sum[2 * x + 1] = fmaf(f, __uint_as_float(r[x] & 0xffff0000u), sum[2 * x + 1]);
+                }
+            }
+        }
     }
+#pragma unroll
+    for (int x = 0; x < 8; ++x) o[x] = sum[x];
+}
+
+// A bit at `shift` and above for each group of 8 columns in which the warp's rows of a tile of v hold a NaN or inf.
+__device__ __noinline__ void note_bad(const unsigned char *vt, int t, int shift, int *apart) {
+    int where = 0;
+#pragma unroll 1
+    for (int x = 0; x < 8; ++x) {
+        const uint4 w = *reinterpret_cast<const uint4 *>(vt + swizzled(t, x));
+        const uint32_t high = ((w.x & 0x7f807f80u) + 0x00800080u) | ((w.y & 0x7f807f80u) + 0x00800080u) |
+                              ((w.z & 0x7f807f80u) + 0x00800080u) | ((w.w & 0x7f807f80u) + 0x00800080u);
+        if (__any_sync(0xffffffffu, high & 0x80008000u)) where |= 1 << x;
+    }
+    if ((t & 31) == 0) atomicOr(apart, 2 | where << shift);
 }
 
 // Two elements of k times the weight, as a high and a low bf16 part: off by 2^-17 of a term at most, about 4e-6 of
@@ -753,12 +785,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
                     break;
                 }
                 tmem_fence_after();
-                const bool v_bad = *(volatile int *)&sh->apart[stage] & 2;
+                const int bad = *(volatile int *)&sh->apart[stage] >> 1;  // v holds a NaN or inf; from bit 7 on, where
                 arrive_warp(&sh->g_empty[stage]);
                 const int t0 = c * kChunk;
                 unsigned char *const vt = v_tile + stage * kTileV;  // v is used up: the rows go through its tile
                 const uint32_t to = tl + kColO + (it & 1) * DV, ta = tl + kColO + (~it & 1) * DV;
-                if (!strong && !v_bad) {
+                if (!strong && !bad) {
                     const f2 pre2 = f2_pack(pre, pre);
 #pragma unroll 2
                     for (int j = 0; j < DV; j += 16) {
@@ -776,7 +808,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
                         *reinterpret_cast<uint4 *>(at + swizzled(i, ((j >> 3) & 7) + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
                     }
                 } else {
-                    // a NaN or an infinity in v has spoiled its column in all rows of A V: the long way then
+                    // where a NaN or an infinity in v has spoiled columns of A V: the long way
                     const float post = strong ? 1.0f : pre;
 #pragma unroll 1
                     for (int j = 0; j < DV; j += 8) {
@@ -785,12 +817,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
                         tmem_ld8x2(x, y, to + j, ta + j);
                         tmem_wait_ld8x2(x, y);
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) part[e] = post * __uint_as_float(y[e]);
-                        if (v_bad && t0 + i < u.n) row_long_way(a, u.row0 + t0, u.h, u.hq, i, j, part);
+                        for (int e = 0; e < 8; ++e) part[e] = __uint_as_float(y[e]);
+                        if (bad >> (7 + j / 8) & 1) row_long_way(a, u.row0 + t0, u.n - t0, u.h, tl + kColP, i, j, part);
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
-                            o[e] = pack_bf16(fmaf(pre, __uint_as_float(x[2 * e]), part[2 * e]),
-                                             fmaf(pre, __uint_as_float(x[2 * e + 1]), part[2 * e + 1]));
+                            o[e] = pack_bf16(fmaf(pre, __uint_as_float(x[2 * e]), post * part[2 * e]),
+                                             fmaf(pre, __uint_as_float(x[2 * e + 1]), post * part[2 * e + 1]));
                         *reinterpret_cast<uint4 *>(vt + (j >> 6) * kBlock + swizzled(i, (j >> 3) & 7)) =
                             make_uint4(o[0], o[1], o[2], o[3]);
                         __syncwarp();
@@ -877,7 +909,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
                         high |= ((w.x & 0x7f807f80u) + 0x00800080u) | ((w.y & 0x7f807f80u) + 0x00800080u) |
                                 ((w.z & 0x7f807f80u) + 0x00800080u) | ((w.w & 0x7f807f80u) + 0x00800080u);
                     }
-                    if (__any_sync(0xffffffffu, high & 0x80008000u) && lane == 0) atomicOr(&sh->apart[stage], 2);
+                    if (__any_sync(0xffffffffu, high & 0x80008000u)) note_bad(vt, t, 8 + 8 * half, &sh->apart[stage]);
                 }
                 // (an arrival before the last chunk's phase is over would count there)
                 if (it > 0 && !wait_warp(&sh->a_ready, (it - 1) & 1, dead)) {
@@ -894,7 +926,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
                        hi = desc_mn(smem_u32(hi_tile), kBlock), lo = desc_mn(smem_u32(lo_tile), kBlock);
         constexpr uint32_t id_qk = mma_desc(128, false, false),
                            id_kv = mma_desc(64, true, true), id_av = mma_desc(DV, false, true);
-        bool apart_before = false;
+        bool apart_before = false, bad_before = false;
         bool ok = true;
         for (int n = 0, idx; ok && (idx = unit_index(p, sh, n)) != -1; ++n) {
             if (idx < 0) continue;
@@ -904,8 +936,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
                 const uint32_t v = desc_mn(smem_u32(v_tile + stage * kTileV), kBlock);
                 ok = false;
                 if (!so) {
-                    // the last chunk's A, under the scores, is used up by the products before these
-                    if (!wait_warp(&sh->k_full, it & 1, dead) || !wait_warp(&sh->q_full, it & 1, dead)) break;
+                    // the last chunk's A, under the scores, is used up by the products before these, unless the output
+                    // warps read it too
+                    if (!wait_warp(&sh->k_full, it & 1, dead) || !wait_warp(&sh->q_full, it & 1, dead) ||
+                        (bad_before && !wait_warp(&sh->out_free[~it & 1], ((it - 1) >> 1) & 1, dead)))
+                        break;
                     tmem_fence_after();
 #pragma unroll 1
                     for (int x = 0; x < 8; ++x) {
@@ -944,14 +979,15 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
                 if (so) mma_commit(lead, &sh->v_empty[stage]);
                 if (!so) {
                     if (!wait_warp(&sh->a_ready, it & 1, dead)) break;
-                    const bool apart = *(volatile int *)&sh->apart[stage] != 0;
+                    const int why = *(volatile int *)&sh->apart[stage];
+                    const bool apart = why != 0;
                     if (apart && !wait_warp(&sh->s_used, it & 1, dead)) break;
                     tmem_fence_after();
 #pragma unroll 1
                     for (int x = 0; x < 8; ++x)
                         mma_ts(lead, apart ? other : mine, tm + kColP + x * 8, v + x * 128, id_av, !apart || x > 0);
                     mma_commit(lead, &sh->out[it & 1]);
-                    apart_before = apart;
+                    apart_before = apart, bad_before = (why & 2) != 0;
                 }
                 ok = true;
             }

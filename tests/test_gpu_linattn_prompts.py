@@ -61,3 +61,59 @@ def test_state_keeps_its_bits_along_a_prompt(cuda_lib, length, n, cut, positive)
     err = [relative(x, want) for x in got]
     print(f"length {length} n {n} positive {positive}: {max(err):.2e}")
     assert max(err) < 2.0 ** -15
+
+
+def timed(run, passes=5):
+    """The shortest of a few passes, in us."""
+    run()
+    best = float("inf")
+    for _ in range(passes):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        run()
+        b.record()
+        torch.cuda.synchronize()
+        best = min(best, a.elapsed_time(b) * 1e3)
+    return best
+
+
+@pytest.mark.parametrize("where", [(3,), (0, 9, 64, 127), tuple(range(128))])
+def test_an_infinity_in_every_chunk_costs_little(cuda_lib, where):
+    """A prompt whose v overflowed here and there takes about as long as any other: each of the 16 groups of 8 columns
+    is 1/16 of A V again, a product at a time, which is no more than the whole chunk; 20 times covers all of them."""
+    c = Case(1, 1, 1, 128, 128, "bf16", counts=[16 * 128], seed=41)
+    d = c.device()
+    run = lambda: cuda_lib.linattn_prefill(d["q"], d["k"], d["v"], d["g"], d["state"], d["out"], d["cu"],  # noqa: E731
+                                           max_seqlen=c.T, cache_idx=d["slot"])
+    clean = timed(run)
+    d["v"][5::128, 0, list(where)] = float("inf")
+    bad = timed(run)
+    print(f"columns {len(where)}: {clean:.1f} us, with an infinity in every chunk {bad:.1f}")
+    assert bad < 20 * clean
+
+
+@pytest.mark.parametrize("dk,dv", [(64, 64), (128, 128), (40, 96)])
+@pytest.mark.parametrize("decay", [0.1, 3.0])
+@pytest.mark.parametrize("skip", [False, True])
+def test_nonfinite_values_spoil_their_columns_alone(cuda_lib, dk, dv, decay, skip):
+    """NaN and infinities in v, several a chunk and in some chunks only: every other column of every output is as
+    without them, before and after, and so are the spoiled columns' outputs up to the first bad token."""
+    c = Case(3, 1, 2, dk, dv, "bf16", counts=[700, 130, 260], seed=42, gain=True, skip=skip, decay=decay)
+    clean = Case(3, 1, 2, dk, dv, "bf16", counts=[700, 130, 260], seed=42, gain=True, skip=skip, decay=decay)
+    v = c.tok["v"]
+    bad = [(130, 0, 3, float("inf")), (131, 0, 3, float("nan")), (200, 1, dv - 1, float("-inf")), (255, 0, 17, float("nan")),
+           (640, 1, 8, float("inf")), (700 + 127, 0, 0, float("inf")), (830 + 3, 1, 5, float("nan"))]
+    for t, h, col, x in bad:
+        v[t, h, col] = x
+    d = c.prefill(cuda_lib)
+    out, lim, state, slim = clean.expect(True, chunked=True)
+    ok = torch.ones_like(out, dtype=torch.bool)
+    fine = torch.ones_like(state, dtype=torch.bool)
+    for t, h, col, _ in bad:
+        s = 0 if t < 700 else 1 if t < 830 else 2
+        ok[t:c.cu[s + 1], h, col] = False
+        fine[int(c.slot[s]), h, :, col] = False
+    assert not torch.isfinite(torch.stack([d["out"][t, h, col] for t, h, col, _ in bad])).any()
+    got, left = d["out"].cpu().double(), d["state"].cpu().double()
+    assert ((got - out).abs()[ok] <= lim.expand_as(out)[ok]).all()
+    assert ((left - state).abs()[fine] <= slim.expand_as(state)[fine]).all()
