@@ -200,7 +200,7 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap *map, i
 // A NaN or an infinity in v spoils its column for the rows above it in A V (0 * NaN).  This computes 8 columns of
 // row i of A V again, over the tokens up to the row itself only, from A in tensor memory: a warp's lanes hold 32 rows of
 // v and pass them around (a prompt of 2048 tokens, one head: 52 us, with an infinity in every chunk 60, in every
-// column of every chunk 135).
+// column of every chunk 135; with the state mended as well, below, 111 and 263).
 __device__ __noinline__ void row_long_way(const LinattnParams &a, long long row0, int rows, int h, uint32_t tp, int i, int c0,
                                           float *o) {
     const uint16_t *const v =
@@ -234,17 +234,97 @@ __device__ __noinline__ void row_long_way(const LinattnParams &a, long long row0
     for (int x = 0; x < 8; ++x) o[x] = sum[x];
 }
 
+// Whether one of 8 bf16 values is a NaN or an infinity: its exponent plus one carries into the sign.
+__device__ __forceinline__ uint32_t carries(uint32_t w) { return (w & 0x7f807f80u) + 0x00800080u; }
+__device__ __forceinline__ uint32_t carries(const uint4 &w) { return carries(w.x) | carries(w.y) | carries(w.z) | carries(w.w); }
+constexpr uint32_t kCarry = 0x80008000u;
+
 // A bit at `shift` and above for each group of 8 columns in which the warp's rows of a tile of v hold a NaN or inf.
 __device__ __noinline__ void note_bad(const unsigned char *vt, int t, int shift, int *apart) {
     int where = 0;
 #pragma unroll 1
     for (int x = 0; x < 8; ++x) {
         const uint4 w = *reinterpret_cast<const uint4 *>(vt + swizzled(t, x));
-        const uint32_t high = ((w.x & 0x7f807f80u) + 0x00800080u) | ((w.y & 0x7f807f80u) + 0x00800080u) |
-                              ((w.z & 0x7f807f80u) + 0x00800080u) | ((w.w & 0x7f807f80u) + 0x00800080u);
-        if (__any_sync(0xffffffffu, high & 0x80008000u)) where |= 1 << x;
+        if (__any_sync(0xffffffffu, carries(w) & kCarry)) where |= 1 << x;
     }
     if ((t & 31) == 0) atomicOr(apart, 2 | where << shift);
+}
+
+// An infinity in k, v or the gain leaves a NaN in K'^T V (of two parts of K', or of the zeros past the end of k), where
+// the recurrence has an infinity.  Outputs that depend on it are not finite either way.  For the state a
+// unit leaves, this goes through its tokens again: an element that is NaN becomes what the
+// tokens that are not finite (and those that drop the state) add up to, since no finite one
+// changes it.  Piece q of the thread's row, 4 columns from c0 + 4 q on, is at[(q ^ flip) * step].
+__device__ __noinline__ void mend_state(const LinattnChunkParams &p, const ChunkShared *sh, int idx, float4 *at, int flip, int step,
+                                        int c0, int pieces) {
+    const LinattnParams &a = p.a;
+    const Unit u = unit_of(p, sh, idx);
+    const int r = threadIdx.x & 127, lane = r & 31;
+    const float nan = __int_as_float(0x7fffffff);
+    unsigned mine[2] = {0u, 0u};  // the columns to mend
+    const float *const start = a.state + (long long)u.slot * a.st_slot + (long long)u.h * a.st_head + (long long)r * a.dv;
+    const float4 *const cut =
+        reinterpret_cast<const float4 *>(p.ws_state) + (((long long)u.s * a.n_heads + u.h) * p.n_segs + u.seg) * (32 * p.dv_pad) + r;
+#pragma unroll 1
+    for (int q = 0; q < pieces; ++q) {
+        const int c = c0 + 4 * q;
+        if (r >= a.dk || c >= a.dv) continue;
+        float4 f = make_float4(0.f, 0.f, 0.f, 0.f);  // the state before the unit
+        if (!p.state_only && (u.seg > 0 || u.init)) f = u.cut ? cut[(c >> 2) * 128] : *reinterpret_cast<const float4 *>(start + c);
+        float *const x = reinterpret_cast<float *>(at + (q ^ flip) * step);
+        const float before[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (isnan(x[e]) && !isnan(before[e])) {
+                mine[q >> 3] |= 1u << (4 * (q & 7) + e);
+                x[e] = isinf(before[e]) ? before[e] : 0.0f;
+            }
+    }
+    if (!__any_sync(0xffffffffu, mine[0] | mine[1])) return;
+    const uint16_t *const k = reinterpret_cast<const uint16_t *>(a.tok.k) + (long long)u.hq * a.tok.k_head;
+    const uint16_t *const v = reinterpret_cast<const uint16_t *>(a.tok.v) + (long long)u.h * a.tok.v_head + c0;
+#pragma unroll 1
+    for (int t = 0; t < u.n; t += 32) {
+        const bool in = t + lane < u.n;
+        const long long row = (long long)u.row0 + t;
+        float decay = 1.0f, gain = 1.0f;
+        uint32_t high = 0u;
+        if (in) {
+            decay = expf(__ldg(a.tok.g + (row + lane) * a.tok.g_tok + u.h));
+            if (a.tok.b) gain = __ldg(a.tok.b + (row + lane) * a.tok.b_tok + u.h);
+#pragma unroll 4
+            for (int x = 0; x < a.dk; x += 8) high |= carries(__ldg(reinterpret_cast<const uint4 *>(k + (row + lane) * a.tok.k_tok + x)));
+        }
+        const unsigned drop = __ballot_sync(0xffffffffu, !(decay > 0.0f));
+        const unsigned all = drop | __ballot_sync(0xffffffffu, (high & kCarry) || !(fabsf(gain) < INFINITY));
+#pragma unroll 1
+        for (int q = 0; q < pieces && c0 + 4 * q < a.dv; ++q) {
+            uint2 w = make_uint2(0u, 0u);
+            if (in) w = __ldg(reinterpret_cast<const uint2 *>(v + (row + lane) * a.tok.v_tok + 4 * q));
+            unsigned todo = all | __ballot_sync(0xffffffffu, (carries(w.x) | carries(w.y)) & kCarry);
+            const unsigned cols = mine[q >> 3] >> (4 * (q & 7)) & 15u;
+            float *const x = reinterpret_cast<float *>(at + (q ^ flip) * step);
+#pragma unroll 1
+            for (; todo; todo &= todo - 1) {
+                const int j = __ffs(todo) - 1;
+                const uint32_t w0 = __shfl_sync(0xffffffffu, w.x, j), w1 = __shfl_sync(0xffffffffu, w.y, j);
+                const float kb = __shfl_sync(0xffffffffu, gain, j) * (r < a.dk ? widen<uint16_t>(__ldg(k + (row + j) * a.tok.k_tok + r)) : 0.0f);
+                const float e = __shfl_sync(0xffffffffu, decay, j), f = drop >> j & 1 ? e : 1.0f;
+                const float y[4] = {__uint_as_float(w0 << 16), __uint_as_float(w0 & 0xffff0000u), __uint_as_float(w1 << 16),
+                                    __uint_as_float(w1 & 0xffff0000u)};
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (cols >> i & 1) x[i] = fmaf(f, x[i], kb * y[i]);
+            }
+        }
+    }
+#pragma unroll 1
+    for (int q = 0; q < pieces; ++q) {  // a NaN of finite tokens (sums past fp32) stays one
+        float *const x = reinterpret_cast<float *>(at + (q ^ flip) * step);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if ((mine[q >> 3] >> (4 * (q & 7) + i) & 1) && fabsf(x[i]) < INFINITY) x[i] = nan;
+    }
 }
 
 // Two elements of k times the weight, as a high and a low bf16 part: off by 2^-17 of a term at most, about 4e-6 of
@@ -723,30 +803,40 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
             // the state after it
             if (so) {
                 float4 *dst = reinterpret_cast<float4 *>(p.ws_state) + (wsi + u.seg + 1) * (32 * DV);
+                bool nan = false;
 #pragma unroll 1
                 for (int j = 0; j < DV; j += 16) {
                     uint32_t v[16];
                     current(v, j, true);
 #pragma unroll
+                    for (int x = 0; x < 16; ++x) nan |= isnan(__uint_as_float(v[x]));
+#pragma unroll
                     for (int x = 0; x < 4; ++x)
                         dst[(j / 4 + x) * 128 + r] = make_float4(__uint_as_float(v[4 * x]), __uint_as_float(v[4 * x + 1]),
                                                                  __uint_as_float(v[4 * x + 2]), __uint_as_float(v[4 * x + 3]));
                 }
+                if (__any_sync(0xffffffffu, nan))
+#pragma unroll 1
+                    for (int h = 0; h < HALVES; ++h) mend_state(p, sh, idx, dst + h * (16 * 128) + r, 0, 128, 64 * h, 16);
                 if (r == 0) p.ws_decay[wsi + u.seg] = total;
             } else if (u.last) {
 #pragma unroll 1
                 for (int h = 0; h < PASSES; ++h) {
+                    bool nan = false;
                     __syncwarp();
 #pragma unroll 1
                     for (int j = 0; j < PW; j += 4) {
                         uint32_t v[16];
                         current(v, (h * PW + j) * 4, true);
 #pragma unroll
+                        for (int x = 0; x < 16; ++x) nan |= isnan(__uint_as_float(v[x]));
+#pragma unroll
                         for (int x = 0; x < 4; ++x)
                             mine[lane * PW + ((j + x) ^ (lane & 7))] =
                                 make_float4(__uint_as_float(v[4 * x]), __uint_as_float(v[4 * x + 1]),
                                             __uint_as_float(v[4 * x + 2]), __uint_as_float(v[4 * x + 3]));
                     }
+                    if (__any_sync(0xffffffffu, nan)) mend_state(p, sh, idx, mine + lane * PW, lane & 7, 1, h * PW * 4, PW);
                     __syncwarp();
 #pragma unroll 4
                     for (int e = lane; e < 32 * PW; e += 32) {
@@ -902,14 +992,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
                 arrive_warp(&sh->keys);
                 if (so) continue;
                 if (half * 64 < DV) {  // while the state's products run: is there a NaN or an infinity in v?
-                    uint32_t high = 0u;  // of exponents plus one: set where it is all ones
+                    uint32_t high = 0u;
 #pragma unroll 2
-                    for (int x = 0; x < 8; ++x) {
-                        const uint4 w = *reinterpret_cast<const uint4 *>(vt + swizzled(t, x));
-                        high |= ((w.x & 0x7f807f80u) + 0x00800080u) | ((w.y & 0x7f807f80u) + 0x00800080u) |
-                                ((w.z & 0x7f807f80u) + 0x00800080u) | ((w.w & 0x7f807f80u) + 0x00800080u);
-                    }
-                    if (__any_sync(0xffffffffu, high & 0x80008000u)) note_bad(vt, t, 8 + 8 * half, &sh->apart[stage]);
+                    for (int x = 0; x < 8; ++x) high |= carries(*reinterpret_cast<const uint4 *>(vt + swizzled(t, x)));
+                    if (__any_sync(0xffffffffu, high & kCarry)) note_bad(vt, t, 8 + 8 * half, &sh->apart[stage]);
                 }
                 // (an arrival before the last chunk's phase is over would count there)
                 if (it > 0 && !wait_warp(&sh->a_ready, (it - 1) & 1, dead)) {

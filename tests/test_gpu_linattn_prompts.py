@@ -4,7 +4,7 @@ from __future__ import annotations
 import pytest
 import torch
 
-from layer_reference import linattn
+from layer_reference import assert_within, linattn
 from test_gpu_linattn import Case
 
 pytestmark = pytest.mark.gpu
@@ -117,3 +117,35 @@ def test_nonfinite_values_spoil_their_columns_alone(cuda_lib, dk, dv, decay, ski
     got, left = d["out"].cpu().double(), d["state"].cpu().double()
     assert ((got - out).abs()[ok] <= lim.expand_as(out)[ok]).all()
     assert ((left - state).abs()[fine] <= slim.expand_as(state)[fine]).all()
+
+
+@pytest.mark.parametrize("counts,nh,dk,dv", [([300, 140], 2, 64, 64), ([3000, 200], 1, 64, 128), ([500], 2, 40, 96),
+                                             ([1200, 129], 1, 128, 128)])
+@pytest.mark.parametrize("where", ["k", "v", "both"])
+@pytest.mark.parametrize("gain", [False, True])
+def test_the_state_holds_the_infinities_of_the_definition(cuda_lib, counts, nh, dk, dv, where, gain):
+    """Infinities and NaN in k and v leave those infinities and NaN in the state that the recurrence does (inf + finite
+    stays inf, inf - inf is NaN), in the pieces of cut prompts and in whole ones, and all else as it is."""
+    c = Case(len(counts), 1, nh, dk, dv, "bf16", counts=counts, seed=43, gain=gain, decay=0.02)
+    d = c.device()
+    assert (workspace(cuda_lib, c, d) > 0) == (counts[0] >= 1000)
+    inf = float("inf")
+    if where != "v":
+        c.tok["k"][130, 0, 3], c.tok["k"][131, 0, 5], c.tok["k"][250, 0, 5] = inf, -inf, inf
+        c.tok["k"][counts[0] - 1, 0, 8] = float("nan")
+    if where != "k":
+        c.tok["v"][5, 0, 3], c.tok["v"][200, 0, 9], c.tok["v"][201, nh - 1, dv - 1] = inf, -inf, -inf
+        c.tok["v"][290, 0, 0], c.tok["v"][290, 0, dv - 8] = float("nan"), inf
+    d = c.prefill(cuda_lib)
+    _, _, state, slim = c.expect(True, chunked=True)
+    assert torch.isinf(state).any() and d["err"].tolist() == [0] * len(counts)
+    assert_within(d["state"], state, slim, "state")
+
+
+def test_infinite_gains_and_initial_states(cuda_lib):
+    c = Case(2, 1, 2, 64, 64, "bf16", counts=[300, 150], seed=44, gain=True, decay=0.02)
+    c.tok["b"][140, 0], c.tok["b"][20, 1] = float("inf"), float("nan")
+    c.state[int(c.slot[1]), 0, 7, 9], c.state[int(c.slot[1]), 1, 3, 4] = float("-inf"), float("nan")
+    d = c.prefill(cuda_lib)
+    _, _, state, slim = c.expect(True, chunked=True)
+    assert_within(d["state"], state, slim, "state")
