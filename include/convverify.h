@@ -51,7 +51,7 @@ extern "C" {
 #define CV_API
 #endif
 
-#define CV_ABI_VERSION 9
+#define CV_ABI_VERSION 10
 #define CV_MAX_T 128 /* draft tokens per verify call */
 
 typedef enum cv_dtype {
@@ -435,7 +435,7 @@ typedef struct cv_linattn_tokens {
  *   has_initial_state  int32 [n_seq] or NULL (all have one): 0 starts from a zero state, the slot's
  *                      old content is not read
  *   err                int32 [n_seq] or NULL: CV_SEQ_* bits (0 for fine and padded sequences).  A
- *                      flagged sequence is left untouched
+ *                      flagged sequence is left untouched (CV_SEQ_TIMEOUT apart: see wait_polls)
  * step only:
  *   prev               the previous step's drafts (q is not read; T = 0: none) and accept_len, int32
  *                      [n_seq], how many of them were accepted, 0..T_s (else CV_SEQ_BAD_ACCEPT): the
@@ -446,6 +446,12 @@ typedef struct cv_linattn_tokens {
  * prefill only:
  *   workspace          device buffer of at least the bytes cv_linattn_workspace reports, 256-byte
  *                      aligned; its content means nothing before and after the call.  NULL when 0
+ *   wait_polls         limit of each bounded wait of the kernel for bf16 prompts, in polls of up to
+ *                      20 us: 0 = the default (65536), negative = none.  A wait that gives up ends
+ *                      its block's work and flags CV_SEQ_TIMEOUT for all sequences that the block
+ *                      had a part of; their outputs and states may be partly written, unless the
+ *                      prompt was cut into pieces and failed in the first pass over them: then the
+ *                      sequence is left untouched
  * Preconditions the library cannot check: distinct sequences use distinct slots; out and state do not
  * overlap an input, each other, or the workspace.
  */
@@ -466,6 +472,7 @@ typedef struct cv_linattn_args {
     cv_linattn_tokens prev;
     const int32_t *accept_len;
     int32_t update_state;
+    int32_t wait_polls; /* prefill: limit of its bounded waits; 0 = the default */
     void *workspace;
     int64_t workspace_bytes;
 } cv_linattn_args;

@@ -106,7 +106,7 @@ class LinattnArgs(ctypes.Structure):
         ("scale", ctypes.c_float), ("n_slots", c_i32), ("tok", LinattnTokens), ("skip", c_vp), ("out", c_vp),
         ("out_seq_stride", c_i64), ("out_tok_stride", c_i64), ("out_head_stride", c_i64), ("state", c_vp),
         ("state_slot_stride", c_i64), ("state_head_stride", c_i64), ("cache_idx", c_vp), ("has_initial_state", c_vp),
-        ("err", c_vp), ("prev", LinattnTokens), ("accept_len", c_vp), ("update_state", c_i32), ("workspace", c_vp),
+        ("err", c_vp), ("prev", LinattnTokens), ("accept_len", c_vp), ("update_state", c_i32), ("wait_polls", c_i32), ("workspace", c_vp),
         ("workspace_bytes", c_i64),
     ]
 
@@ -571,7 +571,7 @@ def _linattn_tokens(q, k, v, log_decay, gain, cu, T, n_seq, check_device, what) 
 
 def make_linattn_args(q, k, v, log_decay, state, out, *, n_seq, gain=None, skip=None, scale=None, cu=None, T=None,
                       prev=None, update_state=False, cache_idx=None, has_initial_state=None, err=None,
-                      workspace=None, check_device=True) -> LinattnArgs:
+                      workspace=None, wait_polls=0, check_device=True) -> LinattnArgs:
     """Build cv_linattn_args (see linattn_prefill and linattn_step; q None: no tokens, prev alone)."""
     f32 = _f32 or _load_types()
     ss, st = state.shape, state.stride()
@@ -614,7 +614,7 @@ def make_linattn_args(q, k, v, log_decay, state, out, *, n_seq, gain=None, skip=
         n_seq, H, nq, dk, dv, BF16 if first.dtype is _bf16 else _dtype_code(first), dk ** -0.5 if scale is None else scale, n_slots, *tok, sk, o, os[0], os[1],
         os[2], _pointer(state, "state", check_device), st[0], st[1], _index_array(cache_idx, "cache_idx", n_seq, check_device),
         _index_array(has_initial_state, "has_initial_state", n_seq, check_device),
-        _index_array(err, "err", n_seq, check_device), *old, accept, 1 if update_state else 0, 0, ws, ws_bytes))
+        _index_array(err, "err", n_seq, check_device), *old, accept, 1 if update_state else 0, wait_polls, ws, ws_bytes))
 
 
 def linattn_workspace(q, k, v, log_decay, state, out, cu_seqlens, *, max_seqlen, **kw) -> int:
@@ -633,19 +633,20 @@ def _linattn_workspace(a: LinattnArgs) -> int:
 
 
 def linattn_prefill(q, k, v, log_decay, state, out, cu_seqlens, *, max_seqlen, gain=None, skip=None, scale=None,
-                    cache_idx=None, has_initial_state=None, err=None, workspace=None, stream=None) -> None:
+                    cache_idx=None, has_initial_state=None, err=None, workspace=None, wait_polls=0, stream=None) -> None:
     """Queue linear attention with a decay for each head over packed prompts (cv_linattn_prefill).
 
     q, k [total, n_qk_heads, dk], v and out [total, n_heads, dv] (innermost stride 1, the others free:
     slices of one conv output will do), log_decay and gain fp32 [total, n_heads], skip fp32 [n_heads],
     state fp32 [n_slots, n_heads, dk, dv], cu_seqlens int32 [n_seq + 1], max_seqlen a host bound on the
     lengths; scale defaults to dk**-0.5.  Writes out, state (and err).  workspace: a uint8 buffer of
-    linattn_workspace bytes; by default torch's allocator gives one for the call."""
+    linattn_workspace bytes; by default torch's allocator gives one for the call.  wait_polls: the limit of the
+    kernel's bounded waits (0: the default; negative: none, a wait gives up at once)."""
     if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
         raise ValueError("cu_seqlens must be [n_seq + 1]")
     a = make_linattn_args(q, k, v, log_decay, state, out, n_seq=cu_seqlens.shape[0] - 1, gain=gain, skip=skip,
                           scale=scale, cu=cu_seqlens, T=max_seqlen, cache_idx=cache_idx,
-                          has_initial_state=has_initial_state, err=err, workspace=workspace)
+                          has_initial_state=has_initial_state, err=err, workspace=workspace, wait_polls=wait_polls)
     lib, on = load_library(), _stream_of(stream, q)
     rc = lib.cv_linattn_prefill(ctypes.byref(a), on)
     if rc == ERR_WORKSPACE and workspace is None:  # nothing was launched: this call needs one

@@ -117,6 +117,7 @@ cvk::LinattnParams make_linattn(const cv_linattn_args *a, bool step) {
     p.o_vec = rows_of(4, a->out, a->out_seq_stride, a->out_tok_stride, a->out_head_stride, a->tok.cu, a->dv,
                       esize_of(a->dtype));
     p.scale = a->scale;
+    p.polls = a->wait_polls == 0 ? cvk::kPolls : a->wait_polls < 0 ? 0u : (unsigned)a->wait_polls;
     return p;
 }
 
@@ -294,8 +295,9 @@ ChunkPlan plan_chunks(const cv_linattn_args *a) {
     return pl;
 }
 
-int64_t chunk_workspace(const ChunkPlan &pl) {
-    return pl.ws_states * (cvk::kChunk * pl.dv_pad * 4) + (pl.ws_states * 4 + 255) / 256 * 256;
+int64_t chunk_workspace(const cv_linattn_args *a, const ChunkPlan &pl) {
+    if (pl.ws_states == 0) return 0;
+    return pl.ws_states * (cvk::kChunk * pl.dv_pad * 4) + ((pl.ws_states + a->n_seq) * 4 + 255) / 256 * 256;
 }
 
 int launch_chunks(const cv_linattn_args *a, const ChunkPlan &pl, cudaStream_t stream) {
@@ -310,10 +312,11 @@ int launch_chunks(const cv_linattn_args *a, const ChunkPlan &pl, cudaStream_t st
     p.sort = (units > sms || pl.pieces > 1) && a->n_seq <= cvk::kChunkMaxSorted;
     p.dv_pad = pl.dv_pad;
     if (pl.ws_states > 0) {
-        if (!a->workspace || !aligned(a->workspace, 256) || a->workspace_bytes < chunk_workspace(pl))
+        if (!a->workspace || !aligned(a->workspace, 256) || a->workspace_bytes < chunk_workspace(a, pl))
             return CV_ERR_WORKSPACE;
         p.ws_state = reinterpret_cast<float *>(a->workspace);
         p.ws_decay = p.ws_state + pl.ws_states * cvk::kChunk * pl.dv_pad;
+        p.ws_left = reinterpret_cast<int *>(p.ws_decay + pl.ws_states);
     }
     const cv_linattn_tokens &t = a->tok;
     if (t.total_tokens > 0 &&
@@ -466,7 +469,7 @@ int cv_linattn_workspace(const cv_linattn_args *args, int64_t *bytes) {
     *bytes = 0;
     if (args->n_seq == 0) return CV_OK;
     const ChunkPlan pl = plan_chunks(args);
-    *bytes = pl.pieces > 0 ? chunk_workspace(pl) : step_workspace(args, plan_step(args, make_linattn(args, false), false));
+    *bytes = pl.pieces > 0 ? chunk_workspace(args, pl) : step_workspace(args, plan_step(args, make_linattn(args, false), false));
     return CV_OK;
 }
 

@@ -45,6 +45,7 @@ struct LinattnParams {
     float *ws_state;  // [sequence][head][pieces][dk][dv]: the state before each piece of a cut sequence
     float *ws_decay;  // [sequence][head][pieces]: over a piece
     float scale;
+    unsigned polls;  // limit of the chunked kernel's waits
 };
 
 constexpr int kStepThreads = 256;
@@ -109,7 +110,9 @@ struct LinattnChunkParams {
     int state_only;  // the pieces' own states into the workspace, instead of outputs
     float *ws_state;  // [sequence][head][n_segs][dv / 4][128] groups of 4 columns of a state row, before each piece
     float *ws_decay;  // [sequence][head][n_segs]: over a piece
+    int *ws_left;     // [sequence]: nonzero where a piece's own state was not made (a wait gave up)
 };
+constexpr unsigned kPolls = 1u << 16;  // of a wait by default, up to 20 us each
 using LinattnChunkKernel = void (*)(LinattnChunkParams);
 struct ChunkKernel {
     LinattnChunkKernel fn;

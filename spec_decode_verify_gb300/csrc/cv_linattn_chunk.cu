@@ -35,8 +35,8 @@
 // of them read and write: about 600 KB a chunk (the operands of the products 288, tiles in and out 160, K' made of
 // k 96, the copy of S 32, the look for NaN in v 32), 2.4 us at 128 bytes a cycle.
 //
-// Every wait is bounded; one that gives up ends the block's work, flags the sequences it had left and
-// returns.
+// Every wait is bounded; one that gives up ends the block's work, flags its sequences and returns.  Where pieces' own
+// states were not made, the join notes their sequences and the launch for the outputs leaves those out.
 #include "cv_linattn.h"
 #include "cv_tcgen05.cuh"
 
@@ -45,8 +45,8 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kMinLog2 = -200.0f * kLog2e;
+constexpr float kNoDecay = -1.0f;  // in the place of a piece's decay (>= 0 or NaN): it was not made
 constexpr float kStrong = -80.0f;  // log2 of a chunk's decay from which on A is made block by block
-constexpr unsigned kPolls = 1u << 16;
 constexpr int kTileQK = kChunk * 256;  // bytes of a q or k tile: two blocks of 64 channels
 
 // Barriers, in order (8 bytes each), then the small arrays.
@@ -115,6 +115,7 @@ __device__ __forceinline__ Unit unit_of(const LinattnChunkParams &p, const Chunk
     const long long start = (long long)u.seg * p.seg_len;
     if (u.on && start >= L && u.seg > 0) u.on = false;
     if (u.on && p.state_only && start + p.seg_len >= L) u.on = false;
+    if (u.on && !p.state_only && L > p.seg_len && p.ws_left[u.s]) u.on = false;
     u.row0 = row0 + (int)(u.on ? start : 0);
     u.n = u.on ? min(p.seg_len, L - (int)start) : 0;
     u.chunks = (u.n + kChunk - 1) / kChunk;
@@ -135,6 +136,11 @@ __device__ __forceinline__ int unit_index(const LinattnChunkParams &p, const Chu
     return idx < units ? (int)idx : (long long)n * G < units ? -2 : -1;
 }
 
+// The block's bounded waits: polls of one wait, and the flag that one of them has given up.
+struct Waits {
+    volatile int *dead;
+    unsigned polls;
+};
 // One poll of a barrier's phase, which may suspend the thread for up to 20 us.
 __device__ __forceinline__ bool poll(uint64_t *bar, unsigned parity) {
     unsigned done;
@@ -155,26 +161,26 @@ __device__ __forceinline__ bool over(uint64_t *bar, unsigned parity) {
         : "memory");
     return __all_sync(0xffffffffu, done != 0);
 }
-__device__ __noinline__ bool wait_long(uint64_t *bar, unsigned parity, volatile int *dead) {
+__device__ __noinline__ bool wait_long(uint64_t *bar, unsigned parity, Waits waits) {
 #pragma unroll 1
-    for (unsigned i = 0; i < kPolls; ++i) {
+    for (unsigned i = 0; i < waits.polls; ++i) {
         if (__all_sync(0xffffffffu, poll(bar, parity))) return true;
-        if (__any_sync(0xffffffffu, *dead)) return false;
+        if (__any_sync(0xffffffffu, *waits.dead)) return false;
     }
-    *dead = 1;
+    *waits.dead = 1;
     return false;
 }
 // Bounded wait of a whole warp; false once the block has given up.
-__device__ __forceinline__ bool wait_warp(uint64_t *bar, unsigned parity, volatile int *dead) {
-    return over(bar, parity) || wait_long(bar, parity, dead);
+__device__ __forceinline__ bool wait_warp(uint64_t *bar, unsigned parity, Waits waits) {
+    return over(bar, parity) || wait_long(bar, parity, waits);
 }
-__device__ __forceinline__ bool wait_one(uint64_t *bar, unsigned parity, volatile int *dead) {
+__device__ __forceinline__ bool wait_one(uint64_t *bar, unsigned parity, Waits waits) {
 #pragma unroll 1
-    for (unsigned i = 0; i < kPolls; ++i) {
+    for (unsigned i = 0; i < waits.polls; ++i) {
         if (poll(bar, parity)) return true;
-        if (*dead) return false;
+        if (*waits.dead) return false;
     }
-    *dead = 1;
+    *waits.dead = 1;
     return false;
 }
 // One arrival for the warp, after all its lanes' earlier work.
@@ -447,6 +453,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
     }
     grid_dep_wait();
     grid_dep_launch();
+    if (so)
+        for (int s = blockIdx.x * kChunkThreads + tid; s < a.n_seq; s += gridDim.x * kChunkThreads) p.ws_left[s] = 0;
     if (p.sort) {
         // each sequence's full pieces and the length of its rest (-1 none; a sequence without tokens has one of
         // length zero; only pieces with a next one have states of their own)
@@ -479,7 +487,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
     __syncthreads();
     tmem_fence_after();
     const uint32_t tm = sh->tmem;
-    volatile int *const dead = &sh->dead;
+    const Waits waits{&sh->dead, a.polls};
     const int role = warp >> 2;
     const int w4 = warp & 3;  // the quarter of tensor memory this warp reaches
     const uint32_t tl = tm + ((uint32_t)(32 * w4) << 16);
@@ -528,8 +536,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
                 if (!strong) before += (block > 0 ? t0 : 0.0f) + (block > 1 ? t1 : 0.0f) + (block > 2 ? t2 : 0.0f);
                 const float ahead = (block < 1 ? t1 : 0.0f) + (block < 2 ? t2 : 0.0f) + (block < 3 ? t3 : 0.0f);
                 const int stage = it & 1;
-                if ((it > 1 && !wait_warp(&sh->g_empty[stage], ((it >> 1) & 1) ^ 1, dead)) ||
-                    (it > 0 && !wait_warp(&sh->key_empty, (it - 1) & 1, dead))) {
+                if ((it > 1 && !wait_warp(&sh->g_empty[stage], ((it >> 1) & 1) ^ 1, waits)) ||
+                    (it > 0 && !wait_warp(&sh->key_empty, (it - 1) & 1, waits))) {
                     ok = false;
                     break;
                 }
@@ -559,7 +567,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
             const Unit u = unit_of(p, sh, idx);
             for (int c = 0; c < u.chunks; ++c, ++it) {
                 const int row = u.row0 + c * kChunk;
-                if (it >= 1 && !wait_one(&sh->k_empty, (it - 1) & 1, dead)) {
+                if (it >= 1 && !wait_one(&sh->k_empty, (it - 1) & 1, waits)) {
                     ok = false;
                     break;
                 }
@@ -569,7 +577,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
                 tma_load(k + kBlock, &p.k_map, 64, u.hq, row, &sh->k_full);
                 ++k_sent;
                 if (!so) {
-                    if (it >= 1 && !wait_one(&sh->q_used, (it - 1) & 1, dead)) {
+                    if (it >= 1 && !wait_one(&sh->q_used, (it - 1) & 1, waits)) {
                         ok = false;
                         break;
                     }
@@ -600,7 +608,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
             }
             for (int c = 0; c < u.chunks; ++c, ++it) {
                 const int stage = it & 1, row = u.row0 + c * kChunk;
-                if (it >= 2 && !wait_one(&sh->v_empty[stage], ((it >> 1) & 1) ^ 1, dead)) {
+                if (it >= 2 && !wait_one(&sh->v_empty[stage], ((it >> 1) & 1) ^ 1, waits)) {
                     ok = false;
                     break;
                 }
@@ -622,7 +630,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
             const float skip = a.skip ? __ldg(a.skip + u.h) : 0.0f;
             for (int c = 0; c < u.chunks; ++c, ++it) {
                 const int stage = it & 1;
-                if (!wait_warp(&sh->g_full[stage], (it >> 1) & 1, dead) || !wait_warp(&sh->scores, it & 1, dead)) {
+                if (!wait_warp(&sh->g_full[stage], (it >> 1) & 1, waits) || !wait_warp(&sh->scores, it & 1, waits)) {
                     ok = false;
                     break;
                 }
@@ -726,7 +734,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
             tmem_wait_st();
             // the copy's rows go over every warp's quarter: all are through with theirs first
             arrive_warp(&sh->s_init);
-            if (!wait_warp(&sh->s_init, units++ & 1, dead)) break;
+            if (!wait_warp(&sh->s_init, units++ & 1, waits)) break;
             float total = 1.0f, tot = 1.0f;  // decays of the unit so far, and of the last chunk
             // 16 columns of S, and of the last chunk's products where there are any
             auto current = [&](uint32_t *x, int j, bool products) {
@@ -751,7 +759,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
             };
             for (int c = 0; c < u.chunks; ++c, ++it) {
                 const int stage = it & 1;
-                if (!wait_warp(&sh->g_full[stage], (it >> 1) & 1, dead)) {
+                if (!wait_warp(&sh->g_full[stage], (it >> 1) & 1, waits)) {
                     ok = false;
                     break;
                 }
@@ -761,7 +769,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
                 for (int h = 0; h < HALVES; ++h) {
                     // the last chunk's products for this half are done, and the one that read its copy (at a
                     // unit's start they were waited for at the end of the one before)
-                    if (c > 0 && !wait_warp(&sh->s_done[h], (it - 1) & 1, dead)) {
+                    if (c > 0 && !wait_warp(&sh->s_done[h], (it - 1) & 1, waits)) {
                         ok = false;
                         break;
                     }
@@ -795,7 +803,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
                 if (c > 0) arrive_warp(&sh->s_used);
                 arrive_warp(&sh->s_ready);
             }
-            if (!ok || !wait_warp(&sh->s_done[HALVES - 1], (it - 1) & 1, dead)) {
+            if (!ok || !wait_warp(&sh->s_done[HALVES - 1], (it - 1) & 1, waits)) {
                 ok = false;
                 break;
             }
@@ -860,7 +868,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
             const Unit u = unit_of(p, sh, idx);
             for (int c = 0; c < u.chunks; ++c, ++it) {
                 const int stage = it & 1;
-                if (!wait_warp(&sh->g_full[stage], (it >> 1) & 1, dead)) {
+                if (!wait_warp(&sh->g_full[stage], (it >> 1) & 1, waits)) {
                     ok = false;
                     break;
                 }
@@ -870,7 +878,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
                 const bool strong = !((bt.x + bt.y) + (bt.z + bt.w) > strong_at);
                 if (strong) G += (w4 > 0 ? bt.x : 0.0f) + (w4 > 1 ? bt.y : 0.0f) + (w4 > 2 ? bt.z : 0.0f);
                 const float pre = exp2_fast(G) * a.scale;
-                if (!wait_warp(&sh->out[it & 1], (it >> 1) & 1, dead)) {
+                if (!wait_warp(&sh->out[it & 1], (it >> 1) & 1, waits)) {
                     ok = false;
                     break;
                 }
@@ -945,7 +953,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
             const Unit u = unit_of(p, sh, idx);
             for (int c = 0; c < u.chunks; ++c, ++it) {
                 const int stage = it & 1;
-                if (!wait_warp(&sh->g_full[stage], (it >> 1) & 1, dead)) {
+                if (!wait_warp(&sh->g_full[stage], (it >> 1) & 1, waits)) {
                     ok = false;
                     break;
                 }
@@ -953,7 +961,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
                 arrive_warp(&sh->key_empty);
                 // K' has its place once the last chunk's products are done (and this role never runs two phases
                 // ahead of the issuing warp)
-                if (!wait_warp(&sh->k_full, it & 1, dead) || (it > 0 && !wait_warp(&sh->s_done[HALVES - 1], (it - 1) & 1, dead))) {
+                if (!wait_warp(&sh->k_full, it & 1, waits) || (it > 0 && !wait_warp(&sh->s_done[HALVES - 1], (it - 1) & 1, waits))) {
                     ok = false;
                     break;
                 }
@@ -980,7 +988,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
                 arrive_warp(&sh->k_empty);
                 unsigned char *const vt = v_tile + stage * kTileV + half * kBlock;
                 if (half * 64 < DV) {
-                    if (!wait_warp(&sh->v_full[stage], (it >> 1) & 1, dead)) {
+                    if (!wait_warp(&sh->v_full[stage], (it >> 1) & 1, waits)) {
                         ok = false;
                         break;
                     }
@@ -998,7 +1006,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
                     if (__any_sync(0xffffffffu, high & kCarry)) note_bad(vt, t, 8 + 8 * half, &sh->apart[stage]);
                 }
                 // (an arrival before the last chunk's phase is over would count there)
-                if (it > 0 && !wait_warp(&sh->a_ready, (it - 1) & 1, dead)) {
+                if (it > 0 && !wait_warp(&sh->a_ready, (it - 1) & 1, waits)) {
                     ok = false;
                     break;
                 }
@@ -1024,8 +1032,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
                 if (!so) {
                     // the last chunk's A, under the scores, is used up by the products before these, unless the output
                     // warps read it too
-                    if (!wait_warp(&sh->k_full, it & 1, dead) || !wait_warp(&sh->q_full, it & 1, dead) ||
-                        (bad_before && !wait_warp(&sh->out_free[~it & 1], ((it - 1) >> 1) & 1, dead)))
+                    if (!wait_warp(&sh->k_full, it & 1, waits) || !wait_warp(&sh->q_full, it & 1, waits) ||
+                        (bad_before && !wait_warp(&sh->out_free[~it & 1], ((it - 1) >> 1) & 1, waits)))
                         break;
                     tmem_fence_after();
 #pragma unroll 1
@@ -1040,17 +1048,17 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
                 // chunk's outputs there and the next one's.  A chunk that keeps Q S and A V apart has A V there, once
                 // K'^T V has been read.
                 const uint32_t mine = tm + kColO + (it & 1) * DV, other = tm + kColO + (~it & 1) * DV;
-                if (!wait_warp(&sh->s_ready, it & 1, dead)) break;  // (the last K'^T V has been read from `mine`)
+                if (!wait_warp(&sh->s_ready, it & 1, waits)) break;  // (the last K'^T V has been read from `mine`)
                 if (!so) {
-                    if (apart_before && !wait_warp(&sh->out_free[~it & 1], ((it - 1) >> 1) & 1, dead)) break;
+                    if (apart_before && !wait_warp(&sh->out_free[~it & 1], ((it - 1) >> 1) & 1, waits)) break;
                     tmem_fence_after();
 #pragma unroll 1
                     for (int x = 0; x < 8; ++x)
                         mma_ss(lead, mine, q + (((x >> 2) * kBlock + (x & 3) * 32) >> 4), sc + x * 128, id_av, x > 0);
                     mma_commit(lead, &sh->q_used);
                 }
-                if (!wait_warp(&sh->keys, it & 1, dead) ||  // (these waited for v)
-                    (!so && it > 0 && !wait_warp(&sh->out_free[~it & 1], ((it - 1) >> 1) & 1, dead)))
+                if (!wait_warp(&sh->keys, it & 1, waits) ||  // (these waited for v)
+                    (!so && it > 0 && !wait_warp(&sh->out_free[~it & 1], ((it - 1) >> 1) & 1, waits)))
                     break;
                 tmem_fence_after();
 #pragma unroll 1
@@ -1064,10 +1072,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
                 }
                 if (so) mma_commit(lead, &sh->v_empty[stage]);
                 if (!so) {
-                    if (!wait_warp(&sh->a_ready, it & 1, dead)) break;
+                    if (!wait_warp(&sh->a_ready, it & 1, waits)) break;
                     const int why = *(volatile int *)&sh->apart[stage];
                     const bool apart = why != 0;
-                    if (apart && !wait_warp(&sh->s_used, it & 1, dead)) break;
+                    if (apart && !wait_warp(&sh->s_used, it & 1, waits)) break;
                     tmem_fence_after();
 #pragma unroll 1
                     for (int x = 0; x < 8; ++x)
@@ -1083,13 +1091,16 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
         mbar_wait_bounded(&sh->last, 0, kPolls);
     }
     __syncwarp();
+    tmem_wait_st();  // (of a role that gave up)
     tmem_fence_before();
     __syncthreads();
-    if (*dead && tid == 0 && a.err)
+    if (*waits.dead && tid == 0)
         for (int n = 0, idx; (idx = unit_index(p, sh, n)) != -1; ++n)
             if (idx >= 0) {
                 const Unit u = unit_of(p, sh, idx);
-                if (u.on) atomicOr(a.err + u.s, kSeqTimeout);
+                if (!u.on) continue;
+                if (a.err) atomicOr(a.err + u.s, kSeqTimeout);
+                if (so) p.ws_decay[((long long)u.s * a.n_heads + u.h) * p.n_segs + u.seg] = kNoDecay;
             }
     if (warp == 23) {
         tmem_fence_after();
@@ -1121,6 +1132,7 @@ __global__ void __launch_bounds__(kJoinThreads) chunk_join(const __grid_constant
     const long long step = 32LL * dv_pad;
     // The first piece's state too: the last piece writes the sequence's while the first may not have begun.
     if (n > 0) *own = S;
+    bool left = false;
     for (int i0 = 0; i0 < n; i0 += 8) {
         float4 f[8];
         float d[8];
@@ -1130,11 +1142,13 @@ __global__ void __launch_bounds__(kJoinThreads) chunk_join(const __grid_constant
 #pragma unroll
         for (int x = 0; x < 8; ++x)
             if (i0 + x < n) {
+                left |= d[x] == kNoDecay;
                 S.x = fmaf(d[x], S.x, f[x].x), S.y = fmaf(d[x], S.y, f[x].y);
                 S.z = fmaf(d[x], S.z, f[x].z), S.w = fmaf(d[x], S.w, f[x].w);
                 own[(i0 + x + 1) * step] = S;
             }
     }
+    if (left && row == 0) p.ws_left[s] = 1;
 }
 
 }  // namespace
