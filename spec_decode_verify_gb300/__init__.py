@@ -236,7 +236,29 @@ def _stream_ptr(stream) -> Optional[int]:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-_current_stream = None
+_current_stream = _current_device = None
+
+
+def _one_device(*tensors) -> None:
+    """Raise unless all of a call's tensors are on the current CUDA device, which is the one that the library plans for
+    and launches on: a pointer of another device would be a bad address there."""
+    dev = None
+    for t in tensors:
+        if t is not None:
+            d = t.get_device()
+            if d != dev:
+                if d < 0:
+                    raise ValueError("every tensor of a call must be a CUDA tensor (there is no CPU path)")
+                if dev is not None:
+                    raise ValueError(f"the tensors of a call must be on one device, got cuda:{dev} and cuda:{d}")
+                dev = d
+    global _current_device
+    if dev is not None:
+        if _current_device is None:
+            import torch
+            _current_device = torch._C._cuda_getDevice
+        if dev != _current_device():
+            raise ValueError(f"the tensors are on cuda:{dev}, but the current device is cuda:{_current_device()}")
 
 
 def _stream_of(stream, t) -> int:
@@ -493,23 +515,19 @@ _NO_TOKENS = (0,) * 21
 _NORM = struct.Struct("<q6i2fQqQqQQqQqQQQq")
 
 
-def _pointer(t, name, check_device, required=True) -> int:
+def _pointer(t, name) -> int:
     if t is None:
-        if required:
-            raise ValueError(f"{name} is required")
-        return 0
-    if check_device and not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor (there is no CPU path)")
+        raise ValueError(f"{name} is required")
     return t.data_ptr()
 
 
-def _index_array(t, name, n, check_device) -> int:
+def _index_array(t, name, n) -> int:
     """Pointer of an int32 array of at least n elements, or 0."""
     if t is None:
         return 0
     if t.dtype is not _i32 or t.numel() < n or not t.is_contiguous():
         _need_int32(t, name, n=n)
-    return _pointer(t, name, check_device)
+    return t.data_ptr()
 
 
 # torch's types, looked up once (the package does not import torch by itself)
@@ -523,7 +541,7 @@ def _load_types():
     return _f32
 
 
-def _linattn_tokens(q, k, v, log_decay, gain, cu, T, n_seq, check_device, what) -> tuple:
+def _linattn_tokens(q, k, v, log_decay, gain, cu, T, n_seq, what) -> tuple:
     """The fields of cv_linattn_tokens for [n_seq, T, heads, d] rows, or packed [total, heads, d] rows with
     cu."""
     f32 = _f32 or _load_types()
@@ -561,9 +579,6 @@ def _linattn_tokens(q, k, v, log_decay, gain, cu, T, n_seq, check_device, what) 
         if T is not None and T != vs[1]:
             raise ValueError(f"{what}: T = {T} but the rows hold {vs[1]} tokens")
         T, total = vs[1], 0
-    if check_device and not (k.is_cuda and v.is_cuda and log_decay.is_cuda and (q is None or q.is_cuda) and
-                             (gain is None or gain.is_cuda) and (cu is None or cu.is_cuda)):
-        raise ValueError(f"{what}: expected a CUDA tensor (there is no CPU path)")
     return (int(T), total, cu.data_ptr() if packed else 0, q.data_ptr() if q is not None else 0, k.data_ptr(), v.data_ptr(),
             qt[0], qt[1], qt[2], kt[0], kt[1], kt[2], vt[0], vt[1], vt[2], log_decay.data_ptr(), gt[0], gt[1],
             gain.data_ptr() if gain is not None else 0, bt[0], bt[1])
@@ -584,37 +599,40 @@ def make_linattn_args(q, k, v, log_decay, state, out, *, n_seq, gain=None, skip=
     nq = first.shape[-2]
     tok, o, os = _NO_TOKENS, 0, (0, 0, 0)
     if q is not None:
-        tok = _linattn_tokens(q, k, v, log_decay, gain, cu, T, n_seq, check_device, "tokens")
+        tok = _linattn_tokens(q, k, v, log_decay, gain, cu, T, n_seq, "tokens")
         if q.shape[-1] != dk or v.shape[-2] != H or v.shape[-1] != dv:
             raise ValueError(f"heads of q|k [.., {q.shape[-1]}] and v {tuple(v.shape[-2:])} do not fit the state {tuple(ss)}")
         if out.shape != v.shape or out.dtype is not v.dtype or out.stride(-1) != 1:
             raise ValueError("out needs the shape and dtype of v and a unit innermost stride")
-        o, os = _pointer(out, "out", check_device), out.stride()
+        o, os = _pointer(out, "out"), out.stride()
         os = (0, os[0], os[1]) if cu is not None else os
     sk = 0
     if skip is not None:
         _need_shape(skip, "skip", (H,))
         if skip.dtype is not f32 or not skip.is_contiguous():
             raise ValueError("skip must be contiguous float32")
-        sk = _pointer(skip, "skip", check_device)
+        sk = skip.data_ptr()
     old, accept = _NO_TOKENS, 0
     if prev is not None:
         pk, pv = prev.k, prev.v
-        old = _linattn_tokens(None, pk, pv, prev.log_decay, prev.gain, prev.cu_draft, prev.T, n_seq, check_device,
+        old = _linattn_tokens(None, pk, pv, prev.log_decay, prev.gain, prev.cu_draft, prev.T, n_seq,
                               "previous drafts")
         if pk.dtype is not first.dtype or pk.shape[-2] != nq or pk.shape[-1] != dk or pv.shape[-2] != H or pv.shape[-1] != dv:
             raise ValueError("the previous drafts must have the dtype, heads and head sizes of the tokens")
         if prev.accept_len is None:
             raise ValueError("accept_len is required")
-        accept = _index_array(prev.accept_len, "accept_len", n_seq, check_device)
+        accept = _index_array(prev.accept_len, "accept_len", n_seq)
     ws, ws_bytes = 0, 0
     if workspace is not None:
-        ws, ws_bytes = _pointer(workspace, "workspace", check_device), workspace.numel() * workspace.element_size()
+        ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    if check_device:
+        _one_device(state, q, k, v, log_decay, out, gain, skip, cu, cache_idx, has_initial_state, err, workspace)
+        if prev is not None:
+            _one_device(state, prev.k, prev.v, prev.log_decay, prev.gain, prev.cu_draft, prev.accept_len)
     return LinattnArgs.from_buffer_copy(_LINATTN.pack(
         n_seq, H, nq, dk, dv, BF16 if first.dtype is _bf16 else _dtype_code(first), dk ** -0.5 if scale is None else scale, n_slots, *tok, sk, o, os[0], os[1],
-        os[2], _pointer(state, "state", check_device), st[0], st[1], _index_array(cache_idx, "cache_idx", n_seq, check_device),
-        _index_array(has_initial_state, "has_initial_state", n_seq, check_device),
-        _index_array(err, "err", n_seq, check_device), *old, accept, 1 if update_state else 0, wait_polls, ws, ws_bytes))
+        os[2], state.data_ptr(), st[0], st[1], _index_array(cache_idx, "cache_idx", n_seq),
+        _index_array(has_initial_state, "has_initial_state", n_seq), _index_array(err, "err", n_seq), *old, accept, 1 if update_state else 0, wait_polls, ws, ws_bytes))
 
 
 def linattn_workspace(q, k, v, log_decay, state, out, cu_seqlens, *, max_seqlen, **kw) -> int:
@@ -716,14 +734,14 @@ def make_norm_args(y, out, *, gate=None, gate_act=None, gate_first=False, group=
             raise ValueError(f"{name} needs a unit channel stride")
         if like and t.dtype is not dt:
             raise TypeError("y, gate and out must share one dtype")
-        return _pointer(t, name, check_device), st[0]
+        return t.data_ptr(), st[0]
 
     def vec(t, name, n):
         if t is None:
             return 0
         if t.dim() != 1 or t.shape[0] != n or t.dtype is not dt or not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous [{n}] and have the dtype of y")
-        return _pointer(t, name, check_device)
+        return t.data_ptr()
 
     if residual is None:
         if out is None or residual_out is not None or channel_scale is not None or pre_weight is not None:
@@ -731,6 +749,8 @@ def make_norm_args(y, out, *, gate=None, gate_act=None, gate_first=False, group=
                              "have no meaning")
     elif residual_out is None or residual_out.dtype is not residual.dtype:
         raise ValueError("residual needs residual_out of its dtype")
+    if check_device:
+        _one_device(y, out, gate, residual, residual_out, post_weight, channel_scale, pre_weight)
     code = BF16 if dt is _bf16 else _dtype_code(y)
     return NormArgs.from_buffer_copy(_NORM.pack(
         rows, dim, group, code, code if residual is None else F32 if residual.dtype is f32 else _dtype_code(residual), act, 1 if gate_first else 0, eps, scale,
