@@ -328,6 +328,8 @@ def make_verify_args(x, conv_state, weight, bias, out, window, *, layout, qk_cha
     if not weight.is_contiguous() or (bias is not None and not bias.is_contiguous()):
         raise ValueError("weight and bias must be contiguous")
     ws = _window_strides(window, lay)
+    if check_device:
+        _one_device(x, conv_state, weight, bias, out, window, cache_idx, state_off, err, parent, cu_draft)
     return VerifyArgs(
         n_seq=n_seq, T=T, dim=dim, width=W, qk_channels=qk_channels, head_dim=head_dim, dtype=_dtype_code(x),
         l2_eps=l2_eps, x=ptr(x, "x", total > 0 or not varlen), x_seq_stride=0 if varlen else x.stride(0),
@@ -413,6 +415,8 @@ def make_commit_args(conv_state, window, accept_len, *, layout, T, width, cache_
             raise ValueError(f"x must be [total_tokens, {dim}] with packed drafts")
     else:
         _need_shape(x, "x", (n_seq, T, dim))
+    if check_device:
+        _one_device(conv_state, window, accept_len, cache_idx, err, x, cu_draft)
     return CommitArgs(
         n_seq=accept_len.shape[0], T=T, dim=conv_state.shape[1], width=width, dtype=_dtype_code(conv_state),
         n_slots=conv_state.shape[0], conv_state=ptr(conv_state, "conv_state"),
@@ -466,6 +470,8 @@ def make_prefill_args(x, conv_state, weight, bias, out, cu_seqlens, *, max_seqle
         raise ValueError("x, out and conv_state need a unit innermost stride")
     if not weight.is_contiguous() or (bias is not None and not bias.is_contiguous()):
         raise ValueError("weight and bias must be contiguous")
+    if check_device:
+        _one_device(x, conv_state, weight, bias, out, cu_seqlens, cache_idx, has_initial_state, err)
     return PrefillArgs(
         n_seq=cu_seqlens.shape[0] - 1, dim=dim, width=weight.shape[1], qk_channels=qk_channels, head_dim=head_dim,
         dtype=_dtype_code(x), l2_eps=l2_eps, total_tokens=total, max_seqlen=int(max_seqlen),

@@ -56,7 +56,24 @@ def layer_calls():
     }
 
 
-CALLS = layer_calls()
+def conv_calls():
+    i32 = torch.zeros(2, dtype=torch.int32)
+    x, state, weight = torch.zeros(2, 3, 16), torch.zeros(2, 16, 3), torch.zeros(16, 4)
+    verify = dict(x=x, conv_state=state, weight=weight, bias=torch.zeros(16), out=x.clone(), window=torch.zeros(2, 16, 5),
+                  cache_idx=i32, state_off=i32.clone(), err=i32.clone())
+    commit = dict(conv_state=state, window=torch.zeros(2, 16, 5), accept_len=i32.clone(), cache_idx=i32, err=i32.clone())
+    flat = torch.zeros(6, 16)
+    prefill = dict(x=flat, conv_state=state, weight=weight, bias=torch.zeros(16), out=flat.clone(),
+                   cu_seqlens=torch.tensor([0, 3, 6], dtype=torch.int32), cache_idx=i32, has_initial_state=i32.clone(),
+                   err=i32.clone())
+    return {
+        "conv_verify": (verify, lambda t: cv.conv_verify(**t, layout="dedup", qk_channels=8, head_dim=8)),
+        "conv_commit": (commit, lambda t: cv.conv_commit(**t, layout="dedup", T=3, width=4)),
+        "conv_prefill": (prefill, lambda t: cv.conv_prefill(**t, max_seqlen=3, qk_channels=8, head_dim=8)),
+    }
+
+
+CALLS = {**layer_calls(), **conv_calls()}
 
 
 def refused(call, on, match):
