@@ -483,7 +483,9 @@ typedef struct cv_linattn_args {
 CV_API int cv_linattn_prefill(const cv_linattn_args *args, void *stream);
 
 /* cv_linattn_workspace -- validates args as cv_linattn_prefill does (pointers apart) and sets *bytes
- * to the workspace that call needs on the current device (0 = none). */
+ * to the workspace that call needs on the current device (0 = none).  Which kernel runs depends on the
+ * alignment of q, k, v, out and state: with those pointers as the call will have them the size
+ * is the call's own; where any of them is NULL it is enough for any pointers. */
 CV_API int cv_linattn_workspace(const cv_linattn_args *args, int64_t *bytes);
 
 /* cv_linattn_step -- one new token or a run of draft tokens per sequence, after the commit of the

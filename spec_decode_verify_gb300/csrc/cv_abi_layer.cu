@@ -468,8 +468,16 @@ int cv_linattn_workspace(const cv_linattn_args *args, int64_t *bytes) {
     if (rc != CV_OK) return rc;
     *bytes = 0;
     if (args->n_seq == 0) return CV_OK;
+    // NULL pointers count as aligned, which either kernel may take: the call's own may be aligned to less and
+    // leave the chunked kernel, so the size then covers both (unaligned rows need none).
+    const cv_linattn_tokens &t = args->tok;
+    const bool known = t.q && t.k && t.v && args->out && args->state;
     const ChunkPlan pl = plan_chunks(args);
-    *bytes = pl.pieces > 0 ? chunk_workspace(args, pl) : step_workspace(args, plan_step(args, make_linattn(args, false), false));
+    if (pl.pieces > 0) *bytes = chunk_workspace(args, pl);
+    if (pl.pieces == 0 || !known) {
+        const int64_t step = step_workspace(args, plan_step(args, make_linattn(args, false), false));
+        *bytes = *bytes > step ? *bytes : step;
+    }
     return CV_OK;
 }
 

@@ -39,3 +39,39 @@ def test_packed_arguments_land_in_their_fields():
                              update_state=True, wait_polls=-5, workspace=torch.zeros(512, dtype=torch.uint8))
     assert (a.update_state, a.wait_polls, a.workspace_bytes, a.tok.T, a.prev.T) == (1, -5, 512, 3, 0)
     assert a.out == t["out"].data_ptr() and a.state == t["state"].data_ptr() and a.tok.log_decay == t["g"].data_ptr()
+
+
+@pytest.fixture(scope="module")
+def lib():
+    cvbuild.build()
+    return cv.load_library()
+
+
+def prompt_args(dtype, total, dk, dv, nh, shift):
+    """Arguments of one prompt whose out rows start `shift` elements past a 16-byte boundary."""
+    x = torch.zeros(total, 1, dk, dtype=dtype)
+    v = torch.zeros(total, nh, dv, dtype=dtype)
+    out = torch.zeros(total * nh * dv + 8, dtype=dtype)[shift:shift + total * nh * dv].view(total, nh, dv)
+    cu = torch.tensor([0, total], dtype=torch.int32)
+    a = cv.make_linattn_args(x, x.clone(), v, torch.zeros(total, nh), torch.zeros(1, nh, dk, dv), out, n_seq=1, cu=cu, T=total,
+                             check_device=False)
+    a.keep = (x, v, out, cu)
+    return a
+
+
+def workspace(lib, a):
+    n = ctypes.c_int64(-1)
+    assert lib.cv_linattn_workspace(ctypes.byref(a), ctypes.byref(n)) == 0
+    return n.value
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("total,dk,dv,nh", [(300, 64, 64, 1), (1000, 128, 128, 2), (700, 8, 16, 1), (4000, 64, 128, 1),
+                                            (20000, 128, 64, 3), (40, 64, 64, 1)])
+def test_a_size_asked_for_without_pointers_is_enough_for_any(lib, dtype, total, dk, dv, nh):
+    needs = [workspace(lib, prompt_args(dtype, total, dk, dv, nh, shift)) for shift in (0, 1, 2, 4)]
+    for null in (("out",), ("state",), ("q", "k", "v"), ("q", "k", "v", "out", "state")):
+        a = prompt_args(dtype, total, dk, dv, nh, 0)
+        for name in null:
+            setattr(a if name in ("out", "state") else a.tok, name, None)
+        assert workspace(lib, a) >= max(needs)
