@@ -568,7 +568,7 @@ def _linattn_tokens(q, k, v, log_decay, gain, cu, T, n_seq, what) -> tuple:
     kt, vt, gt = k.stride(), v.stride(), log_decay.stride()
     qt = q.stride() if q is not None else kt
     bt = gain.stride() if gain is not None else gt
-    if kt[-1] != 1 or vt[-1] != 1 or qt[-1] != 1:
+    if (kt[-1] != 1 or qt[-1] != 1) and ks[-1] > 1 or vt[-1] != 1 and vs[-1] > 1:
         raise ValueError("q, k and v need a unit innermost stride")
     if gs[-1] > 1 and (gt[-1] != 1 or bt[-1] != 1):
         raise ValueError("log_decay and gain need a unit innermost stride")
@@ -608,7 +608,7 @@ def make_linattn_args(q, k, v, log_decay, state, out, *, n_seq, gain=None, skip=
         tok = _linattn_tokens(q, k, v, log_decay, gain, cu, T, n_seq, "tokens")
         if q.shape[-1] != dk or v.shape[-2] != H or v.shape[-1] != dv:
             raise ValueError(f"heads of q|k [.., {q.shape[-1]}] and v {tuple(v.shape[-2:])} do not fit the state {tuple(ss)}")
-        if out.shape != v.shape or out.dtype is not v.dtype or out.stride(-1) != 1:
+        if out.shape != v.shape or out.dtype is not v.dtype or (out.stride(-1) != 1 and dv > 1):
             raise ValueError("out needs the shape and dtype of v and a unit innermost stride")
         o, os = _pointer(out, "out"), out.stride()
         os = (0, os[0], os[1]) if cu is not None else os

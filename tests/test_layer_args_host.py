@@ -75,3 +75,19 @@ def test_a_size_asked_for_without_pointers_is_enough_for_any(lib, dtype, total, 
         for name in null:
             setattr(a if name in ("out", "state") else a.tok, name, None)
         assert workspace(lib, a) >= max(needs)
+
+
+def test_a_stride_over_one_channel_does_not_matter():
+    """Heads of one channel: the innermost stride is never used, whatever a transpose or an expansion left there."""
+    def odd(*shape):
+        return torch.zeros(*shape[:-1], 7)[..., 3:4].as_strided(shape, (*torch.zeros(*shape).stride()[:-1], 5))
+
+    for dk, dv in ((1, 1), (1, 4), (4, 1)):
+        q, v = (odd if dk == 1 else torch.zeros)(2, 3, 1, dk), (odd if dv == 1 else torch.zeros)(2, 3, 2, dv)
+        out = (odd if dv == 1 else torch.zeros)(2, 3, 2, dv)
+        a = cv.make_linattn_args(q, q, v, torch.zeros(2, 3, 2), torch.zeros(2, 2, dk, dv), out, n_seq=2, check_device=False)
+        assert (a.dk, a.dv) == (dk, dv)
+    with pytest.raises(ValueError):
+        wide = torch.zeros(2, 3, 1, 8)[..., ::2]
+        cv.make_linattn_args(wide, wide, torch.zeros(2, 3, 2, 4), torch.zeros(2, 3, 2), torch.zeros(2, 2, 4, 4),
+                             torch.zeros(2, 3, 2, 4), n_seq=2, check_device=False)
