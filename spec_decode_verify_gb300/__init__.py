@@ -252,13 +252,15 @@ def _one_device(*tensors) -> None:
                 if dev is not None:
                     raise ValueError(f"the tensors of a call must be on one device, got cuda:{dev} and cuda:{d}")
                 dev = d
+    if dev is not None and dev != (_current_device or _load_device())():
+        raise ValueError(f"the tensors are on cuda:{dev}, but the current device is cuda:{_current_device()}")
+
+
+def _load_device():
     global _current_device
-    if dev is not None:
-        if _current_device is None:
-            import torch
-            _current_device = torch._C._cuda_getDevice
-        if dev != _current_device():
-            raise ValueError(f"the tensors are on cuda:{dev}, but the current device is cuda:{_current_device()}")
+    import torch
+    _current_device = torch._C._cuda_getDevice
+    return _current_device
 
 
 def _stream_of(stream, t) -> int:
@@ -631,10 +633,19 @@ def make_linattn_args(q, k, v, log_decay, state, out, *, n_seq, gain=None, skip=
     ws, ws_bytes = 0, 0
     if workspace is not None:
         ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    if check_device:
-        _one_device(state, q, k, v, log_decay, out, gain, skip, cu, cache_idx, has_initial_state, err, workspace)
-        if prev is not None:
-            _one_device(state, prev.k, prev.v, prev.log_decay, prev.gain, prev.cu_draft, prev.accept_len)
+    if check_device:  # written out, since a call of one token notices a loop (0.5 us of 11)
+        dev = state.get_device()
+        if not (dev >= 0 and (_current_device or _load_device())() == dev and
+                (q is None or q.get_device() == k.get_device() == v.get_device() == log_decay.get_device() == out.get_device() == dev) and
+                (gain is None or gain.get_device() == dev) and (skip is None or skip.get_device() == dev) and
+                (cu is None or cu.get_device() == dev) and (cache_idx is None or cache_idx.get_device() == dev) and
+                (has_initial_state is None or has_initial_state.get_device() == dev) and
+                (err is None or err.get_device() == dev) and (workspace is None or workspace.get_device() == dev) and
+                (prev is None or prev.k.get_device() == prev.v.get_device() == prev.log_decay.get_device() ==
+                 prev.accept_len.get_device() == dev and (prev.gain is None or prev.gain.get_device() == dev) and
+                 (prev.cu_draft is None or prev.cu_draft.get_device() == dev))):
+            _one_device(state, q, k, v, log_decay, out, gain, skip, cu, cache_idx, has_initial_state, err, workspace,
+                        *((prev.k, prev.v, prev.log_decay, prev.gain, prev.cu_draft, prev.accept_len) if prev is not None else ()))
     return LinattnArgs.from_buffer_copy(_LINATTN.pack(
         n_seq, H, nq, dk, dv, BF16 if first.dtype is _bf16 else _dtype_code(first), dk ** -0.5 if scale is None else scale, n_slots, *tok, sk, o, os[0], os[1],
         os[2], state.data_ptr(), st[0], st[1], _index_array(cache_idx, "cache_idx", n_seq),
@@ -756,7 +767,13 @@ def make_norm_args(y, out, *, gate=None, gate_act=None, gate_first=False, group=
     elif residual_out is None or residual_out.dtype is not residual.dtype:
         raise ValueError("residual needs residual_out of its dtype")
     if check_device:
-        _one_device(y, out, gate, residual, residual_out, post_weight, channel_scale, pre_weight)
+        dev = y.get_device()
+        if not (dev >= 0 and (_current_device or _load_device())() == dev and (out is None or out.get_device() == dev) and
+                (gate is None or gate.get_device() == dev) and (post_weight is None or post_weight.get_device() == dev) and
+                (residual is None or residual.get_device() == residual_out.get_device() == dev) and
+                (channel_scale is None or channel_scale.get_device() == dev) and
+                (pre_weight is None or pre_weight.get_device() == dev)):
+            _one_device(y, out, gate, residual, residual_out, post_weight, channel_scale, pre_weight)
     code = BF16 if dt is _bf16 else _dtype_code(y)
     return NormArgs.from_buffer_copy(_NORM.pack(
         rows, dim, group, code, code if residual is None else F32 if residual.dtype is f32 else _dtype_code(residual), act, 1 if gate_first else 0, eps, scale,
