@@ -149,3 +149,66 @@ def test_infinite_gains_and_initial_states(cuda_lib):
     d = c.prefill(cuda_lib)
     _, _, state, slim = c.expect(True, chunked=True)
     assert_within(d["state"], state, slim, "state")
+
+
+def mix_decays(c, pattern, drops=True):
+    """Per chunk of 128 tokens and head: w slow decays, s strong ones (0.5 to 2 a token: 2^-92 to 2^-370 a chunk), d
+    strong ones with tokens that drop the state; sequence and head shift the pattern."""
+    for s in range(c.n):
+        for h in range(c.nh):
+            for i, lo in enumerate(range(c.cu[s], c.cu[s + 1], 128)):
+                hi, kind = min(lo + 128, c.cu[s + 1]), pattern[(i + s + 2 * h) % len(pattern)]
+                r = torch.rand(hi - lo, generator=c.rng)
+                c.tok["g"][lo:hi, h] = -0.02 * r if kind == "w" else -0.5 - 1.5 * r
+                if kind == "d" and drops:
+                    c.tok["g"][lo + 7:hi:23, h] = float("-inf")
+                    c.tok["g"][lo + 40:lo + 44, h][:max(0, hi - lo - 40)] = torch.finfo(torch.float32).min
+
+
+@pytest.mark.parametrize("pattern,n,nh,dk,dv,skip,gain", [
+    ("wwsds", 20, 8, 64, 64, False, False), ("sd", 20, 8, 128, 128, True, True), ("wsws", 20, 8, 128, 128, False, False)] + [
+    (pattern, n, nh, dk, dv, skip, gain) for pattern in ("ws", "wwsds", "sd", "wdws")
+    for n, nh, dk, dv, skip, gain in ((3, 2, 64, 128, True, False), (2, 1, 128, 64, False, True))])
+def test_weak_and_strong_chunks_follow_one_another(cuda_lib, pattern, n, nh, dk, dv, skip, gain):
+    """The kernel's two forms of a chunk in every order, across a block's units (more units than SMs) and within cut prompts."""
+    counts = [430 - 13 * s for s in range(n)] if n > 3 else [1500, 900, 641][:n]
+    c = Case(n, 1, nh, dk, dv, "bf16", counts=counts, seed=61, skip=skip, gain=gain)
+    mix_decays(c, pattern)
+    d = c.prefill(cuda_lib)
+    c.check(d, True, chunked=True)
+    again = c.prefill(cuda_lib)
+    assert torch.equal(d["out"], again["out"]) and torch.equal(d["state"], again["state"])
+
+
+@pytest.mark.parametrize("scale", [5e-5, 0.0, -1e-3])
+def test_skip_beside_a_small_scale(cuda_lib, scale):
+    """The skip weight enters the scores divided by scale, unless that is too small: then as strong chunks do it."""
+    c = Case(2, 1, 2, 64, 64, "bf16", counts=[300, 140], seed=62, skip=True, gain=True)
+    c.scale = scale
+    c.check(c.prefill(cuda_lib), True, chunked=True)
+
+
+def test_dropped_states_many_to_a_block(cuda_lib):
+    """Half of a block of 32 tokens drops the state, the other half decays slowly."""
+    c = Case(1, 1, 2, 64, 64, "bf16", counts=[256], seed=63)
+    c.tok["g"].mul_(0.01)
+    for lo in range(0, 256, 32):
+        c.tok["g"][lo:lo + 16] = float("-inf")
+    c.check(c.prefill(cuda_lib), True, chunked=True)
+
+
+@pytest.mark.parametrize("n,nh,longest,cut", [(70, 4, 300, False), (66, 1, 2600, True), (65, 1, 260, False)])
+def test_more_sequences_than_are_sorted(cuda_lib, n, nh, longest, cut):
+    counts = [longest if s % 33 == 5 else (s * 37) % 250 for s in range(n)]
+    c = Case(n, 1, nh, 64, 64, "bf16", counts=counts, seed=64, pad_seqs=(3, n - 1), no_init=range(0, n, 4), decay=0.01)
+    d = c.device()
+    assert (workspace(cuda_lib, c, d) > 0) == cut
+    c.check(c.prefill(cuda_lib, d), True, chunked=True)
+
+
+def test_more_recurrent_sequences_than_are_counted(cuda_lib):
+    counts = [1800 if s == 7 else (s * 41) % 120 for s in range(40)]
+    c = Case(40, 1, 1, 64, 64, "f32", counts=counts, seed=65, pad_seqs=(9,), no_init=(0, 7), decay=0.01)
+    d = c.device()
+    assert workspace(cuda_lib, c, d) > 0
+    c.check(c.prefill(cuda_lib, d), True)
