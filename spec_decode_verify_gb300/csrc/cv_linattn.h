@@ -116,7 +116,7 @@ constexpr unsigned kPolls = 1u << 16;  // of a wait by default, up to 20 us each
 using LinattnChunkKernel = void (*)(LinattnChunkParams);
 struct ChunkKernel {
     LinattnChunkKernel fn;
-    int dv_pad, smem_bytes;
+    int smem_bytes;
 };
 ChunkKernel chunk_kernel(int dv);
 // Turns the pieces' own states in the workspace into the states the next pieces start from.

@@ -1157,8 +1157,8 @@ __global__ void __launch_bounds__(kJoinThreads) chunk_join(const __grid_constant
 }  // namespace
 
 ChunkKernel chunk_kernel(int dv) {
-    if (dv <= 64) return {linattn_chunk<64>, 64, chunk_smem_bytes<64>()};
-    return {linattn_chunk<128>, 128, chunk_smem_bytes<128>()};
+    if (dv <= 64) return {linattn_chunk<64>, chunk_smem_bytes<64>()};
+    return {linattn_chunk<128>, chunk_smem_bytes<128>()};
 }
 LinattnChunkKernel chunk_join_kernel() { return chunk_join; }
 
