@@ -266,7 +266,8 @@ ChunkPlan plan_chunks(const cv_linattn_args *a) {
     // Few heads: cut the length into pieces.  A cut costs a pass over k and v for the pieces' own states and their
     // join.  The estimate is in tenths of a us, from measured launches (128 columns): 5.7 us and 3.6 us a chunk of the
     // fullest SM uncut; cut 13.5 us, 5.2 us a chunk, 0.35 us a piece of the join and 4.5 us for each further piece
-    // that an SM takes (1 prompt of 32k tokens, 6 heads: 83 us in 24 pieces; 4.1k tokens, 4 heads: 28 us in 33).
+    // that an SM takes (1 prompt of 32k tokens, 6 heads: 85 us in 24 pieces; 4.1k tokens, 4 heads: 28 us in 33).
+    // (It was not fitted to the kernel for 64 columns, which takes it too.)
     // Lengths are on the device, so the fullest SM is estimated from their sum.
     const int64_t chunks = whole / cvk::kChunk, mean = (a->n_heads * t.total_tokens / cvk::kChunk + sms - 1) / sms;
     int64_t best = 57 + 36 * (chunks > mean ? chunks : mean);

@@ -32,8 +32,8 @@
 // Tensor memory: Q K^T (then A) 128 columns, S and two buffers of dv columns each, which take turns as Q S + A V
 // and, between two chunks' outputs, as K'^T V.
 //
-// Measured: 8 prompts of 1.5k-5.8k tokens, 48 heads of 128 x 128: 315 us, 3.3 TB/s (HBM's floor is 156 us), tensor
-// pipe 30 % and issue slots 44 % busy.  A chunk takes 3.5 us of an SM; its products need 1.7 us of the tensor
+// Measured: 8 prompts of 1.5k-5.8k tokens, 48 heads of 128 x 128: 317 us, 3.3 TB/s (HBM's floor is 156 us), tensor
+// pipe 32 % and issue slots 45 % busy.  A chunk takes 3.6 us of an SM; its products need 1.7 us of the tensor
 // pipe.  What bounds it is the longest cycle through the roles, K'^T V -> S -> Q S, and the shared memory that all
 // of them read and write: about 600 KB a chunk (the operands of the products 288, tiles in and out 160, K' made of
 // k 96, the copy of S 32, the look for NaN in v 32), 2.4 us at 128 bytes a cycle.

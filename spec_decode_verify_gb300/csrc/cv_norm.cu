@@ -10,9 +10,11 @@
 //                32 lanes of one warp, 16 bytes a lane, so no shared memory and no barrier (30822 x 6144
 //                gated, groups of 128, bf16: 202 us, 5.6 TB/s)
 //   norm_row     a block a row, the row's values in registers between the two norms (1023 x 4096, fp32
-//                residual: 12.9 us, one wave of rows; 14648 x 4096: 125 us, 6.7 TB/s)
-//   norm_any     a block a row, values read again (from L1/L2) for each pass: rows too wide for
-//                registers and residual rows with several groups
+//                residual: 12.9 us, 127 registers hold 608 rows on the card, so 1.7 waves; 14648 x 4096: 125 us,
+//                6.7 TB/s)
+//   norm_any     a block a row, values read again (from L1/L2) for each pass, one element an access: rows too wide
+//                for registers and residual rows with several groups (30000 x 4096 gated, groups of 128, fp32
+//                residual: 1155 us, 4.5 times its floor)
 #include "cv_device.cuh"
 #include "cv_norm.h"
 
