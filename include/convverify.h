@@ -397,8 +397,7 @@ CV_API int cv_verify_plan(const cv_verify_args *args, cv_launch_plan *plan);
  * length).  On the way its sums are up to 2^80 times what they add to an output, so finite terms
  * |b (q.k) v| above 2^47 may give infinities.  fp32 tokens avoid all of this.
  * Values that are not finite reach what depends on them and nothing else: an output is then a NaN or an
- * infinity as the order of its sums has it, an element of the state what the recurrence leaves (but a NaN for
- * an infinity that decays by more than 2^126 over a piece of a prompt that was cut).
+ * infinity as the order of its sums has it, an element of the state what the recurrence leaves.
  *
  * cv_linattn_tokens holds one run of tokens per sequence: T tokens for each of the n_seq sequences
  * (cu NULL; token t of sequence s at s*seq_stride + t*tok_stride) or, with cu (int32 [n_seq + 1]

@@ -48,6 +48,7 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kMinLog2 = -200.0f * kLog2e;
+constexpr float kDrop = -150.0f;  // log2 of a decay that is 0 in fp32
 constexpr float kNoDecay = -1.0f;  // in the place of a piece's decay (>= 0 or NaN): it was not made
 constexpr float kStrong = -80.0f;  // log2 of a chunk's decay from which on A is made block by block
 constexpr int kTileQK = kChunk * 256;  // bytes of a q or k tile: two blocks of 64 channels
@@ -60,7 +61,7 @@ struct ChunkShared {
     uint32_t tmem;
     int dead;
     // why the chunk's Q S and A V are kept apart: 1 it decays by more than 2^80, 2 its v holds a NaN or inf; and from
-    // bit 8 on, in which groups of 8 columns v does
+    // bit 8 on, in which groups of 8 columns v does.  4, beside 1: a token drops the state.
     int apart[2];
     // The work of sorted launches: first the full pieces, sequence by sequence (first: the number before a
     // sequence's own), then the shorter rests, longest first (order: their sequences).  Uncut, all are rests.
@@ -538,6 +539,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
                 const bool strong = !((t0 + t1) + (t2 + t3) > strong_at);
                 if (!strong) before += (block > 0 ? t0 : 0.0f) + (block > 1 ? t1 : 0.0f) + (block > 2 ? t2 : 0.0f);
                 const float ahead = (block < 1 ? t1 : 0.0f) + (block < 2 ? t2 : 0.0f) + (block < 3 ? t3 : 0.0f);
+                const bool drops = __any_sync(0xffffffffu, fminf(fminf(g[0], g[1]), fminf(g[2], g[3])) < kDrop);
                 const int stage = it & 1;
                 if ((it > 1 && !wait_warp(&sh->g_empty[stage], ((it >> 1) & 1) ^ 1, waits)) ||
                     (it > 0 && !wait_warp(&sh->key_empty, (it - 1) & 1, waits))) {
@@ -556,7 +558,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
                 *reinterpret_cast<float4 *>(sh->key + 4 * lane) = make_float4(key[0], key[1], key[2], key[3]);
                 if (lane == 0) {
                     *reinterpret_cast<float4 *>(sh->tot[stage]) = make_float4(t0, t1, t2, t3);
-                    sh->apart[stage] = strong;
+                    sh->apart[stage] = strong | (drops ? 4 : 0);
                 }
                 arrive_warp(&sh->g_full[stage]);
             }
@@ -739,6 +741,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
             arrive_warp(&sh->s_init);
             if (!wait_warp(&sh->s_init, units++ & 1, waits)) break;
             float total = 1.0f, tot = 1.0f;  // decays of the unit so far, and of the last chunk
+            bool drops = false;              // some token of the unit drops the state
             // 16 columns of S, and of the last chunk's products where there are any
             auto current = [&](uint32_t *x, int j, bool products) {
                 tmem_ld16(x, ts + j);
@@ -767,6 +770,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
                     break;
                 }
                 const float4 bt = *reinterpret_cast<const float4 *>(sh->tot[stage]);
+                if (so) drops |= (*(volatile int *)&sh->apart[stage] & 4) != 0;
                 arrive_warp(&sh->g_empty[stage]);
 #pragma unroll 1
                 for (int h = 0; h < HALVES; ++h) {
@@ -829,7 +833,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) linattn_chunk(const __grid_c
                 if (__any_sync(0xffffffffu, nan))
 #pragma unroll 1
                     for (int h = 0; h < HALVES; ++h) mend_state(p, sh, idx, dst + h * (16 * 128) + r, 0, 128, 64 * h, 16);
-                if (r == 0) p.ws_decay[wsi + u.seg] = total;
+                // (an infinity before the piece stays one, however small its decay, unless a token drops it)
+                if (r == 0) p.ws_decay[wsi + u.seg] = total == 0.0f && !drops ? __int_as_float(1) : total;
             } else if (u.last) {
 #pragma unroll 1
                 for (int h = 0; h < PASSES; ++h) {

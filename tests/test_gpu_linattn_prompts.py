@@ -212,3 +212,21 @@ def test_more_recurrent_sequences_than_are_counted(cuda_lib):
     d = c.device()
     assert workspace(cuda_lib, c, d) > 0
     c.check(c.prefill(cuda_lib, d), True)
+
+
+@pytest.mark.parametrize("dropped", [False, True])
+@pytest.mark.parametrize("counts,nh", [([1500], 1), ([1500, 40], 60)])
+def test_an_infinity_outlives_small_decays_but_no_drop(cuda_lib, counts, nh, dropped):
+    """An infinity in the state stays one under decays that multiply to far less than fp32 holds, within a chunk, over a
+    whole prompt and over the pieces of a cut one; a token that drops the state makes it a NaN (0 * inf)."""
+    c = Case(len(counts), 1, nh, 64, 64, "bf16", counts=counts, seed=66)
+    d = c.device()
+    assert (workspace(cuda_lib, c, d) > 0) == (nh == 1)
+    c.tok["v"][3, 0, 5] = float("inf")
+    c.tok["g"][200:700, 0] = -2.0
+    if dropped:
+        c.tok["g"][450, 0] = float("-inf")
+    d = c.prefill(cuda_lib)
+    _, _, state, slim = c.expect(True, chunked=True)
+    assert bool(torch.isinf(state).any()) != dropped
+    assert_within(d["state"], state, slim, "state")
