@@ -214,13 +214,15 @@ def _prepare_attend(s, g, seed):
     s["all_parents"] = parent
     s["parent"] = _pack(parent, counts) if s["ragged"] and s["tree"] else parent
     s["out"] = torch.zeros_like(s["q"])
+    _hold(s)
+    return s
+
+
+def _hold(s, **pool):
+    """The library's handle of the cache's tensors, which a program makes once for each layer."""
     if own:
         import spec_decode_verify_gb300 as cv
-        cache = cv.PagedCache(s["k"], s["v"], s["table"])
-        s["ws"] = torch.empty(cv.tree_attention_workspace(s["q"], s["out"], cache, s["len"], parent=s["parent"],
-                                                          cu_draft=s["cu"], T=T, cache_idx=s["slot"]),
-                              dtype=torch.uint8, device="cuda")
-    return s
+        s["cache"] = cv.PagedCache(s["k"], s["v"], s["table"], **pool)
 
 
 def _pack(t, counts):
@@ -295,6 +297,7 @@ def _prepare_rope(s, g, seed):
     s["k"] = torch.zeros(n_pages, page, kv, d, dtype=x.dtype, device="cuda")
     s["v"] = torch.zeros_like(s["k"])
     s["out"] = torch.zeros(*lead, H, d, dtype=x.dtype, device="cuda")
+    _hold(s)
     return s
 
 
@@ -318,6 +321,7 @@ def _prepare_compact(s, g, seed):
     s["path"][i >= a[:, None]] = -1
     s["accept"] = a
     s["new_len"] = torch.zeros(n, dtype=torch.int32, device="cuda")
+    _hold(s)
     return s
 
 
@@ -354,6 +358,7 @@ def _prepare_fork(s, g, seed):
     s["grown"] = _ints([lens[i] + s["grow"] for i in src])
     s["k"] = _randn(g, s["layers"], n_pages, page, s["n_kv"], s["d"], dtype=s["dtype"])
     s["v"] = _randn(g, s["layers"], n_pages, page, s["n_kv"], s["d"], dtype=s["dtype"])
+    _hold(s, held=s["held"], refs=s["refs"])
     return s
 
 
@@ -568,8 +573,8 @@ def _plain(s):
 def _own(s):
     import spec_decode_verify_gb300 as cv
     if s["op"] == "attend":
-        cv.tree_attention(s["q"], s["out"], cv.PagedCache(s["k"], s["v"], s["table"]), s["len"], parent=s["parent"],
-                          cu_draft=s["cu"], T=s["T"], cache_idx=s["slot"], workspace=s["ws"])
+        cv.tree_attention(s["q"], s["out"], s["cache"], s["len"], parent=s["parent"], cu_draft=s["cu"], T=s["T"],
+                          cache_idx=s["slot"])
         return s["out"]
     if s["op"] == "sample":
         cv.draft_verify(s["p"], s["tok"], s["u"], s["accept"], s["new"], draft_probs=s["qp"], parent=s["parent"],
@@ -577,17 +582,15 @@ def _own(s):
         return s["accept"], s["node"], s["new"], s["path"]
     if s["op"] == "rope":
         cv.qk_norm_rope(s["q"], s["kx"], s["out"], cos_sin=s["cos_sin"], q_weight=s["wq"], k_weight=s["wk"], v=s["vx"],
-                        cache=cv.PagedCache(s["k"], s["v"], s["table"]), cache_len=s["len"], positions=s["pos"],
-                        cu_seqlens=s["cu"], max_seqlen=s["T"], cache_idx=s["slot"], pairs=s["pairs"], eps=1e-6)
+                        cache=s["cache"], cache_len=s["len"], positions=s["pos"], cu_seqlens=s["cu"], max_seqlen=s["T"],
+                        cache_idx=s["slot"], pairs=s["pairs"], eps=1e-6)
         return s["out"], s["k"], s["v"]
     if s["op"] == "compact":
-        cv.cache_compact(cv.PagedCache(s["k"], s["v"], s["table"]), s["len"], s["path"], s["accept"],
-                         new_len=s["new_len"], cache_idx=s["slot"])
+        cv.cache_compact(s["cache"], s["len"], s["path"], s["accept"], new_len=s["new_len"], cache_idx=s["slot"])
         return s["k"], s["v"], s["new_len"]
-    cache = cv.PagedCache(s["k"], s["v"], s["table"], held=s["held"], refs=s["refs"])
-    cv.cache_free(cache, cache_idx=s["dst"])
-    cv.cache_fork(cache, s["src"], s["dst"], s["n_tok"])
-    cv.cache_reserve(cache, s["grown"], cache_idx=s["dst"])
+    cv.cache_free(s["cache"], cache_idx=s["dst"])
+    cv.cache_fork(s["cache"], s["src"], s["dst"], s["n_tok"])
+    cv.cache_reserve(s["cache"], s["grown"], cache_idx=s["dst"])
     return s["k"], s["v"], s["table"], s["refs"], s["held"]
 
 
