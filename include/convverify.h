@@ -51,7 +51,7 @@ extern "C" {
 #define CV_API
 #endif
 
-#define CV_ABI_VERSION 10
+#define CV_ABI_VERSION 11
 #define CV_MAX_T 128 /* draft tokens per verify call */
 
 typedef enum cv_dtype {
@@ -128,7 +128,14 @@ enum {
                                written (every sequence whose data the block had not finished) */
 #define CV_SEQ_BAD_SPAN 16  /* prefill: token span invalid or longer than max_seqlen; packed
                                verify / commit: draft span invalid or longer than T */
-#define CV_SEQ_BAD_TREE 32  /* tree verify: a draft token's parent outside [-1, t) */
+#define CV_SEQ_BAD_TREE 32  /* tree verify: a draft token's parent outside [-1, t); cache_compact: a path that does not
+                               rise, or leaves the drafts */
+#define CV_SEQ_BAD_LENGTH 64    /* paged cache: a length < 0, or past what the page table row (or the held pages) can hold */
+#define CV_SEQ_BAD_PAGE 128     /* paged cache: a page outside [0, n_pages) where the call needs one */
+#define CV_SEQ_BAD_TOKEN 256    /* draft_verify: a draft token outside [0, vocab) */
+#define CV_SEQ_BAD_PROBS 512    /* draft_verify: the weights to sample from add up to 0, or to 4 and more */
+#define CV_SEQ_NO_PAGES 1024    /* cache_reserve, cache_fork: not enough free pages */
+#define CV_SEQ_BAD_POSITION 2048 /* qk_norm_rope: a position outside the table of angles */
 
 /*
  * cv_conv_verify -- [atlas-batched] fused multi-token verify, batched over sequences.
@@ -538,6 +545,190 @@ typedef struct cv_norm_args {
 } cv_norm_args;
 
 CV_API int cv_block_norm(const cv_norm_args *args, void *stream);
+
+/*
+ * The attention layers of a hybrid model: a cache of K and V in pages, attention of drafted tokens over it, the
+ * norms and rotation before it, the acceptance of drafts, and the pages' bookkeeping.
+ *
+ * cv_cache describes one cache.  Token position x of slot r stands in row x % page_size of page
+ * page_table[r][x / page_size].  K and V are [n_layers][n_pages][page_size][n_kv_heads][head_dim], every stride but
+ * the innermost (1) free; the layer strides are used by cv_cache_compact and cv_cache_fork alone, the other calls read
+ * and write layer 0 (pass the layer's own address).  page_table entries past those a call needs are not read.
+ *   held   int32 [n_slots]: pages of each slot (reserve, fork, free; else may be NULL)
+ *   refs   int32 [n_pages]: slots that hold each page, 0 = free (reserve, fork, free; else may be NULL)
+ * Sizes: n_layers 1..4096, n_pages 1..2^31-1, page_size 1..65536, n_kv_heads 1..4096, head_dim 1..256, n_slots >= 1,
+ * max_pages >= 1, max_pages * page_size < 2^31 (else CV_ERR_SHAPE; head_dim: CV_ERR_HEAD_DIM).
+ */
+typedef struct cv_cache {
+    void *k, *v;
+    int64_t k_layer_stride, k_page_stride, k_row_stride, k_head_stride;
+    int64_t v_layer_stride, v_page_stride, v_row_stride, v_head_stride;
+    int32_t n_layers, n_pages, page_size, n_kv_heads, head_dim, n_slots, max_pages;
+    int32_t dtype; /* cv_dtype of k and v */
+    int32_t *page_table;
+    int64_t table_stride; /* of its rows, >= max_pages */
+    int32_t *held, *refs;
+} cv_cache;
+
+/*
+ * cv_tree_attention -- attention of T drafted tokens per sequence, a chain or a tree of them, over the cache.  With
+ * slot r = cache_idx ? cache_idx[s] : s, L = cache_len[s] and T_s drafts, whose K and V stand at positions L .. L+T_s-1
+ * already, every draft t and head h (which reads kv head h * n_kv_heads / n_heads):
+ *     w_j = scale * q[t][h] . k_j        for j < L, and for j = L + u with u = t or u an ancestor of t
+ *     out[t][h] = sum_j exp(w_j) v_j / sum_j exp(w_j)
+ * A draft's parent is in [-1, t) (-1: the cached tokens alone precede it); without parent token t follows t-1 (a
+ * causal run: a decoded token with T = 1).  Nothing of any other position reaches an output, whatever stands there.
+ * Products and sums are fp32 and out is rounded once; bf16 calls on the tensor cores also round exp(w_j - max) to
+ * bf16 (2^-8 of a term at most), as the operand of the second product.
+ *   n_seq 0..65535, T 1..CV_MAX_T (the largest T_s), n_heads 1..4096, a multiple of n_kv_heads
+ *   q, out             [n_seq][T][n_heads][head_dim], or with cu_draft [total_tokens][n_heads][head_dim]; dtype = the cache's
+ *   cu_draft           int32 [n_seq + 1] or NULL; sequence s owns rows [cu_draft[s], cu_draft[s+1])
+ *   parent             int32 [n_seq][T], with cu_draft [total_tokens]; or NULL
+ *   cache_len          int32 [n_seq]; cache_idx int32 [n_seq] or NULL, negative = padded (nothing is read or written)
+ *   err                int32 [n_seq] or NULL: CV_SEQ_BAD_SLOT, _BAD_SPAN, _BAD_LENGTH (L < 0 or L + T_s beyond the table's
+ *                      row), _BAD_PAGE, _BAD_TREE, _TIMEOUT; a flagged sequence's out is left untouched (after a
+ *                      timeout it may be partly written)
+ *   workspace          device buffer of at least cv_tree_attention_workspace bytes, 256-byte aligned; its content
+ *                      means nothing before and after the call.  NULL when 0
+ *   wait_polls         limit of the kernel's bounded waits: 0 = the default, negative = none
+ */
+typedef struct cv_tree_attention_args {
+    int32_t n_seq, T, n_heads, total_tokens;
+    float scale;
+    int32_t wait_polls;
+    cv_cache cache;
+    const void *q;
+    int64_t q_seq_stride, q_tok_stride, q_head_stride;
+    void *out;
+    int64_t out_seq_stride, out_tok_stride, out_head_stride;
+    const int32_t *cu_draft, *parent, *cache_len, *cache_idx;
+    int32_t *err;
+    void *workspace;
+    int64_t workspace_bytes;
+} cv_tree_attention_args;
+
+CV_API int cv_tree_attention(const cv_tree_attention_args *args, void *stream);
+
+/* cv_tree_attention_workspace -- validates args (pointers apart) and sets *bytes to the workspace the call needs on
+ * the current device, for q, out, k and v aligned as given (NULL counts as any alignment). */
+CV_API int cv_tree_attention_workspace(const cv_tree_attention_args *args, int64_t *bytes);
+
+/*
+ * cv_draft_verify -- which drafted tokens stand, and the token after them.  Row t of probs is the target's distribution
+ * after draft t.  Token 0 is the last step's token and stands.  From node c = 0 the walk goes on:
+ *     children of c: the drafts whose parent is c, in order; one whose token an earlier one of them has is passed over
+ *     with draft_probs (a chain only; row t is what token t was drawn from, row 0 is not read): the child stands iff
+ *         uniforms[s][c] * draft_probs[child][token] < probs[c][token]
+ *     without: a child stands iff uniforms[s][c] < the sum of probs[c][token] over it and the children before it
+ *     the first child that stands is the next c; without one the walk ends
+ * and the new token is sampled from the weights w at its end:
+ *     no child there: probs[c];   with draft_probs: max(probs[c] - draft_probs[child], 0)
+ *     without: probs[c], the children's tokens left out;   where all w are 0: probs[c]
+ *     new = the lowest token whose cumulative weight exceeds uniforms[s][T] * the sum of w
+ * Weights are summed exactly, in units of 2^-60 (values are cut off there, and at 2; what is not above 0, NaN among it,
+ * counts as 0).  Comparisons are made in 64 bits.  A uniform counts as within [0, 1).
+ *   n_seq 0..65535, T 1..CV_MAX_T, vocab 1..2^24; dtype of probs and draft_probs, innermost stride 1
+ *   tokens             int32 [n_seq][T] (cu_draft: [total_tokens]); parent likewise or NULL (a chain)
+ *   uniforms           fp32 [n_seq][T + 1] contiguous
+ *   accept_len         int32 [n_seq]: tokens that stand, 1..T_s (cv_conv_commit's and cv_linattn_step's, for a chain)
+ *   accept_node        int32 [n_seq] or NULL: 1 + the last one's index (cv_conv_commit's accept_len, for a tree)
+ *   path               int32 [n_seq][T] or NULL: their indexes in order, then -1
+ *   out_tokens         int32 [n_seq][T]: the tokens after token 0 that stand, the new token, then -1
+ *   err                CV_SEQ_BAD_SLOT is not raised (cache_idx only marks padding); _BAD_SPAN (also T_s = 0), _BAD_TREE (token 0 must have
+ *                      parent -1), _BAD_TOKEN (tokens 1 .. T_s-1), _BAD_PROBS.  A flagged sequence is left untouched
+ */
+typedef struct cv_draft_verify_args {
+    int32_t n_seq, T, vocab, dtype, total_tokens;
+    const void *probs;
+    int64_t probs_seq_stride, probs_tok_stride;
+    const void *draft_probs;
+    int64_t draft_seq_stride, draft_tok_stride;
+    const int32_t *tokens, *parent;
+    const float *uniforms;
+    const int32_t *cu_draft, *cache_idx;
+    int32_t *accept_len, *accept_node, *path, *out_tokens, *err;
+} cv_draft_verify_args;
+
+CV_API int cv_draft_verify(const cv_draft_verify_args *args, void *stream);
+
+/*
+ * cv_qk_norm_rope -- the RMS norm of each query and key head and the rotation of its first rot_dim channels by the
+ * token's position, with K and V written into the cache's pages in the same pass.  In fp32, rounded once:
+ *     y = x / sqrt(mean over head_dim of x^2 + eps) * weight       (norm != 0; weight NULL: 1;  norm = 0: y = x)
+ *     (y[a], y[b]) = (y[a] cos - y[b] sin, y[b] cos + y[a] sin)    pair i: a = i, b = i + rot_dim/2; pairs != 0: a = 2i, b = 2i+1
+ * with cos = cos_sin[position][i] and sin = cos_sin[position][rot_dim/2 + i], position = positions of the token, or
+ * cache_len[s] + t without them.
+ *   tokens             [n_seq][T], or with cu [total_tokens] packed, T then bounds a sequence's length
+ *   q, q_out           .. [n_heads][head_dim] (q_out may be q); k .. [n_kv_heads][head_dim]
+ *   k_out              like k, or NULL;  cache (page_table not NULL): K goes to position cache_len[s] + t, and so does v,
+ *                      .. [n_kv_heads][head_dim], unrounded, unless NULL.  One of k_out and the cache is needed unless n_kv_heads = 0
+ *   cos_sin            fp32 [n_positions][rot_dim], row stride cos_sin_stride; rot_dim even, 0..head_dim (0: NULL)
+ *   err                _BAD_SLOT, _BAD_SPAN, _BAD_LENGTH: the sequence is left untouched; _BAD_PAGE, _BAD_POSITION: the tokens
+ *                      concerned are left out
+ */
+typedef struct cv_qk_norm_rope_args {
+    int32_t n_seq, T, n_heads, n_kv_heads, head_dim, dtype, total_tokens, rot_dim, pairs, norm, n_positions;
+    float eps;
+    const void *q;
+    int64_t q_seq_stride, q_tok_stride, q_head_stride;
+    void *q_out;
+    int64_t q_out_seq_stride, q_out_tok_stride, q_out_head_stride;
+    const void *k;
+    int64_t k_seq_stride, k_tok_stride, k_head_stride;
+    void *k_out;
+    int64_t k_out_seq_stride, k_out_tok_stride, k_out_head_stride;
+    const void *v;
+    int64_t v_seq_stride, v_tok_stride, v_head_stride;
+    const void *q_weight, *k_weight;
+    const float *cos_sin;
+    int64_t cos_sin_stride;
+    const int32_t *positions, *cu, *cache_len, *cache_idx;
+    cv_cache cache;
+    int32_t *err;
+} cv_qk_norm_rope_args;
+
+CV_API int cv_qk_norm_rope(const cv_qk_norm_rope_args *args, void *stream);
+
+/*
+ * cv_cache_compact -- the accepted path of each sequence moved to its place: rows L + path[s][i] of every layer's K and V
+ * go to L + i, i < accept_len[s] (0..T), L = cache_len[s]; new_len[s] = L + accept_len[s] unless NULL (it may not be
+ * cache_len).  path int32 [n_seq][T] rises and lies in [0, T).  The pages written must be the slot's alone.
+ * err: _BAD_SLOT, _BAD_ACCEPT, _BAD_TREE, _BAD_LENGTH, _BAD_PAGE; the sequence is left untouched.
+ */
+typedef struct cv_cache_compact_args {
+    int32_t n_seq, T;
+    cv_cache cache;
+    const int32_t *cache_len, *path, *accept_len, *cache_idx;
+    int32_t *new_len, *err;
+} cv_cache_compact_args;
+
+CV_API int cv_cache_compact(const cv_cache_compact_args *args, void *stream);
+
+/*
+ * The pages' bookkeeping, on the device.  A page is free while refs is 0; new pages are the free ones with the lowest
+ * numbers, given to the call's sequences in order.  n_seq 0..4096.  A slot that an earlier sequence of the same call
+ * names too is CV_SEQ_BAD_SLOT (for a fork: as a destination), a negative one is passed over.
+ *
+ * cv_cache_reserve   slot idx[s] (NULL: s) grows to ceil(n_tokens[s] / page_size) pages if it holds fewer.  The sequences are served in
+ *                    order while the free pages last: CV_SEQ_NO_PAGES for the first whose need, added to those before it,
+ *                    exceeds them, and for all with a need after it.
+ * cv_cache_fork      slot idx[s], which holds nothing, gets the first n_tokens[s] tokens of slot src_idx[s]: full pages are
+ *                    shared, the rest of a last one is copied into a new page (every layer's K and V).  The sources are
+ *                    read as they were before the call: a destination may not be a source too (CV_SEQ_BAD_SLOT).
+ * cv_cache_free      slot idx[s] lets go of its pages past those of its first n_tokens[s] tokens (NULL: 0).  Their table
+ *                    entries become -1.
+ * err: _BAD_SLOT (also a destination that holds pages), _BAD_LENGTH, _BAD_PAGE, _NO_PAGES; the slot is left as it was.
+ */
+typedef struct cv_cache_pages_args {
+    int32_t n_seq;
+    cv_cache cache;
+    const int32_t *idx, *src_idx, *n_tokens;
+    int32_t *err;
+} cv_cache_pages_args;
+
+CV_API int cv_cache_reserve(const cv_cache_pages_args *args, void *stream);
+CV_API int cv_cache_fork(const cv_cache_pages_args *args, void *stream);
+CV_API int cv_cache_free(const cv_cache_pages_args *args, void *stream);
 
 /* cv_status_string -- a static, NUL-terminated description of a status code (never NULL). */
 CV_API const char *cv_status_string(int status);

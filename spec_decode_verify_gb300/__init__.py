@@ -15,6 +15,15 @@ and the operators that follow the conv in a hybrid layer:
     linattn_step(q, k, v, log_decay, state, out, prev=LinattnDrafts(...), update_state=...)
     linattn_commit(LinattnDrafts(...), state)
     block_norm(y, out, gate=..., group=..., post_weight=..., residual=..., residual_out=..., pre_weight=...)
+
+and those of its attention layers, with the acceptance of the drafts:
+
+    cache = PagedCache(k, v, page_table, held=..., refs=...)
+    qk_norm_rope(q, k, q_out, cos_sin=..., q_weight=..., k_weight=..., v=v, cache=cache, cache_len=...)
+    tree_attention(q, out, cache, cache_len, parent=...)
+    draft_verify(probs, tokens, uniforms, accept_len, out_tokens, draft_probs=..., parent=..., path=...)
+    cache_compact(cache, cache_len, path, accept_len, new_len=...)
+    cache_reserve(cache, n_tokens), cache_fork(cache, src_idx, dst_idx, n_tokens), cache_free(cache, n_tokens)
 """
 from __future__ import annotations
 
@@ -26,7 +35,9 @@ from typing import Optional
 __all__ = ["conv_verify", "conv_commit", "conv_prefill", "verify_plan", "status_string", "load_library", "library_path",
            "CvError", "DENSE", "DEDUP", "HISTORY", "RECOMPUTE", "SEQ_BAD_SLOT", "SEQ_BAD_OFFSET", "SEQ_BAD_ACCEPT",
            "SEQ_TIMEOUT", "SEQ_BAD_SPAN", "SEQ_BAD_TREE", "linattn_prefill", "linattn_step", "linattn_commit",
-           "linattn_workspace", "LinattnDrafts", "block_norm"]
+           "linattn_workspace", "LinattnDrafts", "block_norm", "PagedCache", "tree_attention",
+           "tree_attention_workspace", "draft_verify", "qk_norm_rope", "cache_compact", "cache_reserve", "cache_fork", "cache_free",
+           "SEQ_BAD_LENGTH", "SEQ_BAD_PAGE", "SEQ_BAD_TOKEN", "SEQ_BAD_PROBS", "SEQ_NO_PAGES", "SEQ_BAD_POSITION"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 library_path = os.path.join(_PKG, "_build", "libconvverify.so")
@@ -34,6 +45,7 @@ library_path = os.path.join(_PKG, "_build", "libconvverify.so")
 DENSE, DEDUP, HISTORY, RECOMPUTE = 1, 2, 3, 4
 F32, BF16 = 0, 1
 SEQ_BAD_SLOT, SEQ_BAD_OFFSET, SEQ_BAD_ACCEPT, SEQ_TIMEOUT, SEQ_BAD_SPAN, SEQ_BAD_TREE = 1, 2, 4, 8, 16, 32
+SEQ_BAD_LENGTH, SEQ_BAD_PAGE, SEQ_BAD_TOKEN, SEQ_BAD_PROBS, SEQ_NO_PAGES, SEQ_BAD_POSITION = 64, 128, 256, 512, 1024, 2048
 MAX_T = 128
 ERR_WORKSPACE = -13
 
@@ -122,6 +134,66 @@ class NormArgs(ctypes.Structure):
     ]
 
 
+class Cache(ctypes.Structure):
+    """Mirror of cv_cache."""
+    _fields_ = [
+        ("k", c_vp), ("v", c_vp),
+        ("k_layer_stride", c_i64), ("k_page_stride", c_i64), ("k_row_stride", c_i64), ("k_head_stride", c_i64),
+        ("v_layer_stride", c_i64), ("v_page_stride", c_i64), ("v_row_stride", c_i64), ("v_head_stride", c_i64),
+        ("n_layers", c_i32), ("n_pages", c_i32), ("page_size", c_i32), ("n_kv_heads", c_i32), ("head_dim", c_i32),
+        ("n_slots", c_i32), ("max_pages", c_i32), ("dtype", c_i32), ("page_table", c_vp), ("table_stride", c_i64),
+        ("held", c_vp), ("refs", c_vp),
+    ]
+
+
+class TreeAttentionArgs(ctypes.Structure):
+    """Mirror of cv_tree_attention_args."""
+    _fields_ = [
+        ("n_seq", c_i32), ("T", c_i32), ("n_heads", c_i32), ("total_tokens", c_i32), ("scale", ctypes.c_float),
+        ("wait_polls", c_i32), ("cache", Cache), ("q", c_vp), ("q_seq_stride", c_i64), ("q_tok_stride", c_i64),
+        ("q_head_stride", c_i64), ("out", c_vp), ("out_seq_stride", c_i64), ("out_tok_stride", c_i64),
+        ("out_head_stride", c_i64), ("cu_draft", c_vp), ("parent", c_vp), ("cache_len", c_vp), ("cache_idx", c_vp),
+        ("err", c_vp), ("workspace", c_vp), ("workspace_bytes", c_i64),
+    ]
+
+
+class DraftVerifyArgs(ctypes.Structure):
+    """Mirror of cv_draft_verify_args."""
+    _fields_ = [
+        ("n_seq", c_i32), ("T", c_i32), ("vocab", c_i32), ("dtype", c_i32), ("total_tokens", c_i32), ("probs", c_vp),
+        ("probs_seq_stride", c_i64), ("probs_tok_stride", c_i64), ("draft_probs", c_vp), ("draft_seq_stride", c_i64),
+        ("draft_tok_stride", c_i64), ("tokens", c_vp), ("parent", c_vp), ("uniforms", c_vp), ("cu_draft", c_vp),
+        ("cache_idx", c_vp), ("accept_len", c_vp), ("accept_node", c_vp), ("path", c_vp), ("out_tokens", c_vp), ("err", c_vp),
+    ]
+
+
+class QkNormRopeArgs(ctypes.Structure):
+    """Mirror of cv_qk_norm_rope_args."""
+    _fields_ = [
+        ("n_seq", c_i32), ("T", c_i32), ("n_heads", c_i32), ("n_kv_heads", c_i32), ("head_dim", c_i32), ("dtype", c_i32),
+        ("total_tokens", c_i32), ("rot_dim", c_i32), ("pairs", c_i32), ("norm", c_i32), ("n_positions", c_i32),
+        ("eps", ctypes.c_float),
+        ("q", c_vp), ("q_seq_stride", c_i64), ("q_tok_stride", c_i64), ("q_head_stride", c_i64),
+        ("q_out", c_vp), ("q_out_seq_stride", c_i64), ("q_out_tok_stride", c_i64), ("q_out_head_stride", c_i64),
+        ("k", c_vp), ("k_seq_stride", c_i64), ("k_tok_stride", c_i64), ("k_head_stride", c_i64),
+        ("k_out", c_vp), ("k_out_seq_stride", c_i64), ("k_out_tok_stride", c_i64), ("k_out_head_stride", c_i64),
+        ("v", c_vp), ("v_seq_stride", c_i64), ("v_tok_stride", c_i64), ("v_head_stride", c_i64),
+        ("q_weight", c_vp), ("k_weight", c_vp), ("cos_sin", c_vp), ("cos_sin_stride", c_i64), ("positions", c_vp), ("cu", c_vp),
+        ("cache_len", c_vp), ("cache_idx", c_vp), ("cache", Cache), ("err", c_vp),
+    ]
+
+
+class CacheCompactArgs(ctypes.Structure):
+    """Mirror of cv_cache_compact_args."""
+    _fields_ = [("n_seq", c_i32), ("T", c_i32), ("cache", Cache), ("cache_len", c_vp), ("path", c_vp), ("accept_len", c_vp),
+                ("cache_idx", c_vp), ("new_len", c_vp), ("err", c_vp)]
+
+
+class CachePagesArgs(ctypes.Structure):
+    """Mirror of cv_cache_pages_args."""
+    _fields_ = [("n_seq", c_i32), ("cache", Cache), ("idx", c_vp), ("src_idx", c_vp), ("n_tokens", c_vp), ("err", c_vp)]
+
+
 class CvError(RuntimeError):
     def __init__(self, status: int, what: str):
         super().__init__(f"{what}: {status_string(status)} (status {status})")
@@ -156,6 +228,13 @@ def load_library(path: Optional[str] = None):
     lib.cv_linattn_step.restype = c_i32
     lib.cv_block_norm.argtypes = [ctypes.POINTER(NormArgs), c_vp]
     lib.cv_block_norm.restype = c_i32
+    for name, args in (("cv_tree_attention", TreeAttentionArgs), ("cv_draft_verify", DraftVerifyArgs),
+                       ("cv_qk_norm_rope", QkNormRopeArgs), ("cv_cache_compact", CacheCompactArgs),
+                       ("cv_cache_reserve", CachePagesArgs), ("cv_cache_fork", CachePagesArgs), ("cv_cache_free", CachePagesArgs)):
+        getattr(lib, name).argtypes = [ctypes.POINTER(args), c_vp]
+        getattr(lib, name).restype = c_i32
+    lib.cv_tree_attention_workspace.argtypes = [ctypes.POINTER(TreeAttentionArgs), ctypes.POINTER(c_i64)]
+    lib.cv_tree_attention_workspace.restype = c_i32
     lib.cv_status_string.argtypes = [c_i32]
     lib.cv_status_string.restype = ctypes.c_char_p
     lib.cv_abi_version.argtypes = []
@@ -798,3 +877,370 @@ def block_norm(y, out, *, gate=None, gate_act=None, gate_first=False, group=0, p
     rc = load_library().cv_block_norm(ctypes.byref(a), _stream_of(stream, y))
     if rc != 0:
         raise CvError(rc, "cv_block_norm")
+
+
+# cv_cache and the structs around it as the struct module writes them
+_CACHE = struct.Struct("<2Q8q8iQq2Q")
+_IN = f"{_CACHE.size}s"
+_TREE_ATTENTION = struct.Struct("<4ifi" + _IN + "Q3qQ3q4QQQq")
+_DRAFT_VERIFY = struct.Struct("<5i4xQ2qQ2q5Q5Q")
+_QK_NORM_ROPE = struct.Struct("<11if" + 5 * "Q3q" + "3Qq4Q" + _IN + "Q")
+_COMPACT = struct.Struct("<2i" + _IN + "6Q")
+_PAGES = struct.Struct("<i4x" + _IN + "4Q")
+_NO_CACHE = bytes(_CACHE.size)
+
+
+class PagedCache:
+    """A cache of K and V in pages (cv_cache): position x of slot r is row x % page_size of page page_table[r, x // page_size].
+
+    k, v [n_pages, page_size, n_kv_heads, head_dim], or [n_layers, n_pages, ...] for cache_compact and cache_fork (innermost
+    stride 1, the others free, one dtype); page_table int32 [n_slots, max_pages], entries past those in use may be
+    anything.  held int32 [n_slots] (pages of each slot) and refs int32 [n_pages] (slots that hold each page, 0 = free) are
+    needed by cache_reserve, cache_fork and cache_free.  Made once for the tensors, which it keeps; layer(i) is the cache
+    of one layer."""
+    __slots__ = ("_k", "_v", "_page_table", "_held", "_refs", "_packed")
+
+    def __init__(self, k, v, page_table, *, held=None, refs=None):
+        if k.dim() not in (4, 5) or v.shape != k.shape:
+            raise ValueError("k and v must be [n_pages, page_size, n_kv_heads, head_dim] or [n_layers, n_pages, ...] alike, got "
+                             f"{tuple(k.shape)} and {tuple(v.shape)}")
+        if v.dtype is not k.dtype:
+            raise TypeError("k and v must share one dtype")
+        dtype = _dtype_code(k)
+        if k.shape[-1] > 1 and (k.stride(-1) != 1 or v.stride(-1) != 1):
+            raise ValueError("k and v need a unit innermost stride")
+        _load_types()
+        if page_table.dim() != 2 or page_table.dtype is not _i32 or (page_table.shape[1] > 1 and page_table.stride(1) != 1):
+            raise ValueError("page_table must be int32 [n_slots, max_pages] with a unit innermost stride")
+        _need_int32(held, "held", shape=(page_table.shape[0],))
+        _need_int32(refs, "refs", shape=(k.shape[-4],))
+        self._k, self._v, self._page_table, self._held, self._refs = k, v, page_table, held, refs
+        ks, vs = k.stride()[-5:-1], v.stride()[-5:-1]
+        if k.dim() == 4:
+            ks, vs = (0, *ks), (0, *vs)
+        rows = page_table.stride(0) if page_table.shape[0] > 1 else page_table.shape[1]
+        self._packed = _CACHE.pack(
+            k.data_ptr(), v.data_ptr(), *ks, *vs, k.shape[0] if k.dim() == 5 else 1, *k.shape[-4:], *page_table.shape, dtype,
+            page_table.data_ptr(), rows, held.data_ptr() if held is not None else 0,
+            refs.data_ptr() if refs is not None else 0)
+
+    k = property(lambda self: self._k)
+    v = property(lambda self: self._v)
+    page_table = property(lambda self: self._page_table)
+    held = property(lambda self: self._held)
+    refs = property(lambda self: self._refs)
+
+    def layer(self, i) -> "PagedCache":
+        """The cache of layer i of [n_layers, ...] tensors."""
+        return PagedCache(self._k[i], self._v[i], self._page_table, held=self._held, refs=self._refs)
+
+    def _tensors(self):
+        return self._k, self._v, self._page_table, self._held, self._refs
+
+
+def _one_layer(cache) -> None:
+    if cache._k.dim() != 4:
+        raise ValueError("this call takes the cache of one layer (PagedCache.layer)")
+
+
+def _required(t, name, n) -> int:
+    if t is None:
+        raise ValueError(f"{name} is required")
+    return _index_array(t, name, n)
+
+
+def _exactly(t, name, shape) -> int:
+    """Pointer of a contiguous int32 array of the given shape, or 0."""
+    if t is None:
+        return 0
+    _need_int32(t, name, shape=shape)
+    return t.data_ptr()
+
+
+def _rows_of(t, name, lead, d, dtype):
+    """Pointer and (sequence, token, head) strides of [*lead, heads, d] rows; packed rows have no sequence stride."""
+    if t is None:
+        return 0, 0, 0, 0
+    if t.dim() != len(lead) + 2 or t.shape[:-2] != lead or t.shape[-1] != d:
+        raise ValueError(f"{name} must be [{', '.join(map(str, lead))}, heads, {d}], got {tuple(t.shape)}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must have dtype {dtype}")
+    st = t.stride()
+    if d > 1 and st[-1] != 1:
+        raise ValueError(f"{name} needs a unit innermost stride")
+    return (t.data_ptr(), *(st[:3] if len(lead) == 2 else (0, st[0], st[1])))
+
+
+def _lead(shape, cu, T, name):
+    """(n_seq, T, total, lead) of [n_seq, T, ...] rows, or [total, ...] with cu."""
+    if cu is None:
+        if len(shape) < 2:
+            raise ValueError(f"{name} must be [n_seq, T, ...]")
+        if T is not None and T != shape[1]:
+            raise ValueError(f"T = {T} but {name} holds {shape[1]} tokens a sequence")
+        return shape[0], shape[1], 0, shape[:2]
+    if cu.dim() != 1 or cu.shape[0] < 1:
+        raise ValueError("the cumulative counts must be [n_seq + 1]")
+    _need_int32(cu, "the cumulative counts")
+    if T is None:
+        raise ValueError("packed rows need T, the largest count")
+    return cu.shape[0] - 1, int(T), shape[0], shape[:1]
+
+
+def make_tree_attention_args(q, out, cache, cache_len, *, parent=None, scale=None, cu_draft=None, T=None, cache_idx=None, err=None,
+                             workspace=None, wait_polls=0, check_device=True) -> TreeAttentionArgs:
+    """Build cv_tree_attention_args (see tree_attention)."""
+    _one_layer(cache)
+    if q.dim() != (4 if cu_draft is None else 3):
+        raise ValueError("q must be [n_seq, T, n_heads, head_dim], or [total, n_heads, head_dim] with cu_draft")
+    n, T, total, lead = _lead(q.shape, cu_draft, T, "q")
+    d, dt = cache._k.shape[-1], cache._k.dtype
+    if out is None or out.shape != q.shape:
+        raise ValueError("out must have the shape of q")
+    rows = (*_rows_of(q, "q", lead, d, dt), *_rows_of(out, "out", lead, d, dt))
+    ws, ws_bytes = (workspace.data_ptr(), workspace.numel() * workspace.element_size()) if workspace is not None else (0, 0)
+    if check_device:
+        _one_device(q, out, *cache._tensors(), cache_len, parent, cu_draft, cache_idx, err, workspace)
+    return TreeAttentionArgs.from_buffer_copy(_TREE_ATTENTION.pack(
+        n, T, q.shape[-2], total, d ** -0.5 if scale is None else scale, wait_polls, cache._packed, *rows,
+        cu_draft.data_ptr() if cu_draft is not None else 0, _exactly(parent, "parent", lead), _required(cache_len, "cache_len", n),
+        _index_array(cache_idx, "cache_idx", n), _index_array(err, "err", n), ws, ws_bytes))
+
+
+def tree_attention_workspace(q, out, cache, cache_len, **kw) -> int:
+    """Bytes of workspace tree_attention needs for these arguments on the current device (0 = none)."""
+    return _attention_workspace(make_tree_attention_args(q, out, cache, cache_len, check_device=False, **kw))
+
+
+def _attention_workspace(a: TreeAttentionArgs) -> int:
+    n = c_i64(0)
+    rc = load_library().cv_tree_attention_workspace(ctypes.byref(a), ctypes.byref(n))
+    if rc != 0:
+        raise CvError(rc, "cv_tree_attention_workspace")
+    return n.value
+
+
+def tree_attention(q, out, cache, cache_len, *, parent=None, scale=None, cu_draft=None, T=None, cache_idx=None, err=None,
+                   workspace=None, wait_polls=0, stream=None) -> None:
+    """Queue attention of drafted tokens over a paged cache (cv_tree_attention).
+
+    q, out [n_seq, T, n_heads, head_dim], or with cu_draft (int32 [n_seq + 1]) packed [total, n_heads, head_dim] rows, T then
+    being the largest count; dtype of the cache, innermost stride 1, the others free.  cache_len int32 [n_seq]: tokens
+    before the drafts, whose own K and V stand at positions cache_len .. cache_len + T - 1 already (qk_norm_rope writes
+    them there).  parent int32 like q's rows: a draft attends to the cached tokens, its ancestors and itself; without parent
+    to all drafts before it.  scale defaults to head_dim**-0.5.  Writes out (and err).  workspace: a uint8 buffer of
+    tree_attention_workspace bytes; by default torch's allocator gives one for the call."""
+    a = make_tree_attention_args(q, out, cache, cache_len, parent=parent, scale=scale, cu_draft=cu_draft, T=T,
+                                 cache_idx=cache_idx, err=err, workspace=workspace, wait_polls=wait_polls)
+    lib, on = load_library(), _stream_of(stream, q)
+    rc = lib.cv_tree_attention(ctypes.byref(a), on)
+    if rc == ERR_WORKSPACE and workspace is None:  # nothing was launched: this call needs one
+        import torch
+        if stream is not None and not isinstance(stream, torch.cuda.Stream):
+            raise ValueError("pass workspace with a raw stream handle")
+        need = _attention_workspace(a)
+        # from the stream's own pool: a block freed on another stream may still be in use there
+        with torch.cuda.stream(stream):
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        a.workspace, a.workspace_bytes = workspace.data_ptr(), need
+        rc = lib.cv_tree_attention(ctypes.byref(a), on)
+    if rc != 0:
+        raise CvError(rc, "cv_tree_attention")
+
+
+def make_draft_verify_args(probs, tokens, uniforms, accept_len, out_tokens, *, draft_probs=None, parent=None, path=None,
+                           accept_node=None, cu_draft=None, T=None, cache_idx=None, err=None,
+                           check_device=True) -> DraftVerifyArgs:
+    """Build cv_draft_verify_args (see draft_verify)."""
+    f32 = _f32 or _load_types()
+    if probs.dim() != (3 if cu_draft is None else 2):
+        raise ValueError("probs must be [n_seq, T, vocab], or [total, vocab] with cu_draft")
+    n, T, total, lead = _lead(probs.shape, cu_draft, T, "probs")
+    V = probs.shape[-1]
+    code = _dtype_code(probs)
+
+    def rows(t, name):
+        if t is None:
+            return 0, 0, 0
+        if t.shape != probs.shape or t.dtype is not probs.dtype:
+            raise ValueError(f"{name} must have the shape and dtype of probs")
+        st = t.stride()
+        if V > 1 and st[-1] != 1:
+            raise ValueError(f"{name} needs a unit innermost stride")
+        return (t.data_ptr(), *(st[:2] if cu_draft is None else (0, st[0])))
+
+    if uniforms.dtype is not f32 or uniforms.shape != (n, T + 1) or not uniforms.is_contiguous():
+        raise ValueError(f"uniforms must be contiguous float32 [{n}, {T + 1}]")
+    if tokens is None or accept_len is None or out_tokens is None:
+        raise ValueError("tokens, accept_len and out_tokens are required")
+    if check_device:
+        _one_device(probs, tokens, uniforms, accept_len, out_tokens, draft_probs, parent, path, accept_node, cu_draft, cache_idx, err)
+    return DraftVerifyArgs.from_buffer_copy(_DRAFT_VERIFY.pack(
+        n, T, V, code, total, *rows(probs, "probs"), *rows(draft_probs, "draft_probs"), _exactly(tokens, "tokens", lead),
+        _exactly(parent, "parent", lead), uniforms.data_ptr(), cu_draft.data_ptr() if cu_draft is not None else 0,
+        _index_array(cache_idx, "cache_idx", n), _index_array(accept_len, "accept_len", n),
+        _index_array(accept_node, "accept_node", n), _exactly(path, "path", (n, T)), _exactly(out_tokens, "out_tokens", (n, T)),
+        _index_array(err, "err", n)))
+
+
+def draft_verify(probs, tokens, uniforms, accept_len, out_tokens, *, draft_probs=None, parent=None, path=None, accept_node=None,
+                 cu_draft=None, T=None, cache_idx=None, err=None, stream=None) -> None:
+    """Queue the verification of drafted tokens (cv_draft_verify): which of them stand, and the token sampled after them.
+
+    probs [n_seq, T, vocab] (bf16 or fp32): the target's distribution after each draft; tokens int32 [n_seq, T], token 0 the
+    last step's; uniforms fp32 [n_seq, T + 1] in [0, 1): one for each draft's choice among its children, and the last for the
+    new token.  draft_probs like probs (a chain only): row t is what token t was drawn from.  parent int32 [n_seq, T] for
+    trees.  With cu_draft packed rows ([total, vocab], [total]), T being the largest count.  Writes accept_len int32
+    [n_seq] (1 .. T: for conv_commit and LinattnDrafts of a chain), accept_node (1 + the last accepted token's index: for
+    conv_commit of a tree), path int32 [n_seq, T] (for cache_compact), out_tokens int32 [n_seq, T] (this step's tokens: the
+    accepted ones after token 0 and the new one, then -1), and err."""
+    a = make_draft_verify_args(probs, tokens, uniforms, accept_len, out_tokens, draft_probs=draft_probs, parent=parent, path=path,
+                               accept_node=accept_node, cu_draft=cu_draft, T=T, cache_idx=cache_idx, err=err)
+    rc = load_library().cv_draft_verify(ctypes.byref(a), _stream_of(stream, probs))
+    if rc != 0:
+        raise CvError(rc, "cv_draft_verify")
+
+
+def make_qk_norm_rope_args(q, k, q_out, *, k_out=None, v=None, cos_sin=None, q_weight=None, k_weight=None, norm=True, eps=1e-6,
+                           pairs=False, positions=None, cache=None, cache_len=None, cu_seqlens=None, max_seqlen=None,
+                           cache_idx=None, err=None, check_device=True) -> QkNormRopeArgs:
+    """Build cv_qk_norm_rope_args (see qk_norm_rope)."""
+    f32 = _f32 or _load_types()
+    if q.dim() != (4 if cu_seqlens is None else 3):
+        raise ValueError("q must be [n_seq, T, n_heads, head_dim], or [total, n_heads, head_dim] with cu_seqlens")
+    n, T, total, lead = _lead(q.shape, cu_seqlens, max_seqlen if cu_seqlens is not None else None, "q")
+    if cu_seqlens is None and max_seqlen is not None and max_seqlen < T:
+        raise ValueError(f"max_seqlen = {max_seqlen} but q holds {T} tokens a sequence")
+    d, dt = q.shape[-1], q.dtype
+    kv = k.shape[-2] if k is not None else 0
+    if q_out is None or q_out.shape != q.shape:
+        raise ValueError("q_out must have the shape of q")
+    if k is None and (k_out is not None or v is not None):
+        raise ValueError("k_out and v need k")
+    for t, name in ((k_out, "k_out"), (v, "v")):
+        if t is not None and t.shape != k.shape:
+            raise ValueError(f"{name} must have the shape of k")
+    if v is not None and cache is None:
+        raise ValueError("v needs a cache to be written to")
+    if k is not None and k_out is None and cache is None:
+        raise ValueError("k needs k_out or a cache to be written to")
+    packed = _NO_CACHE
+    if cache is not None:
+        _one_layer(cache)
+        if k is None or cache._k.shape[-2:] != k.shape[-2:] or cache._k.dtype is not dt:
+            raise ValueError("the cache must have the kv heads, head size and dtype of k")
+        packed = cache._packed
+
+    def weight(t, name):
+        if t is None:
+            return 0
+        if t.shape != (d,) or t.dtype is not dt or not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous [{d}] and have the dtype of q")
+        return t.data_ptr()
+
+    cs, cs_row, rot, n_pos = 0, 0, 0, 0
+    if cos_sin is not None:
+        if cos_sin.dim() != 2 or cos_sin.dtype is not f32 or (cos_sin.shape[1] > 1 and cos_sin.stride(1) != 1):
+            raise ValueError("cos_sin must be float32 [n_positions, rot_dim] with a unit innermost stride")
+        n_pos, rot = cos_sin.shape
+        cs, cs_row = cos_sin.data_ptr(), cos_sin.stride(0) if n_pos > 1 else rot
+        if positions is None and cache_len is None:
+            raise ValueError("the rotation needs positions, or cache_len")
+    if check_device:
+        _one_device(q, k, q_out, k_out, v, cos_sin, q_weight, k_weight, positions, cache_len, cu_seqlens, cache_idx, err,
+                    *(cache._tensors() if cache is not None else ()))
+    return QkNormRopeArgs.from_buffer_copy(_QK_NORM_ROPE.pack(
+        n, T, q.shape[-2], kv, d, _dtype_code(q), total, rot, 1 if pairs else 0, 1 if norm else 0, n_pos, eps,
+        *_rows_of(q, "q", lead, d, dt), *_rows_of(q_out, "q_out", lead, d, dt), *_rows_of(k, "k", lead, d, dt),
+        *_rows_of(k_out, "k_out", lead, d, dt), *_rows_of(v, "v", lead, d, dt), weight(q_weight, "q_weight"),
+        weight(k_weight, "k_weight"), cs, cs_row, _exactly(positions, "positions", lead),
+        cu_seqlens.data_ptr() if cu_seqlens is not None else 0,
+        _required(cache_len, "cache_len", n) if cache is not None else _index_array(cache_len, "cache_len", n),
+        _index_array(cache_idx, "cache_idx", n), packed, _index_array(err, "err", n)))
+
+
+def qk_norm_rope(q, k, q_out, *, k_out=None, v=None, cos_sin=None, q_weight=None, k_weight=None, norm=True, eps=1e-6, pairs=False,
+                 positions=None, cache=None, cache_len=None, cu_seqlens=None, max_seqlen=None, cache_idx=None, err=None,
+                 stream=None) -> None:
+    """Queue the norms of query and key heads and their rotation by position (cv_qk_norm_rope).
+
+    q, q_out [n_seq, T, n_heads, head_dim] and k, k_out, v [n_seq, T, n_kv_heads, head_dim], or with cu_seqlens packed [total, ...]
+    rows, max_seqlen then bounding the lengths; innermost stride 1, the others free (slices of one projection will do).  Every head
+    is RMS-normed with q_weight or k_weight [head_dim] (norm False: not at all) and its first cos_sin.shape[1] channels rotated:
+    cos_sin fp32 [n_positions, rot_dim], a row's cosines then its sines; pairs: neighbouring channels turn together, else
+    channel i and i + rot_dim/2.  positions int32 like q's rows, by default cache_len + t.  With cache, K and V go to positions
+    cache_len + t of the sequences' pages.  q_out may be q and k_out may be k."""
+    a = make_qk_norm_rope_args(q, k, q_out, k_out=k_out, v=v, cos_sin=cos_sin, q_weight=q_weight, k_weight=k_weight, norm=norm,
+                               eps=eps, pairs=pairs, positions=positions, cache=cache, cache_len=cache_len, cu_seqlens=cu_seqlens,
+                               max_seqlen=max_seqlen, cache_idx=cache_idx, err=err)
+    rc = load_library().cv_qk_norm_rope(ctypes.byref(a), _stream_of(stream, q))
+    if rc != 0:
+        raise CvError(rc, "cv_qk_norm_rope")
+
+
+def make_cache_compact_args(cache, cache_len, path, accept_len, *, new_len=None, cache_idx=None, err=None,
+                            check_device=True) -> CacheCompactArgs:
+    """Build cv_cache_compact_args (see cache_compact)."""
+    if path.dim() != 2:
+        raise ValueError("path must be int32 [n_seq, T]")
+    n, T = path.shape
+    _load_types()
+    if check_device:
+        _one_device(path, *cache._tensors(), cache_len, accept_len, new_len, cache_idx, err)
+    return CacheCompactArgs.from_buffer_copy(_COMPACT.pack(
+        n, T, cache._packed, _required(cache_len, "cache_len", n), _exactly(path, "path", (n, T)),
+        _required(accept_len, "accept_len", n), _index_array(cache_idx, "cache_idx", n), _index_array(new_len, "new_len", n),
+        _index_array(err, "err", n)))
+
+
+def cache_compact(cache, cache_len, path, accept_len, *, new_len=None, cache_idx=None, err=None, stream=None) -> None:
+    """Queue the move of each sequence's accepted path to its place in the cache (cv_cache_compact): row cache_len + path[s, i]
+    of every layer's K and V goes to cache_len + i, i < accept_len[s].  path int32 [n_seq, T] as draft_verify leaves it.  new_len
+    int32 [n_seq] receives cache_len + accept_len; it may not be cache_len itself."""
+    a = make_cache_compact_args(cache, cache_len, path, accept_len, new_len=new_len, cache_idx=cache_idx, err=err)
+    rc = load_library().cv_cache_compact(ctypes.byref(a), _stream_of(stream, path))
+    if rc != 0:
+        raise CvError(rc, "cv_cache_compact")
+
+
+def make_cache_pages_args(cache, n_seq, *, idx=None, src_idx=None, n_tokens=None, err=None, check_device=True) -> CachePagesArgs:
+    """Build cv_cache_pages_args (see cache_reserve, cache_fork and cache_free)."""
+    _load_types()
+    if cache._held is None or cache._refs is None:
+        raise ValueError("the cache needs held and refs")
+    if check_device:
+        _one_device(*cache._tensors(), idx, src_idx, n_tokens, err)
+    return CachePagesArgs.from_buffer_copy(_PAGES.pack(
+        n_seq, cache._packed, _exactly(idx, "cache_idx", (n_seq,)), _exactly(src_idx, "src_idx", (n_seq,)),
+        _exactly(n_tokens, "n_tokens", (n_seq,)), _index_array(err, "err", n_seq)))
+
+
+def cache_reserve(cache, n_tokens, *, cache_idx=None, err=None, stream=None) -> None:
+    """Queue the growth of slots (cv_cache_reserve): slot cache_idx[s] (default s) gets pages for n_tokens[s] tokens in all, the free
+    pages with the lowest numbers, sequences in order."""
+    a = make_cache_pages_args(cache, n_tokens.shape[0], idx=cache_idx, n_tokens=n_tokens, err=err)
+    rc = load_library().cv_cache_reserve(ctypes.byref(a), _stream_of(stream, n_tokens))
+    if rc != 0:
+        raise CvError(rc, "cv_cache_reserve")
+
+
+def cache_fork(cache, src_idx, dst_idx, n_tokens, *, err=None, stream=None) -> None:
+    """Queue forks (cv_cache_fork): slot dst_idx[s], which holds no pages, gets the first n_tokens[s] tokens of slot src_idx[s]: full
+    pages shared, the rest of the last one copied (every layer)."""
+    a = make_cache_pages_args(cache, n_tokens.shape[0], idx=dst_idx, src_idx=src_idx, n_tokens=n_tokens, err=err)
+    rc = load_library().cv_cache_fork(ctypes.byref(a), _stream_of(stream, n_tokens))
+    if rc != 0:
+        raise CvError(rc, "cv_cache_fork")
+
+
+def cache_free(cache, n_tokens=None, *, cache_idx=None, err=None, stream=None) -> None:
+    """Queue the release of pages (cv_cache_free): slot cache_idx[s] (default s) keeps those of its first n_tokens[s] tokens
+    (default 0: none).  A page is free again once no slot holds it."""
+    if n_tokens is None and cache_idx is None:
+        n = cache.page_table.shape[0]
+    else:
+        n = (n_tokens if n_tokens is not None else cache_idx).shape[0]
+    a = make_cache_pages_args(cache, n, idx=cache_idx, n_tokens=n_tokens, err=err)
+    rc = load_library().cv_cache_free(ctypes.byref(a), _stream_of(stream, cache.page_table))
+    if rc != 0:
+        raise CvError(rc, "cv_cache_free")

@@ -1,0 +1,416 @@
+// C ABI of the attention layers' operators: attention over a paged cache, draft verification, query and key norms with
+// rotation, and the cache's pages.  Every check runs on the host before anything is launched.
+#include <cstdint>
+#include <cstring>
+
+#include "convverify.h"
+#include "cv_attn.h"
+#include "cv_host.h"
+
+namespace {
+
+using cvk::aligned16;
+using cvk::device_limits;
+using cvk::launch_pdl;
+
+constexpr int kMaxHeads = 4096, kMaxLayers = 4096, kMaxPage = 65536, kMaxHeadDim = 256, kMaxVocab = 1 << 24;
+constexpr int64_t kMaxTokens = 0x7fffffff;
+
+int esize_of(int dtype) { return dtype == CV_BF16 ? 2 : 4; }
+
+int check_cache(const cv_cache &c, bool pointers, bool counts) {
+    if (c.dtype != CV_F32 && c.dtype != CV_BF16) return CV_ERR_DTYPE;
+    if (c.n_layers < 1 || c.n_layers > kMaxLayers || c.n_pages < 1 || c.page_size < 1 || c.page_size > kMaxPage ||
+        c.n_kv_heads < 1 || c.n_kv_heads > kMaxHeads || c.n_slots < 1 || c.max_pages < 1 ||
+        (int64_t)c.max_pages * c.page_size > kMaxTokens)
+        return CV_ERR_SHAPE;
+    if (c.head_dim < 1 || c.head_dim > kMaxHeadDim) return CV_ERR_HEAD_DIM;
+    const int64_t strides[] = {c.k_layer_stride, c.k_page_stride, c.k_row_stride, c.k_head_stride,
+                               c.v_layer_stride, c.v_page_stride, c.v_row_stride, c.v_head_stride};
+    for (int64_t s : strides)
+        if (s < 0) return CV_ERR_STRIDE;
+    if (c.table_stride < c.max_pages && c.n_slots > 1) return CV_ERR_STRIDE;
+    if (pointers && (!c.page_table || !c.k || !c.v)) return CV_ERR_NULL_POINTER;
+    if (pointers && counts && (!c.held || !c.refs)) return CV_ERR_NULL_POINTER;
+    return CV_OK;
+}
+
+cvk::CacheView view(const cv_cache &c) {
+    return {c.k, c.v, c.k_layer_stride, c.k_page_stride, c.k_row_stride, c.k_head_stride, c.v_layer_stride,
+            c.v_page_stride, c.v_row_stride, c.v_head_stride, c.n_layers, c.n_pages, c.page_size, c.n_kv_heads,
+            c.head_dim, c.n_slots, c.max_pages, c.page_table, c.table_stride, c.held, c.refs};
+}
+
+// Whether a cache tensor's rows are whole 16-byte pieces at 16-byte addresses.
+bool rows16(const void *p, int64_t layer, int64_t page, int64_t row, int64_t head, const cv_cache &c) {
+    const int es = esize_of(c.dtype);
+    return aligned16(p) && c.head_dim * es % 16 == 0 && (c.n_layers == 1 || layer * es % 16 == 0) && page * es % 16 == 0 &&
+           (c.page_size == 1 || row * es % 16 == 0) && (c.n_kv_heads == 1 || head * es % 16 == 0);
+}
+
+// Clears err where kernels OR their bits into it.
+int clear_err(int32_t *err, int n_seq, cudaStream_t stream) {
+    return err && cudaMemsetAsync(err, 0, sizeof(int32_t) * (size_t)n_seq, stream) != cudaSuccess ? CV_ERR_LAUNCH : CV_OK;
+}
+
+// ---- attention
+
+int check_attention(const cv_tree_attention_args *a, bool pointers) {
+    if (!a) return CV_ERR_NULL_ARGS;
+    const int rc = check_cache(a->cache, false, false);
+    if (rc != CV_OK) return rc;
+    if (a->n_seq < 0 || a->n_seq > 65535 || a->n_heads < 1 || a->n_heads > kMaxHeads) return CV_ERR_SHAPE;
+    if (a->T < 1 || a->T > CV_MAX_T) return CV_ERR_TOKENS;
+    if (a->n_heads % a->cache.n_kv_heads != 0) return CV_ERR_HEAD_DIM;
+    if (a->cu_draft && a->total_tokens < 0) return CV_ERR_SHAPE;
+    const int64_t strides[] = {a->q_seq_stride, a->q_tok_stride, a->q_head_stride, a->out_seq_stride, a->out_tok_stride,
+                               a->out_head_stride};
+    for (int64_t s : strides)
+        if (s < 0) return CV_ERR_STRIDE;
+    if (!pointers || a->n_seq == 0) return CV_OK;
+    if (a->cu_draft && a->total_tokens == 0) return CV_OK;
+    if (!a->q || !a->out || !a->cache_len || !a->cache.k || !a->cache.v || !a->cache.page_table) return CV_ERR_NULL_POINTER;
+    if (a->out == a->q || a->out == a->cache.k || a->out == a->cache.v) return CV_ERR_ALIAS;
+    return CV_OK;
+}
+
+struct AttnPlan {
+    cvk::AttnSimt simt;
+    int dp, rows, keys, parts;
+    bool cut;
+    int64_t bytes;
+};
+
+AttnPlan plan_attention(const cv_tree_attention_args *a) {
+    const cv_cache &c = a->cache;
+    const int es = esize_of(c.dtype), G = a->n_heads / c.n_kv_heads;
+    AttnPlan pl;
+    const bool vec = rows16(c.k, 0, c.k_page_stride, c.k_row_stride, c.k_head_stride, c) &&
+                     rows16(c.v, 0, c.v_page_stride, c.v_row_stride, c.v_head_stride, c) && aligned16(a->q) &&
+                     a->q_seq_stride * es % 16 == 0 && a->q_tok_stride * es % 16 == 0 && a->q_head_stride * es % 16 == 0;
+    pl.dp = c.head_dim <= 64 ? 64 : c.head_dim <= 128 ? 128 : 256;
+    pl.simt = cvk::attn_simt_kernel(c.dtype == CV_BF16, pl.dp, vec);
+    pl.rows = cvk::kSimtRows, pl.keys = pl.simt.keys;
+    const cvk::DeviceLimits d = device_limits();
+    const int resident = d.smem_per_sm / (pl.simt.smem_bytes + 1024);
+    pl.parts = d.sms * (resident < 1 ? 1 : resident > 2 ? 2 : resident);
+    // tiles there can be at most: fewer blocks are enough for fewer
+    const int64_t tiles = ((int64_t)c.max_pages * c.page_size + pl.keys - 1) / pl.keys;
+    const int64_t units = (int64_t)a->n_seq * c.n_kv_heads * (((int64_t)a->T * G + pl.rows - 1) / pl.rows);
+    if (units * tiles < pl.parts) pl.parts = (int)(units * tiles);
+    pl.cut = tiles > 1;
+    pl.bytes = pl.cut ? 2LL * pl.parts * cvk::part_floats(pl.rows, pl.dp) * 4 : 0;
+    return pl;
+}
+
+int launch_attention(const cv_tree_attention_args *a, cudaStream_t stream) {
+    const cv_cache &c = a->cache;
+    const AttnPlan pl = plan_attention(a);
+    if (pl.bytes > 0 && (!a->workspace || reinterpret_cast<uintptr_t>(a->workspace) % 256 != 0 || a->workspace_bytes < pl.bytes))
+        return CV_ERR_WORKSPACE;
+    cvk::AttnParams p;
+    std::memset(&p, 0, sizeof p);
+    p.n_seq = a->n_seq, p.T = a->T, p.total = a->total_tokens, p.n_heads = a->n_heads, p.G = a->n_heads / c.n_kv_heads;
+    p.scale = a->scale * 1.4426950408889634f;
+    p.c = view(c);
+    p.q = a->q, p.q_seq = a->q_seq_stride, p.q_tok = a->q_tok_stride, p.q_head = a->q_head_stride;
+    p.out = a->out, p.o_seq = a->out_seq_stride, p.o_tok = a->out_tok_stride, p.o_head = a->out_head_stride;
+    p.cu = a->cu_draft, p.parent = a->parent, p.len = a->cache_len, p.idx = a->cache_idx, p.err = a->err;
+    p.rows = pl.rows, p.keys = pl.keys, p.dp = pl.dp, p.parts = pl.parts;
+    p.ws = pl.cut ? reinterpret_cast<float *>(a->workspace) : nullptr;
+    const int rc = clear_err(a->err, a->n_seq, stream);
+    if (rc != CV_OK) return rc;
+    if (cvk::ensure_smem(reinterpret_cast<const void *>(pl.simt.fn), pl.simt.smem_bytes) != cudaSuccess) return CV_ERR_LAUNCH;
+    if (launch_pdl(pl.simt.fn, dim3((unsigned)pl.parts), dim3(cvk::kSimtThreads), pl.simt.smem_bytes, stream, p) != cudaSuccess)
+        return CV_ERR_LAUNCH;
+    if (pl.cut) {
+        const dim3 grid((unsigned)pl.parts, (unsigned)((pl.rows + cvk::kAttnJoinRows - 1) / cvk::kAttnJoinRows));
+        if (launch_pdl(cvk::attn_join_kernel(c.dtype == CV_BF16), grid, dim3(cvk::kAttnJoinThreads), 0, stream, p) != cudaSuccess)
+            return CV_ERR_LAUNCH;
+    }
+    return cudaGetLastError() == cudaSuccess ? CV_OK : CV_ERR_LAUNCH;
+}
+
+// ---- draft verification
+
+int check_sample(const cv_draft_verify_args *a) {
+    if (!a) return CV_ERR_NULL_ARGS;
+    if (a->dtype != CV_F32 && a->dtype != CV_BF16) return CV_ERR_DTYPE;
+    if (a->n_seq < 0 || a->n_seq > 65535 || a->vocab < 1 || a->vocab > kMaxVocab || (a->cu_draft && a->total_tokens < 0))
+        return CV_ERR_SHAPE;
+    if (a->T < 1 || a->T > CV_MAX_T) return CV_ERR_TOKENS;
+    if (a->draft_probs && a->parent) return CV_ERR_LAYOUT;
+    if (a->probs_seq_stride < 0 || a->probs_tok_stride < 0 || a->draft_seq_stride < 0 || a->draft_tok_stride < 0)
+        return CV_ERR_STRIDE;
+    if (a->n_seq == 0) return CV_OK;
+    const bool rows = !a->cu_draft || a->total_tokens > 0;
+    if ((rows && (!a->probs || !a->tokens)) || !a->uniforms || !a->accept_len || !a->out_tokens) return CV_ERR_NULL_POINTER;
+    const void *outs[] = {a->accept_len, a->accept_node, a->path, a->out_tokens, a->err};
+    const void *ins[] = {a->probs, a->draft_probs, a->tokens, a->parent, a->uniforms, a->cu_draft, a->cache_idx};
+    for (int i = 0; i < 5; ++i) {
+        if (!outs[i]) continue;
+        for (const void *in : ins)
+            if (outs[i] == in) return CV_ERR_ALIAS;
+        for (int j = 0; j < i; ++j)
+            if (outs[i] == outs[j]) return CV_ERR_ALIAS;
+    }
+    return CV_OK;
+}
+
+// ---- query and key norms
+
+int check_rope(const cv_qk_norm_rope_args *a) {
+    if (!a) return CV_ERR_NULL_ARGS;
+    if (a->dtype != CV_F32 && a->dtype != CV_BF16) return CV_ERR_DTYPE;
+    if (a->n_seq < 0 || a->n_seq > 65535 || a->n_heads < 0 || a->n_heads > kMaxHeads || a->n_kv_heads < 0 ||
+        a->n_kv_heads > kMaxHeads || (a->cu && a->total_tokens < 0))
+        return CV_ERR_SHAPE;
+    if (a->T < 0) return CV_ERR_TOKENS;
+    if (a->head_dim < 1 || a->head_dim > kMaxHeadDim || a->rot_dim < 0 || a->rot_dim > a->head_dim || a->rot_dim % 2 != 0)
+        return CV_ERR_HEAD_DIM;
+    const bool paged = a->cache.page_table != nullptr;
+    if (paged) {
+        const int rc = check_cache(a->cache, true, false);
+        if (rc != CV_OK) return rc;
+        if (a->cache.dtype != a->dtype) return CV_ERR_DTYPE;
+        if (a->cache.n_kv_heads != a->n_kv_heads || a->cache.head_dim != a->head_dim) return CV_ERR_HEAD_DIM;
+        if (!a->cache_len) return CV_ERR_NULL_POINTER;
+    }
+    const int64_t strides[] = {a->q_seq_stride, a->q_tok_stride, a->q_head_stride, a->q_out_seq_stride, a->q_out_tok_stride,
+                               a->q_out_head_stride, a->k_seq_stride, a->k_tok_stride, a->k_head_stride, a->k_out_seq_stride,
+                               a->k_out_tok_stride, a->k_out_head_stride, a->v_seq_stride, a->v_tok_stride, a->v_head_stride,
+                               a->cos_sin_stride};
+    for (int64_t s : strides)
+        if (s < 0) return CV_ERR_STRIDE;
+    if (a->rot_dim > 0 && (a->n_positions < 1 || (a->n_positions > 1 && a->cos_sin_stride < a->rot_dim))) return CV_ERR_STRIDE;
+    if (a->n_seq == 0 || a->T == 0 || (a->cu && a->total_tokens == 0)) return CV_OK;
+    if ((a->n_heads > 0 && (!a->q || !a->q_out)) || (a->n_kv_heads > 0 && (!a->k || (!a->k_out && !paged))) ||
+        (a->rot_dim > 0 && (!a->cos_sin || (!a->positions && !a->cache_len))) || (a->v && !paged))
+        return CV_ERR_NULL_POINTER;
+    // an output over its own input has to have its strides
+    auto over = [](const void *out, const void *in, int64_t so, int64_t si, int64_t to, int64_t ti, int64_t ho, int64_t hi) {
+        return out && out == in && (so != si || to != ti || ho != hi);
+    };
+    if (over(a->q_out, a->q, a->cu ? 0 : a->q_out_seq_stride, a->cu ? 0 : a->q_seq_stride, a->q_out_tok_stride, a->q_tok_stride,
+             a->q_out_head_stride, a->q_head_stride) ||
+        over(a->k_out, a->k, a->cu ? 0 : a->k_out_seq_stride, a->cu ? 0 : a->k_seq_stride, a->k_out_tok_stride, a->k_tok_stride,
+             a->k_out_head_stride, a->k_head_stride))
+        return CV_ERR_ALIAS;
+    const void *outs[] = {a->n_heads > 0 ? a->q_out : nullptr, a->k_out, paged ? a->cache.k : nullptr, paged ? a->cache.v : nullptr};
+    const void *ins[] = {a->q, a->k, a->v, a->q_weight, a->k_weight, a->cos_sin};
+    for (int i = 0; i < 4; ++i) {
+        if (!outs[i]) continue;
+        for (int j = 0; j < 6; ++j)
+            if (outs[i] == ins[j] && !(i == j && i < 2)) return CV_ERR_ALIAS;
+        for (int j = 0; j < i; ++j)
+            if (outs[i] == outs[j]) return CV_ERR_ALIAS;
+    }
+    return CV_OK;
+}
+
+int launch_rope(const cv_qk_norm_rope_args *a, cudaStream_t stream) {
+    const bool paged = a->cache.page_table != nullptr;
+    const int es = esize_of(a->dtype);
+    cvk::RopeParams p;
+    std::memset(&p, 0, sizeof p);
+    p.n_seq = a->n_seq, p.T = a->T, p.n_heads = a->n_heads, p.n_kv = a->n_kv_heads, p.d = a->head_dim, p.total = a->total_tokens;
+    p.rot = a->rot_dim, p.pairs = a->pairs != 0, p.norm = a->norm != 0, p.n_pos = a->n_positions, p.eps = a->eps;
+    p.tokens = a->cu ? (long long)a->total_tokens : (long long)a->n_seq * a->T;
+    p.q = a->q, p.k = a->k, p.v = a->n_kv_heads > 0 ? a->v : nullptr, p.wq = a->q_weight, p.wk = a->k_weight;
+    p.q_out = a->q_out, p.k_out = a->k_out;
+    p.q_seq = a->q_seq_stride, p.q_tok = a->q_tok_stride, p.q_head = a->q_head_stride;
+    p.qo_seq = a->q_out_seq_stride, p.qo_tok = a->q_out_tok_stride, p.qo_head = a->q_out_head_stride;
+    p.k_seq = a->k_seq_stride, p.k_tok = a->k_tok_stride, p.k_head = a->k_head_stride;
+    p.ko_seq = a->k_out_seq_stride, p.ko_tok = a->k_out_tok_stride, p.ko_head = a->k_out_head_stride;
+    p.v_seq = a->v_seq_stride, p.v_tok = a->v_tok_stride, p.v_head = a->v_head_stride;
+    p.cs = a->cos_sin, p.cs_row = a->cos_sin_stride;
+    p.pos = a->positions, p.cu = a->cu, p.len = a->cache_len, p.idx = a->cache_idx, p.err = a->err;
+    p.paged = paged;
+    if (paged) p.c = view(a->cache);
+    // pieces of 8 channels at 16-byte addresses, in pairs of pieces
+    auto rows = [&](const void *x, int64_t seq, int64_t tok, int64_t head) {
+        return !x || (aligned16(x) && seq * es % 16 == 0 && tok * es % 16 == 0 && head * es % 16 == 0);
+    };
+    const bool vec = a->head_dim % 16 == 0 && a->rot_dim % 16 == 0 && rows(p.q, p.q_seq, p.q_tok, p.q_head) &&
+                     rows(p.q_out, p.qo_seq, p.qo_tok, p.qo_head) && rows(p.k, p.k_seq, p.k_tok, p.k_head) &&
+                     rows(p.k_out, p.ko_seq, p.ko_tok, p.ko_head) && rows(p.v, p.v_seq, p.v_tok, p.v_head) &&
+                     aligned16(p.wq) && aligned16(p.wk) && aligned16(p.cs) && p.cs_row % 4 == 0 &&
+                     (!paged || (rows(p.c.k, p.c.k_page, p.c.k_row, p.c.k_head) && rows(p.c.v, p.c.v_page, p.c.v_row, p.c.v_head)));
+    p.lanes = 1;
+    while (p.lanes * 16 < a->head_dim) p.lanes *= 2;
+    // enough tokens a block for all its threads, fewer while that leaves SMs without one
+    p.block_tokens = cvk::kRopeTokens;
+    while (p.block_tokens > 1 && (p.tokens + p.block_tokens - 1) / p.block_tokens < 4LL * device_limits().sms) p.block_tokens /= 2;
+    const long long blocks = (p.tokens + p.block_tokens - 1) / p.block_tokens;
+    if (blocks > 0x7fffffff) return CV_ERR_SHAPE;
+    const int rc = clear_err(a->err, a->n_seq, stream);
+    if (rc != CV_OK) return rc;
+    if (launch_pdl(cvk::rope_kernel(a->dtype == CV_BF16, vec), dim3((unsigned)blocks), dim3(cvk::kRopeThreads), 0, stream, p) !=
+        cudaSuccess)
+        return CV_ERR_LAUNCH;
+    return cudaGetLastError() == cudaSuccess ? CV_OK : CV_ERR_LAUNCH;
+}
+
+// ---- pages
+
+// Bytes an access of a copy between rows can have.
+int copy_bytes(const cv_cache &c) {
+    return rows16(c.k, c.k_layer_stride, c.k_page_stride, c.k_row_stride, c.k_head_stride, c) &&
+                   rows16(c.v, c.v_layer_stride, c.v_page_stride, c.v_row_stride, c.v_head_stride, c)
+               ? 16
+               : esize_of(c.dtype);
+}
+
+int check_compact(const cv_cache_compact_args *a) {
+    if (!a) return CV_ERR_NULL_ARGS;
+    if (a->n_seq < 0 || a->n_seq > 65535) return CV_ERR_SHAPE;
+    if (a->T < 1 || a->T > CV_MAX_T) return CV_ERR_TOKENS;
+    const int rc = check_cache(a->cache, a->n_seq > 0, false);
+    if (rc != CV_OK || a->n_seq == 0) return rc;
+    if (!a->cache_len || !a->path || !a->accept_len) return CV_ERR_NULL_POINTER;
+    if (a->cache.k == a->cache.v) return CV_ERR_ALIAS;
+    const void *outs[] = {a->new_len, a->err};
+    const void *ins[] = {a->cache_len, a->path, a->accept_len, a->cache_idx, a->cache.page_table};
+    for (const void *o : outs)
+        for (const void *in : ins)
+            if (o && o == in) return CV_ERR_ALIAS;
+    return a->err && a->err == a->new_len ? CV_ERR_ALIAS : CV_OK;
+}
+
+int check_pages(const cv_cache_pages_args *a, bool fork, bool needs_tokens) {
+    if (!a) return CV_ERR_NULL_ARGS;
+    if (a->n_seq < 0 || a->n_seq > cvk::kMaxPageSeqs) return CV_ERR_SHAPE;
+    const int rc = check_cache(a->cache, a->n_seq > 0, true);
+    if (rc != CV_OK || a->n_seq == 0) return rc;
+    if ((needs_tokens && !a->n_tokens) || (fork && !a->src_idx)) return CV_ERR_NULL_POINTER;
+    if (fork && a->cache.k == a->cache.v) return CV_ERR_ALIAS;
+    const void *outs[] = {a->err, a->cache.page_table, a->cache.held, a->cache.refs};
+    const void *ins[] = {a->idx, a->src_idx, a->n_tokens};
+    for (int i = 0; i < 4; ++i) {
+        if (!outs[i]) continue;
+        for (const void *in : ins)
+            if (outs[i] == in) return CV_ERR_ALIAS;
+        for (int j = 0; j < i; ++j)
+            if (outs[i] == outs[j]) return CV_ERR_ALIAS;
+    }
+    return CV_OK;
+}
+
+cvk::PagesParams pages_params(const cv_cache_pages_args *a, int op) {
+    cvk::PagesParams p;
+    std::memset(&p, 0, sizeof p);
+    p.n_seq = a->n_seq, p.op = op, p.c = view(a->cache);
+    p.idx = a->idx, p.src = a->src_idx, p.n_tok = a->n_tokens, p.err = a->err;
+    return p;
+}
+
+int launch_take(const cvk::PagesParams &p, cudaStream_t stream) {
+    const int smem = cvk::pages_take_smem(p.n_seq);
+    const auto k = cvk::pages_take_kernel();
+    if (cvk::ensure_smem(reinterpret_cast<const void *>(k), smem + 1024) != cudaSuccess) return CV_ERR_LAUNCH;
+    return launch_pdl(k, dim3(1), dim3(cvk::kTakeThreads), smem, stream, p) == cudaSuccess ? CV_OK : CV_ERR_LAUNCH;
+}
+
+int done() { return cudaGetLastError() == cudaSuccess ? CV_OK : CV_ERR_LAUNCH; }
+
+}  // namespace
+
+extern "C" {
+
+int cv_tree_attention_workspace(const cv_tree_attention_args *args, int64_t *bytes) {
+    if (!bytes) return CV_ERR_NULL_POINTER;
+    const int rc = check_attention(args, false);
+    if (rc != CV_OK) return rc;
+    *bytes = args->n_seq == 0 ? 0 : plan_attention(args).bytes;
+    return CV_OK;
+}
+
+int cv_tree_attention(const cv_tree_attention_args *args, void *stream) {
+    const int rc = check_attention(args, true);
+    if (rc != CV_OK) return rc;
+    if (args->n_seq == 0 || (args->cu_draft && args->total_tokens == 0)) return CV_OK;
+    return launch_attention(args, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int cv_draft_verify(const cv_draft_verify_args *args, void *stream) {
+    const int rc = check_sample(args);
+    if (rc != CV_OK) return rc;
+    if (args->n_seq == 0) return CV_OK;
+    cvk::SampleParams p{args->n_seq, args->T, args->vocab, args->total_tokens, args->probs, args->draft_probs,
+                        args->probs_seq_stride, args->probs_tok_stride, args->draft_seq_stride, args->draft_tok_stride,
+                        args->tokens, args->parent, args->uniforms, args->cu_draft, args->cache_idx, args->accept_len,
+                        args->accept_node, args->path, args->out_tokens, args->err};
+    cudaStream_t on = reinterpret_cast<cudaStream_t>(stream);
+    const int clear = clear_err(args->err, args->n_seq, on);
+    if (clear != CV_OK) return clear;
+    if (launch_pdl(cvk::sample_kernel(args->dtype == CV_BF16), dim3((unsigned)args->n_seq * cvk::kSampleCluster),
+                   dim3(cvk::kSampleThreads), 0, on, p) != cudaSuccess)
+        return CV_ERR_LAUNCH;
+    return done();
+}
+
+int cv_qk_norm_rope(const cv_qk_norm_rope_args *args, void *stream) {
+    const int rc = check_rope(args);
+    if (rc != CV_OK) return rc;
+    if (args->n_seq == 0 || args->T == 0 || (args->cu && args->total_tokens == 0) || args->n_heads + args->n_kv_heads == 0)
+        return CV_OK;
+    return launch_rope(args, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int cv_cache_compact(const cv_cache_compact_args *args, void *stream) {
+    const int rc = check_compact(args);
+    if (rc != CV_OK) return rc;
+    if (args->n_seq == 0) return CV_OK;
+    cvk::PagesParams p;
+    std::memset(&p, 0, sizeof p);
+    p.n_seq = args->n_seq, p.T = args->T, p.c = view(args->cache);
+    p.idx = args->cache_idx, p.len = args->cache_len, p.path = args->path, p.accept = args->accept_len;
+    p.new_len = args->new_len, p.err = args->err;
+    const int bytes = copy_bytes(args->cache);
+    p.esize = esize_of(args->cache.dtype), p.chunks = args->cache.head_dim * p.esize / bytes;
+    // a piece a thread, fewer blocks where the sequences alone fill the GPU
+    const int64_t items = 2LL * p.c.n_layers * p.c.n_kv * p.chunks;
+    int64_t blocks = (items + cvk::kPagesThreads - 1) / cvk::kPagesThreads;
+    const int64_t most = 16LL * device_limits().sms * 8 / args->n_seq + 1;
+    if (blocks > most) blocks = most;
+    if (launch_pdl(cvk::pages_compact_kernel(bytes), dim3((unsigned)blocks, (unsigned)args->n_seq), dim3(cvk::kPagesThreads), 0,
+                   reinterpret_cast<cudaStream_t>(stream), p) != cudaSuccess)
+        return CV_ERR_LAUNCH;
+    return done();
+}
+
+int cv_cache_reserve(const cv_cache_pages_args *args, void *stream) {
+    const int rc = check_pages(args, false, true);
+    if (rc != CV_OK) return rc;
+    if (args->n_seq == 0) return CV_OK;
+    const int take = launch_take(pages_params(args, cvk::kPagesReserve), reinterpret_cast<cudaStream_t>(stream));
+    return take != CV_OK ? take : done();
+}
+
+int cv_cache_fork(const cv_cache_pages_args *args, void *stream) {
+    const int rc = check_pages(args, true, true);
+    if (rc != CV_OK) return rc;
+    if (args->n_seq == 0) return CV_OK;
+    cvk::PagesParams p = pages_params(args, cvk::kPagesFork);
+    const int bytes = copy_bytes(args->cache);
+    p.esize = esize_of(args->cache.dtype), p.chunks = args->cache.head_dim * p.esize / bytes;
+    const int take = launch_take(p, reinterpret_cast<cudaStream_t>(stream));
+    if (take != CV_OK) return take;
+    if (launch_pdl(cvk::pages_fork_kernel(bytes), dim3((unsigned)args->n_seq * cvk::kForkCluster), dim3(cvk::kPagesThreads), 0,
+                   reinterpret_cast<cudaStream_t>(stream), p) != cudaSuccess)
+        return CV_ERR_LAUNCH;
+    return done();
+}
+
+int cv_cache_free(const cv_cache_pages_args *args, void *stream) {
+    const int rc = check_pages(args, false, false);
+    if (rc != CV_OK) return rc;
+    if (args->n_seq == 0) return CV_OK;
+    const cvk::PagesParams p = pages_params(args, 0);
+    if (launch_pdl(cvk::pages_free_kernel(), dim3((unsigned)args->n_seq), dim3(cvk::kPagesThreads), 0,
+                   reinterpret_cast<cudaStream_t>(stream), p) != cudaSuccess)
+        return CV_ERR_LAUNCH;
+    return done();
+}
+
+}  // extern "C"

@@ -1,0 +1,353 @@
+// The pages of a cache: new pages for growing and forked sequences, shared pages, released pages, and the accepted
+// path of a tree of drafts moved to its place.
+//
+// A page is free while its reference count is 0, and the free pages with the lowest numbers are given out in the order of the
+// call's sequences; so the only state is the table, the counts and the slots' numbers of pages, and results do not depend
+// on the order in which threads come.  One block finds the free pages (16 counts a thread at a time, a scan over the
+// block), since their order is one of all pages: 70,000 counts are 280 KB, and it stops once it has enough.  Sharing
+// and copying take a cluster a sequence, releasing a block a sequence, compacting one for each part of the layers.
+#include "cv_attn.cuh"
+
+namespace cvk {
+namespace {
+
+// Pages that hold n tokens.
+__device__ __forceinline__ int pages_for(int n, int page) { return n <= 0 ? 0 : (n - 1) / page + 1; }
+
+// Sum over a block of 1024 threads, and the sum of the threads before this one.
+__device__ __forceinline__ long long block_scan(long long v, long long &before, long long *scratch) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    long long up = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long x = __shfl_up_sync(0xffffffffu, up, o);
+        if (lane >= o) up += x;
+    }
+    __syncthreads();
+    if (lane == 31) scratch[warp] = up;
+    __syncthreads();
+    const long long mine = scratch[lane];
+    long long sums = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long x = __shfl_up_sync(0xffffffffu, sums, o);
+        if (lane >= o) sums += x;
+    }
+    before = __shfl_sync(0xffffffffu, sums - mine, warp) + up - v;
+    return __shfl_sync(0xffffffffu, sums, 31);
+}
+
+constexpr int kScanEach = 16;
+
+__global__ void __launch_bounds__(kTakeThreads) pages_take(const __grid_constant__ PagesParams p) {
+    extern __shared__ __align__(8) long long smem[];
+    __shared__ long long scratch[32];
+    long long *const pre = smem;  // pages of the sequences before
+    int *const slots = reinterpret_cast<int *>(smem + p.n_seq), *const flagged = slots + p.n_seq;
+    grid_dep_wait();
+    grid_dep_launch();
+    const int tid = threadIdx.x;
+    const bool fork = p.op == kPagesFork;
+    const CacheView &c = p.c;
+    for (int i = tid; i < p.n_seq; i += kTakeThreads) {
+        int slot = p.idx ? __ldg(p.idx + i) : i;
+        if (fork && __ldg(p.src + i) < 0) slot = -1;
+        slots[i] = slot;
+    }
+    __syncthreads();
+    // Pages each sequence needs; -1 - bits where it is flagged.
+    auto needs = [&](int i) {
+        const int slot = slots[i];
+        if (slot < 0) return 0;
+        if (slot >= c.n_slots) return -1 - kSeqBadSlot;
+        int st = 0, need = 0;
+        if (p.idx)
+            for (int j = 0; j < i; ++j)
+                if (slots[j] == slot) st = kSeqBadSlot;
+        const int n = __ldg(p.n_tok + i), held = c.held[slot];
+        if (fork) {
+            const int src = __ldg(p.src + i);
+            for (int j = 0; j < p.n_seq; ++j)
+                if (slots[j] >= 0 && __ldg(p.src + j) == slot) st = kSeqBadSlot;
+            if (src >= c.n_slots || held != 0) st = kSeqBadSlot;
+            if (!st) {
+                const int have = c.held[src];
+                if (n < 0 || have < 0 || have > c.max_pages || n > (long long)have * c.page) st = kSeqBadLength;
+            }
+            need = n % c.page != 0;
+        } else {
+            if (!st && (n < 0 || n > (long long)c.max_pages * c.page || held < 0 || held > c.max_pages)) st = kSeqBadLength;
+            need = max(0, pages_for(n, c.page) - held);
+        }
+        return st ? -1 - st : need;
+    };
+    long long total = 0;
+    for (int base = 0; base < p.n_seq; base += kTakeThreads) {
+        const int i = base + tid;
+        const int need = i < p.n_seq ? needs(i) : 0;
+        long long before;
+        const long long sum = block_scan(max(need, 0), before, scratch);
+        if (i < p.n_seq) {
+            pre[i] = total + before;
+            flagged[i] = need < 0;
+            if (p.err) p.err[i] = need < 0 ? -1 - need : 0;
+        }
+        total += sum;
+    }
+    __syncthreads();
+    // The free pages in order, as far as the first `limit` of them; to the sequences, or counted only.
+    auto scan = [&](long long limit, bool give) {
+        long long found = 0;
+        for (long long base = 0; base < c.n_pages && found < limit; base += kTakeThreads * kScanEach) {
+            const long long at = base + (long long)tid * kScanEach;
+            uint32_t free = 0;
+#pragma unroll
+            for (int x = 0; x < kScanEach; ++x)
+                if (at + x < c.n_pages && c.refs[at + x] == 0) free |= 1u << x;
+            long long before;
+            const long long sum = block_scan(__popc(free), before, scratch);
+            if (give) {
+                long long rank = found + before;
+                for (; free && rank < limit; free &= free - 1, ++rank) {
+                    const int page = (int)at + __ffs(free) - 1;
+                    int lo = 0, hi = p.n_seq - 1;  // the last sequence whose pages begin at or before this one
+                    while (lo < hi) {
+                        const int mid = (lo + hi + 1) >> 1;
+                        if (pre[mid] <= rank) lo = mid;
+                        else hi = mid - 1;
+                    }
+                    const int slot = slots[lo], first = fork ? __ldg(p.n_tok + lo) / c.page : c.held[slot];
+                    c.table[(long long)slot * c.table_row + first + rank - pre[lo]] = page;
+                    c.refs[page] = 1;
+                }
+            }
+            found += sum;
+        }
+        return found;
+    };
+    // Which are served: those whose pages end within what there is (a sequence's need is the difference of two sums).
+    const long long found = total > 0 ? min(scan(total, false), total) : 0;
+    auto ends = [&](int i) { return i + 1 < p.n_seq ? pre[i + 1] : total; };
+    long long limit = 0;
+    for (int i = tid; i < p.n_seq; i += kTakeThreads)
+        if (ends(i) <= found) limit = max(limit, ends(i));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) limit = max(limit, __shfl_xor_sync(0xffffffffu, limit, o));
+    __syncthreads();
+    if ((tid & 31) == 0) scratch[tid >> 5] = limit;
+    __syncthreads();
+    for (int w = 0; w < 32; ++w) limit = max(limit, scratch[w]);
+    if (limit > 0) scan(limit, true);
+    __syncthreads();
+    for (int i = tid; i < p.n_seq; i += kTakeThreads) {
+        const int slot = slots[i];
+        if (slot < 0 || flagged[i]) continue;
+        const long long need = ends(i) - pre[i];
+        if (need > 0 && ends(i) > found) {
+            if (p.err) p.err[i] = kSeqNoPages;
+        } else if (fork) {
+            c.held[slot] = -1 - i;  // until the next kernel has shared and copied: this sequence, and no other, is on
+        } else if (need > 0) {
+            c.held[slot] += (int)need;
+        }
+    }
+}
+
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+}
+
+// An access of BYTES bytes.
+template <int BYTES> struct Piece;
+template <> struct Piece<16> { using T = uint4; };
+template <> struct Piece<4> { using T = uint32_t; };
+template <> struct Piece<2> { using T = uint16_t; };
+
+// The head rows of a copy: item = ((layer * 2 + which) * heads + head) * pieces + piece.  Gives the address of the
+// layer's head in K or V, and that one's strides of pages and rows, in elements of the access.
+template <int BYTES>
+struct CopyItem {
+    typename Piece<BYTES>::T *base;
+    long long page, row;
+    __device__ __forceinline__ CopyItem(const PagesParams &p, long long item) {
+        const CacheView &c = p.c;
+        const int piece = (int)(item % p.chunks);
+        item /= p.chunks;
+        const int h = (int)(item % c.n_kv);
+        item /= c.n_kv;
+        const bool v = item & 1;
+        const long long layer = item >> 1;
+        const int per = BYTES / p.esize;
+        page = (v ? c.v_page : c.k_page) / per, row = (v ? c.v_row : c.k_row) / per;
+        base = reinterpret_cast<typename Piece<BYTES>::T *>(v ? c.v : c.k) +
+               (layer * (v ? c.v_layer : c.k_layer) + (long long)h * (v ? c.v_head : c.k_head)) / per + piece;
+    }
+};
+__device__ __forceinline__ long long copy_items(const PagesParams &p) { return 2LL * p.c.n_layers * p.c.n_kv * p.chunks; }
+
+
+
+// A cluster a sequence: checks its source's pages, copies the rest of the last one, then its first block shares the full
+// ones and closes the slot's entry.
+template <int BYTES>
+__global__ void __cluster_dims__(kForkCluster, 1, 1) __launch_bounds__(kPagesThreads)
+    pages_fork(const __grid_constant__ PagesParams p) {
+    grid_dep_wait();
+    grid_dep_launch();
+    const CacheView &c = p.c;
+    const int tid = threadIdx.x, i = blockIdx.x / kForkCluster, rank = blockIdx.x % kForkCluster;
+    const int slot = p.idx ? __ldg(p.idx + i) : i, src = __ldg(p.src + i);
+    const bool on = slot >= 0 && slot < c.n_slots && src >= 0 && c.held[slot] == -1 - i;
+    int n = 0, full = 0, rest = 0, bad = 0;
+    int *const to = c.table + (long long)(on ? slot : 0) * c.table_row;
+    const int *const from = c.table + (long long)(on ? src : 0) * c.table_row;
+    if (on) {
+        n = __ldg(p.n_tok + i), full = n / c.page, rest = n % c.page;
+        for (int x = tid; x < pages_for(n, c.page); x += kPagesThreads) {
+            const int g = from[x];
+            bad |= g < 0 || g >= c.n_pages;
+        }
+    }
+    bad = __syncthreads_or(bad);
+    const int new_page = on && rest ? to[full] : 0;
+    cluster_sync();  // every block has read the entries that the first one changes
+    if (!on) return;
+    if (bad) {
+        if (rank == 0 && tid == 0) {
+            if (rest) c.refs[new_page] = 0, to[full] = -1;
+            c.held[slot] = 0;
+            if (p.err) p.err[i] = kSeqBadPage;
+        }
+        return;
+    }
+    if (rank == 0) {
+        for (int x = tid; x < full; x += kPagesThreads) {
+            const int g = from[x];
+            to[x] = g;
+            atomicAdd(c.refs + g, 1);
+        }
+        if (tid == 0) c.held[slot] = full + (rest > 0);
+    }
+    if (!rest) return;
+    const int old_page = from[full];
+    const long long items = copy_items(p) * rest;
+    for (long long x = (long long)rank * kPagesThreads + tid; x < items; x += kForkCluster * kPagesThreads) {
+        // the rows of a page innermost but for a row's own pieces
+        const long long row = x / p.chunks % rest, piece = x % p.chunks, head = x / p.chunks / rest;
+        const CopyItem<BYTES> m(p, head * p.chunks + piece);
+        m.base[new_page * m.page + row * m.row] = m.base[old_page * m.page + row * m.row];
+    }
+}
+
+// A block a sequence.
+__global__ void __launch_bounds__(kPagesThreads) pages_free(const __grid_constant__ PagesParams p) {
+    grid_dep_wait();
+    grid_dep_launch();
+    const CacheView &c = p.c;
+    const int tid = threadIdx.x, i = blockIdx.x;
+    const int slot = p.idx ? __ldg(p.idx + i) : i;
+    if (slot < 0) {
+        if (tid == 0 && p.err) p.err[i] = 0;
+        return;
+    }
+    int st = slot >= c.n_slots ? kSeqBadSlot : 0;
+    if (p.idx)
+        for (int j = tid; j < i; j += kPagesThreads)
+            if (__ldg(p.idx + j) == slot) st |= kSeqBadSlot;
+    st = __syncthreads_or(st) ? kSeqBadSlot : 0;
+    int held = 0, keep = 0;
+    int *const row = c.table + (long long)(st ? 0 : slot) * c.table_row;
+    if (!st) {
+        const int n = p.n_tok ? __ldg(p.n_tok + i) : 0;
+        held = c.held[slot], keep = pages_for(n, c.page);
+        if (n < 0 || held < 0 || held > c.max_pages) st = kSeqBadLength;
+        int bad = 0;
+        if (!st)
+            for (int x = keep + tid; x < held; x += kPagesThreads) {
+                const int g = row[x];
+                bad |= g < 0 || g >= c.n_pages;
+            }
+        if (__syncthreads_or(bad)) st = kSeqBadPage;
+    }
+    if (tid == 0 && p.err) p.err[i] = st;
+    if (st || keep >= held) return;
+    for (int x = keep + tid; x < held; x += kPagesThreads) {
+        const int g = row[x];
+        if (atomicSub(c.refs + g, 1) <= 0) atomicAdd(c.refs + g, 1);  // (was free: stays so)
+        row[x] = -1;
+    }
+    if (tid == 0) c.held[slot] = keep;
+}
+
+constexpr int kMaxPath = 128, kMoveRows = 8;
+
+// Blocks (x) of a sequence (y) share its layers' heads.  A thread moves one piece of each row of the path in order, 8 rows
+// read before they are written: the path rises, so a row is written only after every row at or past it was read.
+template <int BYTES>
+__global__ void __launch_bounds__(kPagesThreads) pages_compact(const __grid_constant__ PagesParams p) {
+    __shared__ int src_page[kMaxPath], src_row[kMaxPath], dst_page[kMaxPath], dst_row[kMaxPath];
+    __shared__ int first;
+    grid_dep_wait();
+    grid_dep_launch();
+    const CacheView &c = p.c;
+    const int tid = threadIdx.x, s = blockIdx.y;
+    const int slot = p.idx ? __ldg(p.idx + s) : s;
+    const bool head = blockIdx.x == 0 && tid == 0;
+    if (slot < 0) {
+        if (head && p.err) p.err[s] = 0;
+        return;
+    }
+    int st = slot >= c.n_slots ? kSeqBadSlot : 0;
+    const int a = __ldg(p.accept + s), L = __ldg(p.len + s);
+    if (a < 0 || a > p.T) st |= kSeqBadAccept;
+    if (L < 0) st |= kSeqBadLength;
+    if (tid == 0) first = p.T;
+    __syncthreads();
+    if (!st && tid < a) {
+        const int at = __ldg(p.path + (long long)s * p.T + tid);
+        const int before = tid > 0 ? __ldg(p.path + (long long)s * p.T + tid - 1) : -1;
+        if (at <= before || at < tid || at >= p.T) st |= kSeqBadTree;
+        else if ((long long)L + at >= (long long)c.max_pages * c.page) st |= kSeqBadLength;
+        else if (at != tid) {
+            const int from = L + at, to = L + tid;
+            const int *const row = c.table + (long long)slot * c.table_row;
+            const int g = __ldg(row + from / c.page), h = __ldg(row + to / c.page);
+            if (g < 0 || g >= c.n_pages || h < 0 || h >= c.n_pages) st |= kSeqBadPage;
+            src_page[tid] = g, src_row[tid] = from % c.page;
+            dst_page[tid] = h, dst_row[tid] = to % c.page;
+            atomicMin(&first, tid);
+        }
+    }
+    const int all = (__syncthreads_or(st & kSeqBadSlot) ? kSeqBadSlot : 0) | (__syncthreads_or(st & kSeqBadAccept) ? kSeqBadAccept : 0) |
+                    (__syncthreads_or(st & kSeqBadTree) ? kSeqBadTree : 0) | (__syncthreads_or(st & kSeqBadLength) ? kSeqBadLength : 0) |
+                    (__syncthreads_or(st & kSeqBadPage) ? kSeqBadPage : 0);
+    if (head && p.err) p.err[s] = all;
+    if (all) return;
+    if (head && p.new_len) p.new_len[s] = L + a;
+    const int from = first;  // a rising path that has left its place stays ahead of it
+    const long long items = copy_items(p);
+    for (long long x = (long long)blockIdx.x * kPagesThreads + tid; x < items; x += (long long)gridDim.x * kPagesThreads) {
+        const CopyItem<BYTES> m(p, x);
+        for (int r0 = from; r0 < a; r0 += kMoveRows) {
+            typename Piece<BYTES>::T w[kMoveRows];
+#pragma unroll
+            for (int r = 0; r < kMoveRows; ++r)
+                if (r0 + r < a) w[r] = m.base[src_page[r0 + r] * m.page + src_row[r0 + r] * m.row];
+#pragma unroll
+            for (int r = 0; r < kMoveRows; ++r)
+                if (r0 + r < a) m.base[dst_page[r0 + r] * m.page + dst_row[r0 + r] * m.row] = w[r];
+        }
+    }
+}
+
+}  // namespace
+
+PagesKernel pages_take_kernel() { return pages_take; }
+int pages_take_smem(int n_seq) { return n_seq * 16; }
+PagesKernel pages_fork_kernel(int bytes) { return bytes == 16 ? pages_fork<16> : bytes == 4 ? pages_fork<4> : pages_fork<2>; }
+PagesKernel pages_free_kernel() { return pages_free; }
+PagesKernel pages_compact_kernel(int bytes) {
+    return bytes == 16 ? pages_compact<16> : bytes == 4 ? pages_compact<4> : pages_compact<2>;
+}
+
+}  // namespace cvk
