@@ -15,6 +15,8 @@ using cvk::launch_pdl;
 
 constexpr int kMaxHeads = 4096, kMaxLayers = 4096, kMaxPage = 65536, kMaxHeadDim = 256, kMaxVocab = 1 << 24;
 constexpr int64_t kMaxTokens = 0x7fffffff;
+constexpr int64_t kMaxStride = 1LL << 38;  // elements: a tensor map's strides are below 2^40 bytes
+constexpr unsigned kPolls = 65536;         // of up to 20 us each
 
 int esize_of(int dtype) { return dtype == CV_BF16 ? 2 : 4; }
 
@@ -76,31 +78,72 @@ int check_attention(const cv_tree_attention_args *a, bool pointers) {
 
 struct AttnPlan {
     cvk::AttnSimt simt;
-    int dp, rows, keys, parts;
+    cvk::AttnTc tc;
+    bool on_tc;
+    int dp, rows, keys, parts, page_rows, tok;
     bool cut;
     int64_t bytes;
 };
 
-AttnPlan plan_attention(const cv_tree_attention_args *a) {
+// What the tensor-core kernel's copies need: 16-byte rows, pages of whole groups of 8 rows that fit into tiles or are made of
+// them, a positive scale (its masks are minus infinity before the scale).
+bool tc_takes(const cv_tree_attention_args *a, int keys) {
     const cv_cache &c = a->cache;
-    const int es = esize_of(c.dtype), G = a->n_heads / c.n_kv_heads;
+    const int G = a->n_heads / c.n_kv_heads;
+    auto dim = [](int64_t stride, int64_t n) { return n == 1 || (stride > 0 && stride % 8 == 0 && stride < kMaxStride); };
+    return c.dtype == CV_BF16 && c.head_dim % 8 == 0 && G <= 128 && a->scale > 0.f && a->scale < 1e30f && c.page_size % 8 == 0 &&
+           (c.page_size % keys == 0 || keys % c.page_size == 0) && aligned16(c.k) && aligned16(c.v) && aligned16(a->q) &&
+           dim(c.k_page_stride, c.n_pages) && dim(c.k_row_stride, c.page_size) && dim(c.k_head_stride, c.n_kv_heads) &&
+           dim(c.v_page_stride, c.n_pages) && dim(c.v_row_stride, c.page_size) && dim(c.v_head_stride, c.n_kv_heads) &&
+           dim(a->q_head_stride, a->n_heads) && dim(a->q_tok_stride, a->cu_draft ? a->total_tokens : a->T) &&
+           (a->cu_draft || dim(a->q_seq_stride, a->n_seq));
+}
+
+AttnPlan plan_attention(const cv_tree_attention_args *a, bool tc = true) {
+    const cv_cache &c = a->cache;
+    const int es = esize_of(c.dtype), G = a->n_heads / c.n_kv_heads, d = c.head_dim;
     AttnPlan pl;
-    const bool vec = rows16(c.k, 0, c.k_page_stride, c.k_row_stride, c.k_head_stride, c) &&
-                     rows16(c.v, 0, c.v_page_stride, c.v_row_stride, c.v_head_stride, c) && aligned16(a->q) &&
-                     a->q_seq_stride * es % 16 == 0 && a->q_tok_stride * es % 16 == 0 && a->q_head_stride * es % 16 == 0;
-    pl.dp = c.head_dim <= 64 ? 64 : c.head_dim <= 128 ? 128 : 256;
-    pl.simt = cvk::attn_simt_kernel(c.dtype == CV_BF16, pl.dp, vec);
-    pl.rows = cvk::kSimtRows, pl.keys = pl.simt.keys;
-    const cvk::DeviceLimits d = device_limits();
-    const int resident = d.smem_per_sm / (pl.simt.smem_bytes + 1024);
-    pl.parts = d.sms * (resident < 1 ? 1 : resident > 2 ? 2 : resident);
+    const cvk::DeviceLimits lim = device_limits();
+    pl.dp = d <= 64 ? 64 : d <= 128 ? 128 : d <= 192 ? 192 : 256;
+    pl.tc = cvk::attn_tc_kernel(pl.dp);
+    pl.on_tc = tc && tc_takes(a, pl.tc.keys);
+    if (pl.on_tc) {
+        pl.keys = pl.tc.keys;
+        pl.tok = a->T < 128 / G ? a->T : 128 / G;
+        pl.rows = pl.tok * G;
+        pl.page_rows = c.page_size < pl.keys ? c.page_size : pl.keys;
+        pl.parts = lim.sms;
+    } else {
+        const bool vec = rows16(c.k, 0, c.k_page_stride, c.k_row_stride, c.k_head_stride, c) &&
+                         rows16(c.v, 0, c.v_page_stride, c.v_row_stride, c.v_head_stride, c) && aligned16(a->q) &&
+                         a->q_seq_stride * es % 16 == 0 && a->q_tok_stride * es % 16 == 0 && a->q_head_stride * es % 16 == 0;
+        if (pl.dp == 192) pl.dp = 256;
+        pl.simt = cvk::attn_simt_kernel(c.dtype == CV_BF16, pl.dp, vec);
+        pl.rows = cvk::kSimtRows, pl.keys = pl.simt.keys;
+        const int resident = lim.smem_per_sm / (pl.simt.smem_bytes + 1024);
+        pl.parts = lim.sms * (resident < 1 ? 1 : resident > 2 ? 2 : resident);
+    }
     // tiles there can be at most: fewer blocks are enough for fewer
     const int64_t tiles = ((int64_t)c.max_pages * c.page_size + pl.keys - 1) / pl.keys;
     const int64_t units = (int64_t)a->n_seq * c.n_kv_heads * (((int64_t)a->T * G + pl.rows - 1) / pl.rows);
     if (units * tiles < pl.parts) pl.parts = (int)(units * tiles);
     pl.cut = tiles > 1;
-    pl.bytes = pl.cut ? 2LL * pl.parts * cvk::part_floats(pl.rows, pl.dp) * 4 : 0;
+    pl.bytes = pl.cut ? 2LL * pl.parts * cvk::part_floats((pl.rows + 3) / 4 * 4, pl.dp) * 4 : 0;
     return pl;
+}
+
+// A map of rows of d channels in boxes of 64 channels by `b1` x `b2` rows of the next two dimensions.
+bool encode4(CUtensorMap *map, const void *p, int d, int64_t n1, int64_t s1, int64_t n2, int64_t s2, int64_t n3, int64_t s3, int b1,
+             int b2) {
+    const auto encode = cvk::encode_tiled();
+    if (!encode) return false;
+    const cuuint64_t any = (cuuint64_t)(d + 7) / 8 * 16;
+    const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)n1, (cuuint64_t)n2, (cuuint64_t)n3};
+    const cuuint64_t strides[3] = {n1 > 1 ? (cuuint64_t)s1 * 2 : any, n2 > 1 ? (cuuint64_t)s2 * 2 : any, n3 > 1 ? (cuuint64_t)s3 * 2 : any};
+    const cuuint32_t box[4] = {64, (cuuint32_t)b1, (cuuint32_t)b2, 1}, step[4] = {1, 1, 1, 1};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(p), dims, strides, box, step,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 int launch_attention(const cv_tree_attention_args *a, cudaStream_t stream) {
@@ -108,21 +151,40 @@ int launch_attention(const cv_tree_attention_args *a, cudaStream_t stream) {
     const AttnPlan pl = plan_attention(a);
     if (pl.bytes > 0 && (!a->workspace || reinterpret_cast<uintptr_t>(a->workspace) % 256 != 0 || a->workspace_bytes < pl.bytes))
         return CV_ERR_WORKSPACE;
-    cvk::AttnParams p;
-    std::memset(&p, 0, sizeof p);
+    cvk::AttnMaps mp;
+    std::memset(&mp, 0, sizeof mp);
+    cvk::AttnParams &p = mp.a;
     p.n_seq = a->n_seq, p.T = a->T, p.total = a->total_tokens, p.n_heads = a->n_heads, p.G = a->n_heads / c.n_kv_heads;
     p.scale = a->scale * 1.4426950408889634f;
+    p.polls = a->wait_polls == 0 ? kPolls : a->wait_polls < 0 ? 0u : (unsigned)a->wait_polls;
     p.c = view(c);
     p.q = a->q, p.q_seq = a->q_seq_stride, p.q_tok = a->q_tok_stride, p.q_head = a->q_head_stride;
     p.out = a->out, p.o_seq = a->out_seq_stride, p.o_tok = a->out_tok_stride, p.o_head = a->out_head_stride;
     p.cu = a->cu_draft, p.parent = a->parent, p.len = a->cache_len, p.idx = a->cache_idx, p.err = a->err;
-    p.rows = pl.rows, p.keys = pl.keys, p.dp = pl.dp, p.parts = pl.parts;
+    p.rows = pl.rows, p.pad = (pl.rows + 3) / 4 * 4, p.keys = pl.keys, p.dp = pl.dp, p.parts = pl.parts;
     p.ws = pl.cut ? reinterpret_cast<float *>(a->workspace) : nullptr;
+    if (pl.on_tc) {
+        const int64_t tokens = a->cu_draft ? a->total_tokens : a->T, seqs = a->cu_draft ? 1 : a->n_seq;
+        if (!encode4(&mp.q, a->q, c.head_dim, a->n_heads, a->q_head_stride, tokens, a->q_tok_stride, seqs, a->q_seq_stride, p.G, pl.tok) ||
+            !encode4(&mp.k, c.k, c.head_dim, c.page_size, c.k_row_stride, c.n_kv_heads, c.k_head_stride, c.n_pages, c.k_page_stride,
+                     pl.page_rows, 1) ||
+            !encode4(&mp.v, c.v, c.head_dim, c.page_size, c.v_row_stride, c.n_kv_heads, c.v_head_stride, c.n_pages, c.v_page_stride,
+                     pl.page_rows, 1))
+            return CV_ERR_LAUNCH;
+        mp.page_rows = pl.page_rows, mp.tok = pl.tok;
+        mp.o_vec = aligned16(a->out) && a->out_seq_stride % 8 == 0 && a->out_tok_stride % 8 == 0 && a->out_head_stride % 8 == 0;
+    }
     const int rc = clear_err(a->err, a->n_seq, stream);
     if (rc != CV_OK) return rc;
-    if (cvk::ensure_smem(reinterpret_cast<const void *>(pl.simt.fn), pl.simt.smem_bytes) != cudaSuccess) return CV_ERR_LAUNCH;
-    if (launch_pdl(pl.simt.fn, dim3((unsigned)pl.parts), dim3(cvk::kSimtThreads), pl.simt.smem_bytes, stream, p) != cudaSuccess)
-        return CV_ERR_LAUNCH;
+    if (pl.on_tc) {
+        if (cvk::ensure_smem(reinterpret_cast<const void *>(pl.tc.fn), pl.tc.smem_bytes) != cudaSuccess) return CV_ERR_LAUNCH;
+        if (launch_pdl(pl.tc.fn, dim3((unsigned)pl.parts), dim3((unsigned)pl.tc.threads), pl.tc.smem_bytes, stream, mp) != cudaSuccess)
+            return CV_ERR_LAUNCH;
+    } else {
+        if (cvk::ensure_smem(reinterpret_cast<const void *>(pl.simt.fn), pl.simt.smem_bytes) != cudaSuccess) return CV_ERR_LAUNCH;
+        if (launch_pdl(pl.simt.fn, dim3((unsigned)pl.parts), dim3(cvk::kSimtThreads), pl.simt.smem_bytes, stream, p) != cudaSuccess)
+            return CV_ERR_LAUNCH;
+    }
     if (pl.cut) {
         const dim3 grid((unsigned)pl.parts, (unsigned)((pl.rows + cvk::kAttnJoinRows - 1) / cvk::kAttnJoinRows));
         if (launch_pdl(cvk::attn_join_kernel(c.dtype == CV_BF16), grid, dim3(cvk::kAttnJoinThreads), 0, stream, p) != cudaSuccess)
@@ -321,7 +383,14 @@ int cv_tree_attention_workspace(const cv_tree_attention_args *args, int64_t *byt
     if (!bytes) return CV_ERR_NULL_POINTER;
     const int rc = check_attention(args, false);
     if (rc != CV_OK) return rc;
-    *bytes = args->n_seq == 0 ? 0 : plan_attention(args).bytes;
+    *bytes = 0;
+    if (args->n_seq == 0) return CV_OK;
+    // NULL pointers count as aligned; the call's own may be aligned to less and take the other kernel
+    *bytes = plan_attention(args).bytes;
+    if (!args->q || !args->cache.k || !args->cache.v) {
+        const int64_t other = plan_attention(args, false).bytes;
+        *bytes = *bytes > other ? *bytes : other;
+    }
     return CV_OK;
 }
 

@@ -213,28 +213,9 @@ struct ChunkPlan {
 constexpr int kShortFew = 8, kShortMany = 16;
 constexpr int64_t kMaxStride = 1LL << 38;  // elements: a tensor map's strides are below 2^40 bytes
 
-// The driver's encoder of tensor maps, looked up once.
-using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
-                                 const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-EncodeTiled encode_tiled() {
-    static std::atomic<EncodeTiled> found{nullptr};
-    EncodeTiled f = found.load(std::memory_order_relaxed);
-    if (f) return f;
-    void *fn = nullptr;
-    cudaDriverEntryPointQueryResult st;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &st) != cudaSuccess ||
-        st != cudaDriverEntryPointSuccess) {
-        cudaGetLastError();
-        return nullptr;
-    }
-    f = reinterpret_cast<EncodeTiled>(fn);
-    found.store(f, std::memory_order_relaxed);
-    return f;
-}
 // A map of [tokens][heads][d] bf16 rows read in boxes of 128 tokens of one head's 64 channels.
 bool encode_rows(CUtensorMap *map, const void *p, int d, int heads, int64_t tokens, int64_t head, int64_t tok) {
-    const EncodeTiled encode = encode_tiled();
+    const auto encode = cvk::encode_tiled();
     if (!encode) return false;
     const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)tokens};
     const cuuint64_t strides[2] = {(cuuint64_t)(heads > 1 ? head : d) * 2, (cuuint64_t)tok * 2};

@@ -129,7 +129,7 @@ struct AttnWalk {
 // Where a block leaves what it has of a unit that others have parts of too: slot 0 for one that began before it, 1 for
 // one that begins in it and goes on.
 __device__ __forceinline__ float *attn_part(const AttnParams &p, int block, int slot) {
-    return p.ws + (2LL * block + slot) * part_floats(p.rows, p.dp);
+    return p.ws + (2LL * block + slot) * part_floats(p.pad, p.dp);
 }
 
 // Ancestors-or-selves of the drafts as 128-bit masks, by pointer jumping: after i rounds a mask covers 2^i steps up.
@@ -162,6 +162,7 @@ __device__ __forceinline__ bool attn_ancestors(const int *parent, int T, int dra
         for (int reach = 1; reach < T; reach *= 2) {
             if (draft < 128) {
                 if (up >= 0) {
+                    up &= 127;  // (in bounds even where the other threads' part never came)
                     const uint4 o = tree->mask[from][up];
                     m.x |= o.x, m.y |= o.y, m.z |= o.z, m.w |= o.w;
                     up = tree->up[from][up];

@@ -33,6 +33,7 @@ struct AttnParams {
     // A unit of work is up to `rows` rows (draft, query head of the group) of one kv head of one sequence over all its keys,
     // in tiles of `keys` of them.  All units' tiles, in a row, are cut into `parts` equal runs, one a block.
     int rows, keys, dp, parts;
+    int pad;    // rows of a partial result: rows, a multiple of 4
     float *ws;  // two partial results a block, or NULL where no unit can be cut
 };
 struct AttnMaps {
@@ -43,8 +44,8 @@ struct AttnMaps {
     int o_vec;       // out allows 16-byte accesses
 };
 constexpr int kSimtRows = 32, kSimtThreads = 256;
-constexpr int kPartHead = 16;  // ints before a partial's maxima, sums and outputs
-__host__ __device__ constexpr long long part_floats(int rows, int dp) { return kPartHead + 2 * rows + (long long)rows * dp; }
+constexpr int kPartHead = 16;  // ints before a partial's maxima, sums and outputs, each of them 16-byte aligned
+__host__ __device__ constexpr long long part_floats(int pad, int dp) { return kPartHead + 2 * pad + (long long)pad * dp; }
 
 using AttnKernel = void (*)(AttnParams);
 using AttnTcKernel = void (*)(AttnMaps);

@@ -210,10 +210,10 @@ __global__ void __launch_bounds__(kSimtThreads) attn_simt(const __grid_constant_
             }
         } else {
             float *const part = attn_part(p, blockIdx.x, begins);
-            if (begins && tid < 5) {
-                const long long to = u.first + u.tiles - 1;
-                const int head[5] = {1, (int)(to / sh->range.per) - (int)blockIdx.x + 1, u.s, u.h, u.row};
-                reinterpret_cast<int *>(part)[tid] = head[tid];
+            if (tid == 0) {
+                int *const head = reinterpret_cast<int *>(part);
+                head[0] = begins, head[1] = (int)((u.first + u.tiles - 1) / sh->range.per) - (int)blockIdx.x + 1;
+                head[2] = u.s, head[3] = u.h, head[4] = u.row, head[5] = 1;
             }
             if (tid < kSimtRows) part[kPartHead + tid] = sh->m[tid], part[kPartHead + kSimtRows + tid] = sh->l[tid];
             float4 *const to = reinterpret_cast<float4 *>(part + kPartHead + 2 * kSimtRows);
@@ -241,9 +241,12 @@ __global__ void __launch_bounds__(kAttnJoinThreads) attn_join(const __grid_const
     const int n = head[1], s = head[2], h = head[3], row0 = head[4];
     const AttnSeq q = attn_seq(p, s);
     const int rows = min(p.rows, q.T * p.G - row0);
-    const long long step = 2 * part_floats(p.rows, p.dp);
+    const long long step = 2 * part_floats(p.pad, p.dp);
     // part i > 0 is slot 0 of the block i further on
     auto part = [&](int i) { return i == 0 ? first : first + i * step - step / 2; };
+    bool whole = true;  // (a block that gave up leaves no part)
+    for (int i = lane; i < n; i += 32) whole = whole && reinterpret_cast<const int *>(part(i))[5] != 0;
+    if (!__all_sync(0xffffffffu, whole)) return;
     for (int r = blockIdx.y * kAttnJoinRows + warp; r < min(rows, (int)(blockIdx.y + 1) * kAttnJoinRows); r += kAttnJoinThreads / 32) {
         float top = kNone;
         for (int i = lane; i < n; i += 32) top = fmaxf(top, part(i)[kPartHead + r]);
@@ -254,12 +257,12 @@ __global__ void __launch_bounds__(kAttnJoinThreads) attn_join(const __grid_const
 #pragma unroll 4
         for (int i = 0; i < n; ++i) {
             const float *const x = part(i);
-            const float m = x[kPartHead + r], sum = x[kPartHead + p.rows + r];
+            const float m = x[kPartHead + r], sum = x[kPartHead + p.pad + r];
             // (a part in which the row sees nothing, or minus infinity alone; its sum may be a NaN, which stays)
             if (m == kNone && sum == 0.f) continue;
             const float w = m == kNone ? 1.f : ex2(m - top);
             l = fmaf(w, sum, l);
-            const float4 *const a = reinterpret_cast<const float4 *>(x + kPartHead + 2 * p.rows + (long long)r * p.dp);
+            const float4 *const a = reinterpret_cast<const float4 *>(x + kPartHead + 2 * p.pad + (long long)r * p.dp);
 #pragma unroll
             for (int e = 0; e < 2; ++e)
                 if (4 * (lane + 32 * e) < p.dp) {

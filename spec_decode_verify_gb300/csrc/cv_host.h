@@ -1,6 +1,7 @@
 // Host-side helpers shared by the C ABI units: the device's limits, alignment checks and the launch.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <atomic>
@@ -86,6 +87,26 @@ inline cudaError_t ensure_smem(const void *kernel, int bytes) {
         if (slot.compare_exchange_strong(z, key)) break;
     }
     return cudaSuccess;
+}
+
+// The driver's encoder of tensor maps, looked up once.
+using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
+                                 const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+inline EncodeTiled encode_tiled() {
+    static std::atomic<EncodeTiled> found{nullptr};
+    EncodeTiled f = found.load(std::memory_order_relaxed);
+    if (f) return f;
+    void *fn = nullptr;
+    cudaDriverEntryPointQueryResult st;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &st) != cudaSuccess ||
+        st != cudaDriverEntryPointSuccess) {
+        cudaGetLastError();
+        return nullptr;
+    }
+    f = reinterpret_cast<EncodeTiled>(fn);
+    found.store(f, std::memory_order_relaxed);
+    return f;
 }
 
 }  // namespace cvk
