@@ -76,11 +76,14 @@ int check_attention(const cv_tree_attention_args *a, bool pointers) {
     return CV_OK;
 }
 
+// What a unit takes beside its tiles, in tiles.
+constexpr int kTcUnitCost = 3, kSimtUnitCost = 1;
+
 struct AttnPlan {
     cvk::AttnSimt simt;
     cvk::AttnTc tc;
     bool on_tc;
-    int dp, rows, keys, parts, page_rows, tok;
+    int dp, rows, keys, parts, unit_cost, page_rows, tok;
     bool cut;
     int64_t bytes;
 };
@@ -112,7 +115,7 @@ AttnPlan plan_attention(const cv_tree_attention_args *a, bool tc = true) {
         pl.tok = a->T < 128 / G ? a->T : 128 / G;
         pl.rows = pl.tok * G;
         pl.page_rows = c.page_size < pl.keys ? c.page_size : pl.keys;
-        pl.parts = lim.sms;
+        pl.parts = lim.sms, pl.unit_cost = kTcUnitCost;
     } else {
         const bool vec = rows16(c.k, 0, c.k_page_stride, c.k_row_stride, c.k_head_stride, c) &&
                          rows16(c.v, 0, c.v_page_stride, c.v_row_stride, c.v_head_stride, c) && aligned16(a->q) &&
@@ -122,6 +125,7 @@ AttnPlan plan_attention(const cv_tree_attention_args *a, bool tc = true) {
         pl.rows = cvk::kSimtRows, pl.keys = pl.simt.keys;
         const int resident = lim.smem_per_sm / (pl.simt.smem_bytes + 1024);
         pl.parts = lim.sms * (resident < 1 ? 1 : resident > 2 ? 2 : resident);
+        pl.unit_cost = kSimtUnitCost;
     }
     // tiles there can be at most: fewer blocks are enough for fewer
     const int64_t tiles = ((int64_t)c.max_pages * c.page_size + pl.keys - 1) / pl.keys;
@@ -161,7 +165,7 @@ int launch_attention(const cv_tree_attention_args *a, cudaStream_t stream) {
     p.q = a->q, p.q_seq = a->q_seq_stride, p.q_tok = a->q_tok_stride, p.q_head = a->q_head_stride;
     p.out = a->out, p.o_seq = a->out_seq_stride, p.o_tok = a->out_tok_stride, p.o_head = a->out_head_stride;
     p.cu = a->cu_draft, p.parent = a->parent, p.len = a->cache_len, p.idx = a->cache_idx, p.err = a->err;
-    p.rows = pl.rows, p.pad = (pl.rows + 3) / 4 * 4, p.keys = pl.keys, p.dp = pl.dp, p.parts = pl.parts;
+    p.rows = pl.rows, p.pad = (pl.rows + 3) / 4 * 4, p.keys = pl.keys, p.dp = pl.dp, p.parts = pl.parts, p.unit_cost = pl.unit_cost;
     p.ws = pl.cut ? reinterpret_cast<float *>(a->workspace) : nullptr;
     if (pl.on_tc) {
         const int64_t tokens = a->cu_draft ? a->total_tokens : a->T, seqs = a->cu_draft ? 1 : a->n_seq;
@@ -186,8 +190,8 @@ int launch_attention(const cv_tree_attention_args *a, cudaStream_t stream) {
             return CV_ERR_LAUNCH;
     }
     if (pl.cut) {
-        const dim3 grid((unsigned)pl.parts, (unsigned)((pl.rows + cvk::kAttnJoinRows - 1) / cvk::kAttnJoinRows));
-        if (launch_pdl(cvk::attn_join_kernel(c.dtype == CV_BF16), grid, dim3(cvk::kAttnJoinThreads), 0, stream, p) != cudaSuccess)
+        const dim3 grid((unsigned)pl.parts, (unsigned)cvk::kAttnJoinY, 2);
+        if (launch_pdl(cvk::attn_join_kernel(c.dtype == CV_BF16, pl.dp), grid, dim3(cvk::kAttnJoinThreads), 0, stream, p) != cudaSuccess)
             return CV_ERR_LAUNCH;
     }
     return cudaGetLastError() == cudaSuccess ? CV_OK : CV_ERR_LAUNCH;

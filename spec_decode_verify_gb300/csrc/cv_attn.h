@@ -31,8 +31,9 @@ struct AttnParams {
     const int *cu, *parent, *len, *idx;
     int *err;
     // A unit of work is up to `rows` rows (draft, query head of the group) of one kv head of one sequence over all its keys,
-    // in tiles of `keys` of them.  All units' tiles, in a row, are cut into `parts` equal runs, one a block.
-    int rows, keys, dp, parts;
+    // in tiles of `keys` of them.  All units' work, in a row, is cut into `parts` equal runs, one a block; a unit's work is its tiles
+    // and up to unit_cost more, what its beginning and end take, in tiles.
+    int rows, keys, dp, parts, unit_cost;
     int pad;    // rows of a partial result: rows, a multiple of 4
     float *ws;  // two partial results a block, or NULL where no unit can be cut
 };
@@ -59,8 +60,8 @@ struct AttnTc {
 };
 AttnSimt attn_simt_kernel(bool bf16, int dp, bool vec);
 AttnTc attn_tc_kernel(int dp);
-AttnKernel attn_join_kernel(bool bf16);
-constexpr int kAttnJoinThreads = 128, kAttnJoinRows = 8;
+AttnKernel attn_join_kernel(bool bf16, int dp);
+constexpr int kAttnJoinThreads = 256, kAttnJoinY = 4;
 
 // ---- draft verification
 struct SampleParams {

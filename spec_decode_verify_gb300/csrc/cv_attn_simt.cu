@@ -29,7 +29,7 @@ struct SimtShared {
     AttnTree tree;
     uint4 see[128];
     AttnRange range;
-    long long scratch[32];
+    AttnScratch scratch;
 };
 
 // 4 channels from c on of a row (zeros past d).
@@ -63,13 +63,13 @@ __global__ void __launch_bounds__(kSimtThreads) attn_simt(const __grid_constant_
     grid_dep_wait();
     grid_dep_launch();
     const int tid = threadIdx.x, d = p.c.d;
-    attn_range(p, &sh->range, sh->scratch);
+    attn_range(p, &sh->range, &sh->scratch);
     const int rg = tid / 16, kg = tid % 16;   // scores: rows 2 rg and 2 rg + 1, keys kg + 16 i
     const int c4 = tid % C4, og = tid / C4;   // outputs: channels 4 c4 .., rows og * RPT ..
     AttnWalk walk(p, sh->range);
     AttnUnit u;
     int s_before = -1;
-    bool bad = false;
+    bool bad = false, goes_on = false, came = false;  // parts left in slots 1 and 0
     while (walk.next(p, u)) {
         const B *const K = reinterpret_cast<const B *>(p.c.k) + (long long)u.h * p.c.k_head;
         const B *const V = reinterpret_cast<const B *>(p.c.v) + (long long)u.h * p.c.v_head;
@@ -79,7 +79,7 @@ __global__ void __launch_bounds__(kSimtThreads) attn_simt(const __grid_constant_
         if (u.s != s_before) {
             s_before = u.s;
             const int *parent = p.parent ? p.parent + (p.cu ? (long long)u.q.row0 : (long long)u.s * p.T) : nullptr;
-            int st = attn_ancestors(parent, u.q.T, tid, &sh->tree, sh->see, [] { __syncthreads(); }) ? kSeqBadTree : 0;
+            int st = attn_ancestors(parent, u.q.T, tid, kSimtThreads, &sh->tree, sh->see, [] { __syncthreads(); }) ? kSeqBadTree : 0;
             for (int i = tid; i <= (end - 1) / p.c.page; i += kSimtThreads) {
                 const int g = __ldg(table + i);
                 if (g < 0 || g >= p.c.n_pages) st |= kSeqBadPage;
@@ -88,10 +88,9 @@ __global__ void __launch_bounds__(kSimtThreads) attn_simt(const __grid_constant_
             bad = __syncthreads_or(st) != 0;
         }
         const bool cut = u.last - u.tile < u.tiles, begins = u.tile == 0;
-        if (bad) {
-            if (cut && begins && tid == 0) *reinterpret_cast<int *>(attn_part(p, blockIdx.x, 1)) = 0;
-            continue;
-        }
+        goes_on = cut && begins && !bad;
+        came |= cut && !begins && !bad;
+        if (bad) continue;
         for (int i = tid; i < kSimtRows * C4; i += kSimtThreads) {
             const int r = i / C4, c = i % C4 * 4, t = (u.row + r) / p.G, g = (u.row + r) % p.G;
             float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -210,73 +209,123 @@ __global__ void __launch_bounds__(kSimtThreads) attn_simt(const __grid_constant_
             }
         } else {
             float *const part = attn_part(p, blockIdx.x, begins);
-            if (tid == 0) {
-                int *const head = reinterpret_cast<int *>(part);
-                head[0] = begins, head[1] = (int)((u.first + u.tiles - 1) / sh->range.per) - (int)blockIdx.x + 1;
-                head[2] = u.s, head[3] = u.h, head[4] = u.row, head[5] = 1;
-            }
+            if (tid == 0) attn_part_head(part, sh->range, u.first, u.tiles, u.rows, u.row, u.s, u.h, u.q.row0);
             if (tid < kSimtRows) part[kPartHead + tid] = sh->m[tid], part[kPartHead + kSimtRows + tid] = sh->l[tid];
             float4 *const to = reinterpret_cast<float4 *>(part + kPartHead + 2 * kSimtRows);
 #pragma unroll
             for (int i = 0; i < RPT; ++i) to[(og * RPT + i) * C4 + c4] = o[i];
         }
     }
-    // the join reads this slot of every block
-    __syncthreads();
-    if (p.ws && tid == 0) {
-        const bool goes_on = sh->range.begin < sh->range.end && u.tile == 0 && u.last < u.tiles;  // the last unit
-        if (!goes_on) *reinterpret_cast<int *>(attn_part(p, blockIdx.x, 1)) = 0;
-    }
+    // the join reads both slots of every block
+    if (p.ws && tid == 0 && !goes_on) *reinterpret_cast<int *>(attn_part(p, blockIdx.x, 1)) = 0;
+    if (p.ws && tid == 0 && !came) *reinterpret_cast<int *>(attn_part(p, blockIdx.x, 0)) = 0;
 }
 
-// One warp a row: the parts' maxima first, then the weighted sums.
-template <typename B>
-__global__ void __launch_bounds__(kAttnJoinThreads) attn_join(const __grid_constant__ AttnParams p) {
+// The units that were cut.  A unit of n parts is spread over the blocks of its n parts, kAttnJoinY each; a row takes one warp, or
+// several where there are few rows for them, each with every so many parts: eight parts' flags, maxima, sums and rows on their
+// way at once, added up under a running maximum.
+template <typename B, int E>  // E: 128 channels each that a warp holds
+__global__ void __launch_bounds__(kAttnJoinThreads, 4 - E) attn_join(const __grid_constant__ AttnParams p) {
+    constexpr int WARPS = kAttnJoinThreads / 32, N = 8 / E;
+    __shared__ float4 sum[WARPS][32 * E];
+    __shared__ float sum_l[WARPS], sum_m[WARPS];
+    __shared__ int left_out[WARPS];
     grid_dep_wait();
     grid_dep_launch();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const float *const first = attn_part(p, blockIdx.x, 1);
-    const int *const head = reinterpret_cast<const int *>(first);
-    if (head[0] != 1) return;
-    const int n = head[1], s = head[2], h = head[3], row0 = head[4];
-    const AttnSeq q = attn_seq(p, s);
-    const int rows = min(p.rows, q.T * p.G - row0);
-    const long long step = 2 * part_floats(p.pad, p.dp);
-    // part i > 0 is slot 0 of the block i further on
-    auto part = [&](int i) { return i == 0 ? first : first + i * step - step / 2; };
-    bool whole = true;  // (a block that gave up leaves no part)
-    for (int i = lane; i < n; i += 32) whole = whole && reinterpret_cast<const int *>(part(i))[5] != 0;
-    if (!__all_sync(0xffffffffu, whole)) return;
-    for (int r = blockIdx.y * kAttnJoinRows + warp; r < min(rows, (int)(blockIdx.y + 1) * kAttnJoinRows); r += kAttnJoinThreads / 32) {
-        float top = kNone;
-        for (int i = lane; i < n; i += 32) top = fmaxf(top, part(i)[kPartHead + r]);
+    const int4 *const mine_at = reinterpret_cast<const int4 *>(attn_part(p, blockIdx.x, blockIdx.z));
+    const int4 h0 = mine_at[0], h1 = mine_at[1];  // (see attn_part_head)
+    if (h0.x == 0) return;
+    const int n = h0.y, c0 = h0.z, rows = h0.w, row0 = h1.x, s = h1.y, h = h1.z, packed = h1.w;
+    const float *const first = attn_part(p, c0, 1);
+    const long long step = part_floats(p.pad, p.dp);
+    const int share = ((int)blockIdx.x - c0) * kAttnJoinY + blockIdx.y, shares = n * kAttnJoinY;
+    int each = 1;  // warps a row
+    while (each < WARPS && each * 2 * rows <= shares * WARPS) each *= 2;
+    const int at_once = WARPS / each, mine = warp % each;
+    for (int base = share * at_once; base < rows; base += shares * at_once) {
+        const int r = base + warp / each;
+        const bool on = r < rows;
+        float4 o[E];
 #pragma unroll
-        for (int b = 16; b > 0; b >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, b));
-        float4 o[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
-        float l = 0.f;
-#pragma unroll 4
-        for (int i = 0; i < n; ++i) {
-            const float *const x = part(i);
-            const float m = x[kPartHead + r], sum = x[kPartHead + p.pad + r];
-            // (a part in which the row sees nothing, or minus infinity alone; its sum may be a NaN, which stays)
-            if (m == kNone && sum == 0.f) continue;
-            const float w = m == kNone ? 1.f : ex2(m - top);
-            l = fmaf(w, sum, l);
-            const float4 *const a = reinterpret_cast<const float4 *>(x + kPartHead + 2 * p.pad + (long long)r * p.dp);
+        for (int e = 0; e < E; ++e) o[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+        float l = 0.f, top = kNone;
+        int gone = 0;  // (a block that gave up leaves no part)
+        if (on) {
+            for (int i0 = mine; i0 < n; i0 += N * each) {
+                float4 v[N][E];
+                float m[N], w[N];
+                int flag[N];
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
-                if (4 * (lane + 32 * e) < p.dp) {
-                    const float4 v = a[lane + 32 * e];
-                    o[e].x = fmaf(w, v.x, o[e].x), o[e].y = fmaf(w, v.y, o[e].y);
-                    o[e].z = fmaf(w, v.z, o[e].z), o[e].w = fmaf(w, v.w, o[e].w);
+                for (int x = 0; x < N; ++x) {
+                    const int i = i0 + x * each;
+                    m[x] = kNone, w[x] = 0.f, flag[x] = 1;
+                    if (i < n) {
+                        const float *const a = first + (i == 0 ? 0 : 2 * i - 1) * step;  // i > 0: slot 0 of block c0 + i
+                        flag[x] = *reinterpret_cast<const int *>(a);
+                        m[x] = a[kPartHead + r], w[x] = a[kPartHead + p.pad + r];
+                        const float4 *const row = reinterpret_cast<const float4 *>(a + kPartHead + 2 * p.pad + (long long)r * p.dp);
+#pragma unroll
+                        for (int e = 0; e < E; ++e)
+                            if (4 * (lane + 32 * e) < p.dp) v[x][e] = row[lane + 32 * e];
+                    }
                 }
+                float now = top;
+#pragma unroll
+                for (int x = 0; x < N; ++x) now = fmaxf(now, m[x]);
+                const float down = now == kNone ? 1.f : ex2(top - now);
+                top = now, l *= down;
+#pragma unroll
+                for (int e = 0; e < E; ++e) o[e].x *= down, o[e].y *= down, o[e].z *= down, o[e].w *= down;
+#pragma unroll
+                for (int x = 0; x < N; ++x) {
+                    gone |= flag[x] == 0;
+                    // (a part in which the row sees nothing, or minus infinity alone; its sum may be a NaN, which stays)
+                    if (m[x] == kNone && w[x] == 0.f) continue;
+                    const float f = m[x] == kNone ? 1.f : ex2(m[x] - top);
+                    l = fmaf(f, w[x], l);
+#pragma unroll
+                    for (int e = 0; e < E; ++e) {
+                        o[e].x = fmaf(f, v[x][e].x, o[e].x), o[e].y = fmaf(f, v[x][e].y, o[e].y);
+                        o[e].z = fmaf(f, v[x][e].z, o[e].z), o[e].w = fmaf(f, v[x][e].w, o[e].w);
+                    }
+                }
+            }
         }
+        if (each > 1) {
+            __syncthreads();
+#pragma unroll
+            for (int e = 0; e < E; ++e) sum[warp][lane + 32 * e] = o[e];
+            if (lane == 0) sum_l[warp] = l, sum_m[warp] = top, left_out[warp] = gone;
+            __syncthreads();
+            if (mine == 0) {
+                float now = top;
+                for (int w = warp + 1; w < warp + each; ++w) now = fmaxf(now, sum_m[w]), gone |= left_out[w];
+                const float down = now == kNone ? 1.f : ex2(top - now);
+                l *= down;
+#pragma unroll
+                for (int e = 0; e < E; ++e) o[e].x *= down, o[e].y *= down, o[e].z *= down, o[e].w *= down;
+                for (int w = warp + 1; w < warp + each; ++w) {
+                    const float m = sum_m[w];
+                    if (m == kNone && sum_l[w] == 0.f) continue;
+                    const float f = m == kNone ? 1.f : ex2(m - now);
+                    l = fmaf(f, sum_l[w], l);
+#pragma unroll
+                    for (int e = 0; e < E; ++e) {
+                        const float4 x = sum[w][lane + 32 * e];
+                        o[e].x = fmaf(f, x.x, o[e].x), o[e].y = fmaf(f, x.y, o[e].y);
+                        o[e].z = fmaf(f, x.z, o[e].z), o[e].w = fmaf(f, x.w, o[e].w);
+                    }
+                }
+            }
+        }
+        if (!on || mine != 0 || gone) continue;
         const float inv = 1.0f / l;
         const int t = (row0 + r) / p.G, g = (row0 + r) % p.G;
-        B *const out = reinterpret_cast<B *>(p.out) + (p.cu ? 0LL : (long long)s * p.o_seq) + (long long)(q.row0 + t) * p.o_tok +
+        B *const out = reinterpret_cast<B *>(p.out) + (p.cu ? 0LL : (long long)s * p.o_seq) + (long long)(packed + t) * p.o_tok +
                        (long long)(h * p.G + g) * p.o_head;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
+        for (int e = 0; e < E; ++e) {
             const float f[4] = {o[e].x * inv, o[e].y * inv, o[e].z * inv, o[e].w * inv};
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
@@ -298,6 +347,9 @@ AttnSimt attn_simt_kernel(bool bf16, int dp, bool vec) {
     if (bf16) return dp <= 64 ? simt<uint16_t, 64>(vec) : dp <= 128 ? simt<uint16_t, 128>(vec) : simt<uint16_t, 256>(vec);
     return dp <= 64 ? simt<uint32_t, 64>(vec) : dp <= 128 ? simt<uint32_t, 128>(vec) : simt<uint32_t, 256>(vec);
 }
-AttnKernel attn_join_kernel(bool bf16) { return bf16 ? attn_join<uint16_t> : attn_join<uint32_t>; }
+AttnKernel attn_join_kernel(bool bf16, int dp) {
+    if (dp <= 128) return bf16 ? attn_join<uint16_t, 1> : attn_join<uint32_t, 1>;
+    return bf16 ? attn_join<uint16_t, 2> : attn_join<uint32_t, 2>;
+}
 
 }  // namespace cvk

@@ -7,15 +7,17 @@
 // more than 2^8, since that costs a pass over O; until then p is at most 2^8, which bf16 and the fp32 sums hold as well as 1.
 // P is rounded to bf16 (2^-8 of a term), as the operand of the second product; l sums what was not rounded.
 //
-// Layout.  A block (one per SM) takes a run of key tiles of the units' tiles in a row, so that all blocks read the same
-// number of keys whatever the lengths; a unit that is cut leaves (m, l, O) in the workspace for the join.  All rows of a
-// kv head's group share one read of its keys, so HBM bounds it: a tile of 128 keys of 128 channels is 64 KB, 1.4 us of an SM's
-// share, and takes 0.7 us of the tensor pipe at any number of rows.  Roles, each a stream of tiles of its own:
-//   load     1 warp: units (also for the others, through a queue in shared memory), Q, K and V by TMA, a box for each page
+// Layout.  A block (one per SM) takes an equal run of the units' work: their key tiles in a row, and for each unit about what
+// its beginning and end take, so that all blocks read for the same time whatever the lengths; a unit that is cut leaves (m, l, O) in the workspace
+// for the join.  All rows of a kv head's group share one read of its keys, so HBM bounds it: a tile of 128 keys of 128
+// channels is 64 KB, 1.4 us of an SM's share, and takes 0.7 us of the tensor pipe at any number of rows.  Roles, each a stream of its own:
+//   load K   1 warp: the units (also for the others, through a queue in shared memory), Q and K by TMA, a box for each page
+//   load V   1 warp: V (one warp for both took 45 cycles a box, 64 boxes a tile for pages of 16 tokens: slower than HBM)
 //   issue    1 warp: Q K^T of the next tile, then P V of this one
-//   softmax  4 warps, a row a thread: S from tensor memory, P back over it, O's rescaling, and at the end the outputs
-// Tensor memory: two buffers of S (and P), O (two for up to 192 channels, so that a unit begins while the last one's rows
-// are written).
+//   scout    1 warp: of each sequence the drafts' ancestors, and a look at every page and parent
+//   softmax  4 warps, a row a thread: S from tensor memory, P back over it, O's rescaling
+//   output   4 warps, a row a thread: O / l, or (m, l, O), to memory, while the next unit runs
+// Tensor memory: two buffers of S (and P), O (two for up to 192 channels).
 //
 // Masks.  Cached tokens are seen by every row; only the tiles that reach past them look at masks.  There the rows of V past the
 // end are zeroed in shared memory (0 * what lies there may be NaN), and so are drafts' rows of V that hold a NaN or an
@@ -31,15 +33,15 @@ namespace {
 constexpr float kNone = -INFINITY;
 constexpr float kSlack = 8.0f;  // log2 of what a weight may reach before its row's maximum is moved
 constexpr unsigned kDrainPolls = 1u << 16;
-constexpr int kTcThreads = 192, kQueue = 4;
+constexpr int kTcThreads = 384, kQueue = 4;
 
 template <int DP>
 struct Tc {
     static constexpr int KT = DP <= 128 ? 128 : 64;     // keys a tile
     static constexpr int BLOCKS = DP / 64;              // blocks of 64 channels
     static constexpr int KV = KT * DP * 2, Q = 128 * DP * 2;
-    static constexpr int QBUF = DP <= 192 ? 2 : 1, OBUF = DP <= 192 ? 2 : 1;
-    static constexpr int STAGES = DP == 64 ? 8 : DP == 128 ? 4 : DP == 192 ? 5 : 4;
+    static constexpr int QBUF = DP <= 128 ? 2 : 1, OBUF = DP <= 192 ? 2 : 1;
+    static constexpr int KS = DP == 64 ? 4 : DP == 192 ? 3 : 2, VS = KS;  // stages of K and of V
     static constexpr int COL_O = 2 * KT;
     static_assert(COL_O + OBUF * DP <= 512, "tensor memory");
 };
@@ -51,21 +53,24 @@ struct TcUnit {
 };
 
 struct TcShared {
-    uint64_t kv_full[8], kv_empty[8], q_full[2], q_empty[2], s_full[2], p_ready[2], o_free[2], unit_full[kQueue], unit_empty[kQueue],
-        pv_done, meet, last;
+    uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4], q_full[2], q_empty[2], s_full[2], p_ready[2], o_full[2], o_free[2],
+        ml_full[2], ml_free[2], see_full[2], see_empty[2], unit_full[kQueue], unit_empty[kQueue], pv_done, last;
     TcUnit unit[kQueue];
+    int unit_pages[kQueue][32];  // the pages of its first tiles
     uint32_t tmem;
-    int dead, flags;
-    uint32_t bad[2][4];  // drafts whose v holds a NaN or an infinity; of two units in turn
-    uint4 see[128];
+    int dead;
+    int flags[2];            // of a sequence, and its drafts' ancestors; two in turn
+    uint4 see[2][128];
+    uint32_t bad[2][4][4];   // drafts whose v holds a NaN or an infinity, as each softmax warp saw them; of two units in turn
+    float m[2][128], l[2][128];
     AttnTree tree;
     AttnRange range;
-    long long scratch[32];
+    AttnScratch scratch;
 };
 
 template <int DP>
 __host__ __device__ constexpr int tc_smem() {
-    return Tc<DP>::QBUF * Tc<DP>::Q + Tc<DP>::STAGES * Tc<DP>::KV + (int)sizeof(TcShared) + 1024;
+    return Tc<DP>::QBUF * Tc<DP>::Q + (Tc<DP>::KS + Tc<DP>::VS) * Tc<DP>::KV + (int)sizeof(TcShared) + 1024;
 }
 
 struct Waits {
@@ -175,24 +180,26 @@ __device__ __noinline__ void add_bad_drafts(const AttnParams &p, const TcUnit &u
 template <int DP>
 __global__ void __launch_bounds__(kTcThreads, 1) attn_tc(const __grid_constant__ AttnMaps mp) {
     using K = Tc<DP>;
-    constexpr int KT = K::KT, STAGES = K::STAGES;
+    constexpr int KT = K::KT, KS = K::KS, VS = K::VS;
     extern __shared__ unsigned char smem_raw[];
     unsigned char *const smem = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) / 1024 * 1024);
-    unsigned char *const q_tile = smem, *const kv_tile = smem + K::QBUF * K::Q;
-    TcShared *const sh = reinterpret_cast<TcShared *>(kv_tile + STAGES * K::KV);
+    unsigned char *const q_tile = smem, *const k_tile = smem + K::QBUF * K::Q, *const v_tile = k_tile + KS * K::KV;
+    TcShared *const sh = reinterpret_cast<TcShared *>(v_tile + VS * K::KV);
     const AttnParams &p = mp.a;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (dynamic_smem_bytes() < (unsigned)tc_smem<DP>()) return;
     if (tid == 0) {
-        for (int i = 0; i < 8; ++i) mbar_init(&sh->kv_full[i], 1), mbar_init(&sh->kv_empty[i], 1);
+        for (int i = 0; i < 4; ++i)
+            mbar_init(&sh->k_full[i], 1), mbar_init(&sh->k_empty[i], 1), mbar_init(&sh->v_full[i], 1), mbar_init(&sh->v_empty[i], 1);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&sh->q_full[i], 1), mbar_init(&sh->q_empty[i], 1), mbar_init(&sh->s_full[i], 1);
-            mbar_init(&sh->p_ready[i], 4), mbar_init(&sh->o_free[i], 4);
+            mbar_init(&sh->q_full[i], 1), mbar_init(&sh->q_empty[i], 1), mbar_init(&sh->s_full[i], 1), mbar_init(&sh->p_ready[i], 4);
+            mbar_init(&sh->o_full[i], 1), mbar_init(&sh->o_free[i], 4), mbar_init(&sh->ml_full[i], 4), mbar_init(&sh->ml_free[i], 4);
+            mbar_init(&sh->see_full[i], 1), mbar_init(&sh->see_empty[i], 8);
         }
-        for (int i = 0; i < kQueue; ++i) mbar_init(&sh->unit_full[i], 1), mbar_init(&sh->unit_empty[i], 5);
-        mbar_init(&sh->pv_done, 1), mbar_init(&sh->meet, 4), mbar_init(&sh->last, 1);
+        for (int i = 0; i < kQueue; ++i) mbar_init(&sh->unit_full[i], 1), mbar_init(&sh->unit_empty[i], 11);
+        mbar_init(&sh->pv_done, 1), mbar_init(&sh->last, 1);
         mbar_init_fence();
-        sh->dead = 0, sh->flags = 0;
+        sh->dead = 0;
     }
     if (warp == 5) tmem_alloc(&sh->tmem, kTmemCols);
     if (warp == 4 && lane < 3) {
@@ -201,49 +208,59 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc(const __grid_constant__
     }
     grid_dep_wait();
     grid_dep_launch();
-    attn_range(p, &sh->range, sh->scratch);
+    attn_range(p, &sh->range, &sh->scratch);
     tmem_fence_before();
     __syncthreads();
     tmem_fence_after();
     const uint32_t tm = sh->tmem;
     const Waits waits{&sh->dead, p.polls};
     const AttnRange &range = sh->range;
-    const int total = (int)(range.end > range.begin ? range.end - range.begin : 0);
+    // The next unit of the queue for the calling warp; s < 0 after the last one.
+    auto pop = [&](TcUnit &u, int units) {
+        const int at = units % kQueue;
+        if (!wait_warp(&sh->unit_full[at], (units / kQueue) & 1, waits)) return false;
+        u = sh->unit[at];
+        arrive_warp(&sh->unit_empty[at]);
+        return true;
+    };
+    // Copies of a tile: a lane takes one block of 64 channels of one page's rows.
+    const int boxes = KT / mp.page_rows, tiles_page = p.c.page > KT ? p.c.page / KT : 1;
+    const int blk = lane % K::BLOCKS, box = lane / K::BLOCKS;
+    // A table row's entries, 32 at a time a lane each, the next 32 on their way (a look-up for each tile held every
+    // copy up by its latency: 2850 cycles a tile of 128 x 128, 2.9 us for each stage of shared memory to come round).
+    struct Pages {
+        const int *row;
+        int n, base, cur, next;
+        __device__ __forceinline__ int fetch(int at, int lane) const { return at + lane < n ? __ldg(row + at + lane) : 0; }
+    };
+    Pages pages = {nullptr, 0, 0, 0, 0};
+    auto pages_at = [&](int slot, int end, int tile) {
+        Pages g;
+        g.row = p.c.table + (long long)slot * p.c.table_row, g.n = (end - 1) / p.c.page + 1;
+        g.base = tiles_page > 1 ? tile / tiles_page : tile * boxes;
+        g.cur = g.next = 0;
+        return g;
+    };
+    auto copy = [&](const CUtensorMap *map, unsigned char *dst, uint64_t *bar, int h, int end, int tile) {
+        const int j0 = tile * KT, first = tiles_page > 1 ? tile / tiles_page : tile * boxes;  // (32 is a multiple of boxes)
+        if (first - pages.base >= 32) {
+            pages.cur = pages.next, pages.base += 32;
+            pages.next = pages.fetch(pages.base + 32, lane);
+        }
+        const int page = __shfl_sync(0xffffffffu, pages.cur, first - pages.base + box);
+        const int n = min(boxes, (end - j0 + mp.page_rows - 1) / mp.page_rows);
+        if (lane == 0) mbar_arrive_expect_tx(bar, (unsigned)(n * (K::BLOCKS * 128) * mp.page_rows));
+        __syncwarp();
+        if (box < n)
+            tma_load4(smem_u32(dst) + blk * (KT * 128) + box * mp.page_rows * 128, map, blk * 64, (tile % tiles_page) * KT, h, page, bar);
+    };
 
     if (warp == 4) {
-        // ------------------------------------------------------------------------------ load
+        // ------------------------------------------------------------------- load: units, Q, K
         AttnWalk walk(p, range);
         AttnUnit u, next;
-        bool has = walk.next(p, u), has_next = false;
-        const int boxes = KT / mp.page_rows;           // of a tile
-        const int blk = lane % K::BLOCKS, box = lane / K::BLOCKS;  // this lane's copy
-        int pos = 0, units = 0;
-        bool ok = true;
-        struct Where {
-            int page, row, h, n;  // this lane's; n: bytes of the tile's boxes
-            bool on;
-        };
-        auto where = [&](const AttnUnit &a, int tile) {
-            Where w;
-            const int j = tile * KT + box * mp.page_rows, end = a.q.L + a.q.T;
-            w.on = box < boxes && j < end;
-            w.page = w.on ? __ldg(p.c.table + (long long)a.q.slot * p.c.table_row + j / p.c.page) : 0;
-            w.row = j % p.c.page, w.h = a.h;
-            const int left = end - tile * KT;
-            w.n = min(boxes, (left + mp.page_rows - 1) / mp.page_rows) * (K::BLOCKS * 128) * mp.page_rows;
-            return w;
-        };
-        auto copy = [&](const CUtensorMap *map, const Where &w) {
-            const int stage = pos % STAGES;
-            if (pos >= STAGES && !wait_warp(&sh->kv_empty[stage], (pos / STAGES - 1) & 1, waits)) return false;
-            if (lane == 0) mbar_arrive_expect_tx(&sh->kv_full[stage], (unsigned)w.n);
-            __syncwarp();
-            if (w.on)
-                tma_load4(smem_u32(kv_tile) + stage * K::KV + blk * (KT * 128) + box * mp.page_rows * 128, map, blk * 64, w.row, w.h,
-                          w.page, &sh->kv_full[stage]);
-            ++pos;
-            return true;
-        };
+        bool has = walk.next(p, u), ok = true;
+        int units = 0, it = 0;
         auto publish = [&](bool end) {
             const int at = units % kQueue;
             if (units >= kQueue && !wait_warp(&sh->unit_empty[at], (units / kQueue - 1) & 1, waits)) return false;
@@ -251,51 +268,102 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc(const __grid_constant__
                 TcUnit &t = sh->unit[at];
                 t.s = end ? -1 : u.s, t.h = u.h, t.row = u.row, t.rows = u.rows, t.tile = u.tile, t.last = u.last, t.tiles = u.tiles;
                 t.slot = u.q.slot, t.L = u.q.L, t.T = u.q.T, t.row0 = u.q.row0, t.first = u.first, t.begins = u.tile == 0;
-                mbar_arrive(&sh->unit_full[at]);
             }
-            __syncwarp();
+            sh->unit_pages[at][lane] = pages.cur;
+            arrive_warp(&sh->unit_full[at]);
             return true;
         };
-        Where cur, before;
-        if (has) cur = where(u, u.tile);
-        bool pending = false;  // V of the tile before
-        int q_sent = 0;
+        // a unit ahead of its copies: the next one's lengths and first pages are looked up while this one's keys are copied
+        Pages ahead = pages;
+        auto look = [&](const AttnUnit &a) {
+            ahead = pages_at(a.q.slot, a.q.L + a.q.T, a.tile);
+            ahead.cur = ahead.fetch(ahead.base, lane), ahead.next = ahead.fetch(ahead.base + 32, lane);
+        };
+        if (has) look(u);
         while (ok && has) {
+            pages = ahead;
             if (!(ok = publish(false))) break;
-            const int qb = units % K::QBUF;
+            const int qb = units % K::QBUF, end = u.q.L + u.q.T;
             if (units >= K::QBUF && !(ok = wait_warp(&sh->q_empty[qb], (units / K::QBUF - 1) & 1, waits))) break;
             if (lane == 0) mbar_arrive_expect_tx(&sh->q_full[qb], (unsigned)(K::BLOCKS * 128 * mp.tok * p.G));
             __syncwarp();
             if (lane < K::BLOCKS)
                 tma_load4(smem_u32(q_tile) + qb * K::Q + lane * (128 * 128), &mp.q, lane * 64, u.h * p.G, u.q.row0 + u.row / p.G,
                           p.cu ? 0 : u.s, &sh->q_full[qb]);
-            ++units, ++q_sent;
-            has_next = walk.next(p, next);
-            for (int tile = u.tile; tile < u.last; ++tile) {
-                // the next tile's pages are looked up while this one's copies wait for their place
-                Where then;
-                if (tile + 1 < u.last) then = where(u, tile + 1);
-                else if (has_next) then = where(next, next.tile);
-                if (!(ok = copy(&mp.k, cur))) break;
-                if (pending && !(ok = copy(&mp.v, before))) break;
-                before = cur, pending = true;
-                cur = then;
+            ++units;
+            bool has_next = false;
+            for (int tile = u.tile; tile < u.last; ++tile, ++it) {
+                const int stage = it % KS;
+                if (it >= KS && !(ok = wait_warp(&sh->k_empty[stage], (it / KS - 1) & 1, waits))) break;
+                copy(&mp.k, k_tile + stage * K::KV, &sh->k_full[stage], u.h, end, tile);
+                if (tile == u.tile) {
+                    has_next = walk.next(p, next);
+                    if (has_next) look(next);
+                }
             }
             u = next, has = has_next;
         }
-        if (ok) ok = publish(true);
-        if (ok && pending) copy(&mp.v, before);
+        if (ok) publish(true);
         // nothing of the block's is in flight when it returns
         __syncwarp();
-        for (int x = max(0, pos - STAGES); x < pos; ++x) mbar_wait_bounded(&sh->kv_full[x % STAGES], (x / STAGES) & 1, kDrainPolls);
-        for (int x = max(0, q_sent - K::QBUF); x < q_sent; ++x)
+        for (int x = max(0, it - KS); x < it; ++x) mbar_wait_bounded(&sh->k_full[x % KS], (x / KS) & 1, kDrainPolls);
+        for (int x = max(0, units - K::QBUF); x < units; ++x)
             mbar_wait_bounded(&sh->q_full[x % K::QBUF], (x / K::QBUF) & 1, kDrainPolls);
+    } else if (warp == 7) {
+        // --------------------------------------------------------------------------- load: V
+        int it = 0;
+        bool ok = true;
+        TcUnit u;
+        for (int units = 0; ok; ++units) {
+            const int at = units % kQueue;
+            if (!(ok = wait_warp(&sh->unit_full[at], (units / kQueue) & 1, waits))) break;
+            u = sh->unit[at];
+            const int first = sh->unit_pages[at][lane];
+            arrive_warp(&sh->unit_empty[at]);
+            if (u.s < 0) break;
+            const int end = u.L + u.T;
+            pages = pages_at(u.slot, end, u.tile);
+            pages.cur = first, pages.next = pages.fetch(pages.base + 32, lane);
+            for (int tile = u.tile; tile < u.last; ++tile, ++it) {
+                const int stage = it % VS;
+                if (it >= VS && !(ok = wait_warp(&sh->v_empty[stage], (it / VS - 1) & 1, waits))) break;
+                copy(&mp.v, v_tile + stage * K::KV, &sh->v_full[stage], u.h, end, tile);
+            }
+        }
+        __syncwarp();
+        for (int x = max(0, it - VS); x < it; ++x) mbar_wait_bounded(&sh->v_full[x % VS], (x / VS) & 1, kDrainPolls);
+    } else if (warp == 6) {
+        // ----------------------------------------------------------------------------- scout
+        int seqs = 0, s_before = -1;
+        TcUnit u;
+        for (int units = 0; pop(u, units) && u.s >= 0; ++units) {
+            if (u.s == s_before) continue;
+            s_before = u.s;
+            const int b = seqs & 1;
+            if (seqs >= 2 && !wait_warp(&sh->see_empty[b], ((seqs >> 1) - 1) & 1, waits)) break;
+            ++seqs;
+            const int *const parent = p.parent ? p.parent + (p.cu ? (long long)u.row0 : (long long)u.s * p.T) : nullptr;
+            int st = attn_ancestors(parent, u.T, lane, 32, &sh->tree, sh->see[b], [] { __syncwarp(); }) ? kSeqBadTree : 0;
+            const int *const table = p.c.table + (long long)u.slot * p.c.table_row;
+            const int pages = (u.L + u.T - 1) / p.c.page + 1;
+#pragma unroll 8
+            for (int i = lane; i < pages; i += 32) {
+                const int g = __ldg(table + i);
+                if (g < 0 || g >= p.c.n_pages) st |= kSeqBadPage;
+            }
+            st = __reduce_or_sync(0xffffffffu, (unsigned)st);
+            if (lane == 0) {
+                if (st && p.err) atomicOr(p.err + u.s, st);
+                sh->flags[b] = st;
+            }
+            arrive_warp(&sh->see_full[b]);
+        }
     } else if (warp == 5) {
         // ----------------------------------------------------------------------------- issue
         const uint32_t lead = elect_lane();
         constexpr uint32_t id_qk = mma_desc(KT, false, false), id_pv = mma_desc(DP, false, true);
-        int pos = 0, units = 0, qk_left = 0, n_next = 0, it = 0, pv_unit = 0, pv_left = 0, pv_at = 0;
-        auto pop = [&](int &n) {  // tiles of the next unit, 0 after the last one, -1: gave up
+        int units = 0, qk_left = 0, n_next = 0, it = 0, pv_unit = 0, pv_left = 0, pv_at = 0;
+        auto tiles = [&](int &n) {  // of the next unit; 0 after the last one
             const int at = units % kQueue;
             if (!wait_warp(&sh->unit_full[at], (units / kQueue) & 1, waits)) return false;
             n = sh->unit[at].s < 0 ? 0 : sh->unit[at].last - sh->unit[at].tile;
@@ -304,23 +372,22 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc(const __grid_constant__
             return true;
         };
         auto scores = [&](int i, bool first, bool last) {
-            const int qb = (units - 1) % K::QBUF, stage = pos % STAGES;
+            const int qb = (units - 1) % K::QBUF, stage = i % KS;
             if (first && !wait_warp(&sh->q_full[qb], ((units - 1) / K::QBUF) & 1, waits)) return false;
-            if (!wait_warp(&sh->kv_full[stage], (pos / STAGES) & 1, waits)) return false;
+            if (!wait_warp(&sh->k_full[stage], (i / KS) & 1, waits)) return false;
             tmem_fence_after();
-            const uint32_t q = desc_k(smem_u32(q_tile) + qb * K::Q), k = desc_k(smem_u32(kv_tile) + stage * K::KV);
+            const uint32_t q = desc_k(smem_u32(q_tile) + qb * K::Q), k = desc_k(smem_u32(k_tile) + stage * K::KV);
 #pragma unroll 4
             for (int x = 0; x < DP / 16; ++x)
                 mma_ss(lead, tm + (i & 1) * KT, q + (((x >> 2) * (128 * 128) + (x & 3) * 32) >> 4),
                        k + (((x >> 2) * (KT * 128) + (x & 3) * 32) >> 4), id_qk, x > 0);
             mma_commit(lead, &sh->s_full[i & 1]);
-            mma_commit(lead, &sh->kv_empty[stage]);
+            mma_commit(lead, &sh->k_empty[stage]);
             if (last) mma_commit(lead, &sh->q_empty[qb]);
-            ++pos;
             return true;
         };
         int n = 0;
-        bool ok = pop(n) && n > 0;
+        bool ok = tiles(n) && n > 0;
         if (ok) {
             qk_left = pv_left = n;
             ok = scores(0, true, n == 1);
@@ -328,32 +395,31 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc(const __grid_constant__
         }
         while (ok) {
             ok = false;
-            bool more = qk_left > 0;
-            if (more) {
+            if (qk_left > 0) {
                 if (!scores(it + 1, false, qk_left == 1)) break;
                 --qk_left;
             } else if (n > 0) {
-                if (!pop(n)) break;
+                if (!tiles(n)) break;
                 n_next = n;
                 if (n > 0) {
                     if (!scores(it + 1, true, n == 1)) break;
                     qk_left = n - 1;
                 }
             }
-            const int ob = pv_unit % K::OBUF, stage = pos % STAGES;
+            const int ob = pv_unit % K::OBUF, stage = it % VS;
             if (pv_at == 0 && pv_unit >= K::OBUF && !wait_warp(&sh->o_free[ob], (pv_unit / K::OBUF - 1) & 1, waits)) break;
-            if (!wait_warp(&sh->kv_full[stage], (pos / STAGES) & 1, waits) || !wait_warp(&sh->p_ready[it & 1], (it >> 1) & 1, waits))
-                break;
+            if (!wait_warp(&sh->v_full[stage], (it / VS) & 1, waits) || !wait_warp(&sh->p_ready[it & 1], (it >> 1) & 1, waits)) break;
             tmem_fence_after();
-            const uint32_t v = desc_mn(smem_u32(kv_tile) + stage * K::KV, KT * 128);
+            const uint32_t v = desc_mn(smem_u32(v_tile) + stage * K::KV, KT * 128);
 #pragma unroll 4
             for (int x = 0; x < KT / 16; ++x)
                 mma_ts(lead, tm + K::COL_O + ob * DP, tm + (it & 1) * KT + x * 8, v + x * 128, id_pv, pv_at > 0 || x > 0);
-            mma_commit(lead, &sh->kv_empty[stage]);
+            mma_commit(lead, &sh->v_empty[stage]);
             mma_commit(lead, &sh->pv_done);
-            ++pos, ++it, ++pv_at;
+            ++it, ++pv_at;
             ok = true;
             if (--pv_left == 0) {
+                mma_commit(lead, &sh->o_full[ob]);
                 if (n == 0) break;  // the last unit
                 ++pv_unit, pv_at = 0, pv_left = n_next;
             }
@@ -361,66 +427,48 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc(const __grid_constant__
         // nothing of the block's is in flight when it gives tensor memory back
         mma_commit(lead, &sh->last);
         mbar_wait_bounded(&sh->last, 0, kDrainPolls);
-    } else {
+    } else if (warp < 4) {
         // --------------------------------------------------------------------------- softmax
         const int r = tid;  // the row
         const uint32_t tl = tm + ((uint32_t)(32 * warp) << 16);
-        int it = 0, s_before = -1;
+        int it = 0, s_before = -1, seqs = 0;  // seqs: sequences begun
         uint4 see = make_uint4(0, 0, 0, 0);
         bool ok = true;
-        unsigned met = 0;
-        auto meet = [&] {  // the softmax warps; bounded as every wait
-            arrive_warp(&sh->meet);
-            return wait_warp(&sh->meet, met++ & 1, waits);
-        };
-        for (int units = 0; ok; ++units) {
-            const int at = units % kQueue, ob = units % K::OBUF;
-            if (!wait_warp(&sh->unit_full[at], (units / kQueue) & 1, waits)) break;
-            const TcUnit u = sh->unit[at];
-            arrive_warp(&sh->unit_empty[at]);
-            if (u.s < 0) break;
-            const int end = u.L + u.T;
-            uint32_t *const bad = sh->bad[units & 1];
-            if (r < 4) bad[r] = 0;
+        TcUnit u;
+        for (int units = 0; ok && (ok = pop(u, units)) && u.s >= 0; ++units) {
+            const int ob = units % K::OBUF, b = units & 1;
             if (u.s != s_before) {
-                // ancestors, and a look at every page and parent of the sequence
-                s_before = u.s;
-                if (r == 0) sh->flags = 0;
-                const int *parent = p.parent ? p.parent + (p.cu ? (long long)u.row0 : (long long)u.s * p.T) : nullptr;
-                int st = attn_ancestors(parent, u.T, r, &sh->tree, sh->see, [&] { ok = ok && meet(); }) ? kSeqBadTree : 0;
-                if (!ok) break;
-                const int *const table = p.c.table + (long long)u.slot * p.c.table_row;
-                for (int i = r; i <= (end - 1) / p.c.page; i += 128) {
-                    const int g = __ldg(table + i);
-                    if (g < 0 || g >= p.c.n_pages) st |= kSeqBadPage;
-                }
-                if (st) {
-                    if (p.err) atomicOr(p.err + u.s, st);
-                    atomicOr(&sh->flags, st);
-                }
+                if (seqs > 0) arrive_warp(&sh->see_empty[(seqs - 1) & 1]);
+                s_before = u.s, ++seqs;
             }
-            if (!(ok = meet())) break;
-            const bool bad_unit = sh->flags != 0;
+            // the unit two before has left its place
+            if (units >= 2 && !(ok = wait_warp(&sh->ml_free[b], ((units >> 1) - 1) & 1, waits))) break;
+            if (lane < 4) sh->bad[b][warp][lane] = 0;
+            __syncwarp();
+            const int end = u.L + u.T;
             const bool active = 32 * warp < u.rows;
-            see = sh->see[min((u.row + r) / p.G, 127)];
             float m = kNone, l = 0.f;
-            bool looked = false;
+            bool sees = false;
             for (int tile = u.tile; tile < u.last; ++tile, ++it) {
                 const int j0 = tile * KT, ahead = j0 + KT - u.L;  // keys of the tile that are no cached tokens
                 if (ahead > 0) {
+                    if (!sees) {
+                        if (!(ok = wait_warp(&sh->see_full[(seqs - 1) & 1], ((seqs - 1) >> 1) & 1, waits))) break;
+                        see = sh->see[(seqs - 1) & 1][min((u.row + r) / p.G, 127)];
+                        sees = true;
+                    }
                     // rows of V past the end, and drafts' that are not finite
-                    looked = true;
-                    const int pos = it + 1 < total ? 2 * it + 2 : 2 * it + 1, stage = pos % STAGES;
-                    if (!(ok = wait_warp(&sh->kv_full[stage], (pos / STAGES) & 1, waits))) break;
+                    const int stage = it % VS;
+                    if (!(ok = wait_warp(&sh->v_full[stage], (it / VS) & 1, waits))) break;
                     const int j = j0 + r;
                     if (r < KT && j >= u.L) {
-                        unsigned char *const row = kv_tile + stage * K::KV + r * 128;
+                        unsigned char *const row = v_tile + stage * K::KV + r * 128;
                         bool clear = j >= end;
                         if (!clear) {
 #pragma unroll 4
                             for (int x = 0; x < DP / 8; ++x)
                                 clear |= not_finite(*reinterpret_cast<const uint4 *>(row + (x >> 3) * (KT * 128) + (x & 7) * 16));
-                            if (clear) atomicOr(&bad[(j - u.L) >> 5], 1u << ((j - u.L) & 31));
+                            if (clear) atomicOr(&sh->bad[b][warp][(j - u.L) >> 5], 1u << ((j - u.L) & 31));
                         }
                         if (clear)
 #pragma unroll 4
@@ -509,13 +557,39 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc(const __grid_constant__
                 }
                 arrive_warp(&sh->p_ready[it & 1]);
             }
-            if (!ok || !(ok = wait_warp(&sh->pv_done, (it - 1) & 1, waits))) break;
+            if (!ok) break;
+            sh->m[b][r] = m, sh->l[b][r] = l;
+            arrive_warp(&sh->ml_full[b]);
+        }
+    } else {
+        // ---------------------------------------------------------------------------- output
+        const int w4 = warp - 8, r = 32 * w4 + lane;  // the row
+        const uint32_t tl = tm + ((uint32_t)(32 * w4) << 16);
+        int s_before = -1, seqs = 0;
+        bool ok = true, goes_on = false, came = false;  // parts left in slots 1 and 0
+        TcUnit u;
+        for (int units = 0; ok && (ok = pop(u, units)) && u.s >= 0; ++units) {
+            const int ob = units % K::OBUF, b = units & 1;
+            if (u.s != s_before) {
+                if (seqs > 0) arrive_warp(&sh->see_empty[(seqs - 1) & 1]);
+                s_before = u.s, ++seqs;
+            }
+            if (!(ok = wait_warp(&sh->see_full[(seqs - 1) & 1], ((seqs - 1) >> 1) & 1, waits)) ||
+                !(ok = wait_warp(&sh->ml_full[b], (units >> 1) & 1, waits)) ||
+                !(ok = wait_warp(&sh->o_full[ob], (units / K::OBUF) & 1, waits)))
+                break;
             tmem_fence_after();
+            const bool bad_unit = sh->flags[(seqs - 1) & 1] != 0, cut = u.last - u.tile < u.tiles;
+            const float m = sh->m[b][r], l = sh->l[b][r];
             const uint32_t to = tl + K::COL_O + ob * DP;
-            const bool cut = u.last - u.tile < u.tiles;
-            if (looked && !(ok = meet())) break;  // (all notes of drafts are there)
-            if (active && !bad_unit) {
-                if (looked && (bad[0] | bad[1] | bad[2] | bad[3])) add_bad_drafts<DP>(p, u, bad, see, r, m, to);
+            goes_on = cut && u.begins && !bad_unit;
+            came |= cut && !u.begins && !bad_unit;
+            if (32 * w4 < u.rows && !bad_unit) {
+                uint32_t bad[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) bad[i] = sh->bad[b][0][i] | sh->bad[b][1][i] | sh->bad[b][2][i] | sh->bad[b][3][i];
+                if (bad[0] | bad[1] | bad[2] | bad[3])
+                    add_bad_drafts<DP>(p, u, bad, sh->see[(seqs - 1) & 1][min((u.row + r) / p.G, 127)], r, m, to);
                 const float inv = cut ? 1.0f : 1.0f / l;
                 float *const part = cut ? attn_part(p, blockIdx.x, u.begins) : nullptr;
                 if (cut && r < u.rows) part[kPartHead + r] = m, part[kPartHead + p.pad + r] = l;
@@ -555,29 +629,29 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc(const __grid_constant__
                     __syncwarp();
                 }
             }
-            if (cut && r == 0) {
-                int *const head = reinterpret_cast<int *>(attn_part(p, blockIdx.x, u.begins));
-                head[0] = u.begins && !bad_unit, head[1] = (int)((u.first + u.tiles - 1) / range.per) - (int)blockIdx.x + 1;
-                head[2] = u.s, head[3] = u.h, head[4] = u.row, head[5] = 1;
-            }
-            if (r == 0 && p.ws && !(cut && u.begins)) *reinterpret_cast<int *>(attn_part(p, blockIdx.x, 1)) = 0;
+            if (cut && !bad_unit && r == 0)
+                attn_part_head(attn_part(p, blockIdx.x, u.begins), range, u.first, u.tiles, u.rows, u.row, u.s, u.h, u.row0);
             tmem_fence_before();
             arrive_warp(&sh->o_free[ob]);
+            arrive_warp(&sh->ml_free[b]);
         }
+        // the join reads both slots of every block
+        if (p.ws && r == 0 && !goes_on) *reinterpret_cast<int *>(attn_part(p, blockIdx.x, 1)) = 0;
+        if (p.ws && r == 0 && !came) *reinterpret_cast<int *>(attn_part(p, blockIdx.x, 0)) = 0;
     }
     __syncwarp();
     tmem_wait_st();  // (of a role that gave up)
     tmem_fence_before();
     __syncthreads();
-    if (tid == 0) {
-        if (sh->dead) {
-            AttnWalk walk(p, range);
-            AttnUnit u;
-            while (walk.next(p, u))
-                if (p.err) atomicOr(p.err + u.s, kSeqTimeout);
-            if (p.ws) reinterpret_cast<int *>(attn_part(p, blockIdx.x, 0))[5] = 0;
+    if (tid == 0 && sh->dead) {
+        AttnWalk walk(p, range);
+        AttnUnit u;
+        while (walk.next(p, u))
+            if (p.err) atomicOr(p.err + u.s, kSeqTimeout);
+        if (p.ws) {
+            *reinterpret_cast<int *>(attn_part(p, blockIdx.x, 0)) = 0;
+            *reinterpret_cast<int *>(attn_part(p, blockIdx.x, 1)) = 0;
         }
-        if (p.ws && (sh->dead || total == 0)) *reinterpret_cast<int *>(attn_part(p, blockIdx.x, 1)) = 0;
     }
     if (warp == 5) {
         tmem_fence_after();
