@@ -302,18 +302,31 @@ int launch_rope(const cv_qk_norm_rope_args *a, cudaStream_t stream) {
                      rows(p.k_out, p.ko_seq, p.ko_tok, p.ko_head) && rows(p.v, p.v_seq, p.v_tok, p.v_head) &&
                      aligned16(p.wq) && aligned16(p.wk) && aligned16(p.cs) && p.cs_row % 4 == 0 &&
                      (!paged || (rows(p.c.k, p.c.k_page, p.c.k_row, p.c.k_head) && rows(p.c.v, p.c.v_page, p.c.v_row, p.c.v_head)));
-    p.lanes = 1;
-    while (p.lanes * 16 < a->head_dim) p.lanes *= 2;
-    // enough tokens a block for all its threads, fewer while that leaves SMs without one
-    p.block_tokens = cvk::kRopeTokens;
-    while (p.block_tokens > 1 && (p.tokens + p.block_tokens - 1) / p.block_tokens < 4LL * device_limits().sms) p.block_tokens /= 2;
-    const long long blocks = (p.tokens + p.block_tokens - 1) / p.block_tokens;
+    const long long sms = device_limits().sms;
+    long long blocks;
+    if (vec) {
+        p.lanes = 1;
+        while (p.lanes * 16 < a->head_dim) p.lanes *= 2;
+        // Groups that share a token's heads: as many as are resident at once (2 blocks an SM), at most one a head (1024
+        // tokens of 20 heads: 12.3 us with 4, 14 with 1, 20 with 16); one where the tokens alone are as many (30,822 tokens: 143 us,
+        // with 4 groups a token 168).
+        const long long per = cvk::kRopeThreads / p.lanes, heads = p.n_heads + p.n_kv + (p.v ? p.n_kv : 0);
+        const long long fit = 2 * sms * per / p.tokens, most = fit > 1 ? fit : 1;
+        p.groups = (int)(most < heads ? most : heads);
+        blocks = (p.tokens * p.groups + per - 1) / per;
+    } else {
+        // enough tokens a block for all its threads, fewer while that leaves SMs without one
+        p.block_tokens = cvk::kRopeTokens;
+        while (p.block_tokens > 1 && (p.tokens + p.block_tokens - 1) / p.block_tokens < 4 * sms) p.block_tokens /= 2;
+        blocks = (p.tokens + p.block_tokens - 1) / p.block_tokens;
+    }
     if (blocks > 0x7fffffff) return CV_ERR_SHAPE;
     const int rc = clear_err(a->err, a->n_seq, stream);
     if (rc != CV_OK) return rc;
-    if (launch_pdl(cvk::rope_kernel(a->dtype == CV_BF16, vec), dim3((unsigned)blocks), dim3(cvk::kRopeThreads), 0, stream, p) !=
-        cudaSuccess)
-        return CV_ERR_LAUNCH;
+    const auto k = cvk::rope_kernel(a->dtype == CV_BF16, vec);
+    const int smem = vec ? cvk::rope_smem(a->dtype == CV_BF16) : 0;
+    if (cvk::ensure_smem(reinterpret_cast<const void *>(k), smem) != cudaSuccess) return CV_ERR_LAUNCH;
+    if (launch_pdl(k, dim3((unsigned)blocks), dim3(cvk::kRopeThreads), smem, stream, p) != cudaSuccess) return CV_ERR_LAUNCH;
     return cudaGetLastError() == cudaSuccess ? CV_OK : CV_ERR_LAUNCH;
 }
 
@@ -327,12 +340,18 @@ int copy_bytes(const cv_cache &c) {
                : esize_of(c.dtype);
 }
 
+// Pieces of one position's rows in all layers' K and V.
+int64_t copy_pieces(const cv_cache &c) {
+    return 2LL * c.n_layers * c.n_kv_heads * (c.head_dim * esize_of(c.dtype) / copy_bytes(c));
+}
+
 int check_compact(const cv_cache_compact_args *a) {
     if (!a) return CV_ERR_NULL_ARGS;
     if (a->n_seq < 0 || a->n_seq > 65535) return CV_ERR_SHAPE;
     if (a->T < 1 || a->T > CV_MAX_T) return CV_ERR_TOKENS;
     const int rc = check_cache(a->cache, a->n_seq > 0, false);
     if (rc != CV_OK || a->n_seq == 0) return rc;
+    if (copy_pieces(a->cache) > 0x7fffffff) return CV_ERR_SHAPE;
     if (!a->cache_len || !a->path || !a->accept_len) return CV_ERR_NULL_POINTER;
     if (a->cache.k == a->cache.v) return CV_ERR_ALIAS;
     const void *outs[] = {a->new_len, a->err};
@@ -348,6 +367,7 @@ int check_pages(const cv_cache_pages_args *a, bool fork, bool needs_tokens) {
     if (a->n_seq < 0 || a->n_seq > cvk::kMaxPageSeqs) return CV_ERR_SHAPE;
     const int rc = check_cache(a->cache, a->n_seq > 0, true);
     if (rc != CV_OK || a->n_seq == 0) return rc;
+    if (fork && copy_pieces(a->cache) > 0x7fffffff) return CV_ERR_SHAPE;
     if ((needs_tokens && !a->n_tokens) || (fork && !a->src_idx)) return CV_ERR_NULL_POINTER;
     if (fork && a->cache.k == a->cache.v) return CV_ERR_ALIAS;
     const void *outs[] = {a->err, a->cache.page_table, a->cache.held, a->cache.refs};
@@ -373,7 +393,7 @@ cvk::PagesParams pages_params(const cv_cache_pages_args *a, int op) {
 int launch_take(const cvk::PagesParams &p, cudaStream_t stream) {
     const int smem = cvk::pages_take_smem(p.n_seq);
     const auto k = cvk::pages_take_kernel();
-    if (cvk::ensure_smem(reinterpret_cast<const void *>(k), smem + 1024) != cudaSuccess) return CV_ERR_LAUNCH;
+    if (cvk::ensure_smem(reinterpret_cast<const void *>(k), smem) != cudaSuccess) return CV_ERR_LAUNCH;
     return launch_pdl(k, dim3(1), dim3(cvk::kTakeThreads), smem, stream, p) == cudaSuccess ? CV_OK : CV_ERR_LAUNCH;
 }
 
@@ -409,15 +429,19 @@ int cv_draft_verify(const cv_draft_verify_args *args, void *stream) {
     const int rc = check_sample(args);
     if (rc != CV_OK) return rc;
     if (args->n_seq == 0) return CV_OK;
-    cvk::SampleParams p{args->n_seq, args->T, args->vocab, args->total_tokens, args->probs, args->draft_probs,
+    // blocks a sequence: as many as are resident at once (115 sequences of 128,000 tokens: 38 us in 4 blocks each, 43 in 8, 52 in 2)
+    int cluster = cvk::kSampleCluster;
+    while (cluster > 1 && (int64_t)args->n_seq * cluster > (int64_t)cvk::kSampleBlocks * device_limits().sms) cluster /= 2;
+    cvk::SampleParams p{args->n_seq, args->T, args->vocab, args->total_tokens, cluster, args->probs, args->draft_probs,
                         args->probs_seq_stride, args->probs_tok_stride, args->draft_seq_stride, args->draft_tok_stride,
                         args->tokens, args->parent, args->uniforms, args->cu_draft, args->cache_idx, args->accept_len,
                         args->accept_node, args->path, args->out_tokens, args->err};
     cudaStream_t on = reinterpret_cast<cudaStream_t>(stream);
     const int clear = clear_err(args->err, args->n_seq, on);
     if (clear != CV_OK) return clear;
-    if (launch_pdl(cvk::sample_kernel(args->dtype == CV_BF16), dim3((unsigned)args->n_seq * cvk::kSampleCluster),
-                   dim3(cvk::kSampleThreads), 0, on, p) != cudaSuccess)
+    const auto k = cvk::sample_kernel(args->dtype == CV_BF16);
+    if (cvk::launch_pdl_cluster(k, dim3((unsigned)(args->n_seq * cluster)),
+                                dim3(cvk::kSampleThreads), cluster, on, p) != cudaSuccess)
         return CV_ERR_LAUNCH;
     return done();
 }
@@ -441,11 +465,11 @@ int cv_cache_compact(const cv_cache_compact_args *args, void *stream) {
     p.new_len = args->new_len, p.err = args->err;
     const int bytes = copy_bytes(args->cache);
     p.esize = esize_of(args->cache.dtype), p.chunks = args->cache.head_dim * p.esize / bytes;
-    // a piece a thread, fewer blocks where the sequences alone fill the GPU
-    const int64_t items = 2LL * p.c.n_layers * p.c.n_kv * p.chunks;
+    // a piece a thread, but no more blocks than are resident (4 an SM): a block's start costs as much as several pieces
+    const int64_t items = copy_pieces(args->cache);
     int64_t blocks = (items + cvk::kPagesThreads - 1) / cvk::kPagesThreads;
-    const int64_t most = 16LL * device_limits().sms * 8 / args->n_seq + 1;
-    if (blocks > most) blocks = most;
+    const int64_t most = 4LL * device_limits().sms / args->n_seq;
+    if (blocks > most) blocks = most > 1 ? most : 1;
     if (launch_pdl(cvk::pages_compact_kernel(bytes), dim3((unsigned)blocks, (unsigned)args->n_seq), dim3(cvk::kPagesThreads), 0,
                    reinterpret_cast<cudaStream_t>(stream), p) != cudaSuccess)
         return CV_ERR_LAUNCH;

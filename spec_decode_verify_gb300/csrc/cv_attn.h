@@ -65,7 +65,7 @@ constexpr int kAttnJoinThreads = 256, kAttnJoinY = 4;
 
 // ---- draft verification
 struct SampleParams {
-    int n_seq, T, vocab, total;
+    int n_seq, T, vocab, total, cluster;  // cluster: blocks a sequence
     const void *p, *q;
     long long p_seq, p_tok, q_seq, q_tok;
     const int *tok, *parent;
@@ -74,7 +74,7 @@ struct SampleParams {
     int *accept, *node, *path, *out, *err;
 };
 using SampleKernel = void (*)(SampleParams);
-constexpr int kSampleThreads = 512, kSampleCluster = 8;
+constexpr int kSampleThreads = 384, kSampleBlocks = 4, kSampleCluster = 8;  // threads, blocks an SM, blocks a sequence at most
 SampleKernel sample_kernel(bool bf16);
 
 // ---- query and key norms with the rotation
@@ -91,11 +91,13 @@ struct RopeParams {
     int *err;
     CacheView c;
     int paged;
-    int lanes, block_tokens;
+    int lanes, groups;     // norm_rope: lanes of a group, groups that share a token's heads
+    int block_tokens;      // norm_rope_any
 };
 using RopeKernel = void (*)(RopeParams);
 constexpr int kRopeThreads = 256, kRopeTokens = 16;
 RopeKernel rope_kernel(bool bf16, bool vec);
+int rope_smem(bool bf16);  // of the kernel for 16-byte pieces
 
 // ---- the cache's pages
 struct PagesParams {

@@ -69,6 +69,26 @@ cudaError_t launch_pdl(void (*kernel)(P), dim3 grid, dim3 block, int smem, cudaS
     return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
+// The same in clusters of `cluster` blocks.
+template <typename P>
+cudaError_t launch_pdl_cluster(void (*kernel)(P), dim3 grid, dim3 block, int cluster, cudaStream_t stream, const P &p) {
+    cudaLaunchConfig_t cfg;
+    std::memset(&cfg, 0, sizeof cfg);
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    std::memset(attr, 0, sizeof attr);
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
 // Opt a kernel into more than 48 KB of dynamic shared memory (once per kernel and device).
 inline cudaError_t ensure_smem(const void *kernel, int bytes) {
     if (bytes <= 48 * 1024) return cudaSuccess;

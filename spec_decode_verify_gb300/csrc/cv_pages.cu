@@ -3,7 +3,7 @@
 //
 // A page is free while its reference count is 0, and the free pages with the lowest numbers are given out in the order of the
 // call's sequences; so the only state is the table, the counts and the slots' numbers of pages, and results do not depend
-// on the order in which threads come.  One block finds the free pages (16 counts a thread at a time, a scan over the
+// on the order in which threads come.  One block finds the free pages (8 counts a thread at a time, a scan over the
 // block), since their order is one of all pages: 70,000 counts are 280 KB, and it stops once it has enough.  Sharing
 // and copying take a cluster a sequence, releasing a block a sequence, compacting one for each part of the layers.
 #include "cv_attn.cuh"
@@ -37,13 +37,13 @@ __device__ __forceinline__ long long block_scan(long long v, long long &before, 
     return __shfl_sync(0xffffffffu, sums, 31);
 }
 
-constexpr int kScanEach = 16;
+constexpr int kScanEach = 8, kScanPages = kTakeThreads * kScanEach;  // counts a thread, and the block, looks at in one go
 
 __global__ void __launch_bounds__(kTakeThreads) pages_take(const __grid_constant__ PagesParams p) {
     extern __shared__ __align__(8) long long smem[];
-    __shared__ long long scratch[32];
-    long long *const pre = smem;  // pages of the sequences before
-    int *const slots = reinterpret_cast<int *>(smem + p.n_seq), *const flagged = slots + p.n_seq;
+    long long *const scratch = smem, *const pre = smem + 32;  // pre: pages of the sequences before
+    int *const slots = reinterpret_cast<int *>(pre + p.n_seq), *const flagged = slots + p.n_seq, *const first = flagged + p.n_seq,
+        *const src = first + p.n_seq, *const list = src + p.n_seq;  // list: free pages in order
     grid_dep_wait();
     grid_dep_launch();
     const int tid = threadIdx.x;
@@ -51,35 +51,38 @@ __global__ void __launch_bounds__(kTakeThreads) pages_take(const __grid_constant
     const CacheView &c = p.c;
     for (int i = tid; i < p.n_seq; i += kTakeThreads) {
         int slot = p.idx ? __ldg(p.idx + i) : i;
-        if (fork && __ldg(p.src + i) < 0) slot = -1;
-        slots[i] = slot;
+        const int from = fork ? __ldg(p.src + i) : 0;
+        if (from < 0) slot = -1;
+        slots[i] = slot, src[i] = slot < 0 ? -1 : from;
     }
     __syncthreads();
     // Pages each sequence needs; -1 - bits where it is flagged.
     auto needs = [&](int i) {
         const int slot = slots[i];
+        first[i] = 0;
         if (slot < 0) return 0;
         if (slot >= c.n_slots) return -1 - kSeqBadSlot;
+        const int n = __ldg(p.n_tok + i), held = c.held[slot];
         int st = 0, need = 0;
         if (p.idx)
-            for (int j = 0; j < i; ++j)
-                if (slots[j] == slot) st = kSeqBadSlot;
-        const int n = __ldg(p.n_tok + i), held = c.held[slot];
+#pragma unroll 8
+            for (int j = 0; j < i; ++j) st |= slots[j] == slot;
         if (fork) {
-            const int src = __ldg(p.src + i);
-            for (int j = 0; j < p.n_seq; ++j)
-                if (slots[j] >= 0 && __ldg(p.src + j) == slot) st = kSeqBadSlot;
-            if (src >= c.n_slots || held != 0) st = kSeqBadSlot;
+#pragma unroll 8
+            for (int j = 0; j < p.n_seq; ++j) st |= src[j] == slot;
+            if (src[i] >= c.n_slots || held != 0) st = 1;
             if (!st) {
-                const int have = c.held[src];
-                if (n < 0 || have < 0 || have > c.max_pages || n > (long long)have * c.page) st = kSeqBadLength;
+                const int have = c.held[src[i]];
+                if (n < 0 || have < 0 || have > c.max_pages || n > (long long)have * c.page) return -1 - kSeqBadLength;
             }
             need = n % c.page != 0;
+            first[i] = n / c.page;
         } else {
-            if (!st && (n < 0 || n > (long long)c.max_pages * c.page || held < 0 || held > c.max_pages)) st = kSeqBadLength;
+            if (!st && (n < 0 || n > (long long)c.max_pages * c.page || held < 0 || held > c.max_pages)) return -1 - kSeqBadLength;
             need = max(0, pages_for(n, c.page) - held);
+            first[i] = held;
         }
-        return st ? -1 - st : need;
+        return st ? -1 - kSeqBadSlot : need;
     };
     long long total = 0;
     for (int base = 0; base < p.n_seq; base += kTakeThreads) {
@@ -95,50 +98,74 @@ __global__ void __launch_bounds__(kTakeThreads) pages_take(const __grid_constant
         total += sum;
     }
     __syncthreads();
-    // The free pages in order, as far as the first `limit` of them; to the sequences, or counted only.
-    auto scan = [&](long long limit, bool give) {
-        long long found = 0;
-        for (long long base = 0; base < c.n_pages && found < limit; base += kTakeThreads * kScanEach) {
-            const long long at = base + (long long)tid * kScanEach;
-            uint32_t free = 0;
+    auto ends = [&](int i) { return i + 1 < p.n_seq ? pre[i + 1] : total; };
+    // The free pages among counts [base, base + kScanPages) into the list; how many.
+    const bool wide = reinterpret_cast<uintptr_t>(c.refs) % 16 == 0;
+    auto gather = [&](long long base, bool keep) {
+        const long long at = base + (long long)tid * kScanEach;
+        uint32_t free = 0;
+        if (wide && at + kScanEach <= c.n_pages) {
+#pragma unroll
+            for (int x = 0; x < kScanEach; x += 4) {
+                const int4 r = *reinterpret_cast<const int4 *>(c.refs + at + x);
+                free |= (r.x == 0 ? 1u : 0u) << x | (r.y == 0 ? 2u : 0u) << x | (r.z == 0 ? 4u : 0u) << x | (r.w == 0 ? 8u : 0u) << x;
+            }
+        } else {
 #pragma unroll
             for (int x = 0; x < kScanEach; ++x)
                 if (at + x < c.n_pages && c.refs[at + x] == 0) free |= 1u << x;
-            long long before;
-            const long long sum = block_scan(__popc(free), before, scratch);
-            if (give) {
-                long long rank = found + before;
-                for (; free && rank < limit; free &= free - 1, ++rank) {
-                    const int page = (int)at + __ffs(free) - 1;
-                    int lo = 0, hi = p.n_seq - 1;  // the last sequence whose pages begin at or before this one
-                    while (lo < hi) {
-                        const int mid = (lo + hi + 1) >> 1;
-                        if (pre[mid] <= rank) lo = mid;
-                        else hi = mid - 1;
-                    }
-                    const int slot = slots[lo], first = fork ? __ldg(p.n_tok + lo) / c.page : c.held[slot];
-                    c.table[(long long)slot * c.table_row + first + rank - pre[lo]] = page;
-                    c.refs[page] = 1;
-                }
-            }
-            found += sum;
         }
-        return found;
+        long long before;
+        const int sum = (int)block_scan(__popc(free), before, scratch);
+        if (keep)
+            for (int rank = (int)before; free; free &= free - 1, ++rank) list[rank] = (int)at + __ffs(free) - 1;
+        __syncthreads();
+        return sum;
     };
-    // Which are served: those whose pages end within what there is (a sequence's need is the difference of two sums).
-    const long long found = total > 0 ? min(scan(total, false), total) : 0;
-    auto ends = [&](int i) { return i + 1 < p.n_seq ? pre[i + 1] : total; };
-    long long limit = 0;
-    for (int i = tid; i < p.n_seq; i += kTakeThreads)
-        if (ends(i) <= found) limit = max(limit, ends(i));
+    // Pages `found` .. of those there are, in the list, to the sequences, as far as `limit`.
+    auto give = [&](long long found, int n, long long limit) {
+        for (int k = tid; k < n && found + k < limit; k += kTakeThreads) {
+            const long long rank = found + k;
+            int lo = 0, hi = p.n_seq - 1;  // the last sequence whose pages begin at or before this one
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (pre[mid] <= rank) lo = mid;
+                else hi = mid - 1;
+            }
+            c.table[(long long)slots[lo] * c.table_row + first[lo] + (rank - pre[lo])] = list[k];
+            c.refs[list[k]] = 1;
+        }
+        __syncthreads();
+    };
+    long long found = 0;  // free pages, as far as they are needed
+    if (total > 0) {
+        const int n = gather(0, true);
+        if (n >= total) {
+            found = total;
+            give(0, n, total);
+        } else {
+            // first count, since a sequence gets all of its pages or none: those are served whose pages end within what there is
+            found = n;
+            for (long long base = kScanPages; base < c.n_pages && found < total; base += kScanPages) found += gather(base, false);
+            found = min(found, total);
+            long long limit = 0;
+            for (int i = tid; i < p.n_seq; i += kTakeThreads)
+                if (ends(i) <= found) limit = max(limit, ends(i));
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) limit = max(limit, __shfl_xor_sync(0xffffffffu, limit, o));
-    __syncthreads();
-    if ((tid & 31) == 0) scratch[tid >> 5] = limit;
-    __syncthreads();
-    for (int w = 0; w < 32; ++w) limit = max(limit, scratch[w]);
-    if (limit > 0) scan(limit, true);
-    __syncthreads();
+            for (int o = 16; o > 0; o >>= 1) limit = max(limit, __shfl_xor_sync(0xffffffffu, limit, o));
+            __syncthreads();
+            if ((tid & 31) == 0) scratch[tid >> 5] = limit;
+            __syncthreads();
+            for (int w = 0; w < 32; ++w) limit = max(limit, scratch[w]);
+            __syncthreads();
+            long long given = 0;
+            for (long long base = 0; given < limit && base < c.n_pages; base += kScanPages) {
+                const int m = gather(base, true);
+                give(given, m, limit);
+                given += m;
+            }
+        }
+    }
     for (int i = tid; i < p.n_seq; i += kTakeThreads) {
         const int slot = slots[i];
         if (slot < 0 || flagged[i]) continue;
@@ -148,7 +175,7 @@ __global__ void __launch_bounds__(kTakeThreads) pages_take(const __grid_constant
         } else if (fork) {
             c.held[slot] = -1 - i;  // until the next kernel has shared and copied: this sequence, and no other, is on
         } else if (need > 0) {
-            c.held[slot] += (int)need;
+            c.held[slot] = first[i] + (int)need;
         }
     }
 }
@@ -169,21 +196,18 @@ template <int BYTES>
 struct CopyItem {
     typename Piece<BYTES>::T *base;
     long long page, row;
-    __device__ __forceinline__ CopyItem(const PagesParams &p, long long item) {
+    __device__ __forceinline__ CopyItem(const PagesParams &p, unsigned item) {
         const CacheView &c = p.c;
-        const int piece = (int)(item % p.chunks);
-        item /= p.chunks;
-        const int h = (int)(item % c.n_kv);
-        item /= c.n_kv;
-        const bool v = item & 1;
-        const long long layer = item >> 1;
-        const int per = BYTES / p.esize;
-        page = (v ? c.v_page : c.k_page) / per, row = (v ? c.v_row : c.k_row) / per;
+        const unsigned row_ = item / (unsigned)p.chunks, piece = item - row_ * p.chunks, lw = row_ / (unsigned)c.n_kv, h = row_ - lw * c.n_kv;
+        const bool v = lw & 1;
+        const long long layer = lw >> 1;
+        const int per = BYTES / p.esize, by = per == 8 ? 3 : per == 4 ? 2 : 0;
+        page = (v ? c.v_page : c.k_page) >> by, row = (v ? c.v_row : c.k_row) >> by;
         base = reinterpret_cast<typename Piece<BYTES>::T *>(v ? c.v : c.k) +
-               (layer * (v ? c.v_layer : c.k_layer) + (long long)h * (v ? c.v_head : c.k_head)) / per + piece;
+               ((layer * (v ? c.v_layer : c.k_layer) + (long long)h * (v ? c.v_head : c.k_head)) >> by) + piece;
     }
 };
-__device__ __forceinline__ long long copy_items(const PagesParams &p) { return 2LL * p.c.n_layers * p.c.n_kv * p.chunks; }
+__device__ __forceinline__ unsigned copy_items(const PagesParams &p) { return 2u * p.c.n_layers * p.c.n_kv * p.chunks; }
 
 
 
@@ -230,12 +254,19 @@ __global__ void __cluster_dims__(kForkCluster, 1, 1) __launch_bounds__(kPagesThr
     }
     if (!rest) return;
     const int old_page = from[full];
-    const long long items = copy_items(p) * rest;
-    for (long long x = (long long)rank * kPagesThreads + tid; x < items; x += kForkCluster * kPagesThreads) {
-        // the rows of a page innermost but for a row's own pieces
-        const long long row = x / p.chunks % rest, piece = x % p.chunks, head = x / p.chunks / rest;
-        const CopyItem<BYTES> m(p, head * p.chunks + piece);
-        m.base[new_page * m.page + row * m.row] = m.base[old_page * m.page + row * m.row];
+    // a piece of a head in one row of a layer is an item; a thread takes 4 of its rows at a time
+    const unsigned items = copy_items(p);
+    const int quarters = (rest + 3) / 4;
+    for (unsigned long long x = rank * kPagesThreads + tid; x < (unsigned long long)items * quarters; x += kForkCluster * kPagesThreads) {
+        const unsigned q = (unsigned)(x / items), item = (unsigned)(x - (unsigned long long)q * items);
+        const CopyItem<BYTES> m(p, item);
+        typename Piece<BYTES>::T w[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            if ((int)(4 * q) + r < rest) w[r] = m.base[old_page * m.page + (4 * q + r) * m.row];
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            if ((int)(4 * q) + r < rest) m.base[new_page * m.page + (4 * q + r) * m.row] = w[r];
     }
 }
 
@@ -325,8 +356,8 @@ __global__ void __launch_bounds__(kPagesThreads) pages_compact(const __grid_cons
     if (all) return;
     if (head && p.new_len) p.new_len[s] = L + a;
     const int from = first;  // a rising path that has left its place stays ahead of it
-    const long long items = copy_items(p);
-    for (long long x = (long long)blockIdx.x * kPagesThreads + tid; x < items; x += (long long)gridDim.x * kPagesThreads) {
+    const unsigned items = copy_items(p);
+    for (unsigned x = blockIdx.x * kPagesThreads + tid; x < items; x += gridDim.x * kPagesThreads) {
         const CopyItem<BYTES> m(p, x);
         for (int r0 = from; r0 < a; r0 += kMoveRows) {
             typename Piece<BYTES>::T w[kMoveRows];
@@ -343,7 +374,7 @@ __global__ void __launch_bounds__(kPagesThreads) pages_compact(const __grid_cons
 }  // namespace
 
 PagesKernel pages_take_kernel() { return pages_take; }
-int pages_take_smem(int n_seq) { return n_seq * 16; }
+int pages_take_smem(int n_seq) { return 256 + n_seq * 24 + kScanPages * 4; }
 PagesKernel pages_fork_kernel(int bytes) { return bytes == 16 ? pages_fork<16> : bytes == 4 ? pages_fork<4> : pages_fork<2>; }
 PagesKernel pages_free_kernel() { return pages_free; }
 PagesKernel pages_compact_kernel(int bytes) {

@@ -2,54 +2,39 @@
 //
 // A head's row goes through registers once: read, its mean square over the lanes that share it, scale, rotate, round,
 // write.  A lane owns two pieces of 8 channels chosen so that both partners of a rotated pair are its own: piece i
-// of each half of the rotated channels, or neighbours where pairs are neighbours.  HBM bounds it; nothing is read twice but the
-// angles, which all heads of a token share in L1.
+// of each half of the rotated channels, or neighbours where pairs are neighbours.  A group of lanes takes one token and
+// every so many of its heads, so that the token's angles and the weights are loaded once.  HBM bounds it: nothing is read twice.
 #include "cv_attn.cuh"
 
 namespace cvk {
 namespace {
+
+// Heads that a thread of norm_rope has on their way.
+template <typename B>
+__host__ __device__ constexpr int rope_ring() { return sizeof(B) == 2 ? 8 : 4; }
 
 struct TokenAt {
     long long q, qo, k, ko, v, kc, vc;  // offsets of the token's rows; kc, vc: in the cache
     int pos, on;                        // on: 0 = left out
 };
 
+// 8 channels as they lie in memory.
 template <typename B>
-__device__ __forceinline__ void load8(float *f, const B *p) {
-    if (sizeof(B) == 2) {
-        const uint4 w = ld16(p);
-        const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+struct Raw8 {
+    uint4 w[sizeof(B) / 2];
+};
+template <typename B>
+__device__ __forceinline__ Raw8<B> load8(const B *p) {
+    Raw8<B> r;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = elem_f<B>(x, i);
-    } else {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const float4 w = *reinterpret_cast<const float4 *>(p + 4 * h);
-            f[4 * h] = w.x, f[4 * h + 1] = w.y, f[4 * h + 2] = w.z, f[4 * h + 3] = w.w;
-        }
-    }
+    for (int h = 0; h < (int)sizeof(B) / 2; ++h) r.w[h] = ld16(p + 8 / (sizeof(B) / 2) * h);
+    return r;
 }
 template <typename B>
-__device__ __forceinline__ void store8(B *p, const float *f) {
-    if (sizeof(B) == 2) {
-        uint32_t w[4];
+__device__ __forceinline__ void store8(B *p, const Raw8<B> &r) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = pack_halves(narrow<uint16_t>(f[2 * i]), narrow<uint16_t>(f[2 * i + 1]));
-        st16(p, make_uint4(w[0], w[1], w[2], w[3]));
-    } else {
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-            *reinterpret_cast<float4 *>(p + 4 * h) = make_float4(f[4 * h], f[4 * h + 1], f[4 * h + 2], f[4 * h + 3]);
-    }
+    for (int h = 0; h < (int)sizeof(B) / 2; ++h) st16(p + 8 / (sizeof(B) / 2) * h, r.w[h]);
 }
-
-// 8 channels with their own bits.
-template <typename B>
-__device__ __forceinline__ void copy8(B *to, const B *from) {
-#pragma unroll
-    for (int h = 0; h < (int)sizeof(B) / 2; ++h) st16(to + 4 * h, ld16(from + 4 * h));
-}
-
 // Where token `tok` (of all) reads and writes.
 __device__ __forceinline__ TokenAt token_at(const RopeParams &p, long long tok) {
     TokenAt a;
@@ -137,86 +122,166 @@ __device__ __forceinline__ HeadRow<B> head_row(const RopeParams &p, const TokenA
     return r;
 }
 
-// Rows of 16-byte pieces: p.lanes lanes a head, each two pieces of 8 channels.
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
+}
+// 8 channels as pairs of fp32, and back with one rounding.
 template <typename B>
-__global__ void __launch_bounds__(kRopeThreads) norm_rope(const __grid_constant__ RopeParams p) {
-    __shared__ TokenAt at[kRopeTokens];
+__device__ __forceinline__ void pairs8(f2 *f, const Raw8<B> &r) {
+    const uint32_t *const w = reinterpret_cast<const uint32_t *>(r.w);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = f2_pack(elem_f<B>(w, 2 * i), elem_f<B>(w, 2 * i + 1));
+}
+template <typename B>
+__device__ __forceinline__ Raw8<B> round8(const f2 *f) {
+    Raw8<B> r;
+    uint32_t *const w = reinterpret_cast<uint32_t *>(r.w);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float lo, hi;
+        f2_unpack(f[i], lo, hi);
+        if (sizeof(B) == 2) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(hi), "f"(lo));
+        else w[2 * i] = __float_as_uint(lo), w[2 * i + 1] = __float_as_uint(hi);
+    }
+    return r;
+}
+
+// Rows of 16-byte pieces: p.lanes lanes a group, which takes a token and every p.groups-th of its heads.  A thread's next heads
+// are on their way to places of its own in shared memory (30,822 tokens of 48 heads: 162 us with them in registers, which
+// left 16 warps an SM; 143 so, with products of two channels an instruction).
+template <typename B>
+__global__ void __launch_bounds__(kRopeThreads, 2) norm_rope(const __grid_constant__ RopeParams p) {
+    constexpr int R = rope_ring<B>(), P = 2 * (int)sizeof(B) / 2;  // heads on their way; 16-byte pieces of each
+    extern __shared__ __align__(16) uint4 ring[];
     grid_dep_wait();
     grid_dep_launch();
-    const int tid = threadIdx.x;
-    const long long tok0 = (long long)blockIdx.x * p.block_tokens;
-    const int toks = (int)(p.tokens - tok0 < p.block_tokens ? p.tokens - tok0 : p.block_tokens);
-    if (tid < toks) at[tid] = token_at(p, tok0 + tid);
-    __syncthreads();
-    const int heads = p.n_heads + p.n_kv + (p.v ? p.n_kv : 0);
-    const int i = tid % p.lanes, per = kRopeThreads / p.lanes, half = p.rot / 2;
-    // the channels of this lane's two pieces
+    const int tid = threadIdx.x, i = tid % p.lanes, half = p.rot / 2;
+    const long long group = (long long)blockIdx.x * (kRopeThreads / p.lanes) + tid / p.lanes;
+    const long long tok = group / p.groups;
+    const int part = (int)(group - tok * p.groups);
+    if (tok >= p.tokens) return;
+    const TokenAt at = token_at(p, tok);
+    if (!at.on) return;
+    const unsigned mask = ((1u << p.lanes) - 1) << (tid & 31 & ~(p.lanes - 1));  // this group (16 lanes at most)
+    // the channels of this lane's two pieces of 8; a lane past the last ones reads the first ones, adds nothing and writes nothing
     const bool has = 16 * i < p.d, turned = 16 * i < p.rot;
-    const int c0 = turned && !p.pairs ? 8 * i : 16 * i, c1 = turned && !p.pairs ? half + 8 * i : 16 * i + 8;
-    const int items = toks * heads, rounds = (items + per - 1) / per;
-    for (int n = 0; n < rounds; ++n) {
-        const int item = n * per + tid / p.lanes;
-        const int tk = item / heads;
-        const bool on = item < items && has && at[tk < toks ? tk : 0].on;
-        float x[16];
-        HeadRow<B> r;
-        float sq = 0.f;
-        if (on) {
-            r = head_row<B>(p, at[tk], item - tk * heads);
-            load8<B>(x, r.from + c0);
-            load8<B>(x + 8, r.from + c1);
-#pragma unroll
-            for (int e = 0; e < 16; ++e) sq = fmaf(x[e], x[e], sq);
+    const int c0 = !has ? 0 : turned && !p.pairs ? 8 * i : 16 * i, c1 = !has ? 0 : turned && !p.pairs ? half + 8 * i : 16 * i + 8;
+    // This group's heads are part, part + groups, ... of the queries, keys and values in a row: n_q, n_k and n_v of them.
+    auto upto = [&](int n) { return n > part ? (n - part + p.groups - 1) / p.groups : 0; };
+    const int n_q = upto(p.n_heads), n_k = upto(p.n_heads + p.n_kv) - n_q, n_v = p.v ? upto(p.n_heads + 2 * p.n_kv) - n_q - n_k : 0;
+    const int k0 = part + n_q * p.groups - p.n_heads, v0 = part + (n_q + n_k) * p.groups - p.n_heads - p.n_kv;
+
+    const B *next = reinterpret_cast<const B *>(p.q) + at.q + (long long)part * p.q_head;
+    long long step = p.groups * p.q_head;
+    int left = n_q, stage = 0, put = 0, get = 0;  // of the heads to fetch: left in this tensor, which tensor; places in the ring
+    auto fetch = [&] {
+        while (left == 0 && stage < 2) {
+            ++stage;
+            left = stage == 1 ? n_k : n_v;
+            next = stage == 1 ? reinterpret_cast<const B *>(p.k) + at.k + (long long)k0 * p.k_head
+                              : reinterpret_cast<const B *>(p.v) + at.v + (long long)v0 * p.v_head;
+            step = p.groups * (stage == 1 ? p.k_head : p.v_head);
         }
-        for (int o = p.lanes / 2; o > 0; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
-        if (!on) continue;
-        if (r.norm) {
-            const float inv = 1.0f / sqrtf(sq / (float)p.d + p.eps);
+        if (left > 0) {
+            uint4 *const to = ring + put * (P * kRopeThreads) + tid;
 #pragma unroll
-            for (int e = 0; e < 16; ++e) x[e] *= inv;
-            if (r.w) {
-                float w[16];
-                load8<B>(w, r.w + c0);
-                load8<B>(w + 8, r.w + c1);
-#pragma unroll
-                for (int e = 0; e < 16; ++e) x[e] *= w[e];
+            for (int x = 0; x < P / 2; ++x) {
+                cp_async16(to + x * kRopeThreads, next + c0 + x * (16 / (int)sizeof(B)));
+                cp_async16(to + (P / 2 + x) * kRopeThreads, next + c1 + x * (16 / (int)sizeof(B)));
             }
+            next += step, --left;
         }
-        if (r.turn && turned) {
-            const float *const cs = p.cs + (long long)at[tk].pos * p.cs_row + 8 * i;
-            float co[8], si[8];
-            load8<uint32_t>(co, reinterpret_cast<const uint32_t *>(cs));
-            load8<uint32_t>(si, reinterpret_cast<const uint32_t *>(cs + half));
-            if (!p.pairs) {
+        cp_async_commit();
+        put = put + 1 == R ? 0 : put + 1;
+    };
+    auto take = [&](Raw8<B> &a, Raw8<B> &b) {
+        cp_async_wait<R - 1>();
+        const uint4 *const from = ring + get * (P * kRopeThreads) + tid;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float a = x[e], b = x[e + 8];
-                    x[e] = a * co[e] - b * si[e], x[e + 8] = b * co[e] + a * si[e];
+        for (int x = 0; x < P / 2; ++x) a.w[x] = from[x * kRopeThreads], b.w[x] = from[(P / 2 + x) * kRopeThreads];
+        get = get + 1 == R ? 0 : get + 1;
+        fetch();
+    };
+#pragma unroll
+    for (int n = 0; n < R; ++n) fetch();
+    f2 co[4], si[4], ni[4];  // cosines, sines and the sines' negatives
+    if (turned) {
+        const uint32_t *const cs = reinterpret_cast<const uint32_t *>(p.cs + (long long)at.pos * p.cs_row + 8 * i);
+        pairs8<uint32_t>(co, load8<uint32_t>(cs));
+        pairs8<uint32_t>(si, load8<uint32_t>(cs + half));
+        const f2 minus = f2_pack(-1.f, -1.f);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) ni[e] = f2_mul(si[e], minus);
+    }
+    auto heads = [&](int n, B *to, long long to_step, B *to2, long long to2_step, const B *weight) {
+        f2 w[8];
+        const bool scaled = p.norm && weight;
+        if (scaled && n > 0) pairs8<B>(w, load8<B>(weight + c0)), pairs8<B>(w + 4, load8<B>(weight + c1));
+        for (; n > 0; --n) {
+            Raw8<B> a, b;
+            take(a, b);
+            if (p.norm || turned) {
+                f2 x[8];
+                pairs8<B>(x, a), pairs8<B>(x + 4, b);
+                if (p.norm) {
+                    f2 s2[2] = {f2_mul(x[0], x[0]), f2_mul(x[4], x[4])};
+#pragma unroll
+                    for (int e = 1; e < 4; ++e) s2[0] = f2_fma(x[e], x[e], s2[0]), s2[1] = f2_fma(x[4 + e], x[4 + e], s2[1]);
+                    float lo, hi;
+                    f2_unpack(f2_add(s2[0], s2[1]), lo, hi);
+                    float sq = has ? lo + hi : 0.f;
+                    for (int o = p.lanes / 2; o > 0; o >>= 1) sq += __shfl_xor_sync(mask, sq, o);
+                    const float inv = rsqrtf(sq / (float)p.d + p.eps);
+                    const f2 inv2 = f2_pack(inv, inv);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) x[e] = f2_mul(x[e], inv2);
+                    if (scaled)
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) x[e] = f2_mul(x[e], w[e]);
                 }
-            } else {
+                if (turned && p.pairs) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float a = x[2 * e], b = x[2 * e + 1];
-                    x[2 * e] = a * co[e] - b * si[e], x[2 * e + 1] = b * co[e] + a * si[e];
+                    for (int e = 0; e < 8; ++e) {
+                        float c[2], s[2], f, g;
+                        f2_unpack(co[e / 2], c[0], c[1]), f2_unpack(si[e / 2], s[0], s[1]), f2_unpack(x[e], f, g);
+                        x[e] = f2_fma(f2_pack(g, f), f2_pack(-s[e & 1], s[e & 1]), f2_mul(x[e], f2_pack(c[e & 1], c[e & 1])));
+                    }
+                } else if (turned) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const f2 y = x[e], z = x[4 + e];
+                        x[e] = f2_fma(z, ni[e], f2_mul(y, co[e])), x[4 + e] = f2_fma(y, si[e], f2_mul(z, co[e]));
+                    }
                 }
+                a = round8<B>(x), b = round8<B>(x + 4);
+            }
+            if (has) store8<B>(to + c0, a), store8<B>(to + c1, b);
+            to += to_step;
+            if (to2) {
+                if (has) store8<B>(to2 + c0, a), store8<B>(to2 + c1, b);
+                to2 += to2_step;
             }
         }
-        if (r.norm || r.turn) {
-            store8<B>(r.to + c0, x);
-            store8<B>(r.to + c1, x + 8);
-            if (r.to2) {
-                store8<B>(r.to2 + c0, x);
-                store8<B>(r.to2 + c1, x + 8);
-            }
-        } else {  // raw bits
-            copy8<B>(r.to + c0, r.from + c0);
-            copy8<B>(r.to + c1, r.from + c1);
-            if (r.to2) {
-                copy8<B>(r.to2 + c0, r.from + c0);
-                copy8<B>(r.to2 + c1, r.from + c1);
-            }
+    };
+    heads(n_q, reinterpret_cast<B *>(p.q_out) + at.qo + (long long)part * p.qo_head, p.groups * p.qo_head, nullptr, 0,
+          reinterpret_cast<const B *>(p.wq));
+    if (n_k > 0) {
+        B *const in = p.paged ? reinterpret_cast<B *>(p.c.k) + at.kc + (long long)k0 * p.c.k_head : nullptr;
+        B *const out = p.k_out ? reinterpret_cast<B *>(p.k_out) + at.ko + (long long)k0 * p.ko_head : nullptr;
+        heads(n_k, out ? out : in, p.groups * (out ? p.ko_head : p.c.k_head), out ? in : nullptr, p.groups * p.c.k_head,
+              reinterpret_cast<const B *>(p.wk));
+    }
+    if (n_v > 0) {
+        B *to = reinterpret_cast<B *>(p.c.v) + at.vc + (long long)v0 * p.c.v_head;
+        for (int n = n_v; n > 0; --n, to += p.groups * p.c.v_head) {
+            Raw8<B> a, b;
+            take(a, b);
+            if (has) store8<B>(to + c0, a), store8<B>(to + c1, b);
         }
     }
+    cp_async_wait<0>();
 }
 
 // Any rows: a warp a head, its channels read twice.
@@ -273,6 +338,7 @@ __global__ void __launch_bounds__(kRopeThreads) norm_rope_any(const __grid_const
 
 }  // namespace
 
+int rope_smem(bool bf16) { return bf16 ? rope_ring<uint16_t>() * 2 * kRopeThreads * 16 : rope_ring<uint32_t>() * 4 * kRopeThreads * 16; }
 RopeKernel rope_kernel(bool bf16, bool vec) {
     if (bf16) return vec ? norm_rope<uint16_t> : norm_rope_any<uint16_t>;
     return vec ? norm_rope<uint32_t> : norm_rope_any<uint32_t>;
