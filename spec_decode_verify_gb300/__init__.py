@@ -898,7 +898,7 @@ class PagedCache:
     anything.  held int32 [n_slots] (pages of each slot) and refs int32 [n_pages] (slots that hold each page, 0 = free) are
     needed by cache_reserve, cache_fork and cache_free.  Made once for the tensors, which it keeps; layer(i) is the cache
     of one layer."""
-    __slots__ = ("_k", "_v", "_page_table", "_held", "_refs", "_packed")
+    __slots__ = ("_k", "_v", "_page_table", "_held", "_refs", "_packed", "_device", "_dtype", "_code", "_heads", "_d", "_layers")
 
     def __init__(self, k, v, page_table, *, held=None, refs=None):
         if k.dim() not in (4, 5) or v.shape != k.shape:
@@ -915,6 +915,9 @@ class PagedCache:
         _need_int32(held, "held", shape=(page_table.shape[0],))
         _need_int32(refs, "refs", shape=(k.shape[-4],))
         self._k, self._v, self._page_table, self._held, self._refs = k, v, page_table, held, refs
+        devices = {x.get_device() for x in self._tensors() if x is not None}
+        self._device = devices.pop() if len(devices) == 1 else None
+        self._dtype, self._code, self._heads, self._d, self._layers = k.dtype, dtype, k.shape[-2], k.shape[-1], k.dim() == 5
         ks, vs = k.stride()[-5:-1], v.stride()[-5:-1]
         if k.dim() == 4:
             ks, vs = (0, *ks), (0, *vs)
@@ -939,36 +942,17 @@ class PagedCache:
 
 
 def _one_layer(cache) -> None:
-    if cache._k.dim() != 4:
+    if cache._layers:
         raise ValueError("this call takes the cache of one layer (PagedCache.layer)")
-
-
-def _required(t, name, n) -> int:
-    if t is None:
-        raise ValueError(f"{name} is required")
-    return _index_array(t, name, n)
 
 
 def _exactly(t, name, shape) -> int:
     """Pointer of a contiguous int32 array of the given shape, or 0."""
     if t is None:
         return 0
-    _need_int32(t, name, shape=shape)
+    if t.dtype is not _i32 or t.shape != shape or not t.is_contiguous():
+        _need_int32(t, name, shape=shape)
     return t.data_ptr()
-
-
-def _rows_of(t, name, lead, d, dtype):
-    """Pointer and (sequence, token, head) strides of [*lead, heads, d] rows; packed rows have no sequence stride."""
-    if t is None:
-        return 0, 0, 0, 0
-    if t.dim() != len(lead) + 2 or t.shape[:-2] != lead or t.shape[-1] != d:
-        raise ValueError(f"{name} must be [{', '.join(map(str, lead))}, heads, {d}], got {tuple(t.shape)}")
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must have dtype {dtype}")
-    st = t.stride()
-    if d > 1 and st[-1] != 1:
-        raise ValueError(f"{name} needs a unit innermost stride")
-    return (t.data_ptr(), *(st[:3] if len(lead) == 2 else (0, st[0], st[1])))
 
 
 def _lead(shape, cu, T, name):
@@ -979,32 +963,50 @@ def _lead(shape, cu, T, name):
         if T is not None and T != shape[1]:
             raise ValueError(f"T = {T} but {name} holds {shape[1]} tokens a sequence")
         return shape[0], shape[1], 0, shape[:2]
-    if cu.dim() != 1 or cu.shape[0] < 1:
+    n = cu.shape
+    if len(n) != 1 or n[0] < 1:
         raise ValueError("the cumulative counts must be [n_seq + 1]")
-    _need_int32(cu, "the cumulative counts")
+    if cu.dtype is not _i32 or not cu.is_contiguous():
+        _need_int32(cu, "the cumulative counts")
     if T is None:
         raise ValueError("packed rows need T, the largest count")
-    return cu.shape[0] - 1, int(T), shape[0], shape[:1]
+    return n[0] - 1, int(T), shape[0], shape[:1]
 
 
 def make_tree_attention_args(q, out, cache, cache_len, *, parent=None, scale=None, cu_draft=None, T=None, cache_idx=None, err=None,
                              workspace=None, wait_polls=0, check_device=True) -> TreeAttentionArgs:
     """Build cv_tree_attention_args (see tree_attention)."""
-    _one_layer(cache)
-    if q.dim() != (4 if cu_draft is None else 3):
+    if cache._layers:
+        _one_layer(cache)
+    qs, d, dt = q.shape, cache._d, cache._dtype
+    if len(qs) != (4 if cu_draft is None else 3):
         raise ValueError("q must be [n_seq, T, n_heads, head_dim], or [total, n_heads, head_dim] with cu_draft")
-    n, T, total, lead = _lead(q.shape, cu_draft, T, "q")
-    d, dt = cache._k.shape[-1], cache._k.dtype
-    if out is None or out.shape != q.shape:
-        raise ValueError("out must have the shape of q")
-    rows = (*_rows_of(q, "q", lead, d, dt), *_rows_of(out, "out", lead, d, dt))
+    n, T, total, lead = _lead(qs, cu_draft, T, "q")
+    if out is None or out.shape != qs or qs[-1] != d:
+        raise ValueError(f"q and out must have one shape and heads of {d} channels")
+    if q.dtype is not dt or out.dtype is not dt:
+        raise TypeError(f"q and out must have the dtype of the cache, {dt}")
+    qt, ot = q.stride(), out.stride()
+    if d > 1 and (qt[-1] != 1 or ot[-1] != 1):
+        raise ValueError("q and out need a unit innermost stride")
+    if cu_draft is not None:
+        qt, ot = (0, *qt), (0, *ot)
     ws, ws_bytes = (workspace.data_ptr(), workspace.numel() * workspace.element_size()) if workspace is not None else (0, 0)
-    if check_device:
-        _one_device(q, out, *cache._tensors(), cache_len, parent, cu_draft, cache_idx, err, workspace)
+    if cache_len is None:
+        raise ValueError("cache_len is required")
+    if check_device:  # written out, since a call of one token notices a loop
+        dev = cache._device
+        if not (dev is not None and dev >= 0 and (_current_device or _load_device())() == dev and
+                q.get_device() == out.get_device() == cache_len.get_device() == dev and
+                (parent is None or parent.get_device() == dev) and (cu_draft is None or cu_draft.get_device() == dev) and
+                (cache_idx is None or cache_idx.get_device() == dev) and (err is None or err.get_device() == dev) and
+                (workspace is None or workspace.get_device() == dev)):
+            _one_device(q, out, *cache._tensors(), cache_len, parent, cu_draft, cache_idx, err, workspace)
     return TreeAttentionArgs.from_buffer_copy(_TREE_ATTENTION.pack(
-        n, T, q.shape[-2], total, d ** -0.5 if scale is None else scale, wait_polls, cache._packed, *rows,
-        cu_draft.data_ptr() if cu_draft is not None else 0, _exactly(parent, "parent", lead), _required(cache_len, "cache_len", n),
-        _index_array(cache_idx, "cache_idx", n), _index_array(err, "err", n), ws, ws_bytes))
+        n, T, qs[-2], total, d ** -0.5 if scale is None else scale, wait_polls, cache._packed, q.data_ptr(), qt[0], qt[1], qt[2],
+        out.data_ptr(), ot[0], ot[1], ot[2], cu_draft.data_ptr() if cu_draft is not None else 0,
+        _exactly(parent, "parent", lead), _index_array(cache_len, "cache_len", n), _index_array(cache_idx, "cache_idx", n),
+        _index_array(err, "err", n), ws, ws_bytes))
 
 
 def tree_attention_workspace(q, out, cache, cache_len, **kw) -> int:
@@ -1053,30 +1055,36 @@ def make_draft_verify_args(probs, tokens, uniforms, accept_len, out_tokens, *, d
                            check_device=True) -> DraftVerifyArgs:
     """Build cv_draft_verify_args (see draft_verify)."""
     f32 = _f32 or _load_types()
-    if probs.dim() != (3 if cu_draft is None else 2):
+    ps = probs.shape
+    if len(ps) != (3 if cu_draft is None else 2):
         raise ValueError("probs must be [n_seq, T, vocab], or [total, vocab] with cu_draft")
-    n, T, total, lead = _lead(probs.shape, cu_draft, T, "probs")
-    V = probs.shape[-1]
-    code = _dtype_code(probs)
-
-    def rows(t, name):
-        if t is None:
-            return 0, 0, 0
-        if t.shape != probs.shape or t.dtype is not probs.dtype:
-            raise ValueError(f"{name} must have the shape and dtype of probs")
-        st = t.stride()
-        if V > 1 and st[-1] != 1:
-            raise ValueError(f"{name} needs a unit innermost stride")
-        return (t.data_ptr(), *(st[:2] if cu_draft is None else (0, st[0])))
-
-    if uniforms.dtype is not f32 or uniforms.shape != (n, T + 1) or not uniforms.is_contiguous():
-        raise ValueError(f"uniforms must be contiguous float32 [{n}, {T + 1}]")
+    n, T, total, lead = _lead(ps, cu_draft, T, "probs")
+    V, dt = ps[-1], probs.dtype
+    pt = qt = probs.stride()
+    if draft_probs is not None:
+        qt = draft_probs.stride()
+        if draft_probs.shape != ps or draft_probs.dtype is not dt:
+            raise ValueError("draft_probs must have the shape and dtype of probs")
+    if V > 1 and (pt[-1] != 1 or qt[-1] != 1):
+        raise ValueError("probs and draft_probs need a unit innermost stride")
+    if cu_draft is not None:
+        pt, qt = (0, *pt), (0, *qt)
     if tokens is None or accept_len is None or out_tokens is None:
         raise ValueError("tokens, accept_len and out_tokens are required")
+    if uniforms.dtype is not f32 or uniforms.shape != (n, T + 1) or not uniforms.is_contiguous():
+        raise ValueError(f"uniforms must be contiguous float32 [{n}, {T + 1}]")
     if check_device:
-        _one_device(probs, tokens, uniforms, accept_len, out_tokens, draft_probs, parent, path, accept_node, cu_draft, cache_idx, err)
+        dev = probs.get_device()
+        if not (dev >= 0 and (_current_device or _load_device())() == dev and
+                tokens.get_device() == uniforms.get_device() == accept_len.get_device() == out_tokens.get_device() == dev and
+                (draft_probs is None or draft_probs.get_device() == dev) and (parent is None or parent.get_device() == dev) and
+                (path is None or path.get_device() == dev) and (accept_node is None or accept_node.get_device() == dev) and
+                (cu_draft is None or cu_draft.get_device() == dev) and (cache_idx is None or cache_idx.get_device() == dev) and
+                (err is None or err.get_device() == dev)):
+            _one_device(probs, tokens, uniforms, accept_len, out_tokens, draft_probs, parent, path, accept_node, cu_draft, cache_idx, err)
     return DraftVerifyArgs.from_buffer_copy(_DRAFT_VERIFY.pack(
-        n, T, V, code, total, *rows(probs, "probs"), *rows(draft_probs, "draft_probs"), _exactly(tokens, "tokens", lead),
+        n, T, V, BF16 if dt is _bf16 else _dtype_code(probs), total, probs.data_ptr(), pt[0], pt[1],
+        draft_probs.data_ptr() if draft_probs is not None else 0, qt[0], qt[1], _exactly(tokens, "tokens", lead),
         _exactly(parent, "parent", lead), uniforms.data_ptr(), cu_draft.data_ptr() if cu_draft is not None else 0,
         _index_array(cache_idx, "cache_idx", n), _index_array(accept_len, "accept_len", n),
         _index_array(accept_node, "accept_node", n), _exactly(path, "path", (n, T)), _exactly(out_tokens, "out_tokens", (n, T)),
@@ -1106,56 +1114,79 @@ def make_qk_norm_rope_args(q, k, q_out, *, k_out=None, v=None, cos_sin=None, q_w
                            cache_idx=None, err=None, check_device=True) -> QkNormRopeArgs:
     """Build cv_qk_norm_rope_args (see qk_norm_rope)."""
     f32 = _f32 or _load_types()
-    if q.dim() != (4 if cu_seqlens is None else 3):
+    qs, dt = q.shape, q.dtype
+    batch = cu_seqlens is None
+    if len(qs) != (4 if batch else 3):
         raise ValueError("q must be [n_seq, T, n_heads, head_dim], or [total, n_heads, head_dim] with cu_seqlens")
-    n, T, total, lead = _lead(q.shape, cu_seqlens, max_seqlen if cu_seqlens is not None else None, "q")
-    if cu_seqlens is None and max_seqlen is not None and max_seqlen < T:
+    n, T, total, lead = _lead(qs, cu_seqlens, None if batch else max_seqlen, "q")
+    if batch and max_seqlen is not None and max_seqlen < T:
         raise ValueError(f"max_seqlen = {max_seqlen} but q holds {T} tokens a sequence")
-    d, dt = q.shape[-1], q.dtype
-    kv = k.shape[-2] if k is not None else 0
-    if q_out is None or q_out.shape != q.shape:
+    d = qs[-1]
+    if q_out is None or q_out.shape != qs:
         raise ValueError("q_out must have the shape of q")
-    if k is None and (k_out is not None or v is not None):
-        raise ValueError("k_out and v need k")
-    for t, name in ((k_out, "k_out"), (v, "v")):
-        if t is not None and t.shape != k.shape:
-            raise ValueError(f"{name} must have the shape of k")
-    if v is not None and cache is None:
-        raise ValueError("v needs a cache to be written to")
-    if k is not None and k_out is None and cache is None:
-        raise ValueError("k needs k_out or a cache to be written to")
+    kv, ks = 0, None
+    if k is not None:
+        ks = k.shape
+        kv = ks[-2]
+        if ks[:-2] != lead or ks[-1] != d:
+            raise ValueError(f"k must be [{', '.join(map(str, lead))}, heads, {d}], got {tuple(ks)}")
+        if k_out is None and cache is None:
+            raise ValueError("k needs k_out or a cache to be written to")
+    if (k_out is not None and k_out.shape != ks) or (v is not None and v.shape != ks):
+        raise ValueError("k_out and v must have the shape of k")
     packed = _NO_CACHE
     if cache is not None:
-        _one_layer(cache)
-        if k is None or cache._k.shape[-2:] != k.shape[-2:] or cache._k.dtype is not dt:
+        if cache._layers:
+            _one_layer(cache)
+        if cache._heads != kv or cache._d != d or cache._dtype is not dt:
             raise ValueError("the cache must have the kv heads, head size and dtype of k")
         packed = cache._packed
+        if cache_len is None:
+            raise ValueError("cache_len is required")
+    elif v is not None:
+        raise ValueError("v needs a cache to be written to")
+
+    def rows(t, name):  # pointer and (sequence, token, head) strides
+        if t is None:
+            return 0, 0, 0, 0
+        if t.dtype is not dt:
+            raise TypeError(f"{name} must have the dtype of q")
+        st = t.stride()
+        if st[-1] != 1 and d > 1:
+            raise ValueError(f"{name} needs a unit innermost stride")
+        return (t.data_ptr(), st[0], st[1], st[2]) if batch else (t.data_ptr(), 0, st[0], st[1])
 
     def weight(t, name):
         if t is None:
             return 0
-        if t.shape != (d,) or t.dtype is not dt or not t.is_contiguous():
+        if t.dtype is not dt or t.shape != (d,) or not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous [{d}] and have the dtype of q")
         return t.data_ptr()
 
     cs, cs_row, rot, n_pos = 0, 0, 0, 0
     if cos_sin is not None:
-        if cos_sin.dim() != 2 or cos_sin.dtype is not f32 or (cos_sin.shape[1] > 1 and cos_sin.stride(1) != 1):
+        if cos_sin.dtype is not f32 or cos_sin.dim() != 2 or (cos_sin.shape[1] > 1 and cos_sin.stride(1) != 1):
             raise ValueError("cos_sin must be float32 [n_positions, rot_dim] with a unit innermost stride")
         n_pos, rot = cos_sin.shape
         cs, cs_row = cos_sin.data_ptr(), cos_sin.stride(0) if n_pos > 1 else rot
         if positions is None and cache_len is None:
             raise ValueError("the rotation needs positions, or cache_len")
     if check_device:
-        _one_device(q, k, q_out, k_out, v, cos_sin, q_weight, k_weight, positions, cache_len, cu_seqlens, cache_idx, err,
-                    *(cache._tensors() if cache is not None else ()))
+        dev = q.get_device()
+        if not (dev >= 0 and (_current_device or _load_device())() == dev and q_out.get_device() == dev and
+                (k is None or k.get_device() == dev) and (k_out is None or k_out.get_device() == dev) and
+                (v is None or v.get_device() == dev) and (cos_sin is None or cos_sin.get_device() == dev) and
+                (q_weight is None or q_weight.get_device() == dev) and (k_weight is None or k_weight.get_device() == dev) and
+                (positions is None or positions.get_device() == dev) and (cache_len is None or cache_len.get_device() == dev) and
+                (cu_seqlens is None or cu_seqlens.get_device() == dev) and (cache_idx is None or cache_idx.get_device() == dev) and
+                (err is None or err.get_device() == dev) and (cache is None or cache._device == dev)):
+            _one_device(q, k, q_out, k_out, v, cos_sin, q_weight, k_weight, positions, cache_len, cu_seqlens, cache_idx, err,
+                        *(cache._tensors() if cache is not None else ()))
     return QkNormRopeArgs.from_buffer_copy(_QK_NORM_ROPE.pack(
-        n, T, q.shape[-2], kv, d, _dtype_code(q), total, rot, 1 if pairs else 0, 1 if norm else 0, n_pos, eps,
-        *_rows_of(q, "q", lead, d, dt), *_rows_of(q_out, "q_out", lead, d, dt), *_rows_of(k, "k", lead, d, dt),
-        *_rows_of(k_out, "k_out", lead, d, dt), *_rows_of(v, "v", lead, d, dt), weight(q_weight, "q_weight"),
+        n, T, qs[-2], kv, d, BF16 if dt is _bf16 else _dtype_code(q), total, rot, 1 if pairs else 0, 1 if norm else 0, n_pos, eps,
+        *rows(q, "q"), *rows(q_out, "q_out"), *rows(k, "k"), *rows(k_out, "k_out"), *rows(v, "v"), weight(q_weight, "q_weight"),
         weight(k_weight, "k_weight"), cs, cs_row, _exactly(positions, "positions", lead),
-        cu_seqlens.data_ptr() if cu_seqlens is not None else 0,
-        _required(cache_len, "cache_len", n) if cache is not None else _index_array(cache_len, "cache_len", n),
+        cu_seqlens.data_ptr() if cu_seqlens is not None else 0, _index_array(cache_len, "cache_len", n),
         _index_array(cache_idx, "cache_idx", n), packed, _index_array(err, "err", n)))
 
 
@@ -1183,13 +1214,19 @@ def make_cache_compact_args(cache, cache_len, path, accept_len, *, new_len=None,
     """Build cv_cache_compact_args (see cache_compact)."""
     if path.dim() != 2:
         raise ValueError("path must be int32 [n_seq, T]")
+    if cache_len is None or accept_len is None:
+        raise ValueError("cache_len and accept_len are required")
     n, T = path.shape
-    _load_types()
     if check_device:
-        _one_device(path, *cache._tensors(), cache_len, accept_len, new_len, cache_idx, err)
+        dev = cache._device
+        if not (dev is not None and dev >= 0 and (_current_device or _load_device())() == dev and
+                path.get_device() == cache_len.get_device() == accept_len.get_device() == dev and
+                (new_len is None or new_len.get_device() == dev) and (cache_idx is None or cache_idx.get_device() == dev) and
+                (err is None or err.get_device() == dev)):
+            _one_device(path, *cache._tensors(), cache_len, accept_len, new_len, cache_idx, err)
     return CacheCompactArgs.from_buffer_copy(_COMPACT.pack(
-        n, T, cache._packed, _required(cache_len, "cache_len", n), _exactly(path, "path", (n, T)),
-        _required(accept_len, "accept_len", n), _index_array(cache_idx, "cache_idx", n), _index_array(new_len, "new_len", n),
+        n, T, cache._packed, _index_array(cache_len, "cache_len", n), _exactly(path, "path", (n, T)),
+        _index_array(accept_len, "accept_len", n), _index_array(cache_idx, "cache_idx", n), _index_array(new_len, "new_len", n),
         _index_array(err, "err", n)))
 
 
@@ -1205,11 +1242,14 @@ def cache_compact(cache, cache_len, path, accept_len, *, new_len=None, cache_idx
 
 def make_cache_pages_args(cache, n_seq, *, idx=None, src_idx=None, n_tokens=None, err=None, check_device=True) -> CachePagesArgs:
     """Build cv_cache_pages_args (see cache_reserve, cache_fork and cache_free)."""
-    _load_types()
     if cache._held is None or cache._refs is None:
         raise ValueError("the cache needs held and refs")
     if check_device:
-        _one_device(*cache._tensors(), idx, src_idx, n_tokens, err)
+        dev = cache._device
+        if not (dev is not None and dev >= 0 and (_current_device or _load_device())() == dev and
+                (idx is None or idx.get_device() == dev) and (src_idx is None or src_idx.get_device() == dev) and
+                (n_tokens is None or n_tokens.get_device() == dev) and (err is None or err.get_device() == dev)):
+            _one_device(*cache._tensors(), idx, src_idx, n_tokens, err)
     return CachePagesArgs.from_buffer_copy(_PAGES.pack(
         n_seq, cache._packed, _exactly(idx, "cache_idx", (n_seq,)), _exactly(src_idx, "src_idx", (n_seq,)),
         _exactly(n_tokens, "n_tokens", (n_seq,)), _index_array(err, "err", n_seq)))
