@@ -82,7 +82,7 @@ constexpr int kTcUnitCost = 3, kSimtUnitCost = 1;
 struct AttnPlan {
     cvk::AttnSimt simt;
     cvk::AttnTc tc;
-    bool on_tc;
+    bool on_tc, pair;
     int dp, rows, keys, parts, unit_cost, page_rows, tok;
     bool cut;
     int64_t bytes;
@@ -108,12 +108,13 @@ AttnPlan plan_attention(const cv_tree_attention_args *a, bool tc = true) {
     AttnPlan pl;
     const cvk::DeviceLimits lim = device_limits();
     pl.dp = d <= 64 ? 64 : d <= 128 ? 128 : d <= 192 ? 192 : 256;
-    pl.tc = cvk::attn_tc_kernel(pl.dp);
+    pl.tok = G <= 128 ? (a->T < 128 / G ? a->T : 128 / G) : 1;
+    pl.pair = pl.dp <= 128 && a->T > pl.tok;
+    pl.tc = cvk::attn_tc_kernel(pl.dp, pl.pair);
     pl.on_tc = tc && tc_takes(a, pl.tc.keys);
     if (pl.on_tc) {
         pl.keys = pl.tc.keys;
-        pl.tok = a->T < 128 / G ? a->T : 128 / G;
-        pl.rows = pl.tok * G;
+        pl.rows = pl.tok * G * (pl.pair ? 2 : 1);
         pl.page_rows = c.page_size < pl.keys ? c.page_size : pl.keys;
         pl.parts = lim.sms, pl.unit_cost = kTcUnitCost;
     } else {

@@ -41,7 +41,7 @@ struct AttnMaps {
     AttnParams a;
     CUtensorMap q, k, v;
     int page_rows;   // rows of a copy's box: of a page, at most a tile
-    int tok;         // drafts of a full unit
+    int tok;         // drafts of a row tile
     int o_vec;       // out allows 16-byte accesses
 };
 constexpr int kSimtRows = 32, kSimtThreads = 256;
@@ -59,7 +59,7 @@ struct AttnTc {
     int smem_bytes, keys, threads;
 };
 AttnSimt attn_simt_kernel(bool bf16, int dp, bool vec);
-AttnTc attn_tc_kernel(int dp);
+AttnTc attn_tc_kernel(int dp, bool two);  // two: units of two row tiles (up to 128 channels)
 AttnKernel attn_join_kernel(bool bf16, int dp);
 constexpr int kAttnJoinThreads = 256, kAttnJoinY = 4;
 

@@ -15,8 +15,9 @@
 //   load V   1 warp: V (one warp for both took 45 cycles a box, 64 boxes a tile for pages of 16 tokens: slower than HBM)
 //   issue    1 warp: Q K^T of the next tile, then P V of this one
 //   scout    1 warp: of each sequence the drafts' ancestors, and a look at every page and parent
-//   softmax  4 warps, a row a thread: S from tensor memory, P back over it, O's rescaling
-//   output   4 warps, a row a thread: O / l, or (m, l, O), to memory, while the next unit runs
+//   softmax  4 warps, a row a thread: S from tensor memory, P back over it, O's rescaling; or two groups of 4,
+//            which write their own rows (see Tc)
+//   output   4 warps, a row a thread: O / l, or (m, l, O), to memory, while the next unit runs (beside one group)
 // Tensor memory: two buffers of S (and P), O (two for up to 192 channels).
 //
 // Masks.  Cached tokens are seen by every row; only the tiles that reach past them look at masks.  There the rows of V past the
@@ -35,15 +36,18 @@ constexpr float kSlack = 8.0f;  // log2 of what a weight may reach before its ro
 constexpr unsigned kDrainPolls = 1u << 16;
 constexpr int kTcThreads = 384, kQueue = 4;
 
-template <int DP>
+// GROUPS: groups of 4 softmax warps.  One takes every tile, and 4 more warps write the outputs while the next unit runs.  Two, in units of
+// two row tiles, take a row tile each of every tile of keys, which then serves up to 256 rows, and write their own rows.
+template <int DP, int GROUPS>
 struct Tc {
     static constexpr int KT = DP <= 128 ? 128 : 64;     // keys a tile
     static constexpr int BLOCKS = DP / 64;              // blocks of 64 channels
     static constexpr int KV = KT * DP * 2, Q = 128 * DP * 2;
-    static constexpr int QBUF = DP <= 128 ? 2 : 1, OBUF = DP <= 192 ? 2 : 1;
+    static constexpr int QTILES = DP <= 128 ? 2 : 1;    // of two units in turn, or of the two row tiles
+    static constexpr int OBUF = GROUPS * DP <= 192 ? 2 : 1;
     static constexpr int KS = DP == 64 ? 4 : DP == 192 ? 3 : 2, VS = KS;  // stages of K and of V
     static constexpr int COL_O = 2 * KT;
-    static_assert(COL_O + OBUF * DP <= 512, "tensor memory");
+    static_assert(COL_O + OBUF * GROUPS * DP <= 512, "tensor memory");
 };
 constexpr uint32_t kTmemCols = 512;
 
@@ -53,24 +57,25 @@ struct TcUnit {
 };
 
 struct TcShared {
-    uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4], q_full[2], q_empty[2], s_full[2], p_ready[2], o_full[2], o_free[2],
-        ml_full[2], ml_free[2], see_full[2], see_empty[2], unit_full[kQueue], unit_empty[kQueue], pv_done, last;
+    uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4], q_full[2], q_empty[2], s_full[2], p_ready[2], pv_done[2], o_full[2], o_free[2],
+        ml_full[2], ml_free[2], see_full[2], see_empty[2], unit_full[kQueue], unit_empty[kQueue], last;
     TcUnit unit[kQueue];
     int unit_pages[kQueue][32];  // the pages of its first tiles
     uint32_t tmem;
     int dead;
     int flags[2];            // of a sequence, and its drafts' ancestors; two in turn
     uint4 see[2][128];
-    uint32_t bad[2][4][4];   // drafts whose v holds a NaN or an infinity, as each softmax warp saw them; of two units in turn
-    float m[2][128], l[2][128];
+    uint32_t bad[2][8][4];   // drafts whose v holds a NaN or an infinity, as each softmax warp saw them; of two units in turn
+    float m[2][128], l[2][128];  // of two units in turn
     AttnTree tree;
     AttnRange range;
     AttnScratch scratch;
 };
 
-template <int DP>
+template <int DP, int GROUPS>
 __host__ __device__ constexpr int tc_smem() {
-    return Tc<DP>::QBUF * Tc<DP>::Q + (Tc<DP>::KS + Tc<DP>::VS) * Tc<DP>::KV + (int)sizeof(TcShared) + 1024;
+    using K = Tc<DP, GROUPS>;
+    return K::QTILES * K::Q + (K::KS + K::VS) * K::KV + (int)sizeof(TcShared) + 1024;
 }
 
 struct Waits {
@@ -138,66 +143,50 @@ __device__ __forceinline__ bool not_finite(const uint4 &w) {
     return ((carries(w.x) | carries(w.y) | carries(w.z) | carries(w.w)) & 0x80008000u) != 0;
 }
 
-// Drafts whose v is not finite, to the rows that see them: their weights again from q and k, and O in tensor memory plus
-// weight times v.
-template <int DP>
-__device__ __noinline__ void add_bad_drafts(const AttnParams &p, const TcUnit &u, const uint32_t *bad, uint4 see, int r, float m,
-                                            uint32_t to) {
+// Drafts whose v is not finite, to the rows that see them: their weights again from q and k, and 32 channels of O plus weight
+// times v.
+__device__ __noinline__ void add_bad_drafts(const AttnParams &p, const TcUnit &u, const uint32_t *bad, uint4 see, int row, int first,
+                                            int last, float m, int c0, uint32_t *o) {
     const uint16_t *const q = reinterpret_cast<const uint16_t *>(p.q) + (p.cu ? 0LL : (long long)u.s * p.q_seq) +
-                              (long long)(u.row0 + (u.row + r) / p.G) * p.q_tok +
-                              (long long)(u.h * p.G + (u.row + r) % p.G) * p.q_head;
+                              (long long)(u.row0 + row / p.G) * p.q_tok + (long long)(u.h * p.G + row % p.G) * p.q_head;
     const int *const table = p.c.table + (long long)u.slot * p.c.table_row;
     for (int b = 0; b < u.T; ++b) {
-        if (!(bad[b >> 5] >> (b & 31) & 1)) continue;
         const int j = u.L + b;
-        if (j < u.tile * Tc<DP>::KT || j >= u.last * Tc<DP>::KT) continue;
+        if (!(bad[b >> 5] >> (b & 31) & 1) || !((&see.x)[b >> 5] >> (b & 31) & 1) || j < first || j >= last) continue;
         const int pg = __ldg(table + j / p.c.page), in = j % p.c.page;
         const uint16_t *const k = reinterpret_cast<const uint16_t *>(p.c.k) + (long long)pg * p.c.k_page +
                                   (long long)in * p.c.k_row + (long long)u.h * p.c.k_head;
         const uint16_t *const v = reinterpret_cast<const uint16_t *>(p.c.v) + (long long)pg * p.c.v_page +
                                   (long long)in * p.c.v_row + (long long)u.h * p.c.v_head;
-        const bool sees = r < u.rows && ((&see.x)[b >> 5] >> (b & 31) & 1);
         float w = 0.f;
-        if (sees) {
-            for (int c = 0; c < p.c.d; ++c) w = fmaf(widen<uint16_t>(q[c]), widen<uint16_t>(k[c]), w);
-            w = exp2_fast(fmaf(w, p.scale, m == kNone ? 0.f : -m));
-        }
-        __syncwarp();
-#pragma unroll 1
-        for (int c = 0; c < DP; c += 16) {
-            uint32_t x[16];
-            tmem_ld16(x, to + c);
-            tmem_wait_ld(x);
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-                if (sees && c + e < p.c.d) x[e] = __float_as_uint(fmaf(w, widen<uint16_t>(v[c + e]), __uint_as_float(x[e])));
-            tmem_st16(to + c, x);
-        }
-        tmem_wait_st();
+        for (int c = 0; c < p.c.d; ++c) w = fmaf(widen<uint16_t>(q[c]), widen<uint16_t>(k[c]), w);
+        w = exp2_fast(fmaf(w, p.scale, m == kNone ? 0.f : -m));
+        for (int e = 0; e < 32; ++e)
+            if (c0 + e < p.c.d) o[e] = __float_as_uint(fmaf(w, widen<uint16_t>(v[c0 + e]), __uint_as_float(o[e])));
     }
 }
 
-template <int DP>
+template <int DP, int GROUPS>
 __global__ void __launch_bounds__(kTcThreads, 1) attn_tc(const __grid_constant__ AttnMaps mp) {
-    using K = Tc<DP>;
+    using K = Tc<DP, GROUPS>;
     constexpr int KT = K::KT, KS = K::KS, VS = K::VS;
     extern __shared__ unsigned char smem_raw[];
     unsigned char *const smem = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) / 1024 * 1024);
-    unsigned char *const q_tile = smem, *const k_tile = smem + K::QBUF * K::Q, *const v_tile = k_tile + KS * K::KV;
+    unsigned char *const q_tile = smem, *const k_tile = smem + K::QTILES * K::Q, *const v_tile = k_tile + KS * K::KV;
     TcShared *const sh = reinterpret_cast<TcShared *>(v_tile + VS * K::KV);
     const AttnParams &p = mp.a;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    if (dynamic_smem_bytes() < (unsigned)tc_smem<DP>()) return;
+    if (dynamic_smem_bytes() < (unsigned)tc_smem<DP, GROUPS>()) return;
     if (tid == 0) {
         for (int i = 0; i < 4; ++i)
             mbar_init(&sh->k_full[i], 1), mbar_init(&sh->k_empty[i], 1), mbar_init(&sh->v_full[i], 1), mbar_init(&sh->v_empty[i], 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh->q_full[i], 1), mbar_init(&sh->q_empty[i], 1), mbar_init(&sh->s_full[i], 1), mbar_init(&sh->p_ready[i], 4);
-            mbar_init(&sh->o_full[i], 1), mbar_init(&sh->o_free[i], 4), mbar_init(&sh->ml_full[i], 4), mbar_init(&sh->ml_free[i], 4);
-            mbar_init(&sh->see_full[i], 1), mbar_init(&sh->see_empty[i], 8);
+            mbar_init(&sh->o_full[i], 1), mbar_init(&sh->o_free[i], 4 * GROUPS), mbar_init(&sh->ml_full[i], 4 * GROUPS), mbar_init(&sh->ml_free[i], 4);
+            mbar_init(&sh->see_full[i], 1), mbar_init(&sh->see_empty[i], 8), mbar_init(&sh->pv_done[i], 1);
         }
         for (int i = 0; i < kQueue; ++i) mbar_init(&sh->unit_full[i], 1), mbar_init(&sh->unit_empty[i], 11);
-        mbar_init(&sh->pv_done, 1), mbar_init(&sh->last, 1);
+        mbar_init(&sh->last, 1);
         mbar_init_fence();
         sh->dead = 0;
     }
@@ -215,6 +204,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc(const __grid_constant__
     const uint32_t tm = sh->tmem;
     const Waits waits{&sh->dead, p.polls};
     const AttnRange &range = sh->range;
+    // A step is a tile, or a row tile of one: steps take turns at the two buffers of S, and at the groups.
+    constexpr bool pair = GROUPS == 2;
+    const int half = mp.tok * p.G;                    // rows of a row tile
+    constexpr int q_bufs = pair || K::QTILES == 1 ? 1 : 2;  // units' queries that have a place
     // The next unit of the queue for the calling warp; s < 0 after the last one.
     auto pop = [&](TcUnit &u, int units) {
         const int at = units % kQueue;
@@ -255,6 +248,77 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc(const __grid_constant__
             tma_load4(smem_u32(dst) + blk * (KT * 128) + box * mp.page_rows * 128, map, blk * 64, (tile % tiles_page) * KT, h, page, bar);
     };
 
+    // A row tile's outputs, or its part of them, from tensor memory: row r of the tile a thread, with its maximum and sum; b: which notes
+    // of drafts, q: which sequence's masks.
+    bool goes_on = false, came = false;  // parts left in slots 1 and 0
+    auto leave = [&](const TcUnit &u, int y, uint32_t to, int r, float m, float l, int b, int q) {
+        const bool bad_unit = sh->flags[q] != 0, cut = u.last - u.tile < u.tiles;
+        goes_on = cut && u.begins && !bad_unit;
+        came |= cut && !u.begins && !bad_unit;
+        const int row = y * half + r;  // of the unit
+        const bool on = r < half && row < u.rows;
+        if (bad_unit || !__any_sync(0xffffffffu, on)) return;
+        uint32_t bad[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            bad[i] = 0;
+#pragma unroll
+            for (int w = 0; w < 4 * GROUPS; ++w) bad[i] |= sh->bad[b][w][i];
+        }
+        const float inv = cut ? 1.0f : 1.0f / l;
+        float *const part = cut ? attn_part(p, blockIdx.x, u.begins) : nullptr;
+        if (cut && on) part[kPartHead + row] = m, part[kPartHead + p.pad + row] = l;
+        if (cut && row == 0) attn_part_head(part, range, u.first, u.tiles, u.rows, u.row, u.s, u.h, u.row0);
+        uint16_t *const out = reinterpret_cast<uint16_t *>(p.out) + (p.cu ? 0LL : (long long)u.s * p.o_seq) +
+                              (long long)(u.row0 + (u.row + row) / p.G) * p.o_tok +
+                              (long long)(u.h * p.G + (u.row + row) % p.G) * p.o_head;
+#pragma unroll 1
+        for (int x = 0; x < DP; x += 32) {
+            uint32_t o[32];
+            tmem_ld32(o, to + x);
+            tmem_wait_ld32(o);
+            if (on && (bad[0] | bad[1] | bad[2] | bad[3])) {
+                uint32_t c[32];  // (o itself stays in registers)
+#pragma unroll
+                for (int e = 0; e < 32; ++e) c[e] = o[e];
+                add_bad_drafts(p, u, bad, sh->see[q][(u.row + row) / p.G], u.row + row, u.tile * KT, u.last * KT, m, x, c);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = c[e];
+            }
+            if (on && cut) {
+                float4 *const dst = reinterpret_cast<float4 *>(part + kPartHead + 2 * p.pad + (long long)row * DP + x);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    dst[e] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]), __uint_as_float(o[4 * e + 2]),
+                                         __uint_as_float(o[4 * e + 3]));
+            } else if (on) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if (x + 8 * e >= p.c.d) break;  // (d is a multiple of 8)
+                    uint32_t w[4];
+#pragma unroll
+                    for (int z = 0; z < 4; ++z)
+                        w[z] = pack_bf16(__uint_as_float(o[8 * e + 2 * z]) * inv, __uint_as_float(o[8 * e + 2 * z + 1]) * inv);
+                    if (mp.o_vec) {
+                        *reinterpret_cast<uint4 *>(out + x + 8 * e) = make_uint4(w[0], w[1], w[2], w[3]);
+                    } else {
+#pragma unroll
+                        for (int z = 0; z < 4; ++z) {
+                            out[x + 8 * e + 2 * z] = (uint16_t)w[z];
+                            out[x + 8 * e + 2 * z + 1] = (uint16_t)(w[z] >> 16);
+                        }
+                    }
+                }
+            }
+            __syncwarp();
+        }
+    };
+    // The join reads both slots of every block: what is not there, after the last unit (the caller's first thread).
+    auto left_out = [&] {
+        if (p.ws && !goes_on) *reinterpret_cast<int *>(attn_part(p, blockIdx.x, 1)) = 0;
+        if (p.ws && !came) *reinterpret_cast<int *>(attn_part(p, blockIdx.x, 0)) = 0;
+    };
+
     if (warp == 4) {
         // ------------------------------------------------------------------- load: units, Q, K
         AttnWalk walk(p, range);
@@ -283,13 +347,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc(const __grid_constant__
         while (ok && has) {
             pages = ahead;
             if (!(ok = publish(false))) break;
-            const int qb = units % K::QBUF, end = u.q.L + u.q.T;
-            if (units >= K::QBUF && !(ok = wait_warp(&sh->q_empty[qb], (units / K::QBUF - 1) & 1, waits))) break;
-            if (lane == 0) mbar_arrive_expect_tx(&sh->q_full[qb], (unsigned)(K::BLOCKS * 128 * mp.tok * p.G));
+            const int qb = q_bufs == 2 ? units & 1 : 0, end = u.q.L + u.q.T, tiles_q = pair ? 2 : 1;
+            if (units >= q_bufs && !(ok = wait_warp(&sh->q_empty[qb], (units / q_bufs - 1) & 1, waits))) break;
+            if (lane == 0) mbar_arrive_expect_tx(&sh->q_full[qb], (unsigned)(tiles_q * K::BLOCKS * 128 * half));
             __syncwarp();
-            if (lane < K::BLOCKS)
-                tma_load4(smem_u32(q_tile) + qb * K::Q + lane * (128 * 128), &mp.q, lane * 64, u.h * p.G, u.q.row0 + u.row / p.G,
-                          p.cu ? 0 : u.s, &sh->q_full[qb]);
+            if (lane < K::BLOCKS * tiles_q) {
+                const int x = lane % K::BLOCKS, y = lane / K::BLOCKS;  // (rows past the tensor's end are zeros)
+                tma_load4(smem_u32(q_tile) + (qb + y) * K::Q + x * (128 * 128), &mp.q, x * 64, u.h * p.G,
+                          u.q.row0 + u.row / p.G + y * mp.tok, p.cu ? 0 : u.s, &sh->q_full[qb]);
+            }
             ++units;
             bool has_next = false;
             for (int tile = u.tile; tile < u.last; ++tile, ++it) {
@@ -307,8 +373,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc(const __grid_constant__
         // nothing of the block's is in flight when it returns
         __syncwarp();
         for (int x = max(0, it - KS); x < it; ++x) mbar_wait_bounded(&sh->k_full[x % KS], (x / KS) & 1, kDrainPolls);
-        for (int x = max(0, units - K::QBUF); x < units; ++x)
-            mbar_wait_bounded(&sh->q_full[x % K::QBUF], (x / K::QBUF) & 1, kDrainPolls);
+        for (int x = max(0, units - q_bufs); x < units; ++x) mbar_wait_bounded(&sh->q_full[x % q_bufs], (x / q_bufs) & 1, kDrainPolls);
     } else if (warp == 7) {
         // --------------------------------------------------------------------------- load: V
         int it = 0;
@@ -362,32 +427,32 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc(const __grid_constant__
         // ----------------------------------------------------------------------------- issue
         const uint32_t lead = elect_lane();
         constexpr uint32_t id_qk = mma_desc(KT, false, false), id_pv = mma_desc(DP, false, true);
-        int units = 0, qk_left = 0, n_next = 0, it = 0, pv_unit = 0, pv_left = 0, pv_at = 0;
-        auto tiles = [&](int &n) {  // of the next unit; 0 after the last one
+        int units = 0, qk_left = 0, n_next = 0, it = 0, pv_unit = 0, pv_left = 0, pv_at = 0;  // it: steps
+        auto steps = [&](int &n) {  // of the next unit; 0 after the last one
             const int at = units % kQueue;
             if (!wait_warp(&sh->unit_full[at], (units / kQueue) & 1, waits)) return false;
-            n = sh->unit[at].s < 0 ? 0 : sh->unit[at].last - sh->unit[at].tile;
+            n = sh->unit[at].s < 0 ? 0 : (sh->unit[at].last - sh->unit[at].tile) * (pair ? 2 : 1);
             arrive_warp(&sh->unit_empty[at]);
             ++units;
             return true;
         };
         auto scores = [&](int i, bool first, bool last) {
-            const int qb = (units - 1) % K::QBUF, stage = i % KS;
-            if (first && !wait_warp(&sh->q_full[qb], ((units - 1) / K::QBUF) & 1, waits)) return false;
-            if (!wait_warp(&sh->k_full[stage], (i / KS) & 1, waits)) return false;
+            const int qb = (units - 1) % q_bufs, tile = pair ? i >> 1 : i, stage = tile % KS;
+            if (first && !wait_warp(&sh->q_full[qb], ((units - 1) / q_bufs) & 1, waits)) return false;
+            if (!wait_warp(&sh->k_full[stage], (tile / KS) & 1, waits)) return false;
             tmem_fence_after();
-            const uint32_t q = desc_k(smem_u32(q_tile) + qb * K::Q), k = desc_k(smem_u32(k_tile) + stage * K::KV);
+            const uint32_t q = desc_k(smem_u32(q_tile) + (pair ? i & 1 : qb) * K::Q), k = desc_k(smem_u32(k_tile) + stage * K::KV);
 #pragma unroll 4
             for (int x = 0; x < DP / 16; ++x)
                 mma_ss(lead, tm + (i & 1) * KT, q + (((x >> 2) * (128 * 128) + (x & 3) * 32) >> 4),
                        k + (((x >> 2) * (KT * 128) + (x & 3) * 32) >> 4), id_qk, x > 0);
             mma_commit(lead, &sh->s_full[i & 1]);
-            mma_commit(lead, &sh->k_empty[stage]);
+            if (!pair || (i & 1)) mma_commit(lead, &sh->k_empty[stage]);
             if (last) mma_commit(lead, &sh->q_empty[qb]);
             return true;
         };
         int n = 0;
-        bool ok = tiles(n) && n > 0;
+        bool ok = steps(n) && n > 0;
         if (ok) {
             qk_left = pv_left = n;
             ok = scores(0, true, n == 1);
@@ -399,23 +464,24 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc(const __grid_constant__
                 if (!scores(it + 1, false, qk_left == 1)) break;
                 --qk_left;
             } else if (n > 0) {
-                if (!tiles(n)) break;
+                if (!steps(n)) break;
                 n_next = n;
                 if (n > 0) {
                     if (!scores(it + 1, true, n == 1)) break;
                     qk_left = n - 1;
                 }
             }
-            const int ob = pv_unit % K::OBUF, stage = it % VS;
+            const int ob = pv_unit % K::OBUF, tile = pair ? it >> 1 : it, stage = tile % VS, g = GROUPS == 2 ? it & 1 : 0;
             if (pv_at == 0 && pv_unit >= K::OBUF && !wait_warp(&sh->o_free[ob], (pv_unit / K::OBUF - 1) & 1, waits)) break;
-            if (!wait_warp(&sh->v_full[stage], (it / VS) & 1, waits) || !wait_warp(&sh->p_ready[it & 1], (it >> 1) & 1, waits)) break;
+            if (!wait_warp(&sh->v_full[stage], (tile / VS) & 1, waits) || !wait_warp(&sh->p_ready[it & 1], (it >> 1) & 1, waits)) break;
             tmem_fence_after();
             const uint32_t v = desc_mn(smem_u32(v_tile) + stage * K::KV, KT * 128);
 #pragma unroll 4
             for (int x = 0; x < KT / 16; ++x)
-                mma_ts(lead, tm + K::COL_O + ob * DP, tm + (it & 1) * KT + x * 8, v + x * 128, id_pv, pv_at > 0 || x > 0);
-            mma_commit(lead, &sh->v_empty[stage]);
-            mma_commit(lead, &sh->pv_done);
+                mma_ts(lead, tm + K::COL_O + (ob * GROUPS + g) * DP, tm + (it & 1) * KT + x * 8, v + x * 128, id_pv,
+                       pv_at >= GROUPS || x > 0);
+            if (!pair || (it & 1)) mma_commit(lead, &sh->v_empty[stage]);
+            mma_commit(lead, &sh->pv_done[g]);
             ++it, ++pv_at;
             ok = true;
             if (--pv_left == 0) {
@@ -427,10 +493,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc(const __grid_constant__
         // nothing of the block's is in flight when it gives tensor memory back
         mma_commit(lead, &sh->last);
         mbar_wait_bounded(&sh->last, 0, kDrainPolls);
-    } else if (warp < 4) {
+    } else if (warp < 4 || GROUPS == 2) {
         // --------------------------------------------------------------------------- softmax
-        const int r = tid;  // the row
-        const uint32_t tl = tm + ((uint32_t)(32 * warp) << 16);
+        const int g = warp >= 8, w4 = warp & 3, r = 32 * w4 + lane;  // the group, and the row of its row tile
+        const uint32_t tl = tm + ((uint32_t)(32 * w4) << 16);
         int it = 0, s_before = -1, seqs = 0;  // seqs: sequences begun
         uint4 see = make_uint4(0, 0, 0, 0);
         bool ok = true;
@@ -442,24 +508,27 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc(const __grid_constant__
                 s_before = u.s, ++seqs;
             }
             // the unit two before has left its place
-            if (units >= 2 && !(ok = wait_warp(&sh->ml_free[b], ((units >> 1) - 1) & 1, waits))) break;
-            if (lane < 4) sh->bad[b][warp][lane] = 0;
+            if (!pair && units >= 2 && !(ok = wait_warp(&sh->ml_free[b], ((units >> 1) - 1) & 1, waits))) break;
+            if (lane < 4) sh->bad[b][4 * g + w4][lane] = 0;
             __syncwarp();
             const int end = u.L + u.T;
-            const bool active = 32 * warp < u.rows;
+            const bool active = 32 * w4 < (pair ? min(u.rows - g * half, half) : u.rows);
             float m = kNone, l = 0.f;
-            bool sees = false;
-            for (int tile = u.tile; tile < u.last; ++tile, ++it) {
+            bool sees = false, begun = false;
+            const int to_do = (u.last - u.tile) * (pair ? 2 : 1);
+            for (int step = 0; step < to_do; ++step, ++it) {
+                if (GROUPS == 2 && (it & 1) != g) continue;
+                const int tile = u.tile + (pair ? step >> 1 : step), key_tile = pair ? it >> 1 : it;
                 const int j0 = tile * KT, ahead = j0 + KT - u.L;  // keys of the tile that are no cached tokens
                 if (ahead > 0) {
                     if (!sees) {
                         if (!(ok = wait_warp(&sh->see_full[(seqs - 1) & 1], ((seqs - 1) >> 1) & 1, waits))) break;
-                        see = sh->see[(seqs - 1) & 1][min((u.row + r) / p.G, 127)];
+                        see = sh->see[(seqs - 1) & 1][min((u.row + (pair ? g * half : 0) + r) / p.G, 127)];
                         sees = true;
                     }
                     // rows of V past the end, and drafts' that are not finite
-                    const int stage = it % VS;
-                    if (!(ok = wait_warp(&sh->v_full[stage], (it / VS) & 1, waits))) break;
+                    const int stage = key_tile % VS;
+                    if (!(ok = wait_warp(&sh->v_full[stage], (key_tile / VS) & 1, waits))) break;
                     const int j = j0 + r;
                     if (r < KT && j >= u.L) {
                         unsigned char *const row = v_tile + stage * K::KV + r * 128;
@@ -468,7 +537,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc(const __grid_constant__
 #pragma unroll 4
                             for (int x = 0; x < DP / 8; ++x)
                                 clear |= not_finite(*reinterpret_cast<const uint4 *>(row + (x >> 3) * (KT * 128) + (x & 7) * 16));
-                            if (clear) atomicOr(&sh->bad[b][warp][(j - u.L) >> 5], 1u << ((j - u.L) & 31));
+                            if (clear) atomicOr(&sh->bad[b][4 * g + w4][(j - u.L) >> 5], 1u << ((j - u.L) & 31));
                         }
                         if (clear)
 #pragma unroll 4
@@ -480,49 +549,51 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc(const __grid_constant__
                 if (!(ok = wait_warp(&sh->s_full[it & 1], (it >> 1) & 1, waits))) break;
                 tmem_fence_after();
                 if (active) {
-                    uint32_t s[KT];
                     const uint32_t ts = tl + (it & 1) * KT;
+                    // Word w of the mask: whether the row sees keys j0 + 32 w and on.
+                    auto seen = [&](int w) {
+                        const int lo = 32 * w - (u.L - j0);  // draft of the word's first key
+                        if (lo <= -32) return 0xffffffffu;
+                        if (lo < 0) return ((1u << -lo) - 1) | see.x << -lo;
+                        const int word = lo >> 5;
+                        const uint32_t a = word == 0 ? see.x : word == 1 ? see.y : word == 2 ? see.z : word == 3 ? see.w : 0u;
+                        const uint32_t c = word == 0 ? see.y : word == 1 ? see.z : word == 2 ? see.w : 0u;
+                        return __funnelshift_r(a, c, lo & 31);
+                    };
+                    auto mask = [&](uint32_t *s, int w) {
+                        const uint32_t bits = seen(w);
+#pragma unroll
+                        for (int x = 0; x < 32; ++x)
+                            if (!(bits >> x & 1)) s[x] = __float_as_uint(kNone);
+                    };
+                    float top[4] = {kNone, kNone, kNone, kNone};
+                    auto most = [&](const uint32_t *s) {
+#pragma unroll
+                        for (int x = 0; x < 32; ++x) top[x & 3] = fmaxf(top[x & 3], __uint_as_float(s[x]));
+                    };
+                    uint32_t s[KT];
 #pragma unroll
                     for (int x = 0; x < KT; x += 32) tmem_ld32(s + x, ts + x);
                     tmem_wait_ld32(s);
 #pragma unroll
                     for (int x = 32; x < KT; x += 32) tmem_tie32(s + x);
-                    if (ahead > 0) {
-                        // bit i of the mask: whether the row sees key j0 + i
-                        const int off = u.L - j0;  // of draft 0 in the tile; below 0 it lies before the tile
 #pragma unroll
-                        for (int w = 0; w < KT / 32; ++w) {
-                            const int lo = 32 * w - off;  // draft of the word's first key
-                            uint32_t bits;
-                            if (lo <= -32) {
-                                bits = 0xffffffffu;
-                            } else if (lo < 0) {
-                                bits = (1u << -lo) - 1 | see.x << -lo;
-                            } else {
-                                const int word = lo >> 5;
-                                const uint32_t a = word == 0 ? see.x : word == 1 ? see.y : word == 2 ? see.z : word == 3 ? see.w : 0u;
-                                const uint32_t b = word == 0 ? see.y : word == 1 ? see.z : word == 2 ? see.w : 0u;
-                                bits = __funnelshift_r(a, b, lo & 31);
-                            }
-#pragma unroll
-                            for (int x = 0; x < 32; ++x)
-                                if (!(bits >> x & 1)) s[32 * w + x] = __float_as_uint(kNone);
-                        }
+                    for (int x = 0; x < KT; x += 32) {
+                        if (ahead > 0) mask(s + x, x / 32);
+                        most(s + x);
                     }
-                    float top[4] = {kNone, kNone, kNone, kNone};
-#pragma unroll
-                    for (int x = 0; x < KT; x += 4)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) top[e] = fmaxf(top[e], __uint_as_float(s[x + e]));
                     const float t = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * p.scale;
-                    if (tile == u.tile) {
+                    if (!begun) {
                         m = t;
                     } else if (__any_sync(0xffffffffu, t > m + kSlack)) {
                         const float f = t > m + kSlack ? exp2_fast(m - t) : 1.0f;
                         if (t > m + kSlack) m = t, l *= f;
-                        if (!(ok = wait_warp(&sh->pv_done, (it - 1) & 1, waits))) break;
+                        // (this group's last step: the one before, or the one before that)
+                        if (!(ok = GROUPS == 1 ? wait_warp(&sh->pv_done[0], (it - 1) & 1, waits)
+                                               : wait_warp(&sh->pv_done[g], ((it >> 1) - 1) & 1, waits)))
+                            break;
                         tmem_fence_after();
-                        const uint32_t to = tl + K::COL_O + ob * DP;
+                        const uint32_t to = tl + K::COL_O + (ob * GROUPS + g) * DP;
 #pragma unroll 1
                         for (int x = 0; x < DP; x += 16) {
                             uint32_t o[16];
@@ -541,32 +612,46 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc(const __grid_constant__
                         uint32_t w[16];
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
-                            float a, b;
-                            f2_unpack(f2_fma(f2_pack(__uint_as_float(s[x + 2 * e]), __uint_as_float(s[x + 2 * e + 1])), c2, b2), a, b);
-                            a = exp2_fast(a), b = exp2_fast(b);
-                            sum[e & 1] = f2_add(sum[e & 1], f2_pack(a, b));
-                            w[e] = pack_bf16(a, b);
+                            float a, c;
+                            f2_unpack(f2_fma(f2_pack(__uint_as_float(s[x + 2 * e]), __uint_as_float(s[x + 2 * e + 1])), c2, b2), a, c);
+                            a = exp2_fast(a), c = exp2_fast(c);
+                            sum[e & 1] = f2_add(sum[e & 1], f2_pack(a, c));
+                            w[e] = pack_bf16(a, c);
                         }
                         tmem_st16(ts + x / 2, w);
                     }
-                    float a, b;
-                    f2_unpack(f2_add(sum[0], sum[1]), a, b);
-                    l += a + b;
+                    float a, c;
+                    f2_unpack(f2_add(sum[0], sum[1]), a, c);
+                    l += a + c;
                     tmem_wait_st();
                     tmem_fence_before();
                 }
+                begun = true;
                 arrive_warp(&sh->p_ready[it & 1]);
             }
             if (!ok) break;
-            sh->m[b][r] = m, sh->l[b][r] = l;
+            if (!pair) {
+                sh->m[b][r] = m, sh->l[b][r] = l;
+                arrive_warp(&sh->ml_full[b]);
+                continue;
+            }
+            // its own rows, once both groups' notes of drafts are there (one may have cleared a row before the other looked)
             arrive_warp(&sh->ml_full[b]);
+            if (!(ok = wait_warp(&sh->see_full[(seqs - 1) & 1], ((seqs - 1) >> 1) & 1, waits)) ||
+                !(ok = wait_warp(&sh->ml_full[b], (units >> 1) & 1, waits)) || !(ok = wait_warp(&sh->o_full[ob], (units / K::OBUF) & 1, waits)))
+                break;
+            tmem_fence_after();
+            leave(u, g, tl + K::COL_O + (ob * GROUPS + g) * DP, r, m, l, b, (seqs - 1) & 1);
+            tmem_fence_before();
+            arrive_warp(&sh->o_free[ob]);
         }
+        if (pair && g == 0 && r == 0) left_out();
     } else {
         // ---------------------------------------------------------------------------- output
         const int w4 = warp - 8, r = 32 * w4 + lane;  // the row
         const uint32_t tl = tm + ((uint32_t)(32 * w4) << 16);
         int s_before = -1, seqs = 0;
-        bool ok = true, goes_on = false, came = false;  // parts left in slots 1 and 0
+        bool ok = true;
         TcUnit u;
         for (int units = 0; ok && (ok = pop(u, units)) && u.s >= 0; ++units) {
             const int ob = units % K::OBUF, b = units & 1;
@@ -579,68 +664,16 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc(const __grid_constant__
                 !(ok = wait_warp(&sh->o_full[ob], (units / K::OBUF) & 1, waits)))
                 break;
             tmem_fence_after();
-            const bool bad_unit = sh->flags[(seqs - 1) & 1] != 0, cut = u.last - u.tile < u.tiles;
-            const float m = sh->m[b][r], l = sh->l[b][r];
-            const uint32_t to = tl + K::COL_O + ob * DP;
-            goes_on = cut && u.begins && !bad_unit;
-            came |= cut && !u.begins && !bad_unit;
-            if (32 * w4 < u.rows && !bad_unit) {
-                uint32_t bad[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) bad[i] = sh->bad[b][0][i] | sh->bad[b][1][i] | sh->bad[b][2][i] | sh->bad[b][3][i];
-                if (bad[0] | bad[1] | bad[2] | bad[3])
-                    add_bad_drafts<DP>(p, u, bad, sh->see[(seqs - 1) & 1][min((u.row + r) / p.G, 127)], r, m, to);
-                const float inv = cut ? 1.0f : 1.0f / l;
-                float *const part = cut ? attn_part(p, blockIdx.x, u.begins) : nullptr;
-                if (cut && r < u.rows) part[kPartHead + r] = m, part[kPartHead + p.pad + r] = l;
-                uint16_t *const out = reinterpret_cast<uint16_t *>(p.out) + (p.cu ? 0LL : (long long)u.s * p.o_seq) +
-                                      (long long)(u.row0 + (u.row + r) / p.G) * p.o_tok +
-                                      (long long)(u.h * p.G + (u.row + r) % p.G) * p.o_head;
-#pragma unroll 1
-                for (int x = 0; x < DP; x += 32) {
-                    uint32_t o[32];
-                    tmem_ld32(o, to + x);
-                    tmem_wait_ld32(o);
-                    if (r < u.rows && cut) {
-                        float4 *const dst = reinterpret_cast<float4 *>(part + kPartHead + 2 * p.pad + (long long)r * DP + x);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            dst[e] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]), __uint_as_float(o[4 * e + 2]),
-                                                 __uint_as_float(o[4 * e + 3]));
-                    } else if (r < u.rows) {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            if (x + 8 * e >= p.c.d) break;  // (d is a multiple of 8)
-                            uint32_t w[4];
-#pragma unroll
-                            for (int y = 0; y < 4; ++y)
-                                w[y] = pack_bf16(__uint_as_float(o[8 * e + 2 * y]) * inv, __uint_as_float(o[8 * e + 2 * y + 1]) * inv);
-                            if (mp.o_vec) {
-                                *reinterpret_cast<uint4 *>(out + x + 8 * e) = make_uint4(w[0], w[1], w[2], w[3]);
-                            } else {
-#pragma unroll
-                                for (int y = 0; y < 4; ++y) {
-                                    out[x + 8 * e + 2 * y] = (uint16_t)w[y];
-                                    out[x + 8 * e + 2 * y + 1] = (uint16_t)(w[y] >> 16);
-                                }
-                            }
-                        }
-                    }
-                    __syncwarp();
-                }
-            }
-            if (cut && !bad_unit && r == 0)
-                attn_part_head(attn_part(p, blockIdx.x, u.begins), range, u.first, u.tiles, u.rows, u.row, u.s, u.h, u.row0);
+            leave(u, 0, tl + K::COL_O + ob * DP, r, sh->m[b][r], sh->l[b][r], b, (seqs - 1) & 1);
             tmem_fence_before();
             arrive_warp(&sh->o_free[ob]);
             arrive_warp(&sh->ml_free[b]);
         }
-        // the join reads both slots of every block
-        if (p.ws && r == 0 && !goes_on) *reinterpret_cast<int *>(attn_part(p, blockIdx.x, 1)) = 0;
-        if (p.ws && r == 0 && !came) *reinterpret_cast<int *>(attn_part(p, blockIdx.x, 0)) = 0;
+        if (r == 0) left_out();
     }
     __syncwarp();
-    tmem_wait_st();  // (of a role that gave up)
+    asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory");  // (of a role that gave up)
+    tmem_wait_st();
     tmem_fence_before();
     __syncthreads();
     if (tid == 0 && sh->dead) {
@@ -659,13 +692,17 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc(const __grid_constant__
     }
 }
 
-template <int DP>
+template <int DP, int GROUPS>
 AttnTc tc() {
-    return {attn_tc<DP>, tc_smem<DP>(), Tc<DP>::KT, kTcThreads};
+    return {attn_tc<DP, GROUPS>, tc_smem<DP, GROUPS>(), Tc<DP, GROUPS>::KT, kTcThreads};
 }
 
 }  // namespace
 
-AttnTc attn_tc_kernel(int dp) { return dp == 64 ? tc<64>() : dp == 128 ? tc<128>() : dp == 192 ? tc<192>() : tc<256>(); }
+AttnTc attn_tc_kernel(int dp, bool two) {
+    if (dp == 64) return two ? tc<64, 2>() : tc<64, 1>();
+    if (dp == 128) return two ? tc<128, 2>() : tc<128, 1>();
+    return dp == 192 ? tc<192, 1>() : tc<256, 1>();
+}
 
 }  // namespace cvk
