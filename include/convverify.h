@@ -556,6 +556,9 @@ CV_API int cv_block_norm(const cv_norm_args *args, void *stream);
  * and write layer 0 (pass the layer's own address).  page_table entries past those a call needs are not read.
  *   held   int32 [n_slots]: pages of each slot (reserve, fork, free; else may be NULL)
  *   refs   int32 [n_pages]: slots that hold each page, 0 = free (reserve, fork, free; else may be NULL)
+ * Preconditions the library cannot check: distinct sequences of a call use distinct slots, except where a call only reads the cache;
+ * calls that change a cache, its table or its counts are ordered with the calls that use them; k and v do not overlap each other or an
+ * input.
  * Sizes: n_layers 1..4096, n_pages 1..2^31-1, page_size 1..65536, n_kv_heads 1..4096, head_dim 1..256, n_slots >= 1,
  * max_pages >= 1, max_pages * page_size < 2^31 (else CV_ERR_SHAPE; head_dim: CV_ERR_HEAD_DIM).
  */
@@ -626,7 +629,7 @@ CV_API int cv_tree_attention_workspace(const cv_tree_attention_args *args, int64
  *     without: probs[c], the children's tokens left out;   where all w are 0: probs[c]
  *     new = the lowest token whose cumulative weight exceeds uniforms[s][T] * the sum of w
  * Weights are summed exactly, in units of 2^-60 (values are cut off there, and at 2; what is not above 0, NaN among it,
- * counts as 0).  Comparisons are made in 64 bits.  A uniform counts as within [0, 1).
+ * counts as 0).  Comparisons are made in 64 bits, on the values as they are.  A uniform counts as within [0, 1).
  *   n_seq 0..65535, T 1..CV_MAX_T, vocab 1..2^24; dtype of probs and draft_probs, innermost stride 1
  *   tokens             int32 [n_seq][T] (cu_draft: [total_tokens]); parent likewise or NULL (a chain)
  *   uniforms           fp32 [n_seq][T + 1] contiguous
