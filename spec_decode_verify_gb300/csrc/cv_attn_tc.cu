@@ -503,12 +503,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc(const __grid_constant__
         TcUnit u;
         for (int units = 0; ok && (ok = pop(u, units)) && u.s >= 0; ++units) {
             const int ob = units % K::OBUF, b = units & 1;
+            // the unit two before has left its place (and its sequence's masks: no warp is two sequences ahead of another)
+            if (!pair && units >= 2 && !(ok = wait_warp(&sh->ml_free[b], ((units >> 1) - 1) & 1, waits))) break;
             if (u.s != s_before) {
                 if (seqs > 0) arrive_warp(&sh->see_empty[(seqs - 1) & 1]);
                 s_before = u.s, ++seqs;
             }
-            // the unit two before has left its place
-            if (!pair && units >= 2 && !(ok = wait_warp(&sh->ml_free[b], ((units >> 1) - 1) & 1, waits))) break;
             if (lane < 4) sh->bad[b][4 * g + w4][lane] = 0;
             __syncwarp();
             const int end = u.L + u.T;
@@ -526,8 +526,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc(const __grid_constant__
                         see = sh->see[(seqs - 1) & 1][min((u.row + (pair ? g * half : 0) + r) / p.G, 127)];
                         sees = true;
                     }
-                    // rows of V past the end, and drafts' that are not finite
+                    // Rows of V past the end, and drafts' that are not finite.  A stage is not touched before the tile that it held
+                    // before has been read: it has once this step's scores are there, whose product was issued after that
+                    // one's.  (V's barrier alone does not tell: two phases back looks like this one.)
                     const int stage = key_tile % VS;
+                    if (key_tile >= VS && !(ok = wait_warp(&sh->s_full[it & 1], (it >> 1) & 1, waits))) break;
                     if (!(ok = wait_warp(&sh->v_full[stage], (key_tile / VS) & 1, waits))) break;
                     const int j = j0 + r;
                     if (r < KT && j >= u.L) {
