@@ -20,7 +20,7 @@ INCLUDE = os.path.join(ROOT, "include")
 # the library (conv, linear attention, block norms, attention layers), then (last) the bandwidth probe of bench.py --probe-mix, linked on its own
 SOURCES = (["cv_abi.cu"] + [f"cv_inst_{d}_w{w}.cu" for d in ("bf16", "f32") for w in (2, 3, 4)] +
            [f"cv_inst_varlen_{d}_w{w}.cu" for d in ("bf16", "f32") for w in (2, 3, 4)] +
-           ["cv_abi_attn.cu", "cv_attn_tc.cu", "cv_attn_simt.cu", "cv_sample.cu", "cv_rope.cu", "cv_pages.cu",
+           ["cv_abi_attn.cu", "cv_attn_tc.cu", "cv_attn_simt.cu", "cv_attn_few.cu", "cv_sample.cu", "cv_rope.cu", "cv_pages.cu",
             "cv_abi_layer.cu", "cv_linattn_step.cu", "cv_linattn_chunk.cu", "cv_norm.cu", "cv_probe.cu"])
 PROBE_LIB = os.path.join(BUILD, "libcvprobe.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

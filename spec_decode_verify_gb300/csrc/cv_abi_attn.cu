@@ -122,9 +122,12 @@ AttnPlan plan_attention(const cv_tree_attention_args *a, bool tc = true) {
                          rows16(c.v, 0, c.v_page_stride, c.v_row_stride, c.v_head_stride, c) && aligned16(a->q) &&
                          a->q_seq_stride * es % 16 == 0 && a->q_tok_stride * es % 16 == 0 && a->q_head_stride * es % 16 == 0;
         if (pl.dp == 192) pl.dp = 256;
-        pl.simt = cvk::attn_simt_kernel(c.dtype == CV_BF16, pl.dp, vec);
-        pl.rows = cvk::kSimtRows, pl.keys = pl.simt.keys;
-        const int resident = lim.smem_per_sm / (pl.simt.smem_bytes + 1024);
+        const int64_t rows = (int64_t)a->T * G;
+        const bool few = vec && rows <= cvk::kFewRows;
+        pl.rows = !few ? cvk::kSimtRows : rows <= 4 ? 4 : 8;
+        pl.simt = few ? cvk::attn_few_kernel(c.dtype == CV_BF16, pl.dp, pl.rows) : cvk::attn_simt_kernel(c.dtype == CV_BF16, pl.dp, vec);
+        pl.keys = pl.simt.keys;
+        const int resident = few && pl.dp > 128 ? 1 : lim.smem_per_sm / (pl.simt.smem_bytes + 1024);
         pl.parts = lim.sms * (resident < 1 ? 1 : resident > 2 ? 2 : resident);
         pl.unit_cost = kSimtUnitCost;
     }

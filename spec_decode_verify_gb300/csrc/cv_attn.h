@@ -45,6 +45,7 @@ struct AttnMaps {
     int o_vec;       // out allows 16-byte accesses
 };
 constexpr int kSimtRows = 32, kSimtThreads = 256;
+constexpr int kFewRows = 8, kFewThreads = 256, kFewKeys = 64;  // rows at most, keys a tile
 constexpr int kPartHead = 16;  // ints before a partial's maxima, sums and outputs, each of them 16-byte aligned
 __host__ __device__ constexpr long long part_floats(int pad, int dp) { return kPartHead + 2 * pad + (long long)pad * dp; }
 
@@ -59,6 +60,7 @@ struct AttnTc {
     int smem_bytes, keys, threads;
 };
 AttnSimt attn_simt_kernel(bool bf16, int dp, bool vec);
+AttnSimt attn_few_kernel(bool bf16, int dp, int rows);  // rows: 4 or 8
 AttnTc attn_tc_kernel(int dp, bool two);  // two: units of two row tiles (up to 128 channels)
 AttnKernel attn_join_kernel(bool bf16, int dp);
 constexpr int kAttnJoinThreads = 256, kAttnJoinY = 4;
