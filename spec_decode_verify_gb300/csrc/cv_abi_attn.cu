@@ -76,7 +76,8 @@ int check_attention(const cv_tree_attention_args *a, bool pointers) {
     return CV_OK;
 }
 
-// What a unit takes beside its tiles, in tiles.
+// What a unit takes beside its tiles, in tiles, when the blocks' runs are made equal.  Tensor cores, 128 sequences of 8 drafts over 8k: 0 to
+// 3 tiles 228, 210, 199 and 198 us.  fp32 products, 13 tokens of 64/8 heads over 3k: 0, 1 and 3 tiles 74, 66 and 72 us.
 constexpr int kTcUnitCost = 3, kSimtUnitCost = 1;
 
 struct AttnPlan {
@@ -109,6 +110,8 @@ AttnPlan plan_attention(const cv_tree_attention_args *a, bool tc = true) {
     const cvk::DeviceLimits lim = device_limits();
     pl.dp = d <= 64 ? 64 : d <= 128 ? 128 : d <= 192 ? 192 : 256;
     pl.tok = G <= 128 ? (a->T < 128 / G ? a->T : 128 / G) : 1;
+    // More rows than one tile of 128: two row tiles a unit, so that a tile of keys is read once for both (17 drafts of 64/8 heads over 100k
+    // 141 us with a unit each, 111 with one).  Tensor memory has room for two up to 128 channels.
     pl.pair = pl.dp <= 128 && a->T > pl.tok;
     pl.tc = cvk::attn_tc_kernel(pl.dp, pl.pair);
     pl.on_tc = tc && tc_takes(a, pl.tc.keys);
@@ -122,6 +125,8 @@ AttnPlan plan_attention(const cv_tree_attention_args *a, bool tc = true) {
                          rows16(c.v, 0, c.v_page_stride, c.v_row_stride, c.v_head_stride, c) && aligned16(a->q) &&
                          a->q_seq_stride * es % 16 == 0 && a->q_tok_stride * es % 16 == 0 && a->q_head_stride * es % 16 == 0;
         if (pl.dp == 192) pl.dp = 256;
+        // Up to 8 rows share too little for a tile in shared memory (fp32, device time there and in registers: 13 tokens of 64/8 heads
+        // of 128 over 3k 119 and 66 us, 16 of 8/8 heads of 256 over 4k 374 and 151, 23 of 4/2 heads of 64 over 2.3k 27 and 22).
         const int64_t rows = (int64_t)a->T * G;
         const bool few = vec && rows <= cvk::kFewRows;
         pl.rows = !few ? cvk::kSimtRows : rows <= 4 ? 4 : 8;

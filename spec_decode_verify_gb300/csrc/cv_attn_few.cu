@@ -6,9 +6,13 @@
 //
 // Layout.  Nothing of K and V is used twice by few rows, so they go from memory to registers and not through shared
 // memory: a warp takes 8 keys of every 64, a lane 4 channels of a key (8 of 256; 64 channels are half a warp's), with
-// the rows of O that it needs of them in registers (those of Q as well left no room for the loads ahead).  The lanes' sums of R rows by NK keys are added up by halves that are
-// exchanged, which leaves each lane the score of one row and one key in 31 shuffles, and one exponential a lane.  The warps have
+// the rows of O that it needs of them in registers (those of Q as well spilled: 75 us against 67 for 13 tokens of 64/8 heads of 128
+// over 3k).  The 16 sums of R rows and NK keys are added up over the lanes by halves that are exchanged, 15 shuffles, after
+// which a lane has the score of one row and one key, and one exponential.  (Four keys a lane: 69 us.)  The warps have
 // maxima, sums and outputs of their own, which are joined at a unit's end.
+//
+// HBM bounds one row a head: 16 tokens of 8 heads of 256 over 4k take 152 us, 5.9 TB/s.  Eight rows are bound by the shuffles and
+// the reads of Q in shared memory: the 13 tokens take 67 us, 2.8 TB/s.
 #include "cv_attn.cuh"
 
 namespace cvk {
@@ -71,7 +75,7 @@ template <int DP, int R>
 struct Few {
     static constexpr int NV = DP > 128 ? 2 : 1;                // pieces of 4 channels of a lane
     static constexpr int LANES = DP / (4 * NV), SIDES = 32 / LANES;  // lanes of a key; keys side by side in a warp
-    static constexpr int NK = DP > 128 ? 16 / R : DP > 64 ? 4 : LANES / R;  // keys that a lane has at a time
+    static constexpr int NK = 16 / R;                          // keys that a lane has at a time
     static constexpr int GROUP = NK * SIDES, VALS = R * NK, SAME = LANES / VALS;  // SAME: lanes that end up with the same score
     static_assert(kRun % GROUP == 0 && VALS * SAME == LANES, "a warp's keys of a tile are whole groups");
 };
