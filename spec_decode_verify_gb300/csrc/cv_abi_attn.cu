@@ -103,7 +103,9 @@ bool tc_takes(const cv_tree_attention_args *a, int keys) {
            (a->cu_draft || dim(a->q_seq_stride, a->n_seq));
 }
 
-AttnPlan plan_attention(const cv_tree_attention_args *a, bool tc = true) {
+// Kernels from the most particular one down that a plan may use.
+enum { kAnyAlignment, kWholePieces, kTensorCores };
+AttnPlan plan_attention(const cv_tree_attention_args *a, int best = kTensorCores) {
     const cv_cache &c = a->cache;
     const int es = esize_of(c.dtype), G = a->n_heads / c.n_kv_heads, d = c.head_dim;
     AttnPlan pl;
@@ -114,7 +116,7 @@ AttnPlan plan_attention(const cv_tree_attention_args *a, bool tc = true) {
     // 141 us with a unit each, 111 with one).  Tensor memory has room for two up to 128 channels.
     pl.pair = pl.dp <= 128 && a->T > pl.tok;
     pl.tc = cvk::attn_tc_kernel(pl.dp, pl.pair);
-    pl.on_tc = tc && tc_takes(a, pl.tc.keys);
+    pl.on_tc = best >= kTensorCores && tc_takes(a, pl.tc.keys);
     if (pl.on_tc) {
         pl.keys = pl.tc.keys;
         pl.rows = pl.tok * G * (pl.pair ? 2 : 1);
@@ -128,7 +130,7 @@ AttnPlan plan_attention(const cv_tree_attention_args *a, bool tc = true) {
         // Up to 8 rows share too little for a tile in shared memory (fp32, device time there and in registers: 13 tokens of 64/8 heads
         // of 128 over 3k 119 and 66 us, 16 of 8/8 heads of 256 over 4k 374 and 151, 23 of 4/2 heads of 64 over 2.3k 27 and 22).
         const int64_t rows = (int64_t)a->T * G;
-        const bool few = vec && rows <= cvk::kFewRows;
+        const bool few = best >= kWholePieces && vec && rows <= cvk::kFewRows;
         pl.rows = !few ? cvk::kSimtRows : rows <= 4 ? 4 : 8;
         pl.simt = few ? cvk::attn_few_kernel(c.dtype == CV_BF16, pl.dp, pl.rows) : cvk::attn_simt_kernel(c.dtype == CV_BF16, pl.dp, vec);
         pl.keys = pl.simt.keys;
@@ -418,11 +420,11 @@ int cv_tree_attention_workspace(const cv_tree_attention_args *args, int64_t *byt
     if (rc != CV_OK) return rc;
     *bytes = 0;
     if (args->n_seq == 0) return CV_OK;
-    // NULL pointers count as aligned; the call's own may be aligned to less and take the other kernel
-    *bytes = plan_attention(args).bytes;
-    if (!args->q || !args->cache.k || !args->cache.v) {
-        const int64_t other = plan_attention(args, false).bytes;
-        *bytes = *bytes > other ? *bytes : other;
+    // NULL pointers count as aligned; the call's own may be aligned to less and take another kernel
+    const bool known = args->q && args->cache.k && args->cache.v;
+    for (int best = kTensorCores; best >= (known ? kTensorCores : kAnyAlignment); --best) {
+        const int64_t n = plan_attention(args, best).bytes;
+        *bytes = *bytes > n ? *bytes : n;
     }
     return CV_OK;
 }
