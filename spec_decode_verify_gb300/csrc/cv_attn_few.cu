@@ -11,8 +11,9 @@
 // which a lane has the score of one row and one key, and one exponential.  (Four keys a lane: 69 us.)  The warps have
 // maxima, sums and outputs of their own, which are joined at a unit's end.
 //
-// HBM bounds one row a head: 16 tokens of 8 heads of 256 over 4k take 152 us, 5.9 TB/s.  Eight rows are bound by the shuffles and
-// the reads of Q in shared memory: the 13 tokens take 67 us, 2.8 TB/s.
+// HBM bounds one row a head: 16 tokens of 8 heads of 256 over 4k take 151 us, 5.9 TB/s; 13 tokens of 32/8 heads of 128 over 6k take 80, 4.9
+// TB/s.  With 8 rows instructions (half of the issue slots) and the loads' latency share the time, which 128 registers do not
+// hide better: 13 tokens of 64/8 heads over 20k take 330 us, 3.9 TB/s, and 338 with the loads two steps ahead, which spill.
 #include "cv_attn.cuh"
 
 namespace cvk {
