@@ -560,7 +560,7 @@ CV_API int cv_block_norm(const cv_norm_args *args, void *stream);
  * calls that change a cache, its table or its counts are ordered with the calls that use them; k and v do not overlap each other or an
  * input.
  * Sizes: n_layers 1..4096, n_pages 1..2^31-1, page_size 1..65536, n_kv_heads 1..4096, head_dim 1..256, n_slots >= 1,
- * max_pages >= 1, max_pages * page_size < 2^31 (else CV_ERR_SHAPE; head_dim: CV_ERR_HEAD_DIM).
+ * max_pages >= 1, max_pages * page_size <= 2^31 - 256 (else CV_ERR_SHAPE; head_dim: CV_ERR_HEAD_DIM).
  */
 typedef struct cv_cache {
     void *k, *v;

@@ -14,7 +14,7 @@ using cvk::device_limits;
 using cvk::launch_pdl;
 
 constexpr int kMaxHeads = 4096, kMaxLayers = 4096, kMaxPage = 65536, kMaxHeadDim = 256, kMaxVocab = 1 << 24;
-constexpr int64_t kMaxTokens = 0x7fffffff;
+constexpr int64_t kMaxTokens = 0x7fffffff - 255;  // the end of a tile that begins within them is an int too
 constexpr int64_t kMaxStride = 1LL << 38;  // elements: a tensor map's strides are below 2^40 bytes
 constexpr unsigned kPolls = 65536;         // of up to 20 us each
 

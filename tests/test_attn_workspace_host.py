@@ -34,3 +34,14 @@ def test_unknown_pointers(dtype, T, n_heads, head_dim, page):
     most = need(None, None, None)
     sizes = {need(at + x, at + y, at + z) for x in (0, 4) for y in (0, 4) for z in (0, 4)}
     assert most >= max(sizes) > 0
+
+
+@pytest.mark.parametrize("page,pages,status", [(1, 2 ** 31 - 1, -3), (1, 2 ** 31 - 255, -3), (1, 2 ** 31 - 256, 0), (128, 2 ** 24 - 2, 0),
+                                               (128, 2 ** 24 - 1, -3), (65536, 32767, 0), (65536, 32768, -3)])
+def test_longest_tables(page, pages, status):
+    """A tile that begins within a table's tokens ends below 2^31."""
+    a, n = cv.TreeAttentionArgs(), ctypes.c_int64()
+    c = a.cache
+    c.n_layers, c.n_pages, c.page_size, c.n_kv_heads, c.head_dim, c.n_slots, c.max_pages = 1, 4, page, 1, 8, 1, pages
+    a.n_seq, a.T, a.n_heads, a.scale = 1, 1, 1, 1.0
+    assert cv.load_library().cv_tree_attention_workspace(ctypes.byref(a), ctypes.byref(n)) == status
