@@ -661,7 +661,8 @@ CV_API int cv_draft_verify(const cv_draft_verify_args *args, void *stream);
  *     (y[a], y[b]) = (y[a] cos - y[b] sin, y[b] cos + y[a] sin)    pair i: a = i, b = i + rot_dim/2; pairs != 0: a = 2i, b = 2i+1
  * with cos = cos_sin[position][i] and sin = cos_sin[position][rot_dim/2 + i], position = positions of the token, or
  * cache_len[s] + t without them.
- *   tokens             [n_seq][T], or with cu [total_tokens] packed, T then bounds a sequence's length
+ *   tokens             [n_seq][T], or with cu [total_tokens] packed, T then bounds a sequence's length; a row of several sequences (where cu
+ *                      falls) goes to each one's cache, and to q_out and k_out for the last of them
  *   q, q_out           .. [n_heads][head_dim] (q_out may be q); k .. [n_kv_heads][head_dim]
  *   k_out              like k, or NULL;  cache (page_table not NULL): K goes to position cache_len[s] + t, and so does v,
  *                      .. [n_kv_heads][head_dim], unrounded, unless NULL.  One of k_out and the cache is needed unless n_kv_heads = 0

@@ -35,41 +35,53 @@ __device__ __forceinline__ void store8(B *p, const Raw8<B> &r) {
 #pragma unroll
     for (int h = 0; h < (int)sizeof(B) / 2; ++h) st16(p + 8 / (sizeof(B) / 2) * h, r.w[h]);
 }
-// Where token `tok` (of all) reads and writes.
-__device__ __forceinline__ TokenAt token_at(const RopeParams &p, long long tok) {
+// What is known of sequence s without its tokens.
+struct SeqAt {
+    int slot, L, n, row0, status;  // n, row0: its tokens and the first one's row with cu
+};
+__device__ __forceinline__ SeqAt seq_at(const RopeParams &p, int s) {
+    SeqAt q;
+    q.slot = p.idx ? __ldg(p.idx + s) : s;
+    q.L = p.len ? __ldg(p.len + s) : 0;
+    q.n = p.T, q.row0 = 0, q.status = 0;
+    if (p.cu) q.status = draft_span(p.cu, s, p.T, p.total, q.n, q.row0);
+    if (q.status) q.n = 0;
+    if (p.paged) {
+        if (q.slot >= p.c.n_slots) q.status |= kSeqBadSlot;
+        if (q.L < 0 || (long long)q.L + q.n > (long long)p.c.max_pages * p.c.page) q.status |= kSeqBadLength;
+    } else if (q.L < 0) {
+        q.status |= kSeqBadLength;
+    }
+    if (q.slot < 0) q.status = 0;
+    return q;
+}
+// The flags of sequences that no token may tell of (of packed rows, or none), each raised by one block; and whether counts fall
+// anywhere: then a row may belong to several sequences.  Every thread of the block calls this.
+__device__ __forceinline__ bool check_sequences(const RopeParams &p) {
+    bool falls = false;
+    for (int s = threadIdx.x; s < p.n_seq; s += kRopeThreads) {
+        if (p.cu) falls |= __ldg(p.cu + s + 1) < __ldg(p.cu + s);
+        if (p.err && s % (int)gridDim.x == (int)blockIdx.x) {
+            const SeqAt q = seq_at(p, s);
+            if (q.status) atomicOr(p.err + s, q.status);
+        }
+    }
+    return __syncthreads_or(falls);
+}
+// Where sequence s reads and writes token `tok` (of all).
+__device__ __forceinline__ TokenAt token_of(const RopeParams &p, int s, long long tok) {
     TokenAt a;
     a.on = 0;
-    int s, t, n = p.T, row0 = 0, status = 0;
-    if (p.cu) {
-        if (tok < __ldg(p.cu) || tok >= __ldg(p.cu + p.n_seq)) return a;  // (a row of no sequence)
-        int lo = 0, hi = p.n_seq - 1;
-        while (lo < hi) {  // the last sequence that begins at or before it
-            const int mid = (lo + hi + 1) >> 1;
-            if (__ldg(p.cu + mid) <= tok) lo = mid;
-            else hi = mid - 1;
-        }
-        s = lo;
-        status = draft_span(p.cu, s, p.T, p.total, n, row0);
-        t = (int)(tok - row0);
-        if (status) n = 0;
-        else if (t < 0 || t >= n) return a;
-    } else {
-        s = (int)(tok / p.T), t = (int)(tok - (long long)s * p.T);
-    }
-    const int slot = p.idx ? __ldg(p.idx + s) : s;
-    if (slot < 0) return a;
-    const int L = p.len ? __ldg(p.len + s) : 0;
-    if (p.paged) {
-        if (slot >= p.c.n_slots) status |= kSeqBadSlot;
-        if (L < 0 || (long long)L + n > (long long)p.c.max_pages * p.c.page) status |= kSeqBadLength;
-    } else if (L < 0) {
-        status |= kSeqBadLength;
-    }
+    const SeqAt q = seq_at(p, s);
+    const int t = p.cu ? (int)(tok - q.row0) : (int)(tok - (long long)s * p.T);
+    if (q.slot < 0) return a;
+    int status = q.status;
     if (!status) {
-        a.pos = p.pos ? __ldg(p.pos + tok) : (int)((unsigned)L + (unsigned)t);
+        if (t < 0 || t >= q.n) return a;
+        a.pos = p.pos ? __ldg(p.pos + tok) : (int)((unsigned)q.L + (unsigned)t);
         if (p.rot > 0 && (a.pos < 0 || a.pos >= p.n_pos)) status |= kSeqBadPosition;
         if (p.paged) {
-            const int at = L + t, pg = __ldg(p.c.table + (long long)slot * p.c.table_row + at / p.c.page);
+            const int at = q.L + t, pg = __ldg(p.c.table + (long long)q.slot * p.c.table_row + at / p.c.page);
             if (pg < 0 || pg >= p.c.n_pages) status |= kSeqBadPage;
             else {
                 a.kc = (long long)pg * p.c.k_page + (long long)(at % p.c.page) * p.c.k_row;
@@ -88,8 +100,22 @@ __device__ __forceinline__ TokenAt token_at(const RopeParams &p, long long tok) 
     a.on = 1;
     return a;
 }
+// The same of the sequence that the token belongs to, where counts do not fall.
+__device__ __forceinline__ TokenAt token_at(const RopeParams &p, long long tok) {
+    if (!p.cu) return token_of(p, (int)(tok / p.T), tok);
+    TokenAt none;
+    none.on = 0;
+    if (tok < __ldg(p.cu) || tok >= __ldg(p.cu + p.n_seq)) return none;  // (a row of no sequence)
+    int lo = 0, hi = p.n_seq - 1;
+    while (lo < hi) {  // the last sequence that begins at or before it
+        const int mid = (lo + hi + 1) >> 1;
+        if (__ldg(p.cu + mid) <= tok) lo = mid;
+        else hi = mid - 1;
+    }
+    return token_of(p, lo, tok);
+}
 
-// A head's row: what it is read from and written to (a key may go to two places).
+// A head's row: what it is read from and written to (a key may go to two places, or with outs = false to the cache alone).
 template <typename B>
 struct HeadRow {
     const B *from, *w;
@@ -97,7 +123,7 @@ struct HeadRow {
     bool norm, turn;
 };
 template <typename B>
-__device__ __forceinline__ HeadRow<B> head_row(const RopeParams &p, const TokenAt &a, int h) {
+__device__ __forceinline__ HeadRow<B> head_row(const RopeParams &p, const TokenAt &a, int h, bool outs) {
     HeadRow<B> r;
     r.to2 = nullptr;
     if (h < p.n_heads) {
@@ -109,7 +135,7 @@ __device__ __forceinline__ HeadRow<B> head_row(const RopeParams &p, const TokenA
     h -= p.n_heads;
     if (h < p.n_kv) {
         r.from = reinterpret_cast<const B *>(p.k) + a.k + (long long)h * p.k_head;
-        B *const out = p.k_out ? reinterpret_cast<B *>(p.k_out) + a.ko + (long long)h * p.ko_head : nullptr;
+        B *const out = p.k_out && outs ? reinterpret_cast<B *>(p.k_out) + a.ko + (long long)h * p.ko_head : nullptr;
         B *const in = p.paged ? reinterpret_cast<B *>(p.c.k) + a.kc + (long long)h * p.c.k_head : nullptr;
         r.to = out ? out : in, r.to2 = out ? in : nullptr;
         r.w = reinterpret_cast<const B *>(p.wk), r.norm = p.norm != 0, r.turn = p.rot > 0;
@@ -148,6 +174,72 @@ __device__ __forceinline__ Raw8<B> round8(const f2 *f) {
     return r;
 }
 
+// One head by a warp, its channels read twice.
+template <typename B>
+__device__ __forceinline__ void one_head(const RopeParams &p, const TokenAt &at, const HeadRow<B> &r) {
+    const int lane = threadIdx.x & 31, half = p.rot / 2;
+    float inv = 1.0f;
+    if (r.norm) {
+        float sq = 0.f;
+        for (int c = lane; c < p.d; c += 32) {
+            const float x = widen<B>(r.from[c]);
+            sq = fmaf(x, x, sq);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
+        inv = 1.0f / sqrtf(sq / (float)p.d + p.eps);
+    }
+    __syncwarp();
+    auto value = [&](int c) {
+        float x = widen<B>(r.from[c]);
+        if (r.norm) x = r.w ? x * inv * widen<B>(__ldg(r.w + c)) : x * inv;
+        return x;
+    };
+    const int turned = r.turn ? half : 0;
+    for (int n = lane; n < turned + (p.d - 2 * turned); n += 32) {  // a pair, or a channel that stays
+        if (n < turned) {
+            const int a = p.pairs ? 2 * n : n, b = p.pairs ? 2 * n + 1 : n + half;
+            const float *const cs = p.cs + (long long)at.pos * p.cs_row;
+            const float co = __ldg(cs + n), si = __ldg(cs + half + n), x = value(a), y = value(b);
+            const B lo = narrow<B>(x * co - y * si), hi = narrow<B>(y * co + x * si);
+            r.to[a] = lo, r.to[b] = hi;
+            if (r.to2) r.to2[a] = lo, r.to2[b] = hi;
+        } else {
+            const int c = n + turned;
+            const B x = r.norm ? narrow<B>(value(c)) : r.from[c];
+            r.to[c] = x;
+            if (r.to2) r.to2[c] = x;
+        }
+    }
+}
+
+// Packed rows of counts that fall somewhere, of which several sequences may own one: a warp a row, for each of its sequences in turn.  Every one's
+// cache gets it, q_out and k_out that of the last: they may be q and k, so nothing is read after they are written.
+template <typename B>
+__device__ __noinline__ void falling_rows(const RopeParams &p) {
+    const long long warps = (long long)gridDim.x * (kRopeThreads / 32);
+    const int heads = p.n_heads + p.n_kv + (p.v ? p.n_kv : 0);
+    for (long long tok = (long long)blockIdx.x * (kRopeThreads / 32) + (threadIdx.x >> 5); tok < p.tokens; tok += warps) {
+        auto owns = [&](int s) { return __ldg(p.cu + s) <= tok && tok < __ldg(p.cu + s + 1); };
+        int last = p.n_seq - 1;
+        while (last >= 0 && !(owns(last) && token_of(p, last, tok).on)) --last;
+        for (int s = 0; s <= last; ++s) {
+            if (!owns(s) || (s < last && !p.paged)) continue;
+            const TokenAt at = token_of(p, s, tok);
+            if (!at.on) continue;
+            for (int h = s < last ? p.n_heads : 0; h < heads; ++h) one_head<B>(p, at, head_row<B>(p, at, h, s == last));
+        }
+    }
+}
+// What a kernel does before its tokens: the sequences that no token may tell of.  Whether the rows are done already.
+template <typename B>
+__device__ __forceinline__ bool packed_falls(const RopeParams &p) {
+    if (!p.cu && p.tokens > 0) return false;  // (every sequence has tokens)
+    if (!check_sequences(p)) return false;
+    falling_rows<B>(p);
+    return true;
+}
+
 // Rows of 16-byte pieces: p.lanes lanes a group, which takes a token and every p.groups-th of its heads.  A thread's next heads
 // are on their way to places of its own in shared memory (30,822 tokens of 48 heads: 162 us with them in registers, which
 // left 16 warps an SM; 143 so, with products of two channels an instruction).
@@ -157,6 +249,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2) norm_rope(const __grid_consta
     extern __shared__ __align__(16) uint4 ring[];
     grid_dep_wait();
     grid_dep_launch();
+    if (packed_falls<B>(p)) return;
     const int tid = threadIdx.x, i = tid % p.lanes, half = p.rot / 2;
     const long long group = (long long)blockIdx.x * (kRopeThreads / p.lanes) + tid / p.lanes;
     const long long tok = group / p.groups;
@@ -284,55 +377,22 @@ __global__ void __launch_bounds__(kRopeThreads, 2) norm_rope(const __grid_consta
     cp_async_wait<0>();
 }
 
-// Any rows: a warp a head, its channels read twice.
+// Any rows: a warp a head.
 template <typename B>
 __global__ void __launch_bounds__(kRopeThreads) norm_rope_any(const __grid_constant__ RopeParams p) {
     __shared__ TokenAt at[kRopeTokens];
     grid_dep_wait();
     grid_dep_launch();
-    const int tid = threadIdx.x, lane = tid & 31;
+    if (packed_falls<B>(p)) return;
+    const int tid = threadIdx.x;
     const long long tok0 = (long long)blockIdx.x * p.block_tokens;
     const int toks = (int)(p.tokens - tok0 < p.block_tokens ? p.tokens - tok0 : p.block_tokens);
     if (tid < toks) at[tid] = token_at(p, tok0 + tid);
     __syncthreads();
-    const int heads = p.n_heads + p.n_kv + (p.v ? p.n_kv : 0), half = p.rot / 2;
+    const int heads = p.n_heads + p.n_kv + (p.v ? p.n_kv : 0);
     for (int item = tid >> 5; item < toks * heads; item += kRopeThreads / 32) {
         const int tk = item / heads;
-        if (!at[tk].on) continue;
-        const HeadRow<B> r = head_row<B>(p, at[tk], item - tk * heads);
-        float inv = 1.0f;
-        if (r.norm) {
-            float sq = 0.f;
-            for (int c = lane; c < p.d; c += 32) {
-                const float x = widen<B>(r.from[c]);
-                sq = fmaf(x, x, sq);
-            }
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
-            inv = 1.0f / sqrtf(sq / (float)p.d + p.eps);
-        }
-        __syncwarp();
-        auto value = [&](int c) {
-            float x = widen<B>(r.from[c]);
-            if (r.norm) x = r.w ? x * inv * widen<B>(__ldg(r.w + c)) : x * inv;
-            return x;
-        };
-        const int turned = r.turn ? half : 0;
-        for (int n = lane; n < turned + (p.d - 2 * turned); n += 32) {  // a pair, or a channel that stays
-            if (n < turned) {
-                const int a = p.pairs ? 2 * n : n, b = p.pairs ? 2 * n + 1 : n + half;
-                const float *const cs = p.cs + (long long)at[tk].pos * p.cs_row;
-                const float co = __ldg(cs + n), si = __ldg(cs + half + n), x = value(a), y = value(b);
-                const B lo = narrow<B>(x * co - y * si), hi = narrow<B>(y * co + x * si);
-                r.to[a] = lo, r.to[b] = hi;
-                if (r.to2) r.to2[a] = lo, r.to2[b] = hi;
-            } else {
-                const int c = n + turned;
-                const B x = r.norm ? narrow<B>(value(c)) : r.from[c];
-                r.to[c] = x;
-                if (r.to2) r.to2[c] = x;
-            }
-        }
+        if (at[tk].on) one_head<B>(p, at[tk], head_row<B>(p, at[tk], item - tk * heads, true));
     }
 }
 
