@@ -589,7 +589,7 @@ typedef struct cv_cache {
  *   parent             int32 [n_seq][T], with cu_draft [total_tokens]; or NULL
  *   cache_len          int32 [n_seq]; cache_idx int32 [n_seq] or NULL, negative = padded (nothing is read or written)
  *   err                int32 [n_seq] or NULL: CV_SEQ_BAD_SLOT, _BAD_SPAN, _BAD_LENGTH (L < 0 or L + T_s beyond the table's
- *                      row), _BAD_PAGE, _BAD_TREE, _TIMEOUT; a flagged sequence's out is left untouched (after a
+ *                      row), also of calls without a row; _BAD_PAGE, _BAD_TREE, _TIMEOUT; a flagged sequence's out is left untouched (after a
  *                      timeout it may be partly written)
  *   workspace          device buffer of at least cv_tree_attention_workspace bytes, 256-byte aligned; its content
  *                      means nothing before and after the call.  NULL when 0
@@ -667,7 +667,7 @@ CV_API int cv_draft_verify(const cv_draft_verify_args *args, void *stream);
  *   k_out              like k, or NULL;  cache (page_table not NULL): K goes to position cache_len[s] + t, and so does v,
  *                      .. [n_kv_heads][head_dim], unrounded, unless NULL.  One of k_out and the cache is needed unless n_kv_heads = 0
  *   cos_sin            fp32 [n_positions][rot_dim], row stride cos_sin_stride; rot_dim even, 0..head_dim (0: NULL)
- *   err                _BAD_SLOT, _BAD_SPAN, _BAD_LENGTH: the sequence is left untouched; _BAD_PAGE, _BAD_POSITION: the tokens
+ *   err                _BAD_SLOT, _BAD_SPAN, _BAD_LENGTH (also of calls without a row): the sequence is left untouched; _BAD_PAGE, _BAD_POSITION: the tokens
  *                      concerned are left out
  */
 typedef struct cv_qk_norm_rope_args {

@@ -70,7 +70,7 @@ int check_attention(const cv_tree_attention_args *a, bool pointers) {
     for (int64_t s : strides)
         if (s < 0) return CV_ERR_STRIDE;
     if (!pointers || a->n_seq == 0) return CV_OK;
-    if (a->cu_draft && a->total_tokens == 0) return CV_OK;
+    if (a->cu_draft && a->total_tokens == 0) return a->err && !a->cache_len ? CV_ERR_NULL_POINTER : CV_OK;
     if (!a->q || !a->out || !a->cache_len || !a->cache.k || !a->cache.v || !a->cache.page_table) return CV_ERR_NULL_POINTER;
     if (a->out == a->q || a->out == a->cache.k || a->out == a->cache.v) return CV_ERR_ALIAS;
     return CV_OK;
@@ -161,6 +161,21 @@ bool encode4(CUtensorMap *map, const void *p, int d, int64_t n1, int64_t s1, int
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Of the call, without its kernel's plan and tensor maps.
+cvk::AttnParams attention_params(const cv_tree_attention_args *a) {
+    const cv_cache &c = a->cache;
+    cvk::AttnParams p;
+    std::memset(&p, 0, sizeof p);
+    p.n_seq = a->n_seq, p.T = a->T, p.total = a->total_tokens, p.n_heads = a->n_heads, p.G = a->n_heads / c.n_kv_heads;
+    p.scale = a->scale * 1.4426950408889634f;
+    p.polls = a->wait_polls == 0 ? kPolls : a->wait_polls < 0 ? 0u : (unsigned)a->wait_polls;
+    p.c = view(c);
+    p.q = a->q, p.q_seq = a->q_seq_stride, p.q_tok = a->q_tok_stride, p.q_head = a->q_head_stride;
+    p.out = a->out, p.o_seq = a->out_seq_stride, p.o_tok = a->out_tok_stride, p.o_head = a->out_head_stride;
+    p.cu = a->cu_draft, p.parent = a->parent, p.len = a->cache_len, p.idx = a->cache_idx, p.err = a->err;
+    return p;
+}
+
 int launch_attention(const cv_tree_attention_args *a, cudaStream_t stream) {
     const cv_cache &c = a->cache;
     const AttnPlan pl = plan_attention(a);
@@ -169,13 +184,7 @@ int launch_attention(const cv_tree_attention_args *a, cudaStream_t stream) {
     cvk::AttnMaps mp;
     std::memset(&mp, 0, sizeof mp);
     cvk::AttnParams &p = mp.a;
-    p.n_seq = a->n_seq, p.T = a->T, p.total = a->total_tokens, p.n_heads = a->n_heads, p.G = a->n_heads / c.n_kv_heads;
-    p.scale = a->scale * 1.4426950408889634f;
-    p.polls = a->wait_polls == 0 ? kPolls : a->wait_polls < 0 ? 0u : (unsigned)a->wait_polls;
-    p.c = view(c);
-    p.q = a->q, p.q_seq = a->q_seq_stride, p.q_tok = a->q_tok_stride, p.q_head = a->q_head_stride;
-    p.out = a->out, p.o_seq = a->out_seq_stride, p.o_tok = a->out_tok_stride, p.o_head = a->out_head_stride;
-    p.cu = a->cu_draft, p.parent = a->parent, p.len = a->cache_len, p.idx = a->cache_idx, p.err = a->err;
+    p = attention_params(a);
     p.rows = pl.rows, p.pad = (pl.rows + 3) / 4 * 4, p.keys = pl.keys, p.dp = pl.dp, p.parts = pl.parts, p.unit_cost = pl.unit_cost;
     p.ws = pl.cut ? reinterpret_cast<float *>(a->workspace) : nullptr;
     if (pl.on_tc) {
@@ -205,6 +214,19 @@ int launch_attention(const cv_tree_attention_args *a, cudaStream_t stream) {
         if (launch_pdl(cvk::attn_join_kernel(c.dtype == CV_BF16, pl.dp), grid, dim3(cvk::kAttnJoinThreads), 0, stream, p) != cudaSuccess)
             return CV_ERR_LAUNCH;
     }
+    return cudaGetLastError() == cudaSuccess ? CV_OK : CV_ERR_LAUNCH;
+}
+
+// Packed rows of which there are none: a block that looks at every sequence and finds no work.
+int launch_no_attention(const cv_tree_attention_args *a, cudaStream_t stream) {
+    if (!a->err) return CV_OK;
+    cvk::AttnParams p = attention_params(a);
+    const cvk::AttnSimt k = cvk::attn_simt_kernel(a->cache.dtype == CV_BF16, 64, false);
+    p.rows = p.pad = cvk::kSimtRows, p.keys = k.keys, p.dp = 64, p.parts = 1;
+    const int rc = clear_err(a->err, a->n_seq, stream);
+    if (rc != CV_OK) return rc;
+    if (cvk::ensure_smem(reinterpret_cast<const void *>(k.fn), k.smem_bytes) != cudaSuccess) return CV_ERR_LAUNCH;
+    if (launch_pdl(k.fn, dim3(1), dim3(cvk::kSimtThreads), k.smem_bytes, stream, p) != cudaSuccess) return CV_ERR_LAUNCH;
     return cudaGetLastError() == cudaSuccess ? CV_OK : CV_ERR_LAUNCH;
 }
 
@@ -292,7 +314,10 @@ int launch_rope(const cv_qk_norm_rope_args *a, cudaStream_t stream) {
     std::memset(&p, 0, sizeof p);
     p.n_seq = a->n_seq, p.T = a->T, p.n_heads = a->n_heads, p.n_kv = a->n_kv_heads, p.d = a->head_dim, p.total = a->total_tokens;
     p.rot = a->rot_dim, p.pairs = a->pairs != 0, p.norm = a->norm != 0, p.n_pos = a->n_positions, p.eps = a->eps;
-    p.tokens = a->cu ? (long long)a->total_tokens : (long long)a->n_seq * a->T;
+    p.tokens = a->T == 0 ? 0 : a->cu ? (long long)a->total_tokens : (long long)a->n_seq * a->T;
+    // without a row to work on the sequences' flags are all there is to do
+    const bool flags_only = p.tokens == 0 || a->n_heads + a->n_kv_heads == 0;
+    if (flags_only && !a->err) return CV_OK;
     p.q = a->q, p.k = a->k, p.v = a->n_kv_heads > 0 ? a->v : nullptr, p.wq = a->q_weight, p.wk = a->k_weight;
     p.q_out = a->q_out, p.k_out = a->k_out;
     p.q_seq = a->q_seq_stride, p.q_tok = a->q_tok_stride, p.q_head = a->q_head_stride;
@@ -308,7 +333,7 @@ int launch_rope(const cv_qk_norm_rope_args *a, cudaStream_t stream) {
     auto rows = [&](const void *x, int64_t seq, int64_t tok, int64_t head) {
         return !x || (aligned16(x) && seq * es % 16 == 0 && tok * es % 16 == 0 && head * es % 16 == 0);
     };
-    const bool vec = a->head_dim % 16 == 0 && a->rot_dim % 16 == 0 && rows(p.q, p.q_seq, p.q_tok, p.q_head) &&
+    const bool vec = !flags_only && a->head_dim % 16 == 0 && a->rot_dim % 16 == 0 && rows(p.q, p.q_seq, p.q_tok, p.q_head) &&
                      rows(p.q_out, p.qo_seq, p.qo_tok, p.qo_head) && rows(p.k, p.k_seq, p.k_tok, p.k_head) &&
                      rows(p.k_out, p.ko_seq, p.ko_tok, p.ko_head) && rows(p.v, p.v_seq, p.v_tok, p.v_head) &&
                      aligned16(p.wq) && aligned16(p.wk) && aligned16(p.cs) && p.cs_row % 4 == 0 &&
@@ -329,7 +354,7 @@ int launch_rope(const cv_qk_norm_rope_args *a, cudaStream_t stream) {
         // enough tokens a block for all its threads, fewer while that leaves SMs without one
         p.block_tokens = cvk::kRopeTokens;
         while (p.block_tokens > 1 && (p.tokens + p.block_tokens - 1) / p.block_tokens < 4 * sms) p.block_tokens /= 2;
-        blocks = (p.tokens + p.block_tokens - 1) / p.block_tokens;
+        blocks = p.tokens == 0 ? 1 : (p.tokens + p.block_tokens - 1) / p.block_tokens;
     }
     if (blocks > 0x7fffffff) return CV_ERR_SHAPE;
     const int rc = clear_err(a->err, a->n_seq, stream);
@@ -432,7 +457,8 @@ int cv_tree_attention_workspace(const cv_tree_attention_args *args, int64_t *byt
 int cv_tree_attention(const cv_tree_attention_args *args, void *stream) {
     const int rc = check_attention(args, true);
     if (rc != CV_OK) return rc;
-    if (args->n_seq == 0 || (args->cu_draft && args->total_tokens == 0)) return CV_OK;
+    if (args->n_seq == 0) return CV_OK;
+    if (args->cu_draft && args->total_tokens == 0) return launch_no_attention(args, reinterpret_cast<cudaStream_t>(stream));
     return launch_attention(args, reinterpret_cast<cudaStream_t>(stream));
 }
 
@@ -460,8 +486,7 @@ int cv_draft_verify(const cv_draft_verify_args *args, void *stream) {
 int cv_qk_norm_rope(const cv_qk_norm_rope_args *args, void *stream) {
     const int rc = check_rope(args);
     if (rc != CV_OK) return rc;
-    if (args->n_seq == 0 || args->T == 0 || (args->cu && args->total_tokens == 0) || args->n_heads + args->n_kv_heads == 0)
-        return CV_OK;
+    if (args->n_seq == 0) return CV_OK;
     return launch_rope(args, reinterpret_cast<cudaStream_t>(stream));
 }
 
