@@ -136,6 +136,7 @@ enum {
 #define CV_SEQ_BAD_PROBS 512    /* draft_verify: the weights to sample from add up to 0, or to 4 and more */
 #define CV_SEQ_NO_PAGES 1024    /* cache_reserve, cache_fork: not enough free pages */
 #define CV_SEQ_BAD_POSITION 2048 /* qk_norm_rope: a position outside the table of angles */
+#define CV_SEQ_SHARED_PAGE 4096 /* qk_norm_rope, cache_compact: a page to be written that more than one slot holds (with refs) */
 
 /*
  * cv_conv_verify -- [atlas-batched] fused multi-token verify, batched over sequences.
@@ -555,7 +556,8 @@ CV_API int cv_block_norm(const cv_norm_args *args, void *stream);
  * the innermost (1) free; the layer strides are used by cv_cache_compact and cv_cache_fork alone, the other calls read
  * and write layer 0 (pass the layer's own address).  page_table entries past those a call needs are not read.
  *   held   int32 [n_slots]: pages of each slot (reserve, fork, free; else may be NULL)
- *   refs   int32 [n_pages]: slots that hold each page, 0 = free (reserve, fork, free; else may be NULL)
+ *   refs   int32 [n_pages]: slots that hold each page, 0 = free (reserve, fork, free; else may be NULL).  Where it is given,
+ *          cv_qk_norm_rope and cv_cache_compact write into no page that more than one slot holds; without it that is the caller's to see to.
  * Preconditions the library cannot check: distinct sequences of a call use distinct slots, except where a call only reads the cache;
  * calls that change a cache, its table or its counts are ordered with the calls that use them; k and v do not overlap each other or an
  * input.
@@ -667,8 +669,8 @@ CV_API int cv_draft_verify(const cv_draft_verify_args *args, void *stream);
  *   k_out              like k, or NULL;  cache (page_table not NULL): K goes to position cache_len[s] + t, and so does v,
  *                      .. [n_kv_heads][head_dim], unrounded, unless NULL.  One of k_out and the cache is needed unless n_kv_heads = 0
  *   cos_sin            fp32 [n_positions][rot_dim], row stride cos_sin_stride; rot_dim even, 0..head_dim (0: NULL)
- *   err                _BAD_SLOT, _BAD_SPAN, _BAD_LENGTH (also of calls without a row): the sequence is left untouched; _BAD_PAGE, _BAD_POSITION: the tokens
- *                      concerned are left out
+ *   err                _BAD_SLOT, _BAD_SPAN, _BAD_LENGTH (also of calls without a row): the sequence is left untouched; _BAD_PAGE, _SHARED_PAGE,
+ *                      _BAD_POSITION: the tokens concerned are left out
  */
 typedef struct cv_qk_norm_rope_args {
     int32_t n_seq, T, n_heads, n_kv_heads, head_dim, dtype, total_tokens, rot_dim, pairs, norm, n_positions;
@@ -697,7 +699,7 @@ CV_API int cv_qk_norm_rope(const cv_qk_norm_rope_args *args, void *stream);
  * cv_cache_compact -- the accepted path of each sequence moved to its place: rows L + path[s][i] of every layer's K and V
  * go to L + i, i < accept_len[s] (0..T), L = cache_len[s]; new_len[s] = L + accept_len[s] unless NULL (it may not be
  * cache_len).  path int32 [n_seq][T] rises and lies in [0, T).  The pages written must be the slot's alone.
- * err: _BAD_SLOT, _BAD_ACCEPT, _BAD_TREE, _BAD_LENGTH, _BAD_PAGE; the sequence is left untouched.
+ * err: _BAD_SLOT, _BAD_ACCEPT, _BAD_TREE, _BAD_LENGTH, _BAD_PAGE, _SHARED_PAGE; the sequence is left untouched.
  */
 typedef struct cv_cache_compact_args {
     int32_t n_seq, T;

@@ -37,7 +37,8 @@ __all__ = ["conv_verify", "conv_commit", "conv_prefill", "verify_plan", "status_
            "SEQ_TIMEOUT", "SEQ_BAD_SPAN", "SEQ_BAD_TREE", "linattn_prefill", "linattn_step", "linattn_commit",
            "linattn_workspace", "LinattnDrafts", "block_norm", "PagedCache", "tree_attention",
            "tree_attention_workspace", "draft_verify", "qk_norm_rope", "cache_compact", "cache_reserve", "cache_fork", "cache_free",
-           "SEQ_BAD_LENGTH", "SEQ_BAD_PAGE", "SEQ_BAD_TOKEN", "SEQ_BAD_PROBS", "SEQ_NO_PAGES", "SEQ_BAD_POSITION"]
+           "SEQ_BAD_LENGTH", "SEQ_BAD_PAGE", "SEQ_BAD_TOKEN", "SEQ_BAD_PROBS", "SEQ_NO_PAGES", "SEQ_BAD_POSITION",
+           "SEQ_SHARED_PAGE"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 library_path = os.path.join(_PKG, "_build", "libconvverify.so")
@@ -45,7 +46,7 @@ library_path = os.path.join(_PKG, "_build", "libconvverify.so")
 DENSE, DEDUP, HISTORY, RECOMPUTE = 1, 2, 3, 4
 F32, BF16 = 0, 1
 SEQ_BAD_SLOT, SEQ_BAD_OFFSET, SEQ_BAD_ACCEPT, SEQ_TIMEOUT, SEQ_BAD_SPAN, SEQ_BAD_TREE = 1, 2, 4, 8, 16, 32
-SEQ_BAD_LENGTH, SEQ_BAD_PAGE, SEQ_BAD_TOKEN, SEQ_BAD_PROBS, SEQ_NO_PAGES, SEQ_BAD_POSITION = 64, 128, 256, 512, 1024, 2048
+SEQ_BAD_LENGTH, SEQ_BAD_PAGE, SEQ_BAD_TOKEN, SEQ_BAD_PROBS, SEQ_NO_PAGES, SEQ_BAD_POSITION, SEQ_SHARED_PAGE = 64, 128, 256, 512, 1024, 2048, 4096
 MAX_T = 128
 ERR_WORKSPACE = -13
 
@@ -896,7 +897,8 @@ class PagedCache:
     k, v [n_pages, page_size, n_kv_heads, head_dim], or [n_layers, n_pages, ...] for cache_compact and cache_fork (innermost
     stride 1, the others free, one dtype); page_table int32 [n_slots, max_pages], entries past those in use may be
     anything.  held int32 [n_slots] (pages of each slot) and refs int32 [n_pages] (slots that hold each page, 0 = free) are
-    needed by cache_reserve, cache_fork and cache_free.  Made once for the tensors, which it keeps; layer(i) is the cache
+    needed by cache_reserve, cache_fork and cache_free; with refs, qk_norm_rope and cache_compact write into no page that more than one slot
+    holds (SEQ_SHARED_PAGE): a slot that was forked shares full pages and is not to be written before their end.  Made once for the tensors, which it keeps; layer(i) is the cache
     of one layer."""
     __slots__ = ("_k", "_v", "_page_table", "_held", "_refs", "_packed", "_device", "_dtype", "_code", "_heads", "_d", "_layers")
 

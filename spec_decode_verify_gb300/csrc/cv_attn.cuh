@@ -7,7 +7,7 @@
 namespace cvk {
 
 constexpr int kSeqBadSlot = 1, kSeqBadAccept = 4, kSeqBadTree = 32, kSeqBadLength = 64, kSeqBadPage = 128, kSeqBadToken = 256,
-              kSeqBadProbs = 512, kSeqNoPages = 1024, kSeqBadPosition = 2048;
+              kSeqBadProbs = 512, kSeqNoPages = 1024, kSeqBadPosition = 2048, kSeqSharedPage = 4096;
 
 struct AttnSeq {
     int slot, L, T, row0;  // row0: the first of its packed rows (cu), 0 without

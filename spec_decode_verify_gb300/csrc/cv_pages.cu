@@ -317,7 +317,7 @@ constexpr int kMaxPath = 128, kMoveRows = 8;
 template <int BYTES>
 __global__ void __launch_bounds__(kPagesThreads) pages_compact(const __grid_constant__ PagesParams p) {
     __shared__ int src_page[kMaxPath], src_row[kMaxPath], dst_page[kMaxPath], dst_row[kMaxPath];
-    __shared__ int first;
+    __shared__ int first, flags;
     grid_dep_wait();
     grid_dep_launch();
     const CacheView &c = p.c;
@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(kPagesThreads) pages_compact(const __grid_cons
     const int a = __ldg(p.accept + s), L = __ldg(p.len + s);
     if (a < 0 || a > p.T) st |= kSeqBadAccept;
     if (L < 0) st |= kSeqBadLength;
-    if (tid == 0) first = p.T;
+    if (tid == 0) first = p.T, flags = 0;
     __syncthreads();
     if (!st && tid < a) {
         const int at = __ldg(p.path + (long long)s * p.T + tid);
@@ -344,14 +344,15 @@ __global__ void __launch_bounds__(kPagesThreads) pages_compact(const __grid_cons
             const int *const row = c.table + (long long)slot * c.table_row;
             const int g = __ldg(row + from / c.page), h = __ldg(row + to / c.page);
             if (g < 0 || g >= c.n_pages || h < 0 || h >= c.n_pages) st |= kSeqBadPage;
+            else if (c.refs && __ldg(c.refs + h) > 1) st |= kSeqSharedPage;
             src_page[tid] = g, src_row[tid] = from % c.page;
             dst_page[tid] = h, dst_row[tid] = to % c.page;
             atomicMin(&first, tid);
         }
     }
-    const int all = (__syncthreads_or(st & kSeqBadSlot) ? kSeqBadSlot : 0) | (__syncthreads_or(st & kSeqBadAccept) ? kSeqBadAccept : 0) |
-                    (__syncthreads_or(st & kSeqBadTree) ? kSeqBadTree : 0) | (__syncthreads_or(st & kSeqBadLength) ? kSeqBadLength : 0) |
-                    (__syncthreads_or(st & kSeqBadPage) ? kSeqBadPage : 0);
+    if (st) atomicOr(&flags, st);
+    __syncthreads();
+    const int all = flags;
     if (head && p.err) p.err[s] = all;
     if (all) return;
     if (head && p.new_len) p.new_len[s] = L + a;

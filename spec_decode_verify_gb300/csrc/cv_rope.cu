@@ -84,6 +84,7 @@ __device__ __forceinline__ TokenAt token_of(const RopeParams &p, int s, long lon
             const int at = q.L + t, pg = __ldg(p.c.table + (long long)q.slot * p.c.table_row + at / p.c.page);
             if (pg < 0 || pg >= p.c.n_pages) status |= kSeqBadPage;
             else {
+                if (p.c.refs && __ldg(p.c.refs + pg) > 1) status |= kSeqSharedPage;
                 a.kc = (long long)pg * p.c.k_page + (long long)(at % p.c.page) * p.c.k_row;
                 a.vc = (long long)pg * p.c.v_page + (long long)(at % p.c.page) * p.c.v_row;
             }
