@@ -42,7 +42,7 @@ class AttentionLayer:
         n, T = x.shape[:2]
         H, kv, d = self.n_heads, self.n_kv, self.d
         lens = self.len[slots.long()]
-        cv.cache_reserve(self.cache, lens + T, cache_idx=slots)
+        cv.cache_reserve(self.cache, lens + T, cache_len=lens, cache_idx=slots)
         q = x[..., :H * d].unflatten(-1, (H, d))
         k, v = (x[..., (H + i * kv) * d:(H + (i + 1) * kv) * d].unflatten(-1, (kv, d)) for i in range(2))
         turned, out = torch.empty(n, T, H, d, dtype=x.dtype, device=x.device), torch.empty(n, T, H, d, dtype=x.dtype, device=x.device)

@@ -51,7 +51,7 @@ extern "C" {
 #define CV_API
 #endif
 
-#define CV_ABI_VERSION 11
+#define CV_ABI_VERSION 12
 #define CV_MAX_T 128 /* draft tokens per verify call */
 
 typedef enum cv_dtype {
@@ -717,12 +717,16 @@ CV_API int cv_cache_compact(const cv_cache_compact_args *args, void *stream);
  *
  * cv_cache_reserve   slot idx[s] (NULL: s) grows to ceil(n_tokens[s] / page_size) pages if it holds fewer.  The sequences are served in
  *                    order while the free pages last: CV_SEQ_NO_PAGES for the first whose need, added to those before it,
- *                    exceeds them, and for all with a need after it.
+ *                    exceeds them, and for all with a need after it.  With cache_len, positions cache_len[s] .. n_tokens[s] - 1 then
+ *                    stand in pages that the slot alone holds: of those that it holds already, one that another slot held too before
+ *                    the call is replaced by a new page (before the growth's, in order), with a copy of its rows before
+ *                    cache_len[s] (every layer's K and V).  cache_len[s] is at most what the held pages hold (CV_SEQ_BAD_LENGTH).
  * cv_cache_fork      slot idx[s], which holds nothing, gets the first n_tokens[s] tokens of slot src_idx[s]: full pages are
  *                    shared, the rest of a last one is copied into a new page (every layer's K and V).  The sources are
  *                    read as they were before the call: a destination may not be a source too (CV_SEQ_BAD_SLOT).
  * cv_cache_free      slot idx[s] lets go of its pages past those of its first n_tokens[s] tokens (NULL: 0).  Their table
- *                    entries become -1.
+ *                    entries become -1.  A page that it keeps in part may be a shared one: cv_cache_reserve with cache_len makes it the slot's
+ *                    own before more tokens are written.
  * err: _BAD_SLOT (also a destination that holds pages), _BAD_LENGTH, _BAD_PAGE, _NO_PAGES; the slot is left as it was.
  */
 typedef struct cv_cache_pages_args {
@@ -730,6 +734,7 @@ typedef struct cv_cache_pages_args {
     cv_cache cache;
     const int32_t *idx, *src_idx, *n_tokens;
     int32_t *err;
+    const int32_t *cache_len; /* reserve: or NULL */
 } cv_cache_pages_args;
 
 CV_API int cv_cache_reserve(const cv_cache_pages_args *args, void *stream);

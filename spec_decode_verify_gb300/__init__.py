@@ -23,7 +23,7 @@ and those of its attention layers, with the acceptance of the drafts:
     tree_attention(q, out, cache, cache_len, parent=...)
     draft_verify(probs, tokens, uniforms, accept_len, out_tokens, draft_probs=..., parent=..., path=...)
     cache_compact(cache, cache_len, path, accept_len, new_len=...)
-    cache_reserve(cache, n_tokens), cache_fork(cache, src_idx, dst_idx, n_tokens), cache_free(cache, n_tokens)
+    cache_reserve(cache, n_tokens, cache_len=...), cache_fork(cache, src_idx, dst_idx, n_tokens), cache_free(cache, n_tokens)
 """
 from __future__ import annotations
 
@@ -192,7 +192,8 @@ class CacheCompactArgs(ctypes.Structure):
 
 class CachePagesArgs(ctypes.Structure):
     """Mirror of cv_cache_pages_args."""
-    _fields_ = [("n_seq", c_i32), ("cache", Cache), ("idx", c_vp), ("src_idx", c_vp), ("n_tokens", c_vp), ("err", c_vp)]
+    _fields_ = [("n_seq", c_i32), ("cache", Cache), ("idx", c_vp), ("src_idx", c_vp), ("n_tokens", c_vp), ("err", c_vp),
+                ("cache_len", c_vp)]
 
 
 class CvError(RuntimeError):
@@ -887,7 +888,7 @@ _TREE_ATTENTION = struct.Struct("<4ifi" + _IN + "Q3qQ3q4QQQq")
 _DRAFT_VERIFY = struct.Struct("<5i4xQ2qQ2q5Q5Q")
 _QK_NORM_ROPE = struct.Struct("<11if" + 5 * "Q3q" + "3Qq4Q" + _IN + "Q")
 _COMPACT = struct.Struct("<2i" + _IN + "6Q")
-_PAGES = struct.Struct("<i4x" + _IN + "4Q")
+_PAGES = struct.Struct("<i4x" + _IN + "5Q")
 _NO_CACHE = bytes(_CACHE.size)
 
 
@@ -1242,7 +1243,8 @@ def cache_compact(cache, cache_len, path, accept_len, *, new_len=None, cache_idx
         raise CvError(rc, "cv_cache_compact")
 
 
-def make_cache_pages_args(cache, n_seq, *, idx=None, src_idx=None, n_tokens=None, err=None, check_device=True) -> CachePagesArgs:
+def make_cache_pages_args(cache, n_seq, *, idx=None, src_idx=None, n_tokens=None, err=None, cache_len=None,
+                          check_device=True) -> CachePagesArgs:
     """Build cv_cache_pages_args (see cache_reserve, cache_fork and cache_free)."""
     if cache._held is None or cache._refs is None:
         raise ValueError("the cache needs held and refs")
@@ -1250,17 +1252,20 @@ def make_cache_pages_args(cache, n_seq, *, idx=None, src_idx=None, n_tokens=None
         dev = cache._device
         if not (dev is not None and dev >= 0 and (_current_device or _load_device())() == dev and
                 (idx is None or idx.get_device() == dev) and (src_idx is None or src_idx.get_device() == dev) and
-                (n_tokens is None or n_tokens.get_device() == dev) and (err is None or err.get_device() == dev)):
-            _one_device(*cache._tensors(), idx, src_idx, n_tokens, err)
+                (n_tokens is None or n_tokens.get_device() == dev) and (err is None or err.get_device() == dev) and
+                (cache_len is None or cache_len.get_device() == dev)):
+            _one_device(*cache._tensors(), idx, src_idx, n_tokens, err, cache_len)
     return CachePagesArgs.from_buffer_copy(_PAGES.pack(
         n_seq, cache._packed, _exactly(idx, "cache_idx", (n_seq,)), _exactly(src_idx, "src_idx", (n_seq,)),
-        _exactly(n_tokens, "n_tokens", (n_seq,)), _index_array(err, "err", n_seq)))
+        _exactly(n_tokens, "n_tokens", (n_seq,)), _index_array(err, "err", n_seq), _index_array(cache_len, "cache_len", n_seq)))
 
 
-def cache_reserve(cache, n_tokens, *, cache_idx=None, err=None, stream=None) -> None:
+def cache_reserve(cache, n_tokens, *, cache_len=None, cache_idx=None, err=None, stream=None) -> None:
     """Queue the growth of slots (cv_cache_reserve): slot cache_idx[s] (default s) gets pages for n_tokens[s] tokens in all, the free
-    pages with the lowest numbers, sequences in order."""
-    a = make_cache_pages_args(cache, n_tokens.shape[0], idx=cache_idx, n_tokens=n_tokens, err=err)
+    pages with the lowest numbers, sequences in order.  With cache_len int32 [n_seq], the tokens that the slot has, positions cache_len[s] ..
+    n_tokens[s] - 1 stand in pages of its own: one that another slot holds too is replaced by a copy (every layer), which a slot needs
+    that was trimmed into pages shared by a fork."""
+    a = make_cache_pages_args(cache, n_tokens.shape[0], idx=cache_idx, n_tokens=n_tokens, err=err, cache_len=cache_len)
     rc = load_library().cv_cache_reserve(ctypes.byref(a), _stream_of(stream, n_tokens))
     if rc != 0:
         raise CvError(rc, "cv_cache_reserve")
@@ -1277,7 +1282,8 @@ def cache_fork(cache, src_idx, dst_idx, n_tokens, *, err=None, stream=None) -> N
 
 def cache_free(cache, n_tokens=None, *, cache_idx=None, err=None, stream=None) -> None:
     """Queue the release of pages (cv_cache_free): slot cache_idx[s] (default s) keeps those of its first n_tokens[s] tokens
-    (default 0: none).  A page is free again once no slot holds it."""
+    (default 0: none).  A page is free again once no slot holds it.  The last page kept may be shared with a fork: before more tokens are
+    written there, cache_reserve with cache_len makes it the slot's own."""
     if n_tokens is None and cache_idx is None:
         n = cache.page_table.shape[0]
     else:

@@ -398,16 +398,16 @@ int check_compact(const cv_cache_compact_args *a) {
     return a->err && a->err == a->new_len ? CV_ERR_ALIAS : CV_OK;
 }
 
-int check_pages(const cv_cache_pages_args *a, bool fork, bool needs_tokens) {
+int check_pages(const cv_cache_pages_args *a, bool fork, bool needs_tokens, bool copies) {
     if (!a) return CV_ERR_NULL_ARGS;
     if (a->n_seq < 0 || a->n_seq > cvk::kMaxPageSeqs) return CV_ERR_SHAPE;
     const int rc = check_cache(a->cache, a->n_seq > 0, true);
     if (rc != CV_OK || a->n_seq == 0) return rc;
-    if (fork && copy_pieces(a->cache) > 0x7fffffff) return CV_ERR_SHAPE;
+    if (copies && copy_pieces(a->cache) > 0x7fffffff) return CV_ERR_SHAPE;
     if ((needs_tokens && !a->n_tokens) || (fork && !a->src_idx)) return CV_ERR_NULL_POINTER;
-    if (fork && a->cache.k == a->cache.v) return CV_ERR_ALIAS;
+    if (copies && a->cache.k == a->cache.v) return CV_ERR_ALIAS;
     const void *outs[] = {a->err, a->cache.page_table, a->cache.held, a->cache.refs};
-    const void *ins[] = {a->idx, a->src_idx, a->n_tokens};
+    const void *ins[] = {a->idx, a->src_idx, a->n_tokens, a->cache_len};
     for (int i = 0; i < 4; ++i) {
         if (!outs[i]) continue;
         for (const void *in : ins)
@@ -434,6 +434,15 @@ int launch_take(const cvk::PagesParams &p, cudaStream_t stream) {
 }
 
 int done() { return cudaGetLastError() == cudaSuccess ? CV_OK : CV_ERR_LAUNCH; }
+
+// A kernel that copies rows, a cluster a sequence.
+int launch_copies(cvk::PagesParams p, const cv_cache_pages_args *a, cvk::PagesKernel (*kernel)(int bytes), cudaStream_t stream) {
+    const int bytes = copy_bytes(a->cache);
+    p.esize = esize_of(a->cache.dtype), p.chunks = a->cache.head_dim * p.esize / bytes;
+    if (launch_pdl(kernel(bytes), dim3((unsigned)a->n_seq * cvk::kForkCluster), dim3(cvk::kPagesThreads), 0, stream, p) != cudaSuccess)
+        return CV_ERR_LAUNCH;
+    return done();
+}
 
 }  // namespace
 
@@ -513,30 +522,27 @@ int cv_cache_compact(const cv_cache_compact_args *args, void *stream) {
 }
 
 int cv_cache_reserve(const cv_cache_pages_args *args, void *stream) {
-    const int rc = check_pages(args, false, true);
+    const int rc = check_pages(args, false, true, args && args->cache_len);
     if (rc != CV_OK) return rc;
     if (args->n_seq == 0) return CV_OK;
-    const int take = launch_take(pages_params(args, cvk::kPagesReserve), reinterpret_cast<cudaStream_t>(stream));
-    return take != CV_OK ? take : done();
+    cvk::PagesParams p = pages_params(args, cvk::kPagesReserve);
+    p.len = args->cache_len;
+    const int take = launch_take(p, reinterpret_cast<cudaStream_t>(stream));
+    if (take != CV_OK || !p.len) return take != CV_OK ? take : done();
+    return launch_copies(p, args, cvk::pages_own_kernel, reinterpret_cast<cudaStream_t>(stream));
 }
 
 int cv_cache_fork(const cv_cache_pages_args *args, void *stream) {
-    const int rc = check_pages(args, true, true);
+    const int rc = check_pages(args, true, true, true);
     if (rc != CV_OK) return rc;
     if (args->n_seq == 0) return CV_OK;
-    cvk::PagesParams p = pages_params(args, cvk::kPagesFork);
-    const int bytes = copy_bytes(args->cache);
-    p.esize = esize_of(args->cache.dtype), p.chunks = args->cache.head_dim * p.esize / bytes;
+    const cvk::PagesParams p = pages_params(args, cvk::kPagesFork);
     const int take = launch_take(p, reinterpret_cast<cudaStream_t>(stream));
-    if (take != CV_OK) return take;
-    if (launch_pdl(cvk::pages_fork_kernel(bytes), dim3((unsigned)args->n_seq * cvk::kForkCluster), dim3(cvk::kPagesThreads), 0,
-                   reinterpret_cast<cudaStream_t>(stream), p) != cudaSuccess)
-        return CV_ERR_LAUNCH;
-    return done();
+    return take != CV_OK ? take : launch_copies(p, args, cvk::pages_fork_kernel, reinterpret_cast<cudaStream_t>(stream));
 }
 
 int cv_cache_free(const cv_cache_pages_args *args, void *stream) {
-    const int rc = check_pages(args, false, false);
+    const int rc = check_pages(args, false, false, false);
     if (rc != CV_OK) return rc;
     if (args->n_seq == 0) return CV_OK;
     const cvk::PagesParams p = pages_params(args, 0);

@@ -106,7 +106,8 @@ struct PagesParams {
     int n_seq, T, op;
     CacheView c;
     const int *idx, *src, *n_tok;          // reserve, fork, free
-    const int *len, *path, *accept;        // compact
+    const int *len;                        // compact, reserve
+    const int *path, *accept;              // compact
     int *new_len, *err;
     int esize, chunks;                     // copies: pieces of a head's row
 };
@@ -115,6 +116,7 @@ using PagesKernel = void (*)(PagesParams);
 constexpr int kTakeThreads = 1024, kMaxPageSeqs = 4096, kPagesThreads = 256, kForkCluster = 8;
 PagesKernel pages_take_kernel();                // new pages for reserve and fork: one block
 PagesKernel pages_fork_kernel(int bytes);       // shares and copies; bytes an access
+PagesKernel pages_own_kernel(int bytes);        // copies of shared pages that are to be written
 PagesKernel pages_free_kernel();
 PagesKernel pages_compact_kernel(int bytes);
 int pages_take_smem(int n_seq);

@@ -1,5 +1,5 @@
-// The pages of a cache: new pages for growing and forked sequences, shared pages, released pages, and the accepted
-// path of a tree of drafts moved to its place.
+// The pages of a cache: new pages for growing and forked sequences, shared pages and copies of them, released pages, and the
+// accepted path of a tree of drafts moved to its place.
 //
 // A page is free while its reference count is 0, and the free pages with the lowest numbers are given out in the order of the
 // call's sequences; so the only state is the table, the counts and the slots' numbers of pages, and results do not depend
@@ -81,6 +81,16 @@ __global__ void __launch_bounds__(kTakeThreads) pages_take(const __grid_constant
             if (!st && (n < 0 || n > (long long)c.max_pages * c.page || held < 0 || held > c.max_pages)) return -1 - kSeqBadLength;
             need = max(0, pages_for(n, c.page) - held);
             first[i] = held;
+            if (p.len && !st) {  // and one for each shared page that is to be written
+                const int L = __ldg(p.len + i);
+                if (L < 0 || L > (long long)held * c.page) return -1 - kSeqBadLength;
+                const int *const row = c.table + (long long)slot * c.table_row;
+                for (int x = L / c.page; x < (L < n ? min(held, pages_for(n, c.page)) : 0); ++x) {
+                    const int g = row[x];
+                    if (g < 0 || g >= c.n_pages) return -1 - kSeqBadPage;
+                    if (c.refs[g] > 1) ++need, --first[i];
+                }
+            }
         }
         return st ? -1 - kSeqBadSlot : need;
     };
@@ -132,8 +142,23 @@ __global__ void __launch_bounds__(kTakeThreads) pages_take(const __grid_constant
                 if (pre[mid] <= rank) lo = mid;
                 else hi = mid - 1;
             }
-            c.table[(long long)slots[lo] * c.table_row + first[lo] + (rank - pre[lo])] = list[k];
-            c.refs[list[k]] = 1;
+            int *const row = c.table + (long long)slots[lo] * c.table_row;
+            const int at = first[lo] + (int)(rank - pre[lo]);
+            if (!p.len || at >= c.held[slots[lo]]) {
+                row[at] = list[k];
+                c.refs[list[k]] = 1;
+            } else if (k == 0 || rank == pre[lo]) {
+                // Pages instead of shared ones, all of the sequence's in the list by one thread, in order: a page's count says which one it
+                // replaces, until the next kernel has copied.
+                const int end = min(c.held[slots[lo]], pages_for(__ldg(p.n_tok + lo), c.page));
+                long long left = min(limit, min((long long)n + found, pre[lo] + c.held[slots[lo]] - first[lo])) - rank;
+                for (int x = __ldg(p.len + lo) / c.page, y = k; x < end && left > 0; ++x) {
+                    const int g = row[x];
+                    if (c.refs[g] <= 1) continue;
+                    c.refs[list[y]] = -1 - g, row[x] = list[y];
+                    ++y, --left;
+                }
+            }
         }
         __syncthreads();
     };
@@ -211,6 +236,25 @@ __device__ __forceinline__ unsigned copy_items(const PagesParams &p) { return 2u
 
 
 
+// The first `rest` rows of a page to another, in every layer, by the blocks of a cluster: a piece of a head in one row of a layer is an
+// item; a thread takes 4 of its rows at a time.
+template <int BYTES>
+__device__ __forceinline__ void copy_page(const PagesParams &p, int old_page, int new_page, int rest, int rank) {
+    const unsigned items = copy_items(p);
+    const int quarters = (rest + 3) / 4;
+    for (unsigned long long x = rank * kPagesThreads + threadIdx.x; x < (unsigned long long)items * quarters; x += kForkCluster * kPagesThreads) {
+        const unsigned q = (unsigned)(x / items), item = (unsigned)(x - (unsigned long long)q * items);
+        const CopyItem<BYTES> m(p, item);
+        typename Piece<BYTES>::T w[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            if ((int)(4 * q) + r < rest) w[r] = m.base[old_page * m.page + (4 * q + r) * m.row];
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            if ((int)(4 * q) + r < rest) m.base[new_page * m.page + (4 * q + r) * m.row] = w[r];
+    }
+}
+
 // A cluster a sequence: checks its source's pages, copies the rest of the last one, then its first block shares the full
 // ones and closes the slot's entry.
 template <int BYTES>
@@ -252,22 +296,40 @@ __global__ void __cluster_dims__(kForkCluster, 1, 1) __launch_bounds__(kPagesThr
         }
         if (tid == 0) c.held[slot] = full + (rest > 0);
     }
-    if (!rest) return;
-    const int old_page = from[full];
-    // a piece of a head in one row of a layer is an item; a thread takes 4 of its rows at a time
-    const unsigned items = copy_items(p);
-    const int quarters = (rest + 3) / 4;
-    for (unsigned long long x = rank * kPagesThreads + tid; x < (unsigned long long)items * quarters; x += kForkCluster * kPagesThreads) {
-        const unsigned q = (unsigned)(x / items), item = (unsigned)(x - (unsigned long long)q * items);
-        const CopyItem<BYTES> m(p, item);
-        typename Piece<BYTES>::T w[4];
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-            if ((int)(4 * q) + r < rest) w[r] = m.base[old_page * m.page + (4 * q + r) * m.row];
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-            if ((int)(4 * q) + r < rest) m.base[new_page * m.page + (4 * q + r) * m.row] = w[r];
+    if (rest) copy_page<BYTES>(p, from[full], new_page, rest, rank);
+}
+
+// A cluster a sequence that grows (reserve with lengths): the rows of its last token's page to the page that replaces it, then the
+// counts of the new and the replaced pages.
+template <int BYTES>
+__global__ void __cluster_dims__(kForkCluster, 1, 1) __launch_bounds__(kPagesThreads)
+    pages_own(const __grid_constant__ PagesParams p) {
+    grid_dep_wait();
+    grid_dep_launch();
+    const CacheView &c = p.c;
+    const int tid = threadIdx.x, i = blockIdx.x / kForkCluster, rank = blockIdx.x % kForkCluster;
+    const int slot = p.idx ? __ldg(p.idx + i) : i, n = __ldg(p.n_tok + i), L = __ldg(p.len + i);
+    bool on = slot >= 0 && slot < c.n_slots && L >= 0 && L < n && n <= (long long)c.max_pages * c.page;
+    bool named = false;  // by an earlier sequence, whose pages they are
+    if (p.idx && on)
+        for (int j = tid; j < i; j += kPagesThreads) named |= __ldg(p.idx + j) == slot;
+    on &= !__syncthreads_or(named);
+    int *const row = c.table + (long long)(on ? slot : 0) * c.table_row;
+    const int begin = L / c.page, end = on ? min(c.held[slot], pages_for(n, c.page)) : 0;
+    int old_page = -1, new_page = -1;
+    if (on && begin < end && L % c.page) {
+        new_page = row[begin];
+        if (new_page >= 0 && new_page < c.n_pages) old_page = -1 - c.refs[new_page];
     }
+    cluster_sync();  // every block has read the count that the first one changes
+    if (rank == 0)
+        for (int x = begin + tid; x < end; x += kPagesThreads) {
+            const int g = row[x], of = g >= 0 && g < c.n_pages ? -1 - c.refs[g] : -1;
+            if (of < 0) continue;
+            c.refs[g] = 1;
+            atomicSub(c.refs + of, 1);
+        }
+    if (old_page >= 0) copy_page<BYTES>(p, old_page, new_page, L % c.page, rank);
 }
 
 // A block a sequence.
@@ -377,6 +439,7 @@ __global__ void __launch_bounds__(kPagesThreads) pages_compact(const __grid_cons
 PagesKernel pages_take_kernel() { return pages_take; }
 int pages_take_smem(int n_seq) { return 256 + n_seq * 24 + kScanPages * 4; }
 PagesKernel pages_fork_kernel(int bytes) { return bytes == 16 ? pages_fork<16> : bytes == 4 ? pages_fork<4> : pages_fork<2>; }
+PagesKernel pages_own_kernel(int bytes) { return bytes == 16 ? pages_own<16> : bytes == 4 ? pages_own<4> : pages_own<2>; }
 PagesKernel pages_free_kernel() { return pages_free; }
 PagesKernel pages_compact_kernel(int bytes) {
     return bytes == 16 ? pages_compact<16> : bytes == 4 ? pages_compact<4> : pages_compact<2>;
