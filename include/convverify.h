@@ -723,7 +723,8 @@ CV_API int cv_cache_compact(const cv_cache_compact_args *args, void *stream);
  *                    cache_len[s] (every layer's K and V).  cache_len[s] is at most what the held pages hold (CV_SEQ_BAD_LENGTH).
  * cv_cache_fork      slot idx[s], which holds nothing, gets the first n_tokens[s] tokens of slot src_idx[s]: full pages are
  *                    shared, the rest of a last one is copied into a new page (every layer's K and V).  The sources are
- *                    read as they were before the call: a destination may not be a source too (CV_SEQ_BAD_SLOT).
+ *                    read as they were before the call: a destination may not be a source too (CV_SEQ_BAD_SLOT).  A source with a page
+ *                    that is not there among those tokens' (CV_SEQ_BAD_PAGE) takes no new page.
  * cv_cache_free      slot idx[s] lets go of its pages past those of its first n_tokens[s] tokens (NULL: 0).  Their table
  *                    entries become -1.  A page that it keeps in part may be a shared one: cv_cache_reserve with cache_len makes it the slot's
  *                    own before more tokens are written.

@@ -37,7 +37,9 @@ __device__ __forceinline__ long long block_scan(long long v, long long &before, 
     return __shfl_sync(0xffffffffu, sums, 31);
 }
 
+constexpr int kCheckPages = 128;  // pages of a fork's source that a warp looks at in one go
 constexpr int kScanEach = 8, kScanPages = kTakeThreads * kScanEach;  // counts a thread, and the block, looks at in one go
+static_assert(kScanPages >= 2 * kMaxPageSeqs, "a fork's notes fit into the list");
 
 __global__ void __launch_bounds__(kTakeThreads) pages_take(const __grid_constant__ PagesParams p) {
     extern __shared__ __align__(8) long long smem[];
@@ -49,13 +51,27 @@ __global__ void __launch_bounds__(kTakeThreads) pages_take(const __grid_constant
     const int tid = threadIdx.x;
     const bool fork = p.op == kPagesFork;
     const CacheView &c = p.c;
+    // Of a fork: whether a page of the source is not there, and its tokens (the list's places are not used before the scan).
+    int *const gone = list, *const tokens = list + kMaxPageSeqs;
+    int most = 0;  // pages of a fork, in kCheckPages
     for (int i = tid; i < p.n_seq; i += kTakeThreads) {
         int slot = p.idx ? __ldg(p.idx + i) : i;
         const int from = fork ? __ldg(p.src + i) : 0;
+        if (fork) {
+            int n = __ldg(p.n_tok + i);
+            if (slot < 0 || from < 0 || from >= c.n_slots || n > (long long)c.max_pages * c.page) n = 0;
+            gone[i] = 0, tokens[i] = n;
+            most = max(most, (pages_for(n, c.page) + kCheckPages - 1) / kCheckPages);
+        }
         if (from < 0) slot = -1;
         slots[i] = slot, src[i] = slot < 0 ? -1 : from;
     }
+    if (fork) {
+        most = __reduce_max_sync(0xffffffffu, most);
+        if ((tid & 31) == 0) scratch[tid >> 5] = most;
+    }
     __syncthreads();
+    if (fork) most = __reduce_max_sync(0xffffffffu, (int)scratch[tid & 31]);
     // Pages each sequence needs; -1 - bits where it is flagged.
     auto needs = [&](int i) {
         const int slot = slots[i];
@@ -94,10 +110,28 @@ __global__ void __launch_bounds__(kTakeThreads) pages_take(const __grid_constant
         }
         return st ? -1 - kSeqBadSlot : need;
     };
+    // A fork's sources' pages, in runs of kCheckPages, by the warps that have no sequence to look at, if there are such: a fork that cannot be
+    // made takes no page from the others.
+    const int warp = tid >> 5, busy = p.n_seq <= kTakeThreads / 2 ? (p.n_seq + 31) / 32 : 0;
+    const long long checks = (long long)p.n_seq * most;
+    for (long long q = warp < busy ? checks : warp - busy; q < checks; q += kTakeThreads / 32 - busy) {
+        const int of = (int)attn_div(q, p.n_seq), i = (int)(q - (long long)of * p.n_seq);
+        const long long left = pages_for(tokens[i], c.page) - (long long)of * kCheckPages;
+        const int *const from = c.table + (long long)src[i] * c.table_row + (long long)of * kCheckPages;
+        bool bad = false;
+#pragma unroll 4
+        for (int x = tid & 31; x < kCheckPages; x += 32) {
+            const int g = x < left ? from[x] : 0;
+            bad |= g < 0 || g >= c.n_pages;
+        }
+        if (bad) gone[i] = 1;
+    }
     long long total = 0;
     for (int base = 0; base < p.n_seq; base += kTakeThreads) {
         const int i = base + tid;
-        const int need = i < p.n_seq ? needs(i) : 0;
+        int need = i < p.n_seq ? needs(i) : 0;
+        if (fork && base == 0) __syncthreads();  // (the checks)
+        if (fork && i < p.n_seq && need >= 0 && gone[i]) need = -1 - kSeqBadPage;
         long long before;
         const long long sum = block_scan(max(need, 0), before, scratch);
         if (i < p.n_seq) {
@@ -255,8 +289,7 @@ __device__ __forceinline__ void copy_page(const PagesParams &p, int old_page, in
     }
 }
 
-// A cluster a sequence: checks its source's pages, copies the rest of the last one, then its first block shares the full
-// ones and closes the slot's entry.
+// A cluster a sequence: its first block shares the source's full pages and closes the slot's entry, all copy the rest of the last one.
 template <int BYTES>
 __global__ void __cluster_dims__(kForkCluster, 1, 1) __launch_bounds__(kPagesThreads)
     pages_fork(const __grid_constant__ PagesParams p) {
@@ -265,38 +298,25 @@ __global__ void __cluster_dims__(kForkCluster, 1, 1) __launch_bounds__(kPagesThr
     const CacheView &c = p.c;
     const int tid = threadIdx.x, i = blockIdx.x / kForkCluster, rank = blockIdx.x % kForkCluster;
     const int slot = p.idx ? __ldg(p.idx + i) : i, src = __ldg(p.src + i);
-    const bool on = slot >= 0 && slot < c.n_slots && src >= 0 && c.held[slot] == -1 - i;
-    int n = 0, full = 0, rest = 0, bad = 0;
-    int *const to = c.table + (long long)(on ? slot : 0) * c.table_row;
-    const int *const from = c.table + (long long)(on ? src : 0) * c.table_row;
-    if (on) {
-        n = __ldg(p.n_tok + i), full = n / c.page, rest = n % c.page;
-        for (int x = tid; x < pages_for(n, c.page); x += kPagesThreads) {
-            const int g = from[x];
-            bad |= g < 0 || g >= c.n_pages;
-        }
-    }
-    bad = __syncthreads_or(bad);
-    const int new_page = on && rest ? to[full] : 0;
-    cluster_sync();  // every block has read the entries that the first one changes
+    const int n = __ldg(p.n_tok + i), full = n / c.page, rest = n % c.page;
+    // (bounds once more, of what the pages were taken for: a count that was negative before the call may look like its mark)
+    const bool named = slot >= 0 && slot < c.n_slots && src >= 0 && src < c.n_slots && n >= 0 && n <= (long long)c.max_pages * c.page;
+    int *const to = c.table + (long long)(named ? slot : 0) * c.table_row;
+    const int *const from = c.table + (long long)(named ? src : 0) * c.table_row;
+    const bool on = named && c.held[slot] == -1 - i;
+    const int first = named && tid < full ? from[tid] : -1, old_page = named && rest ? from[full] : -1, new_page = named && rest ? to[full] : -1;
+    auto there = [&](int page) { return page >= 0 && page < c.n_pages; };
+    cluster_sync();  // every block has read the entry that the first one changes
     if (!on) return;
-    if (bad) {
-        if (rank == 0 && tid == 0) {
-            if (rest) c.refs[new_page] = 0, to[full] = -1;
-            c.held[slot] = 0;
-            if (p.err) p.err[i] = kSeqBadPage;
-        }
-        return;
-    }
     if (rank == 0) {
         for (int x = tid; x < full; x += kPagesThreads) {
-            const int g = from[x];
+            const int g = x == tid ? first : from[x];
             to[x] = g;
-            atomicAdd(c.refs + g, 1);
+            if (there(g)) atomicAdd(c.refs + g, 1);
         }
         if (tid == 0) c.held[slot] = full + (rest > 0);
     }
-    if (rest) copy_page<BYTES>(p, from[full], new_page, rest, rank);
+    if (there(old_page) && there(new_page)) copy_page<BYTES>(p, old_page, new_page, rest, rank);
 }
 
 // A cluster a sequence that grows (reserve with lengths): the rows of its last token's page to the page that replaces it, then the
