@@ -7,7 +7,7 @@
 // Layout.  Nothing of K and V is used twice by few rows, so they go from memory to registers and not through shared
 // memory: a warp takes 8 keys of every 64, a lane 4 channels of a key (8 of 256; 64 channels are half a warp's), with
 // the rows of O that it needs of them in registers (those of Q as well spilled: 75 us against 67 for 13 tokens of 64/8 heads of 128
-// over 3k).  The 16 sums of R rows and NK keys are added up over the lanes by halves that are exchanged, 15 shuffles, after
+// over 3k).  The 16 sums of R rows and NK keys are added up over the lanes by halves that are exchanged, 16 shuffles (15 for heads of 64), after
 // which a lane has the score of one row and one key, and one exponential.  (Four keys a lane: 69 us.)  The warps have
 // maxima, sums and outputs of their own, which are joined at a unit's end.
 //
@@ -142,14 +142,21 @@ __global__ void __launch_bounds__(kFewThreads, DP <= 128 ? 2 : 1) attn_few(const
         // the warp's keys, n = 0, 1, ...: kRun of each tile
         const int n_keys = (u.last - u.tile) * kRun, groups = n_keys / GROUP;
         auto key_at = [&](int n) { return (u.tile + n / kRun) * kFewKeys + warp * kRun + n % kRun; };
+        // (looked up two batches ahead: a key past the run's, which may be past 2^31 too, is never made)
         auto page_of = [&](int batch) {
-            const int n = 32 * batch + lane, j = key_at(n);
-            return n < n_keys && j < end ? __ldg(table + j / p.c.page) : -1;
+            const int n = 32 * batch + lane;
+            if (n >= n_keys) return -1;
+            const int j = key_at(n);
+            return j < end ? __ldg(table + j / p.c.page) : -1;
         };
         auto place = [&](int batch, int page) {
-            const int in = key_at(32 * batch + lane) % p.c.page;
-            sh->k_at[warp][batch & 1][lane] = page < 0 ? -1 : (long long)page * p.c.k_page + (long long)in * p.c.k_row;
-            sh->v_at[warp][batch & 1][lane] = page < 0 ? -1 : (long long)page * p.c.v_page + (long long)in * p.c.v_row;
+            long long k_at = -1, v_at = -1;
+            if (page >= 0) {
+                const int in = key_at(32 * batch + lane) % p.c.page;
+                k_at = (long long)page * p.c.k_page + (long long)in * p.c.k_row;
+                v_at = (long long)page * p.c.v_page + (long long)in * p.c.v_row;
+            }
+            sh->k_at[warp][batch & 1][lane] = k_at, sh->v_at[warp][batch & 1][lane] = v_at;
         };
         auto load = [&](Raw4<B> (&x)[NK][NV], const B *base, const long long (&places)[2][32], int g) {
 #pragma unroll
