@@ -900,8 +900,9 @@ class PagedCache:
     anything.  held int32 [n_slots] (pages of each slot) and refs int32 [n_pages] (slots that hold each page, 0 = free) are
     needed by cache_reserve, cache_fork and cache_free; with refs, qk_norm_rope and cache_compact write into no page that more than one slot
     holds (SEQ_SHARED_PAGE): a slot that was forked shares full pages and is not to be written before their end.  Made once for the tensors, which it keeps; layer(i) is the cache
-    of one layer."""
-    __slots__ = ("_k", "_v", "_page_table", "_held", "_refs", "_packed", "_device", "_dtype", "_code", "_heads", "_d", "_layers")
+    of one layer.  A call raises ValueError where one of them has been given other memory since (set_, resize_, .data): the handle is then
+    to be made again."""
+    __slots__ = ("_k", "_v", "_page_table", "_held", "_refs", "_packed", "_at", "_device", "_dtype", "_code", "_heads", "_d", "_layers")
 
     def __init__(self, k, v, page_table, *, held=None, refs=None):
         if k.dim() not in (4, 5) or v.shape != k.shape:
@@ -925,6 +926,7 @@ class PagedCache:
         if k.dim() == 4:
             ks, vs = (0, *ks), (0, *vs)
         rows = page_table.stride(0) if page_table.shape[0] > 1 else page_table.shape[1]
+        self._at = self._addresses()
         self._packed = _CACHE.pack(
             k.data_ptr(), v.data_ptr(), *ks, *vs, k.shape[0] if k.dim() == 5 else 1, *k.shape[-4:], *page_table.shape, dtype,
             page_table.data_ptr(), rows, held.data_ptr() if held is not None else 0,
@@ -942,6 +944,17 @@ class PagedCache:
 
     def _tensors(self):
         return self._k, self._v, self._page_table, self._held, self._refs
+
+    def _addresses(self):
+        held, refs = self._held, self._refs
+        return (self._k.data_ptr(), self._v.data_ptr(), self._page_table.data_ptr(), held.data_ptr() if held is not None else 0,
+                refs.data_ptr() if refs is not None else 0)
+
+    def _args(self) -> bytes:
+        """cv_cache of the tensors, as long as their memory is what it was."""
+        if self._addresses() != self._at:
+            raise ValueError("a tensor of the cache has other memory than when the PagedCache was made: make it again")
+        return self._packed
 
 
 def _one_layer(cache) -> None:
@@ -1006,7 +1019,7 @@ def make_tree_attention_args(q, out, cache, cache_len, *, parent=None, scale=Non
                 (workspace is None or workspace.get_device() == dev)):
             _one_device(q, out, *cache._tensors(), cache_len, parent, cu_draft, cache_idx, err, workspace)
     return TreeAttentionArgs.from_buffer_copy(_TREE_ATTENTION.pack(
-        n, T, qs[-2], total, d ** -0.5 if scale is None else scale, wait_polls, cache._packed, q.data_ptr(), qt[0], qt[1], qt[2],
+        n, T, qs[-2], total, d ** -0.5 if scale is None else scale, wait_polls, cache._args(), q.data_ptr(), qt[0], qt[1], qt[2],
         out.data_ptr(), ot[0], ot[1], ot[2], cu_draft.data_ptr() if cu_draft is not None else 0,
         _exactly(parent, "parent", lead), _index_array(cache_len, "cache_len", n), _index_array(cache_idx, "cache_idx", n),
         _index_array(err, "err", n), ws, ws_bytes))
@@ -1143,7 +1156,7 @@ def make_qk_norm_rope_args(q, k, q_out, *, k_out=None, v=None, cos_sin=None, q_w
             _one_layer(cache)
         if cache._heads != kv or cache._d != d or cache._dtype is not dt:
             raise ValueError("the cache must have the kv heads, head size and dtype of k")
-        packed = cache._packed
+        packed = cache._args()
         if cache_len is None:
             raise ValueError("cache_len is required")
     elif v is not None:
@@ -1228,7 +1241,7 @@ def make_cache_compact_args(cache, cache_len, path, accept_len, *, new_len=None,
                 (err is None or err.get_device() == dev)):
             _one_device(path, *cache._tensors(), cache_len, accept_len, new_len, cache_idx, err)
     return CacheCompactArgs.from_buffer_copy(_COMPACT.pack(
-        n, T, cache._packed, _index_array(cache_len, "cache_len", n), _exactly(path, "path", (n, T)),
+        n, T, cache._args(), _index_array(cache_len, "cache_len", n), _exactly(path, "path", (n, T)),
         _index_array(accept_len, "accept_len", n), _index_array(cache_idx, "cache_idx", n), _index_array(new_len, "new_len", n),
         _index_array(err, "err", n)))
 
@@ -1256,7 +1269,7 @@ def make_cache_pages_args(cache, n_seq, *, idx=None, src_idx=None, n_tokens=None
                 (cache_len is None or cache_len.get_device() == dev)):
             _one_device(*cache._tensors(), idx, src_idx, n_tokens, err, cache_len)
     return CachePagesArgs.from_buffer_copy(_PAGES.pack(
-        n_seq, cache._packed, _exactly(idx, "cache_idx", (n_seq,)), _exactly(src_idx, "src_idx", (n_seq,)),
+        n_seq, cache._args(), _exactly(idx, "cache_idx", (n_seq,)), _exactly(src_idx, "src_idx", (n_seq,)),
         _exactly(n_tokens, "n_tokens", (n_seq,)), _index_array(err, "err", n_seq), _index_array(cache_len, "cache_len", n_seq)))
 
 
