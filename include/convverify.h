@@ -587,7 +587,8 @@ typedef struct cv_cache {
  * bf16 (2^-8 of a term at most), as the operand of the second product.
  *   n_seq 0..65535, T 1..CV_MAX_T (the largest T_s), n_heads 1..4096, a multiple of n_kv_heads
  *   q, out             [n_seq][T][n_heads][head_dim], or with cu_draft [total_tokens][n_heads][head_dim]; dtype = the cache's
- *   cu_draft           int32 [n_seq + 1] or NULL; sequence s owns rows [cu_draft[s], cu_draft[s+1])
+ *   cu_draft           int32 [n_seq + 1] or NULL; sequence s owns rows [cu_draft[s], cu_draft[s+1]); a row of several sequences (where
+ *                      cu_draft falls) receives values of any of them
  *   parent             int32 [n_seq][T], with cu_draft [total_tokens]; or NULL
  *   cache_len          int32 [n_seq]; cache_idx int32 [n_seq] or NULL, negative = padded (nothing is read or written)
  *   err                int32 [n_seq] or NULL: CV_SEQ_BAD_SLOT, _BAD_SPAN, _BAD_LENGTH (L < 0 or L + T_s beyond the table's

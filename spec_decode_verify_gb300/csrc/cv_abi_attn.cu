@@ -76,8 +76,10 @@ int check_attention(const cv_tree_attention_args *a, bool pointers) {
     return CV_OK;
 }
 
-// What a unit takes beside its tiles, in tiles, when the blocks' runs are made equal.  Tensor cores, 128 sequences of 8 drafts over 8k: 0 to
-// 3 tiles 228, 210, 199 and 198 us.  fp32 products, 13 tokens of 64/8 heads over 3k: 0, 1 and 3 tiles 74, 66 and 72 us.
+// What a unit takes beside its tiles, in tiles, when the blocks' runs are made equal; device us with 0, 1, 2 and 3 of them, sequences of n/2 to n
+// cached tokens.  Tensor cores: 128 x 8 drafts of 32/4 heads of 128, n = 8k, 282, 280, 279, 278; 100 x 4 of 16/8 heads of 64, 1k, 91, 87, 86, 86; 300
+// x 1 of 16/8 heads, 300, 170, 167, 161, 165.  fp32 products: 100 x 1 of 32/8 heads, 1k, 123, 119, 120, 122; 13 x 1 of 64/8, 3k, 89, 90, 90, 94; 16 x
+// 8 of 32/4, 2k, 191, 191, 202, 202; 23 x 1 of 4/2 heads of 64, 2.3k, 19.1, 18.3, 18.3, 18.3.
 constexpr int kTcUnitCost = 3, kSimtUnitCost = 1;
 
 struct AttnPlan {
@@ -112,8 +114,11 @@ AttnPlan plan_attention(const cv_tree_attention_args *a, int best = kTensorCores
     const cvk::DeviceLimits lim = device_limits();
     pl.dp = d <= 64 ? 64 : d <= 128 ? 128 : d <= 192 ? 192 : 256;
     pl.tok = G <= 128 ? (a->T < 128 / G ? a->T : 128 / G) : 1;
-    // More rows than one tile of 128: two row tiles a unit, so that a tile of keys is read once for both (17 drafts of 64/8 heads over 100k
-    // 141 us with a unit each, 111 with one).  Tensor memory has room for two up to 128 channels.
+    // More rows than one tile of 128: two row tiles a unit, so that a tile of keys is read once for both.  Device us with one and with a unit
+    // each: 17 drafts of 64/8 heads over 100k 107 and 139, 64 x 17 over 2k-4k 235 and 297, 32 x 128 of 32/8 heads over 2k-4k 272 and 333, 4 x 128 over
+    // 4k-8k 97 and 97; heads of 64: 88 and 106, 185 and 236, 219 and 259.  Where a block has few tiles a unit each is faster (17 drafts over 20k
+    // 45 and 37, 9 of 16/1 heads over 700 18.3 and 14.6), but how many there are stands in the lengths, on the device.  Tensor memory
+    // has room for two up to 128 channels.
     pl.pair = pl.dp <= 128 && a->T > pl.tok;
     pl.tc = cvk::attn_tc_kernel(pl.dp, pl.pair);
     pl.on_tc = best >= kTensorCores && tc_takes(a, pl.tc.keys);
@@ -127,8 +132,11 @@ AttnPlan plan_attention(const cv_tree_attention_args *a, int best = kTensorCores
                          rows16(c.v, 0, c.v_page_stride, c.v_row_stride, c.v_head_stride, c) && aligned16(a->q) &&
                          a->q_seq_stride * es % 16 == 0 && a->q_tok_stride * es % 16 == 0 && a->q_head_stride * es % 16 == 0;
         if (pl.dp == 192) pl.dp = 256;
-        // Up to 8 rows share too little for a tile in shared memory (fp32, device time there and in registers: 13 tokens of 64/8 heads
-        // of 128 over 3k 119 and 66 us, 16 of 8/8 heads of 256 over 4k 374 and 151, 23 of 4/2 heads of 64 over 2.3k 27 and 22).
+        // Up to 8 rows share too little for a tile in shared memory.  Device us there and in registers, n/2 to n cached tokens: fp32, 13 tokens
+        // of 64/8 heads of 128, n = 3k, 182 and 90, 16 of 8/8 heads of 256, 4k, 520 and 160, 23 of 4/2 heads of 64, 2.3k, 29 and 18, 32 x 2 of 32/8 heads
+        // of 64, 2k, 151 and 75; bf16 in pages of 20: 177 and 85, 501 and 141, 29 and 18, and 32 x 4 of 16/8 heads, 4k, 482 and 221.  Of those in
+        // registers, units of 4 rows and of 8: 16 tokens of 8/8 heads of 256, 4k, 160 and 254, 64 of 32/8 heads, 4k, 274 and 415, 64 of 16/8 heads of
+        // 64, 147 and 220; with 8, 6 and 5 rows a kv head, in two units of 4: 108 and 90, 108 and 89, 84 and 75.
         const int64_t rows = (int64_t)a->T * G;
         const bool few = best >= kWholePieces && vec && rows <= cvk::kFewRows;
         pl.rows = !few ? cvk::kSimtRows : rows <= 4 ? 4 : 8;

@@ -10,7 +10,10 @@
 // Layout.  A block (one per SM) takes an equal run of the units' work: their key tiles in a row, and for each unit about what
 // its beginning and end take, so that all blocks read for the same time whatever the lengths; a unit that is cut leaves (m, l, O) in the workspace
 // for the join.  All rows of a kv head's group share one read of its keys, so HBM bounds it: a tile of 128 keys of 128
-// channels is 64 KB, 1.4 us of an SM's share, and takes 0.7 us of the tensor pipe at any number of rows.  Roles, each a stream of its own:
+// channels is 64 KB, 1.4 us of an SM's share, and takes 0.7 us of the tensor pipe at any number of rows.  Two row tiles a unit
+// are a chain instead: each group has one buffer of S, so that its next scores wait for its softmax (1650 cycles), its P V and the
+// next Q K^T behind the other group's, about 2.2 us a tile (17 drafts of 64/8 heads over 100k 107 us, tensor pipe 47 %, HBM 49 %).
+// Roles, each a stream of its own:
 //   load K   1 warp: the units (also for the others, through a queue in shared memory), Q and K by TMA, a box for each page
 //   load V   1 warp: V (one warp for both took 45 cycles a box, 64 boxes a tile for pages of 16 tokens: slower than HBM)
 //   issue    1 warp: Q K^T of the next tile, then P V of this one
