@@ -221,15 +221,25 @@ __device__ __noinline__ void falling_rows(const RopeParams &p) {
     const long long warps = (long long)gridDim.x * (kRopeThreads / 32);
     const int heads = p.n_heads + p.n_kv + (p.v ? p.n_kv : 0);
     for (long long tok = (long long)blockIdx.x * (kRopeThreads / 32) + (threadIdx.x >> 5); tok < p.tokens; tok += warps) {
-        auto owns = [&](int s) { return __ldg(p.cu + s) <= tok && tok < __ldg(p.cu + s + 1); };
-        int last = p.n_seq - 1;
-        while (last >= 0 && !(owns(last) && token_of(p, last, tok).on)) --last;
-        for (int s = 0; s <= last; ++s) {
-            if (!owns(s) || (s < last && !p.paged)) continue;
-            const TokenAt at = token_of(p, s, tok);
-            if (!at.on) continue;
-            for (int h = s < last ? p.n_heads : 0; h < heads; ++h) one_head<B>(p, at, head_row<B>(p, at, h, s == last));
-        }
+        auto owners = [&](int base) {  // of 32 sequences
+            const int s = base + (threadIdx.x & 31);
+            return __ballot_sync(0xffffffffu, s < p.n_seq && __ldg(p.cu + s) <= tok && tok < __ldg(p.cu + s + 1));
+        };
+        int last = -1;
+        for (int base = (p.n_seq - 1) & ~31; base >= 0 && last < 0; base -= 32)
+            for (unsigned of = owners(base); of && last < 0;) {
+                const int s = 31 - __clz(of);
+                if (token_of(p, base + s, tok).on) last = base + s;
+                of ^= 1u << s;
+            }
+        for (int base = 0; base <= last; base += 32)
+            for (unsigned of = owners(base); of; of &= of - 1) {
+                const int s = base + __ffs(of) - 1;
+                if (s > last || (s < last && !p.paged)) continue;
+                const TokenAt at = token_of(p, s, tok);
+                if (!at.on) continue;
+                for (int h = s < last ? p.n_heads : 0; h < heads; ++h) one_head<B>(p, at, head_row<B>(p, at, h, s == last));
+            }
     }
 }
 // What a kernel does before its tokens: the sequences that no token may tell of.  Whether the rows are done already.
