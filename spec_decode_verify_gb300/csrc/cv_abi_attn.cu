@@ -426,17 +426,17 @@ int check_pages(const cv_cache_pages_args *a, bool fork, bool needs_tokens, bool
     return CV_OK;
 }
 
-cvk::PagesParams pages_params(const cv_cache_pages_args *a, int op) {
+cvk::PagesParams pages_params(const cv_cache_pages_args *a) {
     cvk::PagesParams p;
     std::memset(&p, 0, sizeof p);
-    p.n_seq = a->n_seq, p.op = op, p.c = view(a->cache);
+    p.n_seq = a->n_seq, p.c = view(a->cache);
     p.idx = a->idx, p.src = a->src_idx, p.n_tok = a->n_tokens, p.err = a->err;
     return p;
 }
 
-int launch_take(const cvk::PagesParams &p, cudaStream_t stream) {
+int launch_take(const cvk::PagesParams &p, int op, cudaStream_t stream) {
     const int smem = cvk::pages_take_smem(p.n_seq);
-    const auto k = cvk::pages_take_kernel();
+    const auto k = cvk::pages_take_kernel(op);
     if (cvk::ensure_smem(reinterpret_cast<const void *>(k), smem) != cudaSuccess) return CV_ERR_LAUNCH;
     return launch_pdl(k, dim3(1), dim3(cvk::kTakeThreads), smem, stream, p) == cudaSuccess ? CV_OK : CV_ERR_LAUNCH;
 }
@@ -533,9 +533,9 @@ int cv_cache_reserve(const cv_cache_pages_args *args, void *stream) {
     const int rc = check_pages(args, false, true, args && args->cache_len);
     if (rc != CV_OK) return rc;
     if (args->n_seq == 0) return CV_OK;
-    cvk::PagesParams p = pages_params(args, cvk::kPagesReserve);
+    cvk::PagesParams p = pages_params(args);
     p.len = args->cache_len;
-    const int take = launch_take(p, reinterpret_cast<cudaStream_t>(stream));
+    const int take = launch_take(p, p.len ? cvk::kPagesOwn : cvk::kPagesReserve, reinterpret_cast<cudaStream_t>(stream));
     if (take != CV_OK || !p.len) return take != CV_OK ? take : done();
     return launch_copies(p, args, cvk::pages_own_kernel, reinterpret_cast<cudaStream_t>(stream));
 }
@@ -544,8 +544,8 @@ int cv_cache_fork(const cv_cache_pages_args *args, void *stream) {
     const int rc = check_pages(args, true, true, true);
     if (rc != CV_OK) return rc;
     if (args->n_seq == 0) return CV_OK;
-    const cvk::PagesParams p = pages_params(args, cvk::kPagesFork);
-    const int take = launch_take(p, reinterpret_cast<cudaStream_t>(stream));
+    const cvk::PagesParams p = pages_params(args);
+    const int take = launch_take(p, cvk::kPagesFork, reinterpret_cast<cudaStream_t>(stream));
     return take != CV_OK ? take : launch_copies(p, args, cvk::pages_fork_kernel, reinterpret_cast<cudaStream_t>(stream));
 }
 
@@ -553,7 +553,7 @@ int cv_cache_free(const cv_cache_pages_args *args, void *stream) {
     const int rc = check_pages(args, false, false, false);
     if (rc != CV_OK) return rc;
     if (args->n_seq == 0) return CV_OK;
-    const cvk::PagesParams p = pages_params(args, 0);
+    const cvk::PagesParams p = pages_params(args);
     if (launch_pdl(cvk::pages_free_kernel(), dim3((unsigned)args->n_seq), dim3(cvk::kPagesThreads), 0,
                    reinterpret_cast<cudaStream_t>(stream), p) != cudaSuccess)
         return CV_ERR_LAUNCH;

@@ -103,7 +103,7 @@ int rope_smem(bool bf16);  // of the kernel for 16-byte pieces
 
 // ---- the cache's pages
 struct PagesParams {
-    int n_seq, T, op;
+    int n_seq, T;
     CacheView c;
     const int *idx, *src, *n_tok;          // reserve, fork, free
     const int *len;                        // compact, reserve
@@ -111,10 +111,10 @@ struct PagesParams {
     int *new_len, *err;
     int esize, chunks;                     // copies: pieces of a head's row
 };
-enum { kPagesReserve = 0, kPagesFork = 1 };
+enum { kPagesReserve, kPagesOwn, kPagesFork };  // growth, growth with lengths, forks
 using PagesKernel = void (*)(PagesParams);
 constexpr int kTakeThreads = 1024, kMaxPageSeqs = 4096, kPagesThreads = 256, kForkCluster = 8;
-PagesKernel pages_take_kernel();                // new pages for reserve and fork: one block
+PagesKernel pages_take_kernel(int op);          // new pages: one block
 PagesKernel pages_fork_kernel(int bytes);       // shares and copies; bytes an access
 PagesKernel pages_own_kernel(int bytes);        // copies of shared pages that are to be written
 PagesKernel pages_free_kernel();

@@ -41,6 +41,9 @@ constexpr int kCheckPages = 128;  // pages of a fork's source that a warp looks 
 constexpr int kScanEach = 8, kScanPages = kTakeThreads * kScanEach;  // counts a thread, and the block, looks at in one go
 static_assert(kScanPages >= 2 * kMaxPageSeqs, "a fork's notes fit into the list");
 
+// OP: kPages*.  (A kernel for each: the code that a call does not need, on its way from memory, is a good part of the time of a block
+// that runs alone.  64 forks and then 64 slots that grow: 22.6 us with one kernel for all, 20.7 with three.)
+template <int OP>
 __global__ void __launch_bounds__(kTakeThreads) pages_take(const __grid_constant__ PagesParams p) {
     extern __shared__ __align__(8) long long smem[];
     long long *const scratch = smem, *const pre = smem + 32;  // pre: pages of the sequences before
@@ -49,7 +52,7 @@ __global__ void __launch_bounds__(kTakeThreads) pages_take(const __grid_constant
     grid_dep_wait();
     grid_dep_launch();
     const int tid = threadIdx.x;
-    const bool fork = p.op == kPagesFork;
+    constexpr bool fork = OP == kPagesFork, own = OP == kPagesOwn;
     const CacheView &c = p.c;
     // Of a fork: whether a page of the source is not there, and its tokens (the list's places are not used before the scan).
     int *const gone = list, *const tokens = list + kMaxPageSeqs;
@@ -97,7 +100,7 @@ __global__ void __launch_bounds__(kTakeThreads) pages_take(const __grid_constant
             if (!st && (n < 0 || n > (long long)c.max_pages * c.page || held < 0 || held > c.max_pages)) return -1 - kSeqBadLength;
             need = max(0, pages_for(n, c.page) - held);
             first[i] = held;
-            if (p.len && !st) {  // and one for each shared page that is to be written
+            if (own && !st) {  // and one for each shared page that is to be written
                 const int L = __ldg(p.len + i);
                 if (L < 0 || L > (long long)held * c.page) return -1 - kSeqBadLength;
                 const int *const row = c.table + (long long)slot * c.table_row;
@@ -178,7 +181,7 @@ __global__ void __launch_bounds__(kTakeThreads) pages_take(const __grid_constant
             }
             int *const row = c.table + (long long)slots[lo] * c.table_row;
             const int at = first[lo] + (int)(rank - pre[lo]);
-            if (!p.len || at >= c.held[slots[lo]]) {
+            if (!own || at >= c.held[slots[lo]]) {
                 row[at] = list[k];
                 c.refs[list[k]] = 1;
             } else if (k == 0 || rank == pre[lo]) {
@@ -456,7 +459,9 @@ __global__ void __launch_bounds__(kPagesThreads) pages_compact(const __grid_cons
 
 }  // namespace
 
-PagesKernel pages_take_kernel() { return pages_take; }
+PagesKernel pages_take_kernel(int op) {
+    return op == kPagesReserve ? pages_take<kPagesReserve> : op == kPagesOwn ? pages_take<kPagesOwn> : pages_take<kPagesFork>;
+}
 int pages_take_smem(int n_seq) { return 256 + n_seq * 24 + kScanPages * 4; }
 PagesKernel pages_fork_kernel(int bytes) { return bytes == 16 ? pages_fork<16> : bytes == 4 ? pages_fork<4> : pages_fork<2>; }
 PagesKernel pages_own_kernel(int bytes) { return bytes == 16 ? pages_own<16> : bytes == 4 ? pages_own<4> : pages_own<2>; }
