@@ -212,7 +212,8 @@ __device__ __forceinline__ bool attn_ancestors(const int *parent, int T, int thr
         }
         sync();
     }
-    for (int t = thread; t < T; t += threads) out[t] = tree->mask[from][t];
+    // (rows past the drafts see none of them: where rows share a decision, what an earlier call left here would reach the others' bits)
+    for (int t = thread; t < 128; t += threads) out[t] = t < T ? tree->mask[from][t] : make_uint4(0, 0, 0, 0);
     return bad;
 }
 
